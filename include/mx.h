@@ -38,7 +38,8 @@
  *    mx_device_status().  A fault of a kernel on any stream is therefore
  *    reported to whichever caller queries the device first.
  *  - Every device pointer must be 16-byte aligned, and every leading
- *    dimension must span a multiple of 16 bytes (MX_ERR_MISALIGNED).
+ *    dimension must span a multiple of 16 bytes (MX_ERR_MISALIGNED), except
+ *    where an entry point asks for less.
  *  - Sizes: rows, K and leading dimensions up to 2^31 - 1; a GEMM whose
  *    256x256 output tiles (over all groups) number 2^31 or more, and a
  *    quantization whose (padded) tiles of 128 rows x 128 bf16 or 64 FP32
@@ -339,6 +340,126 @@ mx_status mx_grouped_gemm_wgrad(int32_t groups, const int32_t* d_offsets, int64_
                                 const uint8_t* a, const uint8_t* sa, mx_fmt fa,
                                 const uint8_t* b, const uint8_t* sb, mx_fmt fb,
                                 void* y, mx_dtype y_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the products: the norms before and after a block, and a whole
+ * mixture-of-experts layer for a few tokens.
+ * ------------------------------------------------------------------------ */
+
+/* The norm after a block, its gate, the scaled residual and the norm before
+ * the next block, in one pass.  With n(v; w)_c = v_c w_c / sqrt(mean(v^2) + eps):
+ *   res_out[t] = alpha * residual[t] + g[t] * n(block[t]; w_post)
+ *   y[t]       = n(res_out[t]; w_pre)
+ * in FP32, with one rounding (to nearest even) per output; the second norm
+ * reads res_out as it is stored, so that its gradient can be computed from
+ * the stored value alone.
+ * block: device [rows, cols] of c_dtype, the block's output, leading
+ *    dimension ldb; y: the same type, the next block's input (ldy).
+ * residual, res_out: device [rows, cols] of s_dtype (ldr, ldo); res_out may
+ *    be residual itself (same pointer and leading dimension), no other
+ *    output may overlap an input.  The stream is at least as wide as the
+ *    blocks: c_dtype MX_FP32 with s_dtype MX_BF16 is MX_ERR_UNSUPPORTED.
+ * w_post: device [cols] or NULL (no norm after the block: n is block[t]);
+ * w_pre: device [cols].
+ * gate: device [gates, cols] contiguous or NULL (g = 1, gates ignored);
+ *    row t takes row t / (rows / gates) of it: gates = 1 is one gate per
+ *    channel, gates = rows one per element; rows % gates == 0.
+ * w_post, w_pre and gate share w_dtype.
+ * Pointers and leading dimensions need the alignment of one element only
+ * (rows of whole 16-byte runs on 16-byte boundaries are the fast case);
+ * 1 <= cols <= 16384 (more is MX_ERR_UNSUPPORTED), leading dimensions >=
+ * cols, eps >= 0; rows == 0 does nothing. */
+mx_status mx_norm_residual(int64_t rows, int64_t cols,
+                           const void* block, int64_t ldb, mx_dtype c_dtype,
+                           const void* residual, int64_t ldr, mx_dtype s_dtype,
+                           const void* w_post, const void* w_pre,
+                           const void* gate, int64_t gates, mx_dtype w_dtype,
+                           float alpha, float eps,
+                           void* res_out, int64_t ldo, void* y, int64_t ldy,
+                           cudaStream_t stream);
+
+/* Bytes of the workspace of mx_norm_residual_backward for these sizes (gates
+ * = 0 without a gate); 0 for sizes that it refuses. */
+size_t mx_norm_residual_backward_workspace(int64_t rows, int64_t cols, int64_t gates);
+
+/* Gradients of mx_norm_residual.  With r = res_out as the forward pass
+ * stored it, rho = 1 / sqrt(mean(r^2) + eps), sigma = 1 / sqrt(mean(block^2)
+ * + eps) per row, and in FP32:
+ *   D = d_res + rho w_pre dy - r rho^3 mean(w_pre dy r)
+ *   d_residual = alpha D             d_w_pre = sum over rows of dy r rho
+ *   with w_post, u = g D:
+ *     d_block = sigma w_post u - block sigma^3 mean(w_post u block)
+ *     d_w_post = sum over rows of u block sigma
+ *     d_gate = sum over a gate's rows of D w_post block sigma
+ *   without: d_block = g D, d_gate = sum over a gate's rows of D block
+ * d_res: device [rows, cols] of s_dtype, the gradient that arrives at
+ *    res_out from later blocks (ldd), or NULL (zero); dy: device [rows,
+ *    cols] of c_dtype, that of y (lddy).
+ * d_block (c_dtype, lddb) and d_residual (s_dtype, lddr; may be d_res
+ *    itself) are rounded once; d_w_post, d_w_pre [cols] and d_gate [gates,
+ *    cols] are FP32 and always written (zeros when rows == 0); d_w_post and
+ *    d_gate are NULL exactly when w_post and gate are.
+ * Column sums run in a fixed order for given sizes: the same inputs give the
+ * same bits.
+ * workspace: device, at least mx_norm_residual_backward_workspace(rows,
+ *    cols, gate ? gates : 0) bytes, 16-byte aligned; its contents need no
+ *    set-up and are undefined afterwards.
+ * Other arguments and constraints as mx_norm_residual. */
+mx_status mx_norm_residual_backward(int64_t rows, int64_t cols,
+                                    const void* d_res, int64_t ldd, const void* dy, int64_t lddy,
+                                    const void* block, int64_t ldb, mx_dtype c_dtype,
+                                    const void* res_out, int64_t ldr, mx_dtype s_dtype,
+                                    const void* w_post, const void* w_pre,
+                                    const void* gate, int64_t gates, mx_dtype w_dtype,
+                                    float alpha, float eps,
+                                    void* d_block, int64_t lddb, void* d_residual, int64_t lddr,
+                                    float* d_w_post, float* d_w_pre, float* d_gate,
+                                    void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/* Bytes of the workspace of mx_moe_few_tokens for these sizes; 0 for sizes
+ * that it refuses. */
+size_t mx_moe_few_tokens_workspace(int32_t tokens, int64_t hidden, int64_t inter,
+                                   int32_t experts, int32_t top_k);
+
+/* A whole mixture-of-experts layer for a few tokens, weights in MX formats:
+ *   z[t] = router x[t];  p = softmax(z[t]);  the top_k largest z win (equal
+ *   ones: the lowest index first);  w = p of the winners, divided by their
+ *   sum when renormalize != 0;
+ *   y[t] = sum over the winners e of w_e down_e (silu(gate_e x[t]) * (up_e x[t]))
+ * x: device bf16 [tokens, hidden], leading dimension ldx; router: device
+ *    [experts, hidden] contiguous of router_dtype.
+ * gate, up: [experts, inter, hidden] codes of format fmt_gu (K = hidden
+ *    contiguous); down: [experts, hidden, inter] codes of format fmt_d; the
+ *    *_scales hold `experts` consecutive swizzled scale matrices, expert e's
+ *    at byte e * mx_scale_bytes(inter, hidden), for down e *
+ *    mx_scale_bytes(hidden, inter) -- each expert quantized ROWWISE.
+ * fmt_gu, fmt_d: MX_E4M3, MX_E5M2 or MX_E2M1_PACKED (other formats are
+ *    MX_ERR_UNSUPPORTED); hidden and inter are multiples of 16 (of 128 for
+ *    packed codes), at most 65536.
+ * y: device bf16 [tokens, hidden] (ldy), rounded once from FP32.  ids:
+ *    device int32 [tokens, top_k], the winners, largest z first; weights:
+ *    device float [tokens, top_k].  Both contiguous, always written.
+ * Precision: x is taken exactly, products accumulate in FP32, z in FP32; the
+ *    activation silu(..) * (..), times its routing weight, is the only
+ *    intermediate that is rounded (to 8 significant bits, as bf16 has).
+ * A token whose x holds NaN or Inf gets NaN in y; no other token is touched
+ *    by it.  Weights are expected to be finite: an expert with a NaN scale or
+ *    code makes NaN of every token of a call in which some token chose it.
+ * 0 <= tokens <= 64 (more is MX_ERR_UNSUPPORTED), 1 <= experts <= 512, 1 <=
+ *    top_k <= min(experts, 32).
+ * workspace: device, at least mx_moe_few_tokens_workspace(...) bytes,
+ *    16-byte aligned; needs no set-up, undefined afterwards, and belongs to
+ *    one call at a time. */
+mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                            int32_t top_k, const void* x, int64_t ldx,
+                            const void* router, mx_dtype router_dtype,
+                            const uint8_t* gate, const uint8_t* gate_scales,
+                            const uint8_t* up, const uint8_t* up_scales, mx_fmt fmt_gu,
+                            const uint8_t* down, const uint8_t* down_scales, mx_fmt fmt_d,
+                            int32_t renormalize, void* y, int64_t ldy,
+                            int32_t* ids, float* weights,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Synchronizes `stream`, then reads the device status word of the current
  * device and clears the bits it read: MX_OK, MX_ERR_TIMEOUT (a kernel's

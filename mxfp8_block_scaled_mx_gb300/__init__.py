@@ -53,7 +53,9 @@ ACT = {"none": 0, "silu": 1}
 EXPORTS = ("mx_scale_bytes", "mx_grouped_scale_bytes", "mx_grouped_cols_capacity",
            "mx_quantize", "mx_quantize_sr", "mx_quantize_grouped", "mx_quantize_grouped_ex",
            "mx_gemm", "mx_gemm_bias_act", "mx_grouped_gemm", "mx_grouped_gemm_bcat",
-           "mx_grouped_gemm_wgrad", "mx_device_status", "mx_status_str",
+           "mx_grouped_gemm_wgrad", "mx_norm_residual", "mx_norm_residual_backward",
+           "mx_norm_residual_backward_workspace", "mx_moe_few_tokens",
+           "mx_moe_few_tokens_workspace", "mx_device_status", "mx_status_str",
            "mx_set_wait_timeout_ns", "mx_selftest_wait_timeout")
 
 
@@ -101,6 +103,22 @@ def _declare(lib):
     lib.mx_grouped_gemm.argtypes = [i32, vp, i64, i64, i64, vp, vp, c.c_int, vp, vp, c.c_int, vp,
                                     c.c_int, vp]
     lib.mx_grouped_gemm.restype = c.c_int
+    f32 = c.c_float
+    lib.mx_norm_residual.argtypes = [i64, i64, vp, i64, c.c_int, vp, i64, c.c_int, vp, vp, vp, i64,
+                                     c.c_int, f32, f32, vp, i64, vp, i64, vp]
+    lib.mx_norm_residual.restype = c.c_int
+    lib.mx_norm_residual_backward_workspace.argtypes = [i64, i64, i64]
+    lib.mx_norm_residual_backward_workspace.restype = c.c_size_t
+    lib.mx_norm_residual_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, c.c_int, vp, i64,
+                                              c.c_int, vp, vp, vp, i64, c.c_int, f32, f32, vp, i64,
+                                              vp, i64, vp, vp, vp, vp, c.c_size_t, vp]
+    lib.mx_norm_residual_backward.restype = c.c_int
+    lib.mx_moe_few_tokens_workspace.argtypes = [i32, i64, i64, i32, i32]
+    lib.mx_moe_few_tokens_workspace.restype = c.c_size_t
+    lib.mx_moe_few_tokens.argtypes = [i32, i64, i64, i32, i32, vp, i64, vp, c.c_int, vp, vp, vp, vp,
+                                      c.c_int, vp, vp, c.c_int, i32, vp, i64, vp, vp, vp,
+                                      c.c_size_t, vp]
+    lib.mx_moe_few_tokens.restype = c.c_int
     lib.mx_device_status.argtypes = [vp]
     lib.mx_device_status.restype = c.c_int
     lib.mx_status_str.argtypes = [c.c_int]
@@ -250,6 +268,42 @@ def mx_grouped_gemm(groups, d_offsets, total_m, n, k, a, sa, fa, b, sb, fb, y, y
                     stream) -> int:
     return lib().mx_grouped_gemm(groups, d_offsets, total_m, n, k, a, sa, fa, b, sb, fb, y,
                                  y_dtype, stream)
+
+
+def mx_norm_residual(rows, cols, block, ldb, c_dtype, residual, ldr, s_dtype, w_post, w_pre, gate,
+                     gates, w_dtype, alpha, eps, res_out, ldo, y, ldy, stream) -> int:
+    return lib().mx_norm_residual(rows, cols, block, ldb, c_dtype, residual, ldr, s_dtype, w_post,
+                                  w_pre, gate, gates, w_dtype, alpha, eps, res_out, ldo, y, ldy,
+                                  stream)
+
+
+def mx_norm_residual_backward_workspace(rows: int, cols: int, gates: int) -> int:
+    return int(lib().mx_norm_residual_backward_workspace(rows, cols, gates))
+
+
+def mx_norm_residual_backward(rows, cols, d_res, ldd, dy, lddy, block, ldb, c_dtype, res_out, ldr,
+                              s_dtype, w_post, w_pre, gate, gates, w_dtype, alpha, eps, d_block,
+                              lddb, d_residual, lddr, d_w_post, d_w_pre, d_gate, workspace,
+                              workspace_bytes, stream) -> int:
+    return lib().mx_norm_residual_backward(rows, cols, d_res, ldd, dy, lddy, block, ldb, c_dtype,
+                                           res_out, ldr, s_dtype, w_post, w_pre, gate, gates,
+                                           w_dtype, alpha, eps, d_block, lddb, d_residual, lddr,
+                                           d_w_post, d_w_pre, d_gate, workspace, workspace_bytes,
+                                           stream)
+
+
+def mx_moe_few_tokens_workspace(tokens: int, hidden: int, inter: int, experts: int,
+                                top_k: int) -> int:
+    return int(lib().mx_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k))
+
+
+def mx_moe_few_tokens(tokens, hidden, inter, experts, top_k, x, ldx, router, router_dtype, gate,
+                      gate_scales, up, up_scales, fmt_gu, down, down_scales, fmt_d, renormalize, y,
+                      ldy, ids, weights, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_moe_few_tokens(tokens, hidden, inter, experts, top_k, x, ldx, router,
+                                   router_dtype, gate, gate_scales, up, up_scales, fmt_gu, down,
+                                   down_scales, fmt_d, renormalize, y, ldy, ids, weights, workspace,
+                                   workspace_bytes, stream)
 
 
 def mx_device_status(stream=None) -> int:
@@ -474,6 +528,206 @@ def grouped_gemm_wgrad(a: MxTensor, offsets: torch.Tensor, b: MxTensor, total_to
                                FMT[b.fmt], _ptr(out), DTYPE[out_dtype], _stream(stream))
     _check("mx_grouped_gemm_wgrad", st)
     return out
+
+
+def _require_rows(t: torch.Tensor, shape, dtypes, what: str):
+    """A 2-D tensor of one of `dtypes` with unit column stride (rows may be
+    apart, not overlapping)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a {' or '.join(map(str, dtypes))} tensor of shape "
+                         f"{tuple(shape)}")
+    _on_current_device(t, what)
+    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or
+                      (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+        raise ValueError(f"{what} must be row-major with unit column stride")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Leading dimension (that of a single row is whatever torch says, so the
+    row length stands in for it)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _require_vector(t: torch.Tensor, shape, dtype, what: str):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}")
+    _on_current_device(t, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Workspace of one call, kept by the allocator until `stream` is past it."""
+    t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None and _stream(stream) != _stream():
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        t.record_stream(stream)
+    return t
+
+
+def _norm_args(block, residual, w_pre, w_post, gate):
+    """Checks of the operands shared by the norm and its gradient; returns the
+    number of gates (0 without one)."""
+    if not isinstance(block, torch.Tensor) or block.dim() != 2:
+        raise ValueError("block must be a 2-D tensor")
+    rows, cols = block.shape
+    _require_rows(block, (rows, cols), tuple(_X_DTYPE), "block")
+    _require_rows(residual, (rows, cols), tuple(_X_DTYPE), "residual")
+    if not isinstance(w_pre, torch.Tensor) or w_pre.dtype not in _X_DTYPE:
+        raise ValueError("w_pre must be a bf16 or fp32 tensor")
+    _require_vector(w_pre, (cols,), w_pre.dtype, "w_pre")
+    if w_post is not None:
+        _require_vector(w_post, (cols,), w_pre.dtype, "w_post")
+    if gate is None:
+        return 0
+    if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
+        raise ValueError("gate must be a 1-D or 2-D tensor")
+    gates = 1 if gate.dim() == 1 else gate.shape[0]
+    _require_vector(gate, (cols,) if gate.dim() == 1 else (gates, cols), w_pre.dtype, "gate")
+    if gates < 1 or rows % gates:
+        raise ValueError(f"{rows} rows cannot be split evenly over {gates} gates")
+    return gates
+
+
+def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tensor,
+                  w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                  alpha: float = 1.0, eps: float = 1e-6, out_residual: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None):
+    """The norm after a block, its gate, the scaled residual and the norm
+    before the next block in one pass: returns (alpha * residual + gate *
+    rms(block; w_post), rms(that; w_pre)), the first in the residual's type
+    (bf16 or fp32), the second in the block's.  w_post None: no norm after
+    the block.  gate: [cols], or [gates, cols] with one gate per
+    rows/gates consecutive rows.  w_pre, w_post and gate share one type.
+    out_residual may be `residual` itself."""
+    gates = _norm_args(block, residual, w_pre, w_post, gate)
+    rows, cols = block.shape
+    if out_residual is None:
+        out_residual = torch.empty((rows, cols), dtype=residual.dtype, device=block.device)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=block.dtype, device=block.device)
+    _require_rows(out_residual, (rows, cols), (residual.dtype,), "out_residual")
+    _require_rows(out, (rows, cols), (block.dtype,), "out")
+    if rows == 0:
+        return out_residual, out
+    st = mx_norm_residual(rows, cols, _ptr(block), _row_stride(block), _X_DTYPE[block.dtype],
+                          _ptr(residual), _row_stride(residual), _X_DTYPE[residual.dtype],
+                          _ptr(w_post), _ptr(w_pre), _ptr(gate), gates, _X_DTYPE[w_pre.dtype],
+                          alpha, eps, _ptr(out_residual), _row_stride(out_residual), _ptr(out),
+                          _row_stride(out), _stream(stream))
+    _check("mx_norm_residual", st)
+    return out_residual, out
+
+
+@dataclass
+class NormResidualGrads:
+    """Gradients of norm_residual's inputs; those of the weights and the gate
+    are FP32 (None where the forward pass had none)."""
+    block: torch.Tensor
+    residual: torch.Tensor
+    w_pre: torch.Tensor
+    w_post: torch.Tensor | None
+    gate: torch.Tensor | None
+
+
+def norm_residual_backward(d_residual: torch.Tensor | None, d_y: torch.Tensor, block: torch.Tensor,
+                           residual: torch.Tensor, w_pre: torch.Tensor,
+                           w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                           alpha: float = 1.0, eps: float = 1e-6,
+                           workspace: torch.Tensor | None = None, stream=None) -> NormResidualGrads:
+    """Gradients of norm_residual from those of its two outputs (d_residual
+    None: zero).  `residual` is the residual that the forward pass returned.
+    The column sums run in a fixed order: the same inputs give the same bits.
+    workspace: uint8, mx_norm_residual_backward_workspace(rows, cols, gates)
+    bytes; allocated here when None."""
+    gates = _norm_args(block, residual, w_pre, w_post, gate)
+    rows, cols = block.shape
+    _require_rows(d_y, (rows, cols), (block.dtype,), "d_y")
+    if d_residual is not None:
+        _require_rows(d_residual, (rows, cols), (residual.dtype,), "d_residual")
+    dev = block.device
+    grads = NormResidualGrads(
+        torch.empty((rows, cols), dtype=block.dtype, device=dev),
+        torch.empty((rows, cols), dtype=residual.dtype, device=dev),
+        torch.empty(cols, dtype=torch.float32, device=dev),
+        None if w_post is None else torch.empty(cols, dtype=torch.float32, device=dev),
+        None if gate is None else torch.empty(gate.shape, dtype=torch.float32, device=dev))
+    need = mx_norm_residual_backward_workspace(rows, cols, gates)
+    if workspace is None:
+        workspace = _scratch(need, dev, stream)
+    else:
+        _require_scales(workspace, need, "workspace")
+    # an empty tensor has no address: any device pointer stands in for one
+    # that nothing is read from or written to
+    at = (lambda t: _ptr(t) or _ptr(workspace)) if rows == 0 else _ptr
+    st = mx_norm_residual_backward(
+        rows, cols, _ptr(d_residual) or None,
+        cols if d_residual is None else _row_stride(d_residual), at(d_y), _row_stride(d_y),
+        at(block), _row_stride(block), _X_DTYPE[block.dtype], at(residual), _row_stride(residual),
+        _X_DTYPE[residual.dtype], _ptr(w_post), _ptr(w_pre), _ptr(gate), gates,
+        _X_DTYPE[w_pre.dtype], alpha, eps, at(grads.block), cols, at(grads.residual), cols,
+        _ptr(grads.w_post), _ptr(grads.w_pre), _ptr(grads.gate), _ptr(workspace),
+        workspace.numel(), _stream(stream))
+    _check("mx_norm_residual_backward", st)
+    return grads
+
+
+def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: MxTensor,
+                   down: MxTensor, top_k: int, renormalize: bool = True,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   return_routing: bool = False, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens: router product,
+    top-k, gated feed-forward (SiLU) of the chosen experts, weighted sum.
+    x: bf16 [tokens, hidden]; router: bf16 or fp32 [experts, hidden]; gate,
+    up: MxTensor codes [experts, inter, hidden]; down: codes [experts,
+    hidden, inter]; scales: one swizzled matrix per expert, one after the
+    other.  Formats e4m3, e5m2 or e2m1_packed, the same for gate and up.
+    Returns y (bf16 [tokens, hidden]), with return_routing (y, ids int32
+    [tokens, top_k], weights fp32 [tokens, top_k]).  workspace: uint8,
+    mx_moe_few_tokens_workspace(...) bytes, one call at a time; allocated
+    here when None."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    tokens, hidden = x.shape
+    _require_rows(x, (tokens, hidden), (torch.bfloat16,), "x")
+    if not isinstance(router, torch.Tensor) or router.dim() != 2 or router.dtype not in _X_DTYPE:
+        raise ValueError("router must be a 2-D bf16 or fp32 tensor")
+    experts = router.shape[0]
+    _require_vector(router, (experts, hidden), router.dtype, "router")
+    if gate.codes.dim() != 3 or gate.fmt != up.fmt:
+        raise ValueError("gate and up must be [experts, inter, hidden] codes of one format")
+    inter = gate.codes.shape[1]
+    for t, shape, what in ((gate, (experts, inter, storage_bytes(gate.fmt, hidden)), "gate"),
+                           (up, (experts, inter, storage_bytes(up.fmt, hidden)), "up"),
+                           (down, (experts, hidden, storage_bytes(down.fmt, inter)), "down")):
+        _require_codes(t.codes, shape, what)
+    _require_scales(gate.scales, experts * mx_scale_bytes(inter, hidden), "gate")
+    _require_scales(up.scales, experts * mx_scale_bytes(inter, hidden), "up")
+    _require_scales(down.scales, experts * mx_scale_bytes(hidden, inter), "down")
+    if not 1 <= top_k <= experts:
+        raise ValueError(f"top_k must be 1 to {experts}, got {top_k}")
+    dev = x.device
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=dev)
+    _require_rows(out, (tokens, hidden), (torch.bfloat16,), "out")
+    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+    if tokens > 0:
+        need = mx_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k)
+        if workspace is None:
+            workspace = _scratch(need, dev, stream)
+        else:
+            _require_scales(workspace, need, "workspace")
+        st = mx_moe_few_tokens(tokens, hidden, inter, experts, top_k, _ptr(x), _row_stride(x),
+                               _ptr(router), _X_DTYPE[router.dtype], _ptr(gate.codes),
+                               _ptr(gate.scales), _ptr(up.codes), _ptr(up.scales), FMT[gate.fmt],
+                               _ptr(down.codes), _ptr(down.scales), FMT[down.fmt],
+                               int(renormalize), _ptr(out), _row_stride(out), _ptr(ids),
+                               _ptr(weights), _ptr(workspace), workspace.numel(),
+                               _stream(stream))
+        _check("mx_moe_few_tokens", st)
+    return (out, ids, weights) if return_routing else out
 
 
 def device_status(stream=None) -> int:

@@ -1,6 +1,6 @@
 // kernels.h -- launch interface between the C-ABI layer (mx_api.cu) and the
 // CUDA kernels (quantize.cu and quantize_f32.cu, which instantiate
-// quantize_kernel.cuh; gemm_pair.cu; status.cu).  Not part of the public
+// quantize_kernel.cuh; gemm_pair.cu; norm.cu; moe_few.cu; status.cu).  Not part of the public
 // ABI.
 #pragma once
 
@@ -128,6 +128,72 @@ struct GemmParams {
 cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& tmap_a,
                              const CUtensorMap& tmap_b, const CUtensorMap& tmap_sa,
                              const CUtensorMap& tmap_sb, int num_sms, cudaStream_t stream);
+
+struct NormParams {
+  const void* block;     // [rows, cols] of the blocks' type, leading dimension ldb
+  const void* residual;  // [rows, cols] of the stream's type, ldr
+  const void* w_post;    // [cols] or nullptr
+  const void* w_pre;     // [cols]
+  const void* gate;      // [gates, cols] or nullptr
+  void* res_out;         // stream's type, ldo
+  void* y;               // blocks' type, ldy
+  int64_t rows, cols, gates;
+  int64_t ldb, ldr, ldo, ldy;
+  int32_t c_fp32, s_fp32, w_fp32;  // 1: FP32, 0: BF16 (blocks, stream, weights and gate)
+  float alpha, eps;
+};
+
+struct NormBackParams {
+  const void* d_res;    // [rows, cols] of the stream's type, ldd, or nullptr
+  const void* dy;       // blocks' type, lddy
+  const void* block;    // blocks' type, ldb
+  const void* res_out;  // stream's type, ldr
+  const void* w_post;   // [cols] or nullptr
+  const void* w_pre;    // [cols]
+  const void* gate;     // [gates, cols] or nullptr
+  void* d_block;        // blocks' type, lddb
+  void* d_residual;     // stream's type, lddr
+  float* d_w_post;      // [cols] or nullptr
+  float* d_w_pre;       // [cols]
+  float* d_gate;        // [gates, cols] or nullptr
+  float* workspace;
+  float* d_copy;
+  int64_t rows, cols, gates;
+  int64_t ldd, lddy, ldb, ldr, lddb, lddr;
+  int32_t c_fp32, s_fp32, w_fp32;
+  float alpha, eps;
+};
+
+size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates);
+cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
+                                          cudaStream_t stream);
+
+struct MoeFewParams {
+  const void* x;         // bf16 [tokens, hidden], ldx
+  const void* router;    // [experts, hidden]
+  const uint8_t* gate;   // [experts, inter, hidden] codes
+  const uint8_t* up;
+  const uint8_t* down;   // [experts, hidden, inter] codes
+  const uint8_t* gate_scales;
+  const uint8_t* up_scales;
+  const uint8_t* down_scales;
+  void* y;               // bf16 [tokens, hidden], ldy
+  int32_t* ids;          // [tokens, top_k]
+  float* weights;        // [tokens, top_k]
+  void* workspace;
+  float* logits;
+  float* h;
+  int64_t hidden, inter, ldx, ldy;
+  int32_t tokens, experts, top_k, renormalize;
+  int32_t router_fp32;
+  int32_t fmt_gu, fmt_d;   // element formats (mx_fmt)
+  int32_t bits_gu, bits_d; // bits of storage per code
+};
+
+size_t moe_few_workspace(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                         int32_t top_k);
+cudaError_t launch_moe_few(const MoeFewParams& p, cudaStream_t stream);
 
 // Clears the bits `bits` of the device status word (atomically, so bits
 // set meanwhile by kernels on other streams survive).

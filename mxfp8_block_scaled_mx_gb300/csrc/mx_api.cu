@@ -559,6 +559,228 @@ mx_status mx_grouped_gemm_wgrad(int32_t groups, const int32_t* d_offsets, int64_
   return gemm_common(g, a, sa, fa, b, sb, fb, y, y_dtype, n, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+bool valid_dtype(mx_dtype d) { return d == MX_BF16 || d == MX_FP32; }
+
+bool aligned_elt(const void* p, mx_dtype d) {
+  return (reinterpret_cast<uintptr_t>(p) & (d == MX_FP32 ? 3u : 1u)) == 0;
+}
+
+constexpr int64_t kNormMaxCols = 16384;
+
+// Checks shared by the norm and its gradient.
+mx_status norm_check(int64_t rows, int64_t cols, mx_dtype c_dtype, mx_dtype s_dtype,
+                     mx_dtype w_dtype, const void* gate, int64_t gates, float eps) {
+  if (!valid_dtype(c_dtype) || !valid_dtype(s_dtype) || !valid_dtype(w_dtype))
+    return MX_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 1 || !(eps >= 0.f)) return MX_ERR_INVALID_ARG;
+  if (gate && (gates < 1 || rows % gates != 0)) return MX_ERR_INVALID_ARG;
+  if (cols > kNormMaxCols || rows > INT32_MAX) return MX_ERR_UNSUPPORTED;
+  if (c_dtype == MX_FP32 && s_dtype == MX_BF16) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+bool moe_few_sizes_ok(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                      int32_t top_k) {
+  return tokens >= 0 && tokens <= 64 && hidden >= 16 && hidden <= 65536 && hidden % 16 == 0 &&
+         inter >= 16 && inter <= 65536 && inter % 16 == 0 && experts >= 1 && experts <= 512 &&
+         top_k >= 1 && top_k <= experts && top_k <= 32;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_norm_residual(int64_t rows, int64_t cols, const void* block, int64_t ldb,
+                           mx_dtype c_dtype, const void* residual, int64_t ldr, mx_dtype s_dtype,
+                           const void* w_post, const void* w_pre, const void* gate, int64_t gates,
+                           mx_dtype w_dtype, float alpha, float eps, void* res_out, int64_t ldo,
+                           void* y, int64_t ldy, cudaStream_t stream) {
+  if (!block || !residual || !w_pre || !res_out || !y) return MX_ERR_INVALID_ARG;
+  mx_status s = norm_check(rows, cols, c_dtype, s_dtype, w_dtype, gate, gates, eps);
+  if (s != MX_OK) return s;
+  if (ldb < cols || ldr < cols || ldo < cols || ldy < cols) return MX_ERR_INVALID_ARG;
+  if (!aligned_elt(block, c_dtype) || !aligned_elt(y, c_dtype) ||
+      !aligned_elt(residual, s_dtype) || !aligned_elt(res_out, s_dtype) ||
+      !aligned_elt(w_post, w_dtype) || !aligned_elt(w_pre, w_dtype) || !aligned_elt(gate, w_dtype))
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (rows == 0) return MX_OK;
+  if (!all_on_device(st->device, {block, residual, w_post, w_pre, gate, res_out, y}))
+    return MX_ERR_INVALID_ARG;
+  mx::NormParams p{};
+  p.block = block;
+  p.residual = residual;
+  p.w_post = w_post;
+  p.w_pre = w_pre;
+  p.gate = gate;
+  p.res_out = res_out;
+  p.y = y;
+  p.rows = rows;
+  p.cols = cols;
+  p.gates = gate ? gates : 0;
+  p.ldb = ldb;
+  p.ldr = ldr;
+  p.ldo = ldo;
+  p.ldy = ldy;
+  p.c_fp32 = c_dtype == MX_FP32;
+  p.s_fp32 = s_dtype == MX_FP32;
+  p.w_fp32 = w_dtype == MX_FP32;
+  p.alpha = alpha;
+  p.eps = eps;
+  return mx::launch_norm_residual(p, st->num_sms, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+size_t mx_norm_residual_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > kNormMaxCols || gates < 0 ||
+      (gates > 0 && rows % gates != 0))
+    return 0;
+  return mx::norm_backward_workspace(rows, cols, gates);
+}
+
+mx_status mx_norm_residual_backward(int64_t rows, int64_t cols, const void* d_res, int64_t ldd,
+                                    const void* dy, int64_t lddy, const void* block, int64_t ldb,
+                                    mx_dtype c_dtype, const void* res_out, int64_t ldr,
+                                    mx_dtype s_dtype, const void* w_post, const void* w_pre,
+                                    const void* gate, int64_t gates, mx_dtype w_dtype, float alpha,
+                                    float eps, void* d_block, int64_t lddb, void* d_residual,
+                                    int64_t lddr, float* d_w_post, float* d_w_pre, float* d_gate,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!dy || !block || !res_out || !w_pre || !d_block || !d_residual || !d_w_pre)
+    return MX_ERR_INVALID_ARG;
+  if ((w_post == nullptr) != (d_w_post == nullptr) || (gate == nullptr) != (d_gate == nullptr))
+    return MX_ERR_INVALID_ARG;
+  mx_status s = norm_check(rows, cols, c_dtype, s_dtype, w_dtype, gate, gates, eps);
+  if (s != MX_OK) return s;
+  if ((d_res && ldd < cols) || lddy < cols || ldb < cols || ldr < cols || lddb < cols ||
+      lddr < cols)
+    return MX_ERR_INVALID_ARG;
+  const size_t need = mx::norm_backward_workspace(rows, cols, gate ? gates : 0);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  if (!aligned_elt(d_res, s_dtype) || !aligned_elt(dy, c_dtype) || !aligned_elt(block, c_dtype) ||
+      !aligned_elt(res_out, s_dtype) || !aligned_elt(w_post, w_dtype) ||
+      !aligned_elt(w_pre, w_dtype) || !aligned_elt(gate, w_dtype) ||
+      !aligned_elt(d_block, c_dtype) || !aligned_elt(d_residual, s_dtype) ||
+      !aligned_elt(d_w_post, MX_FP32) || !aligned_elt(d_w_pre, MX_FP32) ||
+      !aligned_elt(d_gate, MX_FP32) || !aligned16(workspace))
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (!all_on_device(st->device, {d_w_post, d_w_pre, d_gate, w_post, w_pre, gate}))
+    return MX_ERR_INVALID_ARG;
+  if (rows > 0 &&
+      !all_on_device(st->device, {d_res, dy, block, res_out, d_block, d_residual, workspace}))
+    return MX_ERR_INVALID_ARG;
+  mx::NormBackParams p{};
+  p.d_res = d_res;
+  p.dy = dy;
+  p.block = block;
+  p.res_out = res_out;
+  p.w_post = w_post;
+  p.w_pre = w_pre;
+  p.gate = gate;
+  p.d_block = d_block;
+  p.d_residual = d_residual;
+  p.d_w_post = d_w_post;
+  p.d_w_pre = d_w_pre;
+  p.d_gate = d_gate;
+  p.workspace = static_cast<float*>(workspace);
+  p.rows = rows;
+  p.cols = cols;
+  p.gates = gate ? gates : 0;
+  p.ldd = ldd;
+  p.lddy = lddy;
+  p.ldb = ldb;
+  p.ldr = ldr;
+  p.lddb = lddb;
+  p.lddr = lddr;
+  p.c_fp32 = c_dtype == MX_FP32;
+  p.s_fp32 = s_dtype == MX_FP32;
+  p.w_fp32 = w_dtype == MX_FP32;
+  p.alpha = alpha;
+  p.eps = eps;
+  return mx::launch_norm_residual_backward(p, st->num_sms, stream) == cudaSuccess ? MX_OK
+                                                                                   : MX_ERR_CUDA;
+}
+
+size_t mx_moe_few_tokens_workspace(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                                   int32_t top_k) {
+  if (!moe_few_sizes_ok(tokens, hidden, inter, experts, top_k)) return 0;
+  return mx::moe_few_workspace(tokens, hidden, inter, experts, top_k);
+}
+
+mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                            int32_t top_k, const void* x, int64_t ldx, const void* router,
+                            mx_dtype router_dtype, const uint8_t* gate, const uint8_t* gate_scales,
+                            const uint8_t* up, const uint8_t* up_scales, mx_fmt fmt_gu,
+                            const uint8_t* down, const uint8_t* down_scales, mx_fmt fmt_d,
+                            int32_t renormalize, void* y, int64_t ldy, int32_t* ids,
+                            float* weights, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  if (!x || !router || !gate || !gate_scales || !up || !up_scales || !down || !down_scales || !y ||
+      !ids || !weights)
+    return MX_ERR_INVALID_ARG;
+  if (!valid_dtype(router_dtype) || !valid_gemm_fmt(fmt_gu) || !valid_gemm_fmt(fmt_d))
+    return MX_ERR_INVALID_ARG;
+  if (tokens > 64) return MX_ERR_UNSUPPORTED;
+  if (!moe_few_sizes_ok(tokens, hidden, inter, experts, top_k)) return MX_ERR_INVALID_ARG;
+  if (ldx < hidden || ldy < hidden) return MX_ERR_INVALID_ARG;
+  for (mx_fmt f : {fmt_gu, fmt_d})
+    if (!valid_fmt(f) && f != MX_E2M1_PACKED) return MX_ERR_UNSUPPORTED;
+  // packed operands: whole 128-element K tiles, as for the GEMMs
+  if ((is_packed(fmt_gu) && hidden % 128 != 0) || (is_packed(fmt_d) && inter % 128 != 0))
+    return MX_ERR_INVALID_ARG;
+  const size_t need = mx::moe_few_workspace(tokens, hidden, inter, experts, top_k);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned16(router) || !aligned16(gate) ||
+      !aligned16(gate_scales) || !aligned16(up) || !aligned16(up_scales) || !aligned16(down) ||
+      !aligned16(down_scales) || !aligned16(y) || ldy % 8 != 0 || !aligned16(workspace) ||
+      !aligned_elt(ids, MX_FP32) || !aligned_elt(weights, MX_FP32))
+    return MX_ERR_MISALIGNED;
+  if ((is_packed(fmt_gu) && ((reinterpret_cast<uintptr_t>(gate) & 31u) != 0 ||
+                             (reinterpret_cast<uintptr_t>(up) & 31u) != 0)) ||
+      (is_packed(fmt_d) && (reinterpret_cast<uintptr_t>(down) & 31u) != 0))
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  mx_status s = device_state(&st);
+  if (s != MX_OK) return s;
+  if (tokens == 0) return MX_OK;
+  if (!all_on_device(st->device, {x, router, gate, gate_scales, up, up_scales, down, down_scales,
+                                  y, ids, weights, workspace}))
+    return MX_ERR_INVALID_ARG;
+  mx::MoeFewParams p{};
+  p.x = x;
+  p.router = router;
+  p.gate = gate;
+  p.up = up;
+  p.down = down;
+  p.gate_scales = gate_scales;
+  p.up_scales = up_scales;
+  p.down_scales = down_scales;
+  p.y = y;
+  p.ids = ids;
+  p.weights = weights;
+  p.workspace = workspace;
+  p.hidden = hidden;
+  p.inter = inter;
+  p.ldx = ldx;
+  p.ldy = ldy;
+  p.tokens = tokens;
+  p.experts = experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize;
+  p.router_fp32 = router_dtype == MX_FP32;
+  p.fmt_gu = fmt_gu;
+  p.fmt_d = fmt_d;
+  p.bits_gu = is_packed(fmt_gu) ? code_bits(fmt_gu) : 8;
+  p.bits_d = is_packed(fmt_d) ? code_bits(fmt_d) : 8;
+  return mx::launch_moe_few(p, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
 mx_status mx_device_status(cudaStream_t stream) {
   DeviceState* st = nullptr;
   mx_status s = device_state(&st);

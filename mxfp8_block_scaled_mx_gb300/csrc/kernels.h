@@ -157,7 +157,8 @@ struct NormBackParams {
   float* d_w_pre;       // [cols]
   float* d_gate;        // [gates, cols] or nullptr
   float* workspace;
-  float* d_copy;
+  uint32_t* status;     // device status word
+  uint64_t wait_limit_ns;
   int64_t rows, cols, gates;
   int64_t ldd, lddy, ldb, ldr, lddb, lddr;
   int32_t c_fp32, s_fp32, w_fp32;

@@ -689,6 +689,8 @@ mx_status mx_norm_residual_backward(int64_t rows, int64_t cols, const void* d_re
   p.d_w_pre = d_w_pre;
   p.d_gate = d_gate;
   p.workspace = static_cast<float*>(workspace);
+  p.status = st->status;
+  p.wait_limit_ns = g_wait_ns.load(std::memory_order_relaxed);
   p.rows = rows;
   p.cols = cols;
   p.gates = gate ? gates : 0;

@@ -149,7 +149,9 @@ def _check(fn: str, status: int):
 
 def _stream(stream=None) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # (the same handle as torch.cuda.current_stream().cuda_stream, without
+        # building a Stream object: 0.3 against 3 us on the GB300's host)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -530,30 +532,41 @@ def grouped_gemm_wgrad(a: MxTensor, offsets: torch.Tensor, b: MxTensor, total_to
     return out
 
 
-def _require_rows(t: torch.Tensor, shape, dtypes, what: str):
-    """A 2-D tensor of one of `dtypes` with unit column stride (rows may be
-    apart, not overlapping)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be a {' or '.join(map(str, dtypes))} tensor of shape "
-                         f"{tuple(shape)}")
+# The operators below are called for single tokens, where the host's share of
+# a call counts: each tensor is checked once, by one helper that also returns
+# what the C call needs of it.
+
+def _refuse(t, shape, dtypes, what: str, layout: str):
+    """Says what is wrong with an operand."""
+    want = f"{what} must be a {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)}"
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{want}, got {type(t).__name__}")
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{want}, got {t.dtype} {tuple(t.shape)}")
     _on_current_device(t, what)
-    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or
-                      (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
-        raise ValueError(f"{what} must be row-major with unit column stride")
+    raise ValueError(f"{what} must be {layout}, got strides {t.stride()}")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Leading dimension (that of a single row is whatever torch says, so the
-    row length stands in for it)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _rows_of(t, rows: int, cols: int, dtypes, dev: int, what: str) -> int:
+    """Leading dimension of a [rows, cols] operand with unit column stride whose
+    rows do not overlap (that of a single row is its length)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (rows, cols)
+            and t.get_device() == dev):
+        ld, unit = t.stride()
+        if rows <= 1:
+            if unit == 1 or cols <= 1:
+                return cols
+        elif (unit == 1 or cols == 1) and ld >= cols:
+            return ld
+    _refuse(t, (rows, cols), dtypes, what, "row-major with unit column stride")
 
 
-def _require_vector(t: torch.Tensor, shape, dtype, what: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}")
-    _on_current_device(t, what)
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+def _dense(t, shape, dtypes, dev: int, what: str) -> int:
+    """Address of a contiguous operand."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, shape, dtypes, what, "contiguous")
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -566,28 +579,44 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     return t
 
 
-def _norm_args(block, residual, w_pre, w_post, gate):
-    """Checks of the operands shared by the norm and its gradient; returns the
-    number of gates (0 without one)."""
-    if not isinstance(block, torch.Tensor) or block.dim() != 2:
-        raise ValueError("block must be a 2-D tensor")
-    rows, cols = block.shape
-    _require_rows(block, (rows, cols), tuple(_X_DTYPE), "block")
-    _require_rows(residual, (rows, cols), tuple(_X_DTYPE), "residual")
-    if not isinstance(w_pre, torch.Tensor) or w_pre.dtype not in _X_DTYPE:
-        raise ValueError("w_pre must be a bf16 or fp32 tensor")
-    _require_vector(w_pre, (cols,), w_pre.dtype, "w_pre")
-    if w_post is not None:
-        _require_vector(w_post, (cols,), w_pre.dtype, "w_post")
+def _workspace_ptr(t, need: int, dev: int) -> int:
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.get_device() == dev
+            and t.is_contiguous() and t.numel() >= need):
+        return t.data_ptr()
+    raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on the "
+                     "current CUDA device")
+
+
+def _norm_weights(rows: int, cols: int, w_pre, w_post, gate, dev: int):
+    """(w_post, w_pre, gate addresses, gates, dtype code) of the norm's weights,
+    which share one type; gates is 0 without a gate."""
+    w_type = getattr(w_pre, "dtype", None)
+    if w_type not in _X_DTYPE:
+        _refuse(w_pre, (cols,), tuple(_X_DTYPE), "w_pre", "contiguous")
+    kinds = (w_type,)
+    pre = _dense(w_pre, (cols,), kinds, dev, "w_pre")
+    post = None if w_post is None else _dense(w_post, (cols,), kinds, dev, "w_post")
     if gate is None:
-        return 0
-    if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
-        raise ValueError("gate must be a 1-D or 2-D tensor")
-    gates = 1 if gate.dim() == 1 else gate.shape[0]
-    _require_vector(gate, (cols,) if gate.dim() == 1 else (gates, cols), w_pre.dtype, "gate")
+        return post, pre, None, 0, _X_DTYPE[w_type]
+    shape = getattr(gate, "shape", ())
+    gates = shape[0] if len(shape) == 2 else 1
+    at = _dense(gate, (gates, cols) if len(shape) == 2 else (cols,), kinds, dev, "gate")
     if gates < 1 or rows % gates:
         raise ValueError(f"{rows} rows cannot be split evenly over {gates} gates")
-    return gates
+    return post, pre, at, gates, _X_DTYPE[w_type]
+
+
+def _block_rows(block):
+    if not isinstance(block, torch.Tensor) or block.dim() != 2:
+        raise ValueError("block must be a 2-D bf16 or fp32 tensor")
+    return block.shape
+
+
+def _empty(shape, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+_WIDE = tuple(_X_DTYPE)
 
 
 def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tensor,
@@ -601,22 +630,27 @@ def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tens
     the block.  gate: [cols], or [gates, cols] with one gate per
     rows/gates consecutive rows.  w_pre, w_post and gate share one type.
     out_residual may be `residual` itself."""
-    gates = _norm_args(block, residual, w_pre, w_post, gate)
-    rows, cols = block.shape
+    rows, cols = _block_rows(block)
+    dev = torch.cuda.current_device()
+    ldb = _rows_of(block, rows, cols, _WIDE, dev, "block")
+    ldr = _rows_of(residual, rows, cols, _WIDE, dev, "residual")
+    post, pre, at, gates, w_code = _norm_weights(rows, cols, w_pre, w_post, gate, dev)
     if out_residual is None:
-        out_residual = torch.empty((rows, cols), dtype=residual.dtype, device=block.device)
+        out_residual, ldo = _empty((rows, cols), residual), cols
+    else:
+        ldo = _rows_of(out_residual, rows, cols, (residual.dtype,), dev, "out_residual")
     if out is None:
-        out = torch.empty((rows, cols), dtype=block.dtype, device=block.device)
-    _require_rows(out_residual, (rows, cols), (residual.dtype,), "out_residual")
-    _require_rows(out, (rows, cols), (block.dtype,), "out")
+        out, ldy = _empty((rows, cols), block), cols
+    else:
+        ldy = _rows_of(out, rows, cols, (block.dtype,), dev, "out")
     if rows == 0:
         return out_residual, out
-    st = mx_norm_residual(rows, cols, _ptr(block), _row_stride(block), _X_DTYPE[block.dtype],
-                          _ptr(residual), _row_stride(residual), _X_DTYPE[residual.dtype],
-                          _ptr(w_post), _ptr(w_pre), _ptr(gate), gates, _X_DTYPE[w_pre.dtype],
-                          alpha, eps, _ptr(out_residual), _row_stride(out_residual), _ptr(out),
-                          _row_stride(out), _stream(stream))
-    _check("mx_norm_residual", st)
+    st = lib().mx_norm_residual(
+        rows, cols, block.data_ptr(), ldb, _X_DTYPE[block.dtype], residual.data_ptr(), ldr,
+        _X_DTYPE[residual.dtype], post, pre, at, gates, w_code, alpha, eps,
+        out_residual.data_ptr(), ldo, out.data_ptr(), ldy, _stream(stream))
+    if st:
+        raise MxError("mx_norm_residual", st)
     return out_residual, out
 
 
@@ -641,36 +675,43 @@ def norm_residual_backward(d_residual: torch.Tensor | None, d_y: torch.Tensor, b
     The column sums run in a fixed order: the same inputs give the same bits.
     workspace: uint8, mx_norm_residual_backward_workspace(rows, cols, gates)
     bytes; allocated here when None."""
-    gates = _norm_args(block, residual, w_pre, w_post, gate)
-    rows, cols = block.shape
-    _require_rows(d_y, (rows, cols), (block.dtype,), "d_y")
+    rows, cols = _block_rows(block)
+    dev = torch.cuda.current_device()
+    ldb = _rows_of(block, rows, cols, _WIDE, dev, "block")
+    ldr = _rows_of(residual, rows, cols, _WIDE, dev, "residual")
+    lddy = _rows_of(d_y, rows, cols, (block.dtype,), dev, "d_y")
+    ldd = cols
     if d_residual is not None:
-        _require_rows(d_residual, (rows, cols), (residual.dtype,), "d_residual")
-    dev = block.device
-    grads = NormResidualGrads(
-        torch.empty((rows, cols), dtype=block.dtype, device=dev),
-        torch.empty((rows, cols), dtype=residual.dtype, device=dev),
-        torch.empty(cols, dtype=torch.float32, device=dev),
-        None if w_post is None else torch.empty(cols, dtype=torch.float32, device=dev),
-        None if gate is None else torch.empty(gate.shape, dtype=torch.float32, device=dev))
-    need = mx_norm_residual_backward_workspace(rows, cols, gates)
+        ldd = _rows_of(d_residual, rows, cols, (residual.dtype,), dev, "d_residual")
+    post, pre, at, gates, w_code = _norm_weights(rows, cols, w_pre, w_post, gate, dev)
+    c = lib()
+    need = c.mx_norm_residual_backward_workspace(rows, cols, gates)
     if workspace is None:
-        workspace = _scratch(need, dev, stream)
-    else:
-        _require_scales(workspace, need, "workspace")
-    # an empty tensor has no address: any device pointer stands in for one
-    # that nothing is read from or written to
-    at = (lambda t: _ptr(t) or _ptr(workspace)) if rows == 0 else _ptr
-    st = mx_norm_residual_backward(
-        rows, cols, _ptr(d_residual) or None,
-        cols if d_residual is None else _row_stride(d_residual), at(d_y), _row_stride(d_y),
-        at(block), _row_stride(block), _X_DTYPE[block.dtype], at(residual), _row_stride(residual),
-        _X_DTYPE[residual.dtype], _ptr(w_post), _ptr(w_pre), _ptr(gate), gates,
-        _X_DTYPE[w_pre.dtype], alpha, eps, at(grads.block), cols, at(grads.residual), cols,
-        _ptr(grads.w_post), _ptr(grads.w_pre), _ptr(grads.gate), _ptr(workspace),
-        workspace.numel(), _stream(stream))
-    _check("mx_norm_residual_backward", st)
+        workspace = _scratch(need, block.device, stream)
+    ws = _workspace_ptr(workspace, need, dev)
+    # the weights' gradients are views of one allocation
+    parts = 1 + (w_post is not None) + gates
+    sums = torch.empty((parts, cols), dtype=torch.float32, device=block.device)
+    grads = NormResidualGrads(_empty((rows, cols), block), _empty((rows, cols), residual), sums[0],
+                              None if w_post is None else sums[1],
+                              None if gate is None else sums[parts - gates:].view(gate.shape))
+    first = sums.data_ptr()
+    empty = rows == 0  # such tensors have no address; any device address stands in, unused
+    st = c.mx_norm_residual_backward(
+        rows, cols, None if d_residual is None or empty else d_residual.data_ptr(), ldd,
+        ws if empty else d_y.data_ptr(), lddy, ws if empty else block.data_ptr(), ldb,
+        _X_DTYPE[block.dtype], ws if empty else residual.data_ptr(), ldr,
+        _X_DTYPE[residual.dtype], post, pre, at, gates, w_code, alpha, eps,
+        ws if empty else grads.block.data_ptr(), cols, ws if empty else grads.residual.data_ptr(),
+        cols, None if w_post is None else first + 4 * cols, first,
+        None if gate is None else first + 4 * cols * (parts - gates), ws, workspace.numel(),
+        _stream(stream))
+    if st:
+        raise MxError("mx_norm_residual_backward", st)
     return grads
+
+
+_CODES = (torch.uint8,)
 
 
 def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: MxTensor,
@@ -689,44 +730,47 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: Mx
     here when None."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D tensor")
-    tokens, hidden = x.shape
-    _require_rows(x, (tokens, hidden), (torch.bfloat16,), "x")
-    if not isinstance(router, torch.Tensor) or router.dim() != 2 or router.dtype not in _X_DTYPE:
-        raise ValueError("router must be a 2-D bf16 or fp32 tensor")
-    experts = router.shape[0]
-    _require_vector(router, (experts, hidden), router.dtype, "router")
+    if not isinstance(router, torch.Tensor) or router.dim() != 2:
+        raise ValueError("router must be a 2-D tensor")
     if gate.codes.dim() != 3 or gate.fmt != up.fmt:
         raise ValueError("gate and up must be [experts, inter, hidden] codes of one format")
-    inter = gate.codes.shape[1]
-    for t, shape, what in ((gate, (experts, inter, storage_bytes(gate.fmt, hidden)), "gate"),
-                           (up, (experts, inter, storage_bytes(up.fmt, hidden)), "up"),
-                           (down, (experts, hidden, storage_bytes(down.fmt, inter)), "down")):
-        _require_codes(t.codes, shape, what)
-    _require_scales(gate.scales, experts * mx_scale_bytes(inter, hidden), "gate")
-    _require_scales(up.scales, experts * mx_scale_bytes(inter, hidden), "up")
-    _require_scales(down.scales, experts * mx_scale_bytes(hidden, inter), "down")
+    tokens, hidden = x.shape
+    experts, inter = router.shape[0], gate.codes.shape[1]
     if not 1 <= top_k <= experts:
         raise ValueError(f"top_k must be 1 to {experts}, got {top_k}")
-    dev = x.device
+    dev = torch.cuda.current_device()
+    ldx = _rows_of(x, tokens, hidden, (torch.bfloat16,), dev, "x")
+    wr = _dense(router, (experts, hidden), _WIDE, dev, "router")
+    k_gu, k_d = storage_bytes(gate.fmt, hidden), storage_bytes(down.fmt, inter)
+    g = _dense(gate.codes, (experts, inter, k_gu), _CODES, dev, "gate codes")
+    u = _dense(up.codes, (experts, inter, k_gu), _CODES, dev, "up codes")
+    d = _dense(down.codes, (experts, hidden, k_d), _CODES, dev, "down codes")
+    c = lib()
+    s_gu = experts * c.mx_scale_bytes(inter, hidden)
+    s_d = experts * c.mx_scale_bytes(hidden, inter)
+    for t, need, what in ((gate, s_gu, "gate"), (up, s_gu, "up"), (down, s_d, "down")):
+        s = t.scales
+        if not (s.dtype is torch.uint8 and s.get_device() == dev and s.numel() >= need
+                and s.is_contiguous()):
+            _require_scales(s, need, what)
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=dev)
-    _require_rows(out, (tokens, hidden), (torch.bfloat16,), "out")
-    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+        out, ldy = _empty((tokens, hidden), x), hidden
+    else:
+        ldy = _rows_of(out, tokens, hidden, (torch.bfloat16,), dev, "out")
+    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
+    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
     if tokens > 0:
-        need = mx_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k)
+        need = c.mx_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k)
         if workspace is None:
-            workspace = _scratch(need, dev, stream)
-        else:
-            _require_scales(workspace, need, "workspace")
-        st = mx_moe_few_tokens(tokens, hidden, inter, experts, top_k, _ptr(x), _row_stride(x),
-                               _ptr(router), _X_DTYPE[router.dtype], _ptr(gate.codes),
-                               _ptr(gate.scales), _ptr(up.codes), _ptr(up.scales), FMT[gate.fmt],
-                               _ptr(down.codes), _ptr(down.scales), FMT[down.fmt],
-                               int(renormalize), _ptr(out), _row_stride(out), _ptr(ids),
-                               _ptr(weights), _ptr(workspace), workspace.numel(),
-                               _stream(stream))
-        _check("mx_moe_few_tokens", st)
+            workspace = _scratch(need, x.device, stream)
+        ws = _workspace_ptr(workspace, need, dev)
+        st = c.mx_moe_few_tokens(
+            tokens, hidden, inter, experts, top_k, x.data_ptr(), ldx, wr, _X_DTYPE[router.dtype],
+            g, gate.scales.data_ptr(), u, up.scales.data_ptr(), FMT[gate.fmt], d,
+            down.scales.data_ptr(), FMT[down.fmt], int(renormalize), out.data_ptr(), ldy,
+            ids.data_ptr(), weights.data_ptr(), ws, workspace.numel(), _stream(stream))
+        if st:
+            raise MxError("mx_moe_few_tokens", st)
     return (out, ids, weights) if return_routing else out
 
 

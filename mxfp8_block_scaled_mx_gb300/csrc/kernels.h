@@ -173,28 +173,30 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
 struct MoeFewParams {
   const void* x;         // bf16 [tokens, hidden], ldx
   const void* router;    // [experts, hidden]
-  const uint8_t* gate;   // [experts, inter, hidden] codes
-  const uint8_t* up;
-  const uint8_t* down;   // [experts, hidden, inter] codes
   const uint8_t* gate_scales;
   const uint8_t* up_scales;
   const uint8_t* down_scales;
   void* y;               // bf16 [tokens, hidden], ldy
   int32_t* ids;          // [tokens, top_k]
   float* weights;        // [tokens, top_k]
-  void* workspace;
-  float* logits;
-  float* h;
-  int64_t hidden, inter, ldx, ldy;
+  uint8_t* workspace;
+  int64_t ldx, ldy;
+  int32_t hidden, inter;
   int32_t tokens, experts, top_k, renormalize;
   int32_t router_fp32;
-  int32_t fmt_gu, fmt_d;   // element formats (mx_fmt)
-  int32_t bits_gu, bits_d; // bits of storage per code
+  int32_t type_gu, type_d;  // tensor-core operand type codes
+  int32_t bits_gu, bits_d;  // bits of storage per code
+  uint32_t* status;         // device status word
+  uint64_t wait_limit_ns;
 };
 
 size_t moe_few_workspace(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                          int32_t top_k);
-cudaError_t launch_moe_few(const MoeFewParams& p, cudaStream_t stream);
+// tmap_gate, tmap_up: codes [experts * inter, hidden]; tmap_down: codes
+// [experts * hidden, inter]; boxes of 128 elements x 128 rows.
+cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
+                           const CUtensorMap& tmap_up, const CUtensorMap& tmap_down, int num_sms,
+                           cudaStream_t stream);
 
 // Clears the bits `bits` of the device status word (atomically, so bits
 // set meanwhile by kernels on other streams survive).

@@ -3,7 +3,33 @@
 //   z = x router^T, the top_k largest per token win, w = softmax share;
 //   y = sum over the winners e of w_e down_e (silu(gate_e x) * (up_e x))
 //
-// First form: four launches, one warp per dot product on the FP32 units.
+// What bounds it is reading the chosen experts' weights once.  Weights are
+// the A operand of the tensor cores (128 rows a tile, straight from their MX
+// storage, block scales applied by the MMA), tokens the B operand (N = the
+// token count rounded up to 16), so that nothing is decoded in registers
+// and a token more costs nothing until N outgrows the weights' transfer.
+//
+// Activations keep their precision on FP8 tensor cores as a sum of two E4M3
+// terms per value: hi = E4M3(v / S), lo = E4M3((v / S - hi) * 32), with S the
+// power of two that brings the 32-element block's largest value into
+// [128, 256).  hi has 4 significant bits, the remainder at most 1/16 of v, so
+// hi + lo / 32 holds 8 significant bits: a bf16 exactly (down to 2^-14 of its
+// block's largest), and the FP32 activation rounded once as bf16 would be.
+// Both terms multiply the same A tile into the same accumulator.
+//
+// Two launches.  moe_router_kernel forms the logits and x's B operand.
+// moe_experts_kernel (one block per SM, cooperative) lets every block choose
+// the winners for itself (identical arithmetic), then works through
+//   phase 1  gate and up: items of 128 channels of one active expert, K = hidden
+//   phase 2  down: items of 128 channels of y, K = all active experts'
+//            channels one after the other; the routing weights are in the
+//            activations, so one accumulator sums over experts.
+// Either phase's 128 x 128 tiles are dealt out as one sequence, evenly and in
+// order; an item whose tiles fall to several blocks is summed by the one
+// that finishes last, in block order (same inputs, same bits).  Between the
+// phases blocks wait for all activations, with their rings already full of
+// down tiles.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -11,191 +37,791 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "status.cuh"
 
 namespace mx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxTokens = 64;
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopK = 32;
+constexpr int kMaxBlocks = 192;     // workspaces are sized for this many SMs
+constexpr int kTile = 128;          // rows and K of a weight tile
+constexpr int kTileBytes = kTile * kTile;
+constexpr int kSfBytes = 512;       // scales of a tile, and of a B term
+constexpr int kTerms = 2;
+constexpr int kMaxStages = 9;
 
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__host__ __device__ constexpr int pad_tokens(int t) { return (t + 15) / 16 * 16; }
+__host__ __device__ constexpr int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
+
+// One K tile of the B operand as the ring holds it: per term `pad` rows of
+// 128 codes (128-byte swizzle), then per term a tile of scales.
+__host__ __device__ constexpr int64_t code_bytes(int pad) { return int64_t(kTerms) * pad * kTile; }
+__host__ __device__ constexpr int64_t record_bytes(int pad) {
+  return code_bytes(pad) + kTerms * kSfBytes;
 }
 
-__device__ __forceinline__ float bf16(const void* p, int64_t i) {
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// Workspace: counters, logits, x's records, the activations' records, parts.
+struct Layout {
+  int64_t logits, x, h, parts, bytes;
+};
+__host__ __device__ inline Layout layout(int tokens, int64_t hidden, int64_t inter, int experts,
+                                         int top_k) {
+  const int pad = pad_tokens(tokens);
+  const int64_t active = experts < tokens * top_k ? experts : tokens * top_k;
+  Layout l;
+  l.logits = 4096;
+  l.x = l.logits + (int64_t(tokens) * experts * 4 + 255) / 256 * 256;
+  l.h = l.x + tiles(hidden) * record_bytes(pad);
+  l.parts = l.h + active * tiles(inter) * record_bytes(pad);
+  l.bytes = l.parts + int64_t(kMaxBlocks) * 2 * 2 * pad * kTile * 4;
+  return l;
+}
+constexpr int kDoneWord = 2 * kMaxBlocks;  // after the two phases' tickets
+static_assert((kDoneWord + 1) * 4 <= 4096, "counters");
+
+// Byte of code k (0..127) of row t in a term.
+__device__ __forceinline__ uint32_t code_at(uint32_t t, uint32_t k) {
+  return t * 128 + (((k >> 4) ^ (t & 7)) << 4) + (k & 15);
+}
+// Byte of the scale of block j (0..3) of row t in a term's scale tile.
+__device__ __forceinline__ uint32_t scale_at(uint32_t t, uint32_t j) {
+  return (t & 31) * 16 + (t >> 5) * 4 + j;
 }
 
-// Value of code `i` of a row.
-__device__ __forceinline__ float decode(const uint8_t* row, int64_t i, int32_t fmt) {
-  uint32_t code, ebits, mbits, bias;
-  if (fmt == 7) {
-    code = (row[i >> 1] >> ((i & 1) * 4)) & 15u;
-    ebits = 2, mbits = 1, bias = 1;
+__device__ __forceinline__ uint32_t e4m3_pair(float hi, float lo) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(code)));
+  float f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h2));
+  return f;
+}
+
+// A warp writes its 32 values (one block, one per lane) of row t, block j of a
+// record as two E4M3 terms.
+__device__ __forceinline__ void write_block(uint8_t* record, int pad, uint32_t t, uint32_t j,
+                                            float v) {
+  const uint32_t lane = lane_id();
+  const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
+  // the exponent of S; not below -122, so that lo's scale, S / 32, exists
+  int e = static_cast<int>(amax >> 23) - 127 - 7;
+  e = e < -122 ? -122 : e;
+  uint32_t hi, lo;
+  if (amax >= 0x7F800000u) {  // NaN or Inf in the block
+    hi = lo = 0x7Fu;
+    e = 0;
   } else {
-    code = row[i];
-    ebits = fmt == 0 ? 4 : 5, mbits = fmt == 0 ? 3 : 2, bias = fmt == 0 ? 7 : 15;
+    const float s = v * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    hi = e4m3_pair(0.f, s) & 0xFFu;
+    lo = e4m3_pair(0.f, (s - e4m3_value(hi)) * 32.f) & 0xFFu;
   }
-  const uint32_t e = (code >> mbits) & ((1u << ebits) - 1), m = code & ((1u << mbits) - 1);
-  const bool neg = code >> (ebits + mbits);
-  if ((fmt == 0 && (code & 0x7Fu) == 0x7Fu) || (fmt == 1 && e == 31u && m != 0))
-    return __int_as_float(0x7FC00000);
-  if (fmt == 1 && e == 31u) return __int_as_float(neg ? 0xFF800000 : 0x7F800000);
-  const float v = e == 0 ? ldexpf(static_cast<float>(m), 1 - static_cast<int>(bias + mbits))
-                         : ldexpf(static_cast<float>((1u << mbits) + m),
-                                  static_cast<int>(e) - static_cast<int>(bias + mbits));
-  return neg ? -v : v;
+  const uint32_t at = code_at(t, j * 32 + lane);
+  record[at] = static_cast<uint8_t>(hi);
+  record[pad * kTile + at] = static_cast<uint8_t>(lo);
+  if (lane == 0) {
+    uint8_t* sf = record + code_bytes(pad) + scale_at(t, j);
+    sf[0] = static_cast<uint8_t>(e + 127);
+    sf[kSfBytes] = static_cast<uint8_t>(e + 127 - 5);
+  }
 }
 
-// Scale of block j of row r in an expert's swizzled scale matrix.
-__device__ __forceinline__ float block_scale(const uint8_t* s, int64_t r, int64_t j,
-                                             int64_t k_tiles) {
-  const uint32_t c = s[((r >> 7) * k_tiles + (j >> 2)) * 512 + (r & 31) * 16 +
-                       ((r & 127) >> 5) * 4 + (j & 3)];
-  return c == 255u ? __int_as_float(0x7FC00000)
-                   : __int_as_float(c == 0 ? 0x00400000 : static_cast<int>(c << 23));
+// ------------------------------------------------------------------ router and x
+
+constexpr int kRouterThreads = 256;
+constexpr int kRouterExperts = 2;   // per block, four warps each
+constexpr int kRouterTokens = 8;    // per block: the router's rows are read tokens / 8 times
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) moe_logits_kernel(const MoeFewParams p) {
+// Blocks [0, logit_blocks): logits of two experts for eight tokens.  The rest:
+// x's records, a warp per token and K tile.  Block 0 also clears the counters.
+__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFewParams p,
+                                                                    int logit_blocks) {
+  __shared__ float part[kRouterThreads / 32][kRouterTokens];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(p.tokens) * p.experts) return;
-  const int64_t t = w / p.experts, e = w % p.experts;
-  float s = 0.f;
-  for (int64_t c = lane_id(); c < p.hidden; c += 32) {
-    const float r = p.router_fp32 ? static_cast<const float*>(p.router)[e * p.hidden + c]
-                                  : bf16(p.router, e * p.hidden + c);
-    s += bf16(p.x, t * p.ldx + c) * r;
+  const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= kDoneWord; i += kRouterThreads)
+      reinterpret_cast<uint32_t*>(p.workspace)[i] = 0;
+  if (static_cast<int>(blockIdx.x) >= logit_blocks) {
+    const int kt_count = static_cast<int>(tiles(p.hidden));
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) - logit_blocks) * (kRouterThreads / 32) + warp;
+    const int t = static_cast<int>(w / kt_count), kt = static_cast<int>(w % kt_count);
+    if (t >= p.tokens) return;
+    const int pad = pad_tokens(p.tokens);
+    uint8_t* record = p.workspace + l.x + kt * record_bytes(pad);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = kt * kTile + j * 32 + static_cast<int>(lane);
+      write_block(record, pad, t, j, c < p.hidden ? __bfloat162float(x[t * p.ldx + c]) : 0.f);
+    }
+    return;
   }
-  s = warp_sum(s);
-  if (lane_id() == 0) p.logits[w] = s;
+  const int groups = (p.experts + kRouterExperts - 1) / kRouterExperts;
+  const int e = static_cast<int>(blockIdx.x) % groups * kRouterExperts + static_cast<int>(warp) / 4;
+  const int t0 = static_cast<int>(blockIdx.x) / groups * kRouterTokens;
+  const int nt = p.tokens - t0 < kRouterTokens ? p.tokens - t0 : kRouterTokens;
+  float sum[kRouterTokens];
+#pragma unroll
+  for (int i = 0; i < kRouterTokens; ++i) sum[i] = 0.f;
+  if (e < p.experts) {
+    const int64_t row = static_cast<int64_t>(e) * p.hidden;
+#pragma unroll 2
+    for (int c = (static_cast<int>(warp & 3) * 32 + static_cast<int>(lane)) * 8; c < p.hidden;
+         c += 4 * 32 * 8) {
+      float w[8];
+      if (p.router_fp32) {
+        const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + row + c);
+        const float4 a = r[0], b = r[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else {
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.router) + row + c), w);
+      }
+#pragma unroll
+      for (int i = 0; i < kRouterTokens; ++i) {
+        if (i >= nt) break;
+        float v[8];
+        unpack8(*reinterpret_cast<const uint4*>(x + (t0 + i) * p.ldx + c), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[i] += w[j] * v[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRouterTokens; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    if (lane == 0) part[warp][i] = sum[i];
+  }
+  __syncthreads();
+  if ((warp & 3) == 0 && e < p.experts && static_cast<int>(lane) < nt) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += part[warp + i][lane];
+    reinterpret_cast<float*>(p.workspace + l.logits)[static_cast<int64_t>(t0 + lane) * p.experts + e] = s;
+  }
 }
 
-// Order-preserving key of a logit (equal zeros alike, NaN below everything)
-// with the expert behind it, so that among equal logits the lowest wins.
-__device__ __forceinline__ uint64_t logit_key(float z, uint32_t e) {
+// ------------------------------------------------------------------ experts
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr uint32_t kTmemCols = 512;
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2], mma_done;
+  uint32_t tmem, abort, ticket;
+  int32_t active;                           // number of active experts
+  uint32_t chosen[kMaxExperts / 32];        // bit per expert
+  uint16_t expert[kMaxExperts];             // active experts, ascending
+  float share[kMaxTokens];                  // of the item's expert, -1: not chosen
+  uint16_t id[kMaxTokens * kMaxTopK];       // [tokens][top_k]
+  float weight[kMaxTokens * kMaxTopK];
+};
+
+// Order-preserving key of a logit: equal zeros alike, NaN below everything,
+// never 0.
+__device__ __forceinline__ uint32_t logit_key(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);
-  const uint32_t k = z != z ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return static_cast<uint64_t>(k) << 32 | (0xFFFFFFFFu - e);
+  return z != z ? 1u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(32) moe_select_kernel(const MoeFewParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t t = blockIdx.x;
-  const float* z = p.logits + t * p.experts;
+// A warp chooses token t's winners: largest logit first, the lowest expert
+// among equal ones.
+__device__ __forceinline__ void select_token(const MoeFewParams& p, const float* logits, int t,
+                                             Shared* sh) {
+  constexpr int kPer = kMaxExperts / 32;
+  const uint32_t lane = lane_id();
+  const float* row = logits + static_cast<int64_t>(t) * p.experts;
+  float z[kPer];
   float top = -INFINITY;
-  for (int e = lane_id(); e < p.experts; e += 32) top = fmaxf(top, z[e]);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = j * 32 + static_cast<int>(lane);
+    z[j] = e < p.experts ? row[e] : -INFINITY;
+    top = fmaxf(top, z[j]);
+  }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float sum = 0.f;
-  for (int e = lane_id(); e < p.experts; e += 32) sum += expf(z[e] - top);
-  sum = warp_sum(sum);
-  uint64_t last = ~0ull;
+  uint32_t key[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const bool in = j * 32 + static_cast<int>(lane) < p.experts;
+    key[j] = in ? logit_key(z[j]) : 0u;
+    if (j * 32 < p.experts) {
+      z[j] = in ? expf(z[j] - top) : 0.f;
+      sum += z[j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float chosen = 0.f;
   for (int k = 0; k < p.top_k; ++k) {
-    uint64_t best = 0;
-    for (int e = lane_id(); e < p.experts; e += 32) {
-      const uint64_t key = logit_key(z[e], e);
-      if (key < last && key > best) best = key;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-      if (other > best) best = other;
-    }
-    last = best;
-    const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-    const float w = expf(z[e] - top) / sum;
+    uint32_t best = 0u, at = 0xFFFFFFFFu;
+    float w = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j * 32 + lane;
+        w = z[j];
+      }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
+    w = __shfl_sync(0xffffffffu, w, e & 31u) / sum;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (e == j * 32 + lane) key[j] = 0u;
     chosen += w;
-    if (lane_id() == 0) {
-      p.ids[t * p.top_k + k] = e;
-      p.weights[t * p.top_k + k] = w;
+    if (lane == 0) {
+      sh->id[t * p.top_k + k] = static_cast<uint16_t>(e);
+      sh->weight[t * p.top_k + k] = w;
+      atomicOr(&sh->chosen[e >> 5], 1u << (e & 31u));
     }
   }
   __syncwarp();
   if (p.renormalize)
-    for (int k = lane_id(); k < p.top_k; k += 32) p.weights[t * p.top_k + k] /= chosen;
+    for (int k = lane; k < p.top_k; k += 32) sh->weight[t * p.top_k + k] /= chosen;
 }
 
-// One warp per (token, choice, channel of the expert).
-__global__ void __launch_bounds__(kThreads) moe_gate_up_kernel(const MoeFewParams p) {
+// A block's run of tiles of one item.
+struct Segment {
+  int32_t item, k0, k1;   // tiles [k0, k1) of the item's K
+};
+
+// One phase's tiles, `per` of each of `items` items in sequence, and this
+// block's share [lo, hi).  The first n blocks share them, each at least one.
+struct Share {
+  int64_t total, n, lo, hi;
+  int32_t per;
+  __device__ __forceinline__ Share(int64_t items, int64_t per_item)
+      : total(items * per_item), per(static_cast<int32_t>(per_item)) {
+    n = total < gridDim.x ? total : gridDim.x;
+    lo = hi = total;
+    if (blockIdx.x < n) {
+      lo = total * blockIdx.x / n;
+      hi = total * (blockIdx.x + 1) / n;
+    }
+  }
+  // the segment that starts at tile u
+  __device__ __forceinline__ Segment at(int64_t u) const {
+    Segment s;
+    s.item = static_cast<int32_t>(u / per);
+    s.k0 = static_cast<int32_t>(u - static_cast<int64_t>(s.item) * per);
+    const int64_t left = hi - u;
+    s.k1 = left < per - s.k0 ? s.k0 + static_cast<int32_t>(left) : per;
+    return s;
+  }
+  __device__ __forceinline__ int block_of(int64_t u) const {
+    return static_cast<int>(((u + 1) * n - 1) / total);
+  }
+  // which of block b's two parts belongs to `item`
+  __device__ __forceinline__ int slot_of(int b, int32_t item) const {
+    return total * b / n / per == item ? 0 : 1;
+  }
+};
+
+__device__ __forceinline__ void epi_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
+// Waits until *word reaches `want`.
+__device__ __forceinline__ bool wait_count(const uint32_t* word, uint32_t want,
+                                           volatile uint32_t* abort_flag, uint32_t* status,
+                                           uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  uint32_t spins = 0;
+  while (true) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    if (v >= want) return true;
+    if ((++spins & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > limit_ns) {
+        record_device_status(status, MX_DEV_TIMEOUT);
+        *abort_flag = 1u;
+        return false;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_experts_kernel(const __grid_constant__ CUtensorMap tmap_gate,
+                       const __grid_constant__ CUtensorMap tmap_up,
+                       const __grid_constant__ CUtensorMap tmap_down, const MoeFewParams p,
+                       int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int pad = pad_tokens(p.tokens);
+  const uint32_t b_bytes = static_cast<uint32_t>(code_bytes(pad));
+  uint8_t* sA = smem;                                 // [stages][16 KB]
+  uint8_t* sB = sA + stages * kTileBytes;             // [stages][b_bytes]
+  uint8_t* sSf = sB + stages * b_bytes;               // [stages][A, B hi, B lo][512]
+  Shared* sh = reinterpret_cast<Shared*>(sSf + stages * (1 + kTerms) * kSfBytes);
+  volatile uint32_t* s_abort = &sh->abort;
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.workspace);
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->acc_full[i], 1);
+      mbar_init(&sh->acc_empty[i], kEpiWarps);
+    }
+    mbar_init(&sh->mma_done, 1);
+    sh->abort = 0u;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmap_gate);
+    tma_prefetch_desc(&tmap_up);
+    tma_prefetch_desc(&tmap_down);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < kMaxExperts / 32; i += kThreads) sh->chosen[i] = 0u;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh->tmem;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(p.tokens) * p.top_k * p.inter) return;
-  const int64_t slot = w / p.inter, i = w % p.inter, t = slot / p.top_k;
-  const int64_t e = p.ids[slot];
-  const int64_t k_tiles = (p.hidden + 127) / 128;
-  const int64_t smat = (p.inter + 127) / 128 * k_tiles * 512;
-  const int64_t row = p.hidden * p.bits_gu / 8;
-  const uint8_t* g = p.gate + (e * p.inter + i) * row;
-  const uint8_t* u = p.up + (e * p.inter + i) * row;
-  float a = 0.f, b = 0.f;
-  for (int64_t c = lane_id(); c < p.hidden; c += 32) {
-    const float x = bf16(p.x, t * p.ldx + c);
-    a += x * decode(g, c, p.fmt_gu) * block_scale(p.gate_scales + e * smat, i, c >> 5, k_tiles);
-    b += x * decode(u, c, p.fmt_gu) * block_scale(p.up_scales + e * smat, i, c >> 5, k_tiles);
+
+  // Routing: every block for itself, block 0 reports it.
+  const float* logits = reinterpret_cast<const float*>(p.workspace + l.logits);
+  for (int t = warp; t < p.tokens; t += kThreads / 32) select_token(p, logits, t, sh);
+  __syncthreads();
+  if (warp == 2) {
+    uint32_t before = 0;
+    for (int i = 0; i * 32 < p.experts; ++i) {
+      const uint32_t bits = sh->chosen[i];
+      if (bits >> lane & 1u)
+        sh->expert[before + __popc(bits & ((1u << lane) - 1u))] = static_cast<uint16_t>(i * 32 + lane);
+      before += __popc(bits);
+    }
+    if (lane == 0) sh->active = static_cast<int32_t>(before);
   }
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (lane_id() == 0) p.h[w] = a / (1.f + expf(-a)) * b * p.weights[slot];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.tokens * p.top_k; i += kThreads) {
+      p.ids[i] = sh->id[i];
+      p.weights[i] = sh->weight[i];
+    }
+  __syncthreads();
+
+  const int32_t it_count = static_cast<int32_t>(tiles(p.inter));
+  const int32_t ht_count = static_cast<int32_t>(tiles(p.hidden));
+  const int32_t items1 = sh->active * it_count;       // (expert, 128 channels)
+  const Share share1(items1, ht_count);               // each tile: gate and up
+  const Share share2(ht_count, items1);
+  const uint32_t tx_b = b_bytes + kTerms * kSfBytes;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t tx_gu = kTileBytes * p.bits_gu / 8 + kSfBytes;
+    const uint32_t tx_d = kTileBytes * p.bits_d / 8 + kSfBytes;
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    auto next = [&] {
+      ++issued;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    auto wait_empty = [&] {
+      return mbar_wait_warp(&sh->empty[stage], phase ^ 1u, s_abort, p.status, p.wait_limit_ns);
+    };
+    auto load_a = [&](const CUtensorMap* map, const uint8_t* sf, int32_t x, int32_t y) {
+      tma_load_2d(sA + stage * kTileBytes, map, &sh->full[stage], x, y);
+      bulk_load(sSf + stage * (1 + kTerms) * kSfBytes, sf, kSfBytes, &sh->full[stage]);
+    };
+    auto load_b = [&](int s, const uint8_t* record) {
+      bulk_load(sB + s * b_bytes, record, b_bytes, &sh->full[s]);
+      bulk_load(sSf + (s * (1 + kTerms) + 1) * kSfBytes, record + b_bytes, kTerms * kSfBytes,
+                &sh->full[s]);
+    };
+    // phase 1: gate tile with x's record, then the up tile (same record)
+    const int64_t mat1 = static_cast<int64_t>(it_count) * ht_count * kSfBytes;
+    for (int64_t u = share1.lo; u < share1.hi && ok;) {
+      const Segment g = share1.at(u);
+      const int32_t e = sh->expert[g.item / it_count], tile = g.item % it_count;
+      const int32_t y = e * p.inter + tile * kTile;
+      for (int32_t k = g.k0; k < g.k1 && ok; ++k) {
+        const int64_t sf = e * mat1 + (static_cast<int64_t>(tile) * ht_count + k) * kSfBytes;
+        if (!(ok = wait_empty())) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh->full[stage], tx_gu + tx_b);
+          load_a(&tmap_gate, p.gate_scales + sf, k * kTile, y);
+          load_b(stage, p.workspace + l.x + k * record_bytes(pad));
+        }
+        __syncwarp();
+        next();
+        if (!(ok = wait_empty())) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh->full[stage], tx_gu);
+          load_a(&tmap_up, p.up_scales + sf, k * kTile, y);
+        }
+        __syncwarp();
+        next();
+      }
+      u += g.k1 - g.k0;
+    }
+    // phase 2: the weights of the first tiles may come before the
+    // activations are complete
+    const int64_t mat2 = static_cast<int64_t>(ht_count) * it_count * kSfBytes;
+    auto record2 = [&](int32_t k) { return p.workspace + l.h + k * record_bytes(pad); };
+    auto load_down = [&](int32_t item, int32_t k) {
+      const int32_t e = sh->expert[k / it_count], kt = k % it_count;
+      mbar_arrive_expect_tx(&sh->full[stage], tx_d + tx_b);
+      load_a(&tmap_down,
+             p.down_scales + e * mat2 + (static_cast<int64_t>(item) * it_count + kt) * kSfBytes,
+             kt * kTile, e * p.hidden + item * kTile);
+    };
+    int64_t u = share2.lo;
+    const int first = stage;
+    int ahead = 0;
+    for (; ok && ahead < stages && u < share2.hi; ++ahead, ++u) {
+      if (!(ok = wait_empty())) break;
+      const Segment g = share2.at(u);
+      if (elect_one()) load_down(g.item, g.k0);
+      __syncwarp();
+      next();
+    }
+    if (ahead > 0 || ok) {
+      const bool ready = wait_count(counters + kDoneWord, items1, s_abort, p.status, p.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ready) && ok;
+      fence_proxy_async_global();
+    }
+    // (also after a wait gave up: every stage begun is completed)
+    for (int i = 0; i < ahead; ++i) {
+      const Segment g = share2.at(share2.lo + i);
+      if (elect_one()) load_b((first + i) % stages, record2(g.k0));
+      __syncwarp();
+    }
+    for (; ok && u < share2.hi; ++u) {
+      if (!(ok = wait_empty())) break;
+      const Segment g = share2.at(u);
+      if (elect_one()) {
+        load_down(g.item, g.k0);
+        load_b(stage, record2(g.k0));
+      }
+      __syncwarp();
+      next();
+    }
+    // every copy has landed before the block may end
+    for (int s = 0; s < stages; ++s) {
+      const int64_t fills = issued > s ? (issued - s + stages - 1) / stages : 0;
+      if (fills)
+        mbar_wait_warp(&sh->full[s], static_cast<uint32_t>((fills - 1) & 1), s_abort, p.status,
+                       p.wait_limit_ns, true);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kHiOperand = smem_desc_hi(1024, 2);
+    constexpr uint32_t kHiScale = smem_desc_hi(128, 0);
+    const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), 16);
+    const uint32_t b_lo0 = smem_desc_lo(smem_u32(sB), 16);
+    const uint32_t sf_lo0 = smem_desc_lo(smem_u32(sSf), 0);
+    const uint32_t sf_col0 = tmem + 4u * pad;         // after two accumulators of 2 * pad columns
+    int stage = 0;
+    uint32_t phase = 0, acc = 0, acc_phase = 0;
+    bool ok = true;
+    // the tile in `stage` times the B terms in `b_stage`, into columns `d`
+    auto multiply = [&](int b_stage, uint32_t d, uint32_t idesc, uint32_t blocks, bool add) {
+      const uint32_t sf = sf_col0 + stage * 4u * (1 + kTerms);
+      const uint32_t sfb = sf_col0 + b_stage * 4u * (1 + kTerms) + 4u;
+      const uint32_t sf_lo = sf_lo0 + stage * ((1 + kTerms) * kSfBytes >> 4);
+      tc_cp_32x128b_warpx4(sf, sf_lo, kHiScale);
+      if (b_stage == stage) {
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+          tc_cp_32x128b_warpx4(sf + 4u * (1 + t), sf_lo + (1 + t) * (kSfBytes >> 4), kHiScale);
+      }
+      const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
+      const uint32_t b_lo = b_lo0 + b_stage * (b_bytes >> 4);
+#pragma unroll
+      for (uint32_t kb = 0; kb < 4; ++kb)
+        if (kb < blocks) {
+#pragma unroll
+          for (uint32_t t = 0; t < kTerms; ++t)
+            tc_mma_mxf8(d, a_lo + 2u * kb, kHiOperand, b_lo + t * (pad * kTile >> 4) + 2u * kb,
+                        kHiOperand, idesc | kb << 4 | kb << 29, sf, sfb + 4u * t,
+                        add || kb > 0 || t > 0 ? 1u : 0u);
+        }
+    };
+    auto wait_full = [&] {
+      const bool got =
+          mbar_wait_warp(&sh->full[stage], phase, s_abort, p.status, p.wait_limit_ns);
+      tc_fence_after_sync();
+      return got;
+    };
+    auto next = [&] {
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const Share& share = ph == 0 ? share1 : share2;
+      const uint32_t idesc = mxf8_idesc(ph == 0 ? p.type_gu : p.type_d, 0, kTile, pad, 0, 0);
+      const int32_t k_blocks = ((ph == 0 ? p.hidden : p.inter) + 31) / 32;
+      for (int64_t u = share.lo; u < share.hi && ok;) {
+        const Segment g = share.at(u);
+        if (!mbar_wait_warp(&sh->acc_empty[acc], acc_phase ^ 1u, s_abort, p.status,
+                            p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + acc * 2u * pad;
+        for (int32_t k = g.k0; k < g.k1; ++k) {
+          const int32_t kt = ph == 0 ? k : k % it_count;
+          const uint32_t blocks = k_blocks - kt * 4 < 4 ? k_blocks - kt * 4 : 4;
+          if (!(ok = wait_full())) break;
+          if (elect_one()) {
+            multiply(stage, d, idesc, blocks, k > g.k0);
+            if (ph == 1) tc_commit(&sh->empty[stage]);
+          }
+          __syncwarp();
+          const int b_stage = stage;
+          next();
+          if (ph == 1) continue;
+          if (!(ok = wait_full())) break;
+          if (elect_one()) {
+            multiply(b_stage, d + pad, idesc, blocks, k > g.k0);
+            tc_commit(&sh->empty[b_stage]);
+            tc_commit(&sh->empty[stage]);
+          }
+          __syncwarp();
+          next();
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit(&sh->acc_full[acc]);
+        __syncwarp();
+        u += g.k1 - g.k0;
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    if (elect_one()) {
+      tc_commit(&sh->mma_done);
+      mbar_wait(&sh->mma_done, 0, s_abort, p.status, p.wait_limit_ns, true);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const uint32_t q = warp & 3u;                     // tensor-memory lanes 32 q ..+31
+    const uint32_t half = (warp - 2) >> 2;            // of the token columns
+    const int row = static_cast<int>(q * 32 + lane);  // of the tile
+    const int tid = static_cast<int>(threadIdx.x) - 64;
+    const int t_begin = static_cast<int>(half) * (pad / 2), t_end = t_begin + pad / 2;
+    float* parts = reinterpret_cast<float*>(p.workspace + l.parts);
+    const int64_t part_size = static_cast<int64_t>(2) * pad * kTile;
+    uint32_t acc = 0, acc_phase = 0;
+    // (after a wait gave up every item is still gone through, without work,
+    // so that all epilogue warps meet at every barrier)
+    bool ok = true;
+    for (int ph = 0; ph < 2; ++ph) {
+      const Share& share = ph == 0 ? share1 : share2;
+      const int mats = ph == 0 ? 2 : 1;               // accumulators of an item
+      for (int64_t u = share.lo; u < share.hi;) {
+        const Segment g = share.at(u);
+        const int64_t u0 = static_cast<int64_t>(g.item) * share.per;
+        u += g.k1 - g.k0;
+        const int32_t a = g.item / it_count;          // phase 1: index of the expert
+        if (ph == 0 && tid < p.tokens) {
+          const int e = sh->expert[a];
+          float w = -1.f;
+          for (int k = 0; k < p.top_k; ++k)
+            if (sh->id[tid * p.top_k + k] == e) w = sh->weight[tid * p.top_k + k];
+          sh->share[tid] = w;
+        }
+        const bool got = mbar_wait(&sh->acc_full[acc], acc_phase, s_abort, p.status, p.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, got)) ok = false;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (q * 32u << 16) + acc * 2u * pad;
+        const bool whole = g.k1 - g.k0 == share.per;
+        bool mine = whole;
+        int c0 = 0, c1 = -1;
+        if (!whole) {
+          // leave this block's part, and see whether it was the last
+          float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) +
+                                 share.slot_of(blockIdx.x, g.item)) * part_size;
+          if (ok)
+            for (int m = 0; m < mats; ++m)
+              for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
+                uint32_t v[8];
+                tmem_ld_32x32b_x8(d + m * pad + t, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (t + i < p.tokens)
+                    part[(m * pad + t + i) * kTile + row] = __uint_as_float(v[i]);
+              }
+          c0 = share.block_of(u0);
+          c1 = share.block_of(u0 + share.per - 1);
+          __threadfence();
+          epi_sync();
+          if (tid == 0) {
+            __threadfence();
+            sh->ticket = atomicAdd(counters + ph * kMaxBlocks + c0, 1u);
+          }
+          epi_sync();
+          mine = sh->ticket == static_cast<uint32_t>(c1 - c0);
+          if (mine) __threadfence();
+        } else if (ph == 0) {
+          epi_sync();                                 // sh->share is complete
+        }
+        if (mine && ok) {
+          for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
+            float v[2][8];
+            for (int m = 0; m < mats; ++m) {
+              if (whole) {
+                uint32_t r[8];
+                tmem_ld_32x32b_x8(d + m * pad + t, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[m][i] = __uint_as_float(r[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[m][i] = 0.f;
+                for (int c = c0; c <= c1; ++c) {
+                  const float* part = parts + (2 * static_cast<int64_t>(c) +
+                                               share.slot_of(c, g.item)) * part_size;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (t + i < p.tokens) v[m][i] += __ldcg(part + (m * pad + t + i) * kTile + row);
+                }
+              }
+            }
+            if (ph == 0) {
+              uint8_t* record = p.workspace + l.h + g.item * record_bytes(pad);
+              const bool in = g.item % it_count * kTile + row < p.inter;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (t + i >= p.tokens) break;
+                const float w = sh->share[t + i];
+                const float act = v[0][i] / (1.f + expf(-v[0][i])) * v[1][i];
+                write_block(record, pad, t + i, q, in && !(w < 0.f) ? act * w : 0.f);
+              }
+            } else {
+              const int c = g.item * kTile + row;
+              if (c < p.hidden) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (t + i < p.tokens)
+                    static_cast<__nv_bfloat16*>(p.y)[(t + i) * p.ldy + c] = __float2bfloat16_rn(v[0][i]);
+              }
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+        if (ph == 0 && mine) {
+          // the activations are there for every block's copies
+          fence_proxy_async_global();
+          __threadfence();
+          epi_sync();
+          if (tid == 0) {
+            __threadfence();
+            atomicAdd(counters + kDoneWord, 1u);
+          }
+        } else if (ph == 0) {
+          epi_sync();                                 // sh->share may be written again
+        }
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
-// One warp per (token, channel of y).
-__global__ void __launch_bounds__(kThreads) moe_down_kernel(const MoeFewParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(p.tokens) * p.hidden) return;
-  const int64_t t = w / p.hidden, c = w % p.hidden;
-  const int64_t k_tiles = (p.inter + 127) / 128;
-  const int64_t smat = (p.hidden + 127) / 128 * k_tiles * 512;
-  float s = 0.f;
-  for (int k = 0; k < p.top_k; ++k) {
-    const int64_t slot = t * p.top_k + k, e = p.ids[slot];
-    const uint8_t* d = p.down + (e * p.hidden + c) * (p.inter * p.bits_d / 8);
-    for (int64_t i = lane_id(); i < p.inter; i += 32)
-      s += p.h[slot * p.inter + i] * decode(d, i, p.fmt_d) *
-           block_scale(p.down_scales + e * smat, c, i >> 5, k_tiles);
-  }
-  s = warp_sum(s);
-  if (lane_id() == 0) static_cast<__nv_bfloat16*>(p.y)[t * p.ldy + c] = __float2bfloat16_rn(s);
-}
-
-template <typename K>
-cudaError_t launch(K kern, int64_t grid, int threads, const MoeFewParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
+constexpr size_t kSmemMax = 227 * 1024;
 
 }  // namespace
 
 size_t moe_few_workspace(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                          int32_t top_k) {
-  (void)hidden;
-  return static_cast<size_t>(tokens) *
-         ((static_cast<size_t>(experts) + 3) / 4 * 16 + static_cast<size_t>(top_k) * inter * 4);
+  return static_cast<size_t>(layout(tokens, hidden, inter, experts, top_k).bytes);
 }
 
-cudaError_t launch_moe_few(const MoeFewParams& q, cudaStream_t stream) {
-  MoeFewParams p = q;
-  p.logits = static_cast<float*>(q.workspace);
-  p.h = p.logits + static_cast<int64_t>(p.tokens) * ((p.experts + 3) / 4 * 4);
-  constexpr int64_t kWarps = kThreads / 32;
-  const int64_t t = p.tokens;
-  cudaError_t err = launch(moe_logits_kernel, (t * p.experts + kWarps - 1) / kWarps, kThreads, p, stream);
-  if (err == cudaSuccess) err = launch(moe_select_kernel, t, 32, p, stream);
-  if (err == cudaSuccess)
-    err = launch(moe_gate_up_kernel, (t * p.top_k * p.inter + kWarps - 1) / kWarps, kThreads, p, stream);
-  if (err == cudaSuccess)
-    err = launch(moe_down_kernel, (t * p.hidden + kWarps - 1) / kWarps, kThreads, p, stream);
-  return err;
+cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
+                           const CUtensorMap& tmap_up, const CUtensorMap& tmap_down, int num_sms,
+                           cudaStream_t stream) {
+  static PerDeviceOnce setup;
+  cudaError_t err = setup.run([&]() -> cudaError_t {
+    return cudaFuncSetAttribute(moe_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemMax));
+  });
+  if (err != cudaSuccess) return err;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    const int logit_blocks = (p.experts + kRouterExperts - 1) / kRouterExperts *
+                             ((p.tokens + kRouterTokens - 1) / kRouterTokens);
+    const int64_t warps = static_cast<int64_t>(p.tokens) * tiles(p.hidden);
+    cfg.gridDim = dim3(static_cast<unsigned>(logit_blocks + (warps + kRouterThreads / 32 - 1) /
+                                                                (kRouterThreads / 32)));
+    cfg.blockDim = dim3(kRouterThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, moe_router_kernel, p, logit_blocks);
+    if (err != cudaSuccess) return err;
+  }
+  const int pad = pad_tokens(p.tokens);
+  const size_t stage = kTileBytes + code_bytes(pad) + (1 + kTerms) * kSfBytes;
+  size_t stages = (kSmemMax - 1024 - sizeof(Shared)) / stage;
+  if (stages > kMaxStages) stages = kMaxStages;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the blocks wait for one another
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms < kMaxBlocks ? num_sms : kMaxBlocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = stages * stage + sizeof(Shared) + 1024;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_experts_kernel, tmap_gate, tmap_up, tmap_down, p,
+                            static_cast<int>(stages));
 }
 
 }  // namespace mx

@@ -757,30 +757,34 @@ mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32
   mx::MoeFewParams p{};
   p.x = x;
   p.router = router;
-  p.gate = gate;
-  p.up = up;
-  p.down = down;
   p.gate_scales = gate_scales;
   p.up_scales = up_scales;
   p.down_scales = down_scales;
   p.y = y;
   p.ids = ids;
   p.weights = weights;
-  p.workspace = workspace;
-  p.hidden = hidden;
-  p.inter = inter;
+  p.workspace = static_cast<uint8_t*>(workspace);
   p.ldx = ldx;
   p.ldy = ldy;
+  p.hidden = static_cast<int32_t>(hidden);
+  p.inter = static_cast<int32_t>(inter);
   p.tokens = tokens;
   p.experts = experts;
   p.top_k = top_k;
   p.renormalize = renormalize;
   p.router_fp32 = router_dtype == MX_FP32;
-  p.fmt_gu = fmt_gu;
-  p.fmt_d = fmt_d;
+  p.type_gu = mma_type_code(fmt_gu);
+  p.type_d = mma_type_code(fmt_d);
   p.bits_gu = is_packed(fmt_gu) ? code_bits(fmt_gu) : 8;
   p.bits_d = is_packed(fmt_d) ? code_bits(fmt_d) : 8;
-  return mx::launch_moe_few(p, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+  p.status = st->status;
+  p.wait_limit_ns = g_wait_ns.load(std::memory_order_relaxed);
+  CUtensorMap tg, tu, td;
+  if ((s = encode_operand_map(&tg, gate, fmt_gu, hidden, experts * inter)) != MX_OK) return s;
+  if ((s = encode_operand_map(&tu, up, fmt_gu, hidden, experts * inter)) != MX_OK) return s;
+  if ((s = encode_operand_map(&td, down, fmt_d, inter, experts * hidden)) != MX_OK) return s;
+  return mx::launch_moe_few(p, tg, tu, td, st->num_sms, stream) == cudaSuccess ? MX_OK
+                                                                                : MX_ERR_CUDA;
 }
 
 mx_status mx_device_status(cudaStream_t stream) {

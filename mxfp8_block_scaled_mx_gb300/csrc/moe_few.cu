@@ -15,7 +15,9 @@
 // [128, 256).  hi has 4 significant bits, the remainder at most 1/16 of v, so
 // hi + lo / 32 holds 8 significant bits: a bf16 exactly (down to 2^-14 of its
 // block's largest), and the FP32 activation rounded once as bf16 would be.
-// Both terms multiply the same A tile into the same accumulator.
+// The terms are rows of one B operand (N = 2 x the padded token count, one MMA
+// per 32 of K: an MMA this narrow costs what reading its A tile costs), and
+// the epilogue adds their two accumulator columns.
 //
 // Two launches.  moe_router_kernel forms the logits and x's B operand.
 // moe_experts_kernel (one block per SM, cooperative) lets every block choose
@@ -48,19 +50,20 @@ constexpr int kMaxTopK = 32;
 constexpr int kMaxBlocks = 192;     // workspaces are sized for this many SMs
 constexpr int kTile = 128;          // rows and K of a weight tile
 constexpr int kTileBytes = kTile * kTile;
-constexpr int kSfBytes = 512;       // scales of a tile, and of a B term
+constexpr int kSfBytes = 512;       // scales of a tile, and of a B record
 constexpr int kTerms = 2;
 constexpr int kMaxStages = 9;
 
 __host__ __device__ constexpr int pad_tokens(int t) { return (t + 15) / 16 * 16; }
 __host__ __device__ constexpr int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
 
-// One K tile of the B operand as the ring holds it: per term `pad` rows of
-// 128 codes (128-byte swizzle), then per term a tile of scales.
+// One K tile of the B operand as the ring holds it: 2 * pad rows of 128 codes
+// (128-byte swizzle; row t is token t's hi, row pad + t its lo), then one tile
+// of scales for those rows.
 __host__ __device__ constexpr int64_t code_bytes(int pad) { return int64_t(kTerms) * pad * kTile; }
-__host__ __device__ constexpr int64_t record_bytes(int pad) {
-  return code_bytes(pad) + kTerms * kSfBytes;
-}
+__host__ __device__ constexpr int64_t record_bytes(int pad) { return code_bytes(pad) + kSfBytes; }
+static_assert(kTerms * kMaxTokens <= kTile, "the scales of all rows in one tile");
+static_assert(2 * 192 + kMaxStages * 8 <= 512, "tensor memory: two sets and the scales");
 
 // Workspace: counters, logits, x's records, the activations' records, parts.
 struct Layout {
@@ -81,11 +84,11 @@ __host__ __device__ inline Layout layout(int tokens, int64_t hidden, int64_t int
 constexpr int kDoneWord = 2 * kMaxBlocks;  // after the two phases' tickets
 static_assert((kDoneWord + 1) * 4 <= 4096, "counters");
 
-// Byte of code k (0..127) of row t in a term.
+// Byte of code k (0..127) of row t of a record.
 __device__ __forceinline__ uint32_t code_at(uint32_t t, uint32_t k) {
   return t * 128 + (((k >> 4) ^ (t & 7)) << 4) + (k & 15);
 }
-// Byte of the scale of block j (0..3) of row t in a term's scale tile.
+// Byte of the scale of block j (0..3) of row t in a record's scale tile.
 __device__ __forceinline__ uint32_t scale_at(uint32_t t, uint32_t j) {
   return (t & 31) * 16 + (t >> 5) * 4 + j;
 }
@@ -124,11 +127,11 @@ __device__ __forceinline__ void write_block(uint8_t* record, int pad, uint32_t t
   }
   const uint32_t at = code_at(t, j * 32 + lane);
   record[at] = static_cast<uint8_t>(hi);
-  record[pad * kTile + at] = static_cast<uint8_t>(lo);
+  record[pad * kTile + at] = static_cast<uint8_t>(lo);  // pad % 8 == 0: the same swizzle
   if (lane == 0) {
-    uint8_t* sf = record + code_bytes(pad) + scale_at(t, j);
-    sf[0] = static_cast<uint8_t>(e + 127);
-    sf[kSfBytes] = static_cast<uint8_t>(e + 127 - 5);
+    uint8_t* sf = record + code_bytes(pad);
+    sf[scale_at(t, j)] = static_cast<uint8_t>(e + 127);
+    sf[scale_at(pad + t, j)] = static_cast<uint8_t>(e + 127 - 5);
   }
 }
 
@@ -223,6 +226,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
 // ------------------------------------------------------------------ experts
 
 constexpr int kEpiWarps = 8;
+constexpr int kPartsAtOnce = 4;     // parts of an item read at a time
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
 
@@ -252,26 +256,30 @@ __device__ __forceinline__ void select_token(const MoeFewParams& p, const float*
   constexpr int kPer = kMaxExperts / 32;
   const uint32_t lane = lane_id();
   const float* row = logits + static_cast<int64_t>(t) * p.experts;
+  const int n = (p.experts + 31) / 32;  // logits of a lane
   float z[kPer];
+  uint32_t key[kPer];
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
+    if (j >= n) break;
     const int e = j * 32 + static_cast<int>(lane);
     z[j] = e < p.experts ? row[e] : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (j >= n) break;
+    key[j] = j * 32 + static_cast<int>(lane) < p.experts ? logit_key(z[j]) : 0u;
     top = fmaxf(top, z[j]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float sum = 0.f;
-  uint32_t key[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const bool in = j * 32 + static_cast<int>(lane) < p.experts;
-    key[j] = in ? logit_key(z[j]) : 0u;
-    if (j * 32 < p.experts) {
-      z[j] = in ? expf(z[j] - top) : 0.f;
-      sum += z[j];
-    }
+    if (j >= n) break;
+    z[j] = key[j] ? expf(z[j] - top) : 0.f;
+    sum += z[j];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -280,18 +288,22 @@ __device__ __forceinline__ void select_token(const MoeFewParams& p, const float*
     uint32_t best = 0u, at = 0xFFFFFFFFu;
     float w = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
+    for (int j = 0; j < kPer; ++j) {
+      if (j >= n) break;
       if (key[j] > best) {
         best = key[j];
         at = j * 32 + lane;
         w = z[j];
       }
+    }
     const uint32_t m = __reduce_max_sync(0xffffffffu, best);
     const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
     w = __shfl_sync(0xffffffffu, w, e & 31u) / sum;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
+    for (int j = 0; j < kPer; ++j) {
+      if (j >= n) break;
       if (e == j * 32 + lane) key[j] = 0u;
+    }
     chosen += w;
     if (lane == 0) {
       sh->id[t * p.top_k + k] = static_cast<uint16_t>(e);
@@ -323,7 +335,7 @@ struct Share {
       hi = total * (blockIdx.x + 1) / n;
     }
   }
-  // the segment that starts at tile u
+  // the segment that starts at tile u (an empty one at the end of all)
   __device__ __forceinline__ Segment at(int64_t u) const {
     Segment s;
     s.item = static_cast<int32_t>(u / per);
@@ -335,14 +347,24 @@ struct Share {
   __device__ __forceinline__ int block_of(int64_t u) const {
     return static_cast<int>(((u + 1) * n - 1) / total);
   }
-  // which of block b's two parts belongs to `item`
-  __device__ __forceinline__ int slot_of(int b, int32_t item) const {
+  // the first of block b's parts is that of the item its share begins in; of
+  // an item's blocks only the first may have begun in an earlier one
+  __device__ __forceinline__ int first_slot(int b, int32_t item) const {
     return total * b / n / per == item ? 0 : 1;
   }
 };
 
 __device__ __forceinline__ void epi_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
+// Adds one to *word after everything that this thread has seen done (its
+// block's writes before a barrier among it), and sees what was done before
+// the earlier additions.
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t* word) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(word) : "memory");
+  return old;
 }
 
 // Waits until *word reaches `want`.
@@ -378,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_bytes = static_cast<uint32_t>(code_bytes(pad));
   uint8_t* sA = smem;                                 // [stages][16 KB]
   uint8_t* sB = sA + stages * kTileBytes;             // [stages][b_bytes]
-  uint8_t* sSf = sB + stages * b_bytes;               // [stages][A, B hi, B lo][512]
-  Shared* sh = reinterpret_cast<Shared*>(sSf + stages * (1 + kTerms) * kSfBytes);
+  uint8_t* sSf = sB + stages * b_bytes;               // [stages][A, B][512]
+  Shared* sh = reinterpret_cast<Shared*>(sSf + stages * 2 * kSfBytes);
   volatile uint32_t* s_abort = &sh->abort;
   const uint32_t warp = warp_id(), lane = lane_id();
   const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
@@ -439,7 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t items1 = sh->active * it_count;       // (expert, 128 channels)
   const Share share1(items1, ht_count);               // each tile: gate and up
   const Share share2(ht_count, items1);
-  const uint32_t tx_b = b_bytes + kTerms * kSfBytes;
+  const uint32_t tx_b = b_bytes + kSfBytes;
+  // accumulators: two columns per padded token, for gate and up; a second
+  // set where tensor memory holds it next to the scales
+  const uint32_t acc_cols = 2u * kTerms * pad;
+  const uint32_t acc_sets = acc_cols <= 192u ? 2u : 1u;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -461,12 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto load_a = [&](const CUtensorMap* map, const uint8_t* sf, int32_t x, int32_t y) {
       tma_load_2d(sA + stage * kTileBytes, map, &sh->full[stage], x, y);
-      bulk_load(sSf + stage * (1 + kTerms) * kSfBytes, sf, kSfBytes, &sh->full[stage]);
+      bulk_load(sSf + stage * 2 * kSfBytes, sf, kSfBytes, &sh->full[stage]);
     };
     auto load_b = [&](int s, const uint8_t* record) {
       bulk_load(sB + s * b_bytes, record, b_bytes, &sh->full[s]);
-      bulk_load(sSf + (s * (1 + kTerms) + 1) * kSfBytes, record + b_bytes, kTerms * kSfBytes,
-                &sh->full[s]);
+      bulk_load(sSf + (s * 2 + 1) * kSfBytes, record + b_bytes, kSfBytes, &sh->full[s]);
     };
     // phase 1: gate tile with x's record, then the up tile (same record)
     const int64_t mat1 = static_cast<int64_t>(it_count) * ht_count * kSfBytes;
@@ -498,22 +523,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // activations are complete
     const int64_t mat2 = static_cast<int64_t>(ht_count) * it_count * kSfBytes;
     auto record2 = [&](int32_t k) { return p.workspace + l.h + k * record_bytes(pad); };
-    auto load_down = [&](int32_t item, int32_t k) {
-      const int32_t e = sh->expert[k / it_count], kt = k % it_count;
+    // the tile at the front: item, k and k's expert and tile
+    Segment w = share2.at(share2.lo);
+    int32_t a = w.k0 / it_count, kt = w.k0 % it_count;
+    auto step = [&] {
+      if (++kt == it_count) {
+        kt = 0;
+        ++a;
+      }
+      if (++w.k0 == share2.per) {
+        w.k0 = kt = a = 0;
+        ++w.item;
+      }
+    };
+    auto load_down = [&] {
+      const int32_t e = sh->expert[a], item = w.item;
       mbar_arrive_expect_tx(&sh->full[stage], tx_d + tx_b);
       load_a(&tmap_down,
              p.down_scales + e * mat2 + (static_cast<int64_t>(item) * it_count + kt) * kSfBytes,
              kt * kTile, e * p.hidden + item * kTile);
     };
-    int64_t u = share2.lo;
+    int64_t u = share2.lo;  // (a block without a share has nothing at the front)
     const int first = stage;
     int ahead = 0;
     for (; ok && ahead < stages && u < share2.hi; ++ahead, ++u) {
       if (!(ok = wait_empty())) break;
-      const Segment g = share2.at(u);
-      if (elect_one()) load_down(g.item, g.k0);
+      if (elect_one()) load_down();
       __syncwarp();
       next();
+      step();
     }
     if (ahead > 0 || ok) {
       const bool ready = wait_count(counters + kDoneWord, items1, s_abort, p.status, p.wait_limit_ns);
@@ -528,13 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (; ok && u < share2.hi; ++u) {
       if (!(ok = wait_empty())) break;
-      const Segment g = share2.at(u);
       if (elect_one()) {
-        load_down(g.item, g.k0);
-        load_b(stage, record2(g.k0));
+        load_down();
+        load_b(stage, record2(w.k0));
       }
       __syncwarp();
       next();
+      step();
     }
     // every copy has landed before the block may end
     for (int s = 0; s < stages; ++s) {
@@ -550,32 +588,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), 16);
     const uint32_t b_lo0 = smem_desc_lo(smem_u32(sB), 16);
     const uint32_t sf_lo0 = smem_desc_lo(smem_u32(sSf), 0);
-    const uint32_t sf_col0 = tmem + 4u * pad;         // after two accumulators of 2 * pad columns
+    const uint32_t sf_col0 = tmem + acc_sets * acc_cols;
     int stage = 0;
     uint32_t phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
-    // the tile in `stage` times the B terms in `b_stage`, into columns `d`
+    // the tile in `stage` times the record in `b_stage`, into columns `d`
     auto multiply = [&](int b_stage, uint32_t d, uint32_t idesc, uint32_t blocks, bool add) {
-      const uint32_t sf = sf_col0 + stage * 4u * (1 + kTerms);
-      const uint32_t sfb = sf_col0 + b_stage * 4u * (1 + kTerms) + 4u;
-      const uint32_t sf_lo = sf_lo0 + stage * ((1 + kTerms) * kSfBytes >> 4);
+      const uint32_t sf = sf_col0 + stage * 8u;
+      const uint32_t sfb = sf_col0 + b_stage * 8u + 4u;
+      const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
       tc_cp_32x128b_warpx4(sf, sf_lo, kHiScale);
-      if (b_stage == stage) {
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-          tc_cp_32x128b_warpx4(sf + 4u * (1 + t), sf_lo + (1 + t) * (kSfBytes >> 4), kHiScale);
-      }
+      if (b_stage == stage) tc_cp_32x128b_warpx4(sf + 4u, sf_lo + (kSfBytes >> 4), kHiScale);
       const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
       const uint32_t b_lo = b_lo0 + b_stage * (b_bytes >> 4);
 #pragma unroll
       for (uint32_t kb = 0; kb < 4; ++kb)
-        if (kb < blocks) {
-#pragma unroll
-          for (uint32_t t = 0; t < kTerms; ++t)
-            tc_mma_mxf8(d, a_lo + 2u * kb, kHiOperand, b_lo + t * (pad * kTile >> 4) + 2u * kb,
-                        kHiOperand, idesc | kb << 4 | kb << 29, sf, sfb + 4u * t,
-                        add || kb > 0 || t > 0 ? 1u : 0u);
-        }
+        if (kb < blocks)
+          tc_mma_mxf8(d, a_lo + 2u * kb, kHiOperand, b_lo + 2u * kb, kHiOperand,
+                      idesc | kb << 4 | kb << 29, sf, sfb, add || kb > 0 ? 1u : 0u);
     };
     auto wait_full = [&] {
       const bool got =
@@ -591,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int ph = 0; ph < 2 && ok; ++ph) {
       const Share& share = ph == 0 ? share1 : share2;
-      const uint32_t idesc = mxf8_idesc(ph == 0 ? p.type_gu : p.type_d, 0, kTile, pad, 0, 0);
+      const uint32_t idesc = mxf8_idesc(ph == 0 ? p.type_gu : p.type_d, 0, kTile, kTerms * pad, 0, 0);
       const int32_t k_blocks = ((ph == 0 ? p.hidden : p.inter) + 31) / 32;
       for (int64_t u = share.lo; u < share.hi && ok;) {
         const Segment g = share.at(u);
@@ -601,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + acc * 2u * pad;
+        const uint32_t d = tmem + acc * acc_cols;
         for (int32_t k = g.k0; k < g.k1; ++k) {
           const int32_t kt = ph == 0 ? k : k % it_count;
           const uint32_t blocks = k_blocks - kt * 4 < 4 ? k_blocks - kt * 4 : 4;
@@ -616,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ph == 1) continue;
           if (!(ok = wait_full())) break;
           if (elect_one()) {
-            multiply(b_stage, d + pad, idesc, blocks, k > g.k0);
+            multiply(b_stage, d + kTerms * pad, idesc, blocks, k > g.k0);
             tc_commit(&sh->empty[b_stage]);
             tc_commit(&sh->empty[stage]);
           }
@@ -627,8 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) tc_commit(&sh->acc_full[acc]);
         __syncwarp();
         u += g.k1 - g.k0;
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
+        if (++acc == acc_sets) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
     if (elect_one()) {
@@ -667,59 +699,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool got = mbar_wait(&sh->acc_full[acc], acc_phase, s_abort, p.status, p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, got)) ok = false;
         tc_fence_after_sync();
-        const uint32_t d = tmem + (q * 32u << 16) + acc * 2u * pad;
+        const uint32_t d = tmem + (q * 32u << 16) + acc * acc_cols;
+        // accumulator m's values for tokens t..t+7: hi's column plus lo's
+        auto read_acc = [&](int m, int t, float (&v)[8]) {
+          uint32_t hi[8], lo[8];
+          tmem_ld_32x32b_x8(d + m * kTerms * pad + t, hi);
+          tmem_ld_32x32b_x8(d + m * kTerms * pad + pad + t, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+        };
         const bool whole = g.k1 - g.k0 == share.per;
         bool mine = whole;
         int c0 = 0, c1 = -1;
         if (!whole) {
           // leave this block's part, and see whether it was the last
-          float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) +
-                                 share.slot_of(blockIdx.x, g.item)) * part_size;
+          const int slot = u0 <= share.lo ? 0 : 1;
+          float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * part_size + row;
           if (ok)
             for (int m = 0; m < mats; ++m)
               for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
-                uint32_t v[8];
-                tmem_ld_32x32b_x8(d + m * pad + t, v);
-                tmem_ld_wait();
+                float v[8];
+                read_acc(m, t, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (t + i < p.tokens)
-                    part[(m * pad + t + i) * kTile + row] = __uint_as_float(v[i]);
+                  if (t + i < p.tokens) part[(m * pad + t + i) * kTile] = v[i];
               }
           c0 = share.block_of(u0);
           c1 = share.block_of(u0 + share.per - 1);
-          __threadfence();
           epi_sync();
-          if (tid == 0) {
-            __threadfence();
-            sh->ticket = atomicAdd(counters + ph * kMaxBlocks + c0, 1u);
-          }
+          if (tid == 0) sh->ticket = add_acq_rel(counters + ph * kMaxBlocks + c0);
           epi_sync();
           mine = sh->ticket == static_cast<uint32_t>(c1 - c0);
-          if (mine) __threadfence();
         } else if (ph == 0) {
           epi_sync();                                 // sh->share is complete
         }
         if (mine && ok) {
+          const float* part0 =
+              parts + (2 * static_cast<int64_t>(c0) + (whole ? 0 : share.first_slot(c0, g.item))) * part_size + row;
+          const float* part1 = parts + 2 * static_cast<int64_t>(c0) * part_size + row;  // + 2 per block
           for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
             float v[2][8];
-            for (int m = 0; m < mats; ++m) {
-              if (whole) {
-                uint32_t r[8];
-                tmem_ld_32x32b_x8(d + m * pad + t, r);
-                tmem_ld_wait();
+            if (whole) {
+              for (int m = 0; m < mats; ++m) read_acc(m, t, v[m]);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[m][i] = __uint_as_float(r[i]);
-              } else {
+              for (int i = 0; i < 8; ++i) v[0][i] = v[1][i] = 0.f;
+              for (int c = c0; c <= c1; c += kPartsAtOnce) {
+                float r[kPartsAtOnce][2][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[m][i] = 0.f;
-                for (int c = c0; c <= c1; ++c) {
-                  const float* part = parts + (2 * static_cast<int64_t>(c) +
-                                               share.slot_of(c, g.item)) * part_size;
+                for (int b = 0; b < kPartsAtOnce; ++b) {
+                  const float* from =
+                      c + b == c0 ? part0 : part1 + 2 * static_cast<int64_t>(c + b - c0) * part_size;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (t + i < p.tokens) v[m][i] += __ldcg(part + (m * pad + t + i) * kTile + row);
+                  for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      r[b][m][i] = m < mats && c + b <= c1 && t + i < p.tokens
+                                       ? __ldcg(from + (m * pad + t + i) * kTile)
+                                       : 0.f;
                 }
+#pragma unroll
+                for (int b = 0; b < kPartsAtOnce; ++b)
+#pragma unroll
+                  for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[m][i] += r[b][m][i];
               }
             }
             if (ph == 0) {
@@ -749,17 +794,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ph == 0 && mine) {
           // the activations are there for every block's copies
           fence_proxy_async_global();
-          __threadfence();
           epi_sync();
-          if (tid == 0) {
-            __threadfence();
-            atomicAdd(counters + kDoneWord, 1u);
-          }
+          if (tid == 0) add_acq_rel(counters + kDoneWord);
         } else if (ph == 0) {
           epi_sync();                                 // sh->share may be written again
         }
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
+        if (++acc == acc_sets) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
   }
@@ -807,7 +850,7 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
     if (err != cudaSuccess) return err;
   }
   const int pad = pad_tokens(p.tokens);
-  const size_t stage = kTileBytes + code_bytes(pad) + (1 + kTerms) * kSfBytes;
+  const size_t stage = kTileBytes + code_bytes(pad) + 2 * kSfBytes;
   size_t stages = (kSmemMax - 1024 - sizeof(Shared)) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};

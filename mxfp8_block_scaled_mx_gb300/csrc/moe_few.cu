@@ -27,10 +27,12 @@
 //            channels one after the other; the routing weights are in the
 //            activations, so one accumulator sums over experts.
 // Either phase's 128 x 128 tiles are dealt out as one sequence, evenly and in
-// order; an item whose tiles fall to several blocks is summed by the one
-// that finishes last, in block order (same inputs, same bits).  Between the
-// phases blocks wait for all activations, with their rings already full of
-// down tiles.
+// order.  An item whose tiles fall to several blocks is the last of its first
+// block's share and the first of every other's, so the others leave their
+// part (FP32) and go on, and the first, when it gets there, adds the parts in
+// block order to its own: same inputs, same bits, and nobody waits long.
+// Between the phases blocks wait for all activations, with their rings
+// already full of down tiles.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -78,10 +80,10 @@ __host__ __device__ inline Layout layout(int tokens, int64_t hidden, int64_t int
   l.x = l.logits + (int64_t(tokens) * experts * 4 + 255) / 256 * 256;
   l.h = l.x + tiles(hidden) * record_bytes(pad);
   l.parts = l.h + active * tiles(inter) * record_bytes(pad);
-  l.bytes = l.parts + int64_t(kMaxBlocks) * 2 * 2 * pad * kTile * 4;
+  l.bytes = l.parts + int64_t(kMaxBlocks) * 2 * pad * kTile * 4;
   return l;
 }
-constexpr int kDoneWord = 2 * kMaxBlocks;  // after the two phases' tickets
+constexpr int kDoneWord = 2 * kMaxBlocks;  // after a count per block and phase
 static_assert((kDoneWord + 1) * 4 <= 4096, "counters");
 
 // Byte of code k (0..127) of row t of a record.
@@ -226,18 +228,23 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
 // ------------------------------------------------------------------ experts
 
 constexpr int kEpiWarps = 8;
-constexpr int kPartsAtOnce = 4;     // parts of an item read at a time
+constexpr int kPartsAtOnce = 4;     // parts of an item that are read at a time,
+constexpr int kTokensAtOnce = 4;    // and tokens in phase 1
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2], mma_done;
-  uint32_t tmem, abort, ticket;
+  uint32_t tmem, abort;
   int32_t active;                           // number of active experts
   uint32_t chosen[kMaxExperts / 32];        // bit per expert
   uint16_t expert[kMaxExperts];             // active experts, ascending
-  float share[kMaxTokens];                  // of the item's expert, -1: not chosen
+  // the tokens that chose an item's expert, ascending, and their weights:
+  // written for one item while the item before may still be read
+  uint32_t routed[2][kMaxTokens / 32];      // bit per token
+  uint16_t token[2][kMaxTokens];
+  float share[2][kMaxTokens];
   uint16_t id[kMaxTokens * kMaxTopK];       // [tokens][top_k]
   float weight[kMaxTokens * kMaxTopK];
 };
@@ -249,71 +256,95 @@ __device__ __forceinline__ uint32_t logit_key(float z) {
   return z != z ? 1u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// A warp chooses token t's winners: largest logit first, the lowest expert
-// among equal ones.
-__device__ __forceinline__ void select_token(const MoeFewParams& p, const float* logits, int t,
-                                             Shared* sh) {
-  constexpr int kPer = kMaxExperts / 32;
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// A warp chooses the winners of tokens t0, t0 + step, ... (P of them side by
+// side, N logits a lane each): largest logit first, the lowest expert among
+// equal ones.
+template <int N, int P>
+__device__ __forceinline__ void select_tokens(const MoeFewParams& p, const float* logits, int t0,
+                                              int step, Shared* sh) {
   const uint32_t lane = lane_id();
-  const float* row = logits + static_cast<int64_t>(t) * p.experts;
-  const int n = (p.experts + 31) / 32;  // logits of a lane
-  float z[kPer];
-  uint32_t key[kPer];
-  float top = -INFINITY;
+  float z[P][N];
+  uint32_t key[P][N];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (j >= n) break;
-    const int e = j * 32 + static_cast<int>(lane);
-    z[j] = e < p.experts ? row[e] : -INFINITY;
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int t = t0 + i * step, e = j * 32 + static_cast<int>(lane);
+      z[i][j] = t < p.tokens && e < p.experts ? logits[t * p.experts + e] : -INFINITY;
+    }
+  float sum[P], chosen[P], my_w[P];
+  uint32_t my_e[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      key[i][j] = j * 32 + static_cast<int>(lane) < p.experts ? logit_key(z[i][j]) : 0u;
+      top = key[i][j] > top ? key[i][j] : top;
+    }
+    const float z0 = key_logit(__reduce_max_sync(0xffffffffu, top));
+    sum[i] = chosen[i] = my_w[i] = 0.f;
+    my_e[i] = 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      z[i][j] = key[i][j] ? expf(z[i][j] - z0) : 0.f;
+      sum[i] += z[i][j];
+    }
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (j >= n) break;
-    key[j] = j * 32 + static_cast<int>(lane) < p.experts ? logit_key(z[j]) : 0u;
-    top = fmaxf(top, z[j]);
-  }
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (j >= n) break;
-    z[j] = key[j] ? expf(z[j] - top) : 0.f;
-    sum += z[j];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  float chosen = 0.f;
+    for (int i = 0; i < P; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
   for (int k = 0; k < p.top_k; ++k) {
-    uint32_t best = 0u, at = 0xFFFFFFFFu;
-    float w = 0.f;
+    uint32_t best[P], at[P];
+    float w[P];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j >= n) break;
-      if (key[j] > best) {
-        best = key[j];
-        at = j * 32 + lane;
-        w = z[j];
+    for (int i = 0; i < P; ++i) {
+      best[i] = 0u, at[i] = 0xFFFFFFFFu, w[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (key[i][j] > best[i]) {
+          best[i] = key[i][j];
+          at[i] = j * 32 + lane;
+          w[i] = z[i][j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, best[i]);
+      const uint32_t e = __reduce_min_sync(0xffffffffu, best[i] == m ? at[i] : 0xFFFFFFFFu);
+      w[i] = __shfl_sync(0xffffffffu, w[i], e & 31u);
+      chosen[i] += w[i];
+      if (lane == static_cast<uint32_t>(k)) {
+        my_e[i] = e;
+        my_w[i] = w[i];
       }
-    }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
-    w = __shfl_sync(0xffffffffu, w, e & 31u) / sum;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j >= n) break;
-      if (e == j * 32 + lane) key[j] = 0u;
-    }
-    chosen += w;
-    if (lane == 0) {
-      sh->id[t * p.top_k + k] = static_cast<uint16_t>(e);
-      sh->weight[t * p.top_k + k] = w;
-      atomicOr(&sh->chosen[e >> 5], 1u << (e & 31u));
+      for (int j = 0; j < N; ++j)
+        if (e == j * 32 + lane) key[i][j] = 0u;
     }
   }
-  __syncwarp();
-  if (p.renormalize)
-    for (int k = lane; k < p.top_k; k += 32) sh->weight[t * p.top_k + k] /= chosen;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int t = t0 + i * step;
+    if (t < p.tokens && static_cast<int>(lane) < p.top_k) {
+      sh->id[t * p.top_k + lane] = static_cast<uint16_t>(my_e[i]);
+      sh->weight[t * p.top_k + lane] = my_w[i] / (p.renormalize ? chosen[i] : sum[i]);
+      atomicOr(&sh->chosen[my_e[i] >> 5], 1u << (my_e[i] & 31u));
+    }
+  }
+}
+
+// All tokens, over the block's warps.
+template <int N, int P>
+__device__ __forceinline__ void select_all(const MoeFewParams& p, const float* logits, int warps,
+                                           Shared* sh) {
+  for (int t = warp_id(); t < p.tokens; t += P * warps)
+    select_tokens<N, P>(p, logits, t, warps, sh);
 }
 
 // A block's run of tiles of one item.
@@ -321,36 +352,32 @@ struct Segment {
   int32_t item, k0, k1;   // tiles [k0, k1) of the item's K
 };
 
-// One phase's tiles, `per` of each of `items` items in sequence, and this
-// block's share [lo, hi).  The first n blocks share them, each at least one.
+// One phase's tiles, `per` of each of `items` items in sequence (2^27 at most,
+// from the limits on sizes), dealt to the first n blocks: q each, the first r
+// blocks one more.
 struct Share {
-  int64_t total, n, lo, hi;
-  int32_t per;
-  __device__ __forceinline__ Share(int64_t items, int64_t per_item)
-      : total(items * per_item), per(static_cast<int32_t>(per_item)) {
+  uint32_t per, total, n, q, r, lo, hi;   // this block's: [lo, hi)
+  __device__ __forceinline__ Share(uint32_t items, uint32_t per_item)
+      : per(per_item), total(items * per_item) {
     n = total < gridDim.x ? total : gridDim.x;
-    lo = hi = total;
-    if (blockIdx.x < n) {
-      lo = total * blockIdx.x / n;
-      hi = total * (blockIdx.x + 1) / n;
-    }
+    q = total / n;
+    r = total - q * n;
+    lo = blockIdx.x < n ? start(blockIdx.x) : total;
+    hi = blockIdx.x < n ? start(blockIdx.x + 1) : total;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t b) const { return b * q + (b < r ? b : r); }
+  __device__ __forceinline__ uint32_t block_of(uint32_t u) const {
+    const uint32_t t = r * (q + 1);
+    return u < t ? u / (q + 1) : r + (u - t) / q;
   }
   // the segment that starts at tile u (an empty one at the end of all)
-  __device__ __forceinline__ Segment at(int64_t u) const {
+  __device__ __forceinline__ Segment at(uint32_t u) const {
     Segment s;
     s.item = static_cast<int32_t>(u / per);
-    s.k0 = static_cast<int32_t>(u - static_cast<int64_t>(s.item) * per);
-    const int64_t left = hi - u;
-    s.k1 = left < per - s.k0 ? s.k0 + static_cast<int32_t>(left) : per;
+    s.k0 = static_cast<int32_t>(u - s.item * per);
+    const uint32_t end = s.k0 + (hi - u);
+    s.k1 = static_cast<int32_t>(end < per ? end : per);
     return s;
-  }
-  __device__ __forceinline__ int block_of(int64_t u) const {
-    return static_cast<int>(((u + 1) * n - 1) / total);
-  }
-  // the first of block b's parts is that of the item its share begins in; of
-  // an item's blocks only the first may have begun in an earlier one
-  __device__ __forceinline__ int first_slot(int b, int32_t item) const {
-    return total * b / n / per == item ? 0 : 1;
   }
 };
 
@@ -359,12 +386,9 @@ __device__ __forceinline__ void epi_sync() {
 }
 
 // Adds one to *word after everything that this thread has seen done (its
-// block's writes before a barrier among it), and sees what was done before
-// the earlier additions.
-__device__ __forceinline__ uint32_t add_acq_rel(uint32_t* word) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(word) : "memory");
-  return old;
+// block's writes before a barrier among it).
+__device__ __forceinline__ void add_release(uint32_t* word) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(word) : "memory");
 }
 
 // Waits until *word reaches `want`.
@@ -437,7 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Routing: every block for itself, block 0 reports it.
   const float* logits = reinterpret_cast<const float*>(p.workspace + l.logits);
-  for (int t = warp; t < p.tokens; t += kThreads / 32) select_token(p, logits, t, sh);
+  if (p.experts <= 64)
+    select_all<2, 4>(p, logits, kThreads / 32, sh);
+  else if (p.experts <= 128)
+    select_all<4, 4>(p, logits, kThreads / 32, sh);
+  else
+    select_all<kMaxExperts / 32, 1>(p, logits, kThreads / 32, sh);
   __syncthreads();
   if (warp == 2) {
     uint32_t before = 0;
@@ -495,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // phase 1: gate tile with x's record, then the up tile (same record)
     const int64_t mat1 = static_cast<int64_t>(it_count) * ht_count * kSfBytes;
-    for (int64_t u = share1.lo; u < share1.hi && ok;) {
+    for (uint32_t u = share1.lo; u < share1.hi && ok;) {
       const Segment g = share1.at(u);
       const int32_t e = sh->expert[g.item / it_count], tile = g.item % it_count;
       const int32_t y = e * p.inter + tile * kTile;
@@ -543,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              p.down_scales + e * mat2 + (static_cast<int64_t>(item) * it_count + kt) * kSfBytes,
              kt * kTile, e * p.hidden + item * kTile);
     };
-    int64_t u = share2.lo;  // (a block without a share has nothing at the front)
+    uint32_t u = share2.lo;  // (a block without a share has nothing at the front)
     const int first = stage;
     int ahead = 0;
     for (; ok && ahead < stages && u < share2.hi; ++ahead, ++u) {
@@ -623,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Share& share = ph == 0 ? share1 : share2;
       const uint32_t idesc = mxf8_idesc(ph == 0 ? p.type_gu : p.type_d, 0, kTile, kTerms * pad, 0, 0);
       const int32_t k_blocks = ((ph == 0 ? p.hidden : p.inter) + 31) / 32;
-      for (int64_t u = share.lo; u < share.hi && ok;) {
+      for (uint32_t u = share.lo; u < share.hi && ok;) {
         const Segment g = share.at(u);
         if (!mbar_wait_warp(&sh->acc_empty[acc], acc_phase ^ 1u, s_abort, p.status,
                             p.wait_limit_ns)) {
@@ -670,139 +699,193 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const uint32_t q = warp & 3u;                     // tensor-memory lanes 32 q ..+31
-    const uint32_t half = (warp - 2) >> 2;            // of the token columns
-    const int row = static_cast<int>(q * 32 + lane);  // of the tile
-    const int tid = static_cast<int>(threadIdx.x) - 64;
-    const int t_begin = static_cast<int>(half) * (pad / 2), t_end = t_begin + pad / 2;
-    float* parts = reinterpret_cast<float*>(p.workspace + l.parts);
-    const int64_t part_size = static_cast<int64_t>(2) * pad * kTile;
-    uint32_t acc = 0, acc_phase = 0;
     // (after a wait gave up every item is still gone through, without work,
     // so that all epilogue warps meet at every barrier)
+    const uint32_t q = warp & 3u;                     // tensor-memory lanes 32 q ..+31
+    const int half = static_cast<int>(warp - 2) >> 2; // of an item's tokens
+    const int row = static_cast<int>(q * 32 + lane);  // of the tile
+    const int tid = static_cast<int>(threadIdx.x) - 64;
+    float* parts = reinterpret_cast<float*>(p.workspace + l.parts) + row;
+    const int64_t part_size = static_cast<int64_t>(2) * pad * kTile;
+    const uint32_t t_lane = tmem + (q * 32u << 16);
+    uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
-    for (int ph = 0; ph < 2; ++ph) {
-      const Share& share = ph == 0 ? share1 : share2;
-      const int mats = ph == 0 ? 2 : 1;               // accumulators of an item
-      for (int64_t u = share.lo; u < share.hi;) {
-        const Segment g = share.at(u);
-        const int64_t u0 = static_cast<int64_t>(g.item) * share.per;
-        u += g.k1 - g.k0;
-        const int32_t a = g.item / it_count;          // phase 1: index of the expert
-        if (ph == 0 && tid < p.tokens) {
-          const int e = sh->expert[a];
-          float w = -1.f;
+    auto wait_acc = [&] {
+      const bool got =
+          mbar_wait(&sh->acc_full[acc], acc_phase, s_abort, p.status, p.wait_limit_ns);
+      if (!__all_sync(0xffffffffu, got)) ok = false;
+      tc_fence_after_sync();
+    };
+    auto release_acc = [&] {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+      if (++acc == acc_sets) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    };
+    // Sum of the parts of blocks c0 + 1 .. c1, in that order, of N values, the
+    // i-th `at(i)` floats into a part and wanted where want(i).
+    auto add_parts = [&](uint32_t c0, uint32_t c1, auto& v, auto want, auto at) {
+      constexpr int N = sizeof(v) / sizeof(float);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+      for (uint32_t c = c0 + 1; c <= c1; c += kPartsAtOnce) {
+        float r[kPartsAtOnce][N];
+#pragma unroll
+        for (int b = 0; b < kPartsAtOnce; ++b)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            r[b][i] = c + b <= c1 && want(i) ? __ldcg(parts + (c + b) * part_size + at(i)) : 0.f;
+#pragma unroll
+        for (int b = 0; b < kPartsAtOnce; ++b)
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[i] += r[b][i];
+      }
+    };
+
+    // phase 1: activations of 128 channels of one expert, for its tokens
+    int buf = 0;
+    for (uint32_t u = share1.lo; u < share1.hi; buf ^= 1) {
+      const Segment g = share1.at(u);
+      u += g.k1 - g.k0;
+      const uint32_t u0 = g.item * share1.per;
+      const uint32_t c0 = share1.block_of(u0), c1 = share1.block_of(u0 + share1.per - 1);
+      const bool owner = g.k0 == 0;
+      const int32_t a = g.item / it_count, tile = g.item % it_count;
+      if (tid < kMaxTokens) {
+        const int e = sh->expert[a];
+        float w = -1.f;
+        if (tid < p.tokens)
           for (int k = 0; k < p.top_k; ++k)
             if (sh->id[tid * p.top_k + k] == e) w = sh->weight[tid * p.top_k + k];
-          sh->share[tid] = w;
+        const bool in = !(w < 0.f);
+        const uint32_t bits = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) sh->routed[buf][tid >> 5] = bits;
+        if (in) {
+          // (a second warp's come from the back; the order among tokens has no effect)
+          const int at = __popc(bits & ((1u << lane) - 1u));
+          const int place = tid < 32 ? at : kMaxTokens - 1 - at;
+          sh->token[buf][place] = static_cast<uint16_t>(tid);
+          sh->share[buf][place] = w;
         }
-        const bool got = mbar_wait(&sh->acc_full[acc], acc_phase, s_abort, p.status, p.wait_limit_ns);
-        if (!__all_sync(0xffffffffu, got)) ok = false;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + (q * 32u << 16) + acc * acc_cols;
-        // accumulator m's values for tokens t..t+7: hi's column plus lo's
-        auto read_acc = [&](int m, int t, float (&v)[8]) {
-          uint32_t hi[8], lo[8];
-          tmem_ld_32x32b_x8(d + m * kTerms * pad + t, hi);
-          tmem_ld_32x32b_x8(d + m * kTerms * pad + pad + t, lo);
-          tmem_ld_wait();
+      }
+      if (owner && c1 > c0 && tid == 0)
+        wait_count(counters + c0, c1 - c0, s_abort, p.status, p.wait_limit_ns);
+      epi_sync();
+      if (*s_abort) ok = false;
+      const uint32_t low = __popc(sh->routed[buf][0]);
+      const int count = static_cast<int>(low + __popc(sh->routed[buf][1]));
+      const int i_begin = half == 0 ? 0 : (count + 1) / 2;
+      const int i_end = half == 0 ? (count + 1) / 2 : count;
+      auto place = [&](int i) { return i < static_cast<int>(low) ? i : kMaxTokens - 1 - (i - static_cast<int>(low)); };
+      uint8_t* record = p.workspace + l.h + g.item * record_bytes(pad);
+      if (owner && ok) {
+        // a token that did not choose this expert has zeros: a lane each
+        const int t = half * 32 + static_cast<int>(lane);
+        if (t < p.tokens && !(sh->routed[buf][half] >> lane & 1u)) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
-        };
-        const bool whole = g.k1 - g.k0 == share.per;
-        bool mine = whole;
-        int c0 = 0, c1 = -1;
-        if (!whole) {
-          // leave this block's part, and see whether it was the last
-          const int slot = u0 <= share.lo ? 0 : 1;
-          float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * part_size + row;
-          if (ok)
-            for (int m = 0; m < mats; ++m)
-              for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
-                float v[8];
-                read_acc(m, t, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (t + i < p.tokens) part[(m * pad + t + i) * kTile] = v[i];
-              }
-          c0 = share.block_of(u0);
-          c1 = share.block_of(u0 + share.per - 1);
-          epi_sync();
-          if (tid == 0) sh->ticket = add_acq_rel(counters + ph * kMaxBlocks + c0);
-          epi_sync();
-          mine = sh->ticket == static_cast<uint32_t>(c1 - c0);
-        } else if (ph == 0) {
-          epi_sync();                                 // sh->share is complete
-        }
-        if (mine && ok) {
-          const float* part0 =
-              parts + (2 * static_cast<int64_t>(c0) + (whole ? 0 : share.first_slot(c0, g.item))) * part_size + row;
-          const float* part1 = parts + 2 * static_cast<int64_t>(c0) * part_size + row;  // + 2 per block
-          for (int t = t_begin; t < t_end && t < p.tokens; t += 8) {
-            float v[2][8];
-            if (whole) {
-              for (int m = 0; m < mats; ++m) read_acc(m, t, v[m]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[0][i] = v[1][i] = 0.f;
-              for (int c = c0; c <= c1; c += kPartsAtOnce) {
-                float r[kPartsAtOnce][2][8];
-#pragma unroll
-                for (int b = 0; b < kPartsAtOnce; ++b) {
-                  const float* from =
-                      c + b == c0 ? part0 : part1 + 2 * static_cast<int64_t>(c + b - c0) * part_size;
-#pragma unroll
-                  for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                      r[b][m][i] = m < mats && c + b <= c1 && t + i < p.tokens
-                                       ? __ldcg(from + (m * pad + t + i) * kTile)
-                                       : 0.f;
-                }
-#pragma unroll
-                for (int b = 0; b < kPartsAtOnce; ++b)
-#pragma unroll
-                  for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[m][i] += r[b][m][i];
-              }
-            }
-            if (ph == 0) {
-              uint8_t* record = p.workspace + l.h + g.item * record_bytes(pad);
-              const bool in = g.item % it_count * kTile + row < p.inter;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (t + i >= p.tokens) break;
-                const float w = sh->share[t + i];
-                const float act = v[0][i] / (1.f + expf(-v[0][i])) * v[1][i];
-                write_block(record, pad, t + i, q, in && !(w < 0.f) ? act * w : 0.f);
-              }
-            } else {
-              const int c = g.item * kTile + row;
-              if (c < p.hidden) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (t + i < p.tokens)
-                    static_cast<__nv_bfloat16*>(p.y)[(t + i) * p.ldy + c] = __float2bfloat16_rn(v[0][i]);
-              }
-            }
+          for (int term = 0; term < kTerms; ++term) {
+            const int r = term * pad + t;
+            *reinterpret_cast<uint4*>(record + code_at(r, q * 32)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(record + code_at(r, q * 32 + 16)) = make_uint4(0, 0, 0, 0);
+            record[code_bytes(pad) + scale_at(r, q)] = 127;
           }
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
-        if (ph == 0 && mine) {
-          // the activations are there for every block's copies
-          fence_proxy_async_global();
-          epi_sync();
-          if (tid == 0) add_acq_rel(counters + kDoneWord);
-        } else if (ph == 0) {
-          epi_sync();                                 // sh->share may be written again
+      }
+      bool held = false;                              // the accumulator is there
+      for (int i0 = i_begin; i0 < i_end; i0 += kTokensAtOnce) {
+        float v[2 * kTokensAtOnce];                   // gates, then ups
+        auto want = [&](int i) { return i0 + i % kTokensAtOnce < i_end; };
+        auto at = [&](int i) { return (i / kTokensAtOnce * pad + i0 + i % kTokensAtOnce) * kTile; };
+        if (owner && ok)
+          add_parts(c0, c1, v, want, at);
+        if (!held) wait_acc();
+        held = true;
+        if (!ok) break;
+        const uint32_t d = t_lane + acc * acc_cols;
+        uint32_t hi[2 * kTokensAtOnce], lo[2 * kTokensAtOnce];
+#pragma unroll
+        for (int i = 0; i < 2 * kTokensAtOnce; ++i)
+          if (want(i)) {
+            const uint32_t col = d + i / kTokensAtOnce * kTerms * pad +
+                                 sh->token[buf][place(i0 + i % kTokensAtOnce)];
+            tmem_ld_32x32b_x1(col, hi[i]);
+            tmem_ld_32x32b_x1(col + pad, lo[i]);
+          }
+        tmem_ld_wait();
+        if (!owner) {
+#pragma unroll
+          for (int i = 0; i < 2 * kTokensAtOnce; ++i)
+            if (want(i))
+              parts[blockIdx.x * part_size + at(i)] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+          continue;
         }
-        if (++acc == acc_sets) {
-          acc = 0;
-          acc_phase ^= 1u;
+#pragma unroll
+        for (int i = 0; i < kTokensAtOnce; ++i) {
+          if (!want(i)) break;
+          const int j = i + kTokensAtOnce, pl = place(i0 + i);
+          const float gate = v[i] + (__uint_as_float(hi[i]) + __uint_as_float(lo[i]));
+          const float up = v[j] + (__uint_as_float(hi[j]) + __uint_as_float(lo[j]));
+          const float act = gate / (1.f + expf(-gate)) * up;
+          write_block(record, pad, sh->token[buf][pl], q,
+                      tile * kTile + row < p.inter ? act * sh->share[buf][pl] : 0.f);
         }
+      }
+      if (!held) wait_acc();
+      release_acc();
+      // an owner's records are for every block's copies
+      if (owner) fence_proxy_async_global();
+      epi_sync();
+      if (tid == 0) add_release(owner ? counters + kDoneWord : counters + c0);
+    }
+
+    // phase 2: 128 channels of y, for all tokens
+    const int t_begin = half * (pad / 2);
+    const int t_end = t_begin + pad / 2 < p.tokens ? t_begin + pad / 2 : p.tokens;
+    for (uint32_t u = share2.lo; u < share2.hi;) {
+      const Segment g = share2.at(u);
+      u += g.k1 - g.k0;
+      const uint32_t u0 = g.item * share2.per;
+      const uint32_t c0 = share2.block_of(u0), c1 = share2.block_of(u0 + share2.per - 1);
+      const bool owner = g.k0 == 0;
+      if (owner && c1 > c0) {
+        if (tid == 0)
+          wait_count(counters + kMaxBlocks + c0, c1 - c0, s_abort, p.status, p.wait_limit_ns);
+        epi_sync();
+        if (*s_abort) ok = false;
+      }
+      bool held = false;
+      for (int t = t_begin; t < t_end; t += 8) {
+        float v[8];
+        auto want = [&](int i) { return t + i < t_end; };
+        auto at = [&](int i) { return (t + i) * kTile; };
+        if (owner && ok) add_parts(c0, c1, v, want, at);
+        if (!held) wait_acc();
+        held = true;
+        if (!ok) break;
+        const uint32_t d = t_lane + acc * acc_cols + t;
+        uint32_t hi[8], lo[8];
+        tmem_ld_32x32b_x8(d, hi);
+        tmem_ld_32x32b_x8(d + pad, lo);
+        tmem_ld_wait();
+        const int c = g.item * kTile + row;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!want(i)) break;
+          const float own = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+          if (!owner)
+            parts[blockIdx.x * part_size + at(i)] = own;
+          else if (c < p.hidden)
+            static_cast<__nv_bfloat16*>(p.y)[(t + i) * p.ldy + c] = __float2bfloat16_rn(v[i] + own);
+        }
+      }
+      if (!held) wait_acc();
+      release_acc();
+      if (!owner) {
+        epi_sync();
+        if (tid == 0) add_release(counters + kMaxBlocks + c0);
       }
     }
   }
@@ -854,15 +937,16 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
   size_t stages = (kSmemMax - 1024 - sizeof(Shared)) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // the blocks wait for one another
   attr[0].val.cooperative = 1;
+  attr[1] = pdl_attribute();
   cfg.gridDim = dim3(static_cast<unsigned>(num_sms < kMaxBlocks ? num_sms : kMaxBlocks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = stages * stage + sizeof(Shared) + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, moe_experts_kernel, tmap_gate, tmap_up, tmap_down, p,
                             static_cast<int>(stages));
 }

@@ -396,6 +396,11 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
       : "r"(taddr));
 }
 
+// Load one 32-bit column.
+__device__ __forceinline__ void tmem_ld_32x32b_x1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+
 // Orders this thread's generic-proxy accesses of global memory with copies
 // (async proxy) that it, or a thread it synchronizes with, issues later.
 __device__ __forceinline__ void fence_proxy_async_global() {

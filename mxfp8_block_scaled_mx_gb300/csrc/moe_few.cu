@@ -152,6 +152,44 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
+// Logits of expert e for tokens t0 .. t0 + nt - 1 (nt <= T), the share of the
+// warp's quarter of the row, complete in every lane.
+template <int T>
+__device__ __forceinline__ void dot_tokens(const MoeFewParams& p, int e, int t0, int nt,
+                                           float (&sum)[kRouterTokens]) {
+  const __nv_bfloat16* x[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)  // (past the last token: that token again, not used)
+    x[i] = static_cast<const __nv_bfloat16*>(p.x) + (t0 + (i < nt ? i : nt - 1)) * p.ldx;
+  const int64_t row = static_cast<int64_t>(e) * p.hidden;
+#pragma unroll 2
+  for (int c = static_cast<int>((warp_id() & 3) * 32 + lane_id()) * 8; c < p.hidden; c += 4 * 32 * 8) {
+    uint4 raw[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) raw[i] = *reinterpret_cast<const uint4*>(x[i] + c);
+    float w[8];
+    if (p.router_fp32) {
+      const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + row + c);
+      const float4 a = r[0], b = r[1];
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.router) + row + c), w);
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      float v[8];
+      unpack8(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[i] += w[j] * v[j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < T; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+}
+
 // Blocks [0, logit_blocks): logits of two experts for eight tokens.  The rest:
 // x's records, a warp per token and K tile.  Block 0 also clears the counters.
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFewParams p,
@@ -161,22 +199,25 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
   pdl_launch_dependents();
   const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
   const uint32_t warp = warp_id(), lane = lane_id();
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= kDoneWord; i += kRouterThreads)
       reinterpret_cast<uint32_t*>(p.workspace)[i] = 0;
   if (static_cast<int>(blockIdx.x) >= logit_blocks) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
     const int kt_count = static_cast<int>(tiles(p.hidden));
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) - logit_blocks) * (kRouterThreads / 32) + warp;
-    const int t = static_cast<int>(w / kt_count), kt = static_cast<int>(w % kt_count);
+    const int w = (static_cast<int>(blockIdx.x) - logit_blocks) * (kRouterThreads / 32) + static_cast<int>(warp);
+    const int t = w / kt_count, kt = w % kt_count;
     if (t >= p.tokens) return;
     const int pad = pad_tokens(p.tokens);
     uint8_t* record = p.workspace + l.x + kt * record_bytes(pad);
+    float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = kt * kTile + j * 32 + static_cast<int>(lane);
-      write_block(record, pad, t, j, c < p.hidden ? __bfloat162float(x[t * p.ldx + c]) : 0.f);
+      v[j] = c < p.hidden ? __bfloat162float(x[t * p.ldx + c]) : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) write_block(record, pad, t, j, v[j]);
     return;
   }
   const int groups = (p.experts + kRouterExperts - 1) / kRouterExperts;
@@ -187,35 +228,16 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
 #pragma unroll
   for (int i = 0; i < kRouterTokens; ++i) sum[i] = 0.f;
   if (e < p.experts) {
-    const int64_t row = static_cast<int64_t>(e) * p.hidden;
-#pragma unroll 2
-    for (int c = (static_cast<int>(warp & 3) * 32 + static_cast<int>(lane)) * 8; c < p.hidden;
-         c += 4 * 32 * 8) {
-      float w[8];
-      if (p.router_fp32) {
-        const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + row + c);
-        const float4 a = r[0], b = r[1];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-      } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.router) + row + c), w);
-      }
-#pragma unroll
-      for (int i = 0; i < kRouterTokens; ++i) {
-        if (i >= nt) break;
-        float v[8];
-        unpack8(*reinterpret_cast<const uint4*>(x + (t0 + i) * p.ldx + c), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[i] += w[j] * v[j];
-      }
-    }
+    if (nt == 1)
+      dot_tokens<1>(p, e, t0, nt, sum);
+    else if (nt <= 4)
+      dot_tokens<4>(p, e, t0, nt, sum);
+    else
+      dot_tokens<kRouterTokens>(p, e, t0, nt, sum);
   }
 #pragma unroll
-  for (int i = 0; i < kRouterTokens; ++i) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+  for (int i = 0; i < kRouterTokens; ++i)
     if (lane == 0) part[warp][i] = sum[i];
-  }
   __syncthreads();
   if ((warp & 3) == 0 && e < p.experts && static_cast<int>(lane) < nt) {
     float s = 0.f;

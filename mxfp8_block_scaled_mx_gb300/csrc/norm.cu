@@ -5,9 +5,11 @@
 //   n(v; w)_c = v_c w_c / sqrt(mean(v^2) + eps)
 //
 // Both directions are bound by memory: every row is read and written once.
-// A thread owns the same columns of every array of a row (eight in a run
-// where rows and pointers allow 16-byte accesses, else every T-th one), so
-// the only exchange within a row is the sum behind each norm.
+// A thread owns the same columns of every array of a row (runs of eight where
+// rows and pointers allow 16-byte accesses, else every T-th one), so the only
+// exchange within a row is the sum behind each norm.  Arithmetic is FP32, two
+// columns an instruction (f32x2): at memory speed a row leaves an SM about 20
+// instructions per column pair and direction, so their number counts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,99 +23,162 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+// ------------------------------------------------------------------ pairs of columns
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // ------------------------------------------------------------------ columns of a thread
 
-// The columns that thread `tid` of `threads` owns, NV runs of eight.  VEC:
-// run v is columns 8 (v threads + tid) ..+7, accessed 16 bytes at a time;
-// else element j of run v is column (8 v + j) threads + tid.
-template <bool VEC>
+// How a thread's NV runs of eight columns lie in a row:
+// kWhole  run v is columns 8 (v threads + tid) ..+7, 16 bytes an access, and
+//         the row has exactly 8 NV threads columns;
+// kRuns   the same with an end inside (whole runs of eight);
+// kSingle element j of run v is column (8 v + j) threads + tid, one at a time.
+enum Mode { kWhole, kRuns, kSingle };
+
+template <Mode M>
 struct Cols {
   int32_t cols, tid, threads;
-  __device__ __forceinline__ bool any(int v) const {
-    return VEC ? 8 * (v * threads + tid) < cols : 8 * v * threads + tid < cols;
+  __device__ __forceinline__ int32_t at(int v, int j) const {
+    return M == kSingle ? (8 * v + j) * threads + tid : 8 * (v * threads + tid) + j;
   }
   __device__ __forceinline__ bool has(int v, int j) const {
-    return VEC ? any(v) : (8 * v + j) * threads + tid < cols;
-  }
-  __device__ __forceinline__ int32_t at(int v, int j) const {
-    return VEC ? 8 * (v * threads + tid) + j : (8 * v + j) * threads + tid;
+    return M == kWhole || at(v, M == kRuns ? 0 : j) < cols;
   }
 };
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
+// A run of eight elements as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<bf16> {
+  uint32_t w[4];
+  __device__ __forceinline__ float2 get(int i) const { return unpack2(w[i]); }
+};
+template <>
+struct Raw<float> {
+  float2 f[4];
+  __device__ __forceinline__ float2 get(int i) const { return f[i]; }
+};
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ uint32_t bits(bf16 v) { return *reinterpret_cast<const uint16_t*>(&v); }
 
 // Run v of a row; elements past its end read as zero.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, const Cols<VEC>& c, int v, float (&f)[8]) {
-  if constexpr (VEC) {
-    if (!c.any(v)) {
+template <typename T, Mode M>
+__device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
+  Raw<T> r;
+  if constexpr (M == kSingle) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.f;
-    } else if constexpr (sizeof(T) == 2) {
-      unpack(*reinterpret_cast<const uint4*>(row + c.at(v, 0)), f);
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(row + c.at(v, 0));
-      const float4 b = *reinterpret_cast<const float4*>(row + c.at(v, 4));
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    for (int i = 0; i < 4; ++i) {
+      const bool a = c.has(v, 2 * i), b = c.has(v, 2 * i + 1);
+      if constexpr (sizeof(T) == 2)
+        r.w[i] = (a ? bits(row[c.at(v, 2 * i)]) : 0u) | (b ? bits(row[c.at(v, 2 * i + 1)]) << 16 : 0u);
+      else
+        r.f[i] = make_float2(a ? row[c.at(v, 2 * i)] : 0.f, b ? row[c.at(v, 2 * i + 1)] : 0.f);
     }
   } else {
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (c.has(v, 0)) {
+      const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
+      x = p[0];
+      if constexpr (sizeof(T) == 4) y = p[1];
+    }
+    if constexpr (sizeof(T) == 2) {
+      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+    } else {
+      r.f[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+      r.f[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+      r.f[2] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
+      r.f[3] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
+    }
+  }
+  return r;
+}
+
+// f *= run v of a weight or gate, whose type is a run-time matter.
+template <Mode M>
+__device__ __forceinline__ void times_w(float2 (&f)[4], const void* w, int32_t f32, int64_t off,
+                                        const Cols<M>& c, int v) {
+  if (f32) {
+    const Raw<float> r = load8(static_cast<const float*>(w) + off, c, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c.has(v, j) ? to_float(row[c.at(v, j)]) : 0.f;
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], r.get(i));
+  } else {
+    const Raw<bf16> r = load8(static_cast<const bf16*>(w) + off, c, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], r.get(i));
   }
 }
 
-// The same of a weight or gate, whose type is a run-time matter.
-template <bool VEC>
-__device__ __forceinline__ void load8_w(const void* w, int32_t f32, int64_t off,
-                                        const Cols<VEC>& c, int v, float (&f)[8]) {
-  if (f32)
-    load8(static_cast<const float*>(w) + off, c, v, f);
-  else
-    load8(static_cast<const bf16*>(w) + off, c, v, f);
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int v, const float (&f)[8]) {
-  if constexpr (VEC) {
-    if (!c.any(v)) return;
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(row + c.at(v, 0)) =
-          make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-    } else {
-      *reinterpret_cast<float4*>(row + c.at(v, 0)) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(row + c.at(v, 4)) = make_float4(f[4], f[5], f[6], f[7]);
-    }
-  } else {
+template <typename T, Mode M>
+__device__ __forceinline__ void store8(T* row, const Cols<M>& c, int v, const Raw<T>& r) {
+  if constexpr (M == kSingle) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (c.has(v, j)) {
         if constexpr (sizeof(T) == 2)
-          row[c.at(v, j)] = __float2bfloat16_rn(f[j]);
+          row[c.at(v, j)] = __ushort_as_bfloat16(static_cast<uint16_t>(r.w[j / 2] >> (j % 2 * 16)));
         else
-          row[c.at(v, j)] = f[j];
+          row[c.at(v, j)] = j % 2 ? r.f[j / 2].y : r.f[j / 2].x;
       }
+  } else {
+    if (!c.has(v, 0)) return;
+    uint4* p = reinterpret_cast<uint4*>(row + c.at(v, 0));
+    if constexpr (sizeof(T) == 2) {
+      p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else {
+      p[0] = make_uint4(__float_as_uint(r.f[0].x), __float_as_uint(r.f[0].y),
+                        __float_as_uint(r.f[1].x), __float_as_uint(r.f[1].y));
+      p[1] = make_uint4(__float_as_uint(r.f[2].x), __float_as_uint(r.f[2].y),
+                        __float_as_uint(r.f[3].x), __float_as_uint(r.f[3].y));
+    }
   }
 }
 
+// Eight FP32 values in type T (one rounding).
 template <typename T>
-__device__ __forceinline__ float round_to(float v) {
-  return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v;
+__device__ __forceinline__ Raw<T> round8(const float2 (&f)[4]) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2)
+      r.w[i] = pack2(f[i]);
+    else
+      r.f[i] = f[i];
+  }
+  return r;
 }
 
 // ------------------------------------------------------------------ sums over a row
@@ -121,27 +186,29 @@ __device__ __forceinline__ float round_to(float v) {
 constexpr int kMaxWarps = 32;
 
 // N sums over the block of threads, the same in every thread and run after
-// run.  `part` holds N * 32 floats that the block's previous sum does not
-// use (callers alternate between two), so one barrier is enough.
+// run.  `part` holds N * 32 floats (zeros past the last warp) that the block's
+// previous sum does not use (callers alternate between two), so one barrier
+// is enough.
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (blockDim.x == 32) return;
-  const uint32_t lane = lane_id(), warps = blockDim.x >> 5;
-  if (lane == 0) {
+  if (lane_id() == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) part[i * kMaxWarps + warp_id()] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = lane < warps ? part[i * kMaxWarps + lane] : 0.f;
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (uint32_t w = 0; w < blockDim.x / 32; w += 4)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  }
+    for (int i = 0; i < N; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(part + i * kMaxWarps + w);
+      v[i] += (f.x + f.y) + (f.z + f.w);
+    }
 }
 
 __device__ __forceinline__ float rms_inverse(float sum_squares, float cols, float eps) {
@@ -150,79 +217,95 @@ __device__ __forceinline__ float rms_inverse(float sum_squares, float cols, floa
 
 // ------------------------------------------------------------------ forward
 
-template <typename C, typename S, bool VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_residual_kernel(const NormParams p) {
-  __shared__ float part[2][kMaxWarps];
+// A block of threads goes through every gridDim.x-th row.  A row's registers
+// are free once the stream's row is formed, so the next row is loaded there,
+// behind the second norm.
+template <typename C, typename S, Mode M, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p) {
+  __shared__ __align__(16) float part[2][kMaxWarps];
+  if (threadIdx.x < 2 * kMaxWarps) part[0][threadIdx.x] = 0.f;
+  if (blockDim.x == 32) part[1][threadIdx.x] = 0.f;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const Cols<VEC> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                    static_cast<int32_t>(blockDim.x)};
+  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
+                  static_cast<int32_t>(blockDim.x)};
   const float cols = static_cast<float>(p.cols);
-  for (int64_t t = blockIdx.x; t < p.rows; t += gridDim.x) {
-    const C* brow = static_cast<const C*>(p.block) + t * p.ldb;
-    const S* rrow = static_cast<const S*>(p.residual) + t * p.ldr;
-    const int64_t goff = p.gate ? t / (p.rows / p.gates) * p.cols : 0;
-    float b[NV][8], r[NV][8];
+  const float2 alpha = both(p.alpha);
+  const uint32_t rows = static_cast<uint32_t>(p.rows);
+  const uint32_t per = p.gate ? rows / static_cast<uint32_t>(p.gates) : 1u;
+  Raw<C> b[NV];
+  Raw<S> r[NV];
+  auto fetch = [&](uint32_t t) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) load8(brow, c, v, b[v]);
+    for (int v = 0; v < NV; ++v) b[v] = load8(static_cast<const C*>(p.block) + t * p.ldb, c, v);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) load8(rrow, c, v, r[v]);
+    for (int v = 0; v < NV; ++v) r[v] = load8(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
+  };
+  uint32_t t = blockIdx.x;
+  fetch(t);
+  while (true) {
     float sum[1];
+    float2 sigma = both(1.f);
     if (p.w_post) {
-      sum[0] = 0.f;
+      float2 s = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[0] += b[v][j] * b[v][j];
+        for (int i = 0; i < 4; ++i) s = fma2(b[v].get(i), b[v].get(i), s);
+      sum[0] = s.x + s.y;
       block_sum(sum, part[0]);
-      const float sigma = rms_inverse(sum[0], cols, p.eps);
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float w[8];
-        load8_w(p.w_post, p.w_fp32, 0, c, v, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[v][j] *= sigma * w[j];
-      }
+      sigma = both(rms_inverse(sum[0], cols, p.eps));
     }
-    sum[0] = 0.f;
+    const int64_t goff = p.gate ? t / per * p.cols : 0;
+    Raw<S> out[NV];
+    float2 s = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (p.gate) {
-        float g[8];
-        load8_w(p.gate, p.w_fp32, goff, c, v, g);
+      float2 f[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[v][j] *= g[j];
-      }
+      for (int i = 0; i < 4; ++i) f[i] = mul2(b[v].get(i), sigma);
+      if (p.w_post) times_w(f, p.w_post, p.w_fp32, 0, c, v);
+      if (p.gate) times_w(f, p.gate, p.w_fp32, goff, c, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[v][j] = round_to<S>(p.alpha * r[v][j] + b[v][j]);
-      store8(static_cast<S*>(p.res_out) + t * p.ldo, c, v, r[v]);
+      for (int i = 0; i < 4; ++i) f[i] = fma2(alpha, r[v].get(i), f[i]);
+      out[v] = round8<S>(f);
+      store8(static_cast<S*>(p.res_out) + t * p.ldo, c, v, out[v]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[0] += r[v][j] * r[v][j];
+      for (int i = 0; i < 4; ++i) s = fma2(out[v].get(i), out[v].get(i), s);
     }
+    const uint32_t next = t + gridDim.x;
+    if (next < rows) fetch(next);
+    sum[0] = s.x + s.y;
     block_sum(sum, part[1]);
-    const float rho = rms_inverse(sum[0], cols, p.eps);
+    const float2 rho = both(rms_inverse(sum[0], cols, p.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float w[8];
-      load8_w(p.w_pre, p.w_fp32, 0, c, v, w);
+      float2 f[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[v][j] *= rho * w[j];
-      store8(static_cast<C*>(p.y) + t * p.ldy, c, v, r[v]);
+      for (int i = 0; i < 4; ++i) f[i] = mul2(out[v].get(i), rho);
+      times_w(f, p.w_pre, p.w_fp32, 0, c, v);
+      store8(static_cast<C*>(p.y) + t * p.ldy, c, v, round8<C>(f));
     }
+    if (next >= rows) return;
+    t = next;
     if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[1] is used in every row
   }
 }
 
 // ------------------------------------------------------------------ backward
 
-// Rows of block i of n: [rows i / n, rows (i + 1) / n).
-__host__ __device__ __forceinline__ int64_t first_row(int64_t rows, int64_t i, int64_t n) {
-  return rows * i / n;
-}
-// Block whose rows hold row t.
-__device__ __forceinline__ int64_t block_of_row(int64_t rows, int64_t t, int64_t n) {
-  return ((t + 1) * n - 1) / rows;
-}
+// Rows of block i of n: q each, the first r blocks one more.
+struct RowShare {
+  uint32_t q, r;
+  __host__ __device__ RowShare(uint32_t rows, uint32_t n) : q(rows / n), r(rows - rows / n * n) {}
+  __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * q + (i < r ? i : r); }
+  // block whose rows hold row t
+  __device__ __forceinline__ uint32_t of(uint32_t t) const {
+    const uint32_t m = r * (q + 1);
+    return t < m ? t / (q + 1) : r + (t - m) / q;
+  }
+};
 
 // Workspace of n blocks: sums over each block's rows, FP32 [n][cols] for
 // w_pre, [n][cols] for w_post, and [2n][cols] for gates whose rows several
@@ -237,29 +320,33 @@ __device__ __forceinline__ float* ws_gate(const NormBackParams& p, int64_t n, in
   return p.workspace + (2 * n + slot) * p.cols;
 }
 
+constexpr int kBackThreads = 512;   // at most, with 128 registers each
+
 // One block of threads goes through its own rows in order.  Rows arrive in
 // shared memory by bulk copies, `stages` rows ahead (stages 0: rows whose
 // addresses or sizes do not allow those, read in place), and are read from
-// there as often as needed, so a thread's registers hold only its column
-// sums (w_pre and D b sigma, 8 NV each) and D.
-template <typename C, typename S, bool VEC, int NV, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB)
+// there as often as needed, so a thread's registers hold its column sums
+// (w_pre and D b sigma, 8 NV each) and D, and little else.
+template <typename C, typename S, Mode M, int NV>
+__global__ void __launch_bounds__(kBackThreads)
     norm_backward_kernel(const NormBackParams p, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float part[2][3 * kMaxWarps];
+  __shared__ __align__(16) float part[2][3 * kMaxWarps];
   __shared__ uint64_t full[8];
   __shared__ uint32_t abort_word;
   volatile uint32_t* s_abort = &abort_word;
-  const Cols<VEC> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                    static_cast<int32_t>(blockDim.x)};
+  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
+                  static_cast<int32_t>(blockDim.x)};
   const float cols = static_cast<float>(p.cols);
-  const int64_t n = gridDim.x, me = blockIdx.x;
-  const int64_t lo = first_row(p.rows, me, n), hi = first_row(p.rows, me + 1, n);
+  const uint32_t n = gridDim.x, me = blockIdx.x;
+  const RowShare share(static_cast<uint32_t>(p.rows), n);
+  const uint32_t lo = share.start(me), hi = share.start(me + 1);
   const uint32_t cbytes = static_cast<uint32_t>(p.cols * sizeof(C));
   const uint32_t sbytes = static_cast<uint32_t>(p.cols * sizeof(S));
   const uint32_t stage_bytes = 2 * cbytes + 2 * sbytes;
   // sums of D b sigma g over finished gates (gates > 1), behind the ring
-  float* post_sum = reinterpret_cast<float*>(smem + static_cast<size_t>(stages) * stage_bytes);
+  float* post_sum = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  for (uint32_t i = threadIdx.x; i < 6 * kMaxWarps; i += blockDim.x) part[0][i] = 0.f;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     abort_word = 0;
@@ -268,8 +355,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  auto issue = [&](int64_t t, int s) {
-    uint8_t* dst = smem + static_cast<size_t>(s) * stage_bytes;
+  auto issue = [&](uint32_t t, int s) {
+    uint8_t* dst = smem + s * stage_bytes;
     mbar_arrive_expect_tx(&full[s], p.d_res ? stage_bytes : stage_bytes - sbytes);
     bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy, cbytes, &full[s]);
     bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb, cbytes, &full[s]);
@@ -282,25 +369,27 @@ __global__ void __launch_bounds__(MAXT, MINB)
     for (int s = 0; s < stages && lo + s < hi; ++s) issue(lo + s, s);
 
   const bool many = p.gates > 1;
-  const int64_t per = p.gates ? p.rows / p.gates : p.rows;
-  float pre[NV][8], q[NV][8];
+  const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
+  const float2 alpha = both(p.alpha);
+  float2 pre[NV][4], q[NV][4];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      pre[v][j] = q[v][j] = 0.f;
-      if (many && c.has(v, j)) post_sum[c.at(v, j)] = 0.f;
-    }
-  }
+    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = both(0.f);
+  if (many)
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.cols); i += blockDim.x)
+      post_sum[i] = 0.f;
+  __syncthreads();
   int stage = 0;
   uint32_t phase = 0;
-  int64_t group = lo / per, left = (group + 1) * per - lo;  // rows left of this gate
-  for (int64_t t = lo; t < hi; ++t) {
+  const uint32_t group0 = lo / per;
+  uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
+  for (uint32_t t = lo; t < hi; ++t) {
     const C *dy, *block;
     const S *res, *dres;
-    if (stages > 0) {
+    if (M != kSingle && stages > 0) {
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
-      const uint8_t* src = smem + static_cast<size_t>(stage) * stage_bytes;
+      const uint8_t* src = smem + stage * stage_bytes;
       dy = reinterpret_cast<const C*>(src);
       block = reinterpret_cast<const C*>(src + cbytes);
       res = reinterpret_cast<const S*>(src + 2 * cbytes);
@@ -311,87 +400,82 @@ __global__ void __launch_bounds__(MAXT, MINB)
       res = static_cast<const S*>(p.res_out) + t * p.ldr;
       dres = static_cast<const S*>(p.d_res) + (p.d_res ? t * p.ldd : 0);
     }
-    float d[NV][8];
-    float sum[3] = {0.f, 0.f, 0.f};
+    float2 d[NV][4];
+    float2 ss = both(0.f), sd = both(0.f), sb = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float x[8], y[8];
-      load8(res, c, v, x);
-      load8(dy, c, v, y);
-      load8_w(p.w_pre, p.w_fp32, 0, c, v, d[v]);
+      const Raw<S> x = load8(res, c, v);
+      const Raw<C> y = load8(dy, c, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum[0] += x[j] * x[j];
-        d[v][j] *= y[j];
-        sum[1] += d[v][j] * x[j];
+      for (int i = 0; i < 4; ++i) d[v][i] = y.get(i);
+      times_w(d[v], p.w_pre, p.w_fp32, 0, c, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ss = fma2(x.get(i), x.get(i), ss);
+        sd = fma2(d[v][i], x.get(i), sd);
       }
       if (p.w_post) {
-        load8(block, c, v, x);
+        const Raw<C> b = load8(block, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[2] += x[j] * x[j];
+        for (int i = 0; i < 4; ++i) sb = fma2(b.get(i), b.get(i), sb);
       }
     }
+    float sum[3] = {ss.x + ss.y, sd.x + sd.y, sb.x + sb.y};
     block_sum(sum, part[0]);
     // past this barrier nobody reads the previous row's stage any more
     if (stages > 0 && threadIdx.x == 0 && t > lo && t - 1 + stages < hi)
       issue(t - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
-    const float rho = rms_inverse(sum[0], cols, p.eps);
+    const float rho1 = rms_inverse(sum[0], cols, p.eps);
+    const float sigma1 = p.w_post ? rms_inverse(sum[2], cols, p.eps) : 1.f;
     // (in this order nothing leaves FP32's range before the product does)
-    const float k = rho * (rho * (rho * (sum[1] / cols)));
-    const float sigma = p.w_post ? rms_inverse(sum[2], cols, p.eps) : 1.f;
+    const float2 rho = both(rho1), sigma = both(sigma1);
+    const float2 k = both(-(rho1 * (rho1 * (rho1 * (sum[1] / cols)))));
     const int64_t goff = group * p.cols;
-    float dot[1] = {0.f};
+    float2 dot2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float x[8], y[8];
-      load8(res, c, v, x);
-      load8(dy, c, v, y);
+      const Raw<S> x = load8(res, c, v);
+      const Raw<C> y = load8(dy, c, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        pre[v][j] += y[j] * (x[j] * rho);
-        d[v][j] = rho * d[v][j] - x[j] * k;
+      for (int i = 0; i < 4; ++i) {
+        pre[v][i] = fma2(y.get(i), mul2(x.get(i), rho), pre[v][i]);
+        d[v][i] = fma2(x.get(i), k, mul2(rho, d[v][i]));
       }
       if (p.d_res) {
-        load8(dres, c, v, x);
+        const Raw<S> a = load8(dres, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[v][j] += x[j];
+        for (int i = 0; i < 4; ++i) d[v][i] = add2(d[v][i], a.get(i));
       }
+      float2 f[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = p.alpha * d[v][j];
-      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, x);
-      load8(block, c, v, x);
+      for (int i = 0; i < 4; ++i) f[i] = mul2(alpha, d[v][i]);
+      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, round8<S>(f));
+      const Raw<C> b = load8(block, c, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[v][j] += d[v][j] * (x[j] * sigma);
-      if (p.gate) {
-        load8_w(p.gate, p.w_fp32, goff, c, v, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[v][j] *= y[j];
-      }
+      for (int i = 0; i < 4; ++i) q[v][i] = fma2(d[v][i], mul2(b.get(i), sigma), q[v][i]);
+      if (p.gate) times_w(d[v], p.gate, p.w_fp32, goff, c, v);
       if (p.w_post) {
-        load8_w(p.w_post, p.w_fp32, 0, c, v, y);
+        times_w(d[v], p.w_post, p.w_fp32, 0, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          d[v][j] *= y[j];
-          dot[0] += d[v][j] * x[j];
-        }
+        for (int i = 0; i < 4; ++i) dot2 = fma2(d[v][i], b.get(i), dot2);
       }
     }
-    float m = 0.f;
     if (p.w_post) {
+      float dot[1] = {dot2.x + dot2.y};
       block_sum(dot, part[1]);
-      m = sigma * (sigma * (sigma * (dot[0] / cols)));
-    }
+      const float2 m = both(-(sigma1 * (sigma1 * (sigma1 * (dot[0] / cols)))));
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (p.w_post) {
-        float x[8];
-        load8(block, c, v, x);
+      for (int v = 0; v < NV; ++v) {
+        const Raw<C> b = load8(block, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[v][j] = sigma * d[v][j] - x[j] * m;
+        for (int i = 0; i < 4; ++i) d[v][i] = fma2(b.get(i), m, mul2(sigma, d[v][i]));
       }
-      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, d[v]);
+    } else if (blockDim.x > 32) {
+      __syncthreads();  // part[0] is used in every row
     }
-    if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[0] is used in every row
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, round8<C>(d[v]));
     if (blockDim.x == 32) __syncwarp();  // as the barriers above: this row's reads are done
     if (stages > 0 && ++stage == stages) {
       stage = 0;
@@ -400,19 +484,23 @@ __global__ void __launch_bounds__(MAXT, MINB)
     if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
       if (p.gate) {
         const bool whole = group * per >= lo && t + 1 == (group + 1) * per;
-        float* slot = ws_gate(p, n, 2 * me + (group == lo / per ? 0 : 1));
+        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          float g[8], w[8];
-          load8_w(p.gate, p.w_fp32, goff, c, v, g);
-          if (p.w_post) load8_w(p.w_post, p.w_fp32, 0, c, v, w);
+          float2 dg[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!c.has(v, j)) continue;
-            const float dg = p.w_post ? q[v][j] * w[j] : q[v][j];
-            (whole ? p.d_gate + goff : slot)[c.at(v, j)] = dg;
-            if (many) post_sum[c.at(v, j)] += q[v][j] * g[j];
-            q[v][j] = many ? 0.f : q[v][j] * g[j];
+          for (int i = 0; i < 4; ++i) dg[i] = q[v][i];
+          if (p.w_post) times_w(dg, p.w_post, p.w_fp32, 0, c, v);
+          times_w(q[v], p.gate, p.w_fp32, goff, c, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (c.has(v, 2 * i)) dst[c.at(v, 2 * i)] = dg[i].x;
+            if (c.has(v, 2 * i + 1)) dst[c.at(v, 2 * i + 1)] = dg[i].y;
+            if (many) {
+              if (c.has(v, 2 * i)) post_sum[c.at(v, 2 * i)] += q[v][i].x;
+              if (c.has(v, 2 * i + 1)) post_sum[c.at(v, 2 * i + 1)] += q[v][i].y;
+              q[v][i] = both(0.f);
+            }
           }
         }
       }
@@ -421,33 +509,40 @@ __global__ void __launch_bounds__(MAXT, MINB)
     }
   }
   if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
-    for (int s = 0; s < stages && lo + s < hi; ++s)
-      mbar_wait(&full[s], static_cast<uint32_t>((hi - lo - 1 - s) / stages) & 1u, s_abort,
-                p.status, p.wait_limit_ns, true);
+    for (uint32_t s = 0; s < static_cast<uint32_t>(stages) && lo + s < hi; ++s)
+      mbar_wait(&full[s], (hi - lo - 1 - s) / stages & 1u, s_abort, p.status, p.wait_limit_ns,
+                true);
   }
+  float* pre_out = ws_pre(p, me);
+  float* post_out = ws_post(p, n, me);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!c.has(v, j)) continue;
-      ws_pre(p, me)[c.at(v, j)] = pre[v][j];
-      if (p.w_post) ws_post(p, n, me)[c.at(v, j)] = many ? post_sum[c.at(v, j)] : q[v][j];
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!c.has(v, 2 * i + h)) continue;
+        const int at = c.at(v, 2 * i + h);
+        pre_out[at] = h ? pre[v][i].y : pre[v][i].x;
+        if (p.w_post) post_out[at] = many ? post_sum[at] : h ? q[v][i].y : q[v][i].x;
+      }
 }
 
-constexpr int kSumCols = 32, kSumParts = 16;
+constexpr int kSumCols = 32, kSumParts = 32;
 
-// Sums the blocks' parts in block order: job 0 w_pre, job 1 w_post, then
-// the gates whose rows several blocks share.
+// Sums the blocks' parts: job 0 w_pre, job 1 w_post, then the gates whose rows
+// several blocks share.  A block takes 32 columns; 32 runs of consecutive
+// parts are summed in order side by side, then joined in order.
 __global__ void __launch_bounds__(kSumCols* kSumParts)
-    norm_backward_sum_kernel(const NormBackParams p, int64_t n) {
+    norm_backward_sum_kernel(const NormBackParams p, uint32_t n) {
   __shared__ float part[kSumParts][kSumCols + 1];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t job = blockIdx.y;
+  const uint32_t job = blockIdx.y;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kSumCols + threadIdx.x % kSumCols;
-  const int part_id = threadIdx.x / kSumCols;
-  int64_t first = 0, count = n, group = 0;
+  const uint32_t run = threadIdx.x / kSumCols;
+  const RowShare share(static_cast<uint32_t>(p.rows), n);
+  uint32_t first = 0, count = n, group = 0, per = 0;
   float* out;
   if (job == 0) {
     out = p.d_w_pre;
@@ -455,32 +550,42 @@ __global__ void __launch_bounds__(kSumCols* kSumParts)
     if (!p.w_post) return;
     out = p.d_w_post;
   } else {
-    const int64_t per = p.rows / p.gates;
+    per = static_cast<uint32_t>(p.rows / p.gates);
     // the gates themselves, or the gate at the start of each block's rows
-    group = p.gates <= n ? job - 2 : first_row(p.rows, job - 1, n) / per;
+    group = p.gates <= n ? job - 2 : share.start(job - 1) / per;
     if (group >= p.gates) return;
-    first = block_of_row(p.rows, group * per, n);
-    count = block_of_row(p.rows, (group + 1) * per - 1, n) - first + 1;
+    first = share.of(group * per);
+    count = share.of((group + 1) * per - 1) - first + 1;
     if (count == 1 || (p.gates > n && first != job - 2)) return;
     out = p.d_gate + group * p.cols;
   }
   float s = 0.f;
   if (col < p.cols) {
-    // kSumParts runs of consecutive blocks, each in order
-    const int64_t end = count * (part_id + 1) / kSumParts;
-    for (int64_t i = count * part_id / kSumParts; i < end; ++i) {
-      const int64_t b = first + i;
-      if (job == 0)
-        s += ws_pre(p, b)[col];
-      else if (job == 1)
-        s += ws_post(p, n, b)[col];
-      else
-        s += ws_gate(p, n, 2 * b + (first_row(p.rows, b, n) >= group * (p.rows / p.gates) ? 0 : 1))[col];
+    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(count) * run / kSumParts);
+    const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(count) * (run + 1) / kSumParts);
+    const float* src;
+    int64_t step = p.cols;
+    if (job == 0) {
+      src = ws_pre(p, first);
+    } else if (job == 1) {
+      src = ws_post(p, n, first);
+    } else {
+      // blocks after the first begin inside this gate: their first slot
+      src = ws_gate(p, n, 2 * static_cast<int64_t>(first));
+      step = 2 * p.cols;
+    }
+    src += col;
+    if (job >= 2 && begin == 0 && end > 0 && share.start(first) < group * per) {
+      s = src[p.cols] ;
+      for (uint32_t i = 1; i < end; ++i) s += src[i * step];
+    } else {
+#pragma unroll 8
+      for (uint32_t i = begin; i < end; ++i) s += src[i * step];
     }
   }
-  part[part_id][threadIdx.x % kSumCols] = s;
+  part[run][threadIdx.x % kSumCols] = s;
   __syncthreads();
-  if (part_id == 0 && col < p.cols) {
+  if (run == 0 && col < p.cols) {
 #pragma unroll
     for (int i = 1; i < kSumParts; ++i) s += part[i][threadIdx.x];
     out[col] = s;
@@ -509,32 +614,56 @@ int row_threads(int64_t cols, int nv) {
   const int64_t runs = (cols + 7) / 8;
   return static_cast<int>(((runs + nv - 1) / nv + 31) / 32 * 32);
 }
+bool whole(int64_t cols, int nv) { return cols == 8 * static_cast<int64_t>(nv) * row_threads(cols, nv); }
 
-template <typename C, typename S, bool VEC>
-cudaError_t forward(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.rows));
-  if (p.cols <= 8192 && p.rows <= num_sms)
-    return launch(norm_residual_kernel<C, S, VEC, 1>, grid, row_threads(p.cols, 1), 0, stream, p);
-  if (p.cols <= 2048)
-    return launch(norm_residual_kernel<C, S, VEC, 1>, grid, row_threads(p.cols, 1), 0, stream, p);
-  return launch(norm_residual_kernel<C, S, VEC, 2>, grid, row_threads(p.cols, 2), 0, stream, p);
+template <typename C, typename S, Mode M, int NV>
+cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) {
+  const int threads = row_threads(p.cols, NV);
+  // blocks that an SM holds at once, from the register budget of each form
+  const int64_t fit = threads <= 512 ? 1536 / threads : 1;
+  const int64_t all = num_sms * (fit < 16 ? fit : 16);
+  const dim3 grid(static_cast<unsigned>(p.rows < all ? p.rows : all));
+  if (threads <= 512)
+    return launch(norm_residual_kernel<C, S, M, NV, 512>, grid, threads, 0, stream, p);
+  return launch(norm_residual_kernel<C, S, M, NV, 1024>, grid, threads, 0, stream, p);
 }
 
-// Blocks of the gradient for a row width: those that fit an SM side by side
-// with 64 registers a thread, times the SMs.
+template <typename C, typename S>
+cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
+  // few rows: as many threads as a row takes; else two runs a thread
+  const bool one = p.cols <= 512 || (p.cols <= 8192 && p.rows <= num_sms);
+  if (!vec)
+    return one ? forward_impl<C, S, kSingle, 1>(p, num_sms, stream)
+               : forward_impl<C, S, kSingle, 2>(p, num_sms, stream);
+  if (one)
+    return whole(p.cols, 1) ? forward_impl<C, S, kWhole, 1>(p, num_sms, stream)
+                            : forward_impl<C, S, kRuns, 1>(p, num_sms, stream);
+  return whole(p.cols, 2) ? forward_impl<C, S, kWhole, 2>(p, num_sms, stream)
+                          : forward_impl<C, S, kRuns, 2>(p, num_sms, stream);
+}
+
+// Runs of eight a thread holds in the gradient.
+int backward_runs(int64_t cols) { return cols <= 8192 ? 2 : 4; }
+
+// Blocks of the gradient side by side on an SM (128 registers a thread).
+int backward_fit(int64_t cols) {
+  const int fit = kBackThreads / row_threads(cols, backward_runs(cols));
+  return fit < 1 ? 1 : fit > 8 ? 8 : fit;
+}
+
+// Blocks of the gradient: those that fit the SMs, with four rows each at
+// least (a block's column sums are written and read once more).
 int64_t backward_blocks(int64_t rows, int64_t cols, int num_sms) {
-  const int threads = row_threads(cols, cols <= 8192 ? 1 : 2);
-  const int per_sm = threads <= 256 ? 4 : threads <= 512 ? 2 : 1;
-  const int64_t n = static_cast<int64_t>(num_sms) * per_sm;
-  return rows < n ? rows : n;
+  const int64_t most = static_cast<int64_t>(num_sms) * backward_fit(cols), want = (rows + 3) / 4;
+  return want < num_sms ? (rows < num_sms ? rows : num_sms) : want < most ? want : most;
 }
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
 constexpr size_t kRingBytes = 216 * 1024;
 
-template <typename C, typename S, bool VEC, int NV, int MAXT, int MINB>
+template <typename C, typename S, Mode M, int NV>
 cudaError_t backward_impl(const NormBackParams& p, int64_t n, cudaStream_t stream) {
-  auto kern = norm_backward_kernel<C, S, VEC, NV, MAXT, MINB>;
+  auto kern = norm_backward_kernel<C, S, M, NV>;
   static PerDeviceOnce setup;
   const cudaError_t err = setup.run([&]() -> cudaError_t {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -543,19 +672,20 @@ cudaError_t backward_impl(const NormBackParams& p, int64_t n, cudaStream_t strea
   if (err != cudaSuccess) return err;
   const size_t stage = p.cols * 2 * (sizeof(C) + sizeof(S));
   const size_t post = p.gates > 1 ? p.cols * 4 : 0;
-  size_t stages = VEC ? (kRingBytes / MINB - post) / stage : 0;
+  size_t stages = M != kSingle ? (kRingBytes / backward_fit(p.cols) - post) / stage : 0;
   stages = stages < 2 ? 0 : stages > 4 ? 4 : stages;
   return launch(kern, dim3(static_cast<unsigned>(n)), row_threads(p.cols, NV), stages * stage + post,
                 stream, p, static_cast<int>(stages));
 }
 
-template <typename C, typename S, bool VEC>
-cudaError_t backward(const NormBackParams& p, int64_t n, cudaStream_t stream) {
-  const int threads = row_threads(p.cols, 1);
-  if (threads <= 256) return backward_impl<C, S, VEC, 1, 256, 4>(p, n, stream);
-  if (threads <= 512) return backward_impl<C, S, VEC, 1, 512, 2>(p, n, stream);
-  if (threads <= 1024) return backward_impl<C, S, VEC, 1, 1024, 1>(p, n, stream);
-  return backward_impl<C, S, VEC, 2, 1024, 1>(p, n, stream);
+template <typename C, typename S>
+cudaError_t backward(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
+  if (backward_runs(p.cols) == 4)
+    return !vec ? backward_impl<C, S, kSingle, 4>(p, n, stream)
+                : backward_impl<C, S, kRuns, 4>(p, n, stream);
+  if (!vec) return backward_impl<C, S, kSingle, 2>(p, n, stream);
+  return whole(p.cols, 2) ? backward_impl<C, S, kWhole, 2>(p, n, stream)
+                          : backward_impl<C, S, kRuns, 2>(p, n, stream);
 }
 
 }  // namespace
@@ -572,13 +702,10 @@ cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t 
                    aligned16(p.w_post) && aligned16(p.gate) && p.ldb % ce == 0 &&
                    p.ldy % ce == 0 && p.ldr % se == 0 && p.ldo % se == 0;
   if (p.c_fp32)
-    return vec ? forward<float, float, true>(p, num_sms, stream)
-               : forward<float, float, false>(p, num_sms, stream);
+    return forward<float, float>(p, vec, num_sms, stream);
   if (p.s_fp32)
-    return vec ? forward<bf16, float, true>(p, num_sms, stream)
-               : forward<bf16, float, false>(p, num_sms, stream);
-  return vec ? forward<bf16, bf16, true>(p, num_sms, stream)
-             : forward<bf16, bf16, false>(p, num_sms, stream);
+    return forward<bf16, float>(p, vec, num_sms, stream);
+  return forward<bf16, bf16>(p, vec, num_sms, stream);
 }
 
 cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
@@ -601,20 +728,17 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
       backward_blocks(p.rows, p.cols, num_sms < kMaxSms ? num_sms : kMaxSms);
   cudaError_t err;
   if (p.c_fp32)
-    err = vec ? backward<float, float, true>(p, n, stream)
-              : backward<float, float, false>(p, n, stream);
+    err = backward<float, float>(p, vec, n, stream);
   else if (p.s_fp32)
-    err = vec ? backward<bf16, float, true>(p, n, stream)
-              : backward<bf16, float, false>(p, n, stream);
+    err = backward<bf16, float>(p, vec, n, stream);
   else
-    err = vec ? backward<bf16, bf16, true>(p, n, stream)
-              : backward<bf16, bf16, false>(p, n, stream);
+    err = backward<bf16, bf16>(p, vec, n, stream);
   if (err != cudaSuccess) return err;
   const int64_t jobs = 2 + (p.gates < n ? p.gates : n);
   return launch(norm_backward_sum_kernel,
                 dim3(static_cast<unsigned>((p.cols + kSumCols - 1) / kSumCols),
                      static_cast<unsigned>(jobs)),
-                kSumCols * kSumParts, 0, stream, p, n);
+                kSumCols * kSumParts, 0, stream, p, static_cast<uint32_t>(n));
 }
 
 }  // namespace mx

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "kernels.h"
@@ -59,6 +60,11 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ void store1(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
 // ------------------------------------------------------------------ columns of a thread
 
 // How a thread's NV runs of eight columns lie in a row:
@@ -95,8 +101,19 @@ struct Raw<float> {
 
 __device__ __forceinline__ uint32_t bits(bf16 v) { return *reinterpret_cast<const uint16_t*>(&v); }
 
-// Run v of a row; elements past its end read as zero.
-template <typename T, Mode M>
+// Sixteen bytes of global memory that are read once: they take no place of the
+// weights' in L1.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Run v of a row; elements past its end read as zero.  ONCE: a row of global
+// memory that is not read again.
+template <bool ONCE = false, typename T, Mode M>
 __device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
   Raw<T> r;
   if constexpr (M == kSingle) {
@@ -112,8 +129,8 @@ __device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
     uint4 x = make_uint4(0, 0, 0, 0), y = x;
     if (c.has(v, 0)) {
       const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
-      x = p[0];
-      if constexpr (sizeof(T) == 4) y = p[1];
+      x = ONCE ? load_once(p) : p[0];
+      if constexpr (sizeof(T) == 4) y = ONCE ? load_once(p + 1) : p[1];
     }
     if constexpr (sizeof(T) == 2) {
       r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
@@ -211,8 +228,14 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
     }
 }
 
-__device__ __forceinline__ float rms_inverse(float sum_squares, float cols, float eps) {
-  return 1.f / sqrtf(sum_squares / cols + eps);
+// 1 / sqrt(mean + eps): the hardware's estimate and one Newton step, which
+// leaves an error of about one unit in the last place (and 1 / 0 and 1 / inf
+// as they are, where the step would make NaN).
+__device__ __forceinline__ float rms_inverse(float sum_squares, float inv_cols, float eps) {
+  const float m = sum_squares * inv_cols + eps;
+  const float r = rsqrtf(m);
+  const float s = r + r * 0.5f * (1.f - m * r * r);
+  return m > 0.f && m < INFINITY ? s : r;
 }
 
 // ------------------------------------------------------------------ forward
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
   pdl_launch_dependents();
   const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
                   static_cast<int32_t>(blockDim.x)};
-  const float cols = static_cast<float>(p.cols);
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
   const float2 alpha = both(p.alpha);
   const uint32_t rows = static_cast<uint32_t>(p.rows);
   const uint32_t per = p.gate ? rows / static_cast<uint32_t>(p.gates) : 1u;
@@ -238,9 +261,9 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
   Raw<S> r[NV];
   auto fetch = [&](uint32_t t) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) b[v] = load8(static_cast<const C*>(p.block) + t * p.ldb, c, v);
+    for (int v = 0; v < NV; ++v) b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) r[v] = load8(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
+    for (int v = 0; v < NV; ++v) r[v] = load8<true>(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
   };
   uint32_t t = blockIdx.x;
   fetch(t);
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
         for (int i = 0; i < 4; ++i) s = fma2(b[v].get(i), b[v].get(i), s);
       sum[0] = s.x + s.y;
       block_sum(sum, part[0]);
-      sigma = both(rms_inverse(sum[0], cols, p.eps));
+      sigma = both(rms_inverse(sum[0], inv_cols, p.eps));
     }
     const int64_t goff = p.gate ? t / per * p.cols : 0;
     Raw<S> out[NV];
@@ -278,7 +301,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
     if (next < rows) fetch(next);
     sum[0] = s.x + s.y;
     block_sum(sum, part[1]);
-    const float2 rho = both(rms_inverse(sum[0], cols, p.eps));
+    const float2 rho = both(rms_inverse(sum[0], inv_cols, p.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float2 f[4];
@@ -325,7 +348,8 @@ constexpr int kBackThreads = 512;   // at most, with 128 registers each
 // One block of threads goes through its own rows in order.  Rows arrive in
 // shared memory by bulk copies, `stages` rows ahead (stages 0: rows whose
 // addresses or sizes do not allow those, read in place), and are read from
-// there as often as needed, so a thread's registers hold its column sums
+// there as often as needed; d_res, which is needed once, goes to registers at
+// the start of its row.  A thread's registers hold that, its column sums
 // (w_pre and D b sigma, 8 NV each) and D, and little else.
 template <typename C, typename S, Mode M, int NV>
 __global__ void __launch_bounds__(kBackThreads)
@@ -337,13 +361,13 @@ __global__ void __launch_bounds__(kBackThreads)
   volatile uint32_t* s_abort = &abort_word;
   const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
                   static_cast<int32_t>(blockDim.x)};
-  const float cols = static_cast<float>(p.cols);
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
   const uint32_t n = gridDim.x, me = blockIdx.x;
   const RowShare share(static_cast<uint32_t>(p.rows), n);
   const uint32_t lo = share.start(me), hi = share.start(me + 1);
   const uint32_t cbytes = static_cast<uint32_t>(p.cols * sizeof(C));
   const uint32_t sbytes = static_cast<uint32_t>(p.cols * sizeof(S));
-  const uint32_t stage_bytes = 2 * cbytes + 2 * sbytes;
+  const uint32_t stage_bytes = 2 * cbytes + sbytes;
   // sums of D b sigma g over finished gates (gates > 1), behind the ring
   float* post_sum = reinterpret_cast<float*>(smem + stages * stage_bytes);
   for (uint32_t i = threadIdx.x; i < 6 * kMaxWarps; i += blockDim.x) part[0][i] = 0.f;
@@ -357,13 +381,10 @@ __global__ void __launch_bounds__(kBackThreads)
   pdl_launch_dependents();
   auto issue = [&](uint32_t t, int s) {
     uint8_t* dst = smem + s * stage_bytes;
-    mbar_arrive_expect_tx(&full[s], p.d_res ? stage_bytes : stage_bytes - sbytes);
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
     bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy, cbytes, &full[s]);
     bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb, cbytes, &full[s]);
     bulk_load(dst + 2 * cbytes, static_cast<const S*>(p.res_out) + t * p.ldr, sbytes, &full[s]);
-    if (p.d_res)
-      bulk_load(dst + 2 * cbytes + sbytes, static_cast<const S*>(p.d_res) + t * p.ldd, sbytes,
-                &full[s]);
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && lo + s < hi; ++s) issue(lo + s, s);
@@ -386,33 +407,37 @@ __global__ void __launch_bounds__(kBackThreads)
   uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
   for (uint32_t t = lo; t < hi; ++t) {
     const C *dy, *block;
-    const S *res, *dres;
-    if (M != kSingle && stages > 0) {
+    const S* res;
+    Raw<S> a[NV] = {};
+    if (p.d_res) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd, c, v);
+    }
+    if (stages > 0) {
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
       const uint8_t* src = smem + stage * stage_bytes;
       dy = reinterpret_cast<const C*>(src);
       block = reinterpret_cast<const C*>(src + cbytes);
       res = reinterpret_cast<const S*>(src + 2 * cbytes);
-      dres = reinterpret_cast<const S*>(src + 2 * cbytes + sbytes);
     } else {
       dy = static_cast<const C*>(p.dy) + t * p.lddy;
       block = static_cast<const C*>(p.block) + t * p.ldb;
       res = static_cast<const S*>(p.res_out) + t * p.ldr;
-      dres = static_cast<const S*>(p.d_res) + (p.d_res ? t * p.ldd : 0);
     }
-    float2 d[NV][4];
     float2 ss = both(0.f), sd = both(0.f), sb = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const Raw<S> x = load8(res, c, v);
       const Raw<C> y = load8(dy, c, v);
+      float2 f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[v][i] = y.get(i);
-      times_w(d[v], p.w_pre, p.w_fp32, 0, c, v);
+      for (int i = 0; i < 4; ++i) f[i] = y.get(i);
+      times_w(f, p.w_pre, p.w_fp32, 0, c, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ss = fma2(x.get(i), x.get(i), ss);
-        sd = fma2(d[v][i], x.get(i), sd);
+        sd = fma2(f[i], x.get(i), sd);
       }
       if (p.w_post) {
         const Raw<C> b = load8(block, c, v);
@@ -425,27 +450,28 @@ __global__ void __launch_bounds__(kBackThreads)
     // past this barrier nobody reads the previous row's stage any more
     if (stages > 0 && threadIdx.x == 0 && t > lo && t - 1 + stages < hi)
       issue(t - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
-    const float rho1 = rms_inverse(sum[0], cols, p.eps);
-    const float sigma1 = p.w_post ? rms_inverse(sum[2], cols, p.eps) : 1.f;
+    const float rho1 = rms_inverse(sum[0], inv_cols, p.eps);
+    const float sigma1 = p.w_post ? rms_inverse(sum[2], inv_cols, p.eps) : 1.f;
     // (in this order nothing leaves FP32's range before the product does)
     const float2 rho = both(rho1), sigma = both(sigma1);
-    const float2 k = both(-(rho1 * (rho1 * (rho1 * (sum[1] / cols)))));
+    const float2 k = both(-(rho1 * (rho1 * (rho1 * (sum[1] * inv_cols)))));
     const int64_t goff = group * p.cols;
+    float2 d[NV][4];
     float2 dot2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const Raw<S> x = load8(res, c, v);
       const Raw<C> y = load8(dy, c, v);
 #pragma unroll
+      for (int i = 0; i < 4; ++i) d[v][i] = y.get(i);
+      times_w(d[v], p.w_pre, p.w_fp32, 0, c, v);
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
         pre[v][i] = fma2(y.get(i), mul2(x.get(i), rho), pre[v][i]);
         d[v][i] = fma2(x.get(i), k, mul2(rho, d[v][i]));
       }
-      if (p.d_res) {
-        const Raw<S> a = load8(dres, c, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[v][i] = add2(d[v][i], a.get(i));
-      }
+      for (int i = 0; i < 4; ++i) d[v][i] = add2(d[v][i], a[v].get(i));
       float2 f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = mul2(alpha, d[v][i]);
@@ -463,7 +489,7 @@ __global__ void __launch_bounds__(kBackThreads)
     if (p.w_post) {
       float dot[1] = {dot2.x + dot2.y};
       block_sum(dot, part[1]);
-      const float2 m = both(-(sigma1 * (sigma1 * (sigma1 * (dot[0] / cols)))));
+      const float2 m = both(-(sigma1 * (sigma1 * (sigma1 * (dot[0] * inv_cols)))));
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const Raw<C> b = load8(block, c, v);
@@ -526,6 +552,107 @@ __global__ void __launch_bounds__(kBackThreads)
         pre_out[at] = h ? pre[v][i].y : pre[v][i].x;
         if (p.w_post) post_out[at] = many ? post_sum[at] : h ? q[v][i].y : q[v][i].x;
       }
+}
+
+// The gradient for rows that are not on 16-byte boundaries: element by element,
+// with the column sums of w_pre and D b sigma and the row's u in shared memory
+// (cols floats each).  Sums over finished gates (gates > 1) grow in the
+// workspace.  A thread goes through the same columns everywhere, so no two
+// threads touch the same sum.
+template <typename C, typename S>
+__global__ void __launch_bounds__(kBackThreads)
+    norm_backward_single_kernel(const NormBackParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float part[2][3 * kMaxWarps];
+  const int cols = static_cast<int>(p.cols), tid = static_cast<int>(threadIdx.x);
+  const int step = static_cast<int>(blockDim.x);
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
+  const uint32_t n = gridDim.x, me = blockIdx.x;
+  const RowShare share(static_cast<uint32_t>(p.rows), n);
+  const uint32_t lo = share.start(me), hi = share.start(me + 1);
+  const bool many = p.gates > 1;
+  float* pre = reinterpret_cast<float*>(smem);
+  float* q = pre + cols;
+  float* u_row = q + cols;
+  float* post_out = ws_post(p, n, me);
+  for (int i = tid; i < 6 * kMaxWarps; i += step) part[0][i] = 0.f;
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int c = tid; c < cols; c += step) {
+    pre[c] = q[c] = 0.f;
+    if (many) post_out[c] = 0.f;
+  }
+  auto weight = [&](const void* w, int64_t i) {
+    return p.w_fp32 ? static_cast<const float*>(w)[i] : to_float(static_cast<const bf16*>(w)[i]);
+  };
+  const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
+  const uint32_t group0 = lo / per;
+  uint32_t group = group0, left = (group + 1) * per - lo;
+  for (uint32_t t = lo; t < hi; ++t) {
+    const C* dy = static_cast<const C*>(p.dy) + t * p.lddy;
+    const C* block = static_cast<const C*>(p.block) + t * p.ldb;
+    const S* res = static_cast<const S*>(p.res_out) + t * p.ldr;
+    const S* dres = p.d_res ? static_cast<const S*>(p.d_res) + t * p.ldd : nullptr;
+    const int64_t goff = group * p.cols;
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = tid; c < cols; c += step) {
+      const float x = to_float(res[c]), b = to_float(block[c]);
+      sum[0] += x * x;
+      sum[1] += to_float(dy[c]) * weight(p.w_pre, c) * x;
+      sum[2] += b * b;
+    }
+    block_sum(sum, part[0]);
+    const float rho = rms_inverse(sum[0], inv_cols, p.eps);
+    const float sigma = p.w_post ? rms_inverse(sum[2], inv_cols, p.eps) : 1.f;
+    const float k = rho * (rho * (rho * (sum[1] * inv_cols)));
+    float dot[1] = {0.f};
+#pragma unroll 2
+    for (int c = tid; c < cols; c += step) {
+      const float x = to_float(res[c]), y = to_float(dy[c]), b = to_float(block[c]);
+      const float d = (dres ? to_float(dres[c]) : 0.f) + (rho * (y * weight(p.w_pre, c)) - x * k);
+      store1(static_cast<S*>(p.d_residual) + t * p.lddr + c, p.alpha * d);
+      pre[c] += y * (x * rho);
+      q[c] += d * (b * sigma);
+      float u = d;
+      if (p.gate) u *= weight(p.gate, goff + c);
+      if (p.w_post) u *= weight(p.w_post, c);
+      dot[0] += u * b;
+      u_row[c] = u;
+    }
+    float m = 0.f;
+    if (p.w_post) {
+      block_sum(dot, part[1]);
+      m = sigma * (sigma * (sigma * (dot[0] * inv_cols)));
+    }
+#pragma unroll 2
+    for (int c = tid; c < cols; c += step) {
+      const float u = u_row[c];
+      store1(static_cast<C*>(p.d_block) + t * p.lddb + c,
+             p.w_post ? sigma * u - to_float(block[c]) * m : u);
+    }
+    if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[0] is used in every row
+    if (--left == 0 || t + 1 == hi) {
+      if (p.gate) {
+        const bool whole = group * per >= lo && t + 1 == (group + 1) * per;
+        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
+        for (int c = tid; c < cols; c += step) {
+          const float g = q[c] * weight(p.gate, goff + c);
+          dst[c] = p.w_post ? q[c] * weight(p.w_post, c) : q[c];
+          if (many) post_out[c] += g;
+          q[c] = many ? 0.f : g;
+        }
+      }
+      ++group;
+      left = per;
+    }
+  }
+  float* pre_out = ws_pre(p, me);
+  for (int c = tid; c < cols; c += step) {
+    pre_out[c] = pre[c];
+    if (p.w_post && !many) post_out[c] = q[c];
+  }
 }
 
 constexpr int kSumCols = 32, kSumParts = 32;
@@ -616,82 +743,164 @@ int row_threads(int64_t cols, int nv) {
 }
 bool whole(int64_t cols, int nv) { return cols == 8 * static_cast<int64_t>(nv) * row_threads(cols, nv); }
 
-template <typename C, typename S, Mode M, int NV>
+// Blocks of a kernel that an SM holds at once, asked of the runtime once per
+// device and number of threads.
+class Fit {
+ public:
+  template <typename K>
+  int of(K kern, int threads) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 1;
+    std::atomic<int>& known = fit_[dev][threads / 32];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)
+        n = 1;
+      known.store(n, std::memory_order_relaxed);
+    }
+    return n;
+  }
+
+ private:
+  static constexpr int kDevs = 64;
+  std::atomic<int> fit_[kDevs][33] = {};
+};
+
+template <typename C, typename S, Mode M, int NV, int MAXT>
 cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) {
+  static Fit fit;
   const int threads = row_threads(p.cols, NV);
-  // blocks that an SM holds at once, from the register budget of each form
-  const int64_t fit = threads <= 512 ? 1536 / threads : 1;
-  const int64_t all = num_sms * (fit < 16 ? fit : 16);
-  const dim3 grid(static_cast<unsigned>(p.rows < all ? p.rows : all));
-  if (threads <= 512)
-    return launch(norm_residual_kernel<C, S, M, NV, 512>, grid, threads, 0, stream, p);
-  return launch(norm_residual_kernel<C, S, M, NV, 1024>, grid, threads, 0, stream, p);
+  auto kern = norm_residual_kernel<C, S, M, NV, MAXT>;
+  int64_t grid = p.rows;
+  if (grid > num_sms) {
+    const int64_t most = static_cast<int64_t>(num_sms) * fit.of(kern, threads);
+    grid = grid < most ? grid : most;
+  }
+  return launch(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p);
+}
+
+template <typename C, typename S, int NV, int MAXT>
+cudaError_t forward_mode(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
+  if (!vec) return forward_impl<C, S, kSingle, NV, MAXT>(p, num_sms, stream);
+  if (whole(p.cols, NV)) return forward_impl<C, S, kWhole, NV, MAXT>(p, num_sms, stream);
+  return forward_impl<C, S, kRuns, NV, MAXT>(p, num_sms, stream);
 }
 
 template <typename C, typename S>
 cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  // few rows: as many threads as a row takes; else two runs a thread
-  const bool one = p.cols <= 512 || (p.cols <= 8192 && p.rows <= num_sms);
-  if (!vec)
-    return one ? forward_impl<C, S, kSingle, 1>(p, num_sms, stream)
-               : forward_impl<C, S, kSingle, 2>(p, num_sms, stream);
-  if (one)
-    return whole(p.cols, 1) ? forward_impl<C, S, kWhole, 1>(p, num_sms, stream)
-                            : forward_impl<C, S, kRuns, 1>(p, num_sms, stream);
-  return whole(p.cols, 2) ? forward_impl<C, S, kWhole, 2>(p, num_sms, stream)
-                          : forward_impl<C, S, kRuns, 2>(p, num_sms, stream);
+  // few rows: as many threads as a row takes; else rows of few threads, so
+  // that several are under way on an SM
+  if (p.cols <= 1024 || (p.cols <= 8192 && p.rows <= num_sms))
+    return forward_mode<C, S, 1, 1024>(p, vec, num_sms, stream);
+  if (p.cols <= 4096) return forward_mode<C, S, 2, 256>(p, vec, num_sms, stream);
+  return forward_mode<C, S, 4, 512>(p, vec, num_sms, stream);
 }
 
-// Runs of eight a thread holds in the gradient.
-int backward_runs(int64_t cols) { return cols <= 8192 ? 2 : 4; }
+// Runs of eight columns that a thread holds in the gradient: many, so that
+// rows take few threads and several rows are under way on an SM, but with an
+// FP32 stream two, as more do not fit the registers.
+int backward_runs(int64_t cols, bool s_fp32) {
+  return cols <= 512 ? 1 : cols <= 2048 || (s_fp32 && cols <= 8192) ? 2 : 4;
+}
 
-// Blocks of the gradient side by side on an SM (128 registers a thread).
-int backward_fit(int64_t cols) {
-  const int fit = kBackThreads / row_threads(cols, backward_runs(cols));
-  return fit < 1 ? 1 : fit > 8 ? 8 : fit;
+constexpr int kMaxSms = 192;         // workspaces are sized for this many
+constexpr size_t kRingBytes = 190 * 1024;
+constexpr size_t kSumsBytes = 200 * 1024;
+
+// How a gradient is run: threads of a block, blocks side by side on an SM,
+// rows of the ring, bytes of shared memory of a block.
+struct BackPlan {
+  int threads, fit, stages;
+  size_t smem;
+};
+BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec, bool many) {
+  BackPlan p;
+  if (!vec) {  // by shared memory and 2048 threads
+    p.threads = cols <= 2048 ? static_cast<int>((cols + 127) / 128 * 32) : kBackThreads;
+    p.smem = static_cast<size_t>(cols) * 12;
+    p.fit = static_cast<int>(kSumsBytes / p.smem);
+    const int by_threads = 2 * kBackThreads / p.threads;
+    p.fit = p.fit < by_threads ? p.fit : by_threads;
+    p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
+    p.stages = 0;
+    return p;
+  }
+  // by registers (128 a thread) and rings of two rows at least
+  p.threads = row_threads(cols, backward_runs(cols, s_fp32));
+  p.fit = kBackThreads / p.threads;
+  p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
+  const size_t stage = cols * ((c_fp32 ? 8 : 4) + (s_fp32 ? 4 : 2));
+  const size_t post = many ? cols * 4 : 0;
+  while (p.fit > 1 && p.fit * (2 * stage + post) > kRingBytes) --p.fit;
+  const size_t rows = (kRingBytes / p.fit - post) / stage;
+  p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
+  p.smem = p.stages * stage + post;
+  return p;
 }
 
 // Blocks of the gradient: those that fit the SMs, with four rows each at
 // least (a block's column sums are written and read once more).
-int64_t backward_blocks(int64_t rows, int64_t cols, int num_sms) {
-  const int64_t most = static_cast<int64_t>(num_sms) * backward_fit(cols), want = (rows + 3) / 4;
+int64_t backward_blocks(int64_t rows, int num_sms, int fit) {
+  const int64_t most = static_cast<int64_t>(num_sms) * fit, want = (rows + 3) / 4;
   return want < num_sms ? (rows < num_sms ? rows : num_sms) : want < most ? want : most;
 }
 
-constexpr int kMaxSms = 192;         // workspaces are sized for this many
-constexpr size_t kRingBytes = 216 * 1024;
+template <typename K>
+cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
+  return setup.run([&]() -> cudaError_t {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSumsBytes));
+  });
+}
 
 template <typename C, typename S, Mode M, int NV>
-cudaError_t backward_impl(const NormBackParams& p, int64_t n, cudaStream_t stream) {
-  auto kern = norm_backward_kernel<C, S, M, NV>;
+cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t n,
+                          cudaStream_t stream) {
   static PerDeviceOnce setup;
-  const cudaError_t err = setup.run([&]() -> cudaError_t {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kRingBytes));
-  });
+  auto kern = norm_backward_kernel<C, S, M, NV>;
+  const cudaError_t err = allow_smem(setup, kern);
   if (err != cudaSuccess) return err;
-  const size_t stage = p.cols * 2 * (sizeof(C) + sizeof(S));
-  const size_t post = p.gates > 1 ? p.cols * 4 : 0;
-  size_t stages = M != kSingle ? (kRingBytes / backward_fit(p.cols) - post) / stage : 0;
-  stages = stages < 2 ? 0 : stages > 4 ? 4 : stages;
-  return launch(kern, dim3(static_cast<unsigned>(n)), row_threads(p.cols, NV), stages * stage + post,
-                stream, p, static_cast<int>(stages));
+  return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p,
+                plan.stages);
 }
 
 template <typename C, typename S>
-cudaError_t backward(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
-  if (backward_runs(p.cols) == 4)
-    return !vec ? backward_impl<C, S, kSingle, 4>(p, n, stream)
-                : backward_impl<C, S, kRuns, 4>(p, n, stream);
-  if (!vec) return backward_impl<C, S, kSingle, 2>(p, n, stream);
-  return whole(p.cols, 2) ? backward_impl<C, S, kWhole, 2>(p, n, stream)
-                          : backward_impl<C, S, kRuns, 2>(p, n, stream);
+cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64_t n,
+                            cudaStream_t stream) {
+  static PerDeviceOnce setup;
+  auto kern = norm_backward_single_kernel<C, S>;
+  const cudaError_t err = allow_smem(setup, kern);
+  if (err != cudaSuccess) return err;
+  return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p);
+}
+
+template <typename C, typename S, int NV>
+cudaError_t backward_runs_of(const NormBackParams& p, const BackPlan& plan, int64_t n,
+                             cudaStream_t stream) {
+  return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV>(p, plan, n, stream)
+                           : backward_impl<C, S, kRuns, NV>(p, plan, n, stream);
+}
+
+template <typename C, typename S>
+cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
+                     cudaStream_t stream) {
+  if (!vec) return backward_single<C, S>(p, plan, n, stream);
+  switch (backward_runs(p.cols, sizeof(S) == 4)) {
+    case 1: return backward_runs_of<C, S, 1>(p, plan, n, stream);
+    case 2: return backward_runs_of<C, S, 2>(p, plan, n, stream);
+    default: return backward_runs_of<C, S, 4>(p, plan, n, stream);
+  }
 }
 
 }  // namespace
 
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
-  return static_cast<size_t>(backward_blocks(rows, cols, kMaxSms)) * (gates > 0 ? 4 : 2) *
+  int fit = 1;  // the most that any types and alignment have
+  for (int i = 0; i < 8; ++i) {
+    const int f = backward_plan(cols, i & 1, i & 2, i & 4, false).fit;
+    fit = f > fit ? f : fit;
+  }
+  return static_cast<size_t>(backward_blocks(rows, kMaxSms, fit)) * (gates > 0 ? 4 : 2) *
          static_cast<size_t>(cols) * 4;
 }
 
@@ -724,15 +933,15 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
                    aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
                    aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&
                    p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 && p.lddr % se == 0;
-  const int64_t n =
-      backward_blocks(p.rows, p.cols, num_sms < kMaxSms ? num_sms : kMaxSms);
+  const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec, p.gates > 1);
+  const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan.fit);
   cudaError_t err;
   if (p.c_fp32)
-    err = backward<float, float>(p, vec, n, stream);
+    err = backward<float, float>(p, vec, plan, n, stream);
   else if (p.s_fp32)
-    err = backward<bf16, float>(p, vec, n, stream);
+    err = backward<bf16, float>(p, vec, plan, n, stream);
   else
-    err = backward<bf16, bf16>(p, vec, n, stream);
+    err = backward<bf16, bf16>(p, vec, plan, n, stream);
   if (err != cudaSuccess) return err;
   const int64_t jobs = 2 + (p.gates < n ? p.gates : n);
   return launch(norm_backward_sum_kernel,

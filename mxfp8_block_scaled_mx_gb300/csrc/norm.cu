@@ -343,34 +343,53 @@ __device__ __forceinline__ float* ws_gate(const NormBackParams& p, int64_t n, in
   return p.workspace + (2 * n + slot) * p.cols;
 }
 
-constexpr int kBackThreads = 512;   // at most, with 128 registers each
+constexpr int kBackThreads = 512;   // at most
 
-// One block of threads goes through its own rows in order.  Rows arrive in
-// shared memory by bulk copies, `stages` rows ahead (stages 0: rows whose
-// addresses or sizes do not allow those, read in place), and are read from
-// there as often as needed; d_res, which is needed once, goes to registers at
-// the start of its row.  A thread's registers hold that, its column sums
-// (w_pre and D b sigma, 8 NV each) and D, and little else.
+// The sums behind a row's gradient.  With t = w_pre dy and h = w_post g block,
+//   D = d_res + rho t - rho^3 mean(t r) r,   dot = sum of h D
+//     = sum h d_res + rho sum h t - rho^3 mean(t r) sum h r,
+// so that one pass over the row gives all of them, before rho is known.
+enum RowSum { kRR, kTR, kBB, kHA, kHT, kHR, kRowSums };
+
+// Eight sums over a warp in nine exchanges: lane l gets that of v[l / 4].
+__device__ __forceinline__ float warp_sum8(float (&v)[8]) {
+  const uint32_t lane = lane_id();
+#pragma unroll
+  for (int o = 16, n = 4; n > 0; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// One block of threads goes through its own rows in order, and in each step
+// forms the sums of one row and the gradients of the row before, which do not
+// depend on one another: one barrier a row.  Rows arrive in shared memory by
+// bulk copies, `stages` of them at most (0: rows that do not fit, read in
+// place).  A thread keeps the sums of its columns over the rows.
 template <typename C, typename S, Mode M, int NV>
 __global__ void __launch_bounds__(kBackThreads)
     norm_backward_kernel(const NormBackParams p, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float part[2][3 * kMaxWarps];
+  __shared__ float part[2][kMaxWarps / 2 * 8];
   __shared__ uint64_t full[8];
   __shared__ uint32_t abort_word;
   volatile uint32_t* s_abort = &abort_word;
   const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
                   static_cast<int32_t>(blockDim.x)};
   const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const uint32_t n = gridDim.x, me = blockIdx.x;
+  const uint32_t n = gridDim.x, me = blockIdx.x, lane = lane_id();
   const RowShare share(static_cast<uint32_t>(p.rows), n);
   const uint32_t lo = share.start(me), hi = share.start(me + 1);
   const uint32_t cbytes = static_cast<uint32_t>(p.cols * sizeof(C));
   const uint32_t sbytes = static_cast<uint32_t>(p.cols * sizeof(S));
-  const uint32_t stage_bytes = 2 * cbytes + sbytes;
-  // sums of D b sigma g over finished gates (gates > 1), behind the ring
-  float* post_sum = reinterpret_cast<float*>(smem + stages * stage_bytes);
-  for (uint32_t i = threadIdx.x; i < 6 * kMaxWarps; i += blockDim.x) part[0][i] = 0.f;
+  const uint32_t stage_bytes = 2 * cbytes + 2 * sbytes;
+  for (uint32_t i = threadIdx.x; i < kMaxWarps * 8; i += blockDim.x) part[0][i] = 0.f;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     abort_word = 0;
@@ -381,135 +400,164 @@ __global__ void __launch_bounds__(kBackThreads)
   pdl_launch_dependents();
   auto issue = [&](uint32_t t, int s) {
     uint8_t* dst = smem + s * stage_bytes;
-    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    mbar_arrive_expect_tx(&full[s], p.d_res ? stage_bytes : stage_bytes - sbytes);
     bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy, cbytes, &full[s]);
     bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb, cbytes, &full[s]);
     bulk_load(dst + 2 * cbytes, static_cast<const S*>(p.res_out) + t * p.ldr, sbytes, &full[s]);
+    if (p.d_res)
+      bulk_load(dst + 2 * cbytes + sbytes, static_cast<const S*>(p.d_res) + t * p.ldd, sbytes,
+                &full[s]);
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && lo + s < hi; ++s) issue(lo + s, s);
 
-  const bool many = p.gates > 1;
+  struct Row {
+    const C *dy, *block;
+    const S *res, *dres;
+  };
+  auto row_at = [&](uint32_t t, int stage) {
+    Row r;
+    if (stages > 0) {
+      const uint8_t* src = smem + stage * stage_bytes;
+      r.dy = reinterpret_cast<const C*>(src);
+      r.block = reinterpret_cast<const C*>(src + cbytes);
+      r.res = reinterpret_cast<const S*>(src + 2 * cbytes);
+      r.dres = reinterpret_cast<const S*>(src + 2 * cbytes + sbytes);
+    } else {
+      r.dy = static_cast<const C*>(p.dy) + t * p.lddy;
+      r.block = static_cast<const C*>(p.block) + t * p.ldb;
+      r.res = static_cast<const S*>(p.res_out) + t * p.ldr;
+      r.dres = static_cast<const S*>(p.d_res) + (p.d_res ? t * p.ldd : 0);
+    }
+    return r;
+  };
+
   const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
   const float2 alpha = both(p.alpha);
-  float2 pre[NV][4], q[NV][4];
+  // sums over rows of dy r rho, of D b sigma, and of the latter times g over
+  // finished gates
+  float2 pre[NV][4], q[NV][4], post[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = both(0.f);
-  if (many)
-    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.cols); i += blockDim.x)
-      post_sum[i] = 0.f;
-  __syncthreads();
-  int stage = 0;
-  uint32_t phase = 0;
+    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = post[v][i] = both(0.f);
   const uint32_t group0 = lo / per;
-  uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
-  for (uint32_t t = lo; t < hi; ++t) {
-    const C *dy, *block;
-    const S* res;
-    Raw<S> a[NV] = {};
-    if (p.d_res) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd, c, v);
-    }
-    if (stages > 0) {
+  uint32_t group = group0, left = (group + 1) * per - lo;  // of the gate of row t - 1; rows left
+  uint32_t next_group = group0, next_left = left;          // of row t
+  int stage = 0, last_stage = 0;                           // of rows t and t - 1
+  uint32_t phase = 0;
+  for (uint32_t t = lo; t <= hi; ++t) {
+    const bool stats = t < hi, apply = t > lo;
+    if (stats && stages > 0)
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
-      const uint8_t* src = smem + stage * stage_bytes;
-      dy = reinterpret_cast<const C*>(src);
-      block = reinterpret_cast<const C*>(src + cbytes);
-      res = reinterpret_cast<const S*>(src + 2 * cbytes);
-    } else {
-      dy = static_cast<const C*>(p.dy) + t * p.lddy;
-      block = static_cast<const C*>(p.block) + t * p.ldb;
-      res = static_cast<const S*>(p.res_out) + t * p.ldr;
+    // row t - 1's sums, from the step before
+    float sums[kRowSums];
+    {
+      float s = 0.f;
+#pragma unroll
+      for (uint32_t w = 0; w < kMaxWarps / 2; w += 4)
+        if (w < blockDim.x / 32) s += part[(t & 1) ^ 1][(w + lane / 8) * 8 + lane % 8];
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+      for (int i = 0; i < kRowSums; ++i) sums[i] = __shfl_sync(0xffffffffu, s, i);
     }
-    float2 ss = both(0.f), sd = both(0.f), sb = both(0.f);
+    if (stats) {
+      const Row r = row_at(t, stage);
+      const int64_t goff = next_group * p.cols;
+      float2 s2[kRowSums];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const Raw<S> x = load8(res, c, v);
-      const Raw<C> y = load8(dy, c, v);
-      float2 f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = y.get(i);
-      times_w(f, p.w_pre, p.w_fp32, 0, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ss = fma2(x.get(i), x.get(i), ss);
-        sd = fma2(f[i], x.get(i), sd);
-      }
-      if (p.w_post) {
-        const Raw<C> b = load8(block, c, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sb = fma2(b.get(i), b.get(i), sb);
-      }
-    }
-    float sum[3] = {ss.x + ss.y, sd.x + sd.y, sb.x + sb.y};
-    block_sum(sum, part[0]);
-    // past this barrier nobody reads the previous row's stage any more
-    if (stages > 0 && threadIdx.x == 0 && t > lo && t - 1 + stages < hi)
-      issue(t - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
-    const float rho1 = rms_inverse(sum[0], inv_cols, p.eps);
-    const float sigma1 = p.w_post ? rms_inverse(sum[2], inv_cols, p.eps) : 1.f;
-    // (in this order nothing leaves FP32's range before the product does)
-    const float2 rho = both(rho1), sigma = both(sigma1);
-    const float2 k = both(-(rho1 * (rho1 * (rho1 * (sum[1] * inv_cols)))));
-    const int64_t goff = group * p.cols;
-    float2 d[NV][4];
-    float2 dot2 = both(0.f);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const Raw<S> x = load8(res, c, v);
-      const Raw<C> y = load8(dy, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[v][i] = y.get(i);
-      times_w(d[v], p.w_pre, p.w_fp32, 0, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pre[v][i] = fma2(y.get(i), mul2(x.get(i), rho), pre[v][i]);
-        d[v][i] = fma2(x.get(i), k, mul2(rho, d[v][i]));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[v][i] = add2(d[v][i], a[v].get(i));
-      float2 f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(alpha, d[v][i]);
-      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, round8<S>(f));
-      const Raw<C> b = load8(block, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[v][i] = fma2(d[v][i], mul2(b.get(i), sigma), q[v][i]);
-      if (p.gate) times_w(d[v], p.gate, p.w_fp32, goff, c, v);
-      if (p.w_post) {
-        times_w(d[v], p.w_post, p.w_fp32, 0, c, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dot2 = fma2(d[v][i], b.get(i), dot2);
-      }
-    }
-    if (p.w_post) {
-      float dot[1] = {dot2.x + dot2.y};
-      block_sum(dot, part[1]);
-      const float2 m = both(-(sigma1 * (sigma1 * (sigma1 * (dot[0] * inv_cols)))));
+      for (int i = 0; i < kRowSums; ++i) s2[i] = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const Raw<C> b = load8(block, c, v);
+        const Raw<S> x = load8(r.res, c, v);
+        const Raw<C> y = load8(r.dy, c, v);
+        float2 f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[v][i] = fma2(b.get(i), m, mul2(sigma, d[v][i]));
+        for (int i = 0; i < 4; ++i) f[i] = y.get(i);
+        times_w(f, p.w_pre, p.w_fp32, 0, c, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s2[kRR] = fma2(x.get(i), x.get(i), s2[kRR]);
+          s2[kTR] = fma2(f[i], x.get(i), s2[kTR]);
+        }
+        if (p.w_post) {
+          const Raw<C> b = load8(r.block, c, v);
+          float2 h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[i] = b.get(i);
+            s2[kBB] = fma2(h[i], h[i], s2[kBB]);
+          }
+          times_w(h, p.w_post, p.w_fp32, 0, c, v);
+          if (p.gate) times_w(h, p.gate, p.w_fp32, goff, c, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s2[kHT] = fma2(h[i], f[i], s2[kHT]);
+            s2[kHR] = fma2(h[i], x.get(i), s2[kHR]);
+          }
+          if (p.d_res) {
+            const Raw<S> a = load8(r.dres, c, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s2[kHA] = fma2(h[i], a.get(i), s2[kHA]);
+          }
+        }
       }
-    } else if (blockDim.x > 32) {
-      __syncthreads();  // part[0] is used in every row
-    }
+      float s8[8];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, round8<C>(d[v]));
-    if (blockDim.x == 32) __syncwarp();  // as the barriers above: this row's reads are done
-    if (stages > 0 && ++stage == stages) {
-      stage = 0;
-      phase ^= 1u;
+      for (int i = 0; i < 8; ++i) s8[i] = i < kRowSums ? s2[i < kRowSums ? i : 0].x + s2[i < kRowSums ? i : 0].y : 0.f;
+      const float s = warp_sum8(s8);
+      if ((lane & 3) == 0) part[t & 1][warp_id() * 8 + lane / 4] = s;
     }
-    if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
-      if (p.gate) {
-        const bool whole = group * per >= lo && t + 1 == (group + 1) * per;
+    if (apply) {
+      const uint32_t u = t - 1;
+      const Row r = row_at(u, last_stage);
+      const int64_t goff = group * p.cols;
+      const float rho1 = rms_inverse(sums[kRR], inv_cols, p.eps);
+      // (in this order nothing leaves FP32's range before the product does)
+      const float k1 = rho1 * (rho1 * (rho1 * (sums[kTR] * inv_cols)));
+      float sigma1 = 1.f, m1 = 0.f;
+      if (p.w_post) {
+        sigma1 = rms_inverse(sums[kBB], inv_cols, p.eps);
+        const float dot = (p.d_res ? sums[kHA] : 0.f) + (rho1 * sums[kHT] - k1 * sums[kHR]);
+        m1 = sigma1 * (sigma1 * (sigma1 * (dot * inv_cols)));
+      }
+      const float2 rho = both(rho1), sigma = both(sigma1), k = both(-k1), m = both(-m1);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const Raw<S> x = load8(r.res, c, v);
+        const Raw<C> y = load8(r.dy, c, v);
+        const Raw<C> b = load8(r.block, c, v);
+        float2 d[4], f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = y.get(i);
+        times_w(d, p.w_pre, p.w_fp32, 0, c, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pre[v][i] = fma2(y.get(i), mul2(x.get(i), rho), pre[v][i]);
+          d[i] = fma2(x.get(i), k, mul2(rho, d[i]));
+        }
+        if (p.d_res) {
+          const Raw<S> a = load8(r.dres, c, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = add2(d[i], a.get(i));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[i] = mul2(alpha, d[i]);
+          q[v][i] = fma2(d[i], mul2(b.get(i), sigma), q[v][i]);
+        }
+        store8(static_cast<S*>(p.d_residual) + u * p.lddr, c, v, round8<S>(f));
+        if (p.gate) times_w(d, p.gate, p.w_fp32, goff, c, v);
+        if (p.w_post) {
+          times_w(d, p.w_post, p.w_fp32, 0, c, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = fma2(b.get(i), m, mul2(sigma, d[i]));
+        }
+        store8(static_cast<C*>(p.d_block) + u * p.lddb, c, v, round8<C>(d));
+      }
+      if (p.gate && (left == 1 || t == hi)) {  // the gate's rows, or this block's, end here
+        const bool whole = group * per >= lo && left == 1;
         float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -518,20 +566,32 @@ __global__ void __launch_bounds__(kBackThreads)
           for (int i = 0; i < 4; ++i) dg[i] = q[v][i];
           if (p.w_post) times_w(dg, p.w_post, p.w_fp32, 0, c, v);
           times_w(q[v], p.gate, p.w_fp32, goff, c, v);
+          Raw<float> out;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (c.has(v, 2 * i)) dst[c.at(v, 2 * i)] = dg[i].x;
-            if (c.has(v, 2 * i + 1)) dst[c.at(v, 2 * i + 1)] = dg[i].y;
-            if (many) {
-              if (c.has(v, 2 * i)) post_sum[c.at(v, 2 * i)] += q[v][i].x;
-              if (c.has(v, 2 * i + 1)) post_sum[c.at(v, 2 * i + 1)] += q[v][i].y;
-              q[v][i] = both(0.f);
-            }
+            out.f[i] = dg[i];
+            post[v][i] = add2(post[v][i], q[v][i]);
+            q[v][i] = both(0.f);
           }
+          store8(dst, c, v, out);
         }
       }
-      ++group;
-      left = per;
+    }
+    // row t's sums are complete, and nobody reads row t - 1 any more
+    __syncthreads();
+    if (stages > 0) {
+      if (apply && threadIdx.x == 0 && t - 1 + stages < hi) issue(t - 1 + stages, last_stage);
+      last_stage = stage;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    group = next_group;
+    left = next_left;
+    if (--next_left == 0) {
+      ++next_group;
+      next_left = per;
     }
   }
   if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
@@ -539,19 +599,18 @@ __global__ void __launch_bounds__(kBackThreads)
       mbar_wait(&full[s], (hi - lo - 1 - s) / stages & 1u, s_abort, p.status, p.wait_limit_ns,
                 true);
   }
-  float* pre_out = ws_pre(p, me);
-  float* post_out = ws_post(p, n, me);
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    Raw<float> out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) out.f[i] = pre[v][i];
+    store8(ws_pre(p, me), c, v, out);
+    if (p.w_post) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!c.has(v, 2 * i + h)) continue;
-        const int at = c.at(v, 2 * i + h);
-        pre_out[at] = h ? pre[v][i].y : pre[v][i].x;
-        if (p.w_post) post_out[at] = many ? post_sum[at] : h ? q[v][i].y : q[v][i].x;
-      }
+      for (int i = 0; i < 4; ++i) out.f[i] = p.gate ? post[v][i] : q[v][i];
+      store8(ws_post(p, n, me), c, v, out);
+    }
+  }
 }
 
 // The gradient for rows that are not on 16-byte boundaries: element by element,
@@ -796,16 +855,12 @@ cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t str
   return forward_mode<C, S, 4, 512>(p, vec, num_sms, stream);
 }
 
-// Runs of eight columns that a thread holds in the gradient: many, so that
-// rows take few threads and several rows are under way on an SM, but with an
-// FP32 stream two, as more do not fit the registers.
-int backward_runs(int64_t cols, bool s_fp32) {
-  return cols <= 512 ? 1 : cols <= 2048 || (s_fp32 && cols <= 8192) ? 2 : 4;
-}
+// Runs of eight columns that a thread holds in the gradient: as few as 512
+// threads allow.
+int backward_runs(int64_t cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
-constexpr size_t kRingBytes = 190 * 1024;
-constexpr size_t kSumsBytes = 200 * 1024;
+constexpr size_t kSmemBytes = 200 * 1024;  // of an SM, for rings and sums; L1 keeps the weights
 
 // How a gradient is run: threads of a block, blocks side by side on an SM,
 // rows of the ring, bytes of shared memory of a block.
@@ -813,28 +868,29 @@ struct BackPlan {
   int threads, fit, stages;
   size_t smem;
 };
-BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec, bool many) {
+BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec) {
   BackPlan p;
   if (!vec) {  // by shared memory and 2048 threads
     p.threads = cols <= 2048 ? static_cast<int>((cols + 127) / 128 * 32) : kBackThreads;
     p.smem = static_cast<size_t>(cols) * 12;
-    p.fit = static_cast<int>(kSumsBytes / p.smem);
+    p.fit = static_cast<int>(kSmemBytes / p.smem);
     const int by_threads = 2 * kBackThreads / p.threads;
     p.fit = p.fit < by_threads ? p.fit : by_threads;
     p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
     p.stages = 0;
     return p;
   }
-  // by registers (128 a thread) and rings of two rows at least
-  p.threads = row_threads(cols, backward_runs(cols, s_fp32));
+  // by registers (128 a thread) and rings of three rows: one in each half of
+  // a step and one on its way
+  p.threads = row_threads(cols, backward_runs(cols));
+  const size_t stage = cols * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
   p.fit = kBackThreads / p.threads;
+  const int by_smem = static_cast<int>(kSmemBytes / (3 * stage));
+  p.fit = p.fit < by_smem ? p.fit : by_smem;
   p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-  const size_t stage = cols * ((c_fp32 ? 8 : 4) + (s_fp32 ? 4 : 2));
-  const size_t post = many ? cols * 4 : 0;
-  while (p.fit > 1 && p.fit * (2 * stage + post) > kRingBytes) --p.fit;
-  const size_t rows = (kRingBytes / p.fit - post) / stage;
+  const size_t rows = kSmemBytes / p.fit / stage;
   p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
-  p.smem = p.stages * stage + post;
+  p.smem = p.stages * stage;
   return p;
 }
 
@@ -849,7 +905,7 @@ template <typename K>
 cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
   return setup.run([&]() -> cudaError_t {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kSumsBytes));
+                                static_cast<int>(kSmemBytes));
   });
 }
 
@@ -885,7 +941,7 @@ template <typename C, typename S>
 cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
                      cudaStream_t stream) {
   if (!vec) return backward_single<C, S>(p, plan, n, stream);
-  switch (backward_runs(p.cols, sizeof(S) == 4)) {
+  switch (backward_runs(p.cols)) {
     case 1: return backward_runs_of<C, S, 1>(p, plan, n, stream);
     case 2: return backward_runs_of<C, S, 2>(p, plan, n, stream);
     default: return backward_runs_of<C, S, 4>(p, plan, n, stream);
@@ -897,7 +953,7 @@ cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, in
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
   int fit = 1;  // the most that any types and alignment have
   for (int i = 0; i < 8; ++i) {
-    const int f = backward_plan(cols, i & 1, i & 2, i & 4, false).fit;
+    const int f = backward_plan(cols, i & 1, i & 2, i & 4).fit;
     fit = f > fit ? f : fit;
   }
   return static_cast<size_t>(backward_blocks(rows, kMaxSms, fit)) * (gates > 0 ? 4 : 2) *
@@ -933,7 +989,7 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
                    aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
                    aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&
                    p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 && p.lddr % se == 0;
-  const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec, p.gates > 1);
+  const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec);
   const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan.fit);
   cudaError_t err;
   if (p.c_fp32)

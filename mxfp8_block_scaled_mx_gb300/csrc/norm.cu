@@ -367,12 +367,13 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// One block of threads goes through its own rows in order, and in each step
-// forms the sums of one row and the gradients of the row before, which do not
-// depend on one another: one barrier a row.  Rows arrive in shared memory by
-// bulk copies, `stages` of them at most (0: rows that do not fit, read in
-// place).  A thread keeps the sums of its columns over the rows.
-template <typename C, typename S, Mode M, int NV>
+// One block of threads goes through its own rows in order.  Rows arrive in
+// shared memory by bulk copies, `stages` of them at most (0: rows that do not
+// fit, read in place); a thread takes its columns to registers once, where
+// they stay across the row's one barrier, behind which the next copy starts.
+// A thread also keeps the sums of its columns over the rows.  MANY: more gates
+// than one.
+template <typename C, typename S, Mode M, int NV, bool MANY>
 __global__ void __launch_bounds__(kBackThreads)
     norm_backward_kernel(const NormBackParams p, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -411,153 +412,129 @@ __global__ void __launch_bounds__(kBackThreads)
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && lo + s < hi; ++s) issue(lo + s, s);
 
-  struct Row {
-    const C *dy, *block;
-    const S *res, *dres;
-  };
-  auto row_at = [&](uint32_t t, int stage) {
-    Row r;
-    if (stages > 0) {
-      const uint8_t* src = smem + stage * stage_bytes;
-      r.dy = reinterpret_cast<const C*>(src);
-      r.block = reinterpret_cast<const C*>(src + cbytes);
-      r.res = reinterpret_cast<const S*>(src + 2 * cbytes);
-      r.dres = reinterpret_cast<const S*>(src + 2 * cbytes + sbytes);
-    } else {
-      r.dy = static_cast<const C*>(p.dy) + t * p.lddy;
-      r.block = static_cast<const C*>(p.block) + t * p.ldb;
-      r.res = static_cast<const S*>(p.res_out) + t * p.ldr;
-      r.dres = static_cast<const S*>(p.d_res) + (p.d_res ? t * p.ldd : 0);
-    }
-    return r;
-  };
-
   const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
   const float2 alpha = both(p.alpha);
-  // sums over rows of dy r rho, of D b sigma, and of the latter times g over
-  // finished gates
-  float2 pre[NV][4], q[NV][4], post[NV][4];
+  // sums over rows of dy r rho and of D b sigma, with many gates also of the
+  // latter times g over finished gates
+  constexpr int kPost = MANY ? NV : 1;
+  float2 pre[NV][4], q[NV][4], post[kPost][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = post[v][i] = both(0.f);
+    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = post[MANY ? v : 0][i] = both(0.f);
   const uint32_t group0 = lo / per;
-  uint32_t group = group0, left = (group + 1) * per - lo;  // of the gate of row t - 1; rows left
-  uint32_t next_group = group0, next_left = left;          // of row t
-  int stage = 0, last_stage = 0;                           // of rows t and t - 1
+  uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
+  int stage = 0;
   uint32_t phase = 0;
-  for (uint32_t t = lo; t <= hi; ++t) {
-    const bool stats = t < hi, apply = t > lo;
-    if (stats && stages > 0)
+  for (uint32_t t = lo; t < hi; ++t) {
+    const int64_t goff = group * p.cols;
+    Raw<S> x[NV], a[NV] = {};
+    Raw<C> y[NV], b[NV];
+    if (stages > 0) {
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
-    // row t - 1's sums, from the step before
-    float sums[kRowSums];
-    {
-      float s = 0.f;
-#pragma unroll
-      for (uint32_t w = 0; w < kMaxWarps / 2; w += 4)
-        if (w < blockDim.x / 32) s += part[(t & 1) ^ 1][(w + lane / 8) * 8 + lane % 8];
-      s += __shfl_xor_sync(0xffffffffu, s, 8);
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-#pragma unroll
-      for (int i = 0; i < kRowSums; ++i) sums[i] = __shfl_sync(0xffffffffu, s, i);
-    }
-    if (stats) {
-      const Row r = row_at(t, stage);
-      const int64_t goff = next_group * p.cols;
-      float2 s2[kRowSums];
-#pragma unroll
-      for (int i = 0; i < kRowSums; ++i) s2[i] = both(0.f);
+      const uint8_t* src = smem + stage * stage_bytes;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const Raw<S> x = load8(r.res, c, v);
-        const Raw<C> y = load8(r.dy, c, v);
-        float2 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = y.get(i);
-        times_w(f, p.w_pre, p.w_fp32, 0, c, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s2[kRR] = fma2(x.get(i), x.get(i), s2[kRR]);
-          s2[kTR] = fma2(f[i], x.get(i), s2[kTR]);
-        }
-        if (p.w_post) {
-          const Raw<C> b = load8(r.block, c, v);
-          float2 h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[i] = b.get(i);
-            s2[kBB] = fma2(h[i], h[i], s2[kBB]);
-          }
-          times_w(h, p.w_post, p.w_fp32, 0, c, v);
-          if (p.gate) times_w(h, p.gate, p.w_fp32, goff, c, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s2[kHT] = fma2(h[i], f[i], s2[kHT]);
-            s2[kHR] = fma2(h[i], x.get(i), s2[kHR]);
-          }
-          if (p.d_res) {
-            const Raw<S> a = load8(r.dres, c, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s2[kHA] = fma2(h[i], a.get(i), s2[kHA]);
-          }
-        }
+        y[v] = load8(reinterpret_cast<const C*>(src), c, v);
+        b[v] = load8(reinterpret_cast<const C*>(src + cbytes), c, v);
+        x[v] = load8(reinterpret_cast<const S*>(src + 2 * cbytes), c, v);
+        if (p.d_res) a[v] = load8(reinterpret_cast<const S*>(src + 2 * cbytes + sbytes), c, v);
       }
-      float s8[8];
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s8[i] = i < kRowSums ? s2[i < kRowSums ? i : 0].x + s2[i < kRowSums ? i : 0].y : 0.f;
-      const float s = warp_sum8(s8);
-      if ((lane & 3) == 0) part[t & 1][warp_id() * 8 + lane / 4] = s;
+      for (int v = 0; v < NV; ++v) {
+        y[v] = load8<true>(static_cast<const C*>(p.dy) + t * p.lddy, c, v);
+        b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
+        x[v] = load8<true>(static_cast<const S*>(p.res_out) + t * p.ldr, c, v);
+        if (p.d_res) a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd, c, v);
+      }
     }
-    if (apply) {
-      const uint32_t u = t - 1;
-      const Row r = row_at(u, last_stage);
-      const int64_t goff = group * p.cols;
-      const float rho1 = rms_inverse(sums[kRR], inv_cols, p.eps);
-      // (in this order nothing leaves FP32's range before the product does)
-      const float k1 = rho1 * (rho1 * (rho1 * (sums[kTR] * inv_cols)));
-      float sigma1 = 1.f, m1 = 0.f;
+    float2 s2[kRowSums];
+#pragma unroll
+    for (int i = 0; i < kRowSums; ++i) s2[i] = both(0.f);
+    float2 f[NV][4];                                       // w_pre dy
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[v][i] = y[v].get(i);
+      times_w(f[v], p.w_pre, p.w_fp32, 0, c, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s2[kRR] = fma2(x[v].get(i), x[v].get(i), s2[kRR]);
+        s2[kTR] = fma2(f[v][i], x[v].get(i), s2[kTR]);
+      }
       if (p.w_post) {
-        sigma1 = rms_inverse(sums[kBB], inv_cols, p.eps);
-        const float dot = (p.d_res ? sums[kHA] : 0.f) + (rho1 * sums[kHT] - k1 * sums[kHR]);
-        m1 = sigma1 * (sigma1 * (sigma1 * (dot * inv_cols)));
-      }
-      const float2 rho = both(rho1), sigma = both(sigma1), k = both(-k1), m = both(-m1);
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const Raw<S> x = load8(r.res, c, v);
-        const Raw<C> y = load8(r.dy, c, v);
-        const Raw<C> b = load8(r.block, c, v);
-        float2 d[4], f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = y.get(i);
-        times_w(d, p.w_pre, p.w_fp32, 0, c, v);
+        float2 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          pre[v][i] = fma2(y.get(i), mul2(x.get(i), rho), pre[v][i]);
-          d[i] = fma2(x.get(i), k, mul2(rho, d[i]));
+          h[i] = b[v].get(i);
+          s2[kBB] = fma2(h[i], h[i], s2[kBB]);
         }
-        if (p.d_res) {
-          const Raw<S> a = load8(r.dres, c, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = add2(d[i], a.get(i));
-        }
+        times_w(h, p.w_post, p.w_fp32, 0, c, v);
+        if (p.gate) times_w(h, p.gate, p.w_fp32, goff, c, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          f[i] = mul2(alpha, d[i]);
-          q[v][i] = fma2(d[i], mul2(b.get(i), sigma), q[v][i]);
+          s2[kHA] = fma2(h[i], a[v].get(i), s2[kHA]);
+          s2[kHT] = fma2(h[i], f[v][i], s2[kHT]);
+          s2[kHR] = fma2(h[i], x[v].get(i), s2[kHR]);
         }
-        store8(static_cast<S*>(p.d_residual) + u * p.lddr, c, v, round8<S>(f));
-        if (p.gate) times_w(d, p.gate, p.w_fp32, goff, c, v);
-        if (p.w_post) {
-          times_w(d, p.w_post, p.w_fp32, 0, c, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = fma2(b.get(i), m, mul2(sigma, d[i]));
-        }
-        store8(static_cast<C*>(p.d_block) + u * p.lddb, c, v, round8<C>(d));
       }
-      if (p.gate && (left == 1 || t == hi)) {  // the gate's rows, or this block's, end here
-        const bool whole = group * per >= lo && left == 1;
+    }
+    float sums[8];
+#pragma unroll
+    for (int i = 0; i < kRowSums; ++i) sums[i] = s2[i].x + s2[i].y;
+    sums[6] = sums[7] = 0.f;
+    float s = warp_sum8(sums);
+    if ((lane & 3) == 0) part[t & 1][warp_id() * 8 + lane / 4] = s;
+    __syncthreads();
+    // past this barrier the row is in registers
+    if (stages > 0) {
+      if (threadIdx.x == 0 && t + stages < hi) issue(t + stages, stage);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    s = 0.f;
+#pragma unroll
+    for (uint32_t w = 0; w < kMaxWarps / 2; w += 4)
+      if (w < blockDim.x / 32) s += part[t & 1][(w + lane / 8) * 8 + lane % 8];
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+    for (int i = 0; i < kRowSums; ++i) sums[i] = __shfl_sync(0xffffffffu, s, i);
+    const float rho1 = rms_inverse(sums[kRR], inv_cols, p.eps);
+    // (in this order nothing leaves FP32's range before the product does)
+    const float k1 = rho1 * (rho1 * (rho1 * (sums[kTR] * inv_cols)));
+    float sigma1 = 1.f, m1 = 0.f;
+    if (p.w_post) {
+      sigma1 = rms_inverse(sums[kBB], inv_cols, p.eps);
+      const float dot = sums[kHA] + (rho1 * sums[kHT] - k1 * sums[kHR]);
+      m1 = sigma1 * (sigma1 * (sigma1 * (dot * inv_cols)));
+    }
+    const float2 rho = both(rho1), sigma = both(sigma1), k = both(-k1), m = both(-m1);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float2 d[4], o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pre[v][i] = fma2(y[v].get(i), mul2(x[v].get(i), rho), pre[v][i]);
+        d[i] = fma2(x[v].get(i), k, fma2(rho, f[v][i], a[v].get(i)));
+        o[i] = mul2(alpha, d[i]);
+        q[v][i] = fma2(d[i], mul2(b[v].get(i), sigma), q[v][i]);
+      }
+      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, round8<S>(o));
+      if (p.gate) times_w(d, p.gate, p.w_fp32, goff, c, v);
+      if (p.w_post) {
+        times_w(d, p.w_post, p.w_fp32, 0, c, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = fma2(b[v].get(i), m, mul2(sigma, d[i]));
+      }
+      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, round8<C>(d));
+    }
+    if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
+      if (p.gate) {
+        const bool whole = group * per >= lo && left == 0;
         float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -570,28 +547,16 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             out.f[i] = dg[i];
-            post[v][i] = add2(post[v][i], q[v][i]);
-            q[v][i] = both(0.f);
+            if constexpr (MANY) {
+              post[v][i] = add2(post[v][i], q[v][i]);
+              q[v][i] = both(0.f);
+            }
           }
           store8(dst, c, v, out);
         }
       }
-    }
-    // row t's sums are complete, and nobody reads row t - 1 any more
-    __syncthreads();
-    if (stages > 0) {
-      if (apply && threadIdx.x == 0 && t - 1 + stages < hi) issue(t - 1 + stages, last_stage);
-      last_stage = stage;
-      if (++stage == stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    group = next_group;
-    left = next_left;
-    if (--next_left == 0) {
-      ++next_group;
-      next_left = per;
+      ++group;
+      left = per;
     }
   }
   if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
@@ -607,13 +572,14 @@ __global__ void __launch_bounds__(kBackThreads)
     store8(ws_pre(p, me), c, v, out);
     if (p.w_post) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out.f[i] = p.gate ? post[v][i] : q[v][i];
+      for (int i = 0; i < 4; ++i) out.f[i] = MANY ? post[MANY ? v : 0][i] : q[v][i];
       store8(ws_post(p, n, me), c, v, out);
     }
   }
 }
 
-// The gradient for rows that are not on 16-byte boundaries: element by element,
+// The gradient for rows that are not on 16-byte boundaries, or longer than a
+// block's registers hold: element by element,
 // with the column sums of w_pre and D b sigma and the row's u in shared memory
 // (cols floats each).  Sums over finished gates (gates > 1) grow in the
 // workspace.  A thread goes through the same columns everywhere, so no two
@@ -856,8 +822,9 @@ cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t str
 }
 
 // Runs of eight columns that a thread holds in the gradient: as few as 512
-// threads allow.
-int backward_runs(int64_t cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
+// threads allow (two at most, more do not fit its registers).
+int backward_runs(int64_t cols) { return cols <= 4096 ? 1 : 2; }
+constexpr int64_t kRunsMaxCols = 2 * 8 * kBackThreads;
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
 constexpr size_t kSmemBytes = 200 * 1024;  // of an SM, for rings and sums; L1 keeps the weights
@@ -909,11 +876,11 @@ cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
   });
 }
 
-template <typename C, typename S, Mode M, int NV>
+template <typename C, typename S, Mode M, int NV, bool MANY>
 cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t n,
                           cudaStream_t stream) {
   static PerDeviceOnce setup;
-  auto kern = norm_backward_kernel<C, S, M, NV>;
+  auto kern = norm_backward_kernel<C, S, M, NV, MANY>;
   const cudaError_t err = allow_smem(setup, kern);
   if (err != cudaSuccess) return err;
   return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p,
@@ -933,19 +900,19 @@ cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64
 template <typename C, typename S, int NV>
 cudaError_t backward_runs_of(const NormBackParams& p, const BackPlan& plan, int64_t n,
                              cudaStream_t stream) {
-  return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV>(p, plan, n, stream)
-                           : backward_impl<C, S, kRuns, NV>(p, plan, n, stream);
+  if (p.gates > 1)
+    return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV, true>(p, plan, n, stream)
+                             : backward_impl<C, S, kRuns, NV, true>(p, plan, n, stream);
+  return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV, false>(p, plan, n, stream)
+                           : backward_impl<C, S, kRuns, NV, false>(p, plan, n, stream);
 }
 
 template <typename C, typename S>
 cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
                      cudaStream_t stream) {
   if (!vec) return backward_single<C, S>(p, plan, n, stream);
-  switch (backward_runs(p.cols)) {
-    case 1: return backward_runs_of<C, S, 1>(p, plan, n, stream);
-    case 2: return backward_runs_of<C, S, 2>(p, plan, n, stream);
-    default: return backward_runs_of<C, S, 4>(p, plan, n, stream);
-  }
+  return backward_runs(p.cols) == 1 ? backward_runs_of<C, S, 1>(p, plan, n, stream)
+                                    : backward_runs_of<C, S, 2>(p, plan, n, stream);
 }
 
 }  // namespace
@@ -953,6 +920,7 @@ cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, in
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
   int fit = 1;  // the most that any types and alignment have
   for (int i = 0; i < 8; ++i) {
+    if ((i & 4) && cols > kRunsMaxCols) break;
     const int f = backward_plan(cols, i & 1, i & 2, i & 4).fit;
     fit = f > fit ? f : fit;
   }
@@ -984,7 +952,7 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
     return err;
   }
   const int64_t ce = p.c_fp32 ? 4 : 8, se = p.s_fp32 ? 4 : 8;
-  const bool vec = p.cols % 8 == 0 && aligned16(p.d_res) && aligned16(p.dy) &&
+  const bool vec = p.cols % 8 == 0 && p.cols <= kRunsMaxCols && aligned16(p.d_res) && aligned16(p.dy) &&
                    aligned16(p.block) && aligned16(p.res_out) && aligned16(p.w_post) &&
                    aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
                    aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&

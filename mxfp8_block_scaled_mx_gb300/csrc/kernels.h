@@ -1,6 +1,7 @@
 // kernels.h -- launch interface between the C-ABI layer (mx_api.cu) and the
 // CUDA kernels (quantize.cu and quantize_f32.cu, which instantiate
-// quantize_kernel.cuh; gemm_pair.cu; norm.cu; moe_few.cu; status.cu).  Not part of the public
+// quantize_kernel.cuh; gemm_pair.cu; norm.cu, norm_mixed.cu and norm_f32.cu,
+// which instantiate norm_kernel.cuh; moe_few.cu; status.cu).  Not part of the public
 // ABI.
 #pragma once
 

@@ -1,684 +1,16 @@
-// norm.cu -- the norms before and after a block, with its gate and residual
-// scale, and their gradients.
-//
-//   res_out = alpha * residual + g * n(block; w_post),  y = n(res_out; w_pre)
-//   n(v; w)_c = v_c w_c / sqrt(mean(v^2) + eps)
-//
-// Both directions are bound by memory: every row is read and written once.
-// A thread owns the same columns of every array of a row (runs of eight where
-// rows and pointers allow 16-byte accesses, else every T-th one), so the only
-// exchange within a row is the sum behind each norm.  Arithmetic is FP32, two
-// columns an instruction (f32x2): at memory speed a row leaves an SM about 20
-// instructions per column pair and direction, so their number counts.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
-#include <atomic>
-#include <cstdint>
-
-#include "kernels.h"
-#include "ptx.cuh"
+// norm.cu -- the norms around a block: the choice of kernels by type, the
+// kernels for bf16 blocks on a bf16 stream, and the joining of the gradient's
+// column sums.
+#include "norm_kernel.cuh"
 
 namespace mx {
+
+cudaError_t norm_forward_mixed(const NormParams& p, bool vec, int num_sms, cudaStream_t stream);
+cudaError_t norm_forward_f32(const NormParams& p, bool vec, int num_sms, cudaStream_t stream);
+cudaError_t norm_backward_mixed(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream);
+cudaError_t norm_backward_f32(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream);
+
 namespace {
-
-using bf16 = __nv_bfloat16;
-
-// ------------------------------------------------------------------ pairs of columns
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t pack2(float2 v) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ void store1(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-
-// ------------------------------------------------------------------ columns of a thread
-
-// How a thread's NV runs of eight columns lie in a row:
-// kWhole  run v is columns 8 (v threads + tid) ..+7, 16 bytes an access, and
-//         the row has exactly 8 NV threads columns;
-// kRuns   the same with an end inside (whole runs of eight);
-// kSingle element j of run v is column (8 v + j) threads + tid, one at a time.
-enum Mode { kWhole, kRuns, kSingle };
-
-template <Mode M>
-struct Cols {
-  int32_t cols, tid, threads;
-  __device__ __forceinline__ int32_t at(int v, int j) const {
-    return M == kSingle ? (8 * v + j) * threads + tid : 8 * (v * threads + tid) + j;
-  }
-  __device__ __forceinline__ bool has(int v, int j) const {
-    return M == kWhole || at(v, M == kRuns ? 0 : j) < cols;
-  }
-};
-
-// A run of eight elements as loaded.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<bf16> {
-  uint32_t w[4];
-  __device__ __forceinline__ float2 get(int i) const { return unpack2(w[i]); }
-};
-template <>
-struct Raw<float> {
-  float2 f[4];
-  __device__ __forceinline__ float2 get(int i) const { return f[i]; }
-};
-
-__device__ __forceinline__ uint32_t bits(bf16 v) { return *reinterpret_cast<const uint16_t*>(&v); }
-
-// Sixteen bytes of global memory that are read once: they take no place of the
-// weights' in L1.
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Run v of a row; elements past its end read as zero.  ONCE: a row of global
-// memory that is not read again.
-template <bool ONCE = false, typename T, Mode M>
-__device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
-  Raw<T> r;
-  if constexpr (M == kSingle) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool a = c.has(v, 2 * i), b = c.has(v, 2 * i + 1);
-      if constexpr (sizeof(T) == 2)
-        r.w[i] = (a ? bits(row[c.at(v, 2 * i)]) : 0u) | (b ? bits(row[c.at(v, 2 * i + 1)]) << 16 : 0u);
-      else
-        r.f[i] = make_float2(a ? row[c.at(v, 2 * i)] : 0.f, b ? row[c.at(v, 2 * i + 1)] : 0.f);
-    }
-  } else {
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (c.has(v, 0)) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
-      x = ONCE ? load_once(p) : p[0];
-      if constexpr (sizeof(T) == 4) y = ONCE ? load_once(p + 1) : p[1];
-    }
-    if constexpr (sizeof(T) == 2) {
-      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-    } else {
-      r.f[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-      r.f[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
-      r.f[2] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
-      r.f[3] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
-    }
-  }
-  return r;
-}
-
-// f *= run v of a weight or gate, whose type is a run-time matter.
-template <Mode M>
-__device__ __forceinline__ void times_w(float2 (&f)[4], const void* w, int32_t f32, int64_t off,
-                                        const Cols<M>& c, int v) {
-  if (f32) {
-    const Raw<float> r = load8(static_cast<const float*>(w) + off, c, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], r.get(i));
-  } else {
-    const Raw<bf16> r = load8(static_cast<const bf16*>(w) + off, c, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], r.get(i));
-  }
-}
-
-template <typename T, Mode M>
-__device__ __forceinline__ void store8(T* row, const Cols<M>& c, int v, const Raw<T>& r) {
-  if constexpr (M == kSingle) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.has(v, j)) {
-        if constexpr (sizeof(T) == 2)
-          row[c.at(v, j)] = __ushort_as_bfloat16(static_cast<uint16_t>(r.w[j / 2] >> (j % 2 * 16)));
-        else
-          row[c.at(v, j)] = j % 2 ? r.f[j / 2].y : r.f[j / 2].x;
-      }
-  } else {
-    if (!c.has(v, 0)) return;
-    uint4* p = reinterpret_cast<uint4*>(row + c.at(v, 0));
-    if constexpr (sizeof(T) == 2) {
-      p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-    } else {
-      p[0] = make_uint4(__float_as_uint(r.f[0].x), __float_as_uint(r.f[0].y),
-                        __float_as_uint(r.f[1].x), __float_as_uint(r.f[1].y));
-      p[1] = make_uint4(__float_as_uint(r.f[2].x), __float_as_uint(r.f[2].y),
-                        __float_as_uint(r.f[3].x), __float_as_uint(r.f[3].y));
-    }
-  }
-}
-
-// Eight FP32 values in type T (one rounding).
-template <typename T>
-__device__ __forceinline__ Raw<T> round8(const float2 (&f)[4]) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2)
-      r.w[i] = pack2(f[i]);
-    else
-      r.f[i] = f[i];
-  }
-  return r;
-}
-
-// ------------------------------------------------------------------ sums over a row
-
-constexpr int kMaxWarps = 32;
-
-// N sums over the block of threads, the same in every thread and run after
-// run.  `part` holds N * 32 floats (zeros past the last warp) that the block's
-// previous sum does not use (callers alternate between two), so one barrier
-// is enough.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (blockDim.x == 32) return;
-  if (lane_id() == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[i * kMaxWarps + warp_id()] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (uint32_t w = 0; w < blockDim.x / 32; w += 4)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(part + i * kMaxWarps + w);
-      v[i] += (f.x + f.y) + (f.z + f.w);
-    }
-}
-
-// 1 / sqrt(mean + eps): the hardware's estimate and one Newton step, which
-// leaves an error of about one unit in the last place (and 1 / 0 and 1 / inf
-// as they are, where the step would make NaN).
-__device__ __forceinline__ float rms_inverse(float sum_squares, float inv_cols, float eps) {
-  const float m = sum_squares * inv_cols + eps;
-  const float r = rsqrtf(m);
-  const float s = r + r * 0.5f * (1.f - m * r * r);
-  return m > 0.f && m < INFINITY ? s : r;
-}
-
-// ------------------------------------------------------------------ forward
-
-// A block of threads goes through every gridDim.x-th row.  A row's registers
-// are free once the stream's row is formed, so the next row is loaded there,
-// behind the second norm.
-template <typename C, typename S, Mode M, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p) {
-  __shared__ __align__(16) float part[2][kMaxWarps];
-  if (threadIdx.x < 2 * kMaxWarps) part[0][threadIdx.x] = 0.f;
-  if (blockDim.x == 32) part[1][threadIdx.x] = 0.f;
-  __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                  static_cast<int32_t>(blockDim.x)};
-  const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const float2 alpha = both(p.alpha);
-  const uint32_t rows = static_cast<uint32_t>(p.rows);
-  const uint32_t per = p.gate ? rows / static_cast<uint32_t>(p.gates) : 1u;
-  Raw<C> b[NV];
-  Raw<S> r[NV];
-  auto fetch = [&](uint32_t t) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) r[v] = load8<true>(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
-  };
-  uint32_t t = blockIdx.x;
-  fetch(t);
-  while (true) {
-    float sum[1];
-    float2 sigma = both(1.f);
-    if (p.w_post) {
-      float2 s = both(0.f);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma2(b[v].get(i), b[v].get(i), s);
-      sum[0] = s.x + s.y;
-      block_sum(sum, part[0]);
-      sigma = both(rms_inverse(sum[0], inv_cols, p.eps));
-    }
-    const int64_t goff = p.gate ? t / per * p.cols : 0;
-    Raw<S> out[NV];
-    float2 s = both(0.f);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float2 f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(b[v].get(i), sigma);
-      if (p.w_post) times_w(f, p.w_post, p.w_fp32, 0, c, v);
-      if (p.gate) times_w(f, p.gate, p.w_fp32, goff, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = fma2(alpha, r[v].get(i), f[i]);
-      out[v] = round8<S>(f);
-      store8(static_cast<S*>(p.res_out) + t * p.ldo, c, v, out[v]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(out[v].get(i), out[v].get(i), s);
-    }
-    const uint32_t next = t + gridDim.x;
-    if (next < rows) fetch(next);
-    sum[0] = s.x + s.y;
-    block_sum(sum, part[1]);
-    const float2 rho = both(rms_inverse(sum[0], inv_cols, p.eps));
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float2 f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = mul2(out[v].get(i), rho);
-      times_w(f, p.w_pre, p.w_fp32, 0, c, v);
-      store8(static_cast<C*>(p.y) + t * p.ldy, c, v, round8<C>(f));
-    }
-    if (next >= rows) return;
-    t = next;
-    if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[1] is used in every row
-  }
-}
-
-// ------------------------------------------------------------------ backward
-
-// Rows of block i of n: q each, the first r blocks one more.
-struct RowShare {
-  uint32_t q, r;
-  __host__ __device__ RowShare(uint32_t rows, uint32_t n) : q(rows / n), r(rows - rows / n * n) {}
-  __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * q + (i < r ? i : r); }
-  // block whose rows hold row t
-  __device__ __forceinline__ uint32_t of(uint32_t t) const {
-    const uint32_t m = r * (q + 1);
-    return t < m ? t / (q + 1) : r + (t - m) / q;
-  }
-};
-
-// Workspace of n blocks: sums over each block's rows, FP32 [n][cols] for
-// w_pre, [n][cols] for w_post, and [2n][cols] for gates whose rows several
-// blocks share (a block's first such gate, then its last).
-__device__ __forceinline__ float* ws_pre(const NormBackParams& p, int64_t i) {
-  return p.workspace + i * p.cols;
-}
-__device__ __forceinline__ float* ws_post(const NormBackParams& p, int64_t n, int64_t i) {
-  return p.workspace + (n + i) * p.cols;
-}
-__device__ __forceinline__ float* ws_gate(const NormBackParams& p, int64_t n, int64_t slot) {
-  return p.workspace + (2 * n + slot) * p.cols;
-}
-
-constexpr int kBackThreads = 512;   // at most
-
-// The sums behind a row's gradient.  With t = w_pre dy and h = w_post g block,
-//   D = d_res + rho t - rho^3 mean(t r) r,   dot = sum of h D
-//     = sum h d_res + rho sum h t - rho^3 mean(t r) sum h r,
-// so that one pass over the row gives all of them, before rho is known.
-enum RowSum { kRR, kTR, kBB, kHA, kHT, kHR, kRowSums };
-
-// Eight sums over a warp in nine exchanges: lane l gets that of v[l / 4].
-__device__ __forceinline__ float warp_sum8(float (&v)[8]) {
-  const uint32_t lane = lane_id();
-#pragma unroll
-  for (int o = 16, n = 4; n > 0; o >>= 1, n >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
-
-// One block of threads goes through its own rows in order.  Rows arrive in
-// shared memory by bulk copies, `stages` of them at most (0: rows that do not
-// fit, read in place); a thread takes its columns to registers once, where
-// they stay across the row's one barrier, behind which the next copy starts.
-// A thread also keeps the sums of its columns over the rows.  MANY: more gates
-// than one.
-template <typename C, typename S, Mode M, int NV, bool MANY>
-__global__ void __launch_bounds__(kBackThreads)
-    norm_backward_kernel(const NormBackParams p, int stages) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float part[2][kMaxWarps / 2 * 8];
-  __shared__ uint64_t full[8];
-  __shared__ uint32_t abort_word;
-  volatile uint32_t* s_abort = &abort_word;
-  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                  static_cast<int32_t>(blockDim.x)};
-  const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const uint32_t n = gridDim.x, me = blockIdx.x, lane = lane_id();
-  const RowShare share(static_cast<uint32_t>(p.rows), n);
-  const uint32_t lo = share.start(me), hi = share.start(me + 1);
-  const uint32_t cbytes = static_cast<uint32_t>(p.cols * sizeof(C));
-  const uint32_t sbytes = static_cast<uint32_t>(p.cols * sizeof(S));
-  const uint32_t stage_bytes = 2 * cbytes + 2 * sbytes;
-  for (uint32_t i = threadIdx.x; i < kMaxWarps * 8; i += blockDim.x) part[0][i] = 0.f;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-    abort_word = 0;
-    fence_mbarrier_init();
-  }
-  __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  auto issue = [&](uint32_t t, int s) {
-    uint8_t* dst = smem + s * stage_bytes;
-    mbar_arrive_expect_tx(&full[s], p.d_res ? stage_bytes : stage_bytes - sbytes);
-    bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy, cbytes, &full[s]);
-    bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb, cbytes, &full[s]);
-    bulk_load(dst + 2 * cbytes, static_cast<const S*>(p.res_out) + t * p.ldr, sbytes, &full[s]);
-    if (p.d_res)
-      bulk_load(dst + 2 * cbytes + sbytes, static_cast<const S*>(p.d_res) + t * p.ldd, sbytes,
-                &full[s]);
-  };
-  if (threadIdx.x == 0)
-    for (int s = 0; s < stages && lo + s < hi; ++s) issue(lo + s, s);
-
-  const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
-  const float2 alpha = both(p.alpha);
-  // sums over rows of dy r rho and of D b sigma, with many gates also of the
-  // latter times g over finished gates
-  constexpr int kPost = MANY ? NV : 1;
-  float2 pre[NV][4], q[NV][4], post[kPost][4];
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = post[MANY ? v : 0][i] = both(0.f);
-  const uint32_t group0 = lo / per;
-  uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
-  int stage = 0;
-  uint32_t phase = 0;
-  for (uint32_t t = lo; t < hi; ++t) {
-    const int64_t goff = group * p.cols;
-    Raw<S> x[NV], a[NV] = {};
-    Raw<C> y[NV], b[NV];
-    if (stages > 0) {
-      mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
-      const uint8_t* src = smem + stage * stage_bytes;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        y[v] = load8(reinterpret_cast<const C*>(src), c, v);
-        b[v] = load8(reinterpret_cast<const C*>(src + cbytes), c, v);
-        x[v] = load8(reinterpret_cast<const S*>(src + 2 * cbytes), c, v);
-        if (p.d_res) a[v] = load8(reinterpret_cast<const S*>(src + 2 * cbytes + sbytes), c, v);
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        y[v] = load8<true>(static_cast<const C*>(p.dy) + t * p.lddy, c, v);
-        b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
-        x[v] = load8<true>(static_cast<const S*>(p.res_out) + t * p.ldr, c, v);
-        if (p.d_res) a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd, c, v);
-      }
-    }
-    float2 s2[kRowSums];
-#pragma unroll
-    for (int i = 0; i < kRowSums; ++i) s2[i] = both(0.f);
-    float2 f[NV][4];                                       // w_pre dy
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[v][i] = y[v].get(i);
-      times_w(f[v], p.w_pre, p.w_fp32, 0, c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s2[kRR] = fma2(x[v].get(i), x[v].get(i), s2[kRR]);
-        s2[kTR] = fma2(f[v][i], x[v].get(i), s2[kTR]);
-      }
-      if (p.w_post) {
-        float2 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[i] = b[v].get(i);
-          s2[kBB] = fma2(h[i], h[i], s2[kBB]);
-        }
-        times_w(h, p.w_post, p.w_fp32, 0, c, v);
-        if (p.gate) times_w(h, p.gate, p.w_fp32, goff, c, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s2[kHA] = fma2(h[i], a[v].get(i), s2[kHA]);
-          s2[kHT] = fma2(h[i], f[v][i], s2[kHT]);
-          s2[kHR] = fma2(h[i], x[v].get(i), s2[kHR]);
-        }
-      }
-    }
-    float sums[8];
-#pragma unroll
-    for (int i = 0; i < kRowSums; ++i) sums[i] = s2[i].x + s2[i].y;
-    sums[6] = sums[7] = 0.f;
-    float s = warp_sum8(sums);
-    if ((lane & 3) == 0) part[t & 1][warp_id() * 8 + lane / 4] = s;
-    __syncthreads();
-    // past this barrier the row is in registers
-    if (stages > 0) {
-      if (threadIdx.x == 0 && t + stages < hi) issue(t + stages, stage);
-      if (++stage == stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    s = 0.f;
-#pragma unroll
-    for (uint32_t w = 0; w < kMaxWarps / 2; w += 4)
-      if (w < blockDim.x / 32) s += part[t & 1][(w + lane / 8) * 8 + lane % 8];
-    s += __shfl_xor_sync(0xffffffffu, s, 8);
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-#pragma unroll
-    for (int i = 0; i < kRowSums; ++i) sums[i] = __shfl_sync(0xffffffffu, s, i);
-    const float rho1 = rms_inverse(sums[kRR], inv_cols, p.eps);
-    // (in this order nothing leaves FP32's range before the product does)
-    const float k1 = rho1 * (rho1 * (rho1 * (sums[kTR] * inv_cols)));
-    float sigma1 = 1.f, m1 = 0.f;
-    if (p.w_post) {
-      sigma1 = rms_inverse(sums[kBB], inv_cols, p.eps);
-      const float dot = sums[kHA] + (rho1 * sums[kHT] - k1 * sums[kHR]);
-      m1 = sigma1 * (sigma1 * (sigma1 * (dot * inv_cols)));
-    }
-    const float2 rho = both(rho1), sigma = both(sigma1), k = both(-k1), m = both(-m1);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float2 d[4], o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pre[v][i] = fma2(y[v].get(i), mul2(x[v].get(i), rho), pre[v][i]);
-        d[i] = fma2(x[v].get(i), k, fma2(rho, f[v][i], a[v].get(i)));
-        o[i] = mul2(alpha, d[i]);
-        q[v][i] = fma2(d[i], mul2(b[v].get(i), sigma), q[v][i]);
-      }
-      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, round8<S>(o));
-      if (p.gate) times_w(d, p.gate, p.w_fp32, goff, c, v);
-      if (p.w_post) {
-        times_w(d, p.w_post, p.w_fp32, 0, c, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = fma2(b[v].get(i), m, mul2(sigma, d[i]));
-      }
-      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, round8<C>(d));
-    }
-    if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
-      if (p.gate) {
-        const bool whole = group * per >= lo && left == 0;
-        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float2 dg[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dg[i] = q[v][i];
-          if (p.w_post) times_w(dg, p.w_post, p.w_fp32, 0, c, v);
-          times_w(q[v], p.gate, p.w_fp32, goff, c, v);
-          Raw<float> out;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            out.f[i] = dg[i];
-            if constexpr (MANY) {
-              post[v][i] = add2(post[v][i], q[v][i]);
-              q[v][i] = both(0.f);
-            }
-          }
-          store8(dst, c, v, out);
-        }
-      }
-      ++group;
-      left = per;
-    }
-  }
-  if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
-    for (uint32_t s = 0; s < static_cast<uint32_t>(stages) && lo + s < hi; ++s)
-      mbar_wait(&full[s], (hi - lo - 1 - s) / stages & 1u, s_abort, p.status, p.wait_limit_ns,
-                true);
-  }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    Raw<float> out;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out.f[i] = pre[v][i];
-    store8(ws_pre(p, me), c, v, out);
-    if (p.w_post) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) out.f[i] = MANY ? post[MANY ? v : 0][i] : q[v][i];
-      store8(ws_post(p, n, me), c, v, out);
-    }
-  }
-}
-
-// The gradient for rows that are not on 16-byte boundaries, or longer than a
-// block's registers hold: element by element,
-// with the column sums of w_pre and D b sigma and the row's u in shared memory
-// (cols floats each).  Sums over finished gates (gates > 1) grow in the
-// workspace.  A thread goes through the same columns everywhere, so no two
-// threads touch the same sum.
-template <typename C, typename S>
-__global__ void __launch_bounds__(kBackThreads)
-    norm_backward_single_kernel(const NormBackParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float part[2][3 * kMaxWarps];
-  const int cols = static_cast<int>(p.cols), tid = static_cast<int>(threadIdx.x);
-  const int step = static_cast<int>(blockDim.x);
-  const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const uint32_t n = gridDim.x, me = blockIdx.x;
-  const RowShare share(static_cast<uint32_t>(p.rows), n);
-  const uint32_t lo = share.start(me), hi = share.start(me + 1);
-  const bool many = p.gates > 1;
-  float* pre = reinterpret_cast<float*>(smem);
-  float* q = pre + cols;
-  float* u_row = q + cols;
-  float* post_out = ws_post(p, n, me);
-  for (int i = tid; i < 6 * kMaxWarps; i += step) part[0][i] = 0.f;
-  __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int c = tid; c < cols; c += step) {
-    pre[c] = q[c] = 0.f;
-    if (many) post_out[c] = 0.f;
-  }
-  auto weight = [&](const void* w, int64_t i) {
-    return p.w_fp32 ? static_cast<const float*>(w)[i] : to_float(static_cast<const bf16*>(w)[i]);
-  };
-  const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
-  const uint32_t group0 = lo / per;
-  uint32_t group = group0, left = (group + 1) * per - lo;
-  for (uint32_t t = lo; t < hi; ++t) {
-    const C* dy = static_cast<const C*>(p.dy) + t * p.lddy;
-    const C* block = static_cast<const C*>(p.block) + t * p.ldb;
-    const S* res = static_cast<const S*>(p.res_out) + t * p.ldr;
-    const S* dres = p.d_res ? static_cast<const S*>(p.d_res) + t * p.ldd : nullptr;
-    const int64_t goff = group * p.cols;
-    float sum[3] = {0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int c = tid; c < cols; c += step) {
-      const float x = to_float(res[c]), b = to_float(block[c]);
-      sum[0] += x * x;
-      sum[1] += to_float(dy[c]) * weight(p.w_pre, c) * x;
-      sum[2] += b * b;
-    }
-    block_sum(sum, part[0]);
-    const float rho = rms_inverse(sum[0], inv_cols, p.eps);
-    const float sigma = p.w_post ? rms_inverse(sum[2], inv_cols, p.eps) : 1.f;
-    const float k = rho * (rho * (rho * (sum[1] * inv_cols)));
-    float dot[1] = {0.f};
-#pragma unroll 2
-    for (int c = tid; c < cols; c += step) {
-      const float x = to_float(res[c]), y = to_float(dy[c]), b = to_float(block[c]);
-      const float d = (dres ? to_float(dres[c]) : 0.f) + (rho * (y * weight(p.w_pre, c)) - x * k);
-      store1(static_cast<S*>(p.d_residual) + t * p.lddr + c, p.alpha * d);
-      pre[c] += y * (x * rho);
-      q[c] += d * (b * sigma);
-      float u = d;
-      if (p.gate) u *= weight(p.gate, goff + c);
-      if (p.w_post) u *= weight(p.w_post, c);
-      dot[0] += u * b;
-      u_row[c] = u;
-    }
-    float m = 0.f;
-    if (p.w_post) {
-      block_sum(dot, part[1]);
-      m = sigma * (sigma * (sigma * (dot[0] * inv_cols)));
-    }
-#pragma unroll 2
-    for (int c = tid; c < cols; c += step) {
-      const float u = u_row[c];
-      store1(static_cast<C*>(p.d_block) + t * p.lddb + c,
-             p.w_post ? sigma * u - to_float(block[c]) * m : u);
-    }
-    if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[0] is used in every row
-    if (--left == 0 || t + 1 == hi) {
-      if (p.gate) {
-        const bool whole = group * per >= lo && t + 1 == (group + 1) * per;
-        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
-        for (int c = tid; c < cols; c += step) {
-          const float g = q[c] * weight(p.gate, goff + c);
-          dst[c] = p.w_post ? q[c] * weight(p.w_post, c) : q[c];
-          if (many) post_out[c] += g;
-          q[c] = many ? 0.f : g;
-        }
-      }
-      ++group;
-      left = per;
-    }
-  }
-  float* pre_out = ws_pre(p, me);
-  for (int c = tid; c < cols; c += step) {
-    pre_out[c] = pre[c];
-    if (p.w_post && !many) post_out[c] = q[c];
-  }
-}
 
 constexpr int kSumCols = 32, kSumParts = 32;
 
@@ -728,7 +60,7 @@ __global__ void __launch_bounds__(kSumCols* kSumParts)
     }
     src += col;
     if (job >= 2 && begin == 0 && end > 0 && share.start(first) < group * per) {
-      s = src[p.cols] ;
+      s = src[p.cols];
       for (uint32_t i = 1; i < end; ++i) s += src[i * step];
     } else {
 #pragma unroll 8
@@ -742,177 +74,6 @@ __global__ void __launch_bounds__(kSumCols* kSumParts)
     for (int i = 1; i < kSumParts; ++i) s += part[i][threadIdx.x];
     out[col] = s;
   }
-}
-
-// ------------------------------------------------------------------ launches
-
-template <typename K, typename... A>
-cudaError_t launch(K kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Threads of a row of `cols` columns held in NV runs of eight per thread.
-int row_threads(int64_t cols, int nv) {
-  const int64_t runs = (cols + 7) / 8;
-  return static_cast<int>(((runs + nv - 1) / nv + 31) / 32 * 32);
-}
-bool whole(int64_t cols, int nv) { return cols == 8 * static_cast<int64_t>(nv) * row_threads(cols, nv); }
-
-// Blocks of a kernel that an SM holds at once, asked of the runtime once per
-// device and number of threads.
-class Fit {
- public:
-  template <typename K>
-  int of(K kern, int threads) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 1;
-    std::atomic<int>& known = fit_[dev][threads / 32];
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)
-        n = 1;
-      known.store(n, std::memory_order_relaxed);
-    }
-    return n;
-  }
-
- private:
-  static constexpr int kDevs = 64;
-  std::atomic<int> fit_[kDevs][33] = {};
-};
-
-template <typename C, typename S, Mode M, int NV, int MAXT>
-cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) {
-  static Fit fit;
-  const int threads = row_threads(p.cols, NV);
-  auto kern = norm_residual_kernel<C, S, M, NV, MAXT>;
-  int64_t grid = p.rows;
-  if (grid > num_sms) {
-    const int64_t most = static_cast<int64_t>(num_sms) * fit.of(kern, threads);
-    grid = grid < most ? grid : most;
-  }
-  return launch(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p);
-}
-
-template <typename C, typename S, int NV, int MAXT>
-cudaError_t forward_mode(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  if (!vec) return forward_impl<C, S, kSingle, NV, MAXT>(p, num_sms, stream);
-  if (whole(p.cols, NV)) return forward_impl<C, S, kWhole, NV, MAXT>(p, num_sms, stream);
-  return forward_impl<C, S, kRuns, NV, MAXT>(p, num_sms, stream);
-}
-
-template <typename C, typename S>
-cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  // few rows: as many threads as a row takes; else rows of few threads, so
-  // that several are under way on an SM
-  if (p.cols <= 1024 || (p.cols <= 8192 && p.rows <= num_sms))
-    return forward_mode<C, S, 1, 1024>(p, vec, num_sms, stream);
-  if (p.cols <= 4096) return forward_mode<C, S, 2, 256>(p, vec, num_sms, stream);
-  return forward_mode<C, S, 4, 512>(p, vec, num_sms, stream);
-}
-
-// Runs of eight columns that a thread holds in the gradient: as few as 512
-// threads allow (two at most, more do not fit its registers).
-int backward_runs(int64_t cols) { return cols <= 4096 ? 1 : 2; }
-constexpr int64_t kRunsMaxCols = 2 * 8 * kBackThreads;
-
-constexpr int kMaxSms = 192;         // workspaces are sized for this many
-constexpr size_t kSmemBytes = 200 * 1024;  // of an SM, for rings and sums; L1 keeps the weights
-
-// How a gradient is run: threads of a block, blocks side by side on an SM,
-// rows of the ring, bytes of shared memory of a block.
-struct BackPlan {
-  int threads, fit, stages;
-  size_t smem;
-};
-BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec) {
-  BackPlan p;
-  if (!vec) {  // by shared memory and 2048 threads
-    p.threads = cols <= 2048 ? static_cast<int>((cols + 127) / 128 * 32) : kBackThreads;
-    p.smem = static_cast<size_t>(cols) * 12;
-    p.fit = static_cast<int>(kSmemBytes / p.smem);
-    const int by_threads = 2 * kBackThreads / p.threads;
-    p.fit = p.fit < by_threads ? p.fit : by_threads;
-    p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-    p.stages = 0;
-    return p;
-  }
-  // by registers (128 a thread) and rings of three rows: one in each half of
-  // a step and one on its way
-  p.threads = row_threads(cols, backward_runs(cols));
-  const size_t stage = cols * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
-  p.fit = kBackThreads / p.threads;
-  const int by_smem = static_cast<int>(kSmemBytes / (3 * stage));
-  p.fit = p.fit < by_smem ? p.fit : by_smem;
-  p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-  const size_t rows = kSmemBytes / p.fit / stage;
-  p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
-  p.smem = p.stages * stage;
-  return p;
-}
-
-// Blocks of the gradient: those that fit the SMs, with four rows each at
-// least (a block's column sums are written and read once more).
-int64_t backward_blocks(int64_t rows, int num_sms, int fit) {
-  const int64_t most = static_cast<int64_t>(num_sms) * fit, want = (rows + 3) / 4;
-  return want < num_sms ? (rows < num_sms ? rows : num_sms) : want < most ? want : most;
-}
-
-template <typename K>
-cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
-  return setup.run([&]() -> cudaError_t {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kSmemBytes));
-  });
-}
-
-template <typename C, typename S, Mode M, int NV, bool MANY>
-cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t n,
-                          cudaStream_t stream) {
-  static PerDeviceOnce setup;
-  auto kern = norm_backward_kernel<C, S, M, NV, MANY>;
-  const cudaError_t err = allow_smem(setup, kern);
-  if (err != cudaSuccess) return err;
-  return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p,
-                plan.stages);
-}
-
-template <typename C, typename S>
-cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64_t n,
-                            cudaStream_t stream) {
-  static PerDeviceOnce setup;
-  auto kern = norm_backward_single_kernel<C, S>;
-  const cudaError_t err = allow_smem(setup, kern);
-  if (err != cudaSuccess) return err;
-  return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p);
-}
-
-template <typename C, typename S, int NV>
-cudaError_t backward_runs_of(const NormBackParams& p, const BackPlan& plan, int64_t n,
-                             cudaStream_t stream) {
-  if (p.gates > 1)
-    return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV, true>(p, plan, n, stream)
-                             : backward_impl<C, S, kRuns, NV, true>(p, plan, n, stream);
-  return whole(p.cols, NV) ? backward_impl<C, S, kWhole, NV, false>(p, plan, n, stream)
-                           : backward_impl<C, S, kRuns, NV, false>(p, plan, n, stream);
-}
-
-template <typename C, typename S>
-cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
-                     cudaStream_t stream) {
-  if (!vec) return backward_single<C, S>(p, plan, n, stream);
-  return backward_runs(p.cols) == 1 ? backward_runs_of<C, S, 1>(p, plan, n, stream)
-                                    : backward_runs_of<C, S, 2>(p, plan, n, stream);
 }
 
 }  // namespace
@@ -934,11 +95,9 @@ cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t 
                    aligned16(p.res_out) && aligned16(p.y) && aligned16(p.w_pre) &&
                    aligned16(p.w_post) && aligned16(p.gate) && p.ldb % ce == 0 &&
                    p.ldy % ce == 0 && p.ldr % se == 0 && p.ldo % se == 0;
-  if (p.c_fp32)
-    return forward<float, float>(p, vec, num_sms, stream);
-  if (p.s_fp32)
-    return forward<bf16, float>(p, vec, num_sms, stream);
-  return forward<bf16, bf16>(p, vec, num_sms, stream);
+  if (p.c_fp32) return norm_forward_f32(p, vec, num_sms, stream);
+  if (p.s_fp32) return norm_forward_mixed(p, vec, num_sms, stream);
+  return norm_forward_of<bf16, bf16>(p, vec, num_sms, stream);
 }
 
 cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
@@ -961,11 +120,11 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
   const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan.fit);
   cudaError_t err;
   if (p.c_fp32)
-    err = backward<float, float>(p, vec, plan, n, stream);
+    err = norm_backward_f32(p, vec, n, stream);
   else if (p.s_fp32)
-    err = backward<bf16, float>(p, vec, plan, n, stream);
+    err = norm_backward_mixed(p, vec, n, stream);
   else
-    err = backward<bf16, bf16>(p, vec, plan, n, stream);
+    err = norm_backward_of<bf16, bf16>(p, vec, n, stream);
   if (err != cudaSuccess) return err;
   const int64_t jobs = 2 + (p.gates < n ? p.gates : n);
   return launch(norm_backward_sum_kernel,

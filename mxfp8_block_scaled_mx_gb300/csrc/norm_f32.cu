@@ -1,0 +1,14 @@
+// norm_f32.cu -- the norm kernels for FP32 blocks on an FP32 stream.
+#include "norm_kernel.cuh"
+
+namespace mx {
+
+cudaError_t norm_forward_f32(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
+  return norm_forward_of<float, float>(p, vec, num_sms, stream);
+}
+
+cudaError_t norm_backward_f32(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
+  return norm_backward_of<float, float>(p, vec, n, stream);
+}
+
+}  // namespace mx

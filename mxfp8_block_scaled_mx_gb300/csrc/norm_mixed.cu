@@ -1,0 +1,14 @@
+// norm_mixed.cu -- the norm kernels for bf16 blocks on an FP32 stream.
+#include "norm_kernel.cuh"
+
+namespace mx {
+
+cudaError_t norm_forward_mixed(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
+  return norm_forward_of<bf16, float>(p, vec, num_sms, stream);
+}
+
+cudaError_t norm_backward_mixed(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
+  return norm_backward_of<bf16, float>(p, vec, n, stream);
+}
+
+}  // namespace mx

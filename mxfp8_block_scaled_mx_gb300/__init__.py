@@ -613,7 +613,14 @@ def _block_rows(block):
 
 
 def _empty(shape, like: torch.Tensor) -> torch.Tensor:
+    if like.is_contiguous():
+        return torch.empty_like(like)
     return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _scale_bytes(rows: int, k: int) -> int:
+    """mx_scale_bytes without the call."""
+    return -(-rows // 128) * -(-k // 128) * 512
 
 
 _WIDE = tuple(_X_DTYPE)
@@ -689,13 +696,11 @@ def norm_residual_backward(d_residual: torch.Tensor | None, d_y: torch.Tensor, b
     if workspace is None:
         workspace = _scratch(need, block.device, stream)
     ws = _workspace_ptr(workspace, need, dev)
-    # the weights' gradients are views of one allocation
-    parts = 1 + (w_post is not None) + gates
-    sums = torch.empty((parts, cols), dtype=torch.float32, device=block.device)
-    grads = NormResidualGrads(_empty((rows, cols), block), _empty((rows, cols), residual), sums[0],
-                              None if w_post is None else sums[1],
-                              None if gate is None else sums[parts - gates:].view(gate.shape))
-    first = sums.data_ptr()
+    f32 = dict(dtype=torch.float32, device=block.device)
+    grads = NormResidualGrads(_empty((rows, cols), block), _empty((rows, cols), residual),
+                              torch.empty(cols, **f32),
+                              None if w_post is None else torch.empty(cols, **f32),
+                              None if gate is None else torch.empty(gate.shape, **f32))
     empty = rows == 0  # such tensors have no address; any device address stands in, unused
     st = c.mx_norm_residual_backward(
         rows, cols, None if d_residual is None or empty else d_residual.data_ptr(), ldd,
@@ -703,8 +708,7 @@ def norm_residual_backward(d_residual: torch.Tensor | None, d_y: torch.Tensor, b
         _X_DTYPE[block.dtype], ws if empty else residual.data_ptr(), ldr,
         _X_DTYPE[residual.dtype], post, pre, at, gates, w_code, alpha, eps,
         ws if empty else grads.block.data_ptr(), cols, ws if empty else grads.residual.data_ptr(),
-        cols, None if w_post is None else first + 4 * cols, first,
-        None if gate is None else first + 4 * cols * (parts - gates), ws, workspace.numel(),
+        cols, _ptr(grads.w_post), grads.w_pre.data_ptr(), _ptr(grads.gate), ws, workspace.numel(),
         _stream(stream))
     if st:
         raise MxError("mx_norm_residual_backward", st)
@@ -746,11 +750,11 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: Mx
     u = _dense(up.codes, (experts, inter, k_gu), _CODES, dev, "up codes")
     d = _dense(down.codes, (experts, hidden, k_d), _CODES, dev, "down codes")
     c = lib()
-    s_gu = experts * c.mx_scale_bytes(inter, hidden)
-    s_d = experts * c.mx_scale_bytes(hidden, inter)
+    s_gu = experts * _scale_bytes(inter, hidden)
+    s_d = experts * _scale_bytes(hidden, inter)
     for t, need, what in ((gate, s_gu, "gate"), (up, s_gu, "up"), (down, s_d, "down")):
         s = t.scales
-        if not (s.dtype is torch.uint8 and s.get_device() == dev and s.numel() >= need
+        if not (s.dtype is torch.uint8 and s.numel() >= need and s.get_device() == dev
                 and s.is_contiguous()):
             _require_scales(s, need, what)
     if out is None:

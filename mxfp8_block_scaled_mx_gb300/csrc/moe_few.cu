@@ -483,12 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Routing: every block for itself, block 0 reports it.
   const float* logits = reinterpret_cast<const float*>(p.workspace + l.logits);
-  if (p.experts <= 64)
-    select_all<2, 4>(p, logits, kThreads / 32, sh);
-  else if (p.experts <= 128)
-    select_all<4, 4>(p, logits, kThreads / 32, sh);
+  constexpr int kWarps = kThreads / 32;
+  if (p.experts > 128)
+    select_all<kMaxExperts / 32, 1>(p, logits, kWarps, sh);
+  else if (p.tokens <= kWarps)
+    select_all<4, 1>(p, logits, kWarps, sh);
+  else if (p.tokens <= 2 * kWarps)
+    select_all<4, 2>(p, logits, kWarps, sh);
   else
-    select_all<kMaxExperts / 32, 1>(p, logits, kThreads / 32, sh);
+    select_all<4, 4>(p, logits, kWarps, sh);
   __syncthreads();
   if (warp == 2) {
     uint32_t before = 0;
@@ -520,6 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // (in both this role and the next the whole warp computes the operands and
+    // one elected lane issues: computed in a one-lane branch they cost more
+    // than the tile's transfer)
     const uint32_t tx_gu = kTileBytes * p.bits_gu / 8 + kSfBytes;
     const uint32_t tx_d = kTileBytes * p.bits_d / 8 + kSfBytes;
     int stage = 0;
@@ -536,92 +542,123 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_empty = [&] {
       return mbar_wait_warp(&sh->empty[stage], phase ^ 1u, s_abort, p.status, p.wait_limit_ns);
     };
-    auto load_a = [&](const CUtensorMap* map, const uint8_t* sf, int32_t x, int32_t y) {
-      tma_load_2d(sA + stage * kTileBytes, map, &sh->full[stage], x, y);
-      bulk_load(sSf + stage * 2 * kSfBytes, sf, kSfBytes, &sh->full[stage]);
-    };
-    auto load_b = [&](int s, const uint8_t* record) {
-      bulk_load(sB + s * b_bytes, record, b_bytes, &sh->full[s]);
-      bulk_load(sSf + (s * 2 + 1) * kSfBytes, record + b_bytes, kSfBytes, &sh->full[s]);
-    };
     // phase 1: gate tile with x's record, then the up tile (same record)
     const int64_t mat1 = static_cast<int64_t>(it_count) * ht_count * kSfBytes;
     for (uint32_t u = share1.lo; u < share1.hi && ok;) {
       const Segment g = share1.at(u);
-      const int32_t e = sh->expert[g.item / it_count], tile = g.item % it_count;
+      const int32_t a = g.item / it_count;
+      const int32_t e = sh->expert[a], tile = g.item - a * it_count;
       const int32_t y = e * p.inter + tile * kTile;
-      for (int32_t k = g.k0; k < g.k1 && ok; ++k) {
-        const int64_t sf = e * mat1 + (static_cast<int64_t>(tile) * ht_count + k) * kSfBytes;
+      const int64_t sf0 = e * mat1 + (static_cast<int64_t>(tile) * ht_count + g.k0) * kSfBytes;
+      const uint8_t* gate_sf = p.gate_scales + sf0;
+      const uint8_t* up_sf = p.up_scales + sf0;
+      const uint8_t* record = p.workspace + l.x + g.k0 * record_bytes(pad);
+      int32_t x = g.k0 * kTile;
+      for (int32_t k = g.k0; k < g.k1; ++k) {
         if (!(ok = wait_empty())) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&sh->full[stage], tx_gu + tx_b);
-          load_a(&tmap_gate, p.gate_scales + sf, k * kTile, y);
-          load_b(stage, p.workspace + l.x + k * record_bytes(pad));
+        {
+          uint64_t* bar = &sh->full[stage];
+          uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_bytes;
+          uint8_t* sf_dst = sSf + stage * 2 * kSfBytes;
+          const uint8_t* record_sf = record + b_bytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, tx_gu + tx_b);
+            tma_load_2d(a_dst, &tmap_gate, bar, x, y);
+            bulk_load(sf_dst, gate_sf, kSfBytes, bar);
+            bulk_load(b_dst, record, b_bytes, bar);
+            bulk_load(sf_dst + kSfBytes, record_sf, kSfBytes, bar);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         next();
         if (!(ok = wait_empty())) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&sh->full[stage], tx_gu);
-          load_a(&tmap_up, p.up_scales + sf, k * kTile, y);
+        {
+          uint64_t* bar = &sh->full[stage];
+          uint8_t *a_dst = sA + stage * kTileBytes, *sf_dst = sSf + stage * 2 * kSfBytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, tx_gu);
+            tma_load_2d(a_dst, &tmap_up, bar, x, y);
+            bulk_load(sf_dst, up_sf, kSfBytes, bar);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         next();
+        gate_sf += kSfBytes;
+        up_sf += kSfBytes;
+        record += record_bytes(pad);
+        x += kTile;
       }
       u += g.k1 - g.k0;
     }
-    // phase 2: the weights of the first tiles may come before the
-    // activations are complete
+    // phase 2.  The tile at the front: item, k and k's expert (its place among
+    // the active) and tile.
     const int64_t mat2 = static_cast<int64_t>(ht_count) * it_count * kSfBytes;
-    auto record2 = [&](int32_t k) { return p.workspace + l.h + k * record_bytes(pad); };
-    // the tile at the front: item, k and k's expert and tile
-    Segment w = share2.at(share2.lo);
-    int32_t a = w.k0 / it_count, kt = w.k0 % it_count;
+    Segment w = share2.at(share2.lo);  // (a block without a share has nothing at the front)
+    int32_t a = w.k0 / it_count, kt = w.k0 - a * it_count;
+    int32_t e = share2.lo < share2.hi ? sh->expert[a] : 0;
     auto step = [&] {
-      if (++kt == it_count) {
-        kt = 0;
-        ++a;
-      }
-      if (++w.k0 == share2.per) {
+      if (++w.k0 == static_cast<int32_t>(share2.per)) {
         w.k0 = kt = a = 0;
         ++w.item;
+        e = sh->expert[0];
+      } else if (++kt == it_count) {
+        kt = 0;
+        e = sh->expert[++a];
       }
     };
-    auto load_down = [&] {
-      const int32_t e = sh->expert[a], item = w.item;
-      mbar_arrive_expect_tx(&sh->full[stage], tx_d + tx_b);
-      load_a(&tmap_down,
-             p.down_scales + e * mat2 + (static_cast<int64_t>(item) * it_count + kt) * kSfBytes,
-             kt * kTile, e * p.hidden + item * kTile);
+    auto load_tile = [&](bool with_record) {
+      uint64_t* bar = &sh->full[stage];
+      uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_bytes;
+      uint8_t* sf_dst = sSf + stage * 2 * kSfBytes;
+      const uint8_t* sf = p.down_scales + e * mat2 + (static_cast<int64_t>(w.item) * it_count + kt) * kSfBytes;
+      const uint8_t* record = p.workspace + l.h + w.k0 * record_bytes(pad);
+      const uint8_t* record_sf = record + b_bytes;
+      const int32_t x = kt * kTile, y = e * p.hidden + w.item * kTile;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, tx_d + tx_b);
+        tma_load_2d(a_dst, &tmap_down, bar, x, y);
+        bulk_load(sf_dst, sf, kSfBytes, bar);
+        if (with_record) {
+          bulk_load(b_dst, record, b_bytes, bar);
+          bulk_load(sf_dst + kSfBytes, record_sf, kSfBytes, bar);
+        }
+      }
+      __syncwarp();
     };
-    uint32_t u = share2.lo;  // (a block without a share has nothing at the front)
+    // The weights of the first tiles may come before the activations are
+    // complete; their records follow.
+    uint32_t u = share2.lo;
     const int first = stage;
+    const int32_t first_k = w.k0;
     int ahead = 0;
     for (; ok && ahead < stages && u < share2.hi; ++ahead, ++u) {
       if (!(ok = wait_empty())) break;
-      if (elect_one()) load_down();
-      __syncwarp();
+      load_tile(false);
       next();
       step();
     }
-    if (ahead > 0 || ok) {
+    if (ahead > 0) {
       const bool ready = wait_count(counters + kDoneWord, items1, s_abort, p.status, p.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ready) && ok;
       fence_proxy_async_global();
-    }
-    // (also after a wait gave up: every stage begun is completed)
-    for (int i = 0; i < ahead; ++i) {
-      const Segment g = share2.at(share2.lo + i);
-      if (elect_one()) load_b((first + i) % stages, record2(g.k0));
-      __syncwarp();
+      // (also after a wait gave up: every stage begun is completed)
+      for (int i = 0; i < ahead; ++i) {
+        const int s = first + i < stages ? first + i : first + i - stages;
+        const uint8_t* record =
+            p.workspace + l.h + (first_k + i) % static_cast<int32_t>(share2.per) * record_bytes(pad);
+        uint64_t* bar = &sh->full[s];
+        uint8_t *b_dst = sB + s * b_bytes, *sf_dst = sSf + (s * 2 + 1) * kSfBytes;
+        const uint8_t* record_sf = record + b_bytes;
+        if (elect_one()) {
+          bulk_load(b_dst, record, b_bytes, bar);
+          bulk_load(sf_dst, record_sf, kSfBytes, bar);
+        }
+        __syncwarp();
+      }
     }
     for (; ok && u < share2.hi; ++u) {
       if (!(ok = wait_empty())) break;
-      if (elect_one()) {
-        load_down();
-        load_b(stage, record2(w.k0));
-      }
-      __syncwarp();
+      load_tile(true);
       next();
       step();
     }
@@ -643,21 +680,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0, acc = 0, acc_phase = 0;
     bool ok = true;
-    // the tile in `stage` times the record in `b_stage`, into columns `d`
-    auto multiply = [&](int b_stage, uint32_t d, uint32_t idesc, uint32_t blocks, bool add) {
-      const uint32_t sf = sf_col0 + stage * 8u;
-      const uint32_t sfb = sf_col0 + b_stage * 8u + 4u;
-      const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
-      tc_cp_32x128b_warpx4(sf, sf_lo, kHiScale);
-      if (b_stage == stage) tc_cp_32x128b_warpx4(sf + 4u, sf_lo + (kSfBytes >> 4), kHiScale);
-      const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
-      const uint32_t b_lo = b_lo0 + b_stage * (b_bytes >> 4);
-#pragma unroll
-      for (uint32_t kb = 0; kb < 4; ++kb)
-        if (kb < blocks)
-          tc_mma_mxf8(d, a_lo + 2u * kb, kHiOperand, b_lo + 2u * kb, kHiOperand,
-                      idesc | kb << 4 | kb << 29, sf, sfb, add || kb > 0 ? 1u : 0u);
-    };
     auto wait_full = [&] {
       const bool got =
           mbar_wait_warp(&sh->full[stage], phase, s_abort, p.status, p.wait_limit_ns);
@@ -670,48 +692,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u;
       }
     };
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-      const Share& share = ph == 0 ? share1 : share2;
-      const uint32_t idesc = mxf8_idesc(ph == 0 ? p.type_gu : p.type_d, 0, kTile, kTerms * pad, 0, 0);
-      const int32_t k_blocks = ((ph == 0 ? p.hidden : p.inter) + 31) / 32;
-      for (uint32_t u = share.lo; u < share.hi && ok;) {
-        const Segment g = share.at(u);
-        if (!mbar_wait_warp(&sh->acc_empty[acc], acc_phase ^ 1u, s_abort, p.status,
-                            p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d = tmem + acc * acc_cols;
-        for (int32_t k = g.k0; k < g.k1; ++k) {
-          const int32_t kt = ph == 0 ? k : k % it_count;
-          const uint32_t blocks = k_blocks - kt * 4 < 4 ? k_blocks - kt * 4 : 4;
+    auto begin_item = [&] {
+      const bool got = mbar_wait_warp(&sh->acc_empty[acc], acc_phase ^ 1u, s_abort, p.status,
+                                      p.wait_limit_ns);
+      tc_fence_after_sync();
+      return got;
+    };
+    auto end_item = [&] {
+      uint64_t* bar = &sh->acc_full[acc];
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+      if (++acc == acc_sets) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    };
+    // the elected lane's part: the tile's blocks times the record's
+    auto multiply = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
+                        uint32_t sfb, uint32_t blocks, uint32_t add) {
+#pragma unroll
+      for (uint32_t kb = 0; kb < 4; ++kb)
+        if (kb < blocks)
+          tc_mma_mxf8(d, a_lo + 2u * kb, kHiOperand, b_lo + 2u * kb, kHiOperand,
+                      idesc | kb << 4 | kb << 29, sfa, sfb, kb > 0 ? 1u : add);
+    };
+    {
+      const uint32_t idesc = mxf8_idesc(p.type_gu, 0, kTile, kTerms * pad, 0, 0);
+      const uint32_t k_blocks = (p.hidden + 31) / 32;
+      for (uint32_t u = share1.lo; u < share1.hi && ok;) {
+        const Segment g = share1.at(u);
+        if (!(ok = begin_item())) break;
+        const uint32_t d = tmem + acc * acc_cols, d_up = d + kTerms * pad;
+        uint32_t add = 0;
+        for (int32_t k = g.k0; k < g.k1; ++k, add = 1) {
+          const uint32_t left = k_blocks - k * 4, blocks = left < 4 ? left : 4;
           if (!(ok = wait_full())) break;
+          const int gate_stage = stage;
+          const uint32_t sfa = sf_col0 + stage * 8u, sfb = sfa + 4u;
+          const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (b_bytes >> 4);
           if (elect_one()) {
-            multiply(stage, d, idesc, blocks, k > g.k0);
-            if (ph == 1) tc_commit(&sh->empty[stage]);
+            tc_cp_32x128b_warpx4(sfa, sf_lo, kHiScale);
+            tc_cp_32x128b_warpx4(sfb, sf_lo + (kSfBytes >> 4), kHiScale);
+            multiply(d, a_lo, b_lo, idesc, sfa, sfb, blocks, add);
           }
           __syncwarp();
-          const int b_stage = stage;
           next();
-          if (ph == 1) continue;
           if (!(ok = wait_full())) break;
+          const uint32_t up_sfa = sf_col0 + stage * 8u;
+          const uint32_t up_sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t up_lo = a_lo0 + stage * (kTileBytes >> 4);
+          uint64_t *empty0 = &sh->empty[gate_stage], *empty1 = &sh->empty[stage];
           if (elect_one()) {
-            multiply(b_stage, d + kTerms * pad, idesc, blocks, k > g.k0);
-            tc_commit(&sh->empty[b_stage]);
-            tc_commit(&sh->empty[stage]);
+            tc_cp_32x128b_warpx4(up_sfa, up_sf_lo, kHiScale);
+            multiply(d_up, up_lo, b_lo, idesc, up_sfa, sfb, blocks, add);
+            tc_commit(empty0);
+            tc_commit(empty1);
           }
           __syncwarp();
           next();
         }
         if (!ok) break;
-        if (elect_one()) tc_commit(&sh->acc_full[acc]);
-        __syncwarp();
+        end_item();
         u += g.k1 - g.k0;
-        if (++acc == acc_sets) {
-          acc = 0;
-          acc_phase ^= 1u;
+      }
+    }
+    {
+      const uint32_t idesc = mxf8_idesc(p.type_d, 0, kTile, kTerms * pad, 0, 0);
+      const uint32_t k_blocks = (p.inter + 31) / 32;
+      int32_t kt = share2.lo < share2.hi ? share2.at(share2.lo).k0 % it_count : 0;
+      for (uint32_t u = share2.lo; u < share2.hi && ok;) {
+        const Segment g = share2.at(u);
+        if (!(ok = begin_item())) break;
+        const uint32_t d = tmem + acc * acc_cols;
+        uint32_t add = 0;
+        for (int32_t k = g.k0; k < g.k1; ++k, add = 1) {
+          const uint32_t left = k_blocks - kt * 4, blocks = left < 4 ? left : 4;
+          if (!(ok = wait_full())) break;
+          const uint32_t sfa = sf_col0 + stage * 8u, sfb = sfa + 4u;
+          const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (b_bytes >> 4);
+          uint64_t* empty = &sh->empty[stage];
+          if (elect_one()) {
+            tc_cp_32x128b_warpx4(sfa, sf_lo, kHiScale);
+            tc_cp_32x128b_warpx4(sfb, sf_lo + (kSfBytes >> 4), kHiScale);
+            multiply(d, a_lo, b_lo, idesc, sfa, sfb, blocks, add);
+            tc_commit(empty);
+          }
+          __syncwarp();
+          next();
+          if (++kt == it_count) kt = 0;
         }
+        if (!ok) break;
+        end_item();
+        u += g.k1 - g.k0;
       }
     }
     if (elect_one()) {
@@ -827,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         held = true;
         if (!ok) break;
         const uint32_t d = t_lane + acc * acc_cols;
-        uint32_t hi[2 * kTokensAtOnce], lo[2 * kTokensAtOnce];
+        uint32_t hi[2 * kTokensAtOnce] = {}, lo[2 * kTokensAtOnce] = {};
 #pragma unroll
         for (int i = 0; i < 2 * kTokensAtOnce; ++i)
           if (want(i)) {
@@ -836,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_32x32b_x1(col, hi[i]);
             tmem_ld_32x32b_x1(col + pad, lo[i]);
           }
-        tmem_ld_wait();
+        tmem_ld_wait_for(hi, lo);
         if (!owner) {
 #pragma unroll
           for (int i = 0; i < 2 * kTokensAtOnce; ++i)
@@ -891,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hi[8], lo[8];
         tmem_ld_32x32b_x8(d, hi);
         tmem_ld_32x32b_x8(d + pad, lo);
-        tmem_ld_wait();
+        tmem_ld_wait_for(hi, lo);
         const int c = g.item * kTile + row;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

@@ -12,60 +12,80 @@ cudaError_t norm_backward_f32(const NormBackParams& p, bool vec, int64_t n, cuda
 
 namespace {
 
-constexpr int kSumCols = 32, kSumParts = 32;
+constexpr int kSumCols = 32, kSumParts = 32, kSumThreads = kSumCols * kSumParts;
 
-// Sums the blocks' parts: job 0 w_pre, job 1 w_post, then the gates whose rows
-// several blocks share.  A block takes 32 columns; 32 runs of consecutive
-// parts are summed in order side by side, then joined in order.
-__global__ void __launch_bounds__(kSumCols* kSumParts)
-    norm_backward_sum_kernel(const NormBackParams p, uint32_t n) {
+// What the sum kernel's blocks do: blocks [0, wide) take 32 columns of w_pre,
+// [wide, 2 wide) of w_post; then `gate_jobs` gates whose rows several blocks
+// share, each in `gate_tiles` blocks: of 32 columns too where a gate has many
+// parts, else of 1024, a thread each.
+struct SumPlan {
+  uint32_t wide, gate_jobs, gate_tiles;
+};
+SumPlan sum_plan(int64_t rows, int64_t cols, int64_t gates, int64_t n) {
+  SumPlan s;
+  s.wide = static_cast<uint32_t>((cols + kSumCols - 1) / kSumCols);
+  // (rows == gates: every gate has one row, and no part)
+  s.gate_jobs = static_cast<uint32_t>(gates == rows ? 0 : gates < n ? gates : n);
+  s.gate_tiles = n >= 16 * gates ? s.wide : static_cast<uint32_t>((cols + kSumThreads - 1) / kSumThreads);
+  return s;
+}
+
+// Sums the blocks' parts.  Where a block of threads takes 32 columns, 32 runs
+// of consecutive parts are summed in order side by side, then joined in order.
+__global__ void __launch_bounds__(kSumThreads)
+    norm_backward_sum_kernel(const NormBackParams p, uint32_t n, const SumPlan plan) {
   __shared__ float part[kSumParts][kSumCols + 1];
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t job = blockIdx.y;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kSumCols + threadIdx.x % kSumCols;
-  const uint32_t run = threadIdx.x / kSumCols;
   const RowShare share(static_cast<uint32_t>(p.rows), n);
-  uint32_t first = 0, count = n, group = 0, per = 0;
+  uint32_t first = 0, count = n, tile = blockIdx.x;
+  bool narrow = true;                                 // 32 columns a block
+  const float* src;
+  int64_t step = p.cols, start_of_first = 0;          // floats from part to part
   float* out;
-  if (job == 0) {
+  if (blockIdx.x < plan.wide) {
+    src = ws_pre(p, 0);
     out = p.d_w_pre;
-  } else if (job == 1) {
+  } else if (blockIdx.x < 2 * plan.wide) {
     if (!p.w_post) return;
+    tile -= plan.wide;
+    src = ws_post(p, n, 0);
     out = p.d_w_post;
   } else {
-    per = static_cast<uint32_t>(p.rows / p.gates);
+    const uint32_t job = (blockIdx.x - 2 * plan.wide) / plan.gate_tiles;
+    tile = blockIdx.x - 2 * plan.wide - job * plan.gate_tiles;
+    narrow = plan.gate_tiles == plan.wide;
+    const uint32_t per = static_cast<uint32_t>(p.rows / p.gates);
     // the gates themselves, or the gate at the start of each block's rows
-    group = p.gates <= n ? job - 2 : share.start(job - 1) / per;
+    const uint32_t group = p.gates <= n ? job : share.start(job + 1) / per;
     if (group >= p.gates) return;
     first = share.of(group * per);
     count = share.of((group + 1) * per - 1) - first + 1;
-    if (count == 1 || (p.gates > n && first != job - 2)) return;
+    if (count == 1 || (p.gates > n && first != job)) return;
+    // blocks after the first begin inside this gate: their first slot; the
+    // first block's is its last if it began in an earlier gate
+    src = ws_gate(p, n, 2 * static_cast<int64_t>(first));
+    step = 2 * p.cols;
+    start_of_first = share.start(first) < group * per ? p.cols : 0;
     out = p.d_gate + group * p.cols;
   }
+  if (!narrow) {
+    const int64_t col = static_cast<int64_t>(tile) * kSumThreads + threadIdx.x;
+    if (col >= p.cols) return;
+    float s = src[start_of_first + col];
+    for (uint32_t i = 1; i < count; ++i) s += src[i * step + col];
+    out[col] = s;
+    return;
+  }
+  const int64_t col = static_cast<int64_t>(tile) * kSumCols + threadIdx.x % kSumCols;
+  const uint32_t run = threadIdx.x / kSumCols;
   float s = 0.f;
   if (col < p.cols) {
-    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(count) * run / kSumParts);
+    uint32_t i = static_cast<uint32_t>(static_cast<uint64_t>(count) * run / kSumParts);
     const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(count) * (run + 1) / kSumParts);
-    const float* src;
-    int64_t step = p.cols;
-    if (job == 0) {
-      src = ws_pre(p, first);
-    } else if (job == 1) {
-      src = ws_post(p, n, first);
-    } else {
-      // blocks after the first begin inside this gate: their first slot
-      src = ws_gate(p, n, 2 * static_cast<int64_t>(first));
-      step = 2 * p.cols;
-    }
-    src += col;
-    if (job >= 2 && begin == 0 && end > 0 && share.start(first) < group * per) {
-      s = src[p.cols];
-      for (uint32_t i = 1; i < end; ++i) s += src[i * step];
-    } else {
+    if (i == 0 && end > 0) s = src[start_of_first + col], i = 1;
 #pragma unroll 8
-      for (uint32_t i = begin; i < end; ++i) s += src[i * step];
-    }
+    for (; i < end; ++i) s += src[i * step + col];
   }
   part[run][threadIdx.x % kSumCols] = s;
   __syncthreads();
@@ -79,14 +99,12 @@ __global__ void __launch_bounds__(kSumCols* kSumParts)
 }  // namespace
 
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
-  int fit = 1;  // the most that any types and alignment have
+  int64_t n = 0;  // the most blocks that any types and alignment have
   for (int i = 0; i < 8; ++i) {
-    if ((i & 4) && cols > kRunsMaxCols) break;
-    const int f = backward_plan(cols, i & 1, i & 2, i & 4).fit;
-    fit = f > fit ? f : fit;
+    const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, i & 1, i & 2, i & 4));
+    n = m > n ? m : n;
   }
-  return static_cast<size_t>(backward_blocks(rows, kMaxSms, fit)) * (gates > 0 ? 4 : 2) *
-         static_cast<size_t>(cols) * 4;
+  return static_cast<size_t>(n) * (gates > 0 ? 4 : 2) * static_cast<size_t>(cols) * 4;
 }
 
 cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t stream) {
@@ -111,13 +129,12 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
     return err;
   }
   const int64_t ce = p.c_fp32 ? 4 : 8, se = p.s_fp32 ? 4 : 8;
-  const bool vec = p.cols % 8 == 0 && p.cols <= kRunsMaxCols && aligned16(p.d_res) && aligned16(p.dy) &&
-                   aligned16(p.block) && aligned16(p.res_out) && aligned16(p.w_post) &&
+  const bool vec = p.cols % 8 == 0 && aligned16(p.d_res) && aligned16(p.dy) && aligned16(p.block) && aligned16(p.res_out) && aligned16(p.w_post) &&
                    aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
                    aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&
                    p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 && p.lddr % se == 0;
   const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec);
-  const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan.fit);
+  const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan);
   cudaError_t err;
   if (p.c_fp32)
     err = norm_backward_f32(p, vec, n, stream);
@@ -126,11 +143,10 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
   else
     err = norm_backward_of<bf16, bf16>(p, vec, n, stream);
   if (err != cudaSuccess) return err;
-  const int64_t jobs = 2 + (p.gates < n ? p.gates : n);
+  const SumPlan sum = sum_plan(p.rows, p.cols, p.gates, n);
   return launch(norm_backward_sum_kernel,
-                dim3(static_cast<unsigned>((p.cols + kSumCols - 1) / kSumCols),
-                     static_cast<unsigned>(jobs)),
-                kSumCols * kSumParts, 0, stream, p, static_cast<uint32_t>(n));
+                dim3(2 * sum.wide + sum.gate_jobs * sum.gate_tiles), kSumThreads, 0, stream, p,
+                static_cast<uint32_t>(n), sum);
 }
 
 }  // namespace mx

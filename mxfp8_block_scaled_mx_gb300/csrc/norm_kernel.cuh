@@ -381,41 +381,49 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 // they stay across the row's one barrier, behind which the next copy starts.
 // A thread also keeps the sums of its columns over the rows.  The weights (from
 // L1) are asked for before the wait for the row, where registers hold them
-// that long.  MANY: more gates than one.
-template <typename C, typename S, typename W, Mode M, int NV, bool MANY>
+// that long.  MANY: more gates than one.  CL: blocks of a cluster that share a
+// row (two for rows longer than a block's registers hold, exchanging sums
+// through distributed shared memory).
+template <typename C, typename S, typename W, Mode M, int NV, bool MANY, int CL>
 __global__ void __launch_bounds__(kBackThreads)
     norm_backward_kernel(const NormBackParams p, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float part[2][kMaxWarps / 2 * 8];
+  __shared__ float part[2][CL * kBackThreads / 32 * 8];
   __shared__ uint64_t full[8];
   __shared__ uint32_t abort_word;
   volatile uint32_t* s_abort = &abort_word;
-  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                  static_cast<int32_t>(blockDim.x)};
+  // this block's columns: all, or its half in a cluster of two
+  const uint32_t rank = CL == 1 ? 0u : cluster_ctarank();
+  const int32_t width = static_cast<int32_t>(p.cols);
+  const int32_t half = CL == 1 ? width : (width / 8 + 1) / 2 * 8;
+  const int32_t off = rank * half, mine = rank == 0 ? half : width - half;
+  const Cols<M> c{mine, static_cast<int32_t>(threadIdx.x), static_cast<int32_t>(blockDim.x)};
   const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const uint32_t n = gridDim.x, me = blockIdx.x, lane = lane_id();
+  const uint32_t n = gridDim.x / CL, me = blockIdx.x / CL, lane = lane_id();
   const RowShare share(static_cast<uint32_t>(p.rows), n);
   const uint32_t lo = share.start(me), hi = share.start(me + 1);
-  const uint32_t cbytes = static_cast<uint32_t>(p.cols * sizeof(C));
-  const uint32_t sbytes = static_cast<uint32_t>(p.cols * sizeof(S));
+  const uint32_t cbytes = mine * sizeof(C), sbytes = mine * sizeof(S);
   const uint32_t stage_bytes = 2 * cbytes + 2 * sbytes;
-  for (uint32_t i = threadIdx.x; i < kMaxWarps * 8; i += blockDim.x) part[0][i] = 0.f;
+  for (uint32_t i = threadIdx.x; i < CL * kBackThreads / 32 * 16; i += blockDim.x) part[0][i] = 0.f;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     abort_word = 0;
     fence_mbarrier_init();
   }
-  __syncthreads();
+  if constexpr (CL == 1)
+    __syncthreads();
+  else
+    cluster_sync();  // both blocks' sums are cleared before either adds to them
   pdl_wait();
   pdl_launch_dependents();
   auto issue = [&](uint32_t t, int s) {
     uint8_t* dst = smem + s * stage_bytes;
     mbar_arrive_expect_tx(&full[s], p.d_res ? stage_bytes : stage_bytes - sbytes);
-    bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy, cbytes, &full[s]);
-    bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb, cbytes, &full[s]);
-    bulk_load(dst + 2 * cbytes, static_cast<const S*>(p.res_out) + t * p.ldr, sbytes, &full[s]);
+    bulk_load(dst, static_cast<const C*>(p.dy) + t * p.lddy + off, cbytes, &full[s]);
+    bulk_load(dst + cbytes, static_cast<const C*>(p.block) + t * p.ldb + off, cbytes, &full[s]);
+    bulk_load(dst + 2 * cbytes, static_cast<const S*>(p.res_out) + t * p.ldr + off, sbytes, &full[s]);
     if (p.d_res)
-      bulk_load(dst + 2 * cbytes + sbytes, static_cast<const S*>(p.d_res) + t * p.ldd, sbytes,
+      bulk_load(dst + 2 * cbytes + sbytes, static_cast<const S*>(p.d_res) + t * p.ldd + off, sbytes,
                 &full[s]);
   };
   if (threadIdx.x == 0)
@@ -436,27 +444,27 @@ __global__ void __launch_bounds__(kBackThreads)
   int stage = 0;
   uint32_t phase = 0;
   for (uint32_t t = lo; t < hi; ++t) {
-    const int64_t goff = group * p.cols;
+    const int64_t goff = group * p.cols + off;
     Raw<S> x[NV], a[NV] = {};
     Raw<C> y[NV], b[NV];
     constexpr bool kAhead = NV == 1 || sizeof(W) == 2;
     Raw<W> w_pre[NV], w_post[NV] = {};
 #pragma unroll
     for (int v = 0; kAhead && v < NV; ++v) {
-      w_pre[v] = load8(static_cast<const W*>(p.w_pre), c, v);
-      if (p.w_post) w_post[v] = load8(static_cast<const W*>(p.w_post), c, v);
+      w_pre[v] = load8(static_cast<const W*>(p.w_pre) + off, c, v);
+      if (p.w_post) w_post[v] = load8(static_cast<const W*>(p.w_post) + off, c, v);
     }
     auto times_pre = [&](float2 (&f)[4], int v) {
       if constexpr (kAhead)
         times(f, w_pre[v]);
       else
-        times_w<W>(f, p.w_pre, 0, c, v);
+        times_w<W>(f, p.w_pre, off, c, v);
     };
     auto times_post = [&](float2 (&f)[4], int v) {
       if constexpr (kAhead)
         times(f, w_post[v]);
       else
-        times_w<W>(f, p.w_post, 0, c, v);
+        times_w<W>(f, p.w_post, off, c, v);
     };
     if (stages > 0) {
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
@@ -471,10 +479,10 @@ __global__ void __launch_bounds__(kBackThreads)
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        y[v] = load8<true>(static_cast<const C*>(p.dy) + t * p.lddy, c, v);
-        b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
-        x[v] = load8<true>(static_cast<const S*>(p.res_out) + t * p.ldr, c, v);
-        if (p.d_res) a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd, c, v);
+        y[v] = load8<true>(static_cast<const C*>(p.dy) + t * p.lddy + off, c, v);
+        b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb + off, c, v);
+        x[v] = load8<true>(static_cast<const S*>(p.res_out) + t * p.ldr + off, c, v);
+        if (p.d_res) a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd + off, c, v);
       }
     }
     float2 s2[kRowSums];
@@ -513,8 +521,18 @@ __global__ void __launch_bounds__(kBackThreads)
     for (int i = 0; i < kRowSums; ++i) sums[i] = s2[i].x + s2[i].y;
     sums[6] = sums[7] = 0.f;
     float s = warp_sum8(sums);
-    if ((lane & 3) == 0) part[t & 1][warp_id() * 8 + lane / 4] = s;
-    __syncthreads();
+    const uint32_t warps = blockDim.x / 32;
+    float* to = &part[t & 1][(rank * warps + warp_id()) * 8 + lane / 4];
+    if constexpr (CL == 1) {
+      if ((lane & 3) == 0) *to = s;
+      __syncthreads();
+    } else {
+      if ((lane & 3) == 0) {
+        store_cluster(to, 0, s);
+        store_cluster(to, 1, s);
+      }
+      cluster_sync();
+    }
     // past this barrier the row is in registers
     if (stages > 0) {
       if (threadIdx.x == 0 && t + stages < hi) issue(t + stages, stage);
@@ -525,8 +543,8 @@ __global__ void __launch_bounds__(kBackThreads)
     }
     s = 0.f;
 #pragma unroll
-    for (uint32_t w = 0; w < kMaxWarps / 2; w += 4)
-      if (w < blockDim.x / 32) s += part[t & 1][(w + lane / 8) * 8 + lane % 8];
+    for (uint32_t w = 0; w < CL * kBackThreads / 32; w += 4)
+      if (w < CL * warps) s += part[t & 1][(w + lane / 8) * 8 + lane % 8];
     s += __shfl_xor_sync(0xffffffffu, s, 8);
     s += __shfl_xor_sync(0xffffffffu, s, 16);
 #pragma unroll
@@ -551,25 +569,25 @@ __global__ void __launch_bounds__(kBackThreads)
         o[i] = mul2(alpha, d[i]);
         q[v][i] = fma2(d[i], mul2(b[v].get(i), sigma), q[v][i]);
       }
-      store8(static_cast<S*>(p.d_residual) + t * p.lddr, c, v, round8<S>(o));
+      store8(static_cast<S*>(p.d_residual) + t * p.lddr + off, c, v, round8<S>(o));
       if (p.gate) times_w<W>(d, p.gate, goff, c, v);
       if (p.w_post) {
         times_post(d, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = fma2(b[v].get(i), m, mul2(sigma, d[i]));
       }
-      store8(static_cast<C*>(p.d_block) + t * p.lddb, c, v, round8<C>(d));
+      store8(static_cast<C*>(p.d_block) + t * p.lddb + off, c, v, round8<C>(d));
     }
     if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
       if (p.gate) {
         const bool whole = group * per >= lo && left == 0;
-        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
+        float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1)) + off;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           float2 dg[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) dg[i] = q[v][i];
-          if (p.w_post) times_w<W>(dg, p.w_post, 0, c, v);
+          if (p.w_post) times_w<W>(dg, p.w_post, off, c, v);
           times_w<W>(q[v], p.gate, goff, c, v);
           Raw<float> out;
 #pragma unroll
@@ -597,17 +615,16 @@ __global__ void __launch_bounds__(kBackThreads)
     Raw<float> out;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out.f[i] = pre[v][i];
-    store8(ws_pre(p, me), c, v, out);
+    store8(ws_pre(p, me) + off, c, v, out);
     if (p.w_post) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) out.f[i] = MANY ? post[MANY ? v : 0][i] : q[v][i];
-      store8(ws_post(p, n, me), c, v, out);
+      store8(ws_post(p, n, me) + off, c, v, out);
     }
   }
 }
 
-// The gradient for rows that are not on 16-byte boundaries, or longer than a
-// block's registers hold: element by element,
+// The gradient for long rows that are not on 16-byte boundaries: element by element,
 // with the column sums of w_pre and D b sigma and the row's u in shared memory
 // (cols floats each).  Sums over finished gates (gates > 1) grow in the
 // workspace.  A thread goes through the same columns everywhere, so no two
@@ -789,49 +806,54 @@ cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t str
   return forward_runs<C, S, W, 4, 512>(p, num_sms, stream);
 }
 
-// Runs of eight columns that a thread holds in the gradient: as few as 512
-// threads allow (two at most, more do not fit its registers).
-int backward_runs(int64_t cols) { return cols <= 4096 ? 1 : 2; }
-constexpr int64_t kRunsMaxCols = 2 * 8 * kBackThreads;
-
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
 constexpr size_t kSmemBytes = 200 * 1024;  // of an SM, for rings and sums; L1 keeps the weights
 
-// How a gradient is run: threads of a block, blocks side by side on an SM,
-// rows of the ring, bytes of shared memory of a block.
+// How a gradient is run: runs of eight columns a thread holds (0: the kernel
+// that goes element by element), blocks that share a row, threads of a block,
+// rows on an SM side by side (clusters: on two), rows of the ring, bytes of
+// shared memory.
 struct BackPlan {
-  int threads, fit, stages;
+  int runs, cluster, threads, fit, stages;
   size_t smem;
 };
 BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec) {
   BackPlan p;
-  if (!vec) {  // by shared memory and 2048 threads
-    p.threads = cols <= 2048 ? static_cast<int>((cols + 127) / 128 * 32) : kBackThreads;
+  constexpr int64_t kOneRun = 8 * kBackThreads;
+  if (!vec && cols > kOneRun) {  // by shared memory
+    p.runs = 0, p.cluster = 1, p.stages = 0;
+    p.threads = kBackThreads;
     p.smem = static_cast<size_t>(cols) * 12;
     p.fit = static_cast<int>(kSmemBytes / p.smem);
-    const int by_threads = 2 * kBackThreads / p.threads;
-    p.fit = p.fit < by_threads ? p.fit : by_threads;
-    p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-    p.stages = 0;
+    p.fit = p.fit < 1 ? 1 : p.fit > 2 ? 2 : p.fit;
     return p;
   }
-  // by registers (128 a thread) and rings of three rows: one in each half of
-  // a step and one on its way
-  p.threads = row_threads(cols, backward_runs(cols));
-  const size_t stage = cols * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
+  // by registers (128 a thread) and rings of three rows; a thread holds two
+  // runs where a row takes more than 512
+  p.runs = cols <= kOneRun ? 1 : 2;
+  p.cluster = cols <= 2 * kOneRun ? 1 : 2;
+  const int64_t mine = p.cluster == 1 ? cols : (cols / 8 + 1) / 2 * 8;
+  p.threads = row_threads(mine, p.runs);
   p.fit = kBackThreads / p.threads;
-  const int by_smem = static_cast<int>(kSmemBytes / (3 * stage));
-  p.fit = p.fit < by_smem ? p.fit : by_smem;
-  p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-  const size_t rows = kSmemBytes / p.fit / stage;
-  p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
-  p.smem = p.stages * stage;
+  p.stages = 0;
+  p.smem = 0;
+  if (vec) {
+    const size_t stage = mine * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
+    const int by_smem = static_cast<int>(kSmemBytes / (3 * stage));
+    p.fit = p.fit < by_smem ? p.fit : by_smem;
+    p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
+    const size_t rows = kSmemBytes / p.fit / stage;
+    p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
+    p.smem = p.stages * stage;
+  }
+  p.fit = p.fit > 8 ? 8 : p.fit;
   return p;
 }
 
 // Blocks of the gradient: those that fit the SMs.
-int64_t backward_blocks(int64_t rows, int num_sms, int fit) {
-  const int64_t most = static_cast<int64_t>(num_sms) * fit;
+// (Blocks that share a row count as one.)
+int64_t backward_blocks(int64_t rows, int num_sms, const BackPlan& plan) {
+  const int64_t most = static_cast<int64_t>(num_sms / plan.cluster) * plan.fit;
   return rows < most ? rows : most;
 }
 
@@ -843,15 +865,26 @@ cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
   });
 }
 
-template <typename C, typename S, typename W, Mode M, int NV, bool MANY>
+template <typename C, typename S, typename W, Mode M, int NV, bool MANY, int CL>
 cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t n,
                           cudaStream_t stream) {
   static PerDeviceOnce setup;
-  auto kern = norm_backward_kernel<C, S, W, M, NV, MANY>;
+  auto kern = norm_backward_kernel<C, S, W, M, NV, MANY, CL>;
   const cudaError_t err = allow_smem(setup, kern);
   if (err != cudaSuccess) return err;
-  return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p,
-                plan.stages);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2] = {pdl_attribute()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(n * CL));
+  cfg.blockDim = dim3(plan.threads);
+  cfg.dynamicSmemBytes = plan.smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kern, p, plan.stages);
 }
 
 template <typename C, typename S>
@@ -864,22 +897,24 @@ cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64
   return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p);
 }
 
-template <typename C, typename S, typename W, int NV>
-cudaError_t backward_runs_of(const NormBackParams& p, const BackPlan& plan, int64_t n,
-                             cudaStream_t stream) {
-  if (p.gates > 1)
-    return whole(p.cols, NV) ? backward_impl<C, S, W, kWhole, NV, true>(p, plan, n, stream)
-                             : backward_impl<C, S, W, kRuns, NV, true>(p, plan, n, stream);
-  return whole(p.cols, NV) ? backward_impl<C, S, W, kWhole, NV, false>(p, plan, n, stream)
-                           : backward_impl<C, S, W, kRuns, NV, false>(p, plan, n, stream);
+template <typename C, typename S, typename W, bool MANY>
+cudaError_t backward_of(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
+                        cudaStream_t stream) {
+  if (!vec) return backward_impl<C, S, W, kSingle, 1, MANY, 1>(p, plan, n, stream);
+  if (plan.cluster == 2) return backward_impl<C, S, W, kRuns, 2, MANY, 2>(p, plan, n, stream);
+  if (plan.runs == 1)
+    return whole(p.cols, 1) ? backward_impl<C, S, W, kWhole, 1, MANY, 1>(p, plan, n, stream)
+                            : backward_impl<C, S, W, kRuns, 1, MANY, 1>(p, plan, n, stream);
+  return whole(p.cols, 2) ? backward_impl<C, S, W, kWhole, 2, MANY, 1>(p, plan, n, stream)
+                          : backward_impl<C, S, W, kRuns, 2, MANY, 1>(p, plan, n, stream);
 }
 
 template <typename C, typename S, typename W>
 cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
                      cudaStream_t stream) {
-  if (!vec) return backward_single<C, S>(p, plan, n, stream);
-  return backward_runs(p.cols) == 1 ? backward_runs_of<C, S, W, 1>(p, plan, n, stream)
-                                    : backward_runs_of<C, S, W, 2>(p, plan, n, stream);
+  if (plan.runs == 0) return backward_single<C, S>(p, plan, n, stream);
+  return p.gates > 1 ? backward_of<C, S, W, true>(p, vec, plan, n, stream)
+                     : backward_of<C, S, W, false>(p, vec, plan, n, stream);
 }
 
 }  // namespace

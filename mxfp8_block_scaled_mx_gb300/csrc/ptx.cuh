@@ -240,6 +240,11 @@ __device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
   return r;
 }
 
+// Store to the same shared-memory variable in block `rank` of the cluster.
+__device__ __forceinline__ void store_cluster(float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(p, rank)), "f"(v) : "memory");
+}
+
 // Arrive without memory-ordering semantics: for releasing tensor memory
 // that this thread finished reading with tcgen05.ld + tcgen05.wait::ld and
 // a tcgen05.fence::before_thread_sync.  A release arrive would also wait

@@ -130,6 +130,22 @@ def test_one_gate_per_sequence(mx, rows, gates, cols, post):
     check_backward(mx, d, 1.0)
 
 
+@pytest.mark.parametrize("cols", [8200, 9216, 12000, 16384])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_rows_longer_than_a_block_holds(mx, cols, c, s, w):
+    for rows, gates in ((160, 0), (9, 3), (7, 7)):
+        d = inputs(rows, cols, c, s, w, True, gates, seed=cols)
+        check_forward(mx, d, 0.5)
+        check_backward(mx, d, 0.5)
+
+
+@pytest.mark.parametrize("rows,gates", [(700, 350), (700, 700), (620, 1), (2000, 500)])
+@pytest.mark.parametrize("cols", [1104, 333])
+def test_many_gates_and_many_blocks(mx, rows, gates, cols):
+    """More gates than blocks, gates of one row, two gates to a block."""
+    check_backward(mx, inputs(rows, cols, BF16, BF16, BF16, True, gates, seed=gates), 1.0)
+
+
 @pytest.mark.parametrize("pad", [1, 3, 8, 24])
 @pytest.mark.parametrize("cols", [64, 1000])
 def test_rows_apart_and_off_16_bytes(mx, pad, cols):

@@ -1,19 +1,21 @@
 """MXFP8 training matmul for GB300: a thin Python binding over libmx.so.
 
-The binding only marshals arguments: every step of quantization and of the
-block-scaled GEMM runs in the CUDA kernels behind the C ABI declared in
-include/mx.h.  PyTorch supplies device memory and the current stream.
-There is no CPU fallback: calling any entry point without the built
-library raises.
+The binding only marshals arguments: every step of quantization, of the
+block-scaled GEMM and of the operators around it runs in the CUDA kernels
+behind the C ABI declared in include/mx.h.  PyTorch supplies device memory
+and the current stream.  There is no CPU fallback: calling any entry point
+without the built library raises.
 
 Low-level functions carry the C names (mx_quantize, mx_quantize_grouped,
 mx_gemm, mx_grouped_gemm, mx_device_status, ...) and take raw pointers;
 `quantize`, `quantize_grouped`, `gemm` and `grouped_gemm` wrap them for
-torch tensors.
+torch tensors, and `norm_residual`, `norm_residual_backward` and
+`moe_few_tokens` those of the operators around the products.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -21,6 +23,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmx.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 MX_OK = 0
 STATUS_NAMES = {0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_MISALIGNED",
@@ -533,97 +536,29 @@ def grouped_gemm_wgrad(a: MxTensor, offsets: torch.Tensor, b: MxTensor, total_to
 
 
 # The operators below are called for single tokens, where the host's share of
-# a call counts: each tensor is checked once, by one helper that also returns
-# what the C call needs of it.
+# a call counts: their checks, outputs, workspaces and C calls are in a C++
+# module, built with the library (csrc/binding.cpp).
 
-def _refuse(t, shape, dtypes, what: str, layout: str):
-    """Says what is wrong with an operand."""
-    want = f"{what} must be a {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)}"
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{want}, got {type(t).__name__}")
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{want}, got {t.dtype} {tuple(t.shape)}")
-    _on_current_device(t, what)
-    raise ValueError(f"{what} must be {layout}, got strides {t.stride()}")
+_binding = None
 
 
-def _rows_of(t, rows: int, cols: int, dtypes, dev: int, what: str) -> int:
-    """Leading dimension of a [rows, cols] operand with unit column stride whose
-    rows do not overlap (that of a single row is its length)."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (rows, cols)
-            and t.get_device() == dev):
-        ld, unit = t.stride()
-        if rows <= 1:
-            if unit == 1 or cols <= 1:
-                return cols
-        elif (unit == 1 or cols == 1) and ld >= cols:
-            return ld
-    _refuse(t, (rows, cols), dtypes, what, "row-major with unit column stride")
-
-
-def _dense(t, shape, dtypes, dev: int, what: str) -> int:
-    """Address of a contiguous operand."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
-            and t.get_device() == dev and t.is_contiguous()):
-        return t.data_ptr()
-    _refuse(t, shape, dtypes, what, "contiguous")
-
-
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Workspace of one call, kept by the allocator until `stream` is past it."""
-    t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if stream is not None and _stream(stream) != _stream():
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-        t.record_stream(stream)
-    return t
-
-
-def _workspace_ptr(t, need: int, dev: int) -> int:
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.get_device() == dev
-            and t.is_contiguous() and t.numel() >= need):
-        return t.data_ptr()
-    raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on the "
-                     "current CUDA device")
-
-
-def _norm_weights(rows: int, cols: int, w_pre, w_post, gate, dev: int):
-    """(w_post, w_pre, gate addresses, gates, dtype code) of the norm's weights,
-    which share one type; gates is 0 without a gate."""
-    w_type = getattr(w_pre, "dtype", None)
-    if w_type not in _X_DTYPE:
-        _refuse(w_pre, (cols,), tuple(_X_DTYPE), "w_pre", "contiguous")
-    kinds = (w_type,)
-    pre = _dense(w_pre, (cols,), kinds, dev, "w_pre")
-    post = None if w_post is None else _dense(w_post, (cols,), kinds, dev, "w_post")
-    if gate is None:
-        return post, pre, None, 0, _X_DTYPE[w_type]
-    shape = getattr(gate, "shape", ())
-    gates = shape[0] if len(shape) == 2 else 1
-    at = _dense(gate, (gates, cols) if len(shape) == 2 else (cols,), kinds, dev, "gate")
-    if gates < 1 or rows % gates:
-        raise ValueError(f"{rows} rows cannot be split evenly over {gates} gates")
-    return post, pre, at, gates, _X_DTYPE[w_type]
-
-
-def _block_rows(block):
-    if not isinstance(block, torch.Tensor) or block.dim() != 2:
-        raise ValueError("block must be a 2-D bf16 or fp32 tensor")
-    return block.shape
-
-
-def _empty(shape, like: torch.Tensor) -> torch.Tensor:
-    if like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty(shape, dtype=like.dtype, device=like.device)
-
-
-def _scale_bytes(rows: int, k: int) -> int:
-    """mx_scale_bytes without the call."""
-    return -(-rows // 128) * -(-k // 128) * 512
-
-
-_WIDE = tuple(_X_DTYPE)
+def _native():
+    """The tensor API's module, bound to the loaded library (raises if either
+    was not built)."""
+    global _binding
+    if _binding is None or _lib is None:
+        c = lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is not built; run `python -m mxfp8_block_scaled_mx_gb300.build`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            c.mx_norm_residual, c.mx_norm_residual_backward, c.mx_norm_residual_backward_workspace,
+            c.mx_moe_few_tokens, c.mx_moe_few_tokens_workspace)), torch.cuda.OutOfMemoryError)
+        _binding = module
+    return _binding
 
 
 def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tensor,
@@ -637,28 +572,11 @@ def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tens
     the block.  gate: [cols], or [gates, cols] with one gate per
     rows/gates consecutive rows.  w_pre, w_post and gate share one type.
     out_residual may be `residual` itself."""
-    rows, cols = _block_rows(block)
-    dev = torch.cuda.current_device()
-    ldb = _rows_of(block, rows, cols, _WIDE, dev, "block")
-    ldr = _rows_of(residual, rows, cols, _WIDE, dev, "residual")
-    post, pre, at, gates, w_code = _norm_weights(rows, cols, w_pre, w_post, gate, dev)
-    if out_residual is None:
-        out_residual, ldo = _empty((rows, cols), residual), cols
-    else:
-        ldo = _rows_of(out_residual, rows, cols, (residual.dtype,), dev, "out_residual")
-    if out is None:
-        out, ldy = _empty((rows, cols), block), cols
-    else:
-        ldy = _rows_of(out, rows, cols, (block.dtype,), dev, "out")
-    if rows == 0:
-        return out_residual, out
-    st = lib().mx_norm_residual(
-        rows, cols, block.data_ptr(), ldb, _X_DTYPE[block.dtype], residual.data_ptr(), ldr,
-        _X_DTYPE[residual.dtype], post, pre, at, gates, w_code, alpha, eps,
-        out_residual.data_ptr(), ldo, out.data_ptr(), ldy, _stream(stream))
-    if st:
-        raise MxError("mx_norm_residual", st)
-    return out_residual, out
+    r = _native().norm_residual(block, residual, w_pre, w_post, gate, alpha, eps, out_residual, out,
+                                None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_norm_residual", r)
+    return r
 
 
 @dataclass
@@ -682,40 +600,12 @@ def norm_residual_backward(d_residual: torch.Tensor | None, d_y: torch.Tensor, b
     The column sums run in a fixed order: the same inputs give the same bits.
     workspace: uint8, mx_norm_residual_backward_workspace(rows, cols, gates)
     bytes; allocated here when None."""
-    rows, cols = _block_rows(block)
-    dev = torch.cuda.current_device()
-    ldb = _rows_of(block, rows, cols, _WIDE, dev, "block")
-    ldr = _rows_of(residual, rows, cols, _WIDE, dev, "residual")
-    lddy = _rows_of(d_y, rows, cols, (block.dtype,), dev, "d_y")
-    ldd = cols
-    if d_residual is not None:
-        ldd = _rows_of(d_residual, rows, cols, (residual.dtype,), dev, "d_residual")
-    post, pre, at, gates, w_code = _norm_weights(rows, cols, w_pre, w_post, gate, dev)
-    c = lib()
-    need = c.mx_norm_residual_backward_workspace(rows, cols, gates)
-    if workspace is None:
-        workspace = _scratch(need, block.device, stream)
-    ws = _workspace_ptr(workspace, need, dev)
-    f32 = dict(dtype=torch.float32, device=block.device)
-    grads = NormResidualGrads(_empty((rows, cols), block), _empty((rows, cols), residual),
-                              torch.empty(cols, **f32),
-                              None if w_post is None else torch.empty(cols, **f32),
-                              None if gate is None else torch.empty(gate.shape, **f32))
-    empty = rows == 0  # such tensors have no address; any device address stands in, unused
-    st = c.mx_norm_residual_backward(
-        rows, cols, None if d_residual is None or empty else d_residual.data_ptr(), ldd,
-        ws if empty else d_y.data_ptr(), lddy, ws if empty else block.data_ptr(), ldb,
-        _X_DTYPE[block.dtype], ws if empty else residual.data_ptr(), ldr,
-        _X_DTYPE[residual.dtype], post, pre, at, gates, w_code, alpha, eps,
-        ws if empty else grads.block.data_ptr(), cols, ws if empty else grads.residual.data_ptr(),
-        cols, _ptr(grads.w_post), grads.w_pre.data_ptr(), _ptr(grads.gate), ws, workspace.numel(),
-        _stream(stream))
-    if st:
-        raise MxError("mx_norm_residual_backward", st)
-    return grads
-
-
-_CODES = (torch.uint8,)
+    r = _native().norm_residual_backward(d_residual, d_y, block, residual, w_pre, w_post, gate,
+                                         alpha, eps, workspace,
+                                         None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_norm_residual_backward", r)
+    return NormResidualGrads(*r)
 
 
 def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: MxTensor,
@@ -732,50 +622,16 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: Mx
     [tokens, top_k], weights fp32 [tokens, top_k]).  workspace: uint8,
     mx_moe_few_tokens_workspace(...) bytes, one call at a time; allocated
     here when None."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a 2-D tensor")
-    if not isinstance(router, torch.Tensor) or router.dim() != 2:
-        raise ValueError("router must be a 2-D tensor")
-    if gate.codes.dim() != 3 or gate.fmt != up.fmt:
-        raise ValueError("gate and up must be [experts, inter, hidden] codes of one format")
-    tokens, hidden = x.shape
-    experts, inter = router.shape[0], gate.codes.shape[1]
-    if not 1 <= top_k <= experts:
-        raise ValueError(f"top_k must be 1 to {experts}, got {top_k}")
-    dev = torch.cuda.current_device()
-    ldx = _rows_of(x, tokens, hidden, (torch.bfloat16,), dev, "x")
-    wr = _dense(router, (experts, hidden), _WIDE, dev, "router")
-    k_gu, k_d = storage_bytes(gate.fmt, hidden), storage_bytes(down.fmt, inter)
-    g = _dense(gate.codes, (experts, inter, k_gu), _CODES, dev, "gate codes")
-    u = _dense(up.codes, (experts, inter, k_gu), _CODES, dev, "up codes")
-    d = _dense(down.codes, (experts, hidden, k_d), _CODES, dev, "down codes")
-    c = lib()
-    s_gu = experts * _scale_bytes(inter, hidden)
-    s_d = experts * _scale_bytes(hidden, inter)
-    for t, need, what in ((gate, s_gu, "gate"), (up, s_gu, "up"), (down, s_d, "down")):
-        s = t.scales
-        if not (s.dtype is torch.uint8 and s.numel() >= need and s.get_device() == dev
-                and s.is_contiguous()):
-            _require_scales(s, need, what)
-    if out is None:
-        out, ldy = _empty((tokens, hidden), x), hidden
-    else:
-        ldy = _rows_of(out, tokens, hidden, (torch.bfloat16,), dev, "out")
-    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
-    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
-    if tokens > 0:
-        need = c.mx_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k)
-        if workspace is None:
-            workspace = _scratch(need, x.device, stream)
-        ws = _workspace_ptr(workspace, need, dev)
-        st = c.mx_moe_few_tokens(
-            tokens, hidden, inter, experts, top_k, x.data_ptr(), ldx, wr, _X_DTYPE[router.dtype],
-            g, gate.scales.data_ptr(), u, up.scales.data_ptr(), FMT[gate.fmt], d,
-            down.scales.data_ptr(), FMT[down.fmt], int(renormalize), out.data_ptr(), ldy,
-            ids.data_ptr(), weights.data_ptr(), ws, workspace.numel(), _stream(stream))
-        if st:
-            raise MxError("mx_moe_few_tokens", st)
-    return (out, ids, weights) if return_routing else out
+    if gate.fmt != up.fmt:
+        raise ValueError("gate and up must be of one format")
+    r = _native().moe_few_tokens(x, router, gate.codes, gate.scales, up.codes, up.scales,
+                                 FMT[gate.fmt], STORAGE_BITS.get(gate.fmt, 8), down.codes,
+                                 down.scales, FMT[down.fmt], STORAGE_BITS.get(down.fmt, 8), top_k,
+                                 renormalize, out, workspace,
+                                 None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_moe_few_tokens", r)
+    return r if return_routing else r[0]
 
 
 def device_status(stream=None) -> int:

@@ -1,8 +1,10 @@
-"""Build libmx.so (the C-ABI library) for sm_103a with nvcc, in-tree.
+"""Build libmx.so (the C-ABI library) for sm_103a with nvcc, and _binding.so
+(the block operators' tensor API) with g++, in-tree.
 
 Each .cu file is compiled in parallel, then linked into
-mxfp8_block_scaled_mx_gb300/libmx.so.  `python -m mxfp8_block_scaled_mx_gb300.build`
-runs it from the command line.
+mxfp8_block_scaled_mx_gb300/libmx.so; binding.cpp, against the installed torch,
+into mxfp8_block_scaled_mx_gb300/_binding.so.  `python -m
+mxfp8_block_scaled_mx_gb300.build` runs it from the command line.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmx.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -34,6 +38,21 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def binding_command(out: str):
+    """g++ command of the tensor API's module."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [INCLUDE, os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+                sysconfig.get_paths()["include"]]
+    abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *(f"-I{d}" for d in includes),
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", os.path.join(root, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
@@ -46,6 +65,11 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding = binding_command(BINDING + ".tmp")
+    if verbose:
+        print(" ".join(binding), flush=True)
+    procs.append((os.path.join(CSRC, "binding.cpp"),
+                  subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, proc in procs:
         out, _ = proc.communicate()
@@ -64,6 +88,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

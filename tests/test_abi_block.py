@@ -91,3 +91,28 @@ def test_moe_rejects_bad_arguments_on_the_host(mx):
     assert size(4, 256, 128, 4, 2) > 0
     assert size(65, 256, 128, 4, 2) == 0 and size(4, 250, 128, 4, 2) == 0
     assert size(4, 256, 128, 4, 5) == 0
+
+
+def test_tensor_api_refuses_host_tensors(mx, monkeypatch):
+    """Without a GPU too, and before anything is launched; without the built
+    module every call raises."""
+    import torch
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    w = torch.ones(128, dtype=torch.bfloat16)
+    codes = mx.MxTensor(torch.zeros(2, 128, 128, dtype=torch.uint8),
+                        torch.zeros(1024, dtype=torch.uint8), "e4m3")
+    calls = (lambda: mx.norm_residual(x, x, w), lambda: mx.norm_residual_backward(None, x, x, x, w),
+             lambda: mx.moe_few_tokens(x, torch.zeros(2, 128), codes, codes, codes, 1))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    for bad in (None, 3, [x]):
+        with pytest.raises(ValueError):
+            mx.norm_residual(bad, x, w)
+        with pytest.raises(ValueError):
+            mx.moe_few_tokens(bad, x, codes, codes, codes, 1)
+    monkeypatch.setattr(mx, "_binding", None)
+    monkeypatch.setattr(mx, "BINDING_PATH", "/nowhere/_binding.so")
+    for call in calls:
+        with pytest.raises(RuntimeError):
+            call()

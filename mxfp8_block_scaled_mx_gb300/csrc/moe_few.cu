@@ -30,7 +30,10 @@
 // order.  An item whose tiles fall to several blocks is the last of its first
 // block's share and the first of every other's, so the others leave their
 // part (FP32) and go on, and the first, when it gets there, adds the parts in
-// block order to its own: same inputs, same bits, and nobody waits long.
+// block order to its own: same inputs, same bits, and nobody waits long.  Parts
+// start as a NaN that no sum is written as (the router kernel sets them), so
+// a value is there once it is not that: no flag to wait for, which cost a
+// fence and two more trips to L2.
 // Between the phases blocks wait for all activations, with their rings
 // already full of down tiles.
 #include <cuda.h>
@@ -67,7 +70,9 @@ __host__ __device__ constexpr int64_t record_bytes(int pad) { return code_bytes(
 static_assert(kTerms * kMaxTokens <= kTile, "the scales of all rows in one tile");
 static_assert(2 * 192 + kMaxStages * 8 <= 512, "tensor memory: two sets and the scales");
 
-// Workspace: counters, logits, x's records, the activations' records, parts.
+// Workspace: the count of finished activation items (its first word), logits,
+// x's records, the activations' records, parts.  A block's part: gates and ups of one item of phase 1, then one item of phase 2.
+__host__ __device__ constexpr int64_t part_floats(int tokens) { return int64_t(3) * tokens * kTile; }
 struct Layout {
   int64_t logits, x, h, parts, bytes;
 };
@@ -80,11 +85,21 @@ __host__ __device__ inline Layout layout(int tokens, int64_t hidden, int64_t int
   l.x = l.logits + (int64_t(tokens) * experts * 4 + 255) / 256 * 256;
   l.h = l.x + tiles(hidden) * record_bytes(pad);
   l.parts = l.h + active * tiles(inter) * record_bytes(pad);
-  l.bytes = l.parts + int64_t(kMaxBlocks) * 2 * pad * kTile * 4;
+  l.bytes = l.parts + kMaxBlocks * part_floats(tokens) * 4;
   return l;
 }
-constexpr int kDoneWord = 2 * kMaxBlocks;  // after a count per block and phase
-static_assert((kDoneWord + 1) * 4 <= 4096, "counters");
+
+// What a part's word holds before its sum: a NaN that put_sum never writes.
+constexpr uint32_t kNoSum = 0xFFFFFFFFu;
+__device__ __forceinline__ void put_sum(float* p, float v) {
+  const uint32_t bits = v != v ? 0x7FC00000u : __float_as_uint(v);
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(bits) : "memory");
+}
+__device__ __forceinline__ uint32_t get_sum(const float* p) {
+  uint32_t bits;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(bits) : "l"(p) : "memory");
+  return bits;
+}
 
 // Byte of code k (0..127) of row t of a record.
 __device__ __forceinline__ uint32_t code_at(uint32_t t, uint32_t k) {
@@ -140,6 +155,7 @@ __device__ __forceinline__ void write_block(uint8_t* record, int pad, uint32_t t
 // ------------------------------------------------------------------ router and x
 
 constexpr int kRouterThreads = 256;
+constexpr uint32_t kClearUnits = 16 * kRouterThreads;  // of 16 bytes, per block
 constexpr int kRouterExperts = 2;   // per block, four warps each
 constexpr int kRouterTokens = 8;    // per block: the router's rows are read tokens / 8 times
 
@@ -190,18 +206,28 @@ __device__ __forceinline__ void dot_tokens(const MoeFewParams& p, int e, int t0,
     for (int i = 0; i < T; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
 }
 
-// Blocks [0, logit_blocks): logits of two experts for eight tokens.  The rest:
-// x's records, a warp per token and K tile.  Block 0 also clears the counters.
+// Blocks [0, logit_blocks): logits of two experts for eight tokens.  The next
+// record_blocks: x's records, a warp per token and K tile.  The rest: parts of
+// part_units 16-byte units in all set to kNoSum.  Block 0 also clears the counter.
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFewParams p,
-                                                                    int logit_blocks) {
+                                                                    int logit_blocks,
+                                                                    int record_blocks,
+                                                                    uint32_t part_units) {
   __shared__ float part[kRouterThreads / 32][kRouterTokens];
   pdl_wait();
   pdl_launch_dependents();
   const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
   const uint32_t warp = warp_id(), lane = lane_id();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= kDoneWord; i += kRouterThreads)
-      reinterpret_cast<uint32_t*>(p.workspace)[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint32_t*>(p.workspace) = 0;
+  if (static_cast<int>(blockIdx.x) >= logit_blocks + record_blocks) {
+    uint4* parts = reinterpret_cast<uint4*>(p.workspace + l.parts);
+    const uint4 none = make_uint4(kNoSum, kNoSum, kNoSum, kNoSum);
+    uint32_t i = (blockIdx.x - logit_blocks - record_blocks) * kClearUnits + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kClearUnits / kRouterThreads; ++j, i += kRouterThreads)
+      if (i < part_units) parts[i] = none;
+    return;
+  }
   if (static_cast<int>(blockIdx.x) >= logit_blocks) {
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
     const int kt_count = static_cast<int>(tiles(p.hidden));
@@ -451,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* s_abort = &sh->abort;
   const uint32_t warp = warp_id(), lane = lane_id();
   const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(p.workspace);
+  uint32_t* done_items = reinterpret_cast<uint32_t*>(p.workspace);
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -638,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       step();
     }
     if (ahead > 0) {
-      const bool ready = wait_count(counters + kDoneWord, items1, s_abort, p.status, p.wait_limit_ns);
+      const bool ready = wait_count(done_items, items1, s_abort, p.status, p.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ready) && ok;
       fence_proxy_async_global();
       // (also after a wait gave up: every stage begun is completed)
@@ -803,8 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = static_cast<int>(warp - 2) >> 2; // of an item's tokens
     const int row = static_cast<int>(q * 32 + lane);  // of the tile
     const int tid = static_cast<int>(threadIdx.x) - 64;
-    float* parts = reinterpret_cast<float*>(p.workspace + l.parts) + row;
-    const int64_t part_size = static_cast<int64_t>(2) * pad * kTile;
+    const int64_t part_size = part_floats(p.tokens);
+    float* parts1 = reinterpret_cast<float*>(p.workspace + l.parts) + row;
+    float* parts2 = parts1 + 2 * p.tokens * kTile;
     const uint32_t t_lane = tmem + (q * 32u << 16);
     uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
@@ -824,22 +851,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Sum of the parts of blocks c0 + 1 .. c1, in that order, of N values, the
-    // i-th `at(i)` floats into a part and wanted where want(i).
-    auto add_parts = [&](uint32_t c0, uint32_t c1, auto& v, auto want, auto at) {
+    // i-th `at(i)` floats into a part and wanted where want(i); waits for them
+    // to be there.
+    auto add_parts = [&](const float* parts, uint32_t c0, uint32_t c1, auto& v,
+                         auto want, auto at) {
       constexpr int N = sizeof(v) / sizeof(float);
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = 0.f;
       for (uint32_t c = c0 + 1; c <= c1; c += kPartsAtOnce) {
-        float r[kPartsAtOnce][N];
+        uint32_t r[kPartsAtOnce][N];
+        uint64_t begun = 0;
+        for (uint32_t spins = 0;; ++spins) {
+          bool missing = false;
+#pragma unroll
+          for (int b = 0; b < kPartsAtOnce; ++b)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              r[b][i] = c + b <= c1 && want(i) ? get_sum(parts + (c + b) * part_size + at(i)) : 0u;
+#pragma unroll
+          for (int b = 0; b < kPartsAtOnce; ++b)
+#pragma unroll
+            for (int i = 0; i < N; ++i) missing |= r[b][i] == kNoSum;
+          if (!__any_sync(0xffffffffu, missing)) break;
+          if (spins == 0) begun = global_timer_ns();
+          bool late = *s_abort != 0;
+          if (global_timer_ns() - begun > p.wait_limit_ns) {
+            record_device_status(p.status, MX_DEV_TIMEOUT);
+            *s_abort = 1u;
+            late = true;
+          }
+          if (__any_sync(0xffffffffu, late)) {
+            ok = false;
+            break;
+          }
+        }
 #pragma unroll
         for (int b = 0; b < kPartsAtOnce; ++b)
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            r[b][i] = c + b <= c1 && want(i) ? __ldcg(parts + (c + b) * part_size + at(i)) : 0.f;
-#pragma unroll
-        for (int b = 0; b < kPartsAtOnce; ++b)
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[i] += r[b][i];
+          for (int i = 0; i < N; ++i) v[i] += __uint_as_float(r[b][i]);
       }
     };
 
@@ -869,10 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh->share[buf][place] = w;
         }
       }
-      if (owner && c1 > c0 && tid == 0)
-        wait_count(counters + c0, c1 - c0, s_abort, p.status, p.wait_limit_ns);
       epi_sync();
-      if (*s_abort) ok = false;
       const uint32_t low = __popc(sh->routed[buf][0]);
       const int count = static_cast<int>(low + __popc(sh->routed[buf][1]));
       const int i_begin = half == 0 ? 0 : (count + 1) / 2;
@@ -896,9 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i0 = i_begin; i0 < i_end; i0 += kTokensAtOnce) {
         float v[2 * kTokensAtOnce];                   // gates, then ups
         auto want = [&](int i) { return i0 + i % kTokensAtOnce < i_end; };
-        auto at = [&](int i) { return (i / kTokensAtOnce * pad + i0 + i % kTokensAtOnce) * kTile; };
-        if (owner && ok)
-          add_parts(c0, c1, v, want, at);
+        auto at = [&](int i) { return (i / kTokensAtOnce * p.tokens + i0 + i % kTokensAtOnce) * kTile; };
+        if (owner && ok) add_parts(parts1, c0, c1, v, want, at);
         if (!held) wait_acc();
         held = true;
         if (!ok) break;
@@ -917,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2 * kTokensAtOnce; ++i)
             if (want(i))
-              parts[blockIdx.x * part_size + at(i)] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+              put_sum(parts1 + blockIdx.x * part_size + at(i), __uint_as_float(hi[i]) + __uint_as_float(lo[i]));
           continue;
         }
 #pragma unroll
@@ -933,10 +978,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!held) wait_acc();
       release_acc();
-      // an owner's records are for every block's copies
-      if (owner) fence_proxy_async_global();
-      epi_sync();
-      if (tid == 0) add_release(owner ? counters + kDoneWord : counters + c0);
+      if (owner) {
+        // its records are for every block's copies
+        fence_proxy_async_global();
+        epi_sync();
+        if (tid == 0) add_release(done_items);
+      }
     }
 
     // phase 2: 128 channels of y, for all tokens
@@ -948,18 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t u0 = g.item * share2.per;
       const uint32_t c0 = share2.block_of(u0), c1 = share2.block_of(u0 + share2.per - 1);
       const bool owner = g.k0 == 0;
-      if (owner && c1 > c0) {
-        if (tid == 0)
-          wait_count(counters + kMaxBlocks + c0, c1 - c0, s_abort, p.status, p.wait_limit_ns);
-        epi_sync();
-        if (*s_abort) ok = false;
-      }
       bool held = false;
       for (int t = t_begin; t < t_end; t += 8) {
         float v[8];
         auto want = [&](int i) { return t + i < t_end; };
         auto at = [&](int i) { return (t + i) * kTile; };
-        if (owner && ok) add_parts(c0, c1, v, want, at);
+        if (owner && ok) add_parts(parts2, c0, c1, v, want, at);
         if (!held) wait_acc();
         held = true;
         if (!ok) break;
@@ -974,17 +1015,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!want(i)) break;
           const float own = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
           if (!owner)
-            parts[blockIdx.x * part_size + at(i)] = own;
+            put_sum(parts2 + blockIdx.x * part_size + at(i), own);
           else if (c < p.hidden)
             static_cast<__nv_bfloat16*>(p.y)[(t + i) * p.ldy + c] = __float2bfloat16_rn(v[i] + own);
         }
       }
       if (!held) wait_acc();
       release_acc();
-      if (!owner) {
-        epi_sync();
-        if (tid == 0) add_release(counters + kMaxBlocks + c0);
-      }
     }
   }
 
@@ -1015,19 +1052,22 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
                                 static_cast<int>(kSmemMax));
   });
   if (err != cudaSuccess) return err;
+  const int blocks = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
   {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     const int logit_blocks = (p.experts + kRouterExperts - 1) / kRouterExperts *
                              ((p.tokens + kRouterTokens - 1) / kRouterTokens);
-    const int64_t warps = static_cast<int64_t>(p.tokens) * tiles(p.hidden);
-    cfg.gridDim = dim3(static_cast<unsigned>(logit_blocks + (warps + kRouterThreads / 32 - 1) /
-                                                                (kRouterThreads / 32)));
+    const int record_blocks = static_cast<int>(
+        (p.tokens * tiles(p.hidden) + kRouterThreads / 32 - 1) / (kRouterThreads / 32));
+    const uint32_t units = static_cast<uint32_t>(blocks * part_floats(p.tokens) / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>(logit_blocks + record_blocks) +
+                       (units + kClearUnits - 1) / kClearUnits);
     cfg.blockDim = dim3(kRouterThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, moe_router_kernel, p, logit_blocks);
+    err = cudaLaunchKernelEx(&cfg, moe_router_kernel, p, logit_blocks, record_blocks, units);
     if (err != cudaSuccess) return err;
   }
   const int pad = pad_tokens(p.tokens);
@@ -1039,7 +1079,7 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
   attr[0].id = cudaLaunchAttributeCooperative;  // the blocks wait for one another
   attr[0].val.cooperative = 1;
   attr[1] = pdl_attribute();
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms < kMaxBlocks ? num_sms : kMaxBlocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = stages * stage + sizeof(Shared) + 1024;
   cfg.stream = stream;

@@ -308,91 +308,61 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// A warp chooses the winners of tokens t0, t0 + step, ... (P of them side by
-// side, N logits a lane each): largest logit first, the lowest expert among
-// equal ones.
-template <int N, int P>
-__device__ __forceinline__ void select_tokens(const MoeFewParams& p, const float* logits, int t0,
-                                              int step, Shared* sh) {
+// A warp chooses the winners of token t (N logits a lane): largest logit
+// first, the lowest expert among equal ones.
+template <int N>
+__device__ __forceinline__ void select_experts(const MoeFewParams& p, const float* logits, int t,
+                                               Shared* sh) {
   const uint32_t lane = lane_id();
-  float z[P][N];
-  uint32_t key[P][N];
+  float z[N];
+  uint32_t key[N], top = 0u;
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int t = t0 + i * step, e = j * 32 + static_cast<int>(lane);
-      z[i][j] = t < p.tokens && e < p.experts ? logits[t * p.experts + e] : -INFINITY;
-    }
-  float sum[P], chosen[P], my_w[P];
-  uint32_t my_e[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    uint32_t top = 0u;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      key[i][j] = j * 32 + static_cast<int>(lane) < p.experts ? logit_key(z[i][j]) : 0u;
-      top = key[i][j] > top ? key[i][j] : top;
-    }
-    const float z0 = key_logit(__reduce_max_sync(0xffffffffu, top));
-    sum[i] = chosen[i] = my_w[i] = 0.f;
-    my_e[i] = 0u;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      z[i][j] = key[i][j] ? expf(z[i][j] - z0) : 0.f;
-      sum[i] += z[i][j];
-    }
+  for (int j = 0; j < N; ++j) {
+    const int e = j * 32 + static_cast<int>(lane);
+    z[j] = e < p.experts ? logits[t * p.experts + e] : -INFINITY;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int j = 0; j < N; ++j) {
+    key[j] = j * 32 + static_cast<int>(lane) < p.experts ? logit_key(z[j]) : 0u;
+    top = key[j] > top ? key[j] : top;
+  }
+  const float z0 = key_logit(__reduce_max_sync(0xffffffffu, top));
+  float sum = 0.f, chosen = 0.f, my_w = 0.f;
+  uint32_t my_e = 0u;
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+  for (int j = 0; j < N; ++j) {
+    z[j] = key[j] ? expf(z[j] - z0) : 0.f;
+    sum += z[j];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   for (int k = 0; k < p.top_k; ++k) {
-    uint32_t best[P], at[P];
-    float w[P];
+    uint32_t best = 0u, at = 0xFFFFFFFFu;
+    float w = 0.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      best[i] = 0u, at[i] = 0xFFFFFFFFu, w[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (key[i][j] > best[i]) {
-          best[i] = key[i][j];
-          at[i] = j * 32 + lane;
-          w[i] = z[i][j];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, best[i]);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, best[i] == m ? at[i] : 0xFFFFFFFFu);
-      w[i] = __shfl_sync(0xffffffffu, w[i], e & 31u);
-      chosen[i] += w[i];
-      if (lane == static_cast<uint32_t>(k)) {
-        my_e[i] = e;
-        my_w[i] = w[i];
+    for (int j = 0; j < N; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j * 32 + lane;
+        w = z[j];
       }
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (e == j * 32 + lane) key[i][j] = 0u;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
+    w = __shfl_sync(0xffffffffu, w, e & 31u);
+    chosen += w;
+    if (lane == static_cast<uint32_t>(k)) {
+      my_e = e;
+      my_w = w;
     }
-  }
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int t = t0 + i * step;
-    if (t < p.tokens && static_cast<int>(lane) < p.top_k) {
-      sh->id[t * p.top_k + lane] = static_cast<uint16_t>(my_e[i]);
-      sh->weight[t * p.top_k + lane] = my_w[i] / (p.renormalize ? chosen[i] : sum[i]);
-      atomicOr(&sh->chosen[my_e[i] >> 5], 1u << (my_e[i] & 31u));
-    }
+    for (int j = 0; j < N; ++j)
+      if (e == j * 32 + lane) key[j] = 0u;
   }
-}
-
-// All tokens, over the block's warps.
-template <int N, int P>
-__device__ __forceinline__ void select_all(const MoeFewParams& p, const float* logits, int warps,
-                                           Shared* sh) {
-  for (int t = warp_id(); t < p.tokens; t += P * warps)
-    select_tokens<N, P>(p, logits, t, warps, sh);
+  if (static_cast<int>(lane) < p.top_k) {
+    sh->id[t * p.top_k + lane] = static_cast<uint16_t>(my_e);
+    sh->weight[t * p.top_k + lane] = my_w / (p.renormalize ? chosen : sum);
+    atomicOr(&sh->chosen[my_e >> 5], 1u << (my_e & 31u));
+  }
 }
 
 // A block's run of tiles of one item.
@@ -509,15 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Routing: every block for itself, block 0 reports it.
   const float* logits = reinterpret_cast<const float*>(p.workspace + l.logits);
-  constexpr int kWarps = kThreads / 32;
-  if (p.experts > 128)
-    select_all<kMaxExperts / 32, 1>(p, logits, kWarps, sh);
-  else if (p.tokens <= kWarps)
-    select_all<4, 1>(p, logits, kWarps, sh);
-  else if (p.tokens <= 2 * kWarps)
-    select_all<4, 2>(p, logits, kWarps, sh);
-  else
-    select_all<4, 4>(p, logits, kWarps, sh);
+  for (int t = static_cast<int>(warp); t < p.tokens; t += kThreads / 32) {
+    if (p.experts <= 128)
+      select_experts<4>(p, logits, t, sh);
+    else
+      select_experts<kMaxExperts / 32>(p, logits, t, sh);
+  }
   __syncthreads();
   if (warp == 2) {
     uint32_t before = 0;

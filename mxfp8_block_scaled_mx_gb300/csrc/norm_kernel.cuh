@@ -24,6 +24,12 @@
 #include "ptx.cuh"
 
 namespace mx {
+
+// What the forward pass's arrays allow: 16-byte accesses from each row's first
+// column on; from the same column of a row on in all of them (rows of an odd
+// length); neither.
+enum class NormRows { kAligned, kShifted, kAny };
+
 namespace {
 
 using bf16 = __nv_bfloat16;
@@ -75,17 +81,26 @@ __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 // kWhole  run v is columns 8 (v threads + tid) ..+7, 16 bytes an access, and
 //         the row has exactly 8 NV threads columns;
 // kRuns   the same with an end inside (whole runs of eight);
+// kShift  run v is columns 8 (v threads + tid) - phase ..+7, with the row's phase
+//         (0..7) such that its runs lie on 16 bytes; first and last may be cut;
 // kSingle element j of run v is column (8 v + j) threads + tid, one at a time.
-enum Mode { kWhole, kRuns, kSingle };
+enum Mode { kWhole, kRuns, kShift, kSingle };
 
 template <Mode M>
 struct Cols {
-  int32_t cols, tid, threads;
+  int32_t cols, tid, threads, phase = 0;
   __device__ __forceinline__ int32_t at(int v, int j) const {
-    return M == kSingle ? (8 * v + j) * threads + tid : 8 * (v * threads + tid) + j;
+    return M == kSingle  ? (8 * v + j) * threads + tid
+           : M == kShift ? 8 * (v * threads + tid) - phase + j
+                         : 8 * (v * threads + tid) + j;
   }
   __device__ __forceinline__ bool has(int v, int j) const {
-    return M == kWhole || at(v, M == kRuns ? 0 : j) < cols;
+    return M == kWhole || (M == kShift ? static_cast<uint32_t>(at(v, j)) < static_cast<uint32_t>(cols)
+                                       : at(v, M == kRuns ? 0 : j) < cols);
+  }
+  // run v lies inside the row, with `margin` columns to spare on either side
+  __device__ __forceinline__ bool inside(int v, int margin = 0) const {
+    return at(v, 0) >= margin && at(v, 0) + 8 + margin <= cols;
   }
 };
 
@@ -115,37 +130,77 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
   return v;
 }
 
-// Run v of a row; elements past its end read as zero.  ONCE: a row of global
+// Run v of a row; elements past its ends read as zero.  ONCE: a row of global
 // memory that is not read again.
-template <bool ONCE = false, typename T, Mode M>
-__device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
+template <typename T, Mode M>
+__device__ __forceinline__ Raw<T> load8_singly(const T* row, const Cols<M>& c, int v) {
   Raw<T> r;
-  if constexpr (M == kSingle) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool a = c.has(v, 2 * i), b = c.has(v, 2 * i + 1);
-      if constexpr (sizeof(T) == 2)
-        r.w[i] = (a ? bits(row[c.at(v, 2 * i)]) : 0u) | (b ? bits(row[c.at(v, 2 * i + 1)]) << 16 : 0u);
-      else
-        r.f[i] = make_float2(a ? row[c.at(v, 2 * i)] : 0.f, b ? row[c.at(v, 2 * i + 1)] : 0.f);
-    }
-  } else {
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (c.has(v, 0)) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
-      x = ONCE ? load_once(p) : p[0];
-      if constexpr (sizeof(T) == 4) y = ONCE ? load_once(p + 1) : p[1];
-    }
-    if constexpr (sizeof(T) == 2) {
-      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-    } else {
-      r.f[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-      r.f[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
-      r.f[2] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
-      r.f[3] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
-    }
+  for (int i = 0; i < 4; ++i) {
+    const bool a = c.has(v, 2 * i), b = c.has(v, 2 * i + 1);
+    if constexpr (sizeof(T) == 2)
+      r.w[i] = (a ? bits(row[c.at(v, 2 * i)]) : 0u) | (b ? bits(row[c.at(v, 2 * i + 1)]) << 16 : 0u);
+    else
+      r.f[i] = make_float2(a ? row[c.at(v, 2 * i)] : 0.f, b ? row[c.at(v, 2 * i + 1)] : 0.f);
   }
   return r;
+}
+template <bool ONCE = false, typename T, Mode M>
+__device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
+  if constexpr (M == kSingle) return load8_singly(row, c, v);
+  if constexpr (M == kShift)
+    if (!c.inside(v)) return load8_singly(row, c, v);
+  Raw<T> r;
+  uint4 x = make_uint4(0, 0, 0, 0), y = x;
+  if (M == kShift || c.has(v, 0)) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
+    x = ONCE ? load_once(p) : p[0];
+    if constexpr (sizeof(T) == 4) y = ONCE ? load_once(p + 1) : p[1];
+  }
+  if constexpr (sizeof(T) == 2) {
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+  } else {
+    r.f[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+    r.f[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+    r.f[2] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
+    r.f[3] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
+  }
+  return r;
+}
+
+// Run v of a weight or gate.  Under kShift it lies anywhere: the 16-byte
+// pieces that hold it (inside the row wherever this is done), then the words
+// moved into place.
+template <typename T, Mode M>
+__device__ __forceinline__ Raw<T> load8_weight(const T* row, const Cols<M>& c, int v) {
+  if constexpr (M != kShift) {
+    return load8(row, c, v);
+  } else {
+    if (!c.inside(v, 8)) return load8_singly(row, c, v);
+    constexpr int N = sizeof(T) * 2 + 4;                 // words of the pieces
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + c.at(v, 0));
+    const uint4* p = reinterpret_cast<const uint4*>(a & ~uintptr_t(15));
+    uint32_t w[N];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = p[i];
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
+    const uint32_t by = static_cast<uint32_t>(a) & 15u;  // bytes
+#pragma unroll
+    for (int i = 0; i + 2 < N; ++i) w[i] = by & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) w[i] = by & 4u ? w[i + 1] : w[i];
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2)
+        r.w[i] = __funnelshift_r(w[i], w[i + 1], by & 2u ? 16u : 0u);
+      else
+        r.f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    return r;
+  }
 }
 
 // f *= a run.
@@ -158,12 +213,12 @@ __device__ __forceinline__ void times(float2 (&f)[4], const Raw<T>& r) {
 template <typename W, Mode M>
 __device__ __forceinline__ void times_w(float2 (&f)[4], const void* w, int64_t off,
                                         const Cols<M>& c, int v) {
-  times(f, load8(static_cast<const W*>(w) + off, c, v));
+  times(f, load8_weight(static_cast<const W*>(w) + off, c, v));
 }
 
 template <typename T, Mode M>
 __device__ __forceinline__ void store8(T* row, const Cols<M>& c, int v, const Raw<T>& r) {
-  if constexpr (M == kSingle) {
+  if (M == kSingle || (M == kShift && !c.inside(v))) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (c.has(v, j)) {
@@ -254,29 +309,34 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
-                  static_cast<int32_t>(blockDim.x)};
+  Cols<M> c{static_cast<int32_t>(p.cols), static_cast<int32_t>(threadIdx.x),
+            static_cast<int32_t>(blockDim.x)};
   const float inv_cols = 1.f / static_cast<float>(p.cols);
   const float2 alpha = both(p.alpha);
   const uint32_t rows = static_cast<uint32_t>(p.rows);
   const uint32_t per = p.gate ? rows / static_cast<uint32_t>(p.gates) : 1u;
   Raw<C> b[NV];
   Raw<S> r[NV];
-  auto fetch = [&](uint32_t t) {
+  auto phase = [&](uint32_t t) {  // (of every array's row t the same)
+    const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const C*>(p.block) + t * p.ldb);
+    return M == kShift ? static_cast<int32_t>(row / sizeof(C) & 7u) : 0;
+  };
+  auto fetch = [&](uint32_t t, const Cols<M>& c) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb, c, v);
 #pragma unroll
     for (int v = 0; v < NV; ++v) r[v] = load8<true>(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
   };
   uint32_t t = blockIdx.x;
-  fetch(t);
+  c.phase = phase(t);
+  fetch(t, c);
   while (true) {
     float sum[1];
     float2 sigma = both(1.f);
     Raw<W> w[NV] = {};
     if (p.w_post) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) w[v] = load8(static_cast<const W*>(p.w_post), c, v);
+      for (int v = 0; v < NV; ++v) w[v] = load8_weight(static_cast<const W*>(p.w_post), c, v);
       float2 s = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -304,9 +364,11 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
       for (int i = 0; i < 4; ++i) s = fma2(out[v].get(i), out[v].get(i), s);
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) w[v] = load8(static_cast<const W*>(p.w_pre), c, v);
+    for (int v = 0; v < NV; ++v) w[v] = load8_weight(static_cast<const W*>(p.w_pre), c, v);
     const uint32_t next = t + gridDim.x;
-    if (next < rows) fetch(next);
+    Cols<M> c_next = c;
+    c_next.phase = phase(next);
+    if (next < rows) fetch(next, c_next);
     sum[0] = s.x + s.y;
     block_sum(sum, part[1]);
     const float2 rho = both(rms_inverse(sum[0], inv_cols, p.eps));
@@ -320,6 +382,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
     }
     if (next >= rows) return;
     t = next;
+    c = c_next;
     if (!p.w_post && blockDim.x > 32) __syncthreads();  // part[1] is used in every row
   }
 }
@@ -775,7 +838,7 @@ class Fit {
 template <typename C, typename S, typename W, Mode M, int NV, int MAXT>
 cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) {
   static Fit fit;
-  const int threads = row_threads(p.cols, NV);
+  const int threads = row_threads(p.cols + (M == kShift ? 7 : 0), NV);
   auto kern = norm_residual_kernel<C, S, W, M, NV, MAXT>;
   int64_t grid = p.rows;
   if (grid > num_sms) {
@@ -785,25 +848,32 @@ cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) 
   return launch(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p);
 }
 
+// (kWhole spares the test for the row's end: 16384 x 7168 157 us, as kRuns 162.)
 template <typename C, typename S, typename W, int NV, int MAXT>
-cudaError_t forward_runs(const NormParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t forward_runs(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
+  if (kind == NormRows::kShifted) return forward_impl<C, S, W, kShift, NV, MAXT>(p, num_sms, stream);
   return whole(p.cols, NV) ? forward_impl<C, S, W, kWhole, NV, MAXT>(p, num_sms, stream)
                            : forward_impl<C, S, W, kRuns, NV, MAXT>(p, num_sms, stream);
 }
 
+// Runs of eight columns a thread: one for short rows, which several blocks of
+// threads on an SM then go through side by side (16384 rows of bf16, us: 256
+// columns 8.0, with two runs 9.0; 1024 columns 23.3 against 22.7, but one row
+// 1.58 against 1.73); up to 4096 two (8192 rows of 2048: 22.5, with one 25.5,
+// with four 23.6); above that four (16384 x 7168: 157, with one 238).
+// Shifted rows load every weight in two pieces and move it, which waits: one
+// run to 2048 (777 x 1111: 4.3 us, with two 5.2; 16384 x 2049: 83.6 and 76.6).
+// Element by element the same rows take 5.7 and 135 us.
 template <typename C, typename S, typename W>
-cudaError_t forward(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  // few rows: as many threads as a row takes; else rows of few threads, so
-  // that several are under way on an SM
-  const bool one = p.cols <= 1024 || (p.cols <= 8192 && p.rows <= num_sms);
-  if (!vec) {
-    if (one) return forward_impl<C, S, W, kSingle, 1, 1024>(p, num_sms, stream);
+cudaError_t forward(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
+  if (kind == NormRows::kAny)
     return p.cols <= 4096 ? forward_impl<C, S, W, kSingle, 2, 256>(p, num_sms, stream)
                           : forward_impl<C, S, W, kSingle, 2, 1024>(p, num_sms, stream);
-  }
-  if (one) return forward_runs<C, S, W, 1, 1024>(p, num_sms, stream);
-  if (p.cols <= 4096) return forward_runs<C, S, W, 2, 256>(p, num_sms, stream);
-  return forward_runs<C, S, W, 4, 512>(p, num_sms, stream);
+  const int64_t cols = p.cols + (kind == NormRows::kShifted ? 7 : 0);
+  if (cols <= (kind == NormRows::kShifted ? 2048 : 1024))
+    return forward_runs<C, S, W, 1, 256>(p, kind, num_sms, stream);
+  if (cols <= 4096) return forward_runs<C, S, W, 2, 256>(p, kind, num_sms, stream);
+  return forward_runs<C, S, W, 4, 512>(p, kind, num_sms, stream);
 }
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
@@ -828,11 +898,15 @@ BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec) {
     p.fit = p.fit < 1 ? 1 : p.fit > 2 ? 2 : p.fit;
     return p;
   }
-  // by registers (128 a thread) and rings of three rows; a thread holds two
-  // runs where a row takes more than 512
-  p.runs = cols <= kOneRun ? 1 : 2;
+  // by registers (128 a thread) and rings of three rows.  A thread holds two
+  // runs where a row takes more than 512, and where blocks with one would leave
+  // a quarter of the SM's 512 threads idle (16384 x 2560 in bf16: 88 us, with
+  // one run 161; x 1536: 57 and 84); else one, which spills nothing and has
+  // room to overlap (x 2048 with an FP32 stream: 103, with two runs 116).
   p.cluster = cols <= 2 * kOneRun ? 1 : 2;
   const int64_t mine = p.cluster == 1 ? cols : (cols / 8 + 1) / 2 * 8;
+  p.runs = mine <= kOneRun ? 1 : 2;
+  if (vec && p.runs == 1 && kBackThreads % row_threads(mine, 1) >= kBackThreads / 4) p.runs = 2;
   p.threads = row_threads(mine, p.runs);
   p.fit = kBackThreads / p.threads;
   p.stages = 0;
@@ -919,12 +993,12 @@ cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, in
 
 }  // namespace
 
-// Forward and gradient for blocks of type C and a stream of type S; vec: rows
-// and pointers allow 16-byte accesses.
+// Forward and gradient for blocks of type C and a stream of type S; vec: the
+// gradient's rows and pointers allow 16-byte accesses.
 template <typename C, typename S>
-cudaError_t norm_forward_of(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  return p.w_fp32 ? forward<C, S, float>(p, vec, num_sms, stream)
-                  : forward<C, S, bf16>(p, vec, num_sms, stream);
+cudaError_t norm_forward_of(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
+  return p.w_fp32 ? forward<C, S, float>(p, kind, num_sms, stream)
+                  : forward<C, S, bf16>(p, kind, num_sms, stream);
 }
 template <typename C, typename S>
 cudaError_t norm_backward_of(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {

@@ -3,8 +3,8 @@
 
 namespace mx {
 
-cudaError_t norm_forward_mixed(const NormParams& p, bool vec, int num_sms, cudaStream_t stream) {
-  return norm_forward_of<bf16, float>(p, vec, num_sms, stream);
+cudaError_t norm_forward_mixed(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
+  return norm_forward_of<bf16, float>(p, kind, num_sms, stream);
 }
 
 cudaError_t norm_backward_mixed(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {

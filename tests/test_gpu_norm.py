@@ -329,3 +329,50 @@ def test_refusals(mx):
         with pytest.raises(ValueError):
             back(**bad)
     assert mx.device_status() == 0
+
+
+def placed(t, ld, offset, fill=7.0):
+    """t's values as rows `ld` apart, `offset` elements into a buffer of
+    `fill`; the buffer, too."""
+    rows, cols = t.shape
+    flat = torch.full((offset + rows * ld + 16,), fill, dtype=t.dtype, device="cuda")
+    view = flat[offset:offset + rows * ld].view(rows, ld)[:, :cols]
+    view.copy_(t)
+    return view, flat
+
+
+@pytest.mark.parametrize("cols,ld", [(1, 3), (5, 5), (8, 9), (9, 9), (15, 21), (17, 17), (130, 131),
+                                     (1017, 1017), (1018, 1025), (1111, 1111), (4089, 4089),
+                                     (4090, 4097), (8191, 8191), (16377, 16377), (16378, 16379)])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_rows_off_16_bytes(mx, cols, ld, c, s, w):
+    """Rows that begin anywhere, in step in all arrays or not, with weights
+    and gates off 16 bytes; what lies around the outputs stays."""
+    rows = 11
+    d = inputs(rows, cols, c, s, w, True, rows, seed=cols)
+    d["w_pre"] = placed(d["w_pre"][None], cols, 3)[0][0]
+    d["w_post"] = placed(d["w_post"][None], cols, 5)[0][0]
+    d["gate"] = placed(d["gate"], cols, 1)[0]
+    for base in (0, 3, 7):
+        for apart in (0, 1):                             # every array as far into its 16 bytes, or not
+            for i, n in enumerate(("block", "residual")):
+                d[n] = placed(d[n], ld, base + apart * i)[0]
+            out, flat_out = placed(torch.full((rows, cols), 7.0, dtype=c, device="cuda"), ld, base)
+            res, flat_res = placed(torch.full((rows, cols), 7.0, dtype=s, device="cuda"), ld, base)
+            check_forward(mx, d, 0.875, out_residual=res, out=out)
+            kept = out.clone(), res.clone()
+            for view, flat in ((out, flat_out), (res, flat_res)):
+                view.fill_(7.0)
+                assert bool((flat == 7.0).all())         # nothing around it was written
+            before = d["residual"].clone()
+            mx.norm_residual(d["block"], d["residual"], d["w_pre"], w_post=d["w_post"],
+                             gate=d["gate"], alpha=0.875, out_residual=d["residual"], out=out)
+            assert torch.equal(out, kept[0]) and torch.equal(d["residual"], kept[1])
+            d["residual"] = before
+
+
+@pytest.mark.parametrize("cols", [1032, 1536, 2560, 3584])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_gradient_rows_of_one_or_two_runs(mx, cols, c, s, w):
+    for rows, gates in ((1, 0), (40, 0), (700, 7), (650, 1)):
+        check_backward(mx, inputs(rows, cols, c, s, w, True, gates, seed=cols), 0.5)

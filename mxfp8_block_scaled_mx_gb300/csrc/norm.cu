@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kSumThreads)
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
   int64_t n = 0;  // the most blocks that any types and alignment have
   for (int i = 0; i < 8; ++i) {
-    const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, i & 1, i & 2, i & 4));
+    const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, gates, i & 1, i & 2, i & 4));
     n = m > n ? m : n;
   }
   return static_cast<size_t>(n) * (gates > 0 ? 4 : 2) * static_cast<size_t>(cols) * 4;
@@ -146,7 +146,7 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
                    aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
                    aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&
                    p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 && p.lddr % se == 0;
-  const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec);
+  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, vec);
   const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan);
   cudaError_t err;
   if (p.c_fp32)

@@ -442,14 +442,16 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 // shared memory by bulk copies, `stages` of them at most (0: rows that do not
 // fit, read in place); a thread takes its columns to registers once, where
 // they stay across the row's one barrier, behind which the next copy starts.
-// A thread also keeps the sums of its columns over the rows.  The weights (from
-// L1) are asked for before the wait for the row, where registers hold them
-// that long.  MANY: more gates than one.  CL: blocks of a cluster that share a
-// row (two for rows longer than a block's registers hold, exchanging sums
-// through distributed shared memory).
-template <typename C, typename S, typename W, Mode M, int NV, bool MANY, int CL>
+// A thread also keeps the sums of its columns over the rows and the factors
+// w_post g of its columns for the current gate, which every row wants twice (in
+// FP32; with two runs a thread behind the ring).  w_pre (from L1) is asked for before the wait for the
+// row, where registers hold it that long.  `post` (more gates than one): the sums
+// of D b sigma g over finished gates lie behind ring and factors, else in the workspace.
+// CL: blocks of a cluster that share a row (two for rows longer than a block's
+// registers hold, exchanging sums through distributed shared memory).
+template <typename C, typename S, typename W, Mode M, int NV, int CL>
 __global__ void __launch_bounds__(kBackThreads)
-    norm_backward_kernel(const NormBackParams p, int stages) {
+    norm_backward_kernel(const NormBackParams p, int stages, bool post) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float part[2][CL * kBackThreads / 32 * 8];
   __shared__ uint64_t full[8];
@@ -494,40 +496,55 @@ __global__ void __launch_bounds__(kBackThreads)
 
   const uint32_t per = static_cast<uint32_t>(p.gates ? p.rows / p.gates : p.rows);
   const float2 alpha = both(p.alpha);
-  // sums over rows of dy r rho and of D b sigma, with many gates also of the
-  // latter times g over finished gates
-  constexpr int kPost = MANY ? NV : 1;
-  float2 pre[NV][4], q[NV][4], post[kPost][4];
+  // sums over rows of dy r rho and of D b sigma, the latter over the current
+  // gate's rows
+  float2 pre[NV][4], q[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = post[MANY ? v : 0][i] = both(0.f);
+    for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = both(0.f);
+  constexpr bool kHeld = NV == 1;                          // factors in registers
+  Raw<float> held = {{both(1.f), both(1.f), both(1.f), both(1.f)}};
+  float* behind = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  auto times_factor = [&](float2 (&f)[4], int v) {
+    if constexpr (kHeld)
+      times(f, held);
+    else if (p.gate || p.w_post)
+      times(f, load8(behind, c, v));
+  };
+  float* finished = post ? behind + (kHeld ? 0 : half) : p.w_post ? ws_post(p, n, me) + off : nullptr;
+  auto set_factors = [&](int64_t goff) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      Raw<float> r;
+      float2 f[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
+      if (p.w_post) times_w<W>(f, p.w_post, off, c, v);
+      if (p.gate) times_w<W>(f, p.gate, goff, c, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.f[i] = f[i];
+      if constexpr (kHeld)
+        held = r;
+      else
+        store8(behind, c, v, r);
+    }
+  };
   const uint32_t group0 = lo / per;
   uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
+  if (p.gate || p.w_post) set_factors(group * p.cols + off);
   int stage = 0;
   uint32_t phase = 0;
   for (uint32_t t = lo; t < hi; ++t) {
-    const int64_t goff = group * p.cols + off;
     Raw<S> x[NV], a[NV] = {};
     Raw<C> y[NV], b[NV];
     constexpr bool kAhead = NV == 1 || sizeof(W) == 2;
-    Raw<W> w_pre[NV], w_post[NV] = {};
+    Raw<W> w_pre[NV];
 #pragma unroll
-    for (int v = 0; kAhead && v < NV; ++v) {
-      w_pre[v] = load8(static_cast<const W*>(p.w_pre) + off, c, v);
-      if (p.w_post) w_post[v] = load8(static_cast<const W*>(p.w_post) + off, c, v);
-    }
+    for (int v = 0; kAhead && v < NV; ++v) w_pre[v] = load8(static_cast<const W*>(p.w_pre) + off, c, v);
     auto times_pre = [&](float2 (&f)[4], int v) {
       if constexpr (kAhead)
         times(f, w_pre[v]);
       else
         times_w<W>(f, p.w_pre, off, c, v);
-    };
-    auto times_post = [&](float2 (&f)[4], int v) {
-      if constexpr (kAhead)
-        times(f, w_post[v]);
-      else
-        times_w<W>(f, p.w_post, off, c, v);
     };
     if (stages > 0) {
       mbar_wait(&full[stage], phase, s_abort, p.status, p.wait_limit_ns);
@@ -569,8 +586,7 @@ __global__ void __launch_bounds__(kBackThreads)
           h[i] = b[v].get(i);
           s2[kBB] = fma2(h[i], h[i], s2[kBB]);
         }
-        times_post(h, v);
-        if (p.gate) times_w<W>(h, p.gate, goff, c, v);
+        times_factor(h, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s2[kHA] = fma2(h[i], a[v].get(i), s2[kHA]);
@@ -633,9 +649,8 @@ __global__ void __launch_bounds__(kBackThreads)
         q[v][i] = fma2(d[i], mul2(b[v].get(i), sigma), q[v][i]);
       }
       store8(static_cast<S*>(p.d_residual) + t * p.lddr + off, c, v, round8<S>(o));
-      if (p.gate) times_w<W>(d, p.gate, goff, c, v);
+      times_factor(d, v);
       if (p.w_post) {
-        times_post(d, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = fma2(b[v].get(i), m, mul2(sigma, d[i]));
       }
@@ -643,6 +658,7 @@ __global__ void __launch_bounds__(kBackThreads)
     }
     if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
       if (p.gate) {
+        const int64_t goff = group * p.cols + off;
         const bool whole = group * per >= lo && left == 0;
         float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1)) + off;
 #pragma unroll
@@ -651,21 +667,26 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
           for (int i = 0; i < 4; ++i) dg[i] = q[v][i];
           if (p.w_post) times_w<W>(dg, p.w_post, off, c, v);
-          times_w<W>(q[v], p.gate, goff, c, v);
           Raw<float> out;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            out.f[i] = dg[i];
-            if constexpr (MANY) {
-              post[v][i] = add2(post[v][i], q[v][i]);
-              q[v][i] = both(0.f);
-            }
-          }
+          for (int i = 0; i < 4; ++i) out.f[i] = dg[i];
           store8(dst, c, v, out);
+          times_w<W>(q[v], p.gate, goff, c, v);
+          if (p.gates > 1) {
+            if (p.w_post) {
+              if (group != group0) out = load8(finished, c, v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) out.f[i] = group != group0 ? add2(out.f[i], q[v][i]) : q[v][i];
+              store8(finished, c, v, out);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[v][i] = both(0.f);
+          }
         }
       }
       ++group;
       left = per;
+      if (p.gate && t + 1 < hi) set_factors(group * p.cols + off);
     }
   }
   if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
@@ -679,9 +700,13 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) out.f[i] = pre[v][i];
     store8(ws_pre(p, me) + off, c, v, out);
-    if (p.w_post) {
+    if (p.w_post && (post || p.gates <= 1)) {
+      if (post) {
+        out = load8(finished, c, v);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out.f[i] = MANY ? post[MANY ? v : 0][i] : q[v][i];
+        for (int i = 0; i < 4; ++i) out.f[i] = q[v][i];
+      }
       store8(ws_post(p, n, me) + off, c, v, out);
     }
   }
@@ -877,50 +902,60 @@ cudaError_t forward(const NormParams& p, NormRows kind, int num_sms, cudaStream_
 }
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
-constexpr size_t kSmemBytes = 200 * 1024;  // of an SM, for rings and sums; L1 keeps the weights
+// Shared memory for rings, factors and sums of one of `fit` blocks on an SM (228 KB
+// in all; a block has 2 KB of its own beside these).
+constexpr size_t kSmemBytes = 206 * 1024;
+constexpr size_t smem_of(int fit) {
+  const size_t share = 228 * 1024 / fit - 2304;
+  return share < kSmemBytes ? share : kSmemBytes;
+}
 
 // How a gradient is run: runs of eight columns a thread holds (0: the kernel
 // that goes element by element), blocks that share a row, threads of a block,
 // rows on an SM side by side (clusters: on two), rows of the ring, bytes of
-// shared memory.
+// shared memory, and bytes more for the sums over finished gates (0: too many).
 struct BackPlan {
   int runs, cluster, threads, fit, stages;
-  size_t smem;
+  size_t smem, post;
 };
-BackPlan backward_plan(int64_t cols, bool c_fp32, bool s_fp32, bool vec) {
+BackPlan backward_plan(int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, bool vec) {
   BackPlan p;
   constexpr int64_t kOneRun = 8 * kBackThreads;
   if (!vec && cols > kOneRun) {  // by shared memory
     p.runs = 0, p.cluster = 1, p.stages = 0;
     p.threads = kBackThreads;
     p.smem = static_cast<size_t>(cols) * 12;
-    p.fit = static_cast<int>(kSmemBytes / p.smem);
-    p.fit = p.fit < 1 ? 1 : p.fit > 2 ? 2 : p.fit;
+    p.post = 0;
+    p.fit = p.smem <= smem_of(2) ? 2 : 1;
     return p;
   }
   // by registers (128 a thread) and rings of three rows.  A thread holds two
-  // runs where a row takes more than 512, and where blocks with one would leave
-  // a quarter of the SM's 512 threads idle (16384 x 2560 in bf16: 88 us, with
-  // one run 161; x 1536: 57 and 84); else one, which spills nothing and has
-  // room to overlap (x 2048 with an FP32 stream: 103, with two runs 116).
+  // runs where a row takes more than 512; where blocks with one would leave a
+  // quarter of the SM's 512 threads idle (16384 x 2560 in bf16: 89 us, with one
+  // run 161; x 1536: 58 and 84); and where the SM then holds two such blocks with
+  // their rings instead of one (x 3584: 120 and 144).  Else one: its factors stay
+  // in registers (x 2048: 73, with two 76; x 2048, FP32 stream: 105 and 108).
   p.cluster = cols <= 2 * kOneRun ? 1 : 2;
   const int64_t mine = p.cluster == 1 ? cols : (cols / 8 + 1) / 2 * 8;
   p.runs = mine <= kOneRun ? 1 : 2;
-  if (vec && p.runs == 1 && kBackThreads % row_threads(mine, 1) >= kBackThreads / 4) p.runs = 2;
+  const size_t stage = mine * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
+  const size_t factors = static_cast<size_t>(mine) * 4;
+  if (vec && p.runs == 1 && (kBackThreads % row_threads(mine, 1) >= kBackThreads / 4 ||
+                             (mine > 2048 && factors + 3 * stage <= smem_of(2))))
+    p.runs = 2;
   p.threads = row_threads(mine, p.runs);
   p.fit = kBackThreads / p.threads;
-  p.stages = 0;
-  p.smem = 0;
-  if (vec) {
-    const size_t stage = mine * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
-    const int by_smem = static_cast<int>(kSmemBytes / (3 * stage));
-    p.fit = p.fit < by_smem ? p.fit : by_smem;
-    p.fit = p.fit < 1 ? 1 : p.fit > 8 ? 8 : p.fit;
-    const size_t rows = kSmemBytes / p.fit / stage;
-    p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
-    p.smem = p.stages * stage;
-  }
   p.fit = p.fit > 8 ? 8 : p.fit;
+  p.stages = 0;
+  p.post = gates > 1 ? factors : 0;
+  p.smem = p.runs == 2 ? factors : 0;
+  if (vec) {
+    while (p.fit > 1 && p.smem + 3 * stage > smem_of(p.fit)) --p.fit;
+    const size_t rows = (smem_of(p.fit) - p.smem) / stage;
+    p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
+    p.smem += p.stages * stage;
+  }
+  if (p.smem + p.post > smem_of(p.fit)) p.post = 0;
   return p;
 }
 
@@ -939,11 +974,11 @@ cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
   });
 }
 
-template <typename C, typename S, typename W, Mode M, int NV, bool MANY, int CL>
+template <typename C, typename S, typename W, Mode M, int NV, int CL>
 cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t n,
                           cudaStream_t stream) {
   static PerDeviceOnce setup;
-  auto kern = norm_backward_kernel<C, S, W, M, NV, MANY, CL>;
+  auto kern = norm_backward_kernel<C, S, W, M, NV, CL>;
   const cudaError_t err = allow_smem(setup, kern);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -954,11 +989,11 @@ cudaError_t backward_impl(const NormBackParams& p, const BackPlan& plan, int64_t
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(n * CL));
   cfg.blockDim = dim3(plan.threads);
-  cfg.dynamicSmemBytes = plan.smem;
+  cfg.dynamicSmemBytes = plan.smem + plan.post;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = CL == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, kern, p, plan.stages);
+  return cudaLaunchKernelEx(&cfg, kern, p, plan.stages, plan.post > 0);
 }
 
 template <typename C, typename S>
@@ -971,24 +1006,17 @@ cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64
   return launch(kern, dim3(static_cast<unsigned>(n)), plan.threads, plan.smem, stream, p);
 }
 
-template <typename C, typename S, typename W, bool MANY>
-cudaError_t backward_of(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
-                        cudaStream_t stream) {
-  if (!vec) return backward_impl<C, S, W, kSingle, 1, MANY, 1>(p, plan, n, stream);
-  if (plan.cluster == 2) return backward_impl<C, S, W, kRuns, 2, MANY, 2>(p, plan, n, stream);
-  if (plan.runs == 1)
-    return whole(p.cols, 1) ? backward_impl<C, S, W, kWhole, 1, MANY, 1>(p, plan, n, stream)
-                            : backward_impl<C, S, W, kRuns, 1, MANY, 1>(p, plan, n, stream);
-  return whole(p.cols, 2) ? backward_impl<C, S, W, kWhole, 2, MANY, 1>(p, plan, n, stream)
-                          : backward_impl<C, S, W, kRuns, 2, MANY, 1>(p, plan, n, stream);
-}
-
 template <typename C, typename S, typename W>
 cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
                      cudaStream_t stream) {
   if (plan.runs == 0) return backward_single<C, S>(p, plan, n, stream);
-  return p.gates > 1 ? backward_of<C, S, W, true>(p, vec, plan, n, stream)
-                     : backward_of<C, S, W, false>(p, vec, plan, n, stream);
+  if (!vec) return backward_impl<C, S, W, kSingle, 1, 1>(p, plan, n, stream);
+  if (plan.cluster == 2) return backward_impl<C, S, W, kRuns, 2, 2>(p, plan, n, stream);
+  if (plan.runs == 1)
+    return whole(p.cols, 1) ? backward_impl<C, S, W, kWhole, 1, 1>(p, plan, n, stream)
+                            : backward_impl<C, S, W, kRuns, 1, 1>(p, plan, n, stream);
+  return whole(p.cols, 2) ? backward_impl<C, S, W, kWhole, 2, 1>(p, plan, n, stream)
+                          : backward_impl<C, S, W, kRuns, 2, 1>(p, plan, n, stream);
 }
 
 }  // namespace
@@ -1002,7 +1030,7 @@ cudaError_t norm_forward_of(const NormParams& p, NormRows kind, int num_sms, cud
 }
 template <typename C, typename S>
 cudaError_t norm_backward_of(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
-  const BackPlan plan = backward_plan(p.cols, p.c_fp32, p.s_fp32, vec);
+  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, vec);
   return p.w_fp32 ? backward<C, S, float>(p, vec, plan, n, stream)
                   : backward<C, S, bf16>(p, vec, plan, n, stream);
 }

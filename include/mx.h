@@ -2,7 +2,8 @@
  * mx.h -- C ABI of libmx, the MXFP8 training-matmul library for GB300 (sm_103a).
  *
  * The library has two parts, after "Low-Precision GPU Programming"
- * (leetllm.com):
+ * (leetllm.com), and beside them the operators that stand around the products
+ * in a model (last section):
  *
  *   1. MX quantization (sections "Format taxonomy: range, spacing, and
  *      bitfields", "Numerical hazards: subnormals, saturation, and rounding"
@@ -62,7 +63,9 @@
  *
  * Kernels: quantization runs in one persistent kernel (one block per SM,
  * tiles streamed by TMA); every GEMM runs in one block-pair kernel
- * (tcgen05 cta_group::2, 256x256 output tiles over two SMs).  No
+ * (tcgen05 cta_group::2, 256x256 output tiles over two SMs).  A norm is one
+ * kernel, its gradient two (rows, then the sums over rows); the expert layer
+ * for few tokens two (logits, then everything else, one block per SM).  No
  * environment variable changes what the library does.
  */
 #ifndef MX_H_
@@ -366,7 +369,9 @@ mx_status mx_grouped_gemm_wgrad(int32_t groups, const int32_t* d_offsets, int64_
  *    channel, gates = rows one per element; rows % gates == 0.
  * w_post, w_pre and gate share w_dtype.
  * Pointers and leading dimensions need the alignment of one element only
- * (rows of whole 16-byte runs on 16-byte boundaries are the fast case);
+ * (rows of whole 16-byte runs on 16-byte boundaries are the fast case; rows of
+ *    odd length are nearly as fast forwards when all arrays are as far into
+ *    their 16 bytes, a third as fast backwards);
  * 1 <= cols <= 16384 (more is MX_ERR_UNSUPPORTED), leading dimensions >=
  * cols, eps >= 0; rows == 0 does nothing. */
 mx_status mx_norm_residual(int64_t rows, int64_t cols,

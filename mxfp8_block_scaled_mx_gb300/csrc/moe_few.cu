@@ -5,8 +5,8 @@
 //
 // What bounds it is reading the chosen experts' weights once.  Weights are
 // the A operand of the tensor cores (128 rows a tile, straight from their MX
-// storage, block scales applied by the MMA), tokens the B operand (N = the
-// token count rounded up to 16), so that nothing is decoded in registers
+// storage, block scales applied by the MMA), tokens the B operand (N = twice
+// the token count rounded up to 16), so that nothing is decoded in registers
 // and a token more costs nothing until N outgrows the weights' transfer.
 //
 // Activations keep their precision on FP8 tensor cores as a sum of two E4M3
@@ -44,9 +44,9 @@
 //       router kernel's 8 us, SMs that differ by 5 % in speed, and the last join)
 //   1 token, hidden 2048, 8 of 128 experts of 768:          18.8 us, 0.31 (a chain
 //       of latencies: logits 4, routing 2, first tiles, two joins of 2.5 each)
-//   1 token, hidden 7168, 8 experts of 2048, 4-bit weights: 47.6 us, 0.59 (a tile
-//       takes the tensor cores 256 ns and memory 200 ns: an MMA with few columns
-//       costs the reading of its 128 x 32 A operand, whatever the bits in memory)
+//   1 token, hidden 7168, 8 experts of 2048, 4-bit weights: 47.1 us, 0.60 (about 9
+//       of it that chain; 4-bit tiles alone, without MMAs, tokens and scales, take
+//       41: they come at 0.85 of the copy bandwidth, 64 bytes of a row each)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -457,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pad = pad_tokens(p.tokens);
   const uint32_t b_bytes = static_cast<uint32_t>(code_bytes(pad));
   uint8_t* sA = smem;                                 // [stages][16 KB]
-  uint8_t* sB = sA + stages * kTileBytes;             // [stages][b_bytes]
-  uint8_t* sSf = sB + stages * b_bytes;               // [stages][A, B][512]
-  Shared* sh = reinterpret_cast<Shared*>(sSf + stages * 2 * kSfBytes);
+  uint8_t* sB = sA + stages * kTileBytes;             // [stages][record, A's scales]
+  const uint32_t b_step = b_bytes + 2 * kSfBytes;
+  Shared* sh = reinterpret_cast<Shared*>(sB + stages * b_step);
   volatile uint32_t* s_abort = &sh->abort;
   const uint32_t warp = warp_id(), lane = lane_id();
   const Layout l = layout(p.tokens, p.hidden, p.inter, p.experts, p.top_k);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t items1 = sh->active * it_count;       // (expert, 128 channels)
   const Share share1(items1, ht_count);               // each tile: gate and up
   const Share share2(ht_count, items1);
-  const uint32_t tx_b = b_bytes + kSfBytes;
+  const uint32_t b_record = b_bytes + kSfBytes;
   // accumulators: two columns per padded token, for gate and up; a second
   // set where tensor memory holds it next to the scales (16 tokens of 4096, 64
   // experts of 1024: 136.7 us, with one set 137.5; one token of 2048 18.2 and 18.6)
@@ -570,15 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_empty())) break;
         {
           uint64_t* bar = &sh->full[stage];
-          uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_bytes;
-          uint8_t* sf_dst = sSf + stage * 2 * kSfBytes;
-          const uint8_t* record_sf = record + b_bytes;
+          uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_step;
+          uint8_t* sf_dst = b_dst + b_record;
           if (elect_one()) {
-            mbar_arrive_expect_tx(bar, tx_gu + tx_b);
+            mbar_arrive_expect_tx(bar, tx_gu + b_record);
             tma_load_2d(a_dst, &tmap_gate, bar, x, y);
             bulk_load(sf_dst, gate_sf, kSfBytes, bar);
-            bulk_load(b_dst, record, b_bytes, bar);
-            bulk_load(sf_dst + kSfBytes, record_sf, kSfBytes, bar);
+            bulk_load(b_dst, record, b_record, bar);
           }
           __syncwarp();
         }
@@ -586,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_empty())) break;
         {
           uint64_t* bar = &sh->full[stage];
-          uint8_t *a_dst = sA + stage * kTileBytes, *sf_dst = sSf + stage * 2 * kSfBytes;
+          uint8_t *a_dst = sA + stage * kTileBytes, *sf_dst = sB + stage * b_step + b_record;
           if (elect_one()) {
             mbar_arrive_expect_tx(bar, tx_gu);
             tma_load_2d(a_dst, &tmap_up, bar, x, y);
@@ -620,20 +618,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto load_tile = [&](bool with_record) {
       uint64_t* bar = &sh->full[stage];
-      uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_bytes;
-      uint8_t* sf_dst = sSf + stage * 2 * kSfBytes;
+      uint8_t *a_dst = sA + stage * kTileBytes, *b_dst = sB + stage * b_step;
+      uint8_t* sf_dst = b_dst + b_record;
       const uint8_t* sf = p.down_scales + e * mat2 + (static_cast<int64_t>(w.item) * it_count + kt) * kSfBytes;
       const uint8_t* record = p.workspace + l.h + w.k0 * record_bytes(pad);
-      const uint8_t* record_sf = record + b_bytes;
       const int32_t x = kt * kTile, y = e * p.hidden + w.item * kTile;
       if (elect_one()) {
-        mbar_arrive_expect_tx(bar, tx_d + tx_b);
+        mbar_arrive_expect_tx(bar, tx_d + b_record);
         tma_load_2d(a_dst, &tmap_down, bar, x, y);
         bulk_load(sf_dst, sf, kSfBytes, bar);
-        if (with_record) {
-          bulk_load(b_dst, record, b_bytes, bar);
-          bulk_load(sf_dst + kSfBytes, record_sf, kSfBytes, bar);
-        }
+        if (with_record) bulk_load(b_dst, record, b_record, bar);
       }
       __syncwarp();
     };
@@ -659,12 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* record =
             p.workspace + l.h + (first_k + i) % static_cast<int32_t>(share2.per) * record_bytes(pad);
         uint64_t* bar = &sh->full[s];
-        uint8_t *b_dst = sB + s * b_bytes, *sf_dst = sSf + (s * 2 + 1) * kSfBytes;
-        const uint8_t* record_sf = record + b_bytes;
-        if (elect_one()) {
-          bulk_load(b_dst, record, b_bytes, bar);
-          bulk_load(sf_dst, record_sf, kSfBytes, bar);
-        }
+        uint8_t* b_dst = sB + s * b_step;
+        if (elect_one()) bulk_load(b_dst, record, b_record, bar);
         __syncwarp();
       }
     }
@@ -687,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kHiScale = smem_desc_hi(128, 0);
     const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), 16);
     const uint32_t b_lo0 = smem_desc_lo(smem_u32(sB), 16);
-    const uint32_t sf_lo0 = smem_desc_lo(smem_u32(sSf), 0);
+    const uint32_t sf_lo0 = smem_desc_lo(smem_u32(sB + b_bytes), 0);  // B's, then A's
     const uint32_t sf_col0 = tmem + acc_sets * acc_cols;
     int stage = 0;
     uint32_t phase = 0, acc = 0, acc_phase = 0;
@@ -741,19 +731,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_full())) break;
           const int gate_stage = stage;
           const uint32_t sfa = sf_col0 + stage * 8u, sfb = sfa + 4u;
-          const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t sf_lo = sf_lo0 + stage * (b_step >> 4);
           const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
-          const uint32_t b_lo = b_lo0 + stage * (b_bytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (b_step >> 4);
           if (elect_one()) {
-            tc_cp_32x128b_warpx4(sfa, sf_lo, kHiScale);
-            tc_cp_32x128b_warpx4(sfb, sf_lo + (kSfBytes >> 4), kHiScale);
+            tc_cp_32x128b_warpx4(sfa, sf_lo + (kSfBytes >> 4), kHiScale);
+            tc_cp_32x128b_warpx4(sfb, sf_lo, kHiScale);
             multiply(d, a_lo, b_lo, idesc, sfa, sfb, blocks, add);
           }
           __syncwarp();
           next();
           if (!(ok = wait_full())) break;
           const uint32_t up_sfa = sf_col0 + stage * 8u;
-          const uint32_t up_sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t up_sf_lo = sf_lo0 + stage * (b_step >> 4) + (kSfBytes >> 4);
           const uint32_t up_lo = a_lo0 + stage * (kTileBytes >> 4);
           uint64_t *empty0 = &sh->empty[gate_stage], *empty1 = &sh->empty[stage];
           if (elect_one()) {
@@ -783,13 +773,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t left = k_blocks - kt * 4, blocks = left < 4 ? left : 4;
           if (!(ok = wait_full())) break;
           const uint32_t sfa = sf_col0 + stage * 8u, sfb = sfa + 4u;
-          const uint32_t sf_lo = sf_lo0 + stage * (2 * kSfBytes >> 4);
+          const uint32_t sf_lo = sf_lo0 + stage * (b_step >> 4);
           const uint32_t a_lo = a_lo0 + stage * (kTileBytes >> 4);
-          const uint32_t b_lo = b_lo0 + stage * (b_bytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (b_step >> 4);
           uint64_t* empty = &sh->empty[stage];
           if (elect_one()) {
-            tc_cp_32x128b_warpx4(sfa, sf_lo, kHiScale);
-            tc_cp_32x128b_warpx4(sfb, sf_lo + (kSfBytes >> 4), kHiScale);
+            tc_cp_32x128b_warpx4(sfa, sf_lo + (kSfBytes >> 4), kHiScale);
+            tc_cp_32x128b_warpx4(sfb, sf_lo, kHiScale);
             multiply(d, a_lo, b_lo, idesc, sfa, sfb, blocks, add);
             tc_commit(empty);
           }

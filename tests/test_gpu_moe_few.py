@@ -256,3 +256,15 @@ def test_refusals(mx):
         call(x=torch.zeros(4, 257, dtype=BF16, device="cuda")[:, 1:])
     assert e.value.status == 2
     assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 4, 15, 16, 17, 40])
+@pytest.mark.parametrize("hidden,inter,experts,top_k", [(128, 128, 3, 2), (640, 384, 5, 2),
+                                                        (2048, 128, 4, 1), (256, 2048, 6, 3)])
+def test_packed_4_bit_weights_by_token_count(mx, tokens, hidden, inter, experts, top_k):
+    """Both roles of the operands: odd and even numbers of 128-channel tiles,
+    sums in one block and in many."""
+    d, mats = layer(tokens + hidden, tokens, hidden, inter, experts, "e2m1_packed")
+    y, ids, w = check(mx, d, mats, top_k)
+    again = mx.moe_few_tokens(d["x"], d["router"], d["gate"], d["up"], d["down"], top_k)
+    assert torch.equal(again, y)

@@ -369,9 +369,9 @@ mx_status mx_grouped_gemm_wgrad(int32_t groups, const int32_t* d_offsets, int64_
  *    channel, gates = rows one per element; rows % gates == 0.
  * w_post, w_pre and gate share w_dtype.
  * Pointers and leading dimensions need the alignment of one element only
- * (rows of whole 16-byte runs on 16-byte boundaries are the fast case; rows of
- *    odd length are nearly as fast forwards when all arrays are as far into
- *    their 16 bytes, a third as fast backwards);
+ *    (rows of whole 16-byte runs on 16-byte boundaries are the fast case; rows
+ *    of odd length are about half as fast where all arrays are as far into
+ *    their 16 bytes, else a third);
  * 1 <= cols <= 16384 (more is MX_ERR_UNSUPPORTED), leading dimensions >=
  * cols, eps >= 0; rows == 0 does nothing. */
 mx_status mx_norm_residual(int64_t rows, int64_t cols,

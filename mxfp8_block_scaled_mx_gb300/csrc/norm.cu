@@ -7,8 +7,8 @@ namespace mx {
 
 cudaError_t norm_forward_mixed(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream);
 cudaError_t norm_forward_f32(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream);
-cudaError_t norm_backward_mixed(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream);
-cudaError_t norm_backward_f32(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream);
+cudaError_t norm_backward_mixed(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream);
+cudaError_t norm_backward_f32(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream);
 
 namespace {
 
@@ -101,12 +101,28 @@ __global__ void __launch_bounds__(kSumThreads)
 
 size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
   int64_t n = 0;  // the most blocks that any types and alignment have
-  for (int i = 0; i < 8; ++i) {
-    const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, gates, i & 1, i & 2, i & 4));
-    n = m > n ? m : n;
-  }
+  for (int i = 0; i < 4; ++i)
+    for (NormRows kind : {NormRows::kAligned, NormRows::kShifted, NormRows::kAny}) {
+      if (kind == NormRows::kShifted && cols > kShiftCols) continue;
+      const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, gates, i & 1, i & 2, kind));
+      n = m > n ? m : n;
+    }
   return static_cast<size_t>(n) * (gates > 0 ? 4 : 2) * static_cast<size_t>(cols) * 4;
 }
+
+// Whether rows of another array are as far (in columns modulo 8) into their 16
+// bytes as those of the first.
+struct InStep {
+  uint64_t at;
+  int64_t ld;
+  static uint64_t column(const void* a, bool fp32) {
+    return reinterpret_cast<uintptr_t>(a) / (fp32 ? 4 : 2);
+  }
+  InStep(const void* a, int64_t ld, bool fp32) : at(column(a, fp32)), ld(ld) {}
+  bool with(const void* b, int64_t ldb, bool fp32) const {
+    return ((column(b, fp32) ^ at) & 7u) == 0 && ((ld ^ ldb) & 7) == 0;
+  }
+};
 
 cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t stream) {
   const int64_t ce = p.c_fp32 ? 4 : 8, se = p.s_fp32 ? 4 : 8;
@@ -116,14 +132,9 @@ cudaError_t launch_norm_residual(const NormParams& p, int num_sms, cudaStream_t 
       p.ldb % ce == 0 && p.ldy % ce == 0 && p.ldr % se == 0 && p.ldo % se == 0) {
     kind = NormRows::kAligned;
   } else if (p.cols + 7 <= 8 * 4 * 512) {  // (what the widest kernel holds)
-    // columns (modulo 8) from each array's first 16-byte boundary, and from row to row
-    auto same = [&](const void* a, int64_t ld, bool fp32) {
-      const uint64_t at = reinterpret_cast<uintptr_t>(a) / (fp32 ? 4 : 2);
-      const uint64_t at0 = reinterpret_cast<uintptr_t>(p.block) / (p.c_fp32 ? 4 : 2);
-      return ((at ^ at0) & 7u) == 0 && ((ld ^ p.ldb) & 7) == 0;
-    };
-    if (same(p.y, p.ldy, p.c_fp32) && same(p.residual, p.ldr, p.s_fp32) &&
-        same(p.res_out, p.ldo, p.s_fp32))
+    const InStep step(p.block, p.ldb, p.c_fp32);
+    if (step.with(p.y, p.ldy, p.c_fp32) && step.with(p.residual, p.ldr, p.s_fp32) &&
+        step.with(p.res_out, p.ldo, p.s_fp32))
       kind = NormRows::kShifted;
   }
   if (p.c_fp32) return norm_forward_f32(p, kind, num_sms, stream);
@@ -142,19 +153,34 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
     return err;
   }
   const int64_t ce = p.c_fp32 ? 4 : 8, se = p.s_fp32 ? 4 : 8;
-  const bool vec = p.cols % 8 == 0 && aligned16(p.d_res) && aligned16(p.dy) && aligned16(p.block) && aligned16(p.res_out) && aligned16(p.w_post) &&
-                   aligned16(p.w_pre) && aligned16(p.gate) && aligned16(p.d_block) &&
-                   aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) && p.lddy % ce == 0 &&
-                   p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 && p.lddr % se == 0;
-  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, vec);
+  NormRows kind = NormRows::kAny;
+  if (p.cols % 8 == 0 && aligned16(p.d_res) && aligned16(p.dy) && aligned16(p.block) &&
+      aligned16(p.res_out) && aligned16(p.w_post) && aligned16(p.w_pre) && aligned16(p.gate) &&
+      aligned16(p.d_block) && aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) &&
+      p.lddy % ce == 0 && p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 &&
+      p.lddr % se == 0) {
+    kind = NormRows::kAligned;
+  } else if (p.cols <= kShiftCols && (p.gates == 0 || p.rows >= 16 * p.gates) &&
+             (p.cols > kOneRun || (p.cols > 1024 && p.rows >= 64 * static_cast<int64_t>(num_sms)))) {
+    // Going by phase takes 16-byte accesses, but its sums change hands after
+    // each of up to eight phases: 16384 x 2049 144 us (element by element 311),
+    // x 1111 100 (122), x 501 61 (58); 3000 x 1111 39 (31); 16 rows a gate 131
+    // (134); more than 4096 columns: 16384 x 5001 343 (701), 400 x 5001 31 (29).
+    const InStep step(p.block, p.ldb, p.c_fp32);
+    if (step.with(p.dy, p.lddy, p.c_fp32) && step.with(p.res_out, p.ldr, p.s_fp32) &&
+        (!p.d_res || step.with(p.d_res, p.ldd, p.s_fp32)) &&
+        step.with(p.d_block, p.lddb, p.c_fp32) && step.with(p.d_residual, p.lddr, p.s_fp32))
+      kind = NormRows::kShifted;
+  }
+  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
   const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan);
   cudaError_t err;
   if (p.c_fp32)
-    err = norm_backward_f32(p, vec, n, stream);
+    err = norm_backward_f32(p, kind, n, stream);
   else if (p.s_fp32)
-    err = norm_backward_mixed(p, vec, n, stream);
+    err = norm_backward_mixed(p, kind, n, stream);
   else
-    err = norm_backward_of<bf16, bf16>(p, vec, n, stream);
+    err = norm_backward_of<bf16, bf16>(p, kind, n, stream);
   if (err != cudaSuccess) return err;
   const SumPlan sum = sum_plan(p.rows, p.cols, p.gates, n);
   return launch(norm_backward_sum_kernel,

@@ -7,8 +7,8 @@ cudaError_t norm_forward_f32(const NormParams& p, NormRows kind, int num_sms, cu
   return norm_forward_of<float, float>(p, kind, num_sms, stream);
 }
 
-cudaError_t norm_backward_f32(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
-  return norm_backward_of<float, float>(p, vec, n, stream);
+cudaError_t norm_backward_f32(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream) {
+  return norm_backward_of<float, float>(p, kind, n, stream);
 }
 
 }  // namespace mx

@@ -14,11 +14,11 @@
 // instructions per column pair and direction, so their number counts.
 // Measured on one GB300 (part of the measured copy bandwidth, 6.68 TB/s):
 //   forward   16384 x 7168 bf16: 157 us, 0.89; 8192 x 2048, FP32 stream, four
-//             gates: 34.7 us, 0.87; one row of 7168: 3.3 us, the latency of a
-//             launch, two loads and two sums; 777 x 1111 FP32: 4.6 us, 0.45
-//   gradient  16384 x 7168 bf16: 237 us, 0.89; 8192 x 2048, FP32 stream, four
+//             gates: 34.7 us, 0.87; one row of 7168: 3.1 us, the latency of a
+//             launch, two loads and two sums; 777 x 1111 FP32: 4.9 us, 0.42
+//   gradient  16384 x 7168 bf16: 236 us, 0.89; 8192 x 2048, FP32 stream, four
 //             gates: 60 us, 0.76 (5.5 us of it the sums over rows); 333 x 1111:
-//             10.6 us, three rows a block one after the other, then the sums
+//             10.5 us, three rows a block one after the other, then the sums
 #pragma once
 
 #include <cuda_bf16.h>
@@ -32,7 +32,7 @@
 
 namespace mx {
 
-// What the forward pass's arrays allow: 16-byte accesses from each row's first
+// What a pass's arrays allow: 16-byte accesses from each row's first
 // column on; from the same column of a row on in all of them (rows of an odd
 // length); neither.
 enum class NormRows { kAligned, kShifted, kAny };
@@ -89,13 +89,15 @@ __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 //         the row has exactly 8 NV threads columns;
 // kRuns   the same with an end inside (whole runs of eight);
 // kShift  run v is columns 8 (v threads + tid) - phase ..+7, with the row's phase
-//         (0..7) such that its runs lie on 16 bytes; first and last may be cut;
+//         (0..7) such that its runs lie on 16 bytes; first and last may be cut
+//         (`open`: they may be read whole, rows lie on either side);
 // kSingle element j of run v is column (8 v + j) threads + tid, one at a time.
 enum Mode { kWhole, kRuns, kShift, kSingle };
 
 template <Mode M>
 struct Cols {
   int32_t cols, tid, threads, phase = 0;
+  bool open = false;
   __device__ __forceinline__ int32_t at(int v, int j) const {
     return M == kSingle  ? (8 * v + j) * threads + tid
            : M == kShift ? 8 * (v * threads + tid) - phase + j
@@ -137,8 +139,8 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
   return v;
 }
 
-// Run v of a row; elements past its ends read as zero.  ONCE: a row of global
-// memory that is not read again.
+// Run v of a row; elements past its ends read as zero (of an open row: as
+// anything, until trimmed).  ONCE: a row of global memory that is not read again.
 template <typename T, Mode M>
 __device__ __forceinline__ Raw<T> load8_singly(const T* row, const Cols<M>& c, int v) {
   Raw<T> r;
@@ -156,10 +158,10 @@ template <bool ONCE = false, typename T, Mode M>
 __device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
   if constexpr (M == kSingle) return load8_singly(row, c, v);
   if constexpr (M == kShift)
-    if (!c.inside(v)) return load8_singly(row, c, v);
+    if (!c.open && !c.inside(v)) return load8_singly(row, c, v);
   Raw<T> r;
   uint4 x = make_uint4(0, 0, 0, 0), y = x;
-  if (M == kShift || c.has(v, 0)) {
+  if (M == kShift ? c.at(v, 0) < c.cols : c.has(v, 0)) {
     const uint4* p = reinterpret_cast<const uint4*>(row + c.at(v, 0));
     x = ONCE ? load_once(p) : p[0];
     if constexpr (sizeof(T) == 4) y = ONCE ? load_once(p + 1) : p[1];
@@ -173,6 +175,19 @@ __device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
     r.f[3] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
   }
   return r;
+}
+
+// Clears what lies past the row's ends.
+template <typename T, Mode M>
+__device__ __forceinline__ void trim(Raw<T>& r, const Cols<M>& c, int v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool a = c.has(v, 2 * i), b = c.has(v, 2 * i + 1);
+    if constexpr (sizeof(T) == 2)
+      r.w[i] = (a ? r.w[i] & 0xFFFFu : 0u) | (b ? r.w[i] & 0xFFFF0000u : 0u);
+    else
+      r.f[i] = make_float2(a ? r.f[i].x : 0.f, b ? r.f[i].y : 0.f);
+  }
 }
 
 // Run v of a weight or gate.  Under kShift it lies anywhere: the 16-byte
@@ -208,6 +223,14 @@ __device__ __forceinline__ Raw<T> load8_weight(const T* row, const Cols<M>& c, i
     }
     return r;
   }
+}
+
+// Asks for a row's lines, one a thread (rows have fewer lines than threads).
+template <typename T, Mode M>
+__device__ __forceinline__ void prefetch_row(const T* row, const Cols<M>& c) {
+  constexpr int kLine = 128 / sizeof(T);
+  if (c.tid * kLine < c.cols)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c.tid * kLine));
 }
 
 // f *= a run.
@@ -326,9 +349,12 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
   const uint32_t per = p.gate ? rows / static_cast<uint32_t>(p.gates) : 1u;
   Raw<C> b[NV];
   Raw<S> r[NV];
-  auto phase = [&](uint32_t t) {  // (of every array's row t the same)
-    const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const C*>(p.block) + t * p.ldb);
-    return M == kShift ? static_cast<int32_t>(row / sizeof(C) & 7u) : 0;
+  auto set_row = [&](Cols<M>& c, uint32_t t) {  // (of every array's row t the same)
+    if constexpr (M == kShift) {
+      const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const C*>(p.block) + t * p.ldb);
+      c.phase = static_cast<int32_t>(row / sizeof(C) & 7u);
+      c.open = t >= 8 && t + 8 < rows;
+    }
   };
   auto fetch = [&](uint32_t t, const Cols<M>& c) {
 #pragma unroll
@@ -337,12 +363,18 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
     for (int v = 0; v < NV; ++v) r[v] = load8<true>(static_cast<const S*>(p.residual) + t * p.ldr, c, v);
   };
   uint32_t t = blockIdx.x;
-  c.phase = phase(t);
+  set_row(c, t);
   fetch(t, c);
   while (true) {
     float sum[1];
     float2 sigma = both(1.f);
     Raw<W> w[NV] = {};
+#pragma unroll
+    for (int v = 0; M == kShift && v < NV; ++v)
+      if (!c.inside(v)) {
+        trim(b[v], c, v);
+        trim(r[v], c, v);
+      }
     if (p.w_post) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) w[v] = load8_weight(static_cast<const W*>(p.w_post), c, v);
@@ -376,7 +408,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
     for (int v = 0; v < NV; ++v) w[v] = load8_weight(static_cast<const W*>(p.w_pre), c, v);
     const uint32_t next = t + gridDim.x;
     Cols<M> c_next = c;
-    c_next.phase = phase(next);
+    set_row(c_next, next);
     if (next < rows) fetch(next, c_next);
     sum[0] = s.x + s.y;
     block_sum(sum, part[1]);
@@ -460,6 +492,9 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 // of D b sigma g over finished gates lie behind ring and factors, else in the workspace.
 // CL: blocks of a cluster that share a row (two for rows longer than a block's
 // registers hold, exchanging sums through distributed shared memory).
+// kShift: a thread's columns depend on the row's phase, so a gate's rows are
+// taken by phase (every `stride`-th row has the same), and after each phase the
+// sums go to shared memory by column.  Rows are read in place.
 template <typename C, typename S, typename W, Mode M, int NV, int CL>
 __global__ void __launch_bounds__(kBackThreads)
     norm_backward_kernel(const NormBackParams p, int stages, bool post) {
@@ -473,7 +508,8 @@ __global__ void __launch_bounds__(kBackThreads)
   const int32_t width = static_cast<int32_t>(p.cols);
   const int32_t half = CL == 1 ? width : (width / 8 + 1) / 2 * 8;
   const int32_t off = rank * half, mine = rank == 0 ? half : width - half;
-  const Cols<M> c{mine, static_cast<int32_t>(threadIdx.x), static_cast<int32_t>(blockDim.x)};
+  Cols<M> c{mine, static_cast<int32_t>(threadIdx.x), static_cast<int32_t>(blockDim.x)};
+  const Cols<M == kShift ? kWhole : M> slots{c.cols, c.tid, c.threads};  // of the factors
   const float inv_cols = 1.f / static_cast<float>(p.cols);
   const uint32_t n = gridDim.x / CL, me = blockIdx.x / CL, lane = lane_id();
   const RowShare share(static_cast<uint32_t>(p.rows), n);
@@ -521,7 +557,7 @@ __global__ void __launch_bounds__(kBackThreads)
     if constexpr (kHeld)
       times(f, held);
     else if (p.gate || p.w_post)
-      times(f, load8(behind, c, v));
+      times(f, load8(behind, slots, v));
   };
   float* finished = post ? behind + (kHeld ? 0 : half) : p.w_post ? ws_post(p, n, me) + off : nullptr;
   auto set_factors = [&](int64_t goff) {
@@ -536,21 +572,35 @@ __global__ void __launch_bounds__(kBackThreads)
       if constexpr (kHeld)
         held = r;
       else
-        store8(behind, c, v, r);
+        store8(behind, slots, v, r);
     }
   };
   const uint32_t group0 = lo / per;
   uint32_t group = group0, left = (group + 1) * per - lo;  // rows left of this gate
+  // kShift: the gate's rows [begin, end) of this block, their sums by column
+  const uint32_t stride = p.ldb & 1 ? 8u : p.ldb & 2 ? 4u : p.ldb & 4 ? 2u : 1u;
+  uint32_t begin = lo, end = hi - lo < left ? hi : lo + left;
+  float* pre_sum = behind + (kHeld ? 0 : 8 * NV * blockDim.x);
+  float* q_sum = pre_sum + mine;
+  auto set_phase = [&](uint32_t t) {  // (of every array's row t the same)
+    if constexpr (M == kShift)
+      c.phase = static_cast<int32_t>(
+          reinterpret_cast<uintptr_t>(static_cast<const C*>(p.block) + t * p.ldb) / sizeof(C) & 7u);
+  };
+  if constexpr (M == kShift)  // (the first row's barrier lies before the first use)
+    for (int i = c.tid; i < 2 * mine; i += c.threads) pre_sum[i] = 0.f;
+  set_phase(lo);
   if (p.gate || p.w_post) set_factors(group * p.cols + off);
   int stage = 0;
   uint32_t phase = 0;
-  for (uint32_t t = lo; t < hi; ++t) {
+  for (uint32_t t = lo, done = 0; t < hi; ++done) {
+    const uint32_t turn = (M == kShift ? done : t) & 1u;
     Raw<S> x[NV], a[NV] = {};
     Raw<C> y[NV], b[NV];
     constexpr bool kAhead = NV == 1 || sizeof(W) == 2;
     Raw<W> w_pre[NV];
 #pragma unroll
-    for (int v = 0; kAhead && v < NV; ++v) w_pre[v] = load8(static_cast<const W*>(p.w_pre) + off, c, v);
+    for (int v = 0; kAhead && v < NV; ++v) w_pre[v] = load8_weight(static_cast<const W*>(p.w_pre) + off, c, v);
     auto times_pre = [&](float2 (&f)[4], int v) {
       if constexpr (kAhead)
         times(f, w_pre[v]);
@@ -568,12 +618,28 @@ __global__ void __launch_bounds__(kBackThreads)
         if (p.d_res) a[v] = load8(reinterpret_cast<const S*>(src + 2 * cbytes + sbytes), c, v);
       }
     } else {
+      c.open = t >= 8 && t + 8 < static_cast<uint32_t>(p.rows);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         y[v] = load8<true>(static_cast<const C*>(p.dy) + t * p.lddy + off, c, v);
         b[v] = load8<true>(static_cast<const C*>(p.block) + t * p.ldb + off, c, v);
         x[v] = load8<true>(static_cast<const S*>(p.res_out) + t * p.ldr + off, c, v);
         if (p.d_res) a[v] = load8<true>(static_cast<const S*>(p.d_res) + t * p.ldd + off, c, v);
+      }
+#pragma unroll
+      for (int v = 0; M == kShift && v < NV; ++v)
+        if (!c.inside(v)) {
+          trim(y[v], c, v);
+          trim(b[v], c, v);
+          trim(x[v], c, v);
+          trim(a[v], c, v);
+        }
+      const uint32_t soon = t + (M == kShift ? stride : 1u);
+      if (soon < (M == kShift ? end : hi)) {
+        prefetch_row(static_cast<const C*>(p.dy) + soon * p.lddy + off, c);
+        prefetch_row(static_cast<const C*>(p.block) + soon * p.ldb + off, c);
+        prefetch_row(static_cast<const S*>(p.res_out) + soon * p.ldr + off, c);
+        if (p.d_res) prefetch_row(static_cast<const S*>(p.d_res) + soon * p.ldd + off, c);
       }
     }
     float2 s2[kRowSums];
@@ -612,7 +678,7 @@ __global__ void __launch_bounds__(kBackThreads)
     sums[6] = sums[7] = 0.f;
     float s = warp_sum8(sums);
     const uint32_t warps = blockDim.x / 32;
-    float* to = &part[t & 1][(rank * warps + warp_id()) * 8 + lane / 4];
+    float* to = &part[turn][(rank * warps + warp_id()) * 8 + lane / 4];
     if constexpr (CL == 1) {
       if ((lane & 3) == 0) *to = s;
       __syncthreads();
@@ -634,7 +700,7 @@ __global__ void __launch_bounds__(kBackThreads)
     s = 0.f;
 #pragma unroll
     for (uint32_t w = 0; w < CL * kBackThreads / 32; w += 4)
-      if (w < CL * warps) s += part[t & 1][(w + lane / 8) * 8 + lane % 8];
+      if (w < CL * warps) s += part[turn][(w + lane / 8) * 8 + lane % 8];
     s += __shfl_xor_sync(0xffffffffu, s, 8);
     s += __shfl_xor_sync(0xffffffffu, s, 16);
 #pragma unroll
@@ -666,6 +732,46 @@ __global__ void __launch_bounds__(kBackThreads)
         for (int i = 0; i < 4; ++i) d[i] = fma2(b[v].get(i), m, mul2(sigma, d[i]));
       }
       store8(static_cast<C*>(p.d_block) + t * p.lddb + off, c, v, round8<C>(d));
+    }
+    if constexpr (M == kShift) {
+      t += stride;
+      if (t < end) continue;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (c.has(v, i)) {
+            pre_sum[c.at(v, i)] += i % 2 ? pre[v][i / 2].y : pre[v][i / 2].x;
+            q_sum[c.at(v, i)] += i % 2 ? q[v][i / 2].y : q[v][i / 2].x;
+          }
+          if (i % 2) pre[v][i / 2] = q[v][i / 2] = both(0.f);
+        }
+      // the next phase's first row; a gate's rows end behind its last phase
+      const uint32_t next = (t - begin) % stride + 1;
+      t = begin + next;
+      if (next == stride || t >= end) {
+        __syncthreads();
+        if (p.gate) {
+          const int64_t goff = group * p.cols;
+          const bool whole = group * per >= lo && end == (group + 1) * per;
+          float* dst = whole ? p.d_gate + goff : ws_gate(p, n, 2 * me + (group == group0 ? 0 : 1));
+          const W* w_post = static_cast<const W*>(p.w_post);
+          const W* gate = static_cast<const W*>(p.gate) + goff;
+          for (int i = c.tid; i < mine; i += c.threads) {
+            const float sum = q_sum[i], g = sum * to_float(gate[i]);
+            dst[i] = w_post ? sum * to_float(w_post[i]) : sum;
+            if (p.gates > 1 && w_post) finished[i] = group != group0 ? finished[i] + g : g;
+            q_sum[i] = p.gates > 1 ? 0.f : g;
+          }
+        }
+        if (end == hi) break;
+        ++group;
+        begin = t = end;
+        end = hi - begin < per ? hi : begin + per;
+      }
+      set_phase(t);
+      if (p.gate || p.w_post) set_factors(group * p.cols);
+      continue;
     }
     if (--left == 0 || t + 1 == hi) {  // the gate's rows, or this block's, end here
       if (p.gate) {
@@ -699,6 +805,15 @@ __global__ void __launch_bounds__(kBackThreads)
       left = per;
       if (p.gate && t + 1 < hi) set_factors(group * p.cols + off);
     }
+    ++t;
+  }
+  if constexpr (M == kShift) {
+    float *pre_out = ws_pre(p, me), *post_out = ws_post(p, n, me);
+    for (int i = c.tid; i < mine; i += c.threads) {
+      pre_out[i] = pre_sum[i];
+      if (p.w_post && p.gates <= 1) post_out[i] = q_sum[i];
+    }
+    return;
   }
   if (stages > 0 && *s_abort) {  // a wait gave up: copies still in flight must land first
     for (uint32_t s = 0; s < static_cast<uint32_t>(stages) && lo + s < hi; ++s)
@@ -723,10 +838,10 @@ __global__ void __launch_bounds__(kBackThreads)
   }
 }
 
-// The gradient for rows of more than 4096 columns that are not on 16-byte
-// boundaries: element by element (16384 x 5001: 700 us, a fifth of the copy
-// bandwidth, bound by its accesses; shorter ones keep their columns in registers,
-// 16384 x 4095: 445 us, here 586), with the column sums of w_pre and D b sigma and the row's u in shared memory
+// The gradient for rows of more than 4096 columns that neither lie on 16-byte
+// boundaries nor can go by phase: element by element (16384 x 5001: 700 us, a
+// fifth of the copy bandwidth, bound by its accesses; shorter ones keep their
+// columns in registers, 16384 x 4095: 404 us, here 586), with the column sums of w_pre and D b sigma and the row's u in shared memory
 // (cols floats each).  Sums over finished gates (gates > 1) grow in the
 // workspace.  A thread goes through the same columns everywhere, so no two
 // threads touch the same sum.
@@ -900,8 +1015,8 @@ cudaError_t forward_runs(const NormParams& p, NormRows kind, int num_sms, cudaSt
 // 1.58 against 1.73); up to 4096 two (8192 rows of 2048: 22.5, with one 25.5,
 // with four 23.6); above that four (16384 x 7168: 157, with one 238).
 // Shifted rows load every weight in two pieces and move it, which waits: one
-// run to 2048 (777 x 1111: 4.3 us, with two 5.2; 16384 x 2049: 83.6 and 76.6).
-// Element by element the same rows take 5.7 and 135 us.
+// run to 2048 (777 x 1111: 4.3 us, with two 5.2; 16384 x 2049: 83.6 and 76.6,
+// now 69.8).  Element by element the same rows take 5.7 and 135 us.
 template <typename C, typename S, typename W>
 cudaError_t forward(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
   if (kind == NormRows::kAny)
@@ -931,9 +1046,22 @@ struct BackPlan {
   int runs, cluster, threads, fit, stages;
   size_t smem, post;
 };
-BackPlan backward_plan(int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, bool vec) {
+constexpr int64_t kOneRun = 8 * kBackThreads;
+constexpr int64_t kShiftCols = 2 * kOneRun - 7;  // what two runs hold wherever they begin
+BackPlan backward_plan(int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, NormRows kind) {
   BackPlan p;
-  constexpr int64_t kOneRun = 8 * kBackThreads;
+  const bool vec = kind == NormRows::kAligned;
+  if (kind == NormRows::kShifted) {
+    p.cluster = 1, p.stages = 0, p.post = 0;
+    p.runs = cols + 7 <= kOneRun ? 1 : 2;
+    if (p.runs == 1 && kBackThreads % row_threads(cols + 7, 1) >= kBackThreads / 4) p.runs = 2;
+    p.threads = row_threads(cols + 7, p.runs);
+    p.smem = static_cast<size_t>(cols) * 8 + (p.runs == 2 ? 64 * static_cast<size_t>(p.threads) : 0);
+    p.fit = kBackThreads / p.threads;
+    p.fit = p.fit > 8 ? 8 : p.fit;
+    while (p.fit > 1 && p.smem > smem_of(p.fit)) --p.fit;
+    return p;
+  }
   if (!vec && cols > kOneRun) {  // by shared memory
     p.runs = 0, p.cluster = 1, p.stages = 0;
     p.threads = kBackThreads;
@@ -1020,10 +1148,13 @@ cudaError_t backward_single(const NormBackParams& p, const BackPlan& plan, int64
 }
 
 template <typename C, typename S, typename W>
-cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, int64_t n,
+cudaError_t backward(const NormBackParams& p, NormRows kind, const BackPlan& plan, int64_t n,
                      cudaStream_t stream) {
   if (plan.runs == 0) return backward_single<C, S>(p, plan, n, stream);
-  if (!vec) return backward_impl<C, S, W, kSingle, 1, 1>(p, plan, n, stream);
+  if (kind == NormRows::kAny) return backward_impl<C, S, W, kSingle, 1, 1>(p, plan, n, stream);
+  if (kind == NormRows::kShifted)
+    return plan.runs == 1 ? backward_impl<C, S, W, kShift, 1, 1>(p, plan, n, stream)
+                          : backward_impl<C, S, W, kShift, 2, 1>(p, plan, n, stream);
   if (plan.cluster == 2) return backward_impl<C, S, W, kRuns, 2, 2>(p, plan, n, stream);
   if (plan.runs == 1)
     return whole(p.cols, 1) ? backward_impl<C, S, W, kWhole, 1, 1>(p, plan, n, stream)
@@ -1034,18 +1165,17 @@ cudaError_t backward(const NormBackParams& p, bool vec, const BackPlan& plan, in
 
 }  // namespace
 
-// Forward and gradient for blocks of type C and a stream of type S; vec: the
-// gradient's rows and pointers allow 16-byte accesses.
+// Forward and gradient for blocks of type C and a stream of type S.
 template <typename C, typename S>
 cudaError_t norm_forward_of(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
   return p.w_fp32 ? forward<C, S, float>(p, kind, num_sms, stream)
                   : forward<C, S, bf16>(p, kind, num_sms, stream);
 }
 template <typename C, typename S>
-cudaError_t norm_backward_of(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
-  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, vec);
-  return p.w_fp32 ? backward<C, S, float>(p, vec, plan, n, stream)
-                  : backward<C, S, bf16>(p, vec, plan, n, stream);
+cudaError_t norm_backward_of(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream) {
+  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
+  return p.w_fp32 ? backward<C, S, float>(p, kind, plan, n, stream)
+                  : backward<C, S, bf16>(p, kind, plan, n, stream);
 }
 
 }  // namespace mx

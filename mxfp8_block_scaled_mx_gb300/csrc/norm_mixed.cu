@@ -7,8 +7,8 @@ cudaError_t norm_forward_mixed(const NormParams& p, NormRows kind, int num_sms, 
   return norm_forward_of<bf16, float>(p, kind, num_sms, stream);
 }
 
-cudaError_t norm_backward_mixed(const NormBackParams& p, bool vec, int64_t n, cudaStream_t stream) {
-  return norm_backward_of<bf16, float>(p, vec, n, stream);
+cudaError_t norm_backward_mixed(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream) {
+  return norm_backward_of<bf16, float>(p, kind, n, stream);
 }
 
 }  // namespace mx

@@ -376,3 +376,43 @@ def test_rows_off_16_bytes(mx, cols, ld, c, s, w):
 def test_gradient_rows_of_one_or_two_runs(mx, cols, c, s, w):
     for rows, gates in ((1, 0), (40, 0), (700, 7), (650, 1)):
         check_backward(mx, inputs(rows, cols, c, s, w, True, gates, seed=cols), 0.5)
+
+
+@pytest.mark.parametrize("cols,ld", [(1, 1), (3, 11), (33, 34), (130, 130), (132, 140), (1018, 1026),
+                                     (1111, 1111), (1000, 1000), (2049, 2057), (4089, 4089),
+                                     (4090, 4098), (8185, 8185), (8186, 8186)])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_gradient_rows_off_16_bytes(mx, cols, ld, c, s, w):
+    """Rows that begin anywhere, in step in all arrays or not; gates of few and
+    many rows, none; more rows than blocks and fewer."""
+    for rows, gates, base in ((1, 0, 0), (7, 0, 8), (17, 1, 0), (96, 2, 3), (97, 97, 0), (640, 16, 8),
+                              (1300, 0, 0), (1300, 13, 0)):
+        if rows * cols > 3_000_000:
+            rows, gates = 320, min(gates, 4)
+        d = inputs(rows, cols, c, s, w, True, gates, seed=rows + cols)
+        d["w_pre"] = placed(d["w_pre"][None], cols, 3)[0][0]
+        d["w_post"] = placed(d["w_post"][None], cols, 5)[0][0]
+        for n in ("block", "residual", "d_residual", "d_y"):
+            d[n] = placed(d[n], ld, base)[0]
+        got = check_backward(mx, d, 0.875)
+        again = check_backward(mx, d, 0.875)
+        for name in ("block", "residual", "w_pre", "w_post", "gate"):
+            a, b = getattr(got, name), getattr(again, name)
+            assert a is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,cols,gates", [(9800, 1111, 0), (9800, 1026, 350), (9744, 1028, 1),
+                                             (300, 4101, 0), (320, 5002, 20), (330, 4100, 1),
+                                             (700, 7999, 7)])
+@pytest.mark.parametrize("c,s,w", TYPES[:3])
+def test_gradient_of_many_rows_off_16_bytes(mx, rows, cols, gates, c, s, w):
+    """Rows by phase: eight, four and two phases, gates of one run of rows and
+    of many, within blocks and across."""
+    d = inputs(rows, cols, c, s, w, True, gates, seed=rows + cols, pad=0 if cols % 4 else 1)
+    if cols % 4 == 0:                                    # in step, off 16 bytes by the weights alone
+        for n in ("block", "residual", "d_residual", "d_y"):
+            d[n] = placed(d[n].contiguous(), cols + 8, 8)[0]
+        d["w_pre"] = placed(d["w_pre"][None], cols, 3)[0][0]
+    got = check_backward(mx, d, 0.875)
+    again = check_backward(mx, d, 0.875)
+    assert torch.equal(got.w_pre, again.w_pre) and torch.equal(got.w_post, again.w_post)

@@ -82,7 +82,8 @@ static_assert(kTerms * kMaxTokens <= kTile, "the scales of all rows in one tile"
 static_assert(2 * 192 + kMaxStages * 8 <= 512, "tensor memory: two sets and the scales");
 
 // Workspace: the count of finished activation items (its first word), logits,
-// x's records, the activations' records, parts.  A block's part: gates and ups of one item of phase 1, then one item of phase 2.
+// x's records, the activations' records, parts.  A block's part: gates and ups of
+// one item of phase 1, then one item of phase 2.
 __host__ __device__ constexpr int64_t part_floats(int tokens) { return int64_t(3) * tokens * kTile; }
 struct Layout {
   int64_t logits, x, h, parts, bytes;

@@ -104,7 +104,7 @@ size_t norm_backward_workspace(int64_t rows, int64_t cols, int64_t gates) {
   for (int i = 0; i < 4; ++i)
     for (NormRows kind : {NormRows::kAligned, NormRows::kShifted, NormRows::kAny}) {
       if (kind == NormRows::kShifted && cols > kShiftCols) continue;
-      const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(cols, gates, i & 1, i & 2, kind));
+      const int64_t m = backward_blocks(rows, kMaxSms, backward_plan(rows, cols, gates, i & 1, i & 2, kind));
       n = m > n ? m : n;
     }
   return static_cast<size_t>(n) * (gates > 0 ? 4 : 2) * static_cast<size_t>(cols) * 4;
@@ -172,7 +172,7 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
         step.with(p.d_block, p.lddb, p.c_fp32) && step.with(p.d_residual, p.lddr, p.s_fp32))
       kind = NormRows::kShifted;
   }
-  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
+  const BackPlan plan = backward_plan(p.rows, p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
   const int64_t n = backward_blocks(p.rows, num_sms < kMaxSms ? num_sms : kMaxSms, plan);
   cudaError_t err;
   if (p.c_fp32)

@@ -16,9 +16,9 @@
 //   forward   16384 x 7168 bf16: 157 us, 0.89; 8192 x 2048, FP32 stream, four
 //             gates: 34.7 us, 0.87; one row of 7168: 3.1 us, the latency of a
 //             launch, two loads and two sums; 777 x 1111 FP32: 4.9 us, 0.42
-//   gradient  16384 x 7168 bf16: 236 us, 0.89; 8192 x 2048, FP32 stream, four
-//             gates: 60 us, 0.76 (5.5 us of it the sums over rows); 333 x 1111:
-//             10.5 us, three rows a block one after the other, then the sums
+//   gradient  16384 x 7168 bf16: 217 us, 0.97; 8192 x 2048, FP32 stream, four
+//             gates: 55 us, 0.82 (5.5 us of it the sums over rows); 333 x 1111:
+//             10.5 us, a row's latency, then the sums over 333 parts
 #pragma once
 
 #include <cuda_bf16.h>
@@ -177,7 +177,8 @@ __device__ __forceinline__ Raw<T> load8(const T* row, const Cols<M>& c, int v) {
   return r;
 }
 
-// Clears what lies past the row's ends.
+// Clears what lies past the row's ends (rows beside it, which another block may
+// be writing in place: nothing of it is used).
 template <typename T, Mode M>
 __device__ __forceinline__ void trim(Raw<T>& r, const Cols<M>& c, int v) {
 #pragma unroll
@@ -487,9 +488,10 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 // registers across one barrier instead of two with re-reads 306 -> 278.)
 // A thread also keeps the sums of its columns over the rows and the factors
 // w_post g of its columns for the current gate, which every row wants twice (in
-// FP32; with two runs a thread behind the ring).  w_pre (from L1) is asked for before the wait for the
-// row, where registers hold it that long.  `post` (more gates than one): the sums
-// of D b sigma g over finished gates lie behind ring and factors, else in the workspace.
+// FP32, the first run's in registers, the second's behind the ring).  w_pre (from
+// L1) is asked for before the wait for the row, where registers hold it that long.
+// `post` (more gates than one): the sums of D b sigma g over finished gates lie
+// behind ring and factors, else in the workspace.
 // CL: blocks of a cluster that share a row (two for rows longer than a block's
 // registers hold, exchanging sums through distributed shared memory).
 // kShift: a thread's columns depend on the row's phase, so a gate's rows are
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kBackThreads)
   const int32_t half = CL == 1 ? width : (width / 8 + 1) / 2 * 8;
   const int32_t off = rank * half, mine = rank == 0 ? half : width - half;
   Cols<M> c{mine, static_cast<int32_t>(threadIdx.x), static_cast<int32_t>(blockDim.x)};
-  const Cols<M == kShift ? kWhole : M> slots{c.cols, c.tid, c.threads};  // of the factors
+  const Cols<M == kSingle ? M : kWhole> slots{c.cols, c.tid, c.threads};  // of the factors
   const float inv_cols = 1.f / static_cast<float>(p.cols);
   const uint32_t n = gridDim.x / CL, me = blockIdx.x / CL, lane = lane_id();
   const RowShare share(static_cast<uint32_t>(p.rows), n);
@@ -550,16 +552,17 @@ __global__ void __launch_bounds__(kBackThreads)
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) pre[v][i] = q[v][i] = both(0.f);
-  constexpr bool kHeld = NV == 1;                          // factors in registers
+  constexpr int kHeld = M == kShift && NV > 1 ? 0 : 1;       // runs with factors in registers
   Raw<float> held = {{both(1.f), both(1.f), both(1.f), both(1.f)}};
-  float* behind = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  float* factor = reinterpret_cast<float*>(smem + stages * stage_bytes);
   auto times_factor = [&](float2 (&f)[4], int v) {
-    if constexpr (kHeld)
+    if (v < kHeld)
       times(f, held);
     else if (p.gate || p.w_post)
-      times(f, load8(behind, slots, v));
+      times(f, load8(factor, slots, v - kHeld));
   };
-  float* finished = post ? behind + (kHeld ? 0 : half) : p.w_post ? ws_post(p, n, me) + off : nullptr;
+  float* past = factor + 8 * (NV - kHeld) * blockDim.x;
+  float* finished = post ? past : p.w_post ? ws_post(p, n, me) + off : nullptr;
   auto set_factors = [&](int64_t goff) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -569,10 +572,10 @@ __global__ void __launch_bounds__(kBackThreads)
       if (p.gate) times_w<W>(f, p.gate, goff, c, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) r.f[i] = f[i];
-      if constexpr (kHeld)
+      if (v < kHeld)
         held = r;
       else
-        store8(behind, slots, v, r);
+        store8(factor, slots, v - kHeld, r);
     }
   };
   const uint32_t group0 = lo / per;
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(kBackThreads)
   // kShift: the gate's rows [begin, end) of this block, their sums by column
   const uint32_t stride = p.ldb & 1 ? 8u : p.ldb & 2 ? 4u : p.ldb & 4 ? 2u : 1u;
   uint32_t begin = lo, end = hi - lo < left ? hi : lo + left;
-  float* pre_sum = behind + (kHeld ? 0 : 8 * NV * blockDim.x);
+  float* pre_sum = past;
   float* q_sum = pre_sum + mine;
   auto set_phase = [&](uint32_t t) {  // (of every array's row t the same)
     if constexpr (M == kShift)
@@ -1031,8 +1034,12 @@ cudaError_t forward(const NormParams& p, NormRows kind, int num_sms, cudaStream_
 
 constexpr int kMaxSms = 192;         // workspaces are sized for this many
 // Shared memory for rings, factors and sums of one of `fit` blocks on an SM (228 KB
-// in all; a block has 2 KB of its own beside these).
-constexpr size_t kSmemBytes = 206 * 1024;
+// in all; a block has 2 KB of its own beside these).  One block alone takes no
+// more than 161 KB: what it leaves is L1, where w_pre is read for every row
+// (16384 x 7168: a ring of two rows 218 us, of three 224 and with all of the
+// memory 234; x 12288: 538, with a row more 577 to 637).
+constexpr size_t kSmemBytes = 161 * 1024;
+constexpr size_t kSmemMost = 12 * 16384;  // (row by row element by element)
 constexpr size_t smem_of(int fit) {
   const size_t share = 228 * 1024 / fit - 2304;
   return share < kSmemBytes ? share : kSmemBytes;
@@ -1048,7 +1055,7 @@ struct BackPlan {
 };
 constexpr int64_t kOneRun = 8 * kBackThreads;
 constexpr int64_t kShiftCols = 2 * kOneRun - 7;  // what two runs hold wherever they begin
-BackPlan backward_plan(int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, NormRows kind) {
+BackPlan backward_plan(int64_t rows, int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, NormRows kind) {
   BackPlan p;
   const bool vec = kind == NormRows::kAligned;
   if (kind == NormRows::kShifted) {
@@ -1070,30 +1077,35 @@ BackPlan backward_plan(int64_t cols, int64_t gates, bool c_fp32, bool s_fp32, No
     p.fit = p.smem <= smem_of(2) ? 2 : 1;
     return p;
   }
-  // by registers (128 a thread) and rings of three rows.  A thread holds two
+  // by registers (128 a thread) and rings.  A thread holds two
   // runs where a row takes more than 512; where blocks with one would leave a
-  // quarter of the SM's 512 threads idle (16384 x 2560 in bf16: 89 us, with one
-  // run 161; x 1536: 58 and 84); and where the SM then holds two such blocks with
-  // their rings instead of one (x 3584: 120 and 144).  Else one: its factors stay
-  // in registers (x 2048: 73, with two 76; x 2048, FP32 stream: 105 and 108).
+  // quarter of the SM's 512 threads idle (16384 x 2560 in bf16: 89 us, with one run
+  // 161; x 1536: 58 and 84); and with many rows where the SM then holds two such
+  // blocks with their rings instead of one (x 4096: 130 and 145; x 3584: 115 and
+  // 144).  Else one (100 x 4096: 7.2, with two 8.6; 16384 x 2048: 73 and 76).
   p.cluster = cols <= 2 * kOneRun ? 1 : 2;
   const int64_t mine = p.cluster == 1 ? cols : (cols / 8 + 1) / 2 * 8;
   p.runs = mine <= kOneRun ? 1 : 2;
   const size_t stage = mine * 2 * ((c_fp32 ? 4 : 2) + (s_fp32 ? 4 : 2));
-  const size_t factors = static_cast<size_t>(mine) * 4;
-  if (vec && p.runs == 1 && (kBackThreads % row_threads(mine, 1) >= kBackThreads / 4 ||
-                             (mine > 2048 && factors + 3 * stage <= smem_of(2))))
+  const size_t factors = 32 * static_cast<size_t>(row_threads(mine, 2));  // of two runs: the second's
+  if (vec && p.runs == 1 &&
+      (kBackThreads % row_threads(mine, 1) >= kBackThreads / 4 ||
+       (mine > 2048 && rows > 2 * kMaxSms && factors + 3 * stage <= smem_of(2))))
     p.runs = 2;
   p.threads = row_threads(mine, p.runs);
   p.fit = kBackThreads / p.threads;
   p.fit = p.fit > 8 ? 8 : p.fit;
   p.stages = 0;
-  p.post = gates > 1 ? factors : 0;
+  p.post = gates > 1 ? static_cast<size_t>(mine) * 4 : 0;
   p.smem = p.runs == 2 ? factors : 0;
   if (vec) {
-    while (p.fit > 1 && p.smem + 3 * stage > smem_of(p.fit)) --p.fit;
-    const size_t rows = (smem_of(p.fit) - p.smem) / stage;
-    p.stages = rows < 2 ? 0 : rows > 4 ? 4 : static_cast<int>(rows);
+    // Rows of a ring: two for short rows, of which an SM has several under way
+    // (16384 x 2048, FP32 stream: 95 us, with three 108, with four 105; x 1024:
+    // 52.8 and 56.5), else three or four (x 4096: 130, with two 141).
+    const bool few = mine <= 2560;
+    while (p.fit > 1 && p.smem + (few ? 2 : 3) * stage > smem_of(p.fit)) --p.fit;
+    const size_t ring = (smem_of(p.fit) - p.smem) / stage, most = few ? 2 : 4;
+    p.stages = ring < 2 ? 0 : static_cast<int>(ring < most ? ring : most);
     p.smem += p.stages * stage;
   }
   if (p.smem + p.post > smem_of(p.fit)) p.post = 0;
@@ -1111,7 +1123,7 @@ template <typename K>
 cudaError_t allow_smem(PerDeviceOnce& setup, K kern) {
   return setup.run([&]() -> cudaError_t {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kSmemBytes));
+                                static_cast<int>(kSmemMost));
   });
 }
 
@@ -1173,7 +1185,7 @@ cudaError_t norm_forward_of(const NormParams& p, NormRows kind, int num_sms, cud
 }
 template <typename C, typename S>
 cudaError_t norm_backward_of(const NormBackParams& p, NormRows kind, int64_t n, cudaStream_t stream) {
-  const BackPlan plan = backward_plan(p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
+  const BackPlan plan = backward_plan(p.rows, p.cols, p.gates, p.c_fp32, p.s_fp32, kind);
   return p.w_fp32 ? backward<C, S, float>(p, kind, plan, n, stream)
                   : backward<C, S, bf16>(p, kind, plan, n, stream);
 }

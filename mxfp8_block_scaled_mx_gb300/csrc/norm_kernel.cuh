@@ -13,7 +13,7 @@
 // columns an instruction (f32x2): at memory speed a row leaves an SM about 20
 // instructions per column pair and direction, so their number counts.
 // Measured on one GB300 (part of the measured copy bandwidth, 6.68 TB/s):
-//   forward   16384 x 7168 bf16: 157 us, 0.89; 8192 x 2048, FP32 stream, four
+//   forward   16384 x 7168 bf16: 155 us, 0.91; 8192 x 2048, FP32 stream, four
 //             gates: 34.7 us, 0.87; one row of 7168: 3.1 us, the latency of a
 //             launch, two loads and two sums; 777 x 1111 FP32: 4.9 us, 0.42
 //   gradient  16384 x 7168 bf16: 217 us, 0.97; 8192 x 2048, FP32 stream, four
@@ -247,7 +247,16 @@ __device__ __forceinline__ void times_w(float2 (&f)[4], const void* w, int64_t o
   times(f, load8_weight(static_cast<const W*>(w) + off, c, v));
 }
 
-template <typename T, Mode M>
+__device__ __forceinline__ void store_once(uint4* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// ONCE: a bf16 row of global memory that takes no place in L1 (16384 x 4096: 81.6
+// us, with a place 83.3; FP32 rows are written in two halves that L1 joins:
+// 16384 x 7168 with an FP32 stream 217, past L1 221).
+template <bool ONCE = false, typename T, Mode M>
 __device__ __forceinline__ void store8(T* row, const Cols<M>& c, int v, const Raw<T>& r) {
   if (M == kSingle || (M == kShift && !c.inside(v))) {
 #pragma unroll
@@ -262,7 +271,11 @@ __device__ __forceinline__ void store8(T* row, const Cols<M>& c, int v, const Ra
     if (!c.has(v, 0)) return;
     uint4* p = reinterpret_cast<uint4*>(row + c.at(v, 0));
     if constexpr (sizeof(T) == 2) {
-      p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      const uint4 x = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      if constexpr (ONCE)
+        store_once(p, x);
+      else
+        *p = x;
     } else {
       p[0] = make_uint4(__float_as_uint(r.f[0].x), __float_as_uint(r.f[0].y),
                         __float_as_uint(r.f[1].x), __float_as_uint(r.f[1].y));
@@ -401,7 +414,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = fma2(alpha, r[v].get(i), f[i]);
       out[v] = round8<S>(f);
-      store8(static_cast<S*>(p.res_out) + t * p.ldo, c, v, out[v]);
+      store8<true>(static_cast<S*>(p.res_out) + t * p.ldo, c, v, out[v]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(out[v].get(i), out[v].get(i), s);
     }
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(MAXT) norm_residual_kernel(const NormParams p)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = mul2(out[v].get(i), rho);
       times(f, w[v]);
-      store8(static_cast<C*>(p.y) + t * p.ldy, c, v, round8<C>(f));
+      store8<true>(static_cast<C*>(p.y) + t * p.ldy, c, v, round8<C>(f));
     }
     if (next >= rows) return;
     t = next;
@@ -1004,7 +1017,7 @@ cudaError_t forward_impl(const NormParams& p, int num_sms, cudaStream_t stream) 
   return launch(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p);
 }
 
-// (kWhole spares the test for the row's end: 16384 x 7168 157 us, as kRuns 162.)
+// (kWhole spares the test for the row's end: 16384 x 7168 157 us against 162.)
 template <typename C, typename S, typename W, int NV, int MAXT>
 cudaError_t forward_runs(const NormParams& p, NormRows kind, int num_sms, cudaStream_t stream) {
   if (kind == NormRows::kShifted) return forward_impl<C, S, W, kShift, NV, MAXT>(p, num_sms, stream);

@@ -42,9 +42,9 @@
 //   16 tokens, hidden 7168, 56 of 64 experts of 2048:       384 us, 1.00
 //   64 tokens, hidden 4096, 64 experts of 1536:             223 us, 0.84 (the
 //       router kernel's 8 us, SMs that differ by 5 % in speed, and the last join)
-//   1 token, hidden 2048, 8 of 128 experts of 768:          18.8 us, 0.31 (a chain
+//   1 token, hidden 2048, 8 of 128 experts of 768:          18.2 us, 0.32 (a chain
 //       of latencies: logits 4, routing 2, first tiles, two joins of 2.5 each)
-//   1 token, hidden 7168, 8 experts of 2048, 4-bit weights: 47.1 us, 0.60 (about 9
+//   1 token, hidden 7168, 8 experts of 2048, 4-bit weights: 45.6 us, 0.62 (about 8
 //       of it that chain; 4-bit tiles alone, without MMAs, tokens and scales, take
 //       41: they come at 0.85 of the copy bandwidth, 64 bytes of a row each)
 #include <cuda.h>
@@ -168,7 +168,7 @@ __device__ __forceinline__ void write_block(uint8_t* record, int pad, uint32_t t
 
 constexpr int kRouterThreads = 256;
 constexpr uint32_t kClearUnits = 16 * kRouterThreads;  // of 16 bytes, per block
-constexpr int kRouterExperts = 2;   // per block, four warps each
+constexpr int kRouterWarps = kRouterThreads / 32;  // a block's, shared by one or two experts
 constexpr int kRouterTokens = 8;    // per block: the router's rows are read tokens / 8 times
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
@@ -180,9 +180,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
-// Logits of expert e for tokens t0 .. t0 + nt - 1 (nt <= T), the share of the
-// warp's quarter of the row, complete in every lane.
-template <int T>
+// Logits of expert e for tokens t0 .. t0 + nt - 1 (nt <= T), the part of the row
+// of this warp of PARTS, complete in every lane.
+template <int T, int PARTS>
 __device__ __forceinline__ void dot_tokens(const MoeFewParams& p, int e, int t0, int nt,
                                            float (&sum)[kRouterTokens]) {
   const __nv_bfloat16* x[T];
@@ -191,7 +191,8 @@ __device__ __forceinline__ void dot_tokens(const MoeFewParams& p, int e, int t0,
     x[i] = static_cast<const __nv_bfloat16*>(p.x) + (t0 + (i < nt ? i : nt - 1)) * p.ldx;
   const int64_t row = static_cast<int64_t>(e) * p.hidden;
 #pragma unroll 2
-  for (int c = static_cast<int>((warp_id() & 3) * 32 + lane_id()) * 8; c < p.hidden; c += 4 * 32 * 8) {
+  for (int c = static_cast<int>((warp_id() & (PARTS - 1)) * 32 + lane_id()) * 8; c < p.hidden;
+       c += PARTS * 32 * 8) {
     uint4 raw[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) raw[i] = *reinterpret_cast<const uint4*>(x[i] + c);
@@ -218,14 +219,15 @@ __device__ __forceinline__ void dot_tokens(const MoeFewParams& p, int e, int t0,
     for (int i = 0; i < T; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
 }
 
-// The router's part is latency: 128 experts x 2048 for one token 3.5 us, of which
+// The router's part is latency: 128 experts x 2048 for one token 3 us, of which
 // the launch takes half; rows of x and router are read in 16-byte pieces, and
 // tokens beyond one share the router's (one token alone: layer 18.9 us, by the
 // form for eight 19.8).  The parts are set by blocks of their own: by the blocks
 // that form logits the layer took 1 to 4 us longer.
-// Blocks [0, logit_blocks): logits of two experts for eight tokens.  The next
+// Blocks [0, logit_blocks): logits of EACH experts for eight tokens.  The next
 // record_blocks: x's records, a warp per token and K tile.  The rest: parts of
 // part_units 16-byte units in all set to kNoSum.  Block 0 also clears the counter.
+template <int EACH>
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFewParams p,
                                                                     int logit_blocks,
                                                                     int record_blocks,
@@ -263,8 +265,9 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
     for (int j = 0; j < 4; ++j) write_block(record, pad, t, j, v[j]);
     return;
   }
-  const int groups = (p.experts + kRouterExperts - 1) / kRouterExperts;
-  const int e = static_cast<int>(blockIdx.x) % groups * kRouterExperts + static_cast<int>(warp) / 4;
+  constexpr int kParts = kRouterWarps / EACH;
+  const int groups = (p.experts + EACH - 1) / EACH;
+  const int e = static_cast<int>(blockIdx.x) % groups * EACH + static_cast<int>(warp) / kParts;
   const int t0 = static_cast<int>(blockIdx.x) / groups * kRouterTokens;
   const int nt = p.tokens - t0 < kRouterTokens ? p.tokens - t0 : kRouterTokens;
   float sum[kRouterTokens];
@@ -272,20 +275,20 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeFew
   for (int i = 0; i < kRouterTokens; ++i) sum[i] = 0.f;
   if (e < p.experts) {
     if (nt == 1)
-      dot_tokens<1>(p, e, t0, nt, sum);
+      dot_tokens<1, kParts>(p, e, t0, nt, sum);
     else if (nt <= 4)
-      dot_tokens<4>(p, e, t0, nt, sum);
+      dot_tokens<4, kParts>(p, e, t0, nt, sum);
     else
-      dot_tokens<kRouterTokens>(p, e, t0, nt, sum);
+      dot_tokens<kRouterTokens, kParts>(p, e, t0, nt, sum);
   }
 #pragma unroll
   for (int i = 0; i < kRouterTokens; ++i)
     if (lane == 0) part[warp][i] = sum[i];
   __syncthreads();
-  if ((warp & 3) == 0 && e < p.experts && static_cast<int>(lane) < nt) {
+  if ((warp & (kParts - 1)) == 0 && e < p.experts && static_cast<int>(lane) < nt) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += part[warp + i][lane];
+    for (int i = 0; i < kParts; ++i) s += part[warp + i][lane];
     reinterpret_cast<float*>(p.workspace + l.logits)[static_cast<int64_t>(t0 + lane) * p.experts + e] = s;
   }
 }
@@ -1033,8 +1036,13 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
   {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    const int logit_blocks = (p.experts + kRouterExperts - 1) / kRouterExperts *
-                             ((p.tokens + kRouterTokens - 1) / kRouterTokens);
+    // An expert a block while that makes two blocks an SM at most (one token
+    // of 2048, 128 experts: layer 18.1 us, with two experts a block 18.7; 4-bit
+    // token of 7168 45.4 and 46.8; but 64 tokens of 64 experts 225.5 and 223.8,
+    // 4 tokens of 512 experts 24.9 and 24.2).
+    const int token_groups = (p.tokens + kRouterTokens - 1) / kRouterTokens;
+    const int each = static_cast<int64_t>(p.experts) * token_groups <= 2 * num_sms ? 1 : 2;
+    const int logit_blocks = (p.experts + each - 1) / each * token_groups;
     const int record_blocks = static_cast<int>(
         (p.tokens * tiles(p.hidden) + kRouterThreads / 32 - 1) / (kRouterThreads / 32));
     const uint32_t units = static_cast<uint32_t>(blocks * part_floats(p.tokens) / 4);
@@ -1044,7 +1052,8 @@ cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, moe_router_kernel, p, logit_blocks, record_blocks, units);
+    err = cudaLaunchKernelEx(&cfg, each == 1 ? moe_router_kernel<1> : moe_router_kernel<2>, p, logit_blocks,
+                             record_blocks, units);
     if (err != cudaSuccess) return err;
   }
   const int pad = pad_tokens(p.tokens);

@@ -39,7 +39,8 @@
 //
 // Measured on one GB300 (FP8 weights, part of the time that the measured copy
 // bandwidth takes for the chosen experts' weights):
-//   16 tokens, hidden 7168, 56 of 64 experts of 2048:       384 us, 1.00
+//   16 tokens, hidden 7168, 56 of 64 experts of 2048:       384 us, 1.00 (403 on
+//       the slowest of several GPUs)
 //   64 tokens, hidden 4096, 64 experts of 1536:             223 us, 0.84 (the
 //       router kernel's 8 us, SMs that differ by 5 % in speed, and the last join)
 //   1 token, hidden 2048, 8 of 128 experts of 768:          18.2 us, 0.32 (a chain

@@ -409,7 +409,8 @@ size_t mx_norm_residual_backward_workspace(int64_t rows, int64_t cols, int64_t g
  * workspace: device, at least mx_norm_residual_backward_workspace(rows,
  *    cols, gate ? gates : 0) bytes, 16-byte aligned; its contents need no
  *    set-up and are undefined afterwards.
- * Other arguments and constraints as mx_norm_residual. */
+ * Other arguments and constraints as mx_norm_residual (the fast case wants
+ *    d_gate on a 16-byte boundary too). */
 mx_status mx_norm_residual_backward(int64_t rows, int64_t cols,
                                     const void* d_res, int64_t ldd, const void* dy, int64_t lddy,
                                     const void* block, int64_t ldb, mx_dtype c_dtype,

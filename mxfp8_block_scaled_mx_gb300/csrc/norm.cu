@@ -153,10 +153,14 @@ cudaError_t launch_norm_residual_backward(const NormBackParams& p, int num_sms,
     return err;
   }
   const int64_t ce = p.c_fp32 ? 4 : 8, se = p.s_fp32 ? 4 : 8;
+  // (d_gate is in this: the kernel for aligned rows writes a gate of its own
+  // rows there in 16-byte stores.  d_w_pre and d_w_post are not: the sum kernel
+  // writes them, and gates of several blocks' rows, float by float.)
   NormRows kind = NormRows::kAny;
   if (p.cols % 8 == 0 && aligned16(p.d_res) && aligned16(p.dy) && aligned16(p.block) &&
       aligned16(p.res_out) && aligned16(p.w_post) && aligned16(p.w_pre) && aligned16(p.gate) &&
-      aligned16(p.d_block) && aligned16(p.d_residual) && (!p.d_res || p.ldd % se == 0) &&
+      aligned16(p.d_block) && aligned16(p.d_residual) && aligned16(p.d_gate) &&
+      (!p.d_res || p.ldd % se == 0) &&
       p.lddy % ce == 0 && p.ldb % ce == 0 && p.ldr % se == 0 && p.lddb % ce == 0 &&
       p.lddr % se == 0) {
     kind = NormRows::kAligned;

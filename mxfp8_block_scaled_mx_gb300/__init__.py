@@ -537,7 +537,9 @@ def grouped_gemm_wgrad(a: MxTensor, offsets: torch.Tensor, b: MxTensor, total_to
 
 # The operators below are called for single tokens, where the host's share of
 # a call counts: their checks, outputs, workspaces and C calls are in a C++
-# module, built with the library (csrc/binding.cpp).
+# module, built with the library (csrc/binding.cpp).  Given a stream, they take
+# outputs and workspaces from that stream's memory; that their inputs are ready
+# there is for the caller to see to.
 
 _binding = None
 

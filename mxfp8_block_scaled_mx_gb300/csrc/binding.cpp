@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstdint>
@@ -106,22 +107,44 @@ struct Call {
     return given(i) ? reinterpret_cast<cudaStream_t>(integer(i))
                     : c10::cuda::getCurrentCUDAStream(device).stream();
   }
-  // A workspace of the caller's, or one that the allocator keeps until
-  // `stream` is past it.
-  at::Tensor workspace(int i, size_t need, const at::Tensor& like, cudaStream_t stream) const {
-    if (given(i)) {
-      const at::Tensor& t = tensor(i, "workspace");
-      if (t.scalar_type() != at::kByte || !here(t) || !t.is_contiguous() ||
+};
+
+// The memory that a call takes for itself, on the stream that its kernels run
+// on.  While this stands that stream is the current one, so the allocator hands
+// out memory whose last use is ordered before the kernels, and takes freed
+// memory back (a workspace, routing that is not returned) for use behind them.
+// Outputs are also kept until the caller's stream is past its uses.
+class Memory {
+ public:
+  Memory(const Call& c, int i_stream)
+      : c_(c), caller_(c10::cuda::getCurrentCUDAStream(c.device)), stream_(c.stream(i_stream)) {
+    if (stream_ == caller_.stream()) return;
+    guard_.reset_stream(stream_ ? c10::cuda::getStreamFromExternal(stream_, c.device)
+                                : c10::cuda::getDefaultCUDAStream(c.device));
+  }
+  cudaStream_t stream() const { return stream_; }
+  at::Tensor output(at::IntArrayRef shape, const at::TensorOptions& options) const {
+    const at::Tensor t = at::empty(shape, options);
+    if (stream_ != caller_.stream()) t.record_stream(caller_);
+    return t;
+  }
+  // The caller's workspace, or one of `need` bytes.
+  at::Tensor workspace(int i, size_t need, const at::Tensor& like) const {
+    if (c_.given(i)) {
+      const at::Tensor& t = c_.tensor(i, "workspace");
+      if (t.scalar_type() != at::kByte || !c_.here(t) || !t.is_contiguous() ||
           static_cast<size_t>(t.numel()) < need)
         refuse("workspace", "a contiguous uint8 tensor of at least " + std::to_string(need) + " bytes");
       return t;
     }
-    const int64_t bytes = need < 16 ? 16 : static_cast<int64_t>(need);
-    at::Tensor t = at::empty({bytes}, like.options().dtype(at::kByte));
-    if (stream != c10::cuda::getCurrentCUDAStream(device).stream())
-      t.record_stream(c10::cuda::getStreamFromExternal(stream, device));
-    return t;
+    return at::empty({need < 16 ? 16 : static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
   }
+
+ private:
+  const Call& c_;
+  c10::cuda::CUDAStream caller_;
+  cudaStream_t stream_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
 void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -166,19 +189,19 @@ PyObject* norm_residual(const Call& c) {
   const at::Tensor& residual = c.rows_of(1, "residual", rows, cols, at::ScalarType::Undefined, &ldr);
   const Weights w(c, 2, 3, 4, rows, cols);
   const float alpha = static_cast<float>(c.real(5)), eps = static_cast<float>(c.real(6));
+  const Memory memory(c, 9);
   const at::Tensor res_out =
       c.given(7) ? c.rows_of(7, "out_residual", rows, cols, residual.scalar_type(), &ldo)
-                 : at::empty({rows, cols}, residual.options());
+                 : memory.output({rows, cols}, residual.options());
   const at::Tensor y = c.given(8) ? c.rows_of(8, "out", rows, cols, block.scalar_type(), &ldy)
-                                  : at::empty({rows, cols}, block.options());
+                                  : memory.output({rows, cols}, block.options());
   if (rows > 0) {
-    const cudaStream_t stream = c.stream(9);
     mx_status s;
     Py_BEGIN_ALLOW_THREADS
     s = norm_residual_fn(rows, cols, block.data_ptr(), ldb, code_of(block.scalar_type()),
                          residual.data_ptr(), ldr, code_of(residual.scalar_type()), w.post, w.pre,
                          w.gate, w.gates, w.type, alpha, eps, res_out.data_ptr(), ldo, y.data_ptr(),
-                         ldy, stream);
+                         ldy, memory.stream());
     Py_END_ALLOW_THREADS
     if (s != MX_OK) return status_of(s);
   }
@@ -213,16 +236,16 @@ PyObject* norm_residual_backward(const Call& c) {
     d_res = c.rows_of(0, "d_residual", rows, cols, residual.scalar_type(), &ldd).data_ptr();
   const Weights w(c, 4, 5, 6, rows, cols);
   const float alpha = static_cast<float>(c.real(7)), eps = static_cast<float>(c.real(8));
-  const cudaStream_t stream = c.stream(10);
+  const Memory memory(c, 10);
   const size_t need = norm_workspace_fn(rows, cols, w.gates);
-  const at::Tensor ws = c.workspace(9, need, block, stream);
+  const at::Tensor ws = memory.workspace(9, need, block);
   const at::TensorOptions f32 = block.options().dtype(at::kFloat);
-  const at::Tensor d_block = at::empty({rows, cols}, block.options());
-  const at::Tensor d_residual = at::empty({rows, cols}, residual.options());
-  const at::Tensor d_pre = at::empty({cols}, f32);
+  const at::Tensor d_block = memory.output({rows, cols}, block.options());
+  const at::Tensor d_residual = memory.output({rows, cols}, residual.options());
+  const at::Tensor d_pre = memory.output({cols}, f32);
   at::Tensor d_post, d_gate;
-  if (w.post) d_post = at::empty({cols}, f32);
-  if (w.gate) d_gate = at::empty(w.gate_shape, f32);
+  if (w.post) d_post = memory.output({cols}, f32);
+  if (w.gate) d_gate = memory.output(w.gate_shape, f32);
   // a tensor without rows has no address; the workspace's stands in, unused
   void* none = ws.data_ptr();
   const bool empty = rows == 0;
@@ -235,7 +258,7 @@ PyObject* norm_residual_backward(const Call& c) {
                        empty ? none : d_block.data_ptr(), cols, empty ? none : d_residual.data_ptr(),
                        cols, static_cast<float*>(address(d_post)), static_cast<float*>(d_pre.data_ptr()),
                        static_cast<float*>(address(d_gate)), ws.data_ptr(),
-                       static_cast<size_t>(ws.numel()), stream);
+                       static_cast<size_t>(ws.numel()), memory.stream());
   Py_END_ALLOW_THREADS
   if (s != MX_OK) return status_of(s);
   PyObject* out = PyTuple_New(5);
@@ -276,18 +299,18 @@ PyObject* moe_few_tokens(const Call& c) {
   const int64_t top_k = c.integer(12);
   if (top_k < 1 || top_k > experts)
     throw Refused{"top_k must be 1 to " + std::to_string(experts) + ", got " + std::to_string(top_k)};
+  const Memory memory(c, 16);
   const at::Tensor y = c.given(14) ? c.rows_of(14, "out", tokens, hidden, at::kBFloat16, &ldy)
-                                   : at::empty({tokens, hidden}, x.options());
-  const at::Tensor ids = at::empty({tokens, top_k}, x.options().dtype(at::kInt));
-  const at::Tensor weights = at::empty({tokens, top_k}, x.options().dtype(at::kFloat));
+                                   : memory.output({tokens, hidden}, x.options());
+  const at::Tensor ids = memory.output({tokens, top_k}, x.options().dtype(at::kInt));
+  const at::Tensor weights = memory.output({tokens, top_k}, x.options().dtype(at::kFloat));
   if (tokens > 0) {
-    const cudaStream_t stream = c.stream(16);
     const bool fits = tokens <= INT32_MAX && experts <= INT32_MAX;
     const size_t need =
         fits ? moe_workspace_fn(static_cast<int32_t>(tokens), hidden, inter,
                                 static_cast<int32_t>(experts), static_cast<int32_t>(top_k))
              : 0;
-    const at::Tensor ws = c.workspace(15, need, x, stream);
+    const at::Tensor ws = memory.workspace(15, need, x);
     mx_status status = MX_ERR_UNSUPPORTED;
     const int32_t renormalize = static_cast<int32_t>(c.integer(13));
     if (fits) {
@@ -300,7 +323,7 @@ PyObject* moe_few_tokens(const Call& c) {
                       static_cast<const uint8_t*>(down.data_ptr()), static_cast<const uint8_t*>(s[2]),
                       static_cast<mx_fmt>(fmt_d), renormalize, y.data_ptr(), ldy,
                       static_cast<int32_t*>(ids.data_ptr()), static_cast<float*>(weights.data_ptr()),
-                      ws.data_ptr(), static_cast<size_t>(ws.numel()), stream);
+                      ws.data_ptr(), static_cast<size_t>(ws.numel()), memory.stream());
       Py_END_ALLOW_THREADS
     }
     if (status != MX_OK) return status_of(status);

@@ -75,3 +75,170 @@ def test_gradients_of_weights_off_16_bytes(mx, rows, cols, gates, c, s, w):
         for name, t in (("w_post", post), ("w_pre", pre), ("gate", gate.view(d["gate"].shape))):
             close(t, ref[name], ref["mag"][name], rows)
         assert flat[free].isnan().all()                 # nothing between them was written
+
+
+# ------------------------------------------------------------------ calls on a given stream
+
+SLEEP = 40_000_000                                      # cycles: about 20 ms of one thread
+
+
+def segment_stream(t):
+    """Stream that owns the allocator's segment of a tensor."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+def moe_weights(mx, hidden, inter, experts):
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def weight(rows, k):
+        w = (torch.randn(experts * rows, k, generator=g, device="cuda") * 0.05).to(BF16)
+        q = mx.quantize(w, "e4m3", "row")               # rows % 128 == 0: tiles by expert
+        return mx.MxTensor(q.codes.view(experts, rows, k), q.scales, "e4m3")
+
+    router = (torch.randn(experts, hidden, generator=g, device="cuda") * 0.05).to(BF16)
+    return router, weight(inter, hidden), weight(inter, hidden), weight(hidden, inter)
+
+
+def calls(mx):
+    """Name -> a call on a stream that returns a list of its outputs."""
+    rows, cols = 512, 2048
+    d = inputs(rows, cols, BF16, BF16, BF16, True, 1, seed=2)
+    args, kw = (d["block"], d["residual"], d["w_pre"]), dict(w_post=d["w_post"], gate=d["gate"])
+    layer = moe_weights(mx, 1024, 256, 8)
+    xs = [torch.randn(n, 1024, generator=torch.Generator().manual_seed(n)).to(BF16).cuda()
+          for n in (40, 33)]
+
+    def norm(stream=None, which=0):
+        a = (args[0].flip(0), args[1], args[2]) if which else args
+        torch.cuda.synchronize()
+        return lambda: list(mx.norm_residual(*a, **kw, stream=stream))
+
+    def back(stream=None, which=0):
+        dy = d["d_y"].flip(0) if which else d["d_y"]
+        torch.cuda.synchronize()
+        return lambda: list(vars(mx.norm_residual_backward(d["d_residual"], dy, *args, **kw,
+                                                           stream=stream)).values())
+
+    def moe(stream=None, which=0):
+        return lambda: list(mx.moe_few_tokens(xs[which], *layer, 2, return_routing=True,
+                                              stream=stream))
+
+    return dict(norm=norm, back=back, moe=moe)
+
+
+@pytest.mark.parametrize("name", ["norm", "back", "moe"])
+def test_outputs_come_from_the_given_streams_memory(mx, name):
+    s = torch.cuda.Stream()
+    make = calls(mx)[name]
+    for t in make(s)():
+        assert segment_stream(t) == s.cuda_stream
+    for t in make()():
+        assert segment_stream(t) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(s):                          # the default stream by its handle
+        for t in make(torch.cuda.default_stream())():
+            assert segment_stream(t) == torch.cuda.default_stream().cuda_stream
+    torch.cuda.synchronize()
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["norm", "back", "moe"])
+def test_a_call_beside_one_that_is_still_queued(mx, name):
+    """A call on the current stream, queued behind other work, and at once
+    one of other inputs on another stream: neither takes the other's memory."""
+    make = calls(mx)[name]
+    ref = [make(which=i)() for i in (0, 1)]
+    s = torch.cuda.Stream()
+    for first, second in ((None, s), (s, None)):
+        one, two = make(first, 0), make(second, 1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(first or torch.cuda.current_stream()):
+            torch.cuda._sleep(SLEEP)
+        got = [one(), two()]
+        torch.cuda.synchronize()
+        for a, b in zip(ref, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["norm", "back", "moe"])
+def test_freed_memory_with_uses_still_queued(mx, name):
+    """Tensors of the outputs' sizes, freed while copies of them are queued
+    behind other work, then a call on another stream: the copies hold."""
+    make = calls(mx)[name]
+    s = torch.cuda.Stream()
+    call = make(s)
+    old = [torch.full_like(t, 7) for t in make()() for _ in range(4)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)
+    kept = [t.clone() for t in old]
+    del old
+    outs = [call() for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in kept)
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[-1]))
+    assert mx.device_status() == 0
+
+
+def test_routing_that_is_not_returned(mx):
+    """The layer queued behind other work of its stream; tensors that the
+    current stream takes meanwhile keep their values."""
+    router, gate, up, down = moe_weights(mx, 1024, 256, 8)
+    s = torch.cuda.Stream()
+    x = torch.randn(64, 1024, device="cuda").to(BF16)
+    ref = mx.moe_few_tokens(x, router, gate, up, down, 8)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(SLEEP)
+        y = mx.moe_few_tokens(x, router, gate, up, down, 8, stream=s)
+        mine = [torch.full((64, 8), i, dtype=torch.int32, device="cuda") for i in range(64)]
+        mine_f = [torch.full((64, 1024), float(i), dtype=BF16, device="cuda") for i in range(8)]
+        torch.cuda.synchronize()
+        assert all(bool((t == i).all()) for i, t in enumerate(mine))
+        assert all(bool((t == i).all()) for i, t in enumerate(mine_f))
+        assert torch.equal(y, ref)
+    assert mx.device_status() == 0
+
+
+def test_outputs_that_the_caller_frees(mx):
+    """Outputs of a call on another stream, read on the current one behind
+    other work and freed there: later calls on that stream leave them alone."""
+    make = calls(mx)
+    s = torch.cuda.Stream()
+    for name in ("norm", "back", "moe"):
+        ref, call = make[name]()(), make[name](s)
+        torch.cuda.synchronize()
+        outs = call()
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(SLEEP)
+        kept = [t.clone() for t in outs]
+        del outs
+        other = make[name](s, 1) if name == "moe" else None  # (others synchronize when made)
+        for _ in range(4):
+            (other or call)()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, kept))
+    assert mx.device_status() == 0
+
+
+def test_a_given_stream_in_a_graph(mx):
+    """Capture that forks to a second stream and joins it."""
+    make = calls(mx)
+    s = torch.cuda.Stream()
+    for name in ("norm", "back", "moe"):
+        ref, call = make[name]()(), make[name](s)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s.wait_stream(torch.cuda.current_stream())
+            got = call()
+            torch.cuda.current_stream().wait_stream(s)
+        for t in got:
+            t.zero_()
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    assert mx.device_status() == 0

@@ -446,9 +446,13 @@ size_t mx_moe_few_tokens_workspace(int32_t tokens, int64_t hidden, int64_t inter
  * y: device bf16 [tokens, hidden] (ldy), rounded once from FP32.  ids:
  *    device int32 [tokens, top_k], the winners, largest z first; weights:
  *    device float [tokens, top_k].  Both contiguous, always written.
- * Precision: x is taken exactly, products accumulate in FP32, z in FP32; the
- *    activation silu(..) * (..), times its routing weight, is the only
- *    intermediate that is rounded (to 8 significant bits, as bf16 has).
+ * Precision: products accumulate in FP32, z in FP32 from x as it is.  The
+ *    operands of the expert products are held as two E4M3 terms over a power
+ *    of two per 32 channels: of x, values from 2^-14 of their block's largest
+ *    magnitude up exactly, smaller ones to within 2^-22 of that largest; the
+ *    activation silu(..) * (..), times its routing weight, to 8 significant
+ *    bits, as bf16 has, or to within 2^-22 of its block's largest, whichever
+ *    is more.  Nothing else between x and y is rounded.
  * A token whose x holds NaN or Inf gets NaN in y; no other token is touched
  *    by it.  Weights are expected to be finite: an expert with a NaN scale or
  *    code makes NaN of every token of a call in which some token chose it.

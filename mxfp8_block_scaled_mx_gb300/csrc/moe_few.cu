@@ -14,7 +14,8 @@
 // power of two that brings the 32-element block's largest value into
 // [128, 256).  hi has 4 significant bits, the remainder at most 1/16 of v, so
 // hi + lo / 32 holds 8 significant bits: a bf16 exactly (down to 2^-14 of its
-// block's largest), and the FP32 activation rounded once as bf16 would be.
+// block's largest, below that to within 2^-22 of it), and the FP32 activation
+// rounded once as bf16 would be (or to within 2^-22 of its block's largest).
 // The terms are rows of one B operand (N = 2 x the padded token count, one MMA
 // per 32 of K: an MMA this narrow costs what reading its A tile costs), and
 // the epilogue adds their two accumulator columns.

@@ -99,24 +99,50 @@ def expert_weight(codes, scales, rows, k, fmt):
     return O.decode_table(name)[codes] * np.repeat(s, 32, axis=1)[:, :k]
 
 
-def moe_layer(x, ids, weights, gate, up, down, product_tol, h_rel):
+def _e4m3_round(v):
+    """Nearest E4M3 value, ties to even (4 significant bits, steps of 2^-9 at
+    least; no value here is near the largest, 448)."""
+    step = np.exp2(np.maximum(np.frexp(v)[1] - 4, -9))
+    return np.rint(v / step) * step
+
+
+def _block_largest(v):
+    """The largest magnitude of each element's 32-element block of a row."""
+    return np.repeat([np.abs(v[i:i + 32]).max() for i in range(0, len(v), 32)], 32)[:len(v)]
+
+
+def two_terms(v):
+    """A row as the expert layer's tensor-core operand holds it: per 32
+    elements a power of two S that brings the largest into [128, 256), and
+    E4M3 terms hi of v / S, lo of the rest times 32."""
+    top = _block_largest(v)
+    s = np.exp2(np.frexp(top)[1] - 8.0)
+    u = v / np.where(top > 0, s, 1.0)
+    hi = _e4m3_round(u)
+    return (hi + _e4m3_round((u - hi) * 32) / 32) * np.where(top > 0, s, 1.0)
+
+
+def moe_layer(x, ids, weights, gate, up, down, product_tol, h_rel, x_floor=0.0, h_floor=0.0):
     """sum_e w_e down_e (silu(gate_e x) * (up_e x)) for given winners, and a
     bound of the error of a computation whose products are off by at most
     product_tol times their sum of magnitudes and which rounds the weighted
     activation by a relative h_rel (plus h_rel^3 of the largest of its
-    32-element block, where small values lose bits).  gate, up, down: lists
-    of float64 matrices by expert."""
+    32-element block, where small values lose bits).  x_floor: elements of x
+    below 2^-14 of the largest of their 32-element block are off by up to that
+    much of it; h_floor: so are those of the activation, all of them.  gate,
+    up, down: lists of float64 matrices by expert."""
     y, tol = np.zeros_like(x), np.zeros_like(x)
     for t in range(len(x)):
+        largest = _block_largest(x[t])
+        dx = np.where(np.abs(x[t]) < 2.0 ** -14 * largest, x_floor * largest, 0.0)
         for e, w in zip(ids[t], weights[t]):
             a, b = gate[e] @ x[t], up[e] @ x[t]
-            da = product_tol * (np.abs(gate[e]) @ np.abs(x[t]))
-            db = product_tol * (np.abs(up[e]) @ np.abs(x[t]))
+            da = product_tol * (np.abs(gate[e]) @ np.abs(x[t])) + np.abs(gate[e]) @ dx
+            db = product_tol * (np.abs(up[e]) @ np.abs(x[t])) + np.abs(up[e]) @ dx
             act = a / (1 + np.exp(-a))
             h = w * act * b
             dh = abs(w) * (1.1 * da * (np.abs(b) + db) + np.abs(act) * db)
-            top = np.array([np.abs(h[i:i + 32]).max() for i in range(0, len(h), 32)])
-            dh += h_rel * np.abs(h) + h_rel ** 3 * np.repeat(top, 32)[:len(h)]
+            dh += h_rel * np.abs(h) + (h_rel ** 3 + h_floor) * _block_largest(h)
             y[t] += down[e] @ h
             tol[t] += np.abs(down[e]) @ (dh + product_tol * (np.abs(h) + dh))
     return y, tol

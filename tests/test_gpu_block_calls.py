@@ -1,6 +1,7 @@
 """The block operators' C entries and calls on other streams: pointers as a
 caller with buffers of its own passes them, and memory that a call takes for
 itself.  Tolerances are those of test_gpu_norm and test_gpu_moe_few."""
+import numpy as np
 import pytest
 import torch
 
@@ -242,3 +243,43 @@ def test_a_given_stream_in_a_graph(mx):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(ref, got))
     assert mx.device_status() == 0
+
+
+# ------------------------------------------------------------------ tokens over a wide range
+
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1_packed"])
+def test_tokens_whose_blocks_span_a_wide_range(mx, tokens, fmt):
+    """Blocks of 32 channels with one of 1 and the others down to 2^-24 of
+    it, beside weights of zero at the large channels.  Against the layer of
+    what two E4M3 terms hold of x, the tolerances of test_gpu_moe_few, with
+    2^-22 of its block's largest for the activation; against x itself also
+    2^-22 of each block's largest for x."""
+    from test_gpu_moe_few import layer
+    d, _ = layer(tokens, tokens, 256, 128, 3, fmt)
+    rng = np.random.default_rng(tokens)
+    x = rng.normal(size=(tokens, 256)) * np.exp2(-rng.integers(8, 25, (tokens, 256)))
+    x[:, ::32] = 1.0
+    d["x"] = torch.from_numpy(x).to(BF16).cuda()
+    d["router"][:, ::32] = 0
+    mats = []
+    for n, rows, k in (("gate", 128, 256), ("up", 128, 256), ("down", 256, 128)):
+        codes = d[n].codes.clone()
+        if n != "down" and fmt == "e4m3":
+            codes[:, :, ::32] = 0
+        elif n != "down":
+            codes[:, :, ::16] &= 0xF0                   # the even element of a byte: low bits
+        scales = d[n].scales.view(3, -1)
+        mats.append([B.expert_weight(codes[e].cpu().numpy(), scales[e].cpu().numpy(), rows, k, fmt)
+                     for e in range(3)])
+        d[n] = mx.MxTensor(codes, d[n].scales, fmt)
+    assert all((m[:, ::32] == 0).all() for m in mats[0] + mats[1])
+    y, ids, w = mx.moe_few_tokens(d["x"], d["router"], d["gate"], d["up"], d["down"], 2,
+                                  return_routing=True)
+    assert mx.device_status() == 0
+    x, got, ids, w = to_f64(d["x"]), to_f64(y), ids.cpu().numpy(), to_f64(w)
+    held = np.stack([B.two_terms(v) for v in x])
+    assert (held != x).any()
+    for tokens_in, x_floor in ((held, 0.0), (x, 2.0 ** -22)):
+        ref, tol = B.moe_layer(tokens_in, ids, w, *mats, 1e-4, 2.0 ** -8, x_floor, 2.0 ** -22)
+        assert (np.abs(got - ref) <= tol + 2.0 ** -8 * np.abs(ref) + 1e-30).all()

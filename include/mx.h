@@ -454,8 +454,10 @@ size_t mx_moe_few_tokens_workspace(int32_t tokens, int64_t hidden, int64_t inter
  *    bits, as bf16 has, or to within 2^-22 of its block's largest, whichever
  *    is more.  Nothing else between x and y is rounded.
  * A token whose x holds NaN or Inf gets NaN in y; no other token is touched
- *    by it.  Weights are expected to be finite: an expert with a NaN scale or
- *    code makes NaN of every token of a call in which some token chose it.
+ *    by it.  A NaN among a token's z makes its softmax NaN: its weights and y
+ *    are NaN, its winners the largest of the other z.  Weights are expected
+ *    to be finite: an expert with a NaN scale or code makes NaN of every token
+ *    of a call in which some token chose it.
  * 0 <= tokens <= 64 (more is MX_ERR_UNSUPPORTED), 1 <= experts <= 512, 1 <=
  *    top_k <= min(experts, 32).
  * workspace: device, at least mx_moe_few_tokens_workspace(...) bytes,

@@ -382,7 +382,8 @@ __device__ __forceinline__ void select_experts(const MoeFewParams& p, const floa
   }
   if (static_cast<int>(lane) < p.top_k) {
     sh->id[t * p.top_k + lane] = static_cast<uint16_t>(my_e);
-    sh->weight[t * p.top_k + lane] = my_w / (p.renormalize ? chosen : sum);
+    // (a NaN anywhere among the logits is one of the whole softmax)
+    sh->weight[t * p.top_k + lane] = my_w / (p.renormalize && sum == sum ? chosen : sum);
     atomicOr(&sh->chosen[my_e >> 5], 1u << (my_e & 31u));
   }
 }

@@ -283,3 +283,30 @@ def test_tokens_whose_blocks_span_a_wide_range(mx, tokens, fmt):
     for tokens_in, x_floor in ((held, 0.0), (x, 2.0 ** -22)):
         ref, tol = B.moe_layer(tokens_in, ids, w, *mats, 1e-4, 2.0 ** -8, x_floor, 2.0 ** -22)
         assert (np.abs(got - ref) <= tol + 2.0 ** -8 * np.abs(ref) + 1e-30).all()
+
+
+# ------------------------------------------------------------------ softmax of a NaN
+
+@pytest.mark.parametrize("experts", [6, 200])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_a_nan_logit_makes_the_softmax_nan(mx, experts, renormalize):
+    """softmax of logits with a NaN among them is NaN, so are the winners'
+    shares of it and y; the winners are still the largest numbers."""
+    from test_gpu_moe_few import layer
+    d, _ = layer(8, 5, 128, 64, experts, router=FP32)
+    kw = dict(renormalize=renormalize, return_routing=True)
+    args = [d[n] for n in ("gate", "up", "down")]
+    y, ids, w = mx.moe_few_tokens(d["x"], d["router"], *args, 2, **kw)
+    bad = d["router"].clone()
+    last = next(e for e in range(experts - 1, -1, -1) if not (ids == e).any())
+    bad[last, 3] = float("nan")                         # an expert that nobody chose
+    y2, ids2, w2 = mx.moe_few_tokens(d["x"], bad, *args, 2, **kw)
+    assert torch.equal(ids2, ids)
+    assert w2.isnan().all() and y2.isnan().all()
+    assert w.isfinite().all() and y.isfinite().all()
+    x = d["x"].clone()
+    x[1, 5], x[4, 0] = float("-inf"), float("inf")
+    y3, ids3, w3 = mx.moe_few_tokens(x, d["router"], *args, 2, **kw)
+    assert w3[[1, 4]].isnan().all() and y3[[1, 4]].isnan().all()
+    assert torch.equal(ids3[[0, 2, 3]], ids[[0, 2, 3]]) and torch.equal(w3[[0, 2, 3]], w[[0, 2, 3]])
+    assert mx.device_status() == 0

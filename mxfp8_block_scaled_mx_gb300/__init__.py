@@ -573,12 +573,57 @@ def norm_residual(block: torch.Tensor, residual: torch.Tensor, w_pre: torch.Tens
     (bf16 or fp32), the second in the block's.  w_post None: no norm after
     the block.  gate: [cols], or [gates, cols] with one gate per
     rows/gates consecutive rows.  w_pre, w_post and gate share one type.
-    out_residual may be `residual` itself."""
+    out_residual may be `residual` itself.  Differentiable: where autograd
+    records, the backward pass is norm_residual_backward, on the stream that
+    autograd runs it on."""
+    raw = None if stream is None else _stream(stream)
     r = _native().norm_residual(block, residual, w_pre, w_post, gate, alpha, eps, out_residual, out,
-                                None if stream is None else _stream(stream))
+                                raw)
+    if r is None:
+        r = _NormResidual.apply(block, residual, w_pre, w_post, gate, alpha, eps, raw)
+        return _recorded_copy(r[0], out_residual, stream), _recorded_copy(r[1], out, stream)
     if type(r) is int:
         raise MxError("mx_norm_residual", r)
     return r
+
+
+def _recorded_copy(value, out, stream):
+    """`value`, copied to `out` where that is given: autograd follows a copy
+    also to a view, and what it saved is not the caller's buffer."""
+    if out is None:
+        return value
+    if (not isinstance(out, torch.Tensor) or out.shape != value.shape or out.dtype != value.dtype
+            or out.device != value.device):
+        raise ValueError(f"an output must be a {value.dtype} tensor of shape {tuple(value.shape)} "
+                         f"on {value.device}")
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return out.copy_(value)
+
+
+class _NormResidual(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, block, residual, w_pre, w_post, gate, alpha, eps, stream):
+        stored, y = norm_residual(block, residual, w_pre, w_post, gate, alpha, eps, stream=stream)
+        ctx.save_for_backward(block, stored, w_pre, w_post, gate)
+        ctx.set_materialize_grads(False)
+        ctx.scalars = alpha, eps
+        return stored, y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_residual, d_y):
+        if d_residual is None and d_y is None:
+            return (None,) * 8
+        block, stored, w_pre, w_post, gate = ctx.saved_tensors
+        # (gradients arrive in any strides: that of a sum is one element, expanded)
+        d_residual = None if d_residual is None else d_residual.contiguous()
+        d_y = torch.zeros_like(block) if d_y is None else d_y.contiguous()
+        d = norm_residual_backward(d_residual, d_y, block, stored, w_pre, w_post, gate, *ctx.scalars)
+        grads = (d.block, d.residual, d.w_pre, d.w_post, d.gate)
+        return tuple(g.to(t.dtype) if want else None for g, t, want in zip(
+            grads, (block, stored, w_pre, w_post, gate), ctx.needs_input_grad)) + (None,) * 3
 
 
 @dataclass
@@ -623,17 +668,34 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, gate: MxTensor, up: Mx
     Returns y (bf16 [tokens, hidden]), with return_routing (y, ids int32
     [tokens, top_k], weights fp32 [tokens, top_k]).  workspace: uint8,
     mx_moe_few_tokens_workspace(...) bytes, one call at a time; allocated
-    here when None."""
+    here when None.  An operator of inference: a backward pass through its
+    outputs raises."""
     if gate.fmt != up.fmt:
         raise ValueError("gate and up must be of one format")
+    raw = None if stream is None else _stream(stream)
     r = _native().moe_few_tokens(x, router, gate.codes, gate.scales, up.codes, up.scales,
                                  FMT[gate.fmt], STORAGE_BITS.get(gate.fmt, 8), down.codes,
                                  down.scales, FMT[down.fmt], STORAGE_BITS.get(down.fmt, 8), top_k,
-                                 renormalize, out, workspace,
-                                 None if stream is None else _stream(stream))
+                                 renormalize, out, workspace, raw)
+    if r is None:
+        y, *routing = _MoeFewTokens.apply(x, router, gate, up, down, top_k, renormalize, workspace, raw)
+        r = (_recorded_copy(y, out, stream), *routing)
     if type(r) is int:
         raise MxError("mx_moe_few_tokens", r)
     return r if return_routing else r[0]
+
+
+class _MoeFewTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, router, gate, up, down, top_k, renormalize, workspace, stream):
+        y, ids, weights = moe_few_tokens(x, router, gate, up, down, top_k, renormalize, None,
+                                         workspace, True, stream)
+        ctx.mark_non_differentiable(ids)
+        return y, ids, weights
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("moe_few_tokens has no gradient")
 
 
 def device_status(stream=None) -> int:

@@ -6,18 +6,22 @@
 // A module of the CPython C API (`_binding`).  Each function takes its
 // arguments by position, raises ValueError for a tensor that the kernels
 // could not read or write, and returns its outputs, or the status of the C
-// call (an int) when that is not MX_OK.  The C entry points are handed over as
+// call (an int) when that is not MX_OK, or None where a forward pass is to be
+// recorded for autograd (the caller then calls again from within a Function,
+// where that is off).  The C entry points are handed over as
 // addresses by `init`, so the module is bound to the libmx that the package
 // loaded.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include "mx.h"
@@ -60,6 +64,13 @@ struct Call {
   mutable c10::DeviceIndex device = -1;
 
   bool given(int i) const { return args[i] != Py_None; }
+  // Whether autograd is on and one of these arguments asks for a gradient.
+  bool recorded(std::initializer_list<int> which) const {
+    if (!c10::GradMode::is_enabled()) return false;
+    for (int i : which)
+      if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
+    return false;
+  }
   const at::Tensor& tensor(int i, const char* name) const {
     if (!THPVariable_Check(args[i])) throw Refused{std::string(name) + " must be a tensor"};
     return THPVariable_Unpack(args[i]);
@@ -147,6 +158,12 @@ class Memory {
   c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
+// A tensor of the caller's was written: what autograd saved of it is not valid
+// any more.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // The norm's weights, which share one type; gates is 0 without a gate.
@@ -181,6 +198,7 @@ PyObject* status_of(mx_status s) { return PyLong_FromLong(s); }
 
 // block, residual, w_pre, w_post, gate, alpha, eps, out_residual, out, stream
 PyObject* norm_residual(const Call& c) {
+  if (c.recorded({0, 1, 2, 3, 4, 7, 8})) Py_RETURN_NONE;
   const at::Tensor& block = c.tensor(0, "block");
   if (block.dim() != 2) throw Refused{"block must be a 2-D tensor"};
   const int64_t rows = block.size(0), cols = block.size(1);
@@ -205,6 +223,8 @@ PyObject* norm_residual(const Call& c) {
     Py_END_ALLOW_THREADS
     if (s != MX_OK) return status_of(s);
   }
+  if (c.given(7)) written(res_out);
+  if (c.given(8)) written(y);
   PyObject* out = PyTuple_New(2);
   if (!out) return nullptr;
   if (c.given(7)) {
@@ -272,6 +292,7 @@ PyObject* norm_residual_backward(const Call& c) {
 // x, router, gate codes, gate scales, up codes, up scales, format, bits, down
 // codes, down scales, format, bits, top_k, renormalize, out, workspace, stream
 PyObject* moe_few_tokens(const Call& c) {
+  if (c.recorded({0, 1, 14})) Py_RETURN_NONE;
   const at::Tensor& x = c.tensor(0, "x");
   if (x.dim() != 2) throw Refused{"x must be a 2-D tensor"};
   const at::Tensor& router = c.tensor(1, "router");
@@ -328,6 +349,7 @@ PyObject* moe_few_tokens(const Call& c) {
     }
     if (status != MX_OK) return status_of(status);
   }
+  if (c.given(14)) written(y);
   PyObject* out = PyTuple_New(3);
   if (!out) return nullptr;
   if (c.given(14)) {

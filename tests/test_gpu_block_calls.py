@@ -1,6 +1,7 @@
-"""The block operators' C entries and calls on other streams: pointers as a
-caller with buffers of its own passes them, and memory that a call takes for
-itself.  Tolerances are those of test_gpu_norm and test_gpu_moe_few."""
+"""The block operators' C entries with a caller's buffers, calls on given
+streams (the memory that a call takes for itself), tokens over a wide range,
+and calls that autograd records.  Tolerances are those of test_gpu_norm and
+test_gpu_moe_few."""
 import numpy as np
 import pytest
 import torch
@@ -309,4 +310,88 @@ def test_a_nan_logit_makes_the_softmax_nan(mx, experts, renormalize):
     y3, ids3, w3 = mx.moe_few_tokens(x, d["router"], *args, 2, **kw)
     assert w3[[1, 4]].isnan().all() and y3[[1, 4]].isnan().all()
     assert torch.equal(ids3[[0, 2, 3]], ids[[0, 2, 3]]) and torch.equal(w3[[0, 2, 3]], w[[0, 2, 3]])
+    assert mx.device_status() == 0
+
+
+# ------------------------------------------------------------------ autograd
+
+@pytest.mark.parametrize("rows,cols,gates,post", [(64, 256, 1, True), (40, 1111, 0, False),
+                                                  (12, 4096, 4, True)])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_recorded_gradients_are_those_of_the_backward_entry(mx, rows, cols, gates, post, c, s, w):
+    d = inputs(rows, cols, c, s, w, post, gates, seed=cols)
+    names = ("block", "residual", "w_pre", "w_post", "gate")
+    plain = mx.norm_residual(*(d[n] for n in names), alpha=0.5)
+    want = mx.norm_residual_backward(d["d_residual"], d["d_y"], d["block"], plain[0], d["w_pre"],
+                                     w_post=d["w_post"], gate=d["gate"], alpha=0.5)
+    p = {n: None if d[n] is None else d[n].clone().requires_grad_() for n in names}
+    got = mx.norm_residual(*p.values(), alpha=0.5)
+    assert all(torch.equal(a, b) for a, b in zip(got, plain))
+    torch.autograd.backward(got, (d["d_residual"], d["d_y"]))
+    for n, t in p.items():
+        if t is not None:
+            assert t.grad.dtype == t.dtype and torch.equal(t.grad, getattr(want, n).to(t.dtype))
+    # gradients that are expanded, or absent for one output
+    for which in (0, 1):
+        ones = torch.ones_like(plain[which])
+        want = mx.norm_residual_backward(ones if which == 0 else None,
+                                         torch.zeros_like(d["d_y"]) if which == 0 else ones,
+                                         d["block"], plain[0], d["w_pre"], w_post=d["w_post"],
+                                         gate=d["gate"], alpha=0.5)
+        q = {n: None if d[n] is None else d[n].clone().requires_grad_() for n in names}
+        mx.norm_residual(*q.values(), alpha=0.5)[which].sum().backward()
+        for n, t in q.items():
+            if t is not None:
+                assert torch.equal(t.grad, getattr(want, n).to(t.dtype))
+    assert mx.device_status() == 0
+
+
+def test_recorded_calls_on_a_stream_and_into_given_outputs(mx):
+    d = inputs(48, 512, BF16, BF16, BF16, True, 1)
+    w = d["w_pre"].clone().requires_grad_()
+    ref = mx.norm_residual(d["block"], d["residual"], d["w_pre"], d["w_post"], d["gate"])
+    s = torch.cuda.Stream()
+    wide = torch.full((48, 520), 7.0, dtype=BF16, device="cuda")
+    for stream in (None, s, s.cuda_stream):
+        mine = d["residual"].clone()
+        torch.cuda.synchronize()
+        res, y = mx.norm_residual(d["block"], mine, w, d["w_post"], d["gate"], out_residual=mine,
+                                  out=wide[:, :512], stream=stream)
+        torch.cuda.synchronize()
+        assert res is mine and torch.equal(res, ref[0]) and torch.equal(y, ref[1])
+        assert (wide[:, 512:] == 7.0).all()
+        w.grad = None
+        y.float().sum().backward()
+        want = mx.norm_residual_backward(None, torch.ones_like(y), d["block"], ref[0], d["w_pre"],
+                                         d["w_post"], d["gate"])
+        assert torch.equal(w.grad, want.w_pre.to(BF16))
+        wide = wide.detach()
+
+
+def test_buffers_written_are_known_to_autograd(mx):
+    """A given output that autograd saved for another operator: its backward
+    pass says so."""
+    d = inputs(8, 128, BF16, BF16, BF16, True, 0)
+    layer = moe_weights(mx, 128, 128, 4)
+    a = torch.ones(8, 128, dtype=BF16, device="cuda", requires_grad=True)
+    for write in (lambda t: mx.norm_residual(d["block"], d["residual"], d["w_pre"], out=t),
+                  lambda t: mx.norm_residual(d["block"], d["residual"], d["w_pre"], out_residual=t),
+                  lambda t: mx.moe_few_tokens(d["block"], *layer, 2, out=t)):
+        buffer = torch.ones(8, 128, dtype=BF16, device="cuda")
+        loss = (a * buffer).sum()
+        write(buffer)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+
+def test_the_layer_records_that_it_has_no_gradient(mx):
+    router, *mats = moe_weights(mx, 128, 128, 4)
+    x = torch.randn(5, 128, device="cuda").to(BF16)
+    ref = mx.moe_few_tokens(x, router, *mats, 2, return_routing=True)
+    got = mx.moe_few_tokens(x.requires_grad_(), router, *mats, 2, return_routing=True)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    with pytest.raises(RuntimeError, match="no gradient"):
+        got[0].float().sum().backward()
+    out = torch.empty_like(ref[0])
+    assert torch.equal(mx.moe_few_tokens(x, router, *mats, 2, out=out), ref[0]) and out.requires_grad
     assert mx.device_status() == 0

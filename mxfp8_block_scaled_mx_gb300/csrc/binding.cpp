@@ -68,7 +68,7 @@ struct Call {
   bool recorded(std::initializer_list<int> which) const {
     if (!c10::GradMode::is_enabled()) return false;
     for (int i : which)
-      if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
+      if (given(i) && THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
     return false;
   }
   const at::Tensor& tensor(int i, const char* name) const {

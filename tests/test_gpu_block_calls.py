@@ -395,3 +395,77 @@ def test_the_layer_records_that_it_has_no_gradient(mx):
     out = torch.empty_like(ref[0])
     assert torch.equal(mx.moe_few_tokens(x, router, *mats, 2, out=out), ref[0]) and out.requires_grad
     assert mx.device_status() == 0
+
+
+# ------------------------------------------------------------------ promises of the interface
+
+@pytest.mark.parametrize("rows,cols,gates", [(300, 1024, 3), (40, 4096, 0), (160, 9216, 1),
+                                             (700, 1111, 7), (60, 5001, 0), (9800, 1111, 1)])
+@pytest.mark.parametrize("c,s,w", TYPES)
+def test_gradient_of_the_residual_in_place(mx, rows, cols, gates, c, s, w):
+    """d_residual may be d_res itself: the same bits as apart, whichever form
+    reads the rows (a ring, a cluster, in place, by phase)."""
+    d = inputs(rows, cols, c, s, w, True, gates, seed=rows)
+    ref = mx.norm_residual_backward(d["d_residual"], d["d_y"], d["block"], d["residual"], d["w_pre"],
+                                    d["w_post"], d["gate"], 0.5, EPS)
+    post, pre = torch.empty(2, cols, device="cuda")
+    gate = None if d["gate"] is None else torch.empty(d["gate"].shape, device="cuda")
+    if cols % 4:                                        # slices of one tensor may be off 16 bytes
+        post, pre = post.clone(), pre.clone()
+    d_block = torch.empty_like(d["block"])
+    assert c_backward(mx, d, 0.5, d_block, d["d_residual"], post, pre, gate) == 0
+    assert mx.device_status() == 0
+    assert torch.equal(d_block, ref.block) and torch.equal(d["d_residual"], ref.residual)
+    assert torch.equal(pre, ref.w_pre) and torch.equal(post, ref.w_post)
+    assert gate is None or torch.equal(gate, ref.gate)
+
+
+@pytest.mark.parametrize("cols,ld", [(2048, 1 << 30), (1111, (1 << 30) + 8), (9000, (1 << 30) + 8)])
+def test_rows_far_apart(mx, cols, ld):
+    """Three rows over more than 2^31 elements of every array: the same bits
+    as rows side by side."""
+    d = inputs(3, cols, BF16, BF16, BF16, True, 1, seed=cols)
+    far = {}
+    for n in ("block", "residual", "d_residual", "d_y", "out", "out_residual"):
+        far[n] = torch.empty(2 * ld + cols, dtype=BF16, device="cuda").as_strided((3, cols), (ld, 1))
+        if n in d:
+            far[n].copy_(d[n])
+    w = (d["w_pre"], d["w_post"], d["gate"])
+    ref = mx.norm_residual(d["block"], d["residual"], *w)
+    mx.norm_residual(far["block"], far["residual"], *w, out_residual=far["out_residual"], out=far["out"])
+    assert torch.equal(far["out_residual"], ref[0]) and torch.equal(far["out"], ref[1])
+    near = mx.norm_residual_backward(d["d_residual"], d["d_y"], d["block"], d["residual"], *w)
+    post, pre = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    gate = torch.empty(cols, device="cuda")
+    assert c_backward(mx, {**d, **{n: far[n] for n in d if n in far}}, 1.0, far["out"],
+                      far["out_residual"], post, pre, gate) == 0
+    assert torch.equal(far["out"], near.block) and torch.equal(far["out_residual"], near.residual)
+    for a, b in ((pre, near.w_pre), (post, near.w_post), (gate, near.gate)):
+        assert torch.equal(a, b)
+    assert mx.device_status() == 0
+
+
+def test_more_than_2_31_elements(mx):
+    """Rows past 2^31 elements, against calls on those rows alone."""
+    rows, cols = (1 << 31) // 16384 + 40, 16384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = lambda: torch.randn(rows, cols, generator=g, device="cuda", dtype=BF16)  # noqa: E731
+    block, residual, dy = n(), n(), n()
+    w = torch.ones(cols, device="cuda", dtype=BF16)
+    tail = slice(rows - 64, rows)
+    res, y = mx.norm_residual(block, residual, w, w)
+    ref = mx.norm_residual(block[tail], residual[tail], w, w)
+    assert torch.equal(res[tail], ref[0]) and torch.equal(y[tail], ref[1])
+    del res, y
+    got = mx.norm_residual_backward(None, dy, block, residual, w, w)
+    ref = mx.norm_residual_backward(None, dy[tail], block[tail], residual[tail], w, w)
+    assert torch.equal(got.block[tail], ref.block) and torch.equal(got.residual[tail], ref.residual)
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("experts,tokens,top_k", [(128, 64, 8), (129, 20, 8), (160, 40, 6),
+                                                  (257, 64, 8), (384, 17, 8), (512, 64, 32)])
+def test_many_experts_and_tokens(mx, experts, tokens, top_k):
+    from test_gpu_moe_few import check, layer
+    d, mats = layer(experts + tokens, tokens, 64, 32, experts, router=FP32)
+    check(mx, d, mats, top_k, renormalize=experts % 2 == 0)

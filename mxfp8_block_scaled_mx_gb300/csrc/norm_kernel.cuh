@@ -1050,7 +1050,12 @@ constexpr int kMaxSms = 192;         // workspaces are sized for this many
 // in all; a block has 2 KB of its own beside these).  One block alone takes no
 // more than 161 KB: what it leaves is L1, where w_pre is read for every row
 // (16384 x 7168: a ring of two rows 218 us, of three 224 and with all of the
-// memory 234; x 12288: 538, with a row more 577 to 637).
+// memory 234; x 12288: 538, with a row more 577 to 637; all bf16).  Rows of
+// which no two fit in it are read in place: FP32 blocks from 4840 columns on (from
+// 9672 in a cluster), bf16 blocks on an FP32 stream from 6320 (12632).  For
+// those a ring of two in 206 KB is faster where it fits (8192 x 5120 FP32: 209 us
+// in place, 191; x 6144: 239, 216; x 6400 on an FP32 stream: 177, 165; x 7168:
+// 179, 174), which this one limit does not give them; bf16 x 7168 115, with 206 KB 118.
 constexpr size_t kSmemBytes = 161 * 1024;
 constexpr size_t kSmemMost = 12 * 16384;  // (row by row element by element)
 constexpr size_t smem_of(int fit) {

@@ -596,8 +596,9 @@ def _recorded_copy(value, out, stream):
             or out.device != value.device):
         raise ValueError(f"an output must be a {value.dtype} tensor of shape {tuple(value.shape)} "
                          f"on {value.device}")
-    if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return out.copy_(value)
 

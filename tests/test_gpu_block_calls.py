@@ -2,6 +2,8 @@
 streams (the memory that a call takes for itself), tokens over a wide range,
 and calls that autograd records.  Tolerances are those of test_gpu_norm and
 test_gpu_moe_few."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -352,7 +354,8 @@ def test_recorded_calls_on_a_stream_and_into_given_outputs(mx):
     ref = mx.norm_residual(d["block"], d["residual"], d["w_pre"], d["w_post"], d["gate"])
     s = torch.cuda.Stream()
     wide = torch.full((48, 520), 7.0, dtype=BF16, device="cuda")
-    for stream in (None, s, s.cuda_stream):
+    handle = SimpleNamespace(cuda_stream=s.cuda_stream)  # (another library's stream)
+    for stream in (None, s, s.cuda_stream, handle, 0):
         mine = d["residual"].clone()
         torch.cuda.synchronize()
         res, y = mx.norm_residual(d["block"], mine, w, d["w_post"], d["gate"], out_residual=mine,

@@ -34,7 +34,7 @@
  *  - Arguments are validated on the host before anything is launched; a
  *    non-MX_OK status means nothing was enqueued.
  *  - Faults detected on the device (a pipeline wait that timed out, invalid
- *    group offsets) are recorded in one status word per device, shared by
+ *    group offsets or labels) are recorded in one status word per device, shared by
  *    every stream and host thread of the process, and reported by
  *    mx_device_status().  A fault of a kernel on any stream is therefore
  *    reported to whichever caller queries the device first.
@@ -87,7 +87,7 @@ typedef enum {
   MX_ERR_UNSUPPORTED = 3,   /* valid but not implemented combination          */
   MX_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed            */
   MX_ERR_TIMEOUT = 5,       /* a device pipeline wait gave up (device status) */
-  MX_ERR_DEVICE_ARG = 6     /* the device found invalid data (group offsets)  */
+  MX_ERR_DEVICE_ARG = 6     /* the device found invalid data (offsets, labels) */
 } mx_status;
 
 /* Element formats, section "Format taxonomy: range, spacing, and
@@ -345,8 +345,9 @@ mx_status mx_grouped_gemm_wgrad(int32_t groups, const int32_t* d_offsets, int64_
                                 void* y, mx_dtype y_dtype, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
- * Around the products: the norms before and after a block, and a whole
- * mixture-of-experts layer for a few tokens.
+ * Around the products: the norms before and after a block, a whole
+ * mixture-of-experts layer for a few tokens, the norms of query and key heads
+ * with their rotation, routing for training, and the loss over a vocabulary.
  * ------------------------------------------------------------------------ */
 
 /* The norm after a block, its gate, the scaled residual and the norm before
@@ -473,10 +474,175 @@ mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32
                             int32_t* ids, float* weights,
                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* The norms of query and key heads with the rotation by position, in one pass.
+ * For every token t and head x of `dim` channels, with its tensor's w:
+ *   n_c = x_c w_c / sqrt(mean(x^2) + eps)
+ * and for the pairs (a, b) of the first `rotary` channels -- (i, i + rotary / 2), or
+ * (2 i, 2 i + 1) where interleaved -- with the angle positions[t] * frequencies[i]:
+ *   y_a = scale (n_a cos - n_b sin),  y_b = scale (n_a sin + n_b cos)
+ * the other channels are n.  In FP32, with one rounding (to nearest even).
+ * q, out_q: device [tokens, q_heads, dim] of x_dtype, k, out_k: [tokens,
+ *    k_heads, dim]; channels contiguous, *_st and *_sh the strides of tokens and
+ *    heads in elements (the parts of a product's rows that hold queries and keys,
+ *    for example).  Outputs may be the inputs themselves (same pointer and
+ *    strides) and overlap nothing else; their rows are apart from one another.
+ * w_q, w_k: device [dim] of w_dtype.
+ * positions: device int32 or int64 [tokens] (position_bits 32 or 64), of any sign.
+ * frequencies: device double [rotary / 2], finite, radians per position.  An
+ *    angle is taken modulo a turn in 64-bit integers, so that far positions lose
+ *    nothing: it is off by at most 2^-64 turns times the position, then rounded to
+ *    FP32.
+ * Pointers and strides need the alignment of one element only (chunks of four
+ *    channels -- dim and rotary multiples of 8, rows on four elements -- are the
+ *    fast case);
+ * 2 <= rotary <= dim <= 512, rotary even, eps >= 0; tokens == 0 does nothing. */
+mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
+                         int64_t rotary,
+                         const void* q, int64_t q_st, int64_t q_sh,
+                         const void* k, int64_t k_st, int64_t k_sh, mx_dtype x_dtype,
+                         const void* w_q, const void* w_k, mx_dtype w_dtype,
+                         const void* positions, int32_t position_bits,
+                         const double* frequencies, int32_t interleaved, float scale, float eps,
+                         void* out_q, int64_t oq_st, int64_t oq_sh,
+                         void* out_k, int64_t ok_st, int64_t ok_sh, cudaStream_t stream);
+
+/* Bytes of the workspace of mx_norm_rotate_backward; 0 for sizes that it
+ * refuses. */
+size_t mx_norm_rotate_backward_workspace(int64_t tokens, int64_t dim);
+
+/* Gradients of mx_norm_rotate.  With dn the output's gradient rotated back and
+ * rho = 1 / sqrt(mean(x^2) + eps) per head, in FP32:
+ *   dx = rho (w dn - x rho^2 mean(w dn x)),  dw = sum over tokens and heads of dn x rho
+ * d_q, d_k: the outputs' gradients, q, k: the inputs of the forward pass, all of
+ *    x_dtype with strides as there.
+ * dx_q, dx_k: device, contiguous, of x_dtype; dw_q, dw_k: device float [dim],
+ *    always written (zeros when tokens == 0).  Sums run in a fixed order for given
+ *    sizes: the same inputs give the same bits.
+ * workspace: device, at least mx_norm_rotate_backward_workspace(tokens, dim)
+ *    bytes, 16-byte aligned; needs no set-up, undefined afterwards. */
+mx_status mx_norm_rotate_backward(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
+                                  int64_t rotary,
+                                  const void* d_q, int64_t dq_st, int64_t dq_sh,
+                                  const void* d_k, int64_t dk_st, int64_t dk_sh,
+                                  const void* q, int64_t q_st, int64_t q_sh,
+                                  const void* k, int64_t k_st, int64_t k_sh, mx_dtype x_dtype,
+                                  const void* w_q, const void* w_k, mx_dtype w_dtype,
+                                  const void* positions, int32_t position_bits,
+                                  const double* frequencies, int32_t interleaved, float scale,
+                                  float eps, void* dx_q, void* dx_k, float* dw_q, float* dw_k,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of the workspace of mx_route; 0 where it needs none (few tokens) and for
+ * sizes that it refuses. */
+size_t mx_route_workspace(int64_t tokens, int32_t experts);
+
+/* The experts of every token from the router's logits z, what the grouped
+ * products need of them, and the balance loss:
+ *   p[t] = softmax(z[t]);  the top_k largest z win (equal ones: the lowest index
+ *   first);  w = p of the winners, divided by their sum when renormalize != 0
+ *   counts_e = how many of the n tokens that count chose e
+ *   balance  = experts * sum_e counts_e / (n top_k) * sum_t p[t][e] / n
+ *              (over the tokens that count; 1 where all experts are used alike, 0
+ *              where no token counts)
+ * logits: device [tokens, experts] of dtype, leading dimension ld.
+ * mask: device uint8 [tokens] or NULL: 0 marks a token that does not count
+ *    (padding).  It is routed like any other, but adds nothing to counts and
+ *    balance.
+ * ids: device int32 [tokens, top_k], the winners, largest z first; weights: float
+ *    [tokens, top_k]; lse: float [tokens], log sum exp z.
+ * counts: device int32 [experts].  offsets: device int32 [experts + 1], where
+ *    each expert's pairs start among all tokens * top_k; order: device int32
+ *    [tokens * top_k], the pairs t * top_k + j sorted by expert and, within one,
+ *    ascending: row order[i] / top_k of the tokens is row i of the grouped
+ *    operand (offsets are the d_offsets of mx_quantize_grouped and
+ *    mx_grouped_gemm).  balance: device float [1].
+ * A NaN among a token's z makes its softmax NaN: its weights are NaN, its winners
+ *    the largest of the other z; so does a z of +infinity, or -infinity throughout.
+ * The same inputs give the same bits.
+ * Pointers need the alignment of one element only.  1 <= experts <= 512, 1 <=
+ *    top_k <= min(experts, 32), tokens <= 4194303 (more is MX_ERR_UNSUPPORTED);
+ *    tokens == 0 writes zeros to counts, offsets and balance.
+ * workspace: device, at least mx_route_workspace(tokens, experts) bytes, 16-byte
+ *    aligned; needs no set-up, undefined afterwards. */
+mx_status mx_route(int64_t tokens, int32_t experts, int32_t top_k,
+                   const void* logits, int64_t ld, mx_dtype dtype, const uint8_t* mask,
+                   int32_t renormalize, int32_t* ids, float* weights, float* lse,
+                   int32_t* counts, int32_t* offsets, int32_t* order, float* balance,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of mx_route's weights, balance and lse:
+ *   dz = p (g - sum_e p_e g_e + d_lse),  g_e = d_balance experts counts_e / (n^2 top_k)
+ *   for a token that counts, plus the weights' share at the winners
+ * d_weights: device float [tokens, top_k] or NULL (zero); d_balance: device float
+ *    [1] or NULL; d_lse: device float [tokens] or NULL.
+ * logits, mask, renormalize: those of the forward pass; ids, weights, lse,
+ *    counts: what it wrote.  d_logits: device [tokens, experts] contiguous, of
+ *    dtype, rounded once. */
+mx_status mx_route_backward(int64_t tokens, int32_t experts, int32_t top_k,
+                            const float* d_weights, const float* d_balance, const float* d_lse,
+                            const void* logits, int64_t ld, mx_dtype dtype, const uint8_t* mask,
+                            int32_t renormalize, const int32_t* ids, const float* weights,
+                            const float* lse, const int32_t* counts, void* d_logits,
+                            cudaStream_t stream);
+
+/* Bytes of the workspace of mx_linear_cross_entropy; 0 for sizes that it
+ * refuses. */
+size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t vocab);
+
+/* Softmax cross entropy over a vocabulary with the product that gives its
+ * logits, which are never stored:
+ *   z[t][v] = sum_h x[t][h] w[v][h]
+ *   lse[t]  = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][labels[t]]
+ * x: device bf16 [tokens, hidden], leading dimension ldx; w: device bf16 [vocab,
+ *    hidden], ldw.  Products accumulate in FP32 on the tensor cores; z is not
+ *    rounded to fewer bits.
+ * labels: device int32 or int64 [tokens] (label_bits 32 or 64).  A token whose
+ *    label is ignore_index has loss 0.  Any other label outside [0, vocab) gives
+ *    loss NaN and is reported through mx_device_status (MX_ERR_DEVICE_ARG).
+ * loss, lse: device float [tokens].
+ * x, w and workspace on 16 bytes, ldx and ldw multiples of 8; hidden a multiple
+ *    of 8; tokens and vocab below 2^24, hidden up to 2^20 (more is
+ *    MX_ERR_UNSUPPORTED); tokens == 0 does nothing.
+ * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes;
+ *    needs no set-up, undefined afterwards. */
+mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
+                                  const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                  const void* labels, int32_t label_bits, int64_t ignore_index,
+                                  float* loss, float* lse,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of the workspace of mx_linear_cross_entropy_backward: dz of a piece of the
+ * vocabulary (512 MB at most, or 256 columns) and, where dx is summed over
+ * several pieces or parts, FP32 [parts, tokens, hidden].  0 for sizes that it
+ * refuses. */
+size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden, int64_t vocab);
+
+/* Gradients of mx_linear_cross_entropy:
+ *   dz[t][v] = (d_loss[t] + d_lse[t]) exp(z[t][v] - lse[t]) - d_loss[t] [v = labels[t]]
+ *   dx = dz w,  dw = dz^T x
+ * piece by piece of the vocabulary, z computed again.  d_loss counts as 0 for a
+ * token whose label is ignore_index or outside the vocabulary.  dz is rounded to
+ * bf16, as an operand of the two products, which accumulate in FP32.
+ * d_loss, d_lse: device float [tokens], or NULL (zero).
+ * lse: device float [tokens], of the forward pass.
+ * dx: device bf16 [tokens, hidden] contiguous; dw: device [vocab, hidden]
+ *    contiguous of dw_dtype; both on 16 bytes.  Sums run in a fixed order for
+ *    given sizes: the same inputs give the same bits.  tokens == 0 writes zeros to
+ *    dw.
+ * Other arguments and constraints as mx_linear_cross_entropy. */
+mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64_t vocab,
+                                           const float* d_loss, const float* d_lse,
+                                           const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                           const void* labels, int32_t label_bits,
+                                           int64_t ignore_index, const float* lse,
+                                           void* dx, void* dw, mx_dtype dw_dtype,
+                                           void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
 /* Synchronizes `stream`, then reads the device status word of the current
  * device and clears the bits it read: MX_OK, MX_ERR_TIMEOUT (a kernel's
  * bounded pipeline wait gave up; its outputs are undefined) or
- * MX_ERR_DEVICE_ARG (invalid group offsets).  The word is shared by all
+ * MX_ERR_DEVICE_ARG (invalid group offsets or labels).  The word is shared by all
  * streams of the device, so the fault may come from a kernel on another
  * stream; a bit that such a kernel sets after the read stays set for the
  * next call.  MX_ERR_CUDA if the synchronization itself failed. */

@@ -9,13 +9,15 @@ without the built library raises.
 Low-level functions carry the C names (mx_quantize, mx_quantize_grouped,
 mx_gemm, mx_grouped_gemm, mx_device_status, ...) and take raw pointers;
 `quantize`, `quantize_grouped`, `gemm` and `grouped_gemm` wrap them for
-torch tensors, and `norm_residual`, `norm_residual_backward` and
-`moe_few_tokens` those of the operators around the products.
+torch tensors, and `norm_residual`, `norm_rotate`, `route`,
+`linear_cross_entropy`, their `_backward` and `moe_few_tokens` those of the
+operators around the products.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 from dataclasses import dataclass
 
@@ -58,7 +60,11 @@ EXPORTS = ("mx_scale_bytes", "mx_grouped_scale_bytes", "mx_grouped_cols_capacity
            "mx_gemm", "mx_gemm_bias_act", "mx_grouped_gemm", "mx_grouped_gemm_bcat",
            "mx_grouped_gemm_wgrad", "mx_norm_residual", "mx_norm_residual_backward",
            "mx_norm_residual_backward_workspace", "mx_moe_few_tokens",
-           "mx_moe_few_tokens_workspace", "mx_device_status", "mx_status_str",
+           "mx_moe_few_tokens_workspace", "mx_norm_rotate", "mx_norm_rotate_backward",
+           "mx_norm_rotate_backward_workspace", "mx_route", "mx_route_backward",
+           "mx_route_workspace", "mx_linear_cross_entropy", "mx_linear_cross_entropy_workspace",
+           "mx_linear_cross_entropy_backward", "mx_linear_cross_entropy_backward_workspace",
+           "mx_device_status", "mx_status_str",
            "mx_set_wait_timeout_ns", "mx_selftest_wait_timeout")
 
 
@@ -122,6 +128,32 @@ def _declare(lib):
                                       c.c_int, vp, vp, c.c_int, i32, vp, i64, vp, vp, vp,
                                       c.c_size_t, vp]
     lib.mx_moe_few_tokens.restype = c.c_int
+    heads = [vp, i64, i64]  # a tensor of heads and its strides
+    lib.mx_norm_rotate.argtypes = [i64] * 5 + heads * 2 + [c.c_int, vp, vp, c.c_int, vp, i32, vp, i32,
+                                                           f32, f32] + heads * 2 + [vp]
+    lib.mx_norm_rotate.restype = c.c_int
+    lib.mx_norm_rotate_backward_workspace.argtypes = [i64, i64]
+    lib.mx_norm_rotate_backward_workspace.restype = c.c_size_t
+    lib.mx_norm_rotate_backward.argtypes = [i64] * 5 + heads * 4 + [
+        c.c_int, vp, vp, c.c_int, vp, i32, vp, i32, f32, f32, vp, vp, vp, vp, vp, c.c_size_t, vp]
+    lib.mx_norm_rotate_backward.restype = c.c_int
+    lib.mx_route_workspace.argtypes = [i64, i32]
+    lib.mx_route_workspace.restype = c.c_size_t
+    lib.mx_route.argtypes = [i64, i32, i32, vp, i64, c.c_int, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                             c.c_size_t, vp]
+    lib.mx_route.restype = c.c_int
+    lib.mx_route_backward.argtypes = [i64, i32, i32, vp, vp, vp, vp, i64, c.c_int, vp, i32, vp, vp, vp,
+                                      vp, vp, vp]
+    lib.mx_route_backward.restype = c.c_int
+    for name in ("mx_linear_cross_entropy_workspace", "mx_linear_cross_entropy_backward_workspace"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = c.c_size_t
+    lib.mx_linear_cross_entropy.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp,
+                                            c.c_size_t, vp]
+    lib.mx_linear_cross_entropy.restype = c.c_int
+    lib.mx_linear_cross_entropy_backward.argtypes = [i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, i32,
+                                                     i64, vp, vp, vp, c.c_int, vp, c.c_size_t, vp]
+    lib.mx_linear_cross_entropy_backward.restype = c.c_int
     lib.mx_device_status.argtypes = [vp]
     lib.mx_device_status.restype = c.c_int
     lib.mx_status_str.argtypes = [c.c_int]
@@ -309,6 +341,69 @@ def mx_moe_few_tokens(tokens, hidden, inter, experts, top_k, x, ldx, router, rou
                                    router_dtype, gate, gate_scales, up, up_scales, fmt_gu, down,
                                    down_scales, fmt_d, renormalize, y, ldy, ids, weights, workspace,
                                    workspace_bytes, stream)
+
+
+def mx_norm_rotate(tokens, q_heads, k_heads, dim, rotary, q, q_st, q_sh, k, k_st, k_sh, x_dtype, w_q,
+                   w_k, w_dtype, positions, position_bits, frequencies, interleaved, scale, eps, out_q,
+                   oq_st, oq_sh, out_k, ok_st, ok_sh, stream) -> int:
+    return lib().mx_norm_rotate(tokens, q_heads, k_heads, dim, rotary, q, q_st, q_sh, k, k_st, k_sh,
+                                x_dtype, w_q, w_k, w_dtype, positions, position_bits, frequencies,
+                                interleaved, scale, eps, out_q, oq_st, oq_sh, out_k, ok_st, ok_sh,
+                                stream)
+
+
+def mx_norm_rotate_backward_workspace(tokens: int, dim: int) -> int:
+    return int(lib().mx_norm_rotate_backward_workspace(tokens, dim))
+
+
+def mx_norm_rotate_backward(tokens, q_heads, k_heads, dim, rotary, d_q, dq_st, dq_sh, d_k, dk_st,
+                            dk_sh, q, q_st, q_sh, k, k_st, k_sh, x_dtype, w_q, w_k, w_dtype, positions,
+                            position_bits, frequencies, interleaved, scale, eps, dx_q, dx_k, dw_q, dw_k,
+                            workspace, workspace_bytes, stream) -> int:
+    return lib().mx_norm_rotate_backward(tokens, q_heads, k_heads, dim, rotary, d_q, dq_st, dq_sh, d_k,
+                                         dk_st, dk_sh, q, q_st, q_sh, k, k_st, k_sh, x_dtype, w_q, w_k,
+                                         w_dtype, positions, position_bits, frequencies, interleaved,
+                                         scale, eps, dx_q, dx_k, dw_q, dw_k, workspace,
+                                         workspace_bytes, stream)
+
+
+def mx_route_workspace(tokens: int, experts: int) -> int:
+    return int(lib().mx_route_workspace(tokens, experts))
+
+
+def mx_route(tokens, experts, top_k, logits, ld, dtype, mask, renormalize, ids, weights, lse, counts,
+             offsets, order, balance, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_route(tokens, experts, top_k, logits, ld, dtype, mask, renormalize, ids, weights,
+                          lse, counts, offsets, order, balance, workspace, workspace_bytes, stream)
+
+
+def mx_route_backward(tokens, experts, top_k, d_weights, d_balance, d_lse, logits, ld, dtype, mask,
+                      renormalize, ids, weights, lse, counts, d_logits, stream) -> int:
+    return lib().mx_route_backward(tokens, experts, top_k, d_weights, d_balance, d_lse, logits, ld,
+                                   dtype, mask, renormalize, ids, weights, lse, counts, d_logits,
+                                   stream)
+
+
+def mx_linear_cross_entropy_workspace(tokens: int, hidden: int, vocab: int) -> int:
+    return int(lib().mx_linear_cross_entropy_workspace(tokens, hidden, vocab))
+
+
+def mx_linear_cross_entropy(tokens, hidden, vocab, x, ldx, w, ldw, labels, label_bits, ignore_index,
+                            loss, lse, workspace, workspace_bytes, stream) -> int:
+    return lib().mx_linear_cross_entropy(tokens, hidden, vocab, x, ldx, w, ldw, labels, label_bits,
+                                         ignore_index, loss, lse, workspace, workspace_bytes, stream)
+
+
+def mx_linear_cross_entropy_backward_workspace(tokens: int, hidden: int, vocab: int) -> int:
+    return int(lib().mx_linear_cross_entropy_backward_workspace(tokens, hidden, vocab))
+
+
+def mx_linear_cross_entropy_backward(tokens, hidden, vocab, d_loss, d_lse, x, ldx, w, ldw, labels,
+                                     label_bits, ignore_index, lse, dx, dw, dw_dtype, workspace,
+                                     workspace_bytes, stream) -> int:
+    return lib().mx_linear_cross_entropy_backward(tokens, hidden, vocab, d_loss, d_lse, x, ldx, w, ldw,
+                                                  labels, label_bits, ignore_index, lse, dx, dw,
+                                                  dw_dtype, workspace, workspace_bytes, stream)
 
 
 def mx_device_status(stream=None) -> int:
@@ -556,9 +651,13 @@ def _native():
         spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        module.init(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
             c.mx_norm_residual, c.mx_norm_residual_backward, c.mx_norm_residual_backward_workspace,
-            c.mx_moe_few_tokens, c.mx_moe_few_tokens_workspace)), torch.cuda.OutOfMemoryError)
+            c.mx_moe_few_tokens, c.mx_moe_few_tokens_workspace, c.mx_norm_rotate,
+            c.mx_norm_rotate_backward, c.mx_norm_rotate_backward_workspace, c.mx_route,
+            c.mx_route_backward, c.mx_route_workspace, c.mx_linear_cross_entropy,
+            c.mx_linear_cross_entropy_workspace, c.mx_linear_cross_entropy_backward,
+            c.mx_linear_cross_entropy_backward_workspace)), torch.cuda.OutOfMemoryError)
         _binding = module
     return _binding
 
@@ -697,6 +796,243 @@ class _MoeFewTokens(torch.autograd.Function):
     @staticmethod
     def backward(ctx, *grads):
         raise RuntimeError("moe_few_tokens has no gradient")
+
+
+def rotary_frequencies(rotary: int, base: float = 10000.0, factor: float = 1.0,
+                       trained_length: float | None = None, fast: float = 32.0, slow: float = 1.0,
+                       device="cuda") -> torch.Tensor:
+    """The frequencies of norm_rotate for `rotary` channels: base^(-2 i / rotary)
+    radians per position, float64 [rotary / 2].  For contexts longer than the
+    trained one they are divided by `factor`: all of them, or, given the
+    trained_length, those that turn less than `slow` times within it, none of
+    those that turn more than `fast` times, and in between in proportion to
+    the turns."""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary must be a positive even number, got {rotary}")
+    if base <= 0 or factor <= 0 or not slow < fast:
+        raise ValueError("base and factor must be positive, slow less than fast")
+    f = torch.pow(torch.tensor(base, dtype=torch.float64),
+                  torch.arange(rotary // 2, dtype=torch.float64) * (-2.0 / rotary))
+    stretched = f / factor
+    if trained_length is not None:
+        keep = ((f * trained_length / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        stretched = f * keep + stretched * (1 - keep)
+    return stretched.to(device)
+
+
+def norm_rotate(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.Tensor,
+                positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
+                scale: float = 1.0, eps: float = 1e-6, out_q: torch.Tensor | None = None,
+                out_k: torch.Tensor | None = None, stream=None):
+    """The norms of query and key heads and their rotation by position in one
+    pass: returns (q', k').  q [tokens, q_heads, dim], k [tokens, k_heads,
+    dim]: bf16 or fp32, channels contiguous, any strides of tokens and heads
+    (parts of a product's rows); w_q, w_k: [dim], bf16 or fp32; positions: int32
+    or int64 [tokens]; frequencies: float64 [rotary / 2], radians per position
+    (rotary_frequencies).  The first `rotary` channels are rotated, in pairs (i,
+    i + rotary / 2), or (2 i, 2 i + 1) where interleaved, and scaled by `scale`.
+    out_q, out_k may be q and k themselves.  Differentiable in q, k, w_q and w_k:
+    where autograd records, the backward pass is norm_rotate_backward, on the
+    stream that autograd runs it on."""
+    raw = None if stream is None else _stream(stream)
+    r = _native().norm_rotate(q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, out_q,
+                              out_k, raw)
+    if r is None:
+        r = _NormRotate.apply(q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, raw)
+        return _recorded_copy(r[0], out_q, stream), _recorded_copy(r[1], out_k, stream)
+    if type(r) is int:
+        raise MxError("mx_norm_rotate", r)
+    return r
+
+
+class _NormRotate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, stream):
+        out = norm_rotate(q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, stream=stream)
+        ctx.save_for_backward(q, k, w_q, w_k, positions, frequencies)
+        ctx.set_materialize_grads(False)
+        ctx.scalars = interleaved, scale, eps
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_q, d_k):
+        if d_q is None and d_k is None:
+            return (None,) * 10
+        q, k, w_q, w_k, positions, frequencies = ctx.saved_tensors
+        # (gradients arrive in any strides: that of a sum is one element, expanded)
+        d_q = torch.zeros_like(q) if d_q is None else d_q.contiguous()
+        d_k = torch.zeros_like(k) if d_k is None else d_k.contiguous()
+        d = norm_rotate_backward(d_q, d_k, q, k, w_q, w_k, positions, frequencies, *ctx.scalars)
+        return tuple(g.to(t.dtype) if want else None for g, t, want in zip(
+            (d.q, d.k, d.w_q, d.w_k), (q, k, w_q, w_k), ctx.needs_input_grad)) + (None,) * 6
+
+
+@dataclass
+class NormRotateGrads:
+    """Gradients of norm_rotate's inputs; those of the weights are FP32."""
+    q: torch.Tensor
+    k: torch.Tensor
+    w_q: torch.Tensor
+    w_k: torch.Tensor
+
+
+def norm_rotate_backward(d_q: torch.Tensor, d_k: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                         w_q: torch.Tensor, w_k: torch.Tensor, positions: torch.Tensor,
+                         frequencies: torch.Tensor, interleaved: bool = False, scale: float = 1.0,
+                         eps: float = 1e-6, workspace: torch.Tensor | None = None,
+                         stream=None) -> NormRotateGrads:
+    """Gradients of norm_rotate from those of its outputs.  Sums run in a fixed
+    order: the same inputs give the same bits.  workspace: uint8,
+    mx_norm_rotate_backward_workspace(tokens, dim) bytes, one call at a time;
+    allocated here when None."""
+    r = _native().norm_rotate_backward(d_q, d_k, q, k, w_q, w_k, positions, frequencies, interleaved,
+                                       scale, eps, workspace,
+                                       None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_norm_rotate_backward", r)
+    return NormRotateGrads(*r)
+
+
+@dataclass
+class Routing:
+    """What route returns.  ids int32, weights fp32 [tokens, top_k]; counts int32
+    [experts], of the tokens that count; offsets int32 [experts + 1] and order
+    int32 [tokens * top_k]: the pairs t * top_k + j by expert, of all tokens
+    (row order[i] // top_k of the tokens is row i of the grouped products'
+    operand, offsets are theirs); balance: fp32 scalar; lse: fp32 [tokens]."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    order: torch.Tensor
+    balance: torch.Tensor
+    lse: torch.Tensor
+
+
+def route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
+          mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+          stream=None) -> Routing:
+    """The experts of every token from the router's logits (bf16 or fp32
+    [tokens, experts]): the top_k largest (equal ones: the lowest index first)
+    with their softmax weights, divided by their sum where renormalize, the
+    counts, offsets and order of the pairs by expert, and the balance loss,
+    experts * sum_e (share of the pairs at e) * (mean probability of e).  mask:
+    bool or uint8 [tokens]; a token that it leaves out is routed, but adds
+    nothing to counts and balance.  Differentiable in weights, balance and lse:
+    where autograd records, the backward pass is route_backward.  workspace:
+    uint8, mx_route_workspace(tokens, experts) bytes, one call at a time;
+    allocated here when None."""
+    raw = None if stream is None else _stream(stream)
+    r = _native().route(logits, top_k, renormalize, mask, workspace, raw)
+    if r is None:
+        r = _Route.apply(logits, top_k, renormalize, mask, workspace, raw)
+    if type(r) is int:
+        raise MxError("mx_route", r)
+    return Routing(*r)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, renormalize, mask, workspace, stream):
+        r = route(logits, top_k, renormalize, mask, workspace, stream)
+        ctx.save_for_backward(logits, mask, r.ids, r.weights, r.counts, r.offsets, r.order, r.balance,
+                              r.lse)
+        ctx.mark_non_differentiable(r.ids, r.counts, r.offsets, r.order)
+        ctx.set_materialize_grads(False)
+        ctx.renormalize = renormalize
+        return r.ids, r.weights, r.counts, r.offsets, r.order, r.balance, r.lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _ids, d_weights, _counts, _offsets, _order, d_balance, d_lse):
+        if d_weights is None and d_balance is None and d_lse is None:
+            return (None,) * 6
+        logits, mask, *routing = ctx.saved_tensors
+        d_weights, d_balance, d_lse = (None if d is None else d.contiguous()
+                                       for d in (d_weights, d_balance, d_lse))
+        return (route_backward(d_weights, d_balance, logits, Routing(*routing), ctx.renormalize, mask,
+                               d_lse),) + (None,) * 5
+
+
+def route_backward(d_weights: torch.Tensor | None, d_balance: torch.Tensor | None,
+                   logits: torch.Tensor, routing: Routing, renormalize: bool = True,
+                   mask: torch.Tensor | None = None, d_lse: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The gradient of route's logits (in their type) from those of its weights
+    (fp32 [tokens, top_k]), balance (fp32, one element) and lse (fp32
+    [tokens]); None: zero.  logits, renormalize and mask: those of the forward
+    pass, which returned `routing`."""
+    r = _native().route_backward(d_weights, d_balance, d_lse, logits, routing.ids, routing.weights,
+                                 routing.counts, routing.lse, renormalize, mask,
+                                 None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_route_backward", r)
+    return r
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
+                         ignore_index: int = -100, workspace: torch.Tensor | None = None,
+                         stream=None):
+    """Softmax cross entropy of the logits x weight^T, which are never stored:
+    returns (loss, lse), fp32 [tokens], lse the logarithm of each token's sum
+    of exponentials.  x: bf16 [tokens, hidden]; weight: bf16 [vocab, hidden];
+    labels: int32 or int64 [tokens].  A token whose label is ignore_index has
+    loss 0; any other label outside the vocabulary gives NaN and is reported by
+    device_status.  Differentiable in both outputs: where autograd records, the
+    backward pass is linear_cross_entropy_backward.  workspace: uint8,
+    mx_linear_cross_entropy_workspace(tokens, hidden, vocab) bytes, one call at
+    a time; allocated here when None."""
+    raw = None if stream is None else _stream(stream)
+    r = _native().linear_cross_entropy(x, weight, labels, ignore_index, workspace, raw)
+    if r is None:
+        r = _LinearCrossEntropy.apply(x, weight, labels, ignore_index, workspace, raw)
+    if type(r) is int:
+        raise MxError("mx_linear_cross_entropy", r)
+    return r
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, labels, ignore_index, workspace, stream):
+        loss, lse = linear_cross_entropy(x, weight, labels, ignore_index, workspace, stream)
+        ctx.save_for_backward(x, weight, labels, lse)
+        ctx.set_materialize_grads(False)
+        ctx.ignore_index = ignore_index
+        return loss, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_loss, d_lse):
+        if d_loss is None and d_lse is None:
+            return (None,) * 6
+        x, weight, labels, lse = ctx.saved_tensors
+        d_loss, d_lse = (None if d is None else d.contiguous() for d in (d_loss, d_lse))
+        dx, dw = linear_cross_entropy_backward(d_loss, d_lse, x, weight, labels, lse, ctx.ignore_index)
+        return tuple(g if want else None
+                     for g, want in zip((dx, dw), ctx.needs_input_grad)) + (None,) * 4
+
+
+def linear_cross_entropy_backward(d_loss: torch.Tensor | None, d_lse: torch.Tensor | None,
+                                  x: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
+                                  lse: torch.Tensor, ignore_index: int = -100,
+                                  weight_dtype: str = "bf16",
+                                  workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (of x: bf16, of weight: bf16 or, with weight_dtype "fp32",
+    fp32) of linear_cross_entropy from those of its outputs (fp32 [tokens];
+    None: zero).  lse: what the forward pass returned.  Goes through the
+    vocabulary in pieces, whose logits are computed again.  The same inputs give
+    the same bits.  workspace: uint8,
+    mx_linear_cross_entropy_backward_workspace(tokens, hidden, vocab) bytes, one
+    call at a time; allocated here when None."""
+    if weight_dtype not in DTYPE:
+        raise ValueError(f"weight_dtype must be one of {sorted(DTYPE)}, got {weight_dtype!r}")
+    r = _native().linear_cross_entropy_backward(d_loss, d_lse, x, weight, labels, lse, ignore_index,
+                                                DTYPE[weight_dtype], workspace,
+                                                None if stream is None else _stream(stream))
+    if type(r) is int:
+        raise MxError("mx_linear_cross_entropy_backward", r)
+    return r
 
 
 def device_status(stream=None) -> int:

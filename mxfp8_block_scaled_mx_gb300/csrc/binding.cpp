@@ -1,5 +1,5 @@
-// binding.cpp -- the tensor API of the block operators, in C++: argument
-// checks, outputs, workspace and the C call in one step.  These operators are
+// binding.cpp -- the tensor API of the operators around the products, in C++:
+// argument checks, outputs, workspace and the C call in one step.  These operators are
 // called for single tokens, where the same work in Python and ctypes took
 // longer than the kernels.
 //
@@ -33,6 +33,16 @@ decltype(&mx_norm_residual_backward) norm_backward_fn;
 decltype(&mx_norm_residual_backward_workspace) norm_workspace_fn;
 decltype(&mx_moe_few_tokens) moe_fn;
 decltype(&mx_moe_few_tokens_workspace) moe_workspace_fn;
+decltype(&mx_norm_rotate) rotate_fn;
+decltype(&mx_norm_rotate_backward) rotate_backward_fn;
+decltype(&mx_norm_rotate_backward_workspace) rotate_workspace_fn;
+decltype(&mx_route) route_fn;
+decltype(&mx_route_backward) route_backward_fn;
+decltype(&mx_route_workspace) route_workspace_fn;
+decltype(&mx_linear_cross_entropy) loss_fn;
+decltype(&mx_linear_cross_entropy_workspace) loss_workspace_fn;
+decltype(&mx_linear_cross_entropy_backward) loss_backward_fn;
+decltype(&mx_linear_cross_entropy_backward_workspace) loss_backward_workspace_fn;
 PyObject* out_of_memory;  // torch's exception for it
 
 struct Refused {
@@ -53,7 +63,8 @@ bool wide(at::ScalarType t) { return t == at::kBFloat16 || t == at::kFloat; }
 mx_dtype code_of(at::ScalarType t) { return t == at::kFloat ? MX_FP32 : MX_BF16; }
 const char* name_of(at::ScalarType t) {
   return t == at::kFloat ? "torch.float32" : t == at::kBFloat16 ? "torch.bfloat16"
-         : t == at::kInt ? "torch.int32" : t == at::kByte ? "torch.uint8" : "torch.bfloat16 or torch.float32";
+         : t == at::kInt ? "torch.int32" : t == at::kByte ? "torch.uint8" : t == at::kDouble ? "torch.float64"
+         : "torch.bfloat16 or torch.float32";
 }
 
 // One call's arguments, which have to be on the current device (asked for
@@ -103,6 +114,43 @@ struct Call {
                     t.sizes() == shape && here(t) && t.is_contiguous();
     if (!ok) refuse(name, std::string("a contiguous ") + name_of(type) + " tensor of shape " + shape_text(shape));
     return t;
+  }
+  // Heads [tokens, heads, dim] with contiguous channels; their strides (those of
+  // a single token or head are the contiguous ones).
+  const at::Tensor& heads_of(int i, const char* name, int64_t tokens, int64_t heads, int64_t dim,
+                             at::ScalarType type, int64_t* st, int64_t* sh) const {
+    const at::Tensor& t = tensor(i, name);
+    const bool ok = (type == at::ScalarType::Undefined ? wide(t.scalar_type()) : t.scalar_type() == type) &&
+                    t.dim() == 3 && t.size(0) == tokens && t.size(1) == heads && t.size(2) == dim &&
+                    here(t) && (dim <= 1 || t.stride(2) == 1);
+    if (!ok)
+      refuse(name, std::string("a ") + name_of(type) + " tensor of shape " +
+                       shape_text({tokens, heads, dim}) + " with unit channel stride,");
+    *st = tokens <= 1 ? heads * dim : t.stride(0);
+    *sh = heads <= 1 ? dim : t.stride(1);
+    return t;
+  }
+  // A contiguous int32 or int64 operand; its bits.
+  const at::Tensor& whole_numbers(int i, const char* name, int64_t n, int32_t* bits) const {
+    const at::Tensor& t = tensor(i, name);
+    if ((t.scalar_type() != at::kInt && t.scalar_type() != at::kLong) || t.dim() != 1 ||
+        t.size(0) != n || !here(t) || !t.is_contiguous())
+      refuse(name, "a contiguous torch.int32 or torch.int64 tensor of shape " + shape_text({n}));
+    *bits = t.scalar_type() == at::kLong ? 64 : 32;
+    return t;
+  }
+  // A contiguous mask of bool or uint8, or no address.
+  const uint8_t* mask_of(int i, int64_t n) const {
+    if (!given(i)) return nullptr;
+    const at::Tensor& t = tensor(i, "mask");
+    if ((t.scalar_type() != at::kBool && t.scalar_type() != at::kByte) || t.dim() != 1 ||
+        t.size(0) != n || !here(t) || !t.is_contiguous())
+      refuse("mask", "a contiguous torch.bool or torch.uint8 tensor of shape " + shape_text({n}));
+    return static_cast<const uint8_t*>(t.data_ptr());
+  }
+  // A contiguous FP32 operand, or no address.
+  const float* floats(int i, const char* name, at::IntArrayRef shape) const {
+    return given(i) ? static_cast<const float*>(dense(i, name, shape, at::kFloat).data_ptr()) : nullptr;
   }
   int64_t integer(int i) const {
     const int64_t v = PyLong_AsLongLong(args[i]);
@@ -363,6 +411,277 @@ PyObject* moe_few_tokens(const Call& c) {
   return out;
 }
 
+PyObject* tuple_of(std::initializer_list<at::Tensor> tensors) {
+  PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : tensors) PyTuple_SET_ITEM(out, i++, THPVariable_Wrap(t));
+  return out;
+}
+
+// The arguments that the heads' norms and their gradient share: q, k, w_q, w_k,
+// positions, frequencies, interleaved, scale, eps, from argument `i` on.
+struct Heads {
+  at::Tensor q, k;
+  int64_t tokens, q_heads, k_heads, dim, rotary, q_st, q_sh, k_st, k_sh;
+  const void *w_q, *w_k, *positions;
+  const double* frequencies;
+  int32_t position_bits, interleaved;
+  mx_dtype x_type, w_type;
+  float scale, eps;
+
+  Heads(const Call& c, int i) {
+    q = c.tensor(i, "q");
+    k = c.tensor(i + 1, "k");
+    if (q.dim() != 3 || k.dim() != 3) throw Refused{"q and k must be 3-D tensors [tokens, heads, dim]"};
+    tokens = q.size(0), q_heads = q.size(1), dim = q.size(2), k_heads = k.size(1);
+    c.heads_of(i, "q", tokens, q_heads, dim, at::ScalarType::Undefined, &q_st, &q_sh);
+    c.heads_of(i + 1, "k", tokens, k_heads, dim, q.scalar_type(), &k_st, &k_sh);
+    x_type = code_of(q.scalar_type());
+    const at::Tensor& w = c.dense(i + 2, "w_q", {dim}, at::ScalarType::Undefined);
+    w_q = w.data_ptr();
+    w_type = code_of(w.scalar_type());
+    w_k = c.dense(i + 3, "w_k", {dim}, w.scalar_type()).data_ptr();
+    positions = c.whole_numbers(i + 4, "positions", tokens, &position_bits).data_ptr();
+    const at::Tensor& f = c.tensor(i + 5, "frequencies");
+    if (f.dim() != 1 || f.size(0) < 1 || 2 * f.size(0) > dim)
+      throw Refused{"frequencies must be a 1-D tensor of 1 to dim / 2 (" + std::to_string(dim / 2) + ") entries"};
+    frequencies = static_cast<const double*>(c.dense(i + 5, "frequencies", {f.size(0)}, at::kDouble).data_ptr());
+    rotary = 2 * f.size(0);
+    interleaved = static_cast<int32_t>(c.integer(i + 6));
+    scale = static_cast<float>(c.real(i + 7));
+    eps = static_cast<float>(c.real(i + 8));
+  }
+};
+
+// q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, out_q, out_k, stream
+PyObject* norm_rotate(const Call& c) {
+  if (c.recorded({0, 1, 2, 3, 9, 10})) Py_RETURN_NONE;
+  const Heads h(c, 0);
+  int64_t oq_st = h.q_heads * h.dim, oq_sh = h.dim, ok_st = h.k_heads * h.dim, ok_sh = h.dim;
+  const Memory memory(c, 11);
+  const at::Tensor out_q =
+      c.given(9) ? c.heads_of(9, "out_q", h.tokens, h.q_heads, h.dim, h.q.scalar_type(), &oq_st, &oq_sh)
+                 : memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
+  const at::Tensor out_k =
+      c.given(10) ? c.heads_of(10, "out_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &ok_st, &ok_sh)
+                  : memory.output({h.tokens, h.k_heads, h.dim}, h.k.options());
+  if (h.tokens > 0) {
+    mx_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = rotate_fn(h.tokens, h.q_heads, h.k_heads, h.dim, h.rotary, h.q.data_ptr(), h.q_st, h.q_sh,
+                  h.k.data_ptr(), h.k_st, h.k_sh, h.x_type, h.w_q, h.w_k, h.w_type, h.positions,
+                  h.position_bits, h.frequencies, h.interleaved, h.scale, h.eps, out_q.data_ptr(), oq_st,
+                  oq_sh, out_k.data_ptr(), ok_st, ok_sh, memory.stream());
+    Py_END_ALLOW_THREADS
+    if (s != MX_OK) return status_of(s);
+  }
+  PyObject* out = PyTuple_New(2);
+  if (!out) return nullptr;
+  const at::Tensor* results[2] = {&out_q, &out_k};
+  for (int i = 0; i < 2; ++i) {
+    if (c.given(9 + i)) {
+      written(*results[i]);
+      Py_INCREF(c.args[9 + i]);
+      PyTuple_SET_ITEM(out, i, c.args[9 + i]);
+    } else {
+      PyTuple_SET_ITEM(out, i, THPVariable_Wrap(*results[i]));
+    }
+  }
+  return out;
+}
+
+// d_q, d_k, q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, workspace, stream
+PyObject* norm_rotate_backward(const Call& c) {
+  const Heads h(c, 2);
+  int64_t dq_st, dq_sh, dk_st, dk_sh;
+  const at::Tensor& d_q = c.heads_of(0, "d_q", h.tokens, h.q_heads, h.dim, h.q.scalar_type(), &dq_st, &dq_sh);
+  const at::Tensor& d_k = c.heads_of(1, "d_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &dk_st, &dk_sh);
+  const Memory memory(c, 12);
+  const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim), h.q);
+  const at::TensorOptions f32 = h.q.options().dtype(at::kFloat);
+  const at::Tensor dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
+  const at::Tensor dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.k.options());
+  const at::Tensor dw_q = memory.output({h.dim}, f32), dw_k = memory.output({h.dim}, f32);
+  // a tensor without tokens has no address; the workspace's stands in, unused
+  void* none = ws.data_ptr();
+  const bool empty = h.tokens == 0;
+  mx_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = rotate_backward_fn(h.tokens, h.q_heads, h.k_heads, h.dim, h.rotary, empty ? none : d_q.data_ptr(), dq_st,
+                         dq_sh, empty ? none : d_k.data_ptr(), dk_st, dk_sh, empty ? none : h.q.data_ptr(),
+                         h.q_st, h.q_sh, empty ? none : h.k.data_ptr(), h.k_st, h.k_sh, h.x_type, h.w_q,
+                         h.w_k, h.w_type, empty ? none : h.positions, h.position_bits, h.frequencies,
+                         h.interleaved, h.scale, h.eps, empty ? none : dx_q.data_ptr(),
+                         empty ? none : dx_k.data_ptr(), static_cast<float*>(dw_q.data_ptr()),
+                         static_cast<float*>(dw_k.data_ptr()), ws.data_ptr(),
+                         static_cast<size_t>(ws.numel()), memory.stream());
+  Py_END_ALLOW_THREADS
+  if (s != MX_OK) return status_of(s);
+  return tuple_of({dx_q, dx_k, dw_q, dw_k});
+}
+
+// Logits [tokens, experts] and top_k.
+struct Logits {
+  at::Tensor z;
+  int64_t tokens, experts, ld, top_k;
+  Logits(const Call& c, int i, int i_top_k) {
+    z = c.tensor(i, "logits");
+    if (z.dim() != 2) throw Refused{"logits must be a 2-D tensor [tokens, experts]"};
+    tokens = z.size(0), experts = z.size(1);
+    c.rows_of(i, "logits", tokens, experts, at::ScalarType::Undefined, &ld);
+    top_k = c.integer(i_top_k);
+    if (top_k < 1 || top_k > experts)
+      throw Refused{"top_k must be 1 to " + std::to_string(experts) + ", got " + std::to_string(top_k)};
+    if (experts > 512) throw Refused{"logits of at most 512 experts are taken, got " + std::to_string(experts)};
+    if (top_k > 32) throw Refused{"top_k must be at most 32, got " + std::to_string(top_k)};
+  }
+};
+
+// logits, top_k, renormalize, mask, workspace, stream
+PyObject* route(const Call& c) {
+  if (c.recorded({0})) Py_RETURN_NONE;
+  const Logits l(c, 0, 1);
+  const uint8_t* mask = c.mask_of(3, l.tokens);
+  const int32_t renormalize = static_cast<int32_t>(c.integer(2));
+  const Memory memory(c, 5);
+  const at::TensorOptions i32 = l.z.options().dtype(at::kInt), f32 = l.z.options().dtype(at::kFloat);
+  const at::Tensor ws =
+      memory.workspace(4, route_workspace_fn(l.tokens, static_cast<int32_t>(l.experts)), l.z);
+  const at::Tensor ids = memory.output({l.tokens, l.top_k}, i32);
+  const at::Tensor weights = memory.output({l.tokens, l.top_k}, f32);
+  const at::Tensor counts = memory.output({l.experts}, i32);
+  const at::Tensor offsets = memory.output({l.experts + 1}, i32);
+  const at::Tensor order = memory.output({l.tokens * l.top_k}, i32);
+  const at::Tensor balance = memory.output({}, f32);
+  const at::Tensor lse = memory.output({l.tokens}, f32);
+  void* none = ws.data_ptr();
+  const bool empty = l.tokens == 0;
+  mx_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = route_fn(l.tokens, static_cast<int32_t>(l.experts), static_cast<int32_t>(l.top_k),
+               empty ? none : l.z.data_ptr(), l.ld, code_of(l.z.scalar_type()), mask, renormalize,
+               static_cast<int32_t*>(empty ? none : ids.data_ptr()),
+               static_cast<float*>(empty ? none : weights.data_ptr()),
+               static_cast<float*>(empty ? none : lse.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
+               static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(empty ? none : order.data_ptr()),
+               static_cast<float*>(balance.data_ptr()), ws.data_ptr(), static_cast<size_t>(ws.numel()),
+               memory.stream());
+  Py_END_ALLOW_THREADS
+  if (s != MX_OK) return status_of(s);
+  return tuple_of({ids, weights, counts, offsets, order, balance, lse});
+}
+
+// d_weights, d_balance, d_lse, logits, ids, weights, counts, lse, renormalize, mask, stream
+PyObject* route_backward(const Call& c) {
+  const at::Tensor& ids = c.tensor(4, "ids");
+  if (ids.dim() != 2) throw Refused{"ids must be a 2-D tensor [tokens, top_k]"};
+  const int64_t top_k = ids.size(1);
+  const at::Tensor& z = c.tensor(3, "logits");
+  if (z.dim() != 2) throw Refused{"logits must be a 2-D tensor [tokens, experts]"};
+  const int64_t tokens = z.size(0), experts = z.size(1);
+  int64_t ld;
+  c.rows_of(3, "logits", tokens, experts, at::ScalarType::Undefined, &ld);
+  if (top_k < 1 || top_k > experts || top_k > 32 || experts > 512)
+    throw Refused{"ids must have 1 to min(experts, 32) columns, logits at most 512"};
+  c.dense(4, "ids", {tokens, top_k}, at::kInt);
+  const at::Tensor& weights = c.dense(5, "weights", {tokens, top_k}, at::kFloat);
+  const at::Tensor& counts = c.dense(6, "counts", {experts}, at::kInt);
+  const at::Tensor& lse = c.dense(7, "lse", {tokens}, at::kFloat);
+  const float* d_weights = c.floats(0, "d_weights", {tokens, top_k});
+  const float* d_balance = nullptr;
+  if (c.given(1)) {
+    const at::Tensor& t = c.tensor(1, "d_balance");
+    if (t.scalar_type() != at::kFloat || t.numel() != 1 || !c.here(t))
+      refuse("d_balance", "a torch.float32 tensor of one element");
+    d_balance = static_cast<const float*>(t.data_ptr());
+  }
+  const float* d_lse = c.floats(2, "d_lse", {tokens});
+  const uint8_t* mask = c.mask_of(9, tokens);
+  const int32_t renormalize = static_cast<int32_t>(c.integer(8));
+  const Memory memory(c, 10);
+  const at::Tensor d = memory.output({tokens, experts}, z.options());
+  if (tokens > 0) {
+    mx_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = route_backward_fn(tokens, static_cast<int32_t>(experts), static_cast<int32_t>(top_k), d_weights,
+                          d_balance, d_lse, z.data_ptr(), ld, code_of(z.scalar_type()), mask, renormalize,
+                          static_cast<const int32_t*>(ids.data_ptr()),
+                          static_cast<const float*>(weights.data_ptr()),
+                          static_cast<const float*>(lse.data_ptr()),
+                          static_cast<const int32_t*>(counts.data_ptr()), d.data_ptr(), memory.stream());
+    Py_END_ALLOW_THREADS
+    if (s != MX_OK) return status_of(s);
+  }
+  return THPVariable_Wrap(d);
+}
+
+// x, weight, labels, from argument `i` on.
+struct Vocabulary {
+  at::Tensor x, w;
+  int64_t tokens, hidden, vocab, ldx, ldw;
+  const void* labels;
+  int32_t label_bits;
+  Vocabulary(const Call& c, int i) {
+    x = c.tensor(i, "x");
+    w = c.tensor(i + 1, "weight");
+    if (x.dim() != 2 || w.dim() != 2) throw Refused{"x and weight must be 2-D tensors"};
+    tokens = x.size(0), hidden = x.size(1), vocab = w.size(0);
+    c.rows_of(i, "x", tokens, hidden, at::kBFloat16, &ldx);
+    c.rows_of(i + 1, "weight", vocab, hidden, at::kBFloat16, &ldw);
+    labels = c.whole_numbers(i + 2, "labels", tokens, &label_bits).data_ptr();
+    if (hidden < 8 || hidden % 8 || vocab < 1)
+      throw Refused{"hidden must be a positive multiple of 8 and the vocabulary not empty"};
+  }
+};
+
+// x, weight, labels, ignore_index, workspace, stream
+PyObject* linear_cross_entropy(const Call& c) {
+  if (c.recorded({0, 1})) Py_RETURN_NONE;
+  const Vocabulary v(c, 0);
+  const int64_t ignore = c.integer(3);
+  const Memory memory(c, 5);
+  const at::TensorOptions f32 = v.x.options().dtype(at::kFloat);
+  const at::Tensor loss = memory.output({v.tokens}, f32), lse = memory.output({v.tokens}, f32);
+  if (v.tokens > 0) {
+    const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
+    mx_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = loss_fn(v.tokens, v.hidden, v.vocab, v.x.data_ptr(), v.ldx, v.w.data_ptr(), v.ldw, v.labels,
+                v.label_bits, ignore, static_cast<float*>(loss.data_ptr()), static_cast<float*>(lse.data_ptr()),
+                ws.data_ptr(), static_cast<size_t>(ws.numel()), memory.stream());
+    Py_END_ALLOW_THREADS
+    if (s != MX_OK) return status_of(s);
+  }
+  return tuple_of({loss, lse});
+}
+
+// d_loss, d_lse, x, weight, labels, lse, ignore_index, weight gradient in FP32, workspace, stream
+PyObject* linear_cross_entropy_backward(const Call& c) {
+  const Vocabulary v(c, 2);
+  const float* d_loss = c.floats(0, "d_loss", {v.tokens});
+  const float* d_lse = c.floats(1, "d_lse", {v.tokens});
+  const at::Tensor& lse = c.dense(5, "lse", {v.tokens}, at::kFloat);
+  const int64_t ignore = c.integer(6);
+  const bool f32 = c.integer(7) != 0;
+  const Memory memory(c, 9);
+  const at::Tensor ws = memory.workspace(8, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
+  const at::Tensor dx = memory.output({v.tokens, v.hidden}, v.x.options());
+  const at::Tensor dw = memory.output({v.vocab, v.hidden}, v.x.options().dtype(f32 ? at::kFloat : at::kBFloat16));
+  void* none = ws.data_ptr();
+  const bool empty = v.tokens == 0;
+  mx_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = loss_backward_fn(v.tokens, v.hidden, v.vocab, empty ? nullptr : d_loss, empty ? nullptr : d_lse,
+                       empty ? none : v.x.data_ptr(), v.ldx, v.w.data_ptr(), v.ldw, empty ? none : v.labels,
+                       v.label_bits, ignore, static_cast<const float*>(empty ? none : lse.data_ptr()),
+                       empty ? none : dx.data_ptr(), dw.data_ptr(), f32 ? MX_FP32 : MX_BF16, ws.data_ptr(),
+                       static_cast<size_t>(ws.numel()), memory.stream());
+  Py_END_ALLOW_THREADS
+  if (s != MX_OK) return status_of(s);
+  return tuple_of({dx, dw});
+}
+
 // No C++ exception leaves the module: a refusal is a ValueError, torch's own
 // errors (out of memory among them) and anything else a RuntimeError.
 template <PyObject* (*F)(const Call&), Py_ssize_t N>
@@ -389,17 +708,33 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
+// One C entry point of `init`'s tuple.
+template <typename Fn>
+bool take(PyObject* addresses, Py_ssize_t i, Fn* fn) {
+  void* at = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addresses, i));
+  *fn = reinterpret_cast<Fn>(at);
+  return at != nullptr;
+}
+
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long a[5];
-  PyObject* oom;
-  if (!PyArg_ParseTuple(args, "KKKKKO", &a[0], &a[1], &a[2], &a[3], &a[4], &oom)) return nullptr;
+  PyObject *a, *oom;
+  if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &a, &oom)) return nullptr;
+  if (PyTuple_GET_SIZE(a) != 15) {
+    PyErr_SetString(PyExc_TypeError, "15 addresses are expected");
+    return nullptr;
+  }
   Py_INCREF(oom);
   Py_XSETREF(out_of_memory, oom);
-  norm_residual_fn = reinterpret_cast<decltype(norm_residual_fn)>(a[0]);
-  norm_backward_fn = reinterpret_cast<decltype(norm_backward_fn)>(a[1]);
-  norm_workspace_fn = reinterpret_cast<decltype(norm_workspace_fn)>(a[2]);
-  moe_fn = reinterpret_cast<decltype(moe_fn)>(a[3]);
-  moe_workspace_fn = reinterpret_cast<decltype(moe_workspace_fn)>(a[4]);
+  const bool all = take(a, 14, &loss_backward_workspace_fn) && take(a, 13, &loss_backward_fn) &&
+                   take(a, 12, &loss_workspace_fn) && take(a, 11, &loss_fn) && take(a, 10, &route_workspace_fn) &&
+                   take(a, 9, &route_backward_fn) && take(a, 8, &route_fn) && take(a, 7, &rotate_workspace_fn) &&
+                   take(a, 6, &rotate_backward_fn) && take(a, 5, &rotate_fn) && take(a, 4, &moe_workspace_fn) &&
+                   take(a, 3, &moe_fn) && take(a, 2, &norm_workspace_fn) && take(a, 1, &norm_backward_fn) &&
+                   take(a, 0, &norm_residual_fn);
+  if (!all) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is missing");
+    return nullptr;
+  }
   Py_RETURN_NONE;
 }
 
@@ -409,10 +744,16 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {
-    {"init", init, METH_VARARGS, "Takes the addresses of the five C entry points and torch's out-of-memory exception."},
+    {"init", init, METH_VARARGS, "Takes the addresses of the C entry points and torch's out-of-memory exception."},
     method<norm_residual, 10>("norm_residual"),
     method<norm_residual_backward, 11>("norm_residual_backward"),
     method<moe_few_tokens, 17>("moe_few_tokens"),
+    method<norm_rotate, 12>("norm_rotate"),
+    method<norm_rotate_backward, 13>("norm_rotate_backward"),
+    method<route, 6>("route"),
+    method<route_backward, 11>("route_backward"),
+    method<linear_cross_entropy, 6>("linear_cross_entropy"),
+    method<linear_cross_entropy_backward, 10>("linear_cross_entropy_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,7 +1,7 @@
 // kernels.h -- launch interface between the C-ABI layer (mx_api.cu) and the
 // CUDA kernels (quantize.cu and quantize_f32.cu, which instantiate
 // quantize_kernel.cuh; gemm_pair.cu; norm.cu, norm_mixed.cu and norm_f32.cu,
-// which instantiate norm_kernel.cuh; moe_few.cu; status.cu).  Not part of the public
+// which instantiate norm_kernel.cuh; moe_few.cu; rotate.cu; route.cu; vocab_loss.cu; status.cu).  Not part of the public
 // ABI.
 #pragma once
 
@@ -198,6 +198,113 @@ size_t moe_few_workspace(int32_t tokens, int64_t hidden, int64_t inter, int32_t 
 cudaError_t launch_moe_few(const MoeFewParams& p, const CUtensorMap& tmap_gate,
                            const CUtensorMap& tmap_up, const CUtensorMap& tmap_down, int num_sms,
                            cudaStream_t stream);
+
+// ------------------------------------------------------------------ heads' norms with rotation
+
+struct RotateParams {
+  const void* q;       // [tokens, q_heads, dim], strides of tokens and heads in elements
+  const void* k;       // [tokens, k_heads, dim]
+  const void* d_q;     // gradient: those of the outputs
+  const void* d_k;
+  const void* w_q;     // [dim]
+  const void* w_k;
+  const void* positions;      // int32 or int64 [tokens]
+  const double* frequencies;  // [rotary / 2], radians per position
+  void* out_q;         // outputs, or the gradients of q and k
+  void* out_k;
+  float* dw_q;         // gradient: [dim]
+  float* dw_k;
+  float* workspace;
+  int64_t q_st, q_sh, k_st, k_sh, dq_st, dq_sh, dk_st, dk_sh, oq_st, oq_sh, ok_st, ok_sh;
+  int32_t tokens, q_heads, k_heads, dim, rotary;
+  int32_t interleaved, x_fp32, w_fp32, positions_64;
+  int32_t chunks;      // every row of every array can be read in chunks of four channels
+  int32_t tokens_per_block, heads_per_block;  // set by the launch
+  float scale, eps;
+};
+
+size_t norm_rotate_backward_workspace(int64_t tokens, int64_t dim);
+cudaError_t launch_norm_rotate(const RotateParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_rotate_backward(const RotateParams& p, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------------ routing
+
+struct RouteParams {
+  const void* logits;        // [tokens, experts], ld
+  const uint8_t* mask;       // [tokens] or nullptr: 0 = does not count
+  int64_t ld;
+  int32_t tokens, experts, top_k, renormalize, logits_fp32;
+  int32_t vec;               // rows allow accesses of four logits
+  int32_t* ids;              // [tokens, top_k]
+  float* weights;            // [tokens, top_k]
+  float* lse;                // [tokens]
+  int32_t* counts;           // [experts]
+  int32_t* offsets;          // [experts + 1]
+  int32_t* order;            // [tokens * top_k]
+  float* balance;            // [1]
+  int32_t* workspace;
+  int32_t blocks, tokens_per_block;  // set by the launch
+  // gradient
+  const float* d_weights;    // [tokens, top_k] or nullptr
+  const float* d_balance;    // [1] or nullptr
+  const float* d_lse;        // [tokens] or nullptr
+  const float* w_in;         // weights, ids, counts and lse of the forward pass
+  const int32_t* ids_in;
+  const int32_t* counts_in;
+  const float* lse_in;
+  void* d_logits;            // [tokens, experts] contiguous
+  int32_t vec_out;
+};
+
+size_t route_workspace(int64_t tokens, int32_t experts);
+cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------------ vocabulary loss
+
+// The products of the vocabulary loss, on one kernel (vocab_loss.cu):
+//   kStats   z = x W^T; per row and half tile of columns the running maximum
+//            and sum of the softmax, and the label's logit
+//   kGrad    dz = (d_loss + d_lse) exp(z - lse) - d_loss [label] of a piece of the
+//            vocabulary, bf16
+//   kDx      dx = dz W of the piece, over `splits` parts of its columns
+//   kDw      dW = dz^T x of the piece
+enum class VocabProduct { kStats, kGrad, kDx, kDw };
+
+struct VocabParams {
+  int32_t m, n, k;         // rows and columns of the product, contraction length
+  int32_t splits;          // parts of the contraction (kDx; else 1)
+  int32_t steps;           // 64-element steps of a part
+  int32_t tokens;
+  const void* labels;      // int32 or int64 [tokens]
+  int32_t labels_64;
+  int64_t ignore_index;
+  int32_t vocab;
+  int32_t col0;            // kGrad: the piece's first column of the vocabulary
+  float2* partial;         // kStats: [tokens][slots] (maximum in log2 units, sum)
+  int32_t slots;
+  float* z_label;          // kStats: [tokens]
+  const float* lse;        // kGrad: [tokens]
+  const float* d_loss;     // [tokens] or nullptr (zero)
+  const float* d_lse;      // [tokens] or nullptr
+  int32_t y_fp32;          // kDx, kDw: type of the output
+  int32_t add;             // kDx: 1 adds to the output (FP32)
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+// Boxes of the tensor maps of A and B: 64 elements x 128 rows where the
+// operand is contiguous along the contraction (A of kStats, kGrad, kDx; B of
+// kStats, kGrad), else 64 x 64; of the output (3-D: columns, rows, parts):
+// 128 bytes x 32 rows; all with the 128-byte swizzle.
+cudaError_t launch_vocab_product(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
+                                 const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
+                                 cudaStream_t stream);
+// loss and lse from the parts of every row.
+cudaError_t launch_vocab_finish(const VocabParams& p, float* loss, float* lse, cudaStream_t stream);
+// bf16 y[i] = sum over parts of parts[s][i], n elements (a multiple of 8).
+cudaError_t launch_vocab_join(const float* parts, int32_t splits, int64_t n, void* y, int num_sms,
+                              cudaStream_t stream);
 
 // Clears the bits `bits` of the device status word (atomically, so bits
 // set meanwhile by kernels on other streams survive).

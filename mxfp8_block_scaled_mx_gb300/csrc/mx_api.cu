@@ -787,6 +787,539 @@ mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32
                                                                                 : MX_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Checks of the heads' norms with rotation that both directions share.
+mx_status rotate_check(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
+                       int64_t rotary, mx_dtype x_dtype, mx_dtype w_dtype, int32_t position_bits,
+                       float eps) {
+  if (!valid_dtype(x_dtype) || !valid_dtype(w_dtype)) return MX_ERR_INVALID_ARG;
+  if (tokens < 0 || q_heads < 1 || k_heads < 1 || dim < 2) return MX_ERR_INVALID_ARG;
+  if (rotary < 2 || rotary % 2 != 0 || rotary > dim) return MX_ERR_INVALID_ARG;
+  if ((position_bits != 32 && position_bits != 64) || !(eps >= 0.f)) return MX_ERR_INVALID_ARG;
+  if (dim > 512 || q_heads > 65536 || k_heads > 65536 || tokens > (1 << 30) ||
+      tokens * (q_heads + k_heads) > INT32_MAX)
+    return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// Heads [tokens, heads, dim] whose rows are apart from one another.
+bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t st, int64_t sh) {
+  if (tokens == 0) return true;
+  return (sh >= dim && st >= (heads - 1) * sh + dim) ||
+         (st >= dim && sh >= (tokens - 1) * st + dim);
+}
+
+bool chunk_aligned(const void* p, int64_t st, int64_t sh, mx_dtype d) {
+  const uintptr_t bytes = d == MX_FP32 ? 16 : 8;
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && st % 4 == 0 && sh % 4 == 0;
+}
+
+mx_status route_check(int64_t tokens, int32_t experts, int32_t top_k, int64_t ld,
+                      mx_dtype dtype) {
+  if (tokens < 0 || experts < 1 || top_k < 1 || top_k > experts || top_k > 32 || ld < experts)
+    return MX_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype)) return MX_ERR_INVALID_ARG;
+  if (experts > 512 || tokens > INT32_MAX / 512) return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// Rows that can be read four elements at a time.
+bool quads(const void* p, int64_t ld, int64_t n, mx_dtype d) {
+  const uintptr_t bytes = d == MX_FP32 ? 16 : 8;
+  return n % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
+                         int64_t rotary, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                         int64_t k_st, int64_t k_sh, mx_dtype x_dtype, const void* w_q,
+                         const void* w_k, mx_dtype w_dtype, const void* positions,
+                         int32_t position_bits, const double* frequencies, int32_t interleaved,
+                         float scale, float eps, void* out_q, int64_t oq_st, int64_t oq_sh,
+                         void* out_k, int64_t ok_st, int64_t ok_sh, cudaStream_t stream) {
+  if (!q || !k || !w_q || !w_k || !positions || !frequencies || !out_q || !out_k)
+    return MX_ERR_INVALID_ARG;
+  mx_status s = rotate_check(tokens, q_heads, k_heads, dim, rotary, x_dtype, w_dtype,
+                             position_bits, eps);
+  if (s != MX_OK) return s;
+  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 ||
+      !rows_apart(tokens, q_heads, dim, oq_st, oq_sh) ||
+      !rows_apart(tokens, k_heads, dim, ok_st, ok_sh))
+    return MX_ERR_INVALID_ARG;
+  if (!aligned_elt(q, x_dtype) || !aligned_elt(k, x_dtype) || !aligned_elt(w_q, w_dtype) ||
+      !aligned_elt(w_k, w_dtype) || !aligned_elt(out_q, x_dtype) || !aligned_elt(out_k, x_dtype) ||
+      (reinterpret_cast<uintptr_t>(frequencies) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & (position_bits / 8 - 1)) != 0)
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (tokens == 0) return MX_OK;
+  if (!all_on_device(st->device, {q, k, w_q, w_k, positions, frequencies, out_q, out_k}))
+    return MX_ERR_INVALID_ARG;
+  mx::RotateParams p{};
+  p.q = q;
+  p.k = k;
+  p.w_q = w_q;
+  p.w_k = w_k;
+  p.positions = positions;
+  p.frequencies = frequencies;
+  p.out_q = out_q;
+  p.out_k = out_k;
+  p.q_st = q_st;
+  p.q_sh = q_sh;
+  p.k_st = k_st;
+  p.k_sh = k_sh;
+  p.oq_st = oq_st;
+  p.oq_sh = oq_sh;
+  p.ok_st = ok_st;
+  p.ok_sh = ok_sh;
+  p.tokens = static_cast<int32_t>(tokens);
+  p.q_heads = static_cast<int32_t>(q_heads);
+  p.k_heads = static_cast<int32_t>(k_heads);
+  p.dim = static_cast<int32_t>(dim);
+  p.rotary = static_cast<int32_t>(rotary);
+  p.interleaved = interleaved != 0;
+  p.x_fp32 = x_dtype == MX_FP32;
+  p.w_fp32 = w_dtype == MX_FP32;
+  p.positions_64 = position_bits == 64;
+  p.scale = scale;
+  p.eps = eps;
+  p.chunks = dim % 8 == 0 && rotary % 8 == 0 && chunk_aligned(q, q_st, q_sh, x_dtype) &&
+             chunk_aligned(k, k_st, k_sh, x_dtype) && chunk_aligned(out_q, oq_st, oq_sh, x_dtype) &&
+             chunk_aligned(out_k, ok_st, ok_sh, x_dtype);
+  return mx::launch_norm_rotate(p, st->num_sms, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+size_t mx_norm_rotate_backward_workspace(int64_t tokens, int64_t dim) {
+  if (tokens < 0 || tokens > (1 << 30) || dim < 2 || dim > 512) return 0;
+  return mx::norm_rotate_backward_workspace(tokens, dim);
+}
+
+mx_status mx_norm_rotate_backward(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
+                                  int64_t rotary, const void* d_q, int64_t dq_st, int64_t dq_sh,
+                                  const void* d_k, int64_t dk_st, int64_t dk_sh, const void* q,
+                                  int64_t q_st, int64_t q_sh, const void* k, int64_t k_st,
+                                  int64_t k_sh, mx_dtype x_dtype, const void* w_q, const void* w_k,
+                                  mx_dtype w_dtype, const void* positions, int32_t position_bits,
+                                  const double* frequencies, int32_t interleaved, float scale,
+                                  float eps, void* dx_q, void* dx_k, float* dw_q, float* dw_k,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!d_q || !d_k || !q || !k || !w_q || !w_k || !positions || !frequencies || !dx_q || !dx_k ||
+      !dw_q || !dw_k)
+    return MX_ERR_INVALID_ARG;
+  mx_status s = rotate_check(tokens, q_heads, k_heads, dim, rotary, x_dtype, w_dtype,
+                             position_bits, eps);
+  if (s != MX_OK) return s;
+  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 || dq_st < 0 || dq_sh < 0 || dk_st < 0 ||
+      dk_sh < 0)
+    return MX_ERR_INVALID_ARG;
+  const size_t need = mx::norm_rotate_backward_workspace(tokens, dim);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  if (!aligned_elt(d_q, x_dtype) || !aligned_elt(d_k, x_dtype) || !aligned_elt(q, x_dtype) ||
+      !aligned_elt(k, x_dtype) || !aligned_elt(w_q, w_dtype) || !aligned_elt(w_k, w_dtype) ||
+      !aligned_elt(dx_q, x_dtype) || !aligned_elt(dx_k, x_dtype) || !aligned_elt(dw_q, MX_FP32) ||
+      !aligned_elt(dw_k, MX_FP32) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(frequencies) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & (position_bits / 8 - 1)) != 0)
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (!all_on_device(st->device, {w_q, w_k, frequencies, dw_q, dw_k})) return MX_ERR_INVALID_ARG;
+  if (tokens == 0)
+    return cudaMemsetAsync(dw_q, 0, dim * sizeof(float), stream) == cudaSuccess &&
+                   cudaMemsetAsync(dw_k, 0, dim * sizeof(float), stream) == cudaSuccess
+               ? MX_OK
+               : MX_ERR_CUDA;
+  if (!all_on_device(st->device, {d_q, d_k, q, k, positions, dx_q, dx_k, workspace}))
+    return MX_ERR_INVALID_ARG;
+  mx::RotateParams p{};
+  p.q = q;
+  p.k = k;
+  p.d_q = d_q;
+  p.d_k = d_k;
+  p.w_q = w_q;
+  p.w_k = w_k;
+  p.positions = positions;
+  p.frequencies = frequencies;
+  p.out_q = dx_q;
+  p.out_k = dx_k;
+  p.dw_q = dw_q;
+  p.dw_k = dw_k;
+  p.workspace = static_cast<float*>(workspace);
+  p.q_st = q_st;
+  p.q_sh = q_sh;
+  p.k_st = k_st;
+  p.k_sh = k_sh;
+  p.dq_st = dq_st;
+  p.dq_sh = dq_sh;
+  p.dk_st = dk_st;
+  p.dk_sh = dk_sh;
+  p.oq_st = q_heads * dim;
+  p.ok_st = k_heads * dim;
+  p.oq_sh = p.ok_sh = dim;
+  p.tokens = static_cast<int32_t>(tokens);
+  p.q_heads = static_cast<int32_t>(q_heads);
+  p.k_heads = static_cast<int32_t>(k_heads);
+  p.dim = static_cast<int32_t>(dim);
+  p.rotary = static_cast<int32_t>(rotary);
+  p.interleaved = interleaved != 0;
+  p.x_fp32 = x_dtype == MX_FP32;
+  p.w_fp32 = w_dtype == MX_FP32;
+  p.positions_64 = position_bits == 64;
+  p.scale = scale;
+  p.eps = eps;
+  p.chunks = dim % 8 == 0 && rotary % 8 == 0 && chunk_aligned(q, q_st, q_sh, x_dtype) &&
+             chunk_aligned(k, k_st, k_sh, x_dtype) && chunk_aligned(d_q, dq_st, dq_sh, x_dtype) &&
+             chunk_aligned(d_k, dk_st, dk_sh, x_dtype) && chunk_aligned(dx_q, 0, 0, x_dtype) &&
+             chunk_aligned(dx_k, 0, 0, x_dtype);
+  return mx::launch_norm_rotate_backward(p, st->num_sms, stream) == cudaSuccess ? MX_OK
+                                                                                : MX_ERR_CUDA;
+}
+
+size_t mx_route_workspace(int64_t tokens, int32_t experts) {
+  if (route_check(tokens, experts, 1, experts, MX_FP32) != MX_OK) return 0;
+  return mx::route_workspace(tokens, experts);
+}
+
+mx_status mx_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int64_t ld,
+                   mx_dtype dtype, const uint8_t* mask, int32_t renormalize, int32_t* ids,
+                   float* weights, float* lse, int32_t* counts, int32_t* offsets, int32_t* order,
+                   float* balance, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!logits || !ids || !weights || !lse || !counts || !offsets || !order || !balance)
+    return MX_ERR_INVALID_ARG;
+  mx_status s = route_check(tokens, experts, top_k, ld, dtype);
+  if (s != MX_OK) return s;
+  const size_t need = mx::route_workspace(tokens, experts);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(ids), static_cast<const void*>(weights),
+                        static_cast<const void*>(lse), static_cast<const void*>(counts),
+                        static_cast<const void*>(offsets), static_cast<const void*>(order),
+                        static_cast<const void*>(balance)})
+    if (!aligned_elt(p, MX_FP32)) return MX_ERR_MISALIGNED;
+  if (!aligned_elt(logits, dtype) || !aligned16(workspace)) return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (!all_on_device(st->device, {counts, offsets, balance})) return MX_ERR_INVALID_ARG;
+  if (tokens > 0 &&
+      !all_on_device(st->device, {logits, mask, ids, weights, lse, order, workspace}))
+    return MX_ERR_INVALID_ARG;
+  mx::RouteParams p{};
+  p.logits = logits;
+  p.mask = mask;
+  p.ld = ld;
+  p.tokens = static_cast<int32_t>(tokens);
+  p.experts = experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize != 0;
+  p.logits_fp32 = dtype == MX_FP32;
+  p.vec = quads(logits, ld, experts, dtype);
+  p.ids = ids;
+  p.weights = weights;
+  p.lse = lse;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.order = order;
+  p.balance = balance;
+  p.workspace = static_cast<int32_t*>(workspace);
+  return mx::launch_route(p, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+mx_status mx_route_backward(int64_t tokens, int32_t experts, int32_t top_k, const float* d_weights,
+                            const float* d_balance, const float* d_lse, const void* logits,
+                            int64_t ld, mx_dtype dtype, const uint8_t* mask, int32_t renormalize,
+                            const int32_t* ids, const float* weights, const float* lse,
+                            const int32_t* counts, void* d_logits, cudaStream_t stream) {
+  if (!logits || !ids || !weights || !lse || !counts || !d_logits) return MX_ERR_INVALID_ARG;
+  mx_status s = route_check(tokens, experts, top_k, ld, dtype);
+  if (s != MX_OK) return s;
+  for (const void* p : {static_cast<const void*>(d_weights), static_cast<const void*>(d_balance),
+                        static_cast<const void*>(d_lse), static_cast<const void*>(ids),
+                        static_cast<const void*>(weights), static_cast<const void*>(lse),
+                        static_cast<const void*>(counts)})
+    if (!aligned_elt(p, MX_FP32)) return MX_ERR_MISALIGNED;
+  if (!aligned_elt(logits, dtype) || !aligned_elt(d_logits, dtype)) return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (tokens == 0) return MX_OK;
+  if (!all_on_device(st->device, {d_weights, d_balance, d_lse, logits, mask, ids, weights, lse,
+                                  counts, d_logits}))
+    return MX_ERR_INVALID_ARG;
+  mx::RouteParams p{};
+  p.logits = logits;
+  p.mask = mask;
+  p.ld = ld;
+  p.tokens = static_cast<int32_t>(tokens);
+  p.experts = experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize != 0;
+  p.logits_fp32 = dtype == MX_FP32;
+  p.vec = quads(logits, ld, experts, dtype);
+  p.d_weights = d_weights;
+  p.d_balance = d_balance;
+  p.d_lse = d_lse;
+  p.w_in = weights;
+  p.ids_in = ids;
+  p.counts_in = counts;
+  p.lse_in = lse;
+  p.d_logits = d_logits;
+  p.vec_out = quads(d_logits, experts, experts, dtype);
+  return mx::launch_route_backward(p, st->num_sms, stream) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of the vocabulary loss: tiles of 256 rows x 256 columns are numbered in
+// 32 bits, rows of x and of the weights start on 16 bytes.
+constexpr int64_t kVocabTile = 256;
+// Bytes of dz that a piece of the vocabulary takes at most (and one tile of
+// columns at least).
+constexpr int64_t kVocabPieceBytes = int64_t{1} << 29;
+
+mx_status vocab_check(int64_t tokens, int64_t hidden, int64_t vocab, int64_t ldx, int64_t ldw,
+                      int32_t label_bits) {
+  if (tokens < 0 || hidden < 8 || hidden % 8 != 0 || vocab < 1) return MX_ERR_INVALID_ARG;
+  if (ldx < hidden || ldw < hidden) return MX_ERR_INVALID_ARG;
+  if (label_bits != 32 && label_bits != 64) return MX_ERR_INVALID_ARG;
+  if (tokens > (1 << 24) || hidden > (1 << 20) || vocab > (1 << 24)) return MX_ERR_UNSUPPORTED;
+  if (ceil_div(tokens, kVocabTile) * ceil_div(vocab, kVocabTile) > INT32_MAX ||
+      ceil_div(vocab, kVocabTile) * ceil_div(hidden, kVocabTile) > INT32_MAX)
+    return MX_ERR_UNSUPPORTED;
+  return MX_OK;
+}
+
+// How the gradient goes through the vocabulary: columns of a piece (whole
+// tiles), and the parts over which dx sums each piece.
+struct VocabPieces {
+  int64_t cols;
+  int32_t splits, steps;
+  bool direct;  // dx is written by its one product
+  size_t dz_bytes, dx_bytes;
+};
+
+VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
+  VocabPieces v;
+  const int64_t most = kVocabPieceBytes / 2 / (tokens > 0 ? tokens : 1) / kVocabTile * kVocabTile;
+  const int64_t all = ceil_div(vocab, kVocabTile) * kVocabTile;
+  v.cols = most < kVocabTile ? kVocabTile : most < all ? most : all;
+  // dx has few tiles where tokens and hidden are small: then parts of the
+  // contraction side by side, as many as fill the pairs of blocks
+  const int64_t tiles = ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
+  const int64_t steps = ceil_div(v.cols, 64);
+  int64_t splits = tiles > 0 ? 76 / tiles : 1;
+  if (splits > steps / 4) splits = steps / 4;
+  if (splits < 1) splits = 1;
+  v.steps = static_cast<int32_t>(ceil_div(steps, splits));
+  v.splits = static_cast<int32_t>(ceil_div(steps, v.steps));
+  v.direct = v.splits == 1 && v.cols >= vocab;
+  v.dz_bytes = static_cast<size_t>(tokens * v.cols * 2);
+  v.dx_bytes = v.direct ? 0 : static_cast<size_t>(tokens * hidden * 4 * v.splits);
+  return v;
+}
+
+size_t vocab_forward_bytes(int64_t tokens, int64_t vocab) {
+  // the label's logits (rounded up to 16 bytes), two parts a tile of columns
+  return static_cast<size_t>(ceil_div(tokens, 4) * 16 +
+                             tokens * ceil_div(vocab, kVocabTile) * 2 * 8);
+}
+
+// 2-D bf16 tensor map, box 64 columns x box_rows, 128-byte swizzle, zero fill.
+mx_status encode_bf16_box(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                          int64_t ld, uint32_t box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * 2)};
+  cuuint32_t box[2] = {64u, box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MX_OK : MX_ERR_CUDA;
+}
+
+// 3-D map of an output [parts][rows][cols] (contiguous parts), box of 128 bytes x
+// 32 rows, 128-byte swizzle.
+mx_status encode_output_map(CUtensorMap* map, void* base, bool f32, int64_t cols, int64_t rows,
+                            int64_t ld, int64_t parts) {
+  const int64_t elt = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(parts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * elt),
+                           static_cast<cuuint64_t>(ld * elt * rows)};
+  cuuint32_t box[3] = {f32 ? 32u : 64u, 32u, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = g_encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MX_OK : MX_ERR_CUDA;
+}
+
+mx::VocabParams vocab_params(const DeviceState* st, int64_t tokens, int64_t vocab,
+                             const void* labels, int32_t label_bits, int64_t ignore_index) {
+  mx::VocabParams p{};
+  p.splits = 1;
+  p.tokens = static_cast<int32_t>(tokens);
+  p.labels = labels;
+  p.labels_64 = label_bits == 64;
+  p.ignore_index = ignore_index;
+  p.vocab = static_cast<int32_t>(vocab);
+  p.status = st->status;
+  p.wait_limit_ns = g_wait_ns.load(std::memory_order_relaxed);
+  return p;
+}
+
+bool aligned_label(const void* p, int32_t bits) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bits / 8 - 1)) == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t vocab) {
+  if (vocab_check(tokens, hidden, vocab, hidden, hidden, 64) != MX_OK) return 0;
+  return vocab_forward_bytes(tokens, vocab);
+}
+
+mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab, const void* x,
+                                  int64_t ldx, const void* w, int64_t ldw, const void* labels,
+                                  int32_t label_bits, int64_t ignore_index, float* loss,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  if (!x || !w || !labels || !loss || !lse) return MX_ERR_INVALID_ARG;
+  mx_status s = vocab_check(tokens, hidden, vocab, ldx, ldw, label_bits);
+  if (s != MX_OK) return s;
+  const size_t need = vocab_forward_bytes(tokens, vocab);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || ldx % 8 != 0 || ldw % 8 != 0 || !aligned16(workspace) ||
+      !aligned_label(labels, label_bits) || !aligned_elt(loss, MX_FP32) ||
+      !aligned_elt(lse, MX_FP32))
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (tokens == 0) return MX_OK;
+  if (!all_on_device(st->device, {x, w, labels, loss, lse, workspace})) return MX_ERR_INVALID_ARG;
+  mx::VocabParams p = vocab_params(st, tokens, vocab, labels, label_bits, ignore_index);
+  p.m = static_cast<int32_t>(tokens);
+  p.n = static_cast<int32_t>(vocab);
+  p.k = static_cast<int32_t>(hidden);
+  p.steps = static_cast<int32_t>(ceil_div(hidden, 64));
+  p.slots = static_cast<int32_t>(ceil_div(vocab, kVocabTile) * 2);
+  p.z_label = static_cast<float*>(workspace);
+  p.partial = reinterpret_cast<float2*>(p.z_label + ceil_div(tokens, 4) * 4);
+  CUtensorMap ta, tb;
+  if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, 128)) != MX_OK) return s;
+  if ((s = encode_bf16_box(&tb, w, hidden, vocab, ldw, 128)) != MX_OK) return s;
+  if (mx::launch_vocab_product(mx::VocabProduct::kStats, p, ta, tb, ta, st->num_sms, stream) !=
+          cudaSuccess ||
+      mx::launch_vocab_finish(p, loss, lse, stream) != cudaSuccess)
+    return MX_ERR_CUDA;
+  return MX_OK;
+}
+
+size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden, int64_t vocab) {
+  if (vocab_check(tokens, hidden, vocab, hidden, hidden, 64) != MX_OK) return 0;
+  const VocabPieces v = vocab_pieces(tokens, hidden, vocab);
+  return v.dz_bytes + v.dx_bytes;
+}
+
+mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64_t vocab,
+                                           const float* d_loss, const float* d_lse, const void* x,
+                                           int64_t ldx, const void* w, int64_t ldw,
+                                           const void* labels, int32_t label_bits,
+                                           int64_t ignore_index, const float* lse, void* dx,
+                                           void* dw, mx_dtype dw_dtype, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream) {
+  if (!x || !w || !labels || !lse || !dx || !dw) return MX_ERR_INVALID_ARG;
+  if (!valid_dtype(dw_dtype)) return MX_ERR_INVALID_ARG;
+  mx_status s = vocab_check(tokens, hidden, vocab, ldx, ldw, label_bits);
+  if (s != MX_OK) return s;
+  const VocabPieces v = vocab_pieces(tokens, hidden, vocab);
+  const size_t need = v.dz_bytes + v.dx_bytes;
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
+  const bool dw_f32 = dw_dtype == MX_FP32;
+  if (!aligned16(x) || !aligned16(w) || ldx % 8 != 0 || ldw % 8 != 0 || !aligned16(dx) ||
+      !aligned16(dw) || !aligned16(workspace) ||
+      !aligned_label(labels, label_bits) || !aligned_elt(d_loss, MX_FP32) ||
+      !aligned_elt(d_lse, MX_FP32) || !aligned_elt(lse, MX_FP32))
+    return MX_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((s = device_state(&st)) != MX_OK) return s;
+  if (!all_on_device(st->device, {w, dw})) return MX_ERR_INVALID_ARG;
+  const int64_t dw_elt = dw_f32 ? 4 : 2;
+  if (tokens == 0)
+    return cudaMemsetAsync(dw, 0, static_cast<size_t>(vocab * hidden * dw_elt), stream) ==
+                   cudaSuccess
+               ? MX_OK
+               : MX_ERR_CUDA;
+  if (!all_on_device(st->device, {d_loss, d_lse, x, labels, lse, dx, workspace}))
+    return MX_ERR_INVALID_ARG;
+  uint8_t* dz = static_cast<uint8_t*>(workspace);
+  float* parts = reinterpret_cast<float*>(dz + v.dz_bytes);
+  for (int64_t col0 = 0; col0 < vocab; col0 += v.cols) {
+    const int64_t cols = v.cols < vocab - col0 ? v.cols : vocab - col0;
+    const void* w_piece = static_cast<const uint8_t*>(w) + col0 * ldw * 2;
+    mx::VocabParams p = vocab_params(st, tokens, vocab, labels, label_bits, ignore_index);
+    CUtensorMap ta, tb, ty;
+    // dz of the piece
+    p.m = static_cast<int32_t>(tokens);
+    p.n = static_cast<int32_t>(cols);
+    p.k = static_cast<int32_t>(hidden);
+    p.steps = static_cast<int32_t>(ceil_div(hidden, 64));
+    p.col0 = static_cast<int32_t>(col0);
+    p.lse = lse;
+    p.d_loss = d_loss;
+    p.d_lse = d_lse;
+    if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, 128)) != MX_OK) return s;
+    if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 128)) != MX_OK) return s;
+    if ((s = encode_output_map(&ty, dz, false, cols, tokens, v.cols, 1)) != MX_OK) return s;
+    if (mx::launch_vocab_product(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream) !=
+        cudaSuccess)
+      return MX_ERR_CUDA;
+    // dx of the piece: contiguous along the vocabulary times contiguous along hidden
+    p.n = static_cast<int32_t>(hidden);
+    p.k = static_cast<int32_t>(cols);
+    p.steps = v.steps;
+    p.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
+    p.y_fp32 = !v.direct;
+    p.add = col0 > 0;
+    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, 128)) != MX_OK) return s;
+    if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
+    if ((s = encode_output_map(&ty, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
+                               v.splits)) != MX_OK)
+      return s;
+    if (mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream) !=
+        cudaSuccess)
+      return MX_ERR_CUDA;
+    // dW of the piece: both operands contiguous along their rows
+    p.m = static_cast<int32_t>(cols);
+    p.k = static_cast<int32_t>(tokens);
+    p.steps = static_cast<int32_t>(ceil_div(tokens, 64));
+    p.splits = 1;
+    p.y_fp32 = dw_f32;
+    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, 64)) != MX_OK) return s;
+    if ((s = encode_bf16_box(&tb, x, hidden, tokens, ldx, 64)) != MX_OK) return s;
+    if ((s = encode_output_map(&ty, static_cast<uint8_t*>(dw) + col0 * hidden * dw_elt, dw_f32,
+                               hidden, cols, hidden, 1)) != MX_OK)
+      return s;
+    if (mx::launch_vocab_product(mx::VocabProduct::kDw, p, ta, tb, ty, st->num_sms, stream) !=
+        cudaSuccess)
+      return MX_ERR_CUDA;
+  }
+  if (!v.direct && mx::launch_vocab_join(parts, v.splits, tokens * hidden, dx, st->num_sms,
+                                         stream) != cudaSuccess)
+    return MX_ERR_CUDA;
+  return MX_OK;
+}
+
 mx_status mx_device_status(cudaStream_t stream) {
   DeviceState* st = nullptr;
   mx_status s = device_state(&st);
@@ -803,7 +1336,7 @@ mx_status mx_device_status(cudaStream_t stream) {
       return MX_ERR_CUDA;
   }
   if (word & 1u) return MX_ERR_TIMEOUT;
-  if (word & 2u) return MX_ERR_DEVICE_ARG;
+  if (word & 6u) return MX_ERR_DEVICE_ARG;
   return MX_OK;
 }
 

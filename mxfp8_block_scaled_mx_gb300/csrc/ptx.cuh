@@ -176,6 +176,42 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
       : "memory");
 }
 
+// 3-D tiled tensor store shared -> global, or addition to global memory, in
+// this thread's current group of copies; elements outside the tensor are left
+// out.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* smem_src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(tmap)),
+      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const void* tmap, const void* smem_src, int32_t x,
+                                           int32_t y, int32_t z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+      " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Waits until at most N of this thread's groups of copies still read shared
+// memory (they complete by themselves), or until all are complete.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Orders this thread's stores to shared memory before copies out of it.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tc_fence_before_sync() {
@@ -227,6 +263,15 @@ __host__ __device__ constexpr uint32_t mxf8_idesc(uint32_t fa, uint32_t fb, uint
                                                   uint32_t n, uint32_t sfa_id, uint32_t sfb_id) {
   return (sfb_id & 3u) << 4 | (fa & 7u) << 7 | (fb & 7u) << 10 | ((n >> 3) & 0x3Fu) << 17 |
          1u << 23 | ((m >> 4) & 0x1Fu) << 24 | (sfa_id & 3u) << 29;
+}
+
+// Instruction descriptor of kind::f16 with bf16 operands and an FP32
+// accumulator; a_mn, b_mn: 1 where that operand is contiguous along M or N
+// instead of K.
+__host__ __device__ constexpr uint32_t bf16_idesc(uint32_t m, uint32_t n, uint32_t a_mn,
+                                                  uint32_t b_mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | a_mn << 15 | b_mn << 16 | ((n >> 3) & 0x3Fu) << 17 |
+         ((m >> 4) & 0x1Fu) << 24;
 }
 
 // ---------------------------------------------------------------- block pairs
@@ -327,6 +372,20 @@ __device__ __forceinline__ void tc_mma_pair_mxf8(uint32_t d_tmem, uint32_t a_lo,
       " [%0], da, db, %5, [%6], [%7], p;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
       "r"(accumulate)
+      : "memory");
+}
+
+// The same for 16-bit operands (kind::f16): K = 16 elements an instruction.
+__device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                                uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

@@ -10,6 +10,12 @@
     python -m mxfp8_block_scaled_mx_gb300.cases norm_backward --rows 16384 --cols 7168 [--gates 4] [--fp32]
     python -m mxfp8_block_scaled_mx_gb300.cases moe_few --tokens 16 --experts 64 --k 7168 --inter 2048 --top-k 8 [--fmt e2m1_packed]
     python -m mxfp8_block_scaled_mx_gb300.cases block --tokens 16 --experts 64 --k 7168 --inter 2048 --top-k 8
+    python -m mxfp8_block_scaled_mx_gb300.cases rotate --tokens 16384 --heads 40 --dim 128
+    python -m mxfp8_block_scaled_mx_gb300.cases rotate_backward --tokens 16384 --heads 40 --dim 128
+    python -m mxfp8_block_scaled_mx_gb300.cases route --tokens 65536 --experts 64 --top-k 8
+    python -m mxfp8_block_scaled_mx_gb300.cases route_backward --tokens 65536 --experts 64 --top-k 8
+    python -m mxfp8_block_scaled_mx_gb300.cases loss --tokens 4096 --k 7168 --vocab 131072
+    python -m mxfp8_block_scaled_mx_gb300.cases loss_backward --tokens 4096 --k 7168 --vocab 131072
 
 Inputs are the seeded synthetic workloads; each case launches the kernel
 `--reps` times after building its inputs and prints the mean event time.
@@ -100,7 +106,9 @@ def moe_block(a, dev):
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["gemm", "quantize", "grouped", "moe_dgrad", "moe_wgrad",
-                                     "moe_quantize", "norm", "norm_backward", "moe_few", "block"])
+                                     "moe_quantize", "norm", "norm_backward", "moe_few", "block",
+                                     "rotate", "rotate_backward", "route", "route_backward", "loss",
+                                     "loss_backward"])
     ap.add_argument("--m", type=int, default=4096)
     ap.add_argument("--n", type=int, default=18432)
     ap.add_argument("--k", type=int, default=7168)
@@ -113,6 +121,9 @@ def main(argv=None):
     ap.add_argument("--top-k", type=int, default=8, help="moe_few, block: experts of a token")
     ap.add_argument("--fmt", default="e4m3", choices=["e4m3", "e5m2", "e2m1_packed"],
                     help="moe_few, block: format of the expert weights")
+    ap.add_argument("--heads", type=int, default=40, help="rotate: a fifth of them keys")
+    ap.add_argument("--dim", type=int, default=128, help="rotate: channels of a head")
+    ap.add_argument("--vocab", type=int, default=131072)
     ap.add_argument("--gates", type=int, default=0, help="norm, norm_backward: rows of the gate")
     ap.add_argument("--out", default="bf16", choices=["bf16", "fp32"])
     ap.add_argument("--reps", type=int, default=3)
@@ -204,6 +215,43 @@ def main(argv=None):
         per = (2 if a.case == "norm" else 3) * (2 + res.element_size())
         print(f"{a.case} {a.rows}x{a.cols}{' fp32 stream' if a.fp32 else ''} gates {a.gates}: "
               f"{ms:.4f} ms, {a.rows * a.cols * per / ms / 1e6:.1f} GB/s")
+    elif a.case in ("rotate", "rotate_backward"):
+        keys = a.heads // 5
+        rows, grads = (W.synth_matrix((a.tokens, a.heads, a.dim), std, seed=s, device=dev)
+                       for s, std in ((51, 1.5), (52, 1e-3)))
+        w_q, w_k = (W.synth_matrix((a.dim,), 0.1, seed=s, device=dev) + 1 for s in (53, 54))
+        args = (rows[:, keys:], rows[:, :keys], w_q, w_k, torch.arange(a.tokens, device=dev),
+                mx.rotary_frequencies(a.dim, device=dev))
+        if a.case == "rotate":
+            fn = lambda: mx.norm_rotate(*args)  # noqa: E731
+        else:
+            fn = lambda: mx.norm_rotate_backward(grads[:, keys:], grads[:, :keys], *args)  # noqa: E731
+        ms = _time(fn, a.reps)
+        n = rows.numel() * 2 * (2 if a.case == "rotate" else 3)
+        print(f"{a.case} {a.tokens} tokens x {a.heads} heads of {a.dim}: {ms:.4f} ms, {n / ms / 1e6:.1f} GB/s")
+    elif a.case in ("route", "route_backward"):
+        z = W.synth_matrix((a.tokens, a.experts), 1.0, seed=55, device=dev, dtype=torch.float32)
+        r = mx.route(z, a.top_k)
+        d = W.synth_matrix((a.tokens, a.top_k), 1e-3, seed=56, device=dev, dtype=torch.float32)
+        if a.case == "route":
+            fn = lambda: mx.route(z, a.top_k)  # noqa: E731
+        else:
+            fn = lambda: mx.route_backward(d, r.balance, z, r)  # noqa: E731
+        ms = _time(fn, a.reps)
+        print(f"{a.case} {a.tokens} tokens x {a.experts} experts, top {a.top_k}: {ms:.4f} ms")
+    elif a.case in ("loss", "loss_backward"):
+        x = W.synth_matrix((a.tokens, a.k), 1.0, seed=57, device=dev)
+        w = W.synth_matrix((a.vocab, a.k), 2.0 / a.k ** 0.5, seed=58, device=dev)
+        labels = torch.arange(a.tokens, device=dev) * 7919 % a.vocab
+        loss, lse = mx.linear_cross_entropy(x, w, labels)
+        if a.case == "loss":
+            fn = lambda: mx.linear_cross_entropy(x, w, labels)  # noqa: E731
+        else:
+            one = torch.full_like(lse, 1.0 / a.tokens)
+            fn = lambda: mx.linear_cross_entropy_backward(one, None, x, w, labels, lse)  # noqa: E731
+        ms = _time(fn, a.reps)
+        n = (1 if a.case == "loss" else 3) * 2 * a.tokens * a.k * a.vocab
+        print(f"{a.case} {a.tokens} x {a.k}, vocabulary {a.vocab}: {ms:.4f} ms, {n / ms / 1e9:.1f} TFLOP/s")
     elif a.case in ("moe_few", "block"):
         step, p = moe_block(a, dev)
         x = W.synth_matrix((a.tokens, a.k), 1.0, seed=41, device=dev)

@@ -219,7 +219,8 @@ struct RotateParams {
   int32_t tokens, q_heads, k_heads, dim, rotary;
   int32_t interleaved, x_fp32, w_fp32, positions_64;
   int32_t chunks;      // every row of every array can be read in chunks of four channels
-  int32_t tokens_per_block, heads_per_block;  // set by the launch
+  // items of work, set by the launch
+  int32_t tokens_per_item, heads_per_item, chunks_of_heads, items;
   float scale, eps;
 };
 

@@ -22,8 +22,8 @@
 
 #include <cstdint>
 
-#include "epilogue.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace mx {
@@ -33,7 +33,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTable = 2048;  // pairs of cosine and sine of a block
+constexpr int kMaxTable = 1024;  // angles of an item's tokens
 
 // Fraction of a turn per position, in units of 2^-64, of a frequency in radians:
 // the 53-bit significand times 2^66 / (2 pi), shifted to the binary point (and
@@ -54,15 +54,19 @@ __device__ __forceinline__ uint64_t turns_of(double frequency) {
   return (b >> 63) ? 0 - v : v;
 }
 
-__device__ __forceinline__ float2 angle(const RotateParams& p, int64_t token, int32_t i) {
-  const int64_t pos = p.positions_64 ? static_cast<const int64_t*>(p.positions)[token]
-                                     : static_cast<const int32_t*>(p.positions)[token];
-  const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(p.frequencies[i]);
-  // signed half turns: the top 32 bits, rounded
+// Cosine and sine, times the scale, of an angle given as a fraction of a turn in
+// units of 2^-64: its top 32 bits, rounded, are signed half turns.
+__device__ __forceinline__ float2 unit_of(uint64_t turn, float scale) {
   const int32_t top = static_cast<int32_t>((turn + (1ull << 31)) >> 32);
   float s, c;
   sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
-  return make_float2(c * p.scale, s * p.scale);
+  return make_float2(c * scale, s * scale);
+}
+
+__device__ __forceinline__ uint64_t position_of(const RotateParams& p, int32_t token) {
+  return static_cast<uint64_t>(
+      p.positions_64 ? static_cast<const int64_t*>(p.positions)[token]
+                     : static_cast<int64_t>(static_cast<const int32_t*>(p.positions)[token]));
 }
 
 __device__ __forceinline__ float weight_of(const void* w, int32_t f32, int32_t i) {
@@ -70,55 +74,16 @@ __device__ __forceinline__ float weight_of(const void* w, int32_t f32, int32_t i
              : __bfloat162float(static_cast<const bf16*>(w)[i]);
 }
 
-// C consecutive elements as loaded.
-template <typename T, int C>
-struct Chunk;
-template <>
-struct Chunk<bf16, 4> {
-  uint2 v;
-  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-  }
-  static __device__ __forceinline__ void store(bf16* p, const float* f) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-  }
-};
-template <>
-struct Chunk<float, 4> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <>
-struct Chunk<bf16, 1> {
-  bf16 v;
-  __device__ __forceinline__ void load(const bf16* p) { v = *p; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = __bfloat162float(v); }
-  static __device__ __forceinline__ void store(bf16* p, const float* f) {
-    *p = __float2bfloat16_rn(f[0]);
-  }
-};
-template <>
-struct Chunk<float, 1> {
-  float v;
-  __device__ __forceinline__ void load(const float* p) { v = *p; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = v; }
-  static __device__ __forceinline__ void store(float* p, const float* f) { *p = f[0]; }
-};
+// ------------------------------------------------------------------ a lane's share of a row
 
-// A lane's share of a row: S slots of two chunks of C channels, which hold whole
-// pairs where the slot is one of the rotated part.
+// A slot is two chunks of C channels, at a and b, whose values a lane holds as
+// pairs of floats: with C = 4 the first channels of four pairs, then their
+// second ones; with C = 1 a pair (b may be missing at the end of an odd row).
 template <int C, int LPR, int S, bool INTER>
 struct Lane {
+  static constexpr int kHalves = C == 4 ? 4 : 1;  // float2 of a slot
   int32_t a[S], b[S];  // first channels of the chunks, -1 where there is none
-  int32_t pair[S];     // first pair, or -1
+  int32_t pair[S];     // first pair, or -1: not rotated
   __device__ __forceinline__ Lane(const RotateParams& p, int32_t lane) {
     const int32_t turned = p.rotary / (2 * C);
 #pragma unroll
@@ -136,49 +101,127 @@ struct Lane {
       }
     }
   }
-};
-
-template <typename T, int C, int S>
-struct Row {
-  Chunk<T, C> a[S], b[S];
-  template <typename L>
-  __device__ __forceinline__ void load(const T* p, const L& l) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (l.a[s] >= 0) a[s].load(p + l.a[s]);
-      if (l.b[s] >= 0) b[s].load(p + l.b[s]);
-    }
-  }
-  // values of slot s, zero where there is no channel
-  template <typename L>
-  __device__ __forceinline__ void get(int s, const L& l, float* f) const {
-    if (l.a[s] >= 0) {
-      a[s].get(f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) f[i] = 0.f;
-    }
-    if (l.b[s] >= 0) {
-      b[s].get(f + C);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) f[C + i] = 0.f;
-    }
+  // Channel of value e (0 .. 2 C - 1, in the order held) of slot s, or -1.
+  __device__ __forceinline__ int32_t channel(int s, int e) const {
+    if (C == 1) return e == 0 ? a[s] : b[s];
+    if (a[s] < 0) return -1;
+    if (INTER) return a[s] + (e < C ? 2 * e : 2 * (e - C) + 1);
+    return e < C ? a[s] + e : b[s] + e - C;
   }
 };
 
-// Turns the pairs of a slot by their angles (sign -1: back).
-template <int C, bool INTER>
-__device__ __forceinline__ void turn(float* f, const float2* tab, float sign) {
+// A slot's values as loaded.
+template <typename T, int C>
+struct Raw;
+template <>
+struct Raw<bf16, 4> {
+  uint2 a, b;
+};
+template <>
+struct Raw<float, 4> {
+  float4 a, b;
+};
+template <typename T>
+struct Raw<T, 1> {
+  T a, b;
+};
+
+template <typename T, int C, typename L, int S>
+__device__ __forceinline__ void load_row(Raw<T, C> (&r)[S], const T* p, const L& l) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    float& u = f[INTER ? 2 * i : i];
-    float& v = f[INTER ? 2 * i + 1 : C + i];
-    const float c = tab[i].x, s = tab[i].y * sign;
-    const float y = u * c - v * s;
-    v = u * s + v * c;
-    u = y;
+  for (int s = 0; s < S; ++s) {
+    if (l.a[s] >= 0) r[s].a = *reinterpret_cast<const decltype(r[s].a)*>(p + l.a[s]);
+    if (l.b[s] >= 0) r[s].b = *reinterpret_cast<const decltype(r[s].b)*>(p + l.b[s]);
   }
+}
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+template <bool INTER, typename L>
+__device__ __forceinline__ void values(const Raw<bf16, 4>& r, int s, const L& l, float2* h) {
+  if (l.a[s] < 0) {
+    h[0] = h[1] = h[2] = h[3] = both(0.f);
+  } else if (INTER) {
+    h[0] = make_float2(low(r.a.x), low(r.a.y)), h[1] = make_float2(low(r.b.x), low(r.b.y));
+    h[2] = make_float2(high(r.a.x), high(r.a.y)), h[3] = make_float2(high(r.b.x), high(r.b.y));
+  } else {
+    h[0] = unpack2(r.a.x), h[1] = unpack2(r.a.y), h[2] = unpack2(r.b.x), h[3] = unpack2(r.b.y);
+  }
+}
+template <bool INTER, typename L>
+__device__ __forceinline__ void values(const Raw<float, 4>& r, int s, const L& l, float2* h) {
+  if (l.a[s] < 0) {
+    h[0] = h[1] = h[2] = h[3] = both(0.f);
+  } else if (INTER) {
+    h[0] = make_float2(r.a.x, r.a.z), h[1] = make_float2(r.b.x, r.b.z);
+    h[2] = make_float2(r.a.y, r.a.w), h[3] = make_float2(r.b.y, r.b.w);
+  } else {
+    h[0] = make_float2(r.a.x, r.a.y), h[1] = make_float2(r.a.z, r.a.w);
+    h[2] = make_float2(r.b.x, r.b.y), h[3] = make_float2(r.b.z, r.b.w);
+  }
+}
+__device__ __forceinline__ float wide(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float wide(float v) { return v; }
+template <bool INTER, typename T, typename L>
+__device__ __forceinline__ void values(const Raw<T, 1>& r, int s, const L& l, float2* h) {
+  h[0] = make_float2(l.a[s] < 0 ? 0.f : wide(r.a), l.b[s] < 0 ? 0.f : wide(r.b));
+}
+
+template <bool INTER, typename L>
+__device__ __forceinline__ void store(bf16* p, int s, const L& l, const float2 (&h)[4]) {
+  if (l.a[s] < 0) return;
+  uint2 a, b;
+  if (INTER) {
+    a = make_uint2(pack2(make_float2(h[0].x, h[2].x)), pack2(make_float2(h[0].y, h[2].y)));
+    b = make_uint2(pack2(make_float2(h[1].x, h[3].x)), pack2(make_float2(h[1].y, h[3].y)));
+  } else {
+    a = make_uint2(pack2(h[0]), pack2(h[1]));
+    b = make_uint2(pack2(h[2]), pack2(h[3]));
+  }
+  *reinterpret_cast<uint2*>(p + l.a[s]) = a;
+  *reinterpret_cast<uint2*>(p + l.b[s]) = b;
+}
+template <bool INTER, typename L>
+__device__ __forceinline__ void store(float* p, int s, const L& l, const float2 (&h)[4]) {
+  if (l.a[s] < 0) return;
+  float4 a, b;
+  if (INTER) {
+    a = make_float4(h[0].x, h[2].x, h[0].y, h[2].y);
+    b = make_float4(h[1].x, h[3].x, h[1].y, h[3].y);
+  } else {
+    a = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    b = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
+  }
+  *reinterpret_cast<float4*>(p + l.a[s]) = a;
+  *reinterpret_cast<float4*>(p + l.b[s]) = b;
+}
+__device__ __forceinline__ void store1(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+template <bool INTER, typename T, typename L>
+__device__ __forceinline__ void store(T* p, int s, const L& l, const float2 (&h)[1]) {
+  if (l.a[s] >= 0) store1(p + l.a[s], h[0].x);
+  if (l.b[s] >= 0) store1(p + l.b[s], h[0].y);
+}
+
+// Turns a slot's pairs: c and s are the cosines and sines of its first pair on.
+template <bool BACK>
+__device__ __forceinline__ void turn(float2 (&h)[4], const float* c, const float* s) {
+  const float4 c4 = *reinterpret_cast<const float4*>(c), s4 = *reinterpret_cast<const float4*>(s);
+  const float2 cc[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+  const float2 ss[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 minus = make_float2(-ss[i].x, -ss[i].y);
+    const float2 u = h[i], v = h[2 + i];
+    h[i] = fma2(v, BACK ? ss[i] : minus, mul2(u, cc[i]));
+    h[2 + i] = fma2(u, BACK ? minus : ss[i], mul2(v, cc[i]));
+  }
+}
+template <bool BACK>
+__device__ __forceinline__ void turn(float2 (&h)[1], const float* c, const float* s) {
+  const float sn = BACK ? -*s : *s;
+  h[0] = make_float2(fmaf(-h[0].y, sn, h[0].x * *c), fmaf(h[0].x, sn, h[0].y * *c));
 }
 
 template <int LPR>
@@ -188,246 +231,342 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Rows of a block: tokens [t0, t0 + nt) x heads [h0, h0 + nh) of queries, then keys.
-struct Rows {
+// ------------------------------------------------------------------ work of a block
+
+// An item of work: tokens [t0, t0 + nt) x heads [h0, h0 + nh), queries' first.  Its
+// rows go round the groups of lanes; the rows of a group have the same places in
+// every item.
+struct Item {
   int32_t t0, nt, h0, nh;
-  __device__ __forceinline__ int32_t count() const { return nt * nh; }
+};
+__device__ __forceinline__ Item item_of(const RotateParams& p, int32_t i) {
+  Item it;
+  const int32_t g = p.chunks_of_heads == 1 ? i : i / p.chunks_of_heads;
+  it.t0 = g * p.tokens_per_item;
+  it.nt = min(p.tokens_per_item, p.tokens - it.t0);
+  it.h0 = (i - g * p.chunks_of_heads) * p.heads_per_item;
+  it.nh = min(p.heads_per_item, p.q_heads + p.k_heads - it.h0);
+  return it;
+}
+
+// What all items of a block share, in shared memory: the frequencies as fractions
+// of a turn, the weights in the order that lanes hold values (queries', then
+// keys'), two tables of cosines and sines [token][2][pairs].
+template <int C, int LPR, int S>
+struct Shared {
+  static constexpr int kRow = 2 * C * LPR * S;  // values of a row's slots
+  uint64_t* turns;
+  float* weights;
+  float* table;
+  int32_t half, table_size;
+  __device__ __forceinline__ Shared(const RotateParams& p, uint8_t* smem) {
+    half = p.rotary / 2;
+    weights = reinterpret_cast<float*>(smem);
+    table = weights + 2 * kRow;
+    table_size = p.tokens_per_item * 2 * half;
+    turns = reinterpret_cast<uint64_t*>(table + 2 * table_size);
+  }
+  static size_t bytes(const RotateParams& p) {
+    return sizeof(float) * (2 * kRow + 4 * p.tokens_per_item * (p.rotary / 2)) +
+           sizeof(uint64_t) * (p.rotary / 2);
+  }
+  template <typename L>
+  __device__ __forceinline__ void fill_once(const RotateParams& p, const L& l) {
+    for (int32_t i = threadIdx.x; i < half; i += kThreads) turns[i] = turns_of(p.frequencies[i]);
+    if (threadIdx.x < 2 * LPR) {
+      const bool is_k = threadIdx.x >= LPR;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 2 * C; ++e) {
+          const int32_t at = l.channel(s, e);
+          weights[(is_k ? kRow : 0) + (s * LPR + threadIdx.x % LPR) * 2 * C + e] =
+              at < 0 ? 0.f : weight_of(is_k ? p.w_k : p.w_q, p.w_fp32, at);
+        }
+    }
+  }
+  // Cosines and sines of an item's tokens; `first` is the position that the
+  // thread's first entry needs.
+  __device__ __forceinline__ void fill(const RotateParams& p, const Item& it, int buf,
+                                       uint64_t first) {
+    float* tab = table + buf * table_size;
+    for (int32_t i = threadIdx.x; i < it.nt * half; i += kThreads) {
+      const int32_t t = i < half ? 0 : i / half, f = i - t * half;
+      const uint64_t pos = i < kThreads ? first : position_of(p, it.t0 + t);
+      const float2 u = unit_of(pos * turns[f], p.scale);
+      tab[t * 2 * half + f] = u.x;
+      tab[t * 2 * half + half + f] = u.y;
+    }
+  }
+  __device__ __forceinline__ uint64_t first_position(const RotateParams& p, const Item& it) const {
+    const int32_t i = threadIdx.x;
+    return i < it.nt * half ? position_of(p, it.t0 + (i < half ? 0 : i / half)) : 0;
+  }
 };
 
-template <int C, int S>
-__device__ __forceinline__ void load_weights(const RotateParams& p, const int32_t* a,
-                                             const int32_t* b, float (*wq)[2 * C],
-                                             float (*wk)[2 * C]) {
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int i = 0; i < 2 * C; ++i) {
-      const int32_t at = i < C ? (a[s] < 0 ? -1 : a[s] + i) : (b[s] < 0 ? -1 : b[s] + i - C);
-      wq[s][i] = at < 0 ? 0.f : weight_of(p.w_q, p.w_fp32, at);
-      wk[s][i] = at < 0 ? 0.f : weight_of(p.w_k, p.w_fp32, at);
-    }
-}
-
-__device__ __forceinline__ void fill_table(const RotateParams& p, const Rows& r, float2* tab) {
-  const int32_t half = p.rotary / 2;
-  for (int32_t i = threadIdx.x; i < r.nt * half; i += kThreads) {
-    const int32_t t = i / half;
-    tab[i] = angle(p, r.t0 + t, i - t * half);
-  }
+// Rows under way in a thread: as many as 16 registers hold (of each array), four
+// at most.
+template <typename T, int C, int S>
+constexpr int rows_ahead() {
+  constexpr int regs = C == 1 ? 2 * S : static_cast<int>(sizeof(T)) * 2 * C * S / 4;
+  constexpr int n = 16 / regs;
+  return n > 4 ? 4 : n < 1 ? 1 : n;
 }
 
 template <typename T, int C, int LPR, int S, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const RotateParams p) {
-  extern __shared__ float2 tab[];
-  constexpr int kGroups = kThreads / LPR;
-  constexpr int U = S == 1 ? 2 : 1;  // rows under way
+__global__ void __launch_bounds__(kThreads, C * S >= 8 || S >= 4 ? 2 : 4) norm_rotate_kernel(const RotateParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int G = kThreads / LPR;
+  constexpr int U = rows_ahead<T, C, S>();
+  using L = Lane<C, LPR, S, INTER>;
+  constexpr int H = L::kHalves;
   const int32_t lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-  Rows r;
-  r.t0 = blockIdx.x * p.tokens_per_block;
-  r.nt = min(p.tokens_per_block, p.tokens - r.t0);
-  r.h0 = blockIdx.y * p.heads_per_block;
-  r.nh = min(p.heads_per_block, p.q_heads + p.k_heads - r.h0);
-  const Lane<C, LPR, S, INTER> l(p, lane);
+  const L l(p, lane);
+  Shared<C, LPR, S> sh(p, smem);
+  // rows of an item: row r is token r / heads_per_item, head r % heads_per_item
+  int32_t tu[U], hu[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    tu[u] = (group + u * G) / p.heads_per_item;
+    hu[u] = group + u * G - tu[u] * p.heads_per_item;
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const int32_t rows = r.count();
-  Row<T, C, S> x[U];
-  auto row_at = [&](int32_t i, const T*& src, T*& dst, bool& is_q, int32_t& t) {
-    t = i / r.nh;
-    const int32_t h = r.h0 + i - t * r.nh;
-    const int64_t token = r.t0 + t;
-    is_q = h < p.q_heads;
-    const int64_t hh = is_q ? h : h - p.q_heads;
-    src = static_cast<const T*>(is_q ? p.q : p.k) + token * (is_q ? p.q_st : p.k_st) +
-          hh * (is_q ? p.q_sh : p.k_sh);
-    dst = static_cast<T*>(is_q ? p.out_q : p.out_k) + token * (is_q ? p.oq_st : p.ok_st) +
-          hh * (is_q ? p.oq_sh : p.ok_sh);
+  Raw<T, C> x[U][S];
+  auto here = [&](const Item& it, int u) { return tu[u] < it.nt && hu[u] < it.nh; };
+  auto load = [&](const Item& it, int u) {
+    if (!here(it, u)) return;
+    const int64_t token = it.t0 + tu[u];
+    const int32_t h = it.h0 + hu[u];
+    const T* src = h < p.q_heads
+                       ? static_cast<const T*>(p.q) + token * p.q_st + h * p.q_sh
+                       : static_cast<const T*>(p.k) + token * p.k_st + (h - p.q_heads) * p.k_sh;
+    load_row<T, C, L, S>(x[u], src, l);
   };
-  auto load = [&](int32_t base) {
+  int32_t i = blockIdx.x;
+  Item it = item_of(p, i);
+  uint64_t first = sh.first_position(p, it);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t i = base + u * kGroups;
-      if (i >= rows) continue;
-      const T* src;
-      T* dst;
-      bool is_q;
-      int32_t t;
-      row_at(i, src, dst, is_q, t);
-      x[u].load(src, l);
-    }
-  };
-  load(group);
-  float wq[S][2 * C], wk[S][2 * C];
-  load_weights<C, S>(p, l.a, l.b, wq, wk);
-  fill_table(p, r, tab);
+  for (int u = 0; u < U; ++u) load(it, u);
+  sh.fill_once(p, l);
+  __syncthreads();
+  sh.fill(p, it, 0, first);
+  Item next = it;
+  if (i + gridDim.x < p.items) {
+    next = item_of(p, i + gridDim.x);
+    first = sh.first_position(p, next);
+  }
   __syncthreads();
   const float inv_dim = 1.f / static_cast<float>(p.dim);
-  // (every lane of a warp runs the same rounds: the sums are over whole warps)
-  for (int32_t base = 0; base < rows; base += U * kGroups) {
-    if (base > 0) load(base + group);
+  for (int buf = 0; i < p.items; i += gridDim.x, buf ^= 1) {
+    const bool more = i + gridDim.x < p.items;
+    if (more) sh.fill(p, next, buf ^ 1, first);
+    Item after = next;
+    if (i + 2 * gridDim.x < p.items) {
+      after = item_of(p, i + 2 * gridDim.x);
+      first = sh.first_position(p, after);
+    }
+    const float* table = sh.table + buf * sh.table_size;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int32_t i = base + group + u * kGroups;
-      const bool here = i < rows;
-      float f[S][2 * C];
-      float sum = 0.f;
+      if (u * G >= it.nt * p.heads_per_item) break;
+      float2 f[S][H];
+      float2 sum2 = both(0.f);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        x[u].get(s, l, f[s]);
+        values<INTER>(x[u][s], s, l, f[s]);
 #pragma unroll
-        for (int j = 0; j < 2 * C; ++j) sum = fmaf(f[s][j], f[s][j], sum);
+        for (int j = 0; j < H; ++j) sum2 = fma2(f[s][j], f[s][j], sum2);
       }
-      sum = row_sum<LPR>(sum);
-      if (!here) continue;
-      const float rho = rsqrtf(fmaf(sum, inv_dim, p.eps));
-      const T* src;
-      T* dst;
-      bool is_q;
-      int32_t t;
-      row_at(i, src, dst, is_q, t);
+      const bool mine = here(it, u);
+      if (more) load(next, u);  // into the registers that were just read
+      const float sum = row_sum<LPR>(sum2.x + sum2.y);
+      if (mine) {
+        const float rho = rsqrtf(fmaf(sum, inv_dim, p.eps));
+        const int64_t token = it.t0 + tu[u];
+        const int32_t h = it.h0 + hu[u];
+        const bool is_q = h < p.q_heads;
+        T* dst = is_q ? static_cast<T*>(p.out_q) + token * p.oq_st + h * p.oq_sh
+                      : static_cast<T*>(p.out_k) + token * p.ok_st + (h - p.q_heads) * p.ok_sh;
+        const float2* w = reinterpret_cast<const float2*>(sh.weights + (is_q ? 0 : sh.kRow)) + lane * C;
+        const float* tab = table + tu[u] * 2 * sh.half;
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < S; ++s) {
 #pragma unroll
-        for (int j = 0; j < 2 * C; ++j) f[s][j] = f[s][j] * rho * (is_q ? wq[s][j] : wk[s][j]);
-        if (l.pair[s] >= 0)
-          turn<C, INTER>(f[s], tab + t * (p.rotary / 2) + l.pair[s], 1.f);
-        if (l.a[s] >= 0) Chunk<T, C>::store(dst + l.a[s], f[s]);
-        if (l.b[s] >= 0) Chunk<T, C>::store(dst + l.b[s], f[s] + C);
+          for (int j = 0; j < H; ++j)
+            f[s][j] = mul2(mul2(f[s][j], both(rho)), w[s * LPR * C + j]);
+          if (l.pair[s] >= 0) turn<false>(f[s], tab + l.pair[s], tab + sh.half + l.pair[s]);
+          store<INTER>(dst, s, l, f[s]);
+        }
       }
     }
+    it = next;
+    next = after;
+    __syncthreads();  // the next table is whole, this one may be overwritten
   }
 }
 
-// Gradient: persistent blocks, whose sums of dw end in a part of the workspace each.
+// Gradient: the sums of dw of a block end in its part of the workspace.
 template <typename T, int C, int LPR, int S, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rotate_backward_kernel(const RotateParams p) {
-  extern __shared__ float2 tab[];  // two tables; at the end [warps][2][dim] sums
-  constexpr int kGroups = kThreads / LPR;
+__global__ void __launch_bounds__(kThreads, C * S >= 8 || S >= 4 ? 1 : 2) norm_rotate_backward_kernel(const RotateParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int G = kThreads / LPR;
+  constexpr int U = rows_ahead<T, C, S>();
+  using L = Lane<C, LPR, S, INTER>;
+  constexpr int H = L::kHalves;
   const int32_t lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-  const int32_t heads = p.q_heads + p.k_heads;
-  const int32_t half = p.rotary / 2;
-  const Lane<C, LPR, S, INTER> l(p, lane);
+  const L l(p, lane);
+  Shared<C, LPR, S> sh(p, smem);
+  int32_t tu[U], hu[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    tu[u] = (group + u * G) / p.heads_per_item;
+    hu[u] = group + u * G - tu[u] * p.heads_per_item;
+  }
   pdl_wait();
   pdl_launch_dependents();
-  float wq[S][2 * C], wk[S][2 * C], gq[S][2 * C], gk[S][2 * C];
-  load_weights<C, S>(p, l.a, l.b, wq, wk);
+  Raw<T, C> x[U][S], d[U][S];
+  auto here = [&](const Item& it, int u) { return tu[u] < it.nt && hu[u] < it.nh; };
+  auto load = [&](const Item& it, int u) {
+    if (!here(it, u)) return;
+    const int64_t token = it.t0 + tu[u];
+    const int32_t h = it.h0 + hu[u];
+    const bool is_q = h < p.q_heads;
+    const int64_t hh = is_q ? h : h - p.q_heads;
+    load_row<T, C, L, S>(x[u],
+                         static_cast<const T*>(is_q ? p.q : p.k) + token * (is_q ? p.q_st : p.k_st) +
+                             hh * (is_q ? p.q_sh : p.k_sh),
+                         l);
+    load_row<T, C, L, S>(d[u],
+                         static_cast<const T*>(is_q ? p.d_q : p.d_k) +
+                             token * (is_q ? p.dq_st : p.dk_st) + hh * (is_q ? p.dq_sh : p.dk_sh),
+                         l);
+  };
+  float2 gq[S][H], gk[S][H];
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int j = 0; j < 2 * C; ++j) gq[s][j] = gk[s][j] = 0.f;
+    for (int j = 0; j < H; ++j) gq[s][j] = gk[s][j] = both(0.f);
+  int32_t i = blockIdx.x;
+  Item it = item_of(p, i);
+  uint64_t first = sh.first_position(p, it);
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(it, u);
+  sh.fill_once(p, l);
+  __syncthreads();
+  sh.fill(p, it, 0, first);
+  Item next = it;
+  if (i + gridDim.x < p.items) {
+    next = item_of(p, i + gridDim.x);
+    first = sh.first_position(p, next);
+  }
+  __syncthreads();
   const float inv_dim = 1.f / static_cast<float>(p.dim);
-  const int32_t units = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-  int32_t buf = 0;
-  for (int32_t unit = blockIdx.x; unit < units; unit += gridDim.x, buf ^= 1) {
-    Rows r;
-    r.t0 = unit * p.tokens_per_block;
-    r.nt = min(p.tokens_per_block, p.tokens - r.t0);
-    r.h0 = 0;
-    r.nh = heads;
-    float2* table = tab + buf * p.tokens_per_block * half;
-    fill_table(p, r, table);
-    __syncthreads();  // (and every thread is past the table before the last one)
-    const int32_t rows = r.count();
-    for (int32_t base = 0; base < rows; base += kGroups) {
-      const int32_t i = base + group;
-      const bool here = i < rows;
-      const int32_t t = here ? i / heads : 0;
-      const int32_t h = here ? i - t * heads : 0;
-      const int64_t token = r.t0 + t;
+  for (int buf = 0; i < p.items; i += gridDim.x, buf ^= 1) {
+    const bool more = i + gridDim.x < p.items;
+    if (more) sh.fill(p, next, buf ^ 1, first);
+    Item after = next;
+    if (i + 2 * gridDim.x < p.items) {
+      after = item_of(p, i + 2 * gridDim.x);
+      first = sh.first_position(p, after);
+    }
+    const float* table = sh.table + buf * sh.table_size;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u * G >= it.nt * p.heads_per_item) break;
+      const bool mine = here(it, u);
+      const int32_t h = it.h0 + hu[u];
       const bool is_q = h < p.q_heads;
-      const int64_t hh = is_q ? h : h - p.q_heads;
-      Row<T, C, S> x, d;
-      if (here) {
-        x.load(static_cast<const T*>(is_q ? p.q : p.k) + token * (is_q ? p.q_st : p.k_st) +
-                   hh * (is_q ? p.q_sh : p.k_sh),
-               l);
-        d.load(static_cast<const T*>(is_q ? p.d_q : p.d_k) + token * (is_q ? p.dq_st : p.dk_st) +
-                   hh * (is_q ? p.dq_sh : p.dk_sh),
-               l);
-      }
-      float f[S][2 * C], g[S][2 * C];
-      float sum = 0.f, dot = 0.f;
+      const float2* w = reinterpret_cast<const float2*>(sh.weights + (is_q ? 0 : sh.kRow)) + lane * C;
+      const float* tab = table + (mine ? tu[u] : 0) * 2 * sh.half;
+      float2 f[S][H], g[S][H];
+      float2 sum2 = both(0.f), dot2 = both(0.f);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        x.get(s, l, f[s]);
-        d.get(s, l, g[s]);
-        if (l.pair[s] >= 0) turn<C, INTER>(g[s], table + t * half + l.pair[s], -1.f);
+        values<INTER>(x[u][s], s, l, f[s]);
+        values<INTER>(d[u][s], s, l, g[s]);
+        if (l.pair[s] >= 0) turn<true>(g[s], tab + l.pair[s], tab + sh.half + l.pair[s]);
 #pragma unroll
-        for (int j = 0; j < 2 * C; ++j) {
-          sum = fmaf(f[s][j], f[s][j], sum);
-          dot = fmaf(g[s][j] * (is_q ? wq[s][j] : wk[s][j]), f[s][j], dot);
+        for (int j = 0; j < H; ++j) {
+          sum2 = fma2(f[s][j], f[s][j], sum2);
+          dot2 = fma2(mul2(g[s][j], w[s * LPR * C + j]), f[s][j], dot2);
         }
       }
-      sum = row_sum<LPR>(sum);
-      dot = row_sum<LPR>(dot);
-      if (!here) continue;
-      const float rho = rsqrtf(fmaf(sum, inv_dim, p.eps));
-      const float back = rho * rho * dot * inv_dim;
-      T* dst = static_cast<T*>(is_q ? p.out_q : p.out_k) + token * (is_q ? p.oq_st : p.ok_st) +
-               hh * (is_q ? p.oq_sh : p.ok_sh);
+      if (more) load(next, u);
+      const float sum = row_sum<LPR>(sum2.x + sum2.y), dot = row_sum<LPR>(dot2.x + dot2.y);
+      if (mine) {
+        const float rho = rsqrtf(fmaf(sum, inv_dim, p.eps));
+        const float2 back = both(-rho * rho * rho * dot * inv_dim), rho2 = both(rho);
+        const int64_t token = it.t0 + tu[u];
+        T* dst = is_q ? static_cast<T*>(p.out_q) + token * p.oq_st + h * p.oq_sh
+                      : static_cast<T*>(p.out_k) + token * p.ok_st + (h - p.q_heads) * p.ok_sh;
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < S; ++s) {
 #pragma unroll
-        for (int j = 0; j < 2 * C; ++j) {
-          const float dwj = g[s][j] * f[s][j] * rho;
-          gq[s][j] += is_q ? dwj : 0.f;
-          gk[s][j] += is_q ? 0.f : dwj;
-          g[s][j] = rho * fmaf(g[s][j], is_q ? wq[s][j] : wk[s][j], -f[s][j] * back);
+          for (int j = 0; j < H; ++j) {
+            const float2 gr = mul2(g[s][j], rho2);
+            if (is_q) gq[s][j] = fma2(gr, f[s][j], gq[s][j]);
+            else gk[s][j] = fma2(gr, f[s][j], gk[s][j]);
+            g[s][j] = fma2(f[s][j], back, mul2(gr, w[s * LPR * C + j]));
+          }
+          store<INTER>(dst, s, l, g[s]);
         }
-        if (l.a[s] >= 0) Chunk<T, C>::store(dst + l.a[s], g[s]);
-        if (l.b[s] >= 0) Chunk<T, C>::store(dst + l.b[s], g[s] + C);
       }
     }
+    it = next;
+    next = after;
+    __syncthreads();
   }
   // sums of the rows of a warp, then of the block's warps, in a fixed order
-  __syncthreads();
-  float* sums = reinterpret_cast<float*>(tab);
+  float* sums = reinterpret_cast<float*>(smem);  // [warps][2][dim]
   const int32_t warp = threadIdx.x / 32;
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int j = 0; j < 2 * C; ++j) {
-      float vq = gq[s][j], vk = gk[s][j];
+    for (int e = 0; e < 2 * C; ++e) {
+      float vq = e & 1 ? gq[s][e / 2].y : gq[s][e / 2].x;
+      float vk = e & 1 ? gk[s][e / 2].y : gk[s][e / 2].x;
 #pragma unroll
-      for (int d = LPR; d < 32; d <<= 1) {
-        vq += __shfl_xor_sync(0xffffffffu, vq, d);
-        vk += __shfl_xor_sync(0xffffffffu, vk, d);
+      for (int k = LPR; k < 32; k <<= 1) {
+        vq += __shfl_xor_sync(0xffffffffu, vq, k);
+        vk += __shfl_xor_sync(0xffffffffu, vk, k);
       }
-      const int32_t at = j < C ? l.a[s] : l.b[s];
+      const int32_t at = l.channel(s, e);
       if (at >= 0 && (threadIdx.x & 31) < LPR) {
-        sums[(warp * 2 + 0) * p.dim + at + j % C] = vq;
-        sums[(warp * 2 + 1) * p.dim + at + j % C] = vk;
+        sums[(warp * 2 + 0) * p.dim + at] = vq;
+        sums[(warp * 2 + 1) * p.dim + at] = vk;
       }
     }
   __syncthreads();
-  for (int32_t i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
+  for (int32_t c = threadIdx.x; c < 2 * p.dim; c += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sums[w * 2 * p.dim + i];
-    p.workspace[static_cast<int64_t>(blockIdx.x) * 2 * p.dim + i] = v;
+    for (int w = 0; w < kWarps; ++w) v += sums[w * 2 * p.dim + c];
+    p.workspace[static_cast<int64_t>(blockIdx.x) * 2 * p.dim + c] = v;
   }
 }
 
-// dw_q and dw_k from the blocks' parts: 32 columns a block, 8 rows of parts side
-// by side.
-__global__ void __launch_bounds__(256) norm_rotate_sums_kernel(const RotateParams p,
-                                                               int32_t parts) {
-  __shared__ float s[8][32];
+// dw_q and dw_k from the blocks' parts: 32 columns a block, 32 parts side by side.
+__global__ void __launch_bounds__(1024) norm_rotate_sums_kernel(const RotateParams p,
+                                                                int32_t parts) {
+  __shared__ float s[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int32_t x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int32_t col = blockIdx.x * 32 + x;
   float v = 0.f;
-  if (col < 2 * p.dim)
-    for (int32_t i = y; i < parts; i += 8)
+  if (col < 2 * p.dim) {
+#pragma unroll 8
+    for (int32_t i = y; i < parts; i += 32)
       v += p.workspace[static_cast<int64_t>(i) * 2 * p.dim + col];
+  }
   s[y][x] = v;
   __syncthreads();
-  if (y == 0 && col < 2 * p.dim) {
+  v = s[x][y];  // column blockIdx.x * 32 + y
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][x];
-    (col < p.dim ? p.dw_q : p.dw_k)[col < p.dim ? col : col - p.dim] = v;
-  }
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  const int32_t c = blockIdx.x * 32 + y;
+  if (x == 0 && c < 2 * p.dim) (c < p.dim ? p.dw_q : p.dw_k)[c < p.dim ? c : c - p.dim] = v;
 }
 
 struct Shape {
@@ -452,38 +591,44 @@ constexpr int32_t kBackBlocks = 4 * 152;
 
 template <typename T, int C, int LPR, int S, bool INTER>
 cudaError_t launch(RotateParams p, bool back, int num_sms, cudaStream_t stream) {
-  constexpr int kGroups = kThreads / LPR;
+  constexpr int G = kThreads / LPR;
+  constexpr int kRows = G * rows_ahead<T, C, S>();  // of an item at most
   const int32_t heads = p.q_heads + p.k_heads, half = p.rotary / 2;
-  // whole tokens a block, as many as give every group of lanes two rows
-  int32_t per = heads >= 2 * kGroups ? 1 : 2 * kGroups / heads;
-  if (per > kMaxTable / half) per = kMaxTable / half;
-  // (no more than leave every SM a block)
-  if (per > (p.tokens + num_sms - 1) / num_sms) per = (p.tokens + num_sms - 1) / num_sms;
-  p.tokens_per_block = per;
+  if (heads >= G) {
+    // one token an item; its heads in as few equal chunks as hold them, or, where
+    // that leaves SMs without an item, in chunks of one row a group
+    const int32_t most = static_cast<int64_t>(p.tokens) * ((heads + kRows - 1) / kRows) < num_sms
+                             ? G : kRows;
+    p.tokens_per_item = 1;
+    p.chunks_of_heads = (heads + most - 1) / most;
+    p.heads_per_item = (heads + p.chunks_of_heads - 1) / p.chunks_of_heads;
+  } else {
+    // several tokens an item, but no fewer items than SMs
+    int32_t per = kRows / heads;
+    if (per > kMaxTable / half) per = kMaxTable / half;
+    if (per > (p.tokens + num_sms - 1) / num_sms) per = (p.tokens + num_sms - 1) / num_sms;
+    p.tokens_per_item = per;
+    p.chunks_of_heads = 1;
+    p.heads_per_item = heads;
+  }
+  p.items = (p.tokens + p.tokens_per_item - 1) / p.tokens_per_item * p.chunks_of_heads;
+  const int32_t blocks = p.items < kBackBlocks ? p.items : kBackBlocks;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = pdl_attribute();
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (!back) {
-    // few tokens: their heads over several blocks
-    p.heads_per_block = p.tokens < num_sms && heads > kGroups ? kGroups : heads;
-    cfg.gridDim = dim3((p.tokens + per - 1) / per,
-                       (heads + p.heads_per_block - 1) / p.heads_per_block);
-    cfg.dynamicSmemBytes = sizeof(float2) * per * half;
-    return cudaLaunchKernelEx(&cfg, norm_rotate_kernel<T, C, LPR, S, INTER>, p);
-  }
-  const int32_t units = (p.tokens + per - 1) / per;
-  const int32_t blocks = units < kBackBlocks ? units : kBackBlocks;
-  const size_t tables = sizeof(float2) * 2 * per * half;
+  cfg.dynamicSmemBytes = Shared<C, LPR, S>::bytes(p);
+  if (!back) return cudaLaunchKernelEx(&cfg, norm_rotate_kernel<T, C, LPR, S, INTER>, p);
   const size_t sums = sizeof(float) * kWarps * 2 * p.dim;
-  cfg.gridDim = dim3(blocks);
-  cfg.dynamicSmemBytes = tables > sums ? tables : sums;
-  cudaError_t err =
+  if (cfg.dynamicSmemBytes < sums) cfg.dynamicSmemBytes = sums;
+  const cudaError_t err =
       cudaLaunchKernelEx(&cfg, norm_rotate_backward_kernel<T, C, LPR, S, INTER>, p);
   if (err != cudaSuccess) return err;
   cfg.gridDim = dim3((2 * p.dim + 31) / 32);
+  cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, norm_rotate_sums_kernel, p, blocks);
 }
@@ -515,9 +660,9 @@ cudaError_t by_type(const RotateParams& p, bool back, int num_sms, cudaStream_t 
 
 }  // namespace
 
-// (a block has at least one token)
+// (a block has at least one item: a token, or a chunk of one token's heads)
 size_t norm_rotate_backward_workspace(int64_t tokens, int64_t dim) {
-  const int64_t blocks = tokens < kBackBlocks ? tokens : kBackBlocks;
+  const int64_t blocks = tokens > 0 ? kBackBlocks : 0;
   return static_cast<size_t>(blocks * 2 * dim * sizeof(float));
 }
 

@@ -495,7 +495,9 @@ mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32
  * Pointers and strides need the alignment of one element only (chunks of four
  *    channels -- dim and rotary multiples of 8, rows on four elements -- are the
  *    fast case);
- * 2 <= rotary <= dim <= 512, rotary even, eps >= 0; tokens == 0 does nothing. */
+ * 2 <= rotary <= dim <= 512, rotary even, strides below 2^29, fewer than 2^31
+ *    heads in all (more is MX_ERR_UNSUPPORTED), eps >= 0; tokens == 0 does
+ *    nothing. */
 mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
                          int64_t rotary,
                          const void* q, int64_t q_st, int64_t q_sh,

@@ -1,7 +1,9 @@
 // kernels.h -- launch interface between the C-ABI layer (mx_api.cu) and the
 // CUDA kernels (quantize.cu and quantize_f32.cu, which instantiate
 // quantize_kernel.cuh; gemm_pair.cu; norm.cu, norm_mixed.cu and norm_f32.cu,
-// which instantiate norm_kernel.cuh; moe_few.cu; rotate.cu; route.cu; vocab_loss.cu; status.cu).  Not part of the public
+// which instantiate norm_kernel.cuh; moe_few.cu; rotate.cu,
+// rotate_f32.cu, rotate_back.cu and rotate_back_f32.cu, which instantiate
+// rotate_kernel.cuh; route.cu; vocab_loss.cu; status.cu).  Not part of the public
 // ABI.
 #pragma once
 
@@ -227,6 +229,10 @@ struct RotateParams {
 size_t norm_rotate_backward_workspace(int64_t tokens, int64_t dim);
 cudaError_t launch_norm_rotate(const RotateParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_rotate_backward(const RotateParams& p, int num_sms, cudaStream_t stream);
+// (FP32 heads; called by the two above)
+cudaError_t launch_norm_rotate_f32(const RotateParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_rotate_backward_f32(const RotateParams& p, int num_sms,
+                                            cudaStream_t stream);
 
 // ------------------------------------------------------------------ routing
 

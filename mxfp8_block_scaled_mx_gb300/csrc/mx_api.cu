@@ -812,6 +812,13 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t st, int64_t 
          (st >= dim && sh >= (tokens - 1) * st + dim);
 }
 
+// (in bytes they stay below 2^31)
+bool strides_fit(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if (s >= (1 << 29)) return false;
+  return true;
+}
+
 bool chunk_aligned(const void* p, int64_t st, int64_t sh, mx_dtype d) {
   const uintptr_t bytes = d == MX_FP32 ? 16 : 8;
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && st % 4 == 0 && sh % 4 == 0;
@@ -852,6 +859,8 @@ mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64
       !rows_apart(tokens, q_heads, dim, oq_st, oq_sh) ||
       !rows_apart(tokens, k_heads, dim, ok_st, ok_sh))
     return MX_ERR_INVALID_ARG;
+  if (!strides_fit({q_st, q_sh, k_st, k_sh, oq_st, oq_sh, ok_st, ok_sh}))
+    return MX_ERR_UNSUPPORTED;
   if (!aligned_elt(q, x_dtype) || !aligned_elt(k, x_dtype) || !aligned_elt(w_q, w_dtype) ||
       !aligned_elt(w_k, w_dtype) || !aligned_elt(out_q, x_dtype) || !aligned_elt(out_k, x_dtype) ||
       (reinterpret_cast<uintptr_t>(frequencies) & 7u) != 0 ||
@@ -919,6 +928,8 @@ mx_status mx_norm_rotate_backward(int64_t tokens, int64_t q_heads, int64_t k_hea
   if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 || dq_st < 0 || dq_sh < 0 || dk_st < 0 ||
       dk_sh < 0)
     return MX_ERR_INVALID_ARG;
+  if (!strides_fit({q_st, q_sh, k_st, k_sh, dq_st, dq_sh, dk_st, dk_sh}))
+    return MX_ERR_UNSUPPORTED;
   const size_t need = mx::norm_rotate_backward_workspace(tokens, dim);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
   if (!aligned_elt(d_q, x_dtype) || !aligned_elt(d_k, x_dtype) || !aligned_elt(q, x_dtype) ||

@@ -1,0 +1,11 @@
+// rotate_back_f32.cu -- their gradient of FP32 heads (rotate_kernel.cuh).
+#include "rotate_kernel.cuh"
+
+namespace mx {
+
+cudaError_t launch_norm_rotate_backward_f32(const RotateParams& p, int num_sms,
+                                            cudaStream_t stream) {
+  return by_layout<float, true>(p, num_sms, stream);
+}
+
+}  // namespace mx

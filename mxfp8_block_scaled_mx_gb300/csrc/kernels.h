@@ -250,7 +250,7 @@ struct RouteParams {
   int32_t* order;            // [tokens * top_k]
   float* balance;            // [1]
   int32_t* workspace;
-  int32_t blocks, tokens_per_block;  // set by the launch
+  int32_t blocks, tokens_per_block, vec_ids;  // set by the launch
   // gradient
   const float* d_weights;    // [tokens, top_k] or nullptr
   const float* d_balance;    // [1] or nullptr

@@ -39,6 +39,13 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxBlocks = 304;
 constexpr int kOneBlock = 64;
+// Tokens from which on, and experts and winners up to which, a token is a lane's.
+#ifndef TMIN
+#define TMIN 16384
+#endif
+constexpr int kTileTokens = TMIN;
+constexpr int kTileExperts = 128;
+constexpr int kTileTopK = 8;
 
 // Unsigned keys in the order of the logits: NaN below everything, 0 taken.
 __device__ __forceinline__ uint32_t key_of(float z) {
@@ -57,11 +64,18 @@ __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); 
 template <typename T, int V>
 __device__ __forceinline__ void load_logits(const T* row, int32_t c, int32_t n, bool vec,
                                             float (&z)[V]) {
-  if (vec) {
+  if (V > 1 && vec) {
 #pragma unroll
     for (int v = 0; v < V; v += 4) {
       if (c + v >= n) continue;
-      if constexpr (sizeof(T) == 4) {
+      if constexpr (V == 2 && sizeof(T) == 4) {
+        const float2 q = *reinterpret_cast<const float2*>(row + c);
+        z[0] = q.x, z[1] = q.y;
+      } else if constexpr (V == 2) {
+        const uint32_t q = *reinterpret_cast<const uint32_t*>(row + c);
+        z[0] = __uint_as_float(q << 16), z[1] = __uint_as_float(q & 0xFFFF0000u);
+      } else if constexpr (V < 2) {
+      } else if constexpr (sizeof(T) == 4) {
         const float4 q = *reinterpret_cast<const float4*>(row + c + v);
         z[v] = q.x, z[v + 1] = q.y, z[v + 2] = q.z, z[v + 3] = q.w;
       } else {
@@ -82,12 +96,6 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
-}
-
-// The lanes of this thread's group, as a mask of the warp.
-template <int L>
-__device__ __forceinline__ uint32_t group_mask() {
-  return (L == 32 ? 0xffffffffu : (1u << (L % 32)) - 1u) << (lane_id() / L * L);
 }
 
 // Counts of a block in the workspace, rows of whole 16 bytes: pairs, pairs that
@@ -114,7 +122,7 @@ struct RouteShared {
   int32_t tokens;
   float sums[kWarps];
   union {
-    int2 win[kWarps][4][kMaxTopK];         // winners of the tokens under way: expert, key
+    int2 win[kWarps][kMaxTopK];            // winners of the tokens under way: expert, key
     float p[kWarps][kMaxExperts];
     int32_t next[kWarps][kMaxExperts];     // a warp's next place for each expert
     int4 part[2][kThreads];                // a thread's sums over blocks
@@ -152,14 +160,21 @@ __device__ __forceinline__ void scan_experts(RouteShared& s, int32_t experts, co
 // Places of the pairs of tokens [t0, t1): s.base holds each expert's first.
 __device__ __forceinline__ void place_pairs(const RouteParams& r, RouteShared& s, int32_t t0,
                                             int32_t t1) {
+  constexpr int kKept = 4;  // runs of 32 pairs whose experts stay in registers
   const int32_t warp = warp_id(), lane = lane_id();
   const int32_t lo = t0 * r.top_k, n = (t1 - t0) * r.top_k;
   const int32_t per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
   const int32_t a = lo + min(n, warp * per), b = lo + min(n, (warp + 1) * per);
   int32_t* next = s.next[warp];
+  int32_t kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) kept[i] = a + i * 32 + lane < b ? r.ids[a + i * 32 + lane] : -1;
   for (int32_t e = lane; e < r.experts; e += 32) next[e] = 0;
   __syncwarp();
-  for (int32_t i = a + lane; i < b; i += 32) atomicAdd(&next[r.ids[i]], 1);
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (kept[i] >= 0) atomicAdd(&next[kept[i]], 1);
+  for (int32_t i = a + kKept * 32 + lane; i < b; i += 32) atomicAdd(&next[r.ids[i]], 1);
   __syncthreads();
   for (int32_t e = threadIdx.x; e < r.experts; e += kThreads) {
     int32_t at = s.base[e];
@@ -171,20 +186,21 @@ __device__ __forceinline__ void place_pairs(const RouteParams& r, RouteShared& s
     }
   }
   __syncthreads();
-  for (int32_t i = a; i < b; i += 32) {
-    const bool here = i + lane < b;
-    const int32_t e = here ? r.ids[i + lane] : -1;
+  auto place = [&](int32_t i, int32_t e) {  // the pairs i + lane, of experts e (-1: none)
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     const int32_t rank = __popc(same & ((1u << lane) - 1u));
-    int32_t at = 0;
-    if (here) at = next[e] + rank;
+    const int32_t at = e >= 0 ? next[e] + rank : 0;
     __syncwarp();
-    if (here) {
+    if (e >= 0) {
       r.order[at] = i + lane;
       if (rank == 0) next[e] = at + __popc(same);
     }
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (a + i * 32 < b) place(a + i * 32, kept[i]);
+  for (int32_t i = a + kKept * 32; i < b; i += 32) place(i, i + lane < b ? r.ids[i + lane] : -1);
 }
 
 // The balance loss from each thread's share of sum counts_e sum p_te.
@@ -202,13 +218,11 @@ __device__ __forceinline__ void write_balance(const RouteParams& r, RouteShared&
   }
 }
 
-template <typename T, int L, int V, bool ONE>
+template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
-  constexpr int kGroups = 32 / L;  // tokens of a warp at a time
   __shared__ RouteShared s;
   const int32_t warp = warp_id();
-  const int32_t lane = lane_id() % L, group = lane_id() / L;
-  const uint32_t mask = group_mask<L>();
+  const int32_t lane = lane_id();
   for (int32_t e = threadIdx.x; e < r.experts; e += kThreads) s.pairs[e] = s.counted[e] = 0;
   if (threadIdx.x == 0) s.tokens = 0;
   __syncthreads();
@@ -220,16 +234,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
   float acc[V], z[V], ahead[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = z[v] = ahead[v] = 0.f;
-  int2* win = s.win[warp][group];
+  int2* win = s.win[warp];
   const T* logits = static_cast<const T*>(r.logits);
-  int32_t base = t0 + warp * kGroups;
-  if (base + group < t1) load_logits<T, V>(logits + (base + group) * r.ld, c0, r.experts, r.vec, z);
-  for (; base < t1; base += kWarps * kGroups) {
-    const int32_t t = base + group;
-    const bool here = t < t1;
-    const bool valid = here && (!r.mask || r.mask[t] != 0);
-    if (t + kWarps * kGroups < t1)
-      load_logits<T, V>(logits + (t + kWarps * kGroups) * r.ld, c0, r.experts, r.vec, ahead);
+  int32_t t = t0 + warp;
+  if (t < t1) load_logits<T, V>(logits + t * r.ld, c0, r.experts, r.vec, z);
+  for (; t < t1; t += kWarps) {
+    const bool valid = !r.mask || r.mask[t] != 0;
+    if (t + kWarps < t1)
+      load_logits<T, V>(logits + (t + kWarps) * r.ld, c0, r.experts, r.vec, ahead);
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = c0 + v < r.experts ? key_of(z[v]) : 0u;
@@ -238,10 +250,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
       uint32_t best = key[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) best = max(best, key[v]);
-      const uint32_t most = __reduce_max_sync(mask, best);
-      const uint32_t who = __ballot_sync(0xffffffffu, best == most) & mask;
+      const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+      const uint32_t who = __ballot_sync(0xffffffffu, best == most);
       if (j == 0) top = logit_of(most);
-      if (static_cast<int32_t>(lane_id()) == __ffs(who) - 1) {
+      if (lane == __ffs(who) - 1) {
         int32_t at = 0;
         bool found = false;
 #pragma unroll
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
       z[v] = c0 + v < r.experts ? expf(z[v] - top) : 0.f;
       sum += z[v];
     }
-    sum = group_sum<L>(sum);
+    sum = group_sum<32>(sum);
     const float inv = 1.f / sum;
     if (valid) {
 #pragma unroll
@@ -266,40 +278,32 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
     __syncwarp();
     // the winners side by side
     float picked = 0.f;
-    for (int32_t j = lane; j < r.top_k; j += L) {
+    for (int32_t j = lane; j < r.top_k; j += 32) {
       const int2 w = win[j];
       const float e = expf(logit_of(static_cast<uint32_t>(w.y)) - top);
       picked += e;
-      if (here) {
-        r.ids[t * r.top_k + j] = w.x;
-        atomicAdd(&s.pairs[w.x], 1);
-        if (valid) atomicAdd(&s.counted[w.x], 1);
-        if (!r.renormalize) r.weights[t * r.top_k + j] = e * inv;
-        win[j].y = __float_as_int(e);
-      }
+      r.ids[t * r.top_k + j] = w.x;
+      atomicAdd(&s.pairs[w.x], 1);
+      if (valid) atomicAdd(&s.counted[w.x], 1);
+      if (!r.renormalize) r.weights[t * r.top_k + j] = e * inv;
+      win[j].y = __float_as_int(e);
     }
     if (r.renormalize) {
       // p / sum of p, so that a softmax that is NaN stays so
-      picked = group_sum<L>(picked);
+      picked = group_sum<32>(picked);
       const float scale = inv / (picked * inv);
-      if (here)
-        for (int32_t j = lane; j < r.top_k; j += L)
-          r.weights[t * r.top_k + j] = __int_as_float(win[j].y) * scale;
+      for (int32_t j = lane; j < r.top_k; j += 32)
+        r.weights[t * r.top_k + j] = __int_as_float(win[j].y) * scale;
     }
-    if (here && lane == 0) r.lse[t] = top + logf(sum);
+    if (lane == 0) r.lse[t] = top + logf(sum);
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) z[v] = ahead[v];
   }
-  // sums of p: groups of a warp, then warps
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float a = acc[v];
-#pragma unroll
-    for (int d = L; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-    if (group == 0 && c0 + v < r.experts) s.p[warp][c0 + v] = a;
-  }
+  for (int v = 0; v < V; ++v)
+    if (c0 + v < r.experts) s.p[warp][c0 + v] = acc[v];
   __syncthreads();
   const Parts parts(r);
   float share = 0.f;
@@ -329,6 +333,148 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
   }
 }
 
+// The first kernel for many tokens: a warp takes 32 of them at a time, a token a
+// lane.  The logits' keys come to shared memory in rows of an odd length; every
+// lane goes along its row with its K largest so far in registers, then along it
+// again with the exponentials, which it leaves there; the sums of p go down the
+// columns, an expert a lane.
+template <typename T, int K>
+__global__ void __launch_bounds__(256) route_tile_kernel(const RouteParams r) {
+  extern __shared__ uint32_t tiles[];
+  __shared__ int32_t pairs[kTileExperts], counted[kTileExperts], tokens;
+  __shared__ float factor[8][32];
+  const int32_t warp = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
+  const int32_t stride = r.experts | 1;
+  uint32_t* tile = tiles + warp * 32 * stride;
+  for (int32_t e = threadIdx.x; e < r.experts; e += blockDim.x) pairs[e] = counted[e] = 0;
+  if (threadIdx.x == 0) tokens = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int32_t end = min(r.tokens, (static_cast<int32_t>(blockIdx.x) + 1) * r.tokens_per_block);
+  float acc[kTileExperts / 32];
+#pragma unroll
+  for (int i = 0; i < kTileExperts / 32; ++i) acc[i] = 0.f;
+  const T* logits = static_cast<const T*>(r.logits);
+  // lanes of a row's four-logit runs, a power of two
+  const int32_t shift = r.experts <= 32 ? 3 : r.experts <= 64 ? 4 : 5;
+  for (int32_t t0 = blockIdx.x * r.tokens_per_block + warp * 32; t0 < end; t0 += warps * 32) {
+    const int32_t rows = min(32, end - t0);
+    if (r.vec) {
+      const int32_t c = (lane & ((1 << shift) - 1)) * 4, step = 32 >> shift;
+      if (c < r.experts) {
+#pragma unroll 4
+        for (int32_t row = lane >> shift; row < rows; row += step) {
+          float z[4];
+          load_logits<T, 4>(logits + (t0 + row) * r.ld, c, r.experts, true, z);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) tile[row * stride + c + v] = key_of(z[v]);
+        }
+      }
+    } else {
+      for (int32_t row = 0; row < rows; ++row)
+        for (int32_t c = lane; c < r.experts; c += 32)
+          tile[row * stride + c] = key_of(to_float(logits[(t0 + row) * r.ld + c]));
+    }
+    __syncwarp();
+    const bool here = lane < rows;
+    const int32_t t = t0 + lane;
+    uint32_t* mine = tile + lane * stride;
+    bool valid = false;
+    if (here) {
+      valid = !r.mask || r.mask[t] != 0;
+      uint32_t key[K];
+      int32_t id[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) key[j] = 0u, id[j] = 0;
+#pragma unroll 4
+      for (int32_t e = 0; e < r.experts; ++e) {
+        const uint32_t v = mine[e];
+        bool over[K];  // the new key goes before place j (after equal ones)
+#pragma unroll
+        for (int j = 0; j < K; ++j) over[j] = v > key[j];
+#pragma unroll
+        for (int j = K - 1; j > 0; --j) {
+          key[j] = over[j - 1] ? key[j - 1] : over[j] ? v : key[j];
+          id[j] = over[j - 1] ? id[j - 1] : over[j] ? e : id[j];
+        }
+        key[0] = over[0] ? v : key[0];
+        id[0] = over[0] ? e : id[0];
+      }
+      const float top = logit_of(key[0]);
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int32_t e = 0; e < r.experts; ++e) {
+        const float p = expf(logit_of(mine[e]) - top);
+        mine[e] = __float_as_uint(p);
+        s4[e & 3] += p;
+      }
+      const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]), inv = 1.f / sum;
+      r.lse[t] = top + logf(sum);
+      float w[K], picked = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        w[j] = 0.f;
+        if (j < r.top_k) {
+          w[j] = __uint_as_float(mine[id[j]]);
+          picked += w[j];
+          atomicAdd(&pairs[id[j]], 1);
+          if (valid) atomicAdd(&counted[id[j]], 1);
+        }
+      }
+      // p / sum of p, so that a softmax that is NaN stays so
+      const float scale = r.renormalize ? inv / (picked * inv) : inv;
+      const int64_t at = static_cast<int64_t>(t) * r.top_k;
+      if (K == 8 && r.top_k == 8 && r.vec_ids) {
+        int4* ids = reinterpret_cast<int4*>(r.ids + at);
+        float4* ws = reinterpret_cast<float4*>(r.weights + at);
+        ids[0] = make_int4(id[0], id[1], id[2], id[3]);
+        ids[1] = make_int4(id[4 % K], id[5 % K], id[6 % K], id[7 % K]);
+        ws[0] = make_float4(w[0] * scale, w[1] * scale, w[2] * scale, w[3] * scale);
+        ws[1] = make_float4(w[4 % K] * scale, w[5 % K] * scale, w[6 % K] * scale, w[7 % K] * scale);
+      } else {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (j < r.top_k) {
+            r.ids[at + j] = id[j];
+            r.weights[at + j] = w[j] * scale;
+          }
+      }
+      factor[warp][lane] = inv;
+    }
+    const uint32_t count = __ballot_sync(0xffffffffu, valid);
+    if (lane == 0) atomicAdd(&tokens, __popc(count));
+    __syncwarp();
+    for (uint32_t left = count; left; left &= left - 1) {
+      const int32_t row = __ffs(left) - 1;
+      const float f = factor[warp][row];
+#pragma unroll
+      for (int i = 0; i < kTileExperts / 32; ++i)
+        if (i * 32 + lane < r.experts)
+          acc[i] = fmaf(__uint_as_float(tile[row * stride + i * 32 + lane]), f, acc[i]);
+    }
+    __syncwarp();
+  }
+  // sums of p, warp by warp
+  float* sums = reinterpret_cast<float*>(tile);
+#pragma unroll
+  for (int i = 0; i < kTileExperts / 32; ++i)
+    if (i * 32 + lane < r.experts) sums[i * 32 + lane] = acc[i];
+  __syncthreads();
+  const Parts parts(r);
+  for (int32_t e = threadIdx.x; e < parts.row; e += blockDim.x) {
+    float a = 0.f;
+    if (e < r.experts)
+      for (int32_t w = 0; w < warps; ++w)
+        a += __uint_as_float(tiles[w * 32 * stride + e]);
+    const int32_t at = blockIdx.x * parts.row + e;
+    parts.pairs[at] = e < r.experts ? pairs[e] : 0;
+    parts.counted[at] = e < r.experts ? counted[e] : 0;
+    parts.p[at] = a;
+  }
+  if (threadIdx.x == 0) parts.tokens[blockIdx.x] = tokens;
+}
+
 __device__ __forceinline__ void add4(int4& a, const int4& b) {
   a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
 }
@@ -346,26 +492,23 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteParams
   // are for each
   const int32_t quads = parts.row / 4, slices = kThreads / quads;
   const int32_t quad = threadIdx.x % quads, slice = threadIdx.x / quads;
-  int4 all = make_int4(0, 0, 0, 0), before = all;
+  for (int32_t e = threadIdx.x; e < parts.row; e += kThreads) s.pairs[e] = s.base[e] = 0;
+  __syncthreads();
   if (slice < slices) {
-#pragma unroll 4
+    int4 all = make_int4(0, 0, 0, 0), before = all;
+#pragma unroll 5
     for (int32_t b = slice; b < r.blocks; b += slices) {
       const int4 c = *reinterpret_cast<const int4*>(parts.pairs + b * parts.row + quad * 4);
       add4(all, c);
       if (b < block) add4(before, c);
     }
-    s.part[0][slice * quads + quad] = all;
-    s.part[1][slice * quads + quad] = before;
-  }
-  __syncthreads();
-  for (int32_t e = threadIdx.x; e < r.experts; e += kThreads) {
-    int32_t a = 0, b = 0;
-    for (int32_t i = 0; i < slices; ++i) {
-      a += reinterpret_cast<const int32_t*>(s.part[0])[i * parts.row + e];
-      b += reinterpret_cast<const int32_t*>(s.part[1])[i * parts.row + e];
+    const int32_t sums[4] = {all.x, all.y, all.z, all.w};
+    const int32_t bases[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      atomicAdd(&s.pairs[quad * 4 + i], sums[i]);
+      if (!last) atomicAdd(&s.base[quad * 4 + i], bases[i]);
     }
-    s.pairs[e] = a;
-    s.base[e] = last ? 0 : b;
   }
   __syncthreads();
   scan_experts(s, r.experts, s.pairs, last ? r.offsets : nullptr);
@@ -525,22 +668,42 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const Rout
 
 template <typename F>
 cudaError_t launch_pdl(F* kern, int blocks, int threads, const RouteParams& r,
-                       cudaStream_t stream) {
+                       cudaStream_t stream, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, r);
 }
 
-template <typename T, int L, int V>
+bool tiled(int64_t tokens, int32_t experts, int32_t top_k) {
+  return tokens >= kTileTokens && experts <= kTileExperts && top_k <= kTileTopK;
+}
+
+template <typename T, int K>
+cudaError_t tile_forward(const RouteParams& r, cudaStream_t stream) {
+  auto kern = route_tile_kernel<T, K>;
+  static PerDeviceOnce setup;
+  const cudaError_t err = setup.run([&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                8 * 32 * (kTileExperts + 1) * 4);
+  });
+  if (err != cudaSuccess) return err;
+  const int32_t warps = r.tokens_per_block < 256 ? (r.tokens_per_block + 31) / 32 : 8;
+  return launch_pdl(kern, r.blocks, warps * 32, r, stream, warps * 32 * (r.experts | 1) * 4);
+}
+
+template <typename T, int V>
 cudaError_t forward(const RouteParams& r, cudaStream_t stream) {
-  if (r.blocks == 1) return launch_pdl(route_kernel<T, L, V, true>, 1, kThreads, r, stream);
+  if (r.blocks == 1) return launch_pdl(route_kernel<T, V, true>, 1, kThreads, r, stream);
   const cudaError_t err =
-      launch_pdl(route_kernel<T, L, V, false>, r.blocks, kThreads, r, stream);
+      !tiled(r.tokens, r.experts, r.top_k)
+          ? launch_pdl(route_kernel<T, V, false>, r.blocks, kThreads, r, stream)
+          : r.top_k <= 4 ? tile_forward<T, 4>(r, stream) : tile_forward<T, 8>(r, stream);
   return err != cudaSuccess ? err
                             : launch_pdl(route_order_kernel, r.blocks + 1, kThreads, r, stream);
 }
@@ -554,18 +717,19 @@ cudaError_t backward(const RouteParams& r, int num_sms, cudaStream_t stream) {
                     stream);
 }
 
-// Lanes of a token: four logits each where that is at most a warp.
+// Logits of a lane: a token has a warp forward, and in the gradient as many lanes
+// as give each four.
 template <typename T>
 cudaError_t by_experts(const RouteParams& r, bool back, int num_sms, cudaStream_t stream) {
   if (r.experts <= 32)
-    return back ? backward<T, 8, 4>(r, num_sms, stream) : forward<T, 8, 4>(r, stream);
+    return back ? backward<T, 8, 4>(r, num_sms, stream) : forward<T, 1>(r, stream);
   if (r.experts <= 64)
-    return back ? backward<T, 16, 4>(r, num_sms, stream) : forward<T, 16, 4>(r, stream);
+    return back ? backward<T, 16, 4>(r, num_sms, stream) : forward<T, 2>(r, stream);
   if (r.experts <= 128)
-    return back ? backward<T, 32, 4>(r, num_sms, stream) : forward<T, 32, 4>(r, stream);
+    return back ? backward<T, 32, 4>(r, num_sms, stream) : forward<T, 4>(r, stream);
   if (r.experts <= 256)
-    return back ? backward<T, 32, 8>(r, num_sms, stream) : forward<T, 32, 8>(r, stream);
-  return back ? backward<T, 32, 16>(r, num_sms, stream) : forward<T, 32, 16>(r, stream);
+    return back ? backward<T, 32, 8>(r, num_sms, stream) : forward<T, 8>(r, stream);
+  return back ? backward<T, 32, 16>(r, num_sms, stream) : forward<T, 16>(r, stream);
 }
 
 // Blocks of the two kernels: one up to kOneBlock tokens, then of 32 tokens at
@@ -578,7 +742,7 @@ void split(int64_t tokens, int32_t* blocks, int32_t* per) {
   }
   int64_t b = (tokens + 31) / 32;
   if (b > kMaxBlocks) b = kMaxBlocks;
-  *per = static_cast<int32_t>((tokens + b - 1) / b);
+  *per = static_cast<int32_t>((tokens + b - 1) / b + 31) / 32 * 32;
   *blocks = static_cast<int32_t>((tokens + *per - 1) / *per);
 }
 
@@ -593,6 +757,7 @@ size_t route_workspace(int64_t tokens, int32_t experts) {
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
   RouteParams r = p;
+  r.vec_ids = ((reinterpret_cast<uintptr_t>(r.ids) | reinterpret_cast<uintptr_t>(r.weights)) & 15u) == 0;
   split(r.tokens, &r.blocks, &r.tokens_per_block);
   return r.logits_fp32 ? by_experts<float>(r, false, 0, stream)
                        : by_experts<bf16>(r, false, 0, stream);

@@ -56,10 +56,10 @@ def softmax(z):
 def route(z, top_k, renormalize, mask):
     """What mx.route returns, as a dict (and p)."""
     tokens, experts = z.shape
-    keys = np.where(np.isnan(z), -np.inf, z)
-    # NaN below -infinity, equal ones by index
-    ids = np.stack([sorted(range(experts), key=lambda e: (np.isnan(z[t, e]), -keys[t, e], e))[:top_k]
-                    for t in range(tokens)]) if tokens else np.zeros((0, top_k), dtype=int)
+    # equal ones by index, NaN below -infinity
+    ids = np.argsort(-z, axis=1, kind="stable")[:, :top_k]
+    for t in np.nonzero(np.isnan(z).any(1))[0]:
+        ids[t] = sorted(range(experts), key=lambda e: (np.isnan(z[t, e]), 0.0 if np.isnan(z[t, e]) else -z[t, e], e))[:top_k]
     p = softmax(z) if tokens else z
     w = np.take_along_axis(p, ids, 1)
     if renormalize:

@@ -101,13 +101,14 @@ def test_gradients_one_by_one(mx, use, renormalize):
 @pytest.mark.parametrize("experts", [24, 64, 130])
 def test_ties(mx, experts):
     """Equal logits, among them +0 and -0: the lowest index first."""
-    for z in (torch.zeros(200, experts), torch.randint(-2, 3, (200, experts)).float(),
-              torch.where(torch.rand(200, experts) < 0.5, 0.0, -0.0)):
-        for dtype in (BF16, FP32):
-            check(mx, z.to(dtype).cuda(), 8)
+    for tokens in (200, 16389):
+        for z in (torch.zeros(tokens, experts), torch.randint(-2, 3, (tokens, experts)).float(),
+                  torch.where(torch.rand(tokens, experts) < 0.5, 0.0, -0.0)):
+            for dtype in (BF16, FP32):
+                check(mx, z.to(dtype).cuda(), 8)
 
 
-@pytest.mark.parametrize("tokens", [3, 200])
+@pytest.mark.parametrize("tokens", [3, 200, 16500])
 @pytest.mark.parametrize("experts", [8, 48, 300])
 def test_special_logits(mx, tokens, experts):
     z = logits(tokens, experts, FP32)
@@ -136,9 +137,10 @@ def test_special_logits(mx, tokens, experts):
 
 def test_strided_logits(mx):
     for dtype in (BF16, FP32):
-        wide = logits(300, 80, dtype)
-        for z in (wide[:, :64], wide[:, 1:62], wide[::2, 4:36]):
-            check_backward(mx, z, 4)
+        for tokens in (300, 33000):
+            wide = logits(tokens, 80, dtype)
+            for z in (wide[:, :64], wide[:, 1:62], wide[::2, 4:36]):
+                check_backward(mx, z, 4)
 
 
 def test_without_tokens(mx):
@@ -149,13 +151,14 @@ def test_without_tokens(mx):
 
 
 def test_same_bits_again_and_a_workspace(mx):
-    z = logits(20000, 64, FP32)
-    a = mx.route(z, 8)
-    ws = torch.full((mx.mx_route_workspace(20000, 64),), 255, dtype=torch.uint8, device="cuda")
-    b = mx.route(z, 8, workspace=ws)
-    assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
-    with pytest.raises(ValueError):
-        mx.route(z, 8, workspace=ws[:-1])
+    for tokens in (3000, 20000):
+        z = logits(tokens, 64, FP32)
+        a = mx.route(z, 8)
+        ws = torch.full((mx.mx_route_workspace(tokens, 64),), 255, dtype=torch.uint8, device="cuda")
+        b = mx.route(z, 8, workspace=ws)
+        assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
+        with pytest.raises(ValueError):
+            mx.route(z, 8, workspace=ws[:-1])
 
 
 def test_refusals(mx):

@@ -206,6 +206,27 @@ class Memory {
   c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
+// Small outputs out of one allocation, 16 bytes apart at least: an allocation each
+// takes longer than the kernels of a call for a single token.
+class Together {
+ public:
+  Together(const Memory& memory, int64_t tensors, int64_t bytes, const at::Tensor& like)
+      : block_(memory.output({bytes + 16 * tensors}, like.options().dtype(at::kByte))) {}
+  at::Tensor take(at::IntArrayRef shape, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(block_.storage()), block_.key_set(), c10::scalarTypeToTypeMeta(type));
+    const int64_t size = static_cast<int64_t>(c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(at_ / size);
+    at_ = (at_ + t.numel() * size + 15) / 16 * 16;
+    return t;
+  }
+
+ private:
+  at::Tensor block_;
+  int64_t at_ = 0;
+};
+
 // A tensor of the caller's was written: what autograd saved of it is not valid
 // any more.
 void written(const at::Tensor& t) {
@@ -499,10 +520,10 @@ PyObject* norm_rotate_backward(const Call& c) {
   const at::Tensor& d_k = c.heads_of(1, "d_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &dk_st, &dk_sh);
   const Memory memory(c, 12);
   const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim), h.q);
-  const at::TensorOptions f32 = h.q.options().dtype(at::kFloat);
   const at::Tensor dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
   const at::Tensor dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.k.options());
-  const at::Tensor dw_q = memory.output({h.dim}, f32), dw_k = memory.output({h.dim}, f32);
+  Together sums(memory, 2, 8 * h.dim, h.q);
+  const at::Tensor dw_q = sums.take({h.dim}, at::kFloat), dw_k = sums.take({h.dim}, at::kFloat);
   // a tensor without tokens has no address; the workspace's stands in, unused
   void* none = ws.data_ptr();
   const bool empty = h.tokens == 0;
@@ -545,16 +566,17 @@ PyObject* route(const Call& c) {
   const uint8_t* mask = c.mask_of(3, l.tokens);
   const int32_t renormalize = static_cast<int32_t>(c.integer(2));
   const Memory memory(c, 5);
-  const at::TensorOptions i32 = l.z.options().dtype(at::kInt), f32 = l.z.options().dtype(at::kFloat);
   const at::Tensor ws =
       memory.workspace(4, route_workspace_fn(l.tokens, static_cast<int32_t>(l.experts)), l.z);
-  const at::Tensor ids = memory.output({l.tokens, l.top_k}, i32);
-  const at::Tensor weights = memory.output({l.tokens, l.top_k}, f32);
-  const at::Tensor counts = memory.output({l.experts}, i32);
-  const at::Tensor offsets = memory.output({l.experts + 1}, i32);
-  const at::Tensor order = memory.output({l.tokens * l.top_k}, i32);
-  const at::Tensor balance = memory.output({}, f32);
-  const at::Tensor lse = memory.output({l.tokens}, f32);
+  const int64_t pairs = l.tokens * l.top_k;
+  Together outputs(memory, 7, 4 * (3 * pairs + 2 * l.experts + 2 + l.tokens), l.z);
+  const at::Tensor ids = outputs.take({l.tokens, l.top_k}, at::kInt);
+  const at::Tensor weights = outputs.take({l.tokens, l.top_k}, at::kFloat);
+  const at::Tensor order = outputs.take({pairs}, at::kInt);
+  const at::Tensor counts = outputs.take({l.experts}, at::kInt);
+  const at::Tensor offsets = outputs.take({l.experts + 1}, at::kInt);
+  const at::Tensor balance = outputs.take({}, at::kFloat);
+  const at::Tensor lse = outputs.take({l.tokens}, at::kFloat);
   void* none = ws.data_ptr();
   const bool empty = l.tokens == 0;
   mx_status s;
@@ -641,8 +663,8 @@ PyObject* linear_cross_entropy(const Call& c) {
   const Vocabulary v(c, 0);
   const int64_t ignore = c.integer(3);
   const Memory memory(c, 5);
-  const at::TensorOptions f32 = v.x.options().dtype(at::kFloat);
-  const at::Tensor loss = memory.output({v.tokens}, f32), lse = memory.output({v.tokens}, f32);
+  Together outputs(memory, 2, 8 * v.tokens, v.x);
+  const at::Tensor loss = outputs.take({v.tokens}, at::kFloat), lse = outputs.take({v.tokens}, at::kFloat);
   if (v.tokens > 0) {
     const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
     mx_status s;

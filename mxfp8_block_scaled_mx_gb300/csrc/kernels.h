@@ -3,7 +3,8 @@
 // quantize_kernel.cuh; gemm_pair.cu; norm.cu, norm_mixed.cu and norm_f32.cu,
 // which instantiate norm_kernel.cuh; moe_few.cu; rotate.cu,
 // rotate_f32.cu, rotate_back.cu and rotate_back_f32.cu, which instantiate
-// rotate_kernel.cuh; route.cu; vocab_loss.cu; status.cu).  Not part of the public
+// rotate_kernel.cuh; route.cu; vocab_loss.cu; vocab_few.cu;
+// status.cu).  Not part of the public
 // ABI.
 #pragma once
 
@@ -296,6 +297,8 @@ struct VocabParams {
   const float* d_lse;      // [tokens] or nullptr
   int32_t y_fp32;          // kDx, kDw: type of the output
   int32_t add;             // kDx: 1 adds to the output (FP32)
+  void* out;               // few tokens, kGrad, kDx: the output, ld_out elements a row
+  int64_t ld_out;
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -307,6 +310,16 @@ struct VocabParams {
 cudaError_t launch_vocab_product(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
                                  const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
                                  cudaStream_t stream);
+// kStats, kGrad and kDx for few tokens (vocab_few.cu), with rows of W (kDx: hidden
+// channels) as the m rows of the product and tokens as its columns.  Boxes: A 64
+// elements x 128 rows (kDx 64 x 64), B 64 elements x vocab_few_box(tokens) rows.
+// p.m = vocabulary, columns of the piece, or hidden; slots = 4 vocab_few_blocks.
+constexpr int kVocabFewTokens = 64;
+constexpr int kVocabFewBlocks = 152;  // one an SM
+constexpr int vocab_few_box(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
+int vocab_few_blocks(int64_t rows, int splits);
+cudaError_t launch_vocab_few(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
+                             const CUtensorMap& tmap_b, cudaStream_t stream);
 // loss and lse from the parts of every row.
 cudaError_t launch_vocab_finish(const VocabParams& p, float* loss, float* lse, cudaStream_t stream);
 // bf16 y[i] = sum over parts of parts[s][i], n elements (a multiple of 8).

@@ -1107,7 +1107,26 @@ mx_status vocab_check(int64_t tokens, int64_t hidden, int64_t vocab, int64_t ldx
 }
 
 // How the gradient goes through the vocabulary: columns of a piece (whole
-// tiles), and the parts over which dx sums each piece.
+// tiles), and the parts over which dx sums each piece.  Few tokens have kernels of
+// their own, with a tile's rows along hidden.
+bool vocab_few(int64_t tokens) { return tokens <= mx::kVocabFewTokens; }
+
+// Parts of a contraction of `steps` steps, four at least a part, for `tiles` tiles on
+// `places` places: as many as leave fewest places empty in the last round, and no
+// more than that takes.
+int64_t vocab_splits(int64_t tiles, int64_t steps, int64_t places) {
+  int64_t best = 1;
+  double used = 0.0;
+  for (int64_t s = 1; s <= 32 && s * 4 <= steps; ++s) {
+    const int64_t per = ceil_div(steps, s), parts = ceil_div(steps, per);
+    // steps that are work, of those that all places could take meanwhile
+    const double u = static_cast<double>(tiles * steps) /
+                     static_cast<double>(ceil_div(tiles * parts, places) * places * per);
+    if (u > used + 0.03) best = parts, used = u;
+  }
+  return best;
+}
+
 struct VocabPieces {
   int64_t cols;
   int32_t splits, steps;
@@ -1121,24 +1140,29 @@ VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
   const int64_t all = ceil_div(vocab, kVocabTile) * kVocabTile;
   v.cols = most < kVocabTile ? kVocabTile : most < all ? most : all;
   // dx has few tiles where tokens and hidden are small: then parts of the
-  // contraction side by side, as many as fill the pairs of blocks
-  const int64_t tiles = ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
+  // contraction side by side
+  const bool few = vocab_few(tokens);
+  const int64_t tiles = few ? ceil_div(hidden, 128)
+                            : ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
   const int64_t steps = ceil_div(v.cols, 64);
-  int64_t splits = tiles > 0 ? 76 / tiles : 1;
-  if (splits > steps / 4) splits = steps / 4;
-  if (splits < 1) splits = 1;
+  const int64_t splits = vocab_splits(tiles, steps, few ? mx::kVocabFewBlocks : 76);
   v.steps = static_cast<int32_t>(ceil_div(steps, splits));
   v.splits = static_cast<int32_t>(ceil_div(steps, v.steps));
-  v.direct = v.splits == 1 && v.cols >= vocab;
+  v.direct = !few && v.splits == 1 && v.cols >= vocab;
   v.dz_bytes = static_cast<size_t>(tokens * v.cols * 2);
   v.dx_bytes = v.direct ? 0 : static_cast<size_t>(tokens * hidden * 4 * v.splits);
   return v;
 }
 
+// Parts that a token's softmax is joined from: two a tile of columns, or four a
+// block.
+int64_t vocab_slots(int64_t tokens, int64_t vocab) {
+  return vocab_few(tokens) ? 4 * mx::vocab_few_blocks(vocab, 1) : 2 * ceil_div(vocab, kVocabTile);
+}
+
 size_t vocab_forward_bytes(int64_t tokens, int64_t vocab) {
-  // the label's logits (rounded up to 16 bytes), two parts a tile of columns
-  return static_cast<size_t>(ceil_div(tokens, 4) * 16 +
-                             tokens * ceil_div(vocab, kVocabTile) * 2 * 8);
+  // the label's logits (rounded up to 16 bytes), then the parts
+  return static_cast<size_t>(ceil_div(tokens, 4) * 16 + tokens * vocab_slots(tokens, vocab) * 8);
 }
 
 // 2-D bf16 tensor map, box 64 columns x box_rows, 128-byte swizzle, zero fill.
@@ -1219,19 +1243,22 @@ mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
   if (tokens == 0) return MX_OK;
   if (!all_on_device(st->device, {x, w, labels, loss, lse, workspace})) return MX_ERR_INVALID_ARG;
   mx::VocabParams p = vocab_params(st, tokens, vocab, labels, label_bits, ignore_index);
-  p.m = static_cast<int32_t>(tokens);
-  p.n = static_cast<int32_t>(vocab);
   p.k = static_cast<int32_t>(hidden);
   p.steps = static_cast<int32_t>(ceil_div(hidden, 64));
-  p.slots = static_cast<int32_t>(ceil_div(vocab, kVocabTile) * 2);
+  p.slots = static_cast<int32_t>(vocab_slots(tokens, vocab));
   p.z_label = static_cast<float*>(workspace);
   p.partial = reinterpret_cast<float2*>(p.z_label + ceil_div(tokens, 4) * 4);
-  CUtensorMap ta, tb;
-  if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, 128)) != MX_OK) return s;
-  if ((s = encode_bf16_box(&tb, w, hidden, vocab, ldw, 128)) != MX_OK) return s;
-  if (mx::launch_vocab_product(mx::VocabProduct::kStats, p, ta, tb, ta, st->num_sms, stream) !=
-          cudaSuccess ||
-      mx::launch_vocab_finish(p, loss, lse, stream) != cudaSuccess)
+  CUtensorMap tx, tw;
+  const bool few = vocab_few(tokens);
+  const uint32_t box = few ? static_cast<uint32_t>(mx::vocab_few_box(tokens)) : 128u;
+  if ((s = encode_bf16_box(&tx, x, hidden, tokens, ldx, box)) != MX_OK) return s;
+  if ((s = encode_bf16_box(&tw, w, hidden, vocab, ldw, 128)) != MX_OK) return s;
+  p.m = static_cast<int32_t>(few ? vocab : tokens);
+  p.n = static_cast<int32_t>(few ? tokens : vocab);
+  const cudaError_t err =
+      few ? mx::launch_vocab_few(mx::VocabProduct::kStats, p, tw, tx, stream)
+          : mx::launch_vocab_product(mx::VocabProduct::kStats, p, tx, tw, tx, st->num_sms, stream);
+  if (err != cudaSuccess || mx::launch_vocab_finish(p, loss, lse, stream) != cudaSuccess)
     return MX_ERR_CUDA;
   return MX_OK;
 }
@@ -1281,37 +1308,46 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
     mx::VocabParams p = vocab_params(st, tokens, vocab, labels, label_bits, ignore_index);
     CUtensorMap ta, tb, ty;
     // dz of the piece
-    p.m = static_cast<int32_t>(tokens);
-    p.n = static_cast<int32_t>(cols);
+    const bool few = vocab_few(tokens);
+    const uint32_t box = few ? static_cast<uint32_t>(mx::vocab_few_box(tokens)) : 128u;
+    p.m = static_cast<int32_t>(few ? cols : tokens);
+    p.n = static_cast<int32_t>(few ? tokens : cols);
     p.k = static_cast<int32_t>(hidden);
     p.steps = static_cast<int32_t>(ceil_div(hidden, 64));
     p.col0 = static_cast<int32_t>(col0);
     p.lse = lse;
     p.d_loss = d_loss;
     p.d_lse = d_lse;
-    if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, 128)) != MX_OK) return s;
+    p.out = dz;
+    p.ld_out = v.cols;
+    if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, box)) != MX_OK) return s;
     if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 128)) != MX_OK) return s;
     if ((s = encode_output_map(&ty, dz, false, cols, tokens, v.cols, 1)) != MX_OK) return s;
-    if (mx::launch_vocab_product(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream) !=
-        cudaSuccess)
-      return MX_ERR_CUDA;
+    cudaError_t err =
+        few ? mx::launch_vocab_few(mx::VocabProduct::kGrad, p, tb, ta, stream)
+            : mx::launch_vocab_product(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream);
+    if (err != cudaSuccess) return MX_ERR_CUDA;
     // dx of the piece: contiguous along the vocabulary times contiguous along hidden
-    p.n = static_cast<int32_t>(hidden);
+    p.m = static_cast<int32_t>(few ? hidden : tokens);
+    p.n = static_cast<int32_t>(few ? tokens : hidden);
     p.k = static_cast<int32_t>(cols);
     p.steps = v.steps;
     p.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
     p.y_fp32 = !v.direct;
     p.add = col0 > 0;
-    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, 128)) != MX_OK) return s;
+    p.out = parts;
+    p.ld_out = hidden;
+    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
     if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
     if ((s = encode_output_map(&ty, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
                                v.splits)) != MX_OK)
       return s;
-    if (mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream) !=
-        cudaSuccess)
-      return MX_ERR_CUDA;
+    err = few ? mx::launch_vocab_few(mx::VocabProduct::kDx, p, tb, ta, stream)
+              : mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream);
+    if (err != cudaSuccess) return MX_ERR_CUDA;
     // dW of the piece: both operands contiguous along their rows
     p.m = static_cast<int32_t>(cols);
+    p.n = static_cast<int32_t>(hidden);
     p.k = static_cast<int32_t>(tokens);
     p.steps = static_cast<int32_t>(ceil_div(tokens, 64));
     p.splits = 1;

@@ -20,12 +20,14 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "status.cuh"
+#include "vocab.cuh"
 
 namespace mx {
 namespace {
@@ -49,24 +51,6 @@ constexpr uint16_t kBoth = 0x3;
 // Tiles are walked in bands of this many rows of tiles, columns outer inside a
 // band: the band's part of A and a few tiles of B are in use at a time.
 constexpr int kBand = 16;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ int64_t label_of(const VocabParams& p, int32_t row) {
-  return p.labels_64 ? static_cast<const int64_t*>(p.labels)[row]
-                     : static_cast<const int32_t*>(p.labels)[row];
-}
-
-__device__ __forceinline__ bool counts(const VocabParams& p, int64_t label) {
-  return label != p.ignore_index && label >= 0 && label < p.vocab;
-}
-
 // Tile of a unit of work.
 struct Unit {
   int32_t m, n, step0, steps, part;
@@ -393,13 +377,6 @@ template <VocabProduct W>
 cudaError_t launch(const VocabParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
                    const CUtensorMap& ty, int num_sms, cudaStream_t stream) {
   auto kern = vocab_product_kernel<W>;
-  static PerDeviceOnce setup;
-  cudaError_t err = setup.run([&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  });
-  if (err != cudaSuccess) return err;
-  const int64_t units = static_cast<int64_t>((p.m + kTile - 1) / kTile) *
-                        ((p.n + kTile - 1) / kTile) * p.splits;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -411,12 +388,30 @@ cudaError_t launch(const VocabParams& p, const CUtensorMap& ta, const CUtensorMa
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;  // the occupancy query sees the cluster shape only
-  int max_clusters = num_sms / 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(max_clusters * 2));
-  int active = 0;
-  if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) == cudaSuccess && active > 0)
-    max_clusters = ::min(max_clusters, active);
+  // Pairs of blocks that fit the device at once, asked of the runtime the first time
+  // (the query takes longer than a launch) and kept as the set-up flag's companion.
+  static PerDeviceOnce setup;
+  static std::atomic<int> fit[64];
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  std::atomic<int>& clusters = fit[device < 64 ? device : 63];
+  err = setup.run([&]() -> cudaError_t {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;  // the query sees the cluster shape only
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess || active < 1)
+      active = num_sms / 2;
+    clusters.store(active < num_sms / 2 ? active : num_sms / 2);
+    return cudaSuccess;
+  });
+  if (err != cudaSuccess) return err;
+  const int max_clusters = clusters.load();
+  const int64_t units = static_cast<int64_t>((p.m + kTile - 1) / kTile) *
+                        ((p.n + kTile - 1) / kTile) * p.splits;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < max_clusters ? units : max_clusters)));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, p);
@@ -427,7 +422,7 @@ __global__ void vocab_finish_kernel(const VocabParams p, float* loss, float* lse
   pdl_wait();
   pdl_launch_dependents();
   const int32_t row = blockIdx.x * (blockDim.x / 32) + warp_id();
-  if (row >= p.m) return;
+  if (row >= p.tokens) return;
   const float2* part = p.partial + static_cast<int64_t>(row) * p.slots;
   float top = -INFINITY, sum = 0.f;
   for (int32_t i = lane_id(); i < p.slots; i += 32) {
@@ -501,7 +496,7 @@ cudaError_t launch_vocab_finish(const VocabParams& p, float* loss, float* lse,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = pdl_attribute();
-  cfg.gridDim = dim3(static_cast<unsigned>((p.m + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>((p.tokens + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = &attr;

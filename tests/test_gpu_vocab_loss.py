@@ -77,7 +77,10 @@ def check_backward(mx, x, w, labels, ignore=-100, weight_dtype="bf16", use=(True
 # tiles that end inside: rows and columns around 128 and 256, a vocabulary of
 # one; contractions of one element run up to several stages' rounds
 SHAPES = [(1, 64, 1000), (2, 8, 1), (5, 16, 2), (127, 72, 255), (128, 64, 256), (129, 200, 257), (256, 64, 31),
-          (257, 136, 513), (600, 520, 1100), (33, 1000, 2000), (1, 2048, 300), (300, 24, 5000)]
+          (257, 136, 513), (600, 520, 1100), (33, 1000, 2000), (1, 2048, 300), (300, 24, 5000),
+          # few tokens: boxes of 16, 32 and 64, the first count that is not few; more tiles than
+          # blocks, a hidden length of several tiles
+          (16, 72, 700), (17, 64, 129), (32, 136, 1500), (64, 320, 33000), (65, 64, 300), (3, 64, 20001)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)

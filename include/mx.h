@@ -578,7 +578,7 @@ mx_status mx_route(int64_t tokens, int32_t experts, int32_t top_k,
  * d_weights: device float [tokens, top_k] or NULL (zero); d_balance: device float
  *    [1] or NULL; d_lse: device float [tokens] or NULL.
  * logits, mask, renormalize: those of the forward pass; ids, weights, lse,
- *    counts: what it wrote.  d_logits: device [tokens, experts] contiguous, of
+ *    counts: what it wrote (an id outside [0, experts) is passed over).  d_logits: device [tokens, experts] contiguous, of
  *    dtype, rounded once. */
 mx_status mx_route_backward(int64_t tokens, int32_t experts, int32_t top_k,
                             const float* d_weights, const float* d_balance, const float* d_lse,

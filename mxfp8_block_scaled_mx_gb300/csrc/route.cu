@@ -26,6 +26,7 @@
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "softmax.cuh"
 
 namespace mx {
 namespace {
@@ -40,10 +41,10 @@ constexpr int kMaxTopK = 32;
 constexpr int kMaxBlocks = 304;
 constexpr int kOneBlock = 64;
 // Tokens from which on, and experts and winners up to which, a token is a lane's.
-#ifndef TMIN
-#define TMIN 16384
-#endif
-constexpr int kTileTokens = TMIN;
+// (64 experts, top 8, a token a lane against a token a warp, both kernels: 8192 tokens
+// 16.7 and 17.2 us, 65536 27.2 and 46; 128 experts: 8192 22.1 and 20.1, 16384 22.8 and
+// 28.)
+constexpr int kTileTokens = 16384;
 constexpr int kTileExperts = 128;
 constexpr int kTileTopK = 8;
 
@@ -90,6 +91,10 @@ __device__ __forceinline__ void load_logits(const T* row, int32_t c, int32_t n, 
       if (c + v < n) z[v] = to_float(row[c + v]);
   }
 }
+
+// exp(x) for x <= 0, the distance of a logit from its row's largest (or lse): 2^-22
+// of the result and, from rounding the argument, |x| 2^-24.
+__device__ __forceinline__ float exp_below(float x) { return exp2_fast(x * kLog2e); }
 
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      z[v] = c0 + v < r.experts ? expf(z[v] - top) : 0.f;
+      z[v] = c0 + v < r.experts ? exp_below(z[v] - top) : 0.f;
       sum += z[v];
     }
     sum = group_sum<32>(sum);
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
     float picked = 0.f;
     for (int32_t j = lane; j < r.top_k; j += 32) {
       const int2 w = win[j];
-      const float e = expf(logit_of(static_cast<uint32_t>(w.y)) - top);
+      const float e = exp_below(logit_of(static_cast<uint32_t>(w.y)) - top);
       picked += e;
       r.ids[t * r.top_k + j] = w.x;
       atomicAdd(&s.pairs[w.x], 1);
@@ -334,27 +339,30 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams r) {
 }
 
 // The first kernel for many tokens: a warp takes 32 of them at a time, a token a
-// lane.  The logits' keys come to shared memory in rows of an odd length; every
-// lane goes along its row with its K largest so far in registers, then along it
-// again with the exponentials, which it leaves there; the sums of p go down the
-// columns, an expert a lane.
-template <typename T, int K>
+// lane.  The logits come to shared memory in rows of an odd length.  Every lane
+// keeps the largest of each eight of its row in registers; a winner is the largest
+// of those, looked up among its eight, which then give their next largest (a NaN
+// in its place: the maximum passes over it).  The exponentials take the logits'
+// places, and the sums of p go down the columns, an expert a lane.
+template <typename T, int EIGHTS>
 __global__ void __launch_bounds__(256) route_tile_kernel(const RouteParams r) {
-  extern __shared__ uint32_t tiles[];
+  extern __shared__ float tiles[];
   __shared__ int32_t pairs[kTileExperts], counted[kTileExperts], tokens;
   __shared__ float factor[8][32];
   const int32_t warp = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
-  const int32_t stride = r.experts | 1;
-  uint32_t* tile = tiles + warp * 32 * stride;
+  const int32_t row_size = (r.experts + 7) / 8 * 8 + 1;
+  float* tile = tiles + warp * 32 * row_size;
   for (int32_t e = threadIdx.x; e < r.experts; e += blockDim.x) pairs[e] = counted[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
+  float* mine = tile + lane * row_size;
+  for (int32_t e = r.experts; e < row_size; ++e) mine[e] = NAN;  // (no expert: never chosen)
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   const int32_t end = min(r.tokens, (static_cast<int32_t>(blockIdx.x) + 1) * r.tokens_per_block);
-  float acc[kTileExperts / 32];
+  float acc[EIGHTS / 4];
 #pragma unroll
-  for (int i = 0; i < kTileExperts / 32; ++i) acc[i] = 0.f;
+  for (int i = 0; i < EIGHTS / 4; ++i) acc[i] = 0.f;
   const T* logits = static_cast<const T*>(r.logits);
   // lanes of a row's four-logit runs, a power of two
   const int32_t shift = r.experts <= 32 ? 3 : r.experts <= 64 ? 4 : 5;
@@ -363,78 +371,108 @@ __global__ void __launch_bounds__(256) route_tile_kernel(const RouteParams r) {
     if (r.vec) {
       const int32_t c = (lane & ((1 << shift) - 1)) * 4, step = 32 >> shift;
       if (c < r.experts) {
-#pragma unroll 4
+#pragma unroll 8
         for (int32_t row = lane >> shift; row < rows; row += step) {
           float z[4];
           load_logits<T, 4>(logits + (t0 + row) * r.ld, c, r.experts, true, z);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) tile[row * stride + c + v] = key_of(z[v]);
+          for (int v = 0; v < 4; ++v) tile[row * row_size + c + v] = z[v];
         }
       }
     } else {
       for (int32_t row = 0; row < rows; ++row)
         for (int32_t c = lane; c < r.experts; c += 32)
-          tile[row * stride + c] = key_of(to_float(logits[(t0 + row) * r.ld + c]));
+          tile[row * row_size + c] = to_float(logits[(t0 + row) * r.ld + c]);
     }
     __syncwarp();
-    const bool here = lane < rows;
     const int32_t t = t0 + lane;
-    uint32_t* mine = tile + lane * stride;
     bool valid = false;
-    if (here) {
+    if (lane < rows) {
       valid = !r.mask || r.mask[t] != 0;
-      uint32_t key[K];
-      int32_t id[K];
+      float most[EIGHTS];
 #pragma unroll
-      for (int j = 0; j < K; ++j) key[j] = 0u, id[j] = 0;
-#pragma unroll 4
-      for (int32_t e = 0; e < r.experts; ++e) {
-        const uint32_t v = mine[e];
-        bool over[K];  // the new key goes before place j (after equal ones)
+      for (int g = 0; g < EIGHTS; ++g) {
+        most[g] = NAN;
+        if (g * 8 < r.experts) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) over[j] = v > key[j];
-#pragma unroll
-        for (int j = K - 1; j > 0; --j) {
-          key[j] = over[j - 1] ? key[j - 1] : over[j] ? v : key[j];
-          id[j] = over[j - 1] ? id[j - 1] : over[j] ? e : id[j];
+          for (int i = 0; i < 8; ++i) most[g] = fmaxf(most[g], mine[g * 8 + i]);
         }
-        key[0] = over[0] ? v : key[0];
-        id[0] = over[0] ? e : id[0];
       }
-      const float top = logit_of(key[0]);
+      float w[kTileTopK];
+      int32_t id[kTileTopK];
+#pragma unroll
+      for (int j = 0; j < kTileTopK; ++j) {
+        w[j] = 0.f;
+        id[j] = 0;
+        if (j >= r.top_k) continue;
+        float best = most[0];
+#pragma unroll
+        for (int g = 1; g < EIGHTS; ++g) best = fmaxf(best, most[g]);
+        if (best == best) {
+          int32_t at = 0;
+#pragma unroll
+          for (int g = EIGHTS - 1; g >= 0; --g) at = most[g] == best ? g : at;
+          float* eight = mine + at * 8;
+          float v[8], next = NAN;
+          int32_t place = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = eight[i];
+#pragma unroll
+          for (int i = 7; i >= 0; --i) place = v[i] == best ? i : place;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) next = i == place ? next : fmaxf(next, v[i]);
+#pragma unroll
+          for (int g = 0; g < EIGHTS; ++g) most[g] = g == at ? next : most[g];
+          w[j] = eight[place];
+          eight[place] = NAN;
+          id[j] = at * 8 + place;
+        } else {
+          // nothing but NaN is left: the lowest expert that was not taken
+          int32_t e = 0;
+          for (bool taken = true; taken; e += taken) {
+            taken = false;
+#pragma unroll
+            for (int i = 0; i < j; ++i) taken = taken || id[i] == e;
+          }
+          w[j] = NAN;
+          id[j] = e;
+        }
+      }
+      const float top = w[0];
+#pragma unroll
+      for (int j = 0; j < kTileTopK; ++j)
+        if (j < r.top_k) mine[id[j]] = w[j];
       float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
       for (int32_t e = 0; e < r.experts; ++e) {
-        const float p = expf(logit_of(mine[e]) - top);
-        mine[e] = __float_as_uint(p);
+        const float p = exp_below(mine[e] - top);
+        mine[e] = p;
         s4[e & 3] += p;
       }
       const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]), inv = 1.f / sum;
       r.lse[t] = top + logf(sum);
-      float w[K], picked = 0.f;
+      float picked = 0.f;
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        w[j] = 0.f;
+      for (int j = 0; j < kTileTopK; ++j)
         if (j < r.top_k) {
-          w[j] = __uint_as_float(mine[id[j]]);
+          w[j] = mine[id[j]];
           picked += w[j];
           atomicAdd(&pairs[id[j]], 1);
           if (valid) atomicAdd(&counted[id[j]], 1);
         }
-      }
       // p / sum of p, so that a softmax that is NaN stays so
       const float scale = r.renormalize ? inv / (picked * inv) : inv;
       const int64_t at = static_cast<int64_t>(t) * r.top_k;
-      if (K == 8 && r.top_k == 8 && r.vec_ids) {
+      if (r.top_k == 8 && r.vec_ids) {
         int4* ids = reinterpret_cast<int4*>(r.ids + at);
         float4* ws = reinterpret_cast<float4*>(r.weights + at);
         ids[0] = make_int4(id[0], id[1], id[2], id[3]);
-        ids[1] = make_int4(id[4 % K], id[5 % K], id[6 % K], id[7 % K]);
+        ids[1] = make_int4(id[4], id[5], id[6], id[7]);
         ws[0] = make_float4(w[0] * scale, w[1] * scale, w[2] * scale, w[3] * scale);
-        ws[1] = make_float4(w[4 % K] * scale, w[5 % K] * scale, w[6 % K] * scale, w[7 % K] * scale);
+        ws[1] = make_float4(w[4] * scale, w[5] * scale, w[6] * scale, w[7] * scale);
       } else {
 #pragma unroll
-        for (int j = 0; j < K; ++j)
+        for (int j = 0; j < kTileTopK; ++j)
           if (j < r.top_k) {
             r.ids[at + j] = id[j];
             r.weights[at + j] = w[j] * scale;
@@ -449,24 +487,23 @@ __global__ void __launch_bounds__(256) route_tile_kernel(const RouteParams r) {
       const int32_t row = __ffs(left) - 1;
       const float f = factor[warp][row];
 #pragma unroll
-      for (int i = 0; i < kTileExperts / 32; ++i)
+      for (int i = 0; i < EIGHTS / 4; ++i)
         if (i * 32 + lane < r.experts)
-          acc[i] = fmaf(__uint_as_float(tile[row * stride + i * 32 + lane]), f, acc[i]);
+          acc[i] = fmaf(tile[row * row_size + i * 32 + lane], f, acc[i]);
     }
     __syncwarp();
   }
   // sums of p, warp by warp
-  float* sums = reinterpret_cast<float*>(tile);
 #pragma unroll
-  for (int i = 0; i < kTileExperts / 32; ++i)
-    if (i * 32 + lane < r.experts) sums[i * 32 + lane] = acc[i];
+  for (int i = 0; i < EIGHTS / 4; ++i)
+    if (i * 32 + lane < r.experts) tile[i * 32 + lane] = acc[i];
   __syncthreads();
   const Parts parts(r);
   for (int32_t e = threadIdx.x; e < parts.row; e += blockDim.x) {
     float a = 0.f;
     if (e < r.experts)
       for (int32_t w = 0; w < warps; ++w)
-        a += __uint_as_float(tiles[w * 32 * stride + e]);
+        a += tiles[w * 32 * row_size + e];
     const int32_t at = blockIdx.x * parts.row + e;
     parts.pairs[at] = e < r.experts ? pairs[e] : 0;
     parts.counted[at] = e < r.experts ? counted[e] : 0;
@@ -585,40 +622,54 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const Rout
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[c0 + v] = add[v] = 0.f;
   __syncwarp();
-  const int32_t step = gridDim.x * kWarps * kGroups;
-  for (int32_t base = (blockIdx.x * kWarps + warp_id()) * kGroups; base < r.tokens; base += step) {
-    const int32_t t = base + group;
-    const bool here = t < r.tokens;
-    float z[V];
+  // a token's loads, asked for one round ahead
+  struct Token {
+    float z[V], lse, w[kPer], g[kPer];
+    int32_t id[kPer];
+    bool here, valid;
+  };
+  auto load = [&](Token& k, int32_t t) {
+    k.here = t < r.tokens;
+    k.valid = false;
+    k.lse = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) z[v] = 0.f;
-    float lse = 0.f;
-    bool valid = false;
-    if (here) {
-      load_logits<T, V>(static_cast<const T*>(r.logits) + t * r.ld, c0, r.experts, r.vec, z);
-      lse = r.lse_in[t];
-      valid = !r.mask || r.mask[t] != 0;
+    for (int v = 0; v < V; ++v) k.z[v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) k.id[i] = -1;
+    if (!k.here) return;
+    load_logits<T, V>(static_cast<const T*>(r.logits) + t * r.ld, c0, r.experts, r.vec, k.z);
+    k.lse = r.lse_in[t];
+    k.valid = !r.mask || r.mask[t] != 0;
+    if (!r.d_weights) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int32_t j = lane + i * L, at = t * r.top_k + j;
+      if (j >= r.top_k) continue;
+      const int32_t id = r.ids_in[at];
+      k.id[i] = static_cast<uint32_t>(id) < static_cast<uint32_t>(r.experts) ? id : -1;
+      k.w[i] = r.w_in[at];
+      k.g[i] = r.d_weights[at];
     }
+  };
+  const int32_t step = gridDim.x * kWarps * kGroups;
+  int32_t base = (blockIdx.x * kWarps + warp_id()) * kGroups;
+  Token ahead;
+  load(ahead, base + group);
+  for (; base < r.tokens; base += step) {
+    const int32_t t = base + group;
+    const Token k = ahead;
+    if (base + step < r.tokens) load(ahead, t + step);
+    const bool here = k.here, valid = k.valid;
+    float z[V];
     float dot = 0.f;
     if (r.d_weights) {
-      float w[kPer], g[kPer];
-      int32_t id[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int32_t j = lane + i * L;
-        id[i] = -1;
-        if (here && j < r.top_k) {
-          const int32_t at = t * r.top_k + j;
-          id[i] = r.ids_in[at];
-          w[i] = r.w_in[at];
-          g[i] = r.d_weights[at];
-          dot = fmaf(w[i], g[i], dot);
-        }
-      }
+      for (int i = 0; i < kPer; ++i)
+        if (k.id[i] >= 0) dot = fmaf(k.w[i], k.g[i], dot);
       dot = group_sum<L>(dot);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (id[i] >= 0) mine[id[i]] = w[i] * (g[i] - (r.renormalize ? dot : 0.f));
+        if (k.id[i] >= 0) mine[k.id[i]] = k.w[i] * (k.g[i] - (r.renormalize ? dot : 0.f));
       __syncwarp();
 #pragma unroll
       for (int v = 0; v < V; v += 4) {
@@ -628,12 +679,13 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const Rout
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (id[i] >= 0) mine[id[i]] = 0.f;
+        if (k.id[i] >= 0) mine[k.id[i]] = 0.f;
+      __syncwarp();
     }
     float inner = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      z[v] = c0 + v < r.experts ? expf(z[v] - lse) : 0.f;
+      z[v] = c0 + v < r.experts ? exp_below(k.z[v] - k.lse) : 0.f;
       if (valid) inner = fmaf(z[v], c[v], inner);
     }
     inner = group_sum<L>(inner);
@@ -684,17 +736,18 @@ bool tiled(int64_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= kTileTokens && experts <= kTileExperts && top_k <= kTileTopK;
 }
 
-template <typename T, int K>
+template <typename T, int EIGHTS>
 cudaError_t tile_forward(const RouteParams& r, cudaStream_t stream) {
-  auto kern = route_tile_kernel<T, K>;
+  auto kern = route_tile_kernel<T, EIGHTS>;
   static PerDeviceOnce setup;
   const cudaError_t err = setup.run([&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                8 * 32 * (kTileExperts + 1) * 4);
+                                8 * 32 * (EIGHTS * 8 + 1) * 4);
   });
   if (err != cudaSuccess) return err;
   const int32_t warps = r.tokens_per_block < 256 ? (r.tokens_per_block + 31) / 32 : 8;
-  return launch_pdl(kern, r.blocks, warps * 32, r, stream, warps * 32 * (r.experts | 1) * 4);
+  return launch_pdl(kern, r.blocks, warps * 32, r, stream,
+                    warps * 32 * ((r.experts + 7) / 8 * 8 + 1) * 4);
 }
 
 template <typename T, int V>
@@ -703,7 +756,7 @@ cudaError_t forward(const RouteParams& r, cudaStream_t stream) {
   const cudaError_t err =
       !tiled(r.tokens, r.experts, r.top_k)
           ? launch_pdl(route_kernel<T, V, false>, r.blocks, kThreads, r, stream)
-          : r.top_k <= 4 ? tile_forward<T, 4>(r, stream) : tile_forward<T, 8>(r, stream);
+          : r.experts <= 64 ? tile_forward<T, 8>(r, stream) : tile_forward<T, 16>(r, stream);
   return err != cudaSuccess ? err
                             : launch_pdl(route_order_kernel, r.blocks + 1, kThreads, r, stream);
 }

@@ -1,21 +1,13 @@
-// vocab.cuh -- what the kernels of the vocabulary loss share: the softmax in powers
-// of two, and labels.
+// vocab.cuh -- what the kernels of the vocabulary loss share: labels, and the runs of
+// a logit's contraction.
 #pragma once
 
 #include <cstdint>
 
 #include "kernels.h"
+#include "softmax.cuh"
 
 namespace mx {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ int64_t label_of(const VocabParams& p, int32_t row) {
   return p.labels_64 ? static_cast<const int64_t*>(p.labels)[row]
@@ -25,5 +17,19 @@ __device__ __forceinline__ int64_t label_of(const VocabParams& p, int32_t row) {
 __device__ __forceinline__ bool counts(const VocabParams& p, int64_t label) {
   return label != p.ignore_index && label >= 0 && label < p.vocab;
 }
+
+// The tensor core cuts its FP32 accumulator off where it adds to it, so a long
+// contraction loses a little of every term in the same direction: over 4096
+// elements 1.2e-6 of lse.  For the losses a contraction of more than 16 steps of
+// 64 elements is therefore taken in equal runs of at most 16, each in an
+// accumulator of its own, which the epilogue adds in FP32, rounded to nearest.
+struct Runs {
+  int32_t count, steps;  // steps of all but the last
+  __device__ __forceinline__ explicit Runs(int32_t all, bool split) {
+    count = split ? (all + 15) / 16 : 1;
+    steps = (all + count - 1) / count;
+    count = (all + steps - 1) / steps;
+  }
+};
 
 }  // namespace mx

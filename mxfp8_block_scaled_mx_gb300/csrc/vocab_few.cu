@@ -172,35 +172,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int32_t u = block; u < units && ok; u += blocks) {
       const int32_t step0 = u / tiles * p.steps, steps = min(p.steps, all_steps - step0);
-      if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns))
-        break;
-      tc_fence_after_sync();
-      for (int32_t i = 0; i < steps; ++i) {
-        if (!mbar_wait_warp(&full[stage], phase, s_abort, p.status, p.wait_limit_ns)) {
+      const Runs runs(steps, W == VocabProduct::kStats);
+      for (int32_t i0 = 0; i0 < steps && ok; i0 += runs.steps) {
+        if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t a_lo = a_lo0 + stage * (kABytes >> 4);
-        const uint32_t b_lo = b_lo0 + stage * (C::kBBytes >> 4);
-        if (elect_one()) {
+        const int32_t end = min(steps, i0 + runs.steps);
+        for (int32_t i = i0; i < end; ++i) {
+          if (!mbar_wait_warp(&full[stage], phase, s_abort, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_lo = a_lo0 + stage * (kABytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (C::kBBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t j = 0; j < kStep / 16; ++j)
-            tc_mma_f16(tmem_base + buf * N, a_lo + j * kNextA, kHi, b_lo + j * kNextB, kHi, kIdesc,
-                       (i > 0 || j > 0) ? 1u : 0u);
-          tc_commit(&empty[stage]);
+            for (uint32_t j = 0; j < kStep / 16; ++j)
+              tc_mma_f16(tmem_base + buf * N, a_lo + j * kNextA, kHi, b_lo + j * kNextB, kHi,
+                         kIdesc, (i > i0 || j > 0) ? 1u : 0u);
+            tc_commit(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (!ok) break;
+        if (elect_one()) tc_commit(&acc_full[buf]);
         __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if (elect_one()) tc_commit(&acc_full[buf]);
-      __syncwarp();
-      buf ^= 1u;
-      if (buf == 0) acc_phase ^= 1u;
     }
     if (elect_one()) {
       tc_commit(mma_done);
@@ -246,20 +252,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t part = u / tiles;
       const int32_t row0 = (u - part * tiles) * kRows + static_cast<int32_t>(q * 32);
       const int32_t row = row0 + static_cast<int32_t>(lane);
-      const bool got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after_sync();
-      uint32_t v[N];
-      load_accumulator<N>(tmem_base + ((q * 32u) << 16) + buf * N, v);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      float v[N];
+      const Runs runs(min(p.steps, all_steps - part * p.steps), W == VocabProduct::kStats);
+      bool got = true;
+      for (int32_t run = 0; run < runs.count; ++run) {
+        got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
+        if (!(got = __all_sync(0xffffffffu, got))) break;
+        tc_fence_after_sync();
+        uint32_t w[N];
+        load_accumulator<N>(tmem_base + ((q * 32u) << 16) + buf * N, w);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          v[j] = run == 0 ? __uint_as_float(w[j]) : v[j] + __uint_as_float(w[j]);
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (!got) break;
       if constexpr (W == VocabProduct::kStats) {
 #pragma unroll
         for (int o = 0; o < kOwn; ++o) {
 #pragma unroll
           for (int j = 0; j < C::kShare; ++j)
-            z[j * 33 + lane] = row < p.m ? __uint_as_float(v[o * 32 + j]) : -INFINITY;
+            z[j * 33 + lane] = row < p.m ? v[o * 32 + j] : -INFINITY;
           __syncwarp();
           const int32_t t = static_cast<int32_t>(lane) + o * 32;
           if (t < p.tokens && row0 < p.m) {
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < N; ++j) {
             if (j >= p.tokens) break;
             const float4 r = s_row[j];
-            float d = r.y * exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, -r.x));
+            float d = r.y * exp2_fast(fmaf(v[j], kLog2e, -r.x));
             if (__float_as_int(r.w) == row) d -= r.z;
             dz[j * p.ld_out] = __float2bfloat16_rn(d);
           }
@@ -300,12 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < N; ++j) {
             if (j >= p.tokens) break;
             float* at = y + j * p.ld_out;
-            *at = p.add ? *at + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+            *at = p.add ? *at + v[j] : v[j];
           }
         }
       }
-      buf ^= 1u;
-      if (buf == 0) acc_phase ^= 1u;
     }
     if constexpr (W == VocabProduct::kStats) {
 #pragma unroll

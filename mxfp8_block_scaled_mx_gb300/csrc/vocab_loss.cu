@@ -197,36 +197,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int32_t u = cluster; u < units && ok; u += clusters) {
       const Unit t = unit_of(p, u, m_units, n_tiles);
-      if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns))
-        break;
-      tc_fence_after_sync();
-      const uint32_t acc = tmem_base + buf * kTile;
-      for (int32_t i = 0; i < t.steps; ++i) {
-        if (!mbar_wait_warp(&full[stage], phase, s_abort, p.status, p.wait_limit_ns)) {
+      const Runs runs(t.steps, W == VocabProduct::kStats);
+      for (int32_t i0 = 0; i0 < t.steps && ok; i0 += runs.steps) {
+        if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t a_lo = a_lo0 + stage * (kOperandBytes >> 4);
-        const uint32_t b_lo = b_lo0 + stage * (kOperandBytes >> 4);
-        if (elect_one()) {
+        const uint32_t acc = tmem_base + buf * kTile;
+        const int32_t end = min(t.steps, i0 + runs.steps);
+        for (int32_t i = i0; i < end; ++i) {
+          if (!mbar_wait_warp(&full[stage], phase, s_abort, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_lo = a_lo0 + stage * (kOperandBytes >> 4);
+          const uint32_t b_lo = b_lo0 + stage * (kOperandBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t j = 0; j < kStep / 16; ++j)
-            tc_mma_pair_f16(acc, a_lo + j * kNextA, kHi, b_lo + j * kNextB, kHi, kIdesc,
-                            (i > 0 || j > 0) ? 1u : 0u);
-          tc_commit_pair_multicast(&empty[stage], kBoth);
+            for (uint32_t j = 0; j < kStep / 16; ++j)
+              tc_mma_pair_f16(acc, a_lo + j * kNextA, kHi, b_lo + j * kNextB, kHi, kIdesc,
+                              (i > i0 || j > 0) ? 1u : 0u);
+            tc_commit_pair_multicast(&empty[stage], kBoth);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (!ok) break;
+        if (elect_one()) tc_commit_pair_multicast(&acc_full[buf], kBoth);
         __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if (elect_one()) tc_commit_pair_multicast(&acc_full[buf], kBoth);
-      __syncwarp();
-      buf ^= 1u;
-      if (buf == 0) acc_phase ^= 1u;
     }
     if (elect_one()) {
       tc_commit_pair_multicast(mma_done, 0x1);
@@ -263,40 +269,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const bool got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after_sync();
-      const uint32_t taddr = tmem_base + ((q * 32u) << 16) + buf * kTile + half * kHalf;
       auto release = [&] {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed_cluster(empty_leader0 + buf * 8u);
       };
+      auto wait = [&] {
+        const bool got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
+        return __all_sync(0xffffffffu, got);
+      };
+      const uint32_t taddr0 = tmem_base + ((q * 32u) << 16) + half * kHalf;
       if constexpr (W == VocabProduct::kStats) {
+        // the runs' sums, each accumulator released as soon as it is read
+        float z[kHalf];
+        const Runs runs(t.steps, true);
+        bool got = true;
+        for (int32_t run = 0; run < runs.count; ++run) {
+          if (!(got = wait())) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 16) {
+            uint32_t a[8], b[8];
+            tmem_ld_32x32b_x8(taddr0 + buf * kTile + c, a);
+            tmem_ld_32x32b_x8(taddr0 + buf * kTile + c + 8, b);
+            tmem_ld_wait_for(a, b);
+            if (c + 16 == kHalf) release();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              z[c + j] = __uint_as_float(a[j]) + (run == 0 ? 0.f : z[c + j]);
+              z[c + 8 + j] = __uint_as_float(b[j]) + (run == 0 ? 0.f : z[c + 8 + j]);
+            }
+          }
+          buf ^= 1u;
+          if (buf == 0) acc_phase ^= 1u;
+        }
+        if (!got) break;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(taddr + c * 32, v);
-          tmem_ld_wait();
-          if (c == 3) release();
           const int32_t left = p.n - (col0 + c * 32);  // columns of the matrix from here on
           if (left < 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (j >= left) v[j] = __float_as_uint(-INFINITY);
+              if (j >= left) z[c * 32 + j] = -INFINITY;
           }
           const int32_t at = label - c * 32;
           if (__any_sync(0xffffffffu, label >= 0 && at >= 0 && at < 32)) {
-            float z = 0.f;
+            float chosen = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (j == at) z = __uint_as_float(v[j]);
-            if (label >= 0 && at >= 0 && at < 32) p.z_label[row] = z;
+              if (j == at) chosen = z[c * 32 + j];
+            if (label >= 0 && at >= 0 && at < 32) p.z_label[row] = chosen;
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[j]));
+          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], z[c * 32 + j]);
           // the reference that both the sum and its later uses take: a value of
           // float, in log2 units
           const float next =
@@ -304,14 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ref = next == -INFINITY ? 0.f : next;
           float s4[4] = {sum * exp2_fast(top - ref), 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            s4[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
+          for (int j = 0; j < 32; ++j) s4[j & 3] += exp2_fast(fmaf(z[c * 32 + j], kLog2e, -ref));
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
           top = next;
         }
         if (row < p.m)
           p.partial[static_cast<int64_t>(row) * p.slots + t.n * 2 + half] = make_float2(top, sum);
       } else {
+        if (!wait()) break;
+        tc_fence_after_sync();
+        const uint32_t taddr = taddr0 + buf * kTile;
         const bool f32 = W != VocabProduct::kGrad && p.y_fp32 != 0;
         const int32_t rounds = f32 ? 4 : 2;  // of 128 bytes a row
         for (int32_t c = 0; c < rounds; ++c) {
@@ -356,9 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         }
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      buf ^= 1u;
-      if (buf == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_all();
   }

@@ -175,6 +175,15 @@ def test_refusals(mx):
             bad()
 
 
+def test_ids_out_of_range_are_passed_over(mx):
+    z = logits(50, 24, FP32)
+    r = mx.route(z, 4)
+    dw = torch.randn_like(r.weights)
+    r.ids[3, 1], r.ids[4, 2], r.ids[5, 0] = -1, 24, 2 ** 30
+    d = mx.route_backward(dw, None, z, r)
+    assert torch.isfinite(d).all() and mx.device_status() == 0
+
+
 def test_autograd(mx):
     for dtype in (BF16, FP32):
         z = logits(200, 24, dtype).requires_grad_()

@@ -628,7 +628,8 @@ size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden
  * d_loss, d_lse: device float [tokens], or NULL (zero).
  * lse: device float [tokens], of the forward pass.
  * dx: device bf16 [tokens, hidden] contiguous; dw: device [vocab, hidden]
- *    contiguous of dw_dtype; both on 16 bytes.  Sums run in a fixed order for
+ *    contiguous of dw_dtype; both on 16 bytes.  One of them may be NULL, and its
+ *    product is left out.  Sums run in a fixed order for
  *    given sizes: the same inputs give the same bits.  tokens == 0 writes zeros to
  *    dw.
  * Other arguments and constraints as mx_linear_cross_entropy. */

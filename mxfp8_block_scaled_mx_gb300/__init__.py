@@ -1008,27 +1008,29 @@ class _LinearCrossEntropy(torch.autograd.Function):
             return (None,) * 6
         x, weight, labels, lse = ctx.saved_tensors
         d_loss, d_lse = (None if d is None else d.contiguous() for d in (d_loss, d_lse))
-        dx, dw = linear_cross_entropy_backward(d_loss, d_lse, x, weight, labels, lse, ctx.ignore_index)
-        return tuple(g if want else None
-                     for g, want in zip((dx, dw), ctx.needs_input_grad)) + (None,) * 4
+        need_x, need_weight = ctx.needs_input_grad[:2]
+        return linear_cross_entropy_backward(d_loss, d_lse, x, weight, labels, lse, ctx.ignore_index,
+                                             need_x=need_x, need_weight=need_weight) + (None,) * 4
 
 
 def linear_cross_entropy_backward(d_loss: torch.Tensor | None, d_lse: torch.Tensor | None,
                                   x: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
                                   lse: torch.Tensor, ignore_index: int = -100,
-                                  weight_dtype: str = "bf16",
+                                  weight_dtype: str = "bf16", need_x: bool = True,
+                                  need_weight: bool = True,
                                   workspace: torch.Tensor | None = None, stream=None):
     """Gradients (of x: bf16, of weight: bf16 or, with weight_dtype "fp32",
     fp32) of linear_cross_entropy from those of its outputs (fp32 [tokens];
     None: zero).  lse: what the forward pass returned.  Goes through the
-    vocabulary in pieces, whose logits are computed again.  The same inputs give
-    the same bits.  workspace: uint8,
+    vocabulary in pieces, whose logits are computed again.  need_x, need_weight:
+    a gradient that is not needed is None, and its product left out.  The same
+    inputs give the same bits.  workspace: uint8,
     mx_linear_cross_entropy_backward_workspace(tokens, hidden, vocab) bytes, one
     call at a time; allocated here when None."""
     if weight_dtype not in DTYPE:
         raise ValueError(f"weight_dtype must be one of {sorted(DTYPE)}, got {weight_dtype!r}")
     r = _native().linear_cross_entropy_backward(d_loss, d_lse, x, weight, labels, lse, ignore_index,
-                                                DTYPE[weight_dtype], workspace,
+                                                DTYPE[weight_dtype], need_x, need_weight, workspace,
                                                 None if stream is None else _stream(stream))
     if type(r) is int:
         raise MxError("mx_linear_cross_entropy_backward", r)

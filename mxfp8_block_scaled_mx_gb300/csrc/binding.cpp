@@ -206,8 +206,10 @@ class Memory {
   c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
-// Small outputs out of one allocation, 16 bytes apart at least: an allocation each
-// takes longer than the kernels of a call for a single token.
+// Small outputs out of one allocation, each on 16 bytes: an allocation each takes
+// longer than the kernels of a call for a single token.  (Up to kSmall bytes; what is
+// larger is its own, so that the caller can free one without the other.)
+constexpr int64_t kSmall = 1 << 20;
 class Together {
  public:
   Together(const Memory& memory, int64_t tensors, int64_t bytes, const at::Tensor& like)
@@ -451,6 +453,9 @@ struct Heads {
   mx_dtype x_type, w_type;
   float scale, eps;
 
+  // of q and k together
+  int64_t bytes() const { return tokens * (q_heads + k_heads) * dim * (x_type == MX_FP32 ? 4 : 2); }
+
   Heads(const Call& c, int i) {
     q = c.tensor(i, "q");
     k = c.tensor(i + 1, "k");
@@ -481,12 +486,19 @@ PyObject* norm_rotate(const Call& c) {
   const Heads h(c, 0);
   int64_t oq_st = h.q_heads * h.dim, oq_sh = h.dim, ok_st = h.k_heads * h.dim, ok_sh = h.dim;
   const Memory memory(c, 11);
-  const at::Tensor out_q =
-      c.given(9) ? c.heads_of(9, "out_q", h.tokens, h.q_heads, h.dim, h.q.scalar_type(), &oq_st, &oq_sh)
-                 : memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
-  const at::Tensor out_k =
-      c.given(10) ? c.heads_of(10, "out_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &ok_st, &ok_sh)
-                  : memory.output({h.tokens, h.k_heads, h.dim}, h.k.options());
+  at::Tensor out_q, out_k;
+  if (c.given(9))
+    out_q = c.heads_of(9, "out_q", h.tokens, h.q_heads, h.dim, h.q.scalar_type(), &oq_st, &oq_sh);
+  if (c.given(10))
+    out_k = c.heads_of(10, "out_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &ok_st, &ok_sh);
+  if (!c.given(9) && !c.given(10) && h.bytes() <= kSmall) {
+    Together outputs(memory, 2, h.bytes(), h.q);
+    out_q = outputs.take({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
+    out_k = outputs.take({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
+  } else {
+    if (!c.given(9)) out_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
+    if (!c.given(10)) out_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.options());
+  }
   if (h.tokens > 0) {
     mx_status s;
     Py_BEGIN_ALLOW_THREADS
@@ -520,10 +532,17 @@ PyObject* norm_rotate_backward(const Call& c) {
   const at::Tensor& d_k = c.heads_of(1, "d_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &dk_st, &dk_sh);
   const Memory memory(c, 12);
   const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim), h.q);
-  const at::Tensor dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
-  const at::Tensor dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.k.options());
-  Together sums(memory, 2, 8 * h.dim, h.q);
-  const at::Tensor dw_q = sums.take({h.dim}, at::kFloat), dw_k = sums.take({h.dim}, at::kFloat);
+  const bool small = h.bytes() <= kSmall;
+  Together outputs(memory, 4, (small ? h.bytes() : 0) + 8 * h.dim, h.q);
+  const at::Tensor dw_q = outputs.take({h.dim}, at::kFloat), dw_k = outputs.take({h.dim}, at::kFloat);
+  at::Tensor dx_q, dx_k;
+  if (small) {
+    dx_q = outputs.take({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
+    dx_k = outputs.take({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
+  } else {
+    dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
+    dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.options());
+  }
   // a tensor without tokens has no address; the workspace's stands in, unused
   void* none = ws.data_ptr();
   const bool empty = h.tokens == 0;
@@ -678,7 +697,8 @@ PyObject* linear_cross_entropy(const Call& c) {
   return tuple_of({loss, lse});
 }
 
-// d_loss, d_lse, x, weight, labels, lse, ignore_index, weight gradient in FP32, workspace, stream
+// d_loss, d_lse, x, weight, labels, lse, ignore_index, weight gradient in FP32, x and
+// weight wanted, workspace, stream
 PyObject* linear_cross_entropy_backward(const Call& c) {
   const Vocabulary v(c, 2);
   const float* d_loss = c.floats(0, "d_loss", {v.tokens});
@@ -686,10 +706,13 @@ PyObject* linear_cross_entropy_backward(const Call& c) {
   const at::Tensor& lse = c.dense(5, "lse", {v.tokens}, at::kFloat);
   const int64_t ignore = c.integer(6);
   const bool f32 = c.integer(7) != 0;
-  const Memory memory(c, 9);
-  const at::Tensor ws = memory.workspace(8, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
-  const at::Tensor dx = memory.output({v.tokens, v.hidden}, v.x.options());
-  const at::Tensor dw = memory.output({v.vocab, v.hidden}, v.x.options().dtype(f32 ? at::kFloat : at::kBFloat16));
+  const bool need_x = c.integer(8) != 0, need_w = c.integer(9) != 0;
+  if (!need_x && !need_w) return tuple_of({at::Tensor(), at::Tensor()});
+  const Memory memory(c, 11);
+  const at::Tensor ws = memory.workspace(10, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
+  at::Tensor dx, dw;
+  if (need_x) dx = memory.output({v.tokens, v.hidden}, v.x.options());
+  if (need_w) dw = memory.output({v.vocab, v.hidden}, v.x.options().dtype(f32 ? at::kFloat : at::kBFloat16));
   void* none = ws.data_ptr();
   const bool empty = v.tokens == 0;
   mx_status s;
@@ -697,7 +720,7 @@ PyObject* linear_cross_entropy_backward(const Call& c) {
   s = loss_backward_fn(v.tokens, v.hidden, v.vocab, empty ? nullptr : d_loss, empty ? nullptr : d_lse,
                        empty ? none : v.x.data_ptr(), v.ldx, v.w.data_ptr(), v.ldw, empty ? none : v.labels,
                        v.label_bits, ignore, static_cast<const float*>(empty ? none : lse.data_ptr()),
-                       empty ? none : dx.data_ptr(), dw.data_ptr(), f32 ? MX_FP32 : MX_BF16, ws.data_ptr(),
+                       !need_x ? nullptr : empty ? none : dx.data_ptr(), address(dw), f32 ? MX_FP32 : MX_BF16, ws.data_ptr(),
                        static_cast<size_t>(ws.numel()), memory.stream());
   Py_END_ALLOW_THREADS
   if (s != MX_OK) return status_of(s);
@@ -775,7 +798,7 @@ PyMethodDef methods[] = {
     method<route, 6>("route"),
     method<route_backward, 11>("route_backward"),
     method<linear_cross_entropy, 6>("linear_cross_entropy"),
-    method<linear_cross_entropy_backward, 10>("linear_cross_entropy_backward"),
+    method<linear_cross_entropy_backward, 12>("linear_cross_entropy_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1276,7 +1276,7 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
                                            int64_t ignore_index, const float* lse, void* dx,
                                            void* dw, mx_dtype dw_dtype, void* workspace,
                                            size_t workspace_bytes, cudaStream_t stream) {
-  if (!x || !w || !labels || !lse || !dx || !dw) return MX_ERR_INVALID_ARG;
+  if (!x || !w || !labels || !lse || (!dx && !dw)) return MX_ERR_INVALID_ARG;
   if (!valid_dtype(dw_dtype)) return MX_ERR_INVALID_ARG;
   mx_status s = vocab_check(tokens, hidden, vocab, ldx, ldw, label_bits);
   if (s != MX_OK) return s;
@@ -1293,6 +1293,7 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
   if ((s = device_state(&st)) != MX_OK) return s;
   if (!all_on_device(st->device, {w, dw})) return MX_ERR_INVALID_ARG;
   const int64_t dw_elt = dw_f32 ? 4 : 2;
+  if (tokens == 0 && !dw) return MX_OK;
   if (tokens == 0)
     return cudaMemsetAsync(dw, 0, static_cast<size_t>(vocab * hidden * dw_elt), stream) ==
                    cudaSuccess
@@ -1328,24 +1329,27 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
             : mx::launch_vocab_product(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream);
     if (err != cudaSuccess) return MX_ERR_CUDA;
     // dx of the piece: contiguous along the vocabulary times contiguous along hidden
-    p.m = static_cast<int32_t>(few ? hidden : tokens);
-    p.n = static_cast<int32_t>(few ? tokens : hidden);
-    p.k = static_cast<int32_t>(cols);
-    p.steps = v.steps;
-    p.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
-    p.y_fp32 = !v.direct;
-    p.add = col0 > 0;
-    p.out = parts;
-    p.ld_out = hidden;
-    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
-    if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
-    if ((s = encode_output_map(&ty, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
-                               v.splits)) != MX_OK)
-      return s;
-    err = few ? mx::launch_vocab_few(mx::VocabProduct::kDx, p, tb, ta, stream)
-              : mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream);
-    if (err != cudaSuccess) return MX_ERR_CUDA;
+    if (dx) {
+      p.m = static_cast<int32_t>(few ? hidden : tokens);
+      p.n = static_cast<int32_t>(few ? tokens : hidden);
+      p.k = static_cast<int32_t>(cols);
+      p.steps = v.steps;
+      p.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
+      p.y_fp32 = !v.direct;
+      p.add = col0 > 0;
+      p.out = parts;
+      p.ld_out = hidden;
+      if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
+      if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
+      if ((s = encode_output_map(&ty, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
+                                 v.splits)) != MX_OK)
+        return s;
+      err = few ? mx::launch_vocab_few(mx::VocabProduct::kDx, p, tb, ta, stream)
+                : mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream);
+      if (err != cudaSuccess) return MX_ERR_CUDA;
+    }
     // dW of the piece: both operands contiguous along their rows
+    if (!dw) continue;
     p.m = static_cast<int32_t>(cols);
     p.n = static_cast<int32_t>(hidden);
     p.k = static_cast<int32_t>(tokens);
@@ -1361,7 +1365,7 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
         cudaSuccess)
       return MX_ERR_CUDA;
   }
-  if (!v.direct && mx::launch_vocab_join(parts, v.splits, tokens * hidden, dx, st->num_sms,
+  if (dx && !v.direct && mx::launch_vocab_join(parts, v.splits, tokens * hidden, dx, st->num_sms,
                                          stream) != cudaSuccess)
     return MX_ERR_CUDA;
   return MX_OK;

@@ -100,8 +100,9 @@ def test_loss_rejects_bad_arguments_on_the_host(mx):
     back = lambda **kw: mx.mx_linear_cross_entropy_backward(*{**LOSS_BACK, **kw}.values())  # noqa: E731
     for name in ("x", "w", "labels", "loss", "lse", "workspace"):
         assert call(**{name: None}) == 1, name
-    for name in ("x", "w", "labels", "lse", "dx", "dw", "workspace"):
+    for name in ("x", "w", "labels", "lse", "workspace"):
         assert back(**{name: None}) == 1, name
+    assert back(dx=None, dw=None) == 1
     for f in (call, back):
         assert f(tokens=-1) == 1 and f(vocab=0) == 1 and f(hidden=0) == 1 and f(hidden=60) == 1
         assert f(ldx=56) == 1 and f(ldw=56) == 1 and f(label_bits=8) == 1

@@ -99,6 +99,22 @@ def test_gradients_one_by_one(mx, use):
     check_backward(mx, *inputs(100, 64, 700), use=use)
 
 
+@pytest.mark.parametrize("tokens", [20, 300])
+def test_only_one_gradient(mx, tokens):
+    x, w, labels = inputs(tokens, 64, 700)
+    _, lse = mx.linear_cross_entropy(x, w, labels)
+    ones = torch.ones(tokens, device="cuda")
+    dx, dw = mx.linear_cross_entropy_backward(ones, None, x, w, labels, lse)
+    a, none = mx.linear_cross_entropy_backward(ones, None, x, w, labels, lse, need_weight=False)
+    assert none is None and torch.equal(a, dx)
+    none, b = mx.linear_cross_entropy_backward(ones, None, x, w, labels, lse, need_x=False)
+    assert none is None and torch.equal(b, dw)
+    assert mx.linear_cross_entropy_backward(ones, None, x, w, labels, lse, need_x=False,
+                                            need_weight=False) == (None, None)
+    none, b = mx.linear_cross_entropy_backward(None, None, x[:0], w, labels[:0], lse[:0], need_x=False)
+    assert none is None and (b == 0).all()
+
+
 def test_labels(mx):
     x, w, labels = inputs(70, 64, 300, dtype=torch.int32)
     check_backward(mx, x, w, labels)
@@ -230,7 +246,10 @@ def test_autograd(mx):
     dx, dw = mx.linear_cross_entropy_backward(torch.full((90,), 1 / 64, device="cuda"), torch.full((90,), 0.25, device="cuda"),
                                               x, w, labels, lse.detach())
     assert torch.equal(gx, dx) and torch.equal(gw, dw)
-    loss, _ = mx.linear_cross_entropy(a, w, labels)      # one input alone, an expanded gradient
+    loss, _ = mx.linear_cross_entropy(x, b, labels)      # one input alone, an expanded gradient
+    gw, = torch.autograd.grad(loss.sum(), b)
+    assert torch.equal(gw, mx.linear_cross_entropy_backward(torch.ones(90, device="cuda"), None, x, w, labels, lse.detach())[1])
+    loss, _ = mx.linear_cross_entropy(a, w, labels)
     gx, = torch.autograd.grad(loss.sum(), a)
     assert torch.equal(gx, mx.linear_cross_entropy_backward(torch.ones(90, device="cuda"), None, x, w, labels, lse.detach())[0])
 

@@ -14,8 +14,9 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/StorageImpl.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -168,6 +169,21 @@ struct Call {
   }
 };
 
+// A contiguous tensor in new memory of the current device, for the current stream,
+// straight from the caching allocator: through torch's own operator it takes about a
+// microsecond longer, as long as a kernel of a single token.
+at::Tensor fresh(at::IntArrayRef shape, c10::ScalarType type) {
+  int64_t bytes = static_cast<int64_t>(c10::elementSize(type));
+  for (int64_t n : shape) bytes *= n;
+  c10::Allocator* allocator = c10::cuda::CUDACachingAllocator::get();
+  c10::Storage storage(c10::make_intrusive<c10::StorageImpl>(
+      c10::StorageImpl::use_byte_size_t(), bytes, allocator->allocate(static_cast<size_t>(bytes)), allocator, true));
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // The memory that a call takes for itself, on the stream that its kernels run
 // on.  While this stands that stream is the current one, so the allocator hands
 // out memory whose last use is ordered before the kernels, and takes freed
@@ -183,12 +199,12 @@ class Memory {
   }
   cudaStream_t stream() const { return stream_; }
   at::Tensor output(at::IntArrayRef shape, const at::TensorOptions& options) const {
-    const at::Tensor t = at::empty(shape, options);
+    const at::Tensor t = fresh(shape, c10::typeMetaToScalarType(options.dtype()));
     if (stream_ != caller_.stream()) t.record_stream(caller_);
     return t;
   }
   // The caller's workspace, or one of `need` bytes.
-  at::Tensor workspace(int i, size_t need, const at::Tensor& like) const {
+  at::Tensor workspace(int i, size_t need) const {
     if (c_.given(i)) {
       const at::Tensor& t = c_.tensor(i, "workspace");
       if (t.scalar_type() != at::kByte || !c_.here(t) || !t.is_contiguous() ||
@@ -196,7 +212,7 @@ class Memory {
         refuse("workspace", "a contiguous uint8 tensor of at least " + std::to_string(need) + " bytes");
       return t;
     }
-    return at::empty({need < 16 ? 16 : static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
+    return fresh({need < 16 ? 16 : static_cast<int64_t>(need)}, at::kByte);
   }
 
  private:
@@ -329,7 +345,7 @@ PyObject* norm_residual_backward(const Call& c) {
   const float alpha = static_cast<float>(c.real(7)), eps = static_cast<float>(c.real(8));
   const Memory memory(c, 10);
   const size_t need = norm_workspace_fn(rows, cols, w.gates);
-  const at::Tensor ws = memory.workspace(9, need, block);
+  const at::Tensor ws = memory.workspace(9, need);
   const at::TensorOptions f32 = block.options().dtype(at::kFloat);
   const at::Tensor d_block = memory.output({rows, cols}, block.options());
   const at::Tensor d_residual = memory.output({rows, cols}, residual.options());
@@ -402,7 +418,7 @@ PyObject* moe_few_tokens(const Call& c) {
         fits ? moe_workspace_fn(static_cast<int32_t>(tokens), hidden, inter,
                                 static_cast<int32_t>(experts), static_cast<int32_t>(top_k))
              : 0;
-    const at::Tensor ws = memory.workspace(15, need, x);
+    const at::Tensor ws = memory.workspace(15, need);
     mx_status status = MX_ERR_UNSUPPORTED;
     const int32_t renormalize = static_cast<int32_t>(c.integer(13));
     if (fits) {
@@ -531,7 +547,7 @@ PyObject* norm_rotate_backward(const Call& c) {
   const at::Tensor& d_q = c.heads_of(0, "d_q", h.tokens, h.q_heads, h.dim, h.q.scalar_type(), &dq_st, &dq_sh);
   const at::Tensor& d_k = c.heads_of(1, "d_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &dk_st, &dk_sh);
   const Memory memory(c, 12);
-  const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim), h.q);
+  const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim));
   const bool small = h.bytes() <= kSmall;
   Together outputs(memory, 4, (small ? h.bytes() : 0) + 8 * h.dim, h.q);
   const at::Tensor dw_q = outputs.take({h.dim}, at::kFloat), dw_k = outputs.take({h.dim}, at::kFloat);
@@ -585,8 +601,8 @@ PyObject* route(const Call& c) {
   const uint8_t* mask = c.mask_of(3, l.tokens);
   const int32_t renormalize = static_cast<int32_t>(c.integer(2));
   const Memory memory(c, 5);
-  const at::Tensor ws =
-      memory.workspace(4, route_workspace_fn(l.tokens, static_cast<int32_t>(l.experts)), l.z);
+  const size_t need = route_workspace_fn(l.tokens, static_cast<int32_t>(l.experts));
+  const at::Tensor ws = need > 0 || c.given(4) ? memory.workspace(4, need) : at::Tensor();
   const int64_t pairs = l.tokens * l.top_k;
   Together outputs(memory, 7, 4 * (3 * pairs + 2 * l.experts + 2 + l.tokens), l.z);
   const at::Tensor ids = outputs.take({l.tokens, l.top_k}, at::kInt);
@@ -596,7 +612,8 @@ PyObject* route(const Call& c) {
   const at::Tensor offsets = outputs.take({l.experts + 1}, at::kInt);
   const at::Tensor balance = outputs.take({}, at::kFloat);
   const at::Tensor lse = outputs.take({l.tokens}, at::kFloat);
-  void* none = ws.data_ptr();
+  // a tensor without tokens has no address; another one's stands in, unused
+  void* none = counts.data_ptr();
   const bool empty = l.tokens == 0;
   mx_status s;
   Py_BEGIN_ALLOW_THREADS
@@ -606,7 +623,8 @@ PyObject* route(const Call& c) {
                static_cast<float*>(empty ? none : weights.data_ptr()),
                static_cast<float*>(empty ? none : lse.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
                static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(empty ? none : order.data_ptr()),
-               static_cast<float*>(balance.data_ptr()), ws.data_ptr(), static_cast<size_t>(ws.numel()),
+               static_cast<float*>(balance.data_ptr()), address(ws),
+               ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
                memory.stream());
   Py_END_ALLOW_THREADS
   if (s != MX_OK) return status_of(s);
@@ -685,7 +703,7 @@ PyObject* linear_cross_entropy(const Call& c) {
   Together outputs(memory, 2, 8 * v.tokens, v.x);
   const at::Tensor loss = outputs.take({v.tokens}, at::kFloat), lse = outputs.take({v.tokens}, at::kFloat);
   if (v.tokens > 0) {
-    const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
+    const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab));
     mx_status s;
     Py_BEGIN_ALLOW_THREADS
     s = loss_fn(v.tokens, v.hidden, v.vocab, v.x.data_ptr(), v.ldx, v.w.data_ptr(), v.ldw, v.labels,
@@ -709,7 +727,7 @@ PyObject* linear_cross_entropy_backward(const Call& c) {
   const bool need_x = c.integer(8) != 0, need_w = c.integer(9) != 0;
   if (!need_x && !need_w) return tuple_of({at::Tensor(), at::Tensor()});
   const Memory memory(c, 11);
-  const at::Tensor ws = memory.workspace(10, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab), v.x);
+  const at::Tensor ws = memory.workspace(10, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab));
   at::Tensor dx, dw;
   if (need_x) dx = memory.output({v.tokens, v.hidden}, v.x.options());
   if (need_w) dw = memory.output({v.vocab, v.hidden}, v.x.options().dtype(f32 ? at::kFloat : at::kBFloat16));

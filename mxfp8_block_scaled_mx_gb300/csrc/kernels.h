@@ -270,7 +270,7 @@ cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_
 
 // ------------------------------------------------------------------ vocabulary loss
 
-// The products of the vocabulary loss, on one kernel (vocab_loss.cu):
+// The products of the vocabulary loss (vocab_loss.cu):
 //   kStats   z = x W^T; per row and half tile of columns the running maximum
 //            and sum of the softmax, and the label's logit
 //   kGrad    dz = (d_loss + d_lse) exp(z - lse) - d_loss [label] of a piece of the
@@ -303,13 +303,20 @@ struct VocabParams {
   uint64_t wait_limit_ns;
 };
 
-// Boxes of the tensor maps of A and B: 64 elements x 128 rows where the
-// operand is contiguous along the contraction (A of kStats, kGrad, kDx; B of
-// kStats, kGrad), else 64 x 64; of the output (3-D: columns, rows, parts):
-// 128 bytes x 32 rows; all with the 128-byte swizzle.
-cudaError_t launch_vocab_product(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
-                                 const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
-                                 cudaStream_t stream);
+// kStats or kGrad.  Boxes of the tensor maps of A and B: 64 elements x 128 rows; of
+// the output (3-D: columns, rows, parts): 128 bytes x 32 rows; all with the 128-byte
+// swizzle.
+cudaError_t launch_vocab_logits(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
+                                const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
+                                cudaStream_t stream);
+// kDx and kDw of a piece in one launch; either may be absent.  Boxes: A of kDx 64
+// elements x 128 rows, all other operands 64 x 64.
+struct VocabGradient {
+  const VocabParams* p;
+  const CUtensorMap *a, *b, *y;
+};
+cudaError_t launch_vocab_gradients(const VocabGradient* dx, const VocabGradient* dw, int num_sms,
+                                   cudaStream_t stream);
 // kStats, kGrad and kDx for few tokens (vocab_few.cu), with rows of W (kDx: hidden
 // channels) as the m rows of the product and tokens as its columns.  Boxes: A 64
 // elements x 128 rows (kDx 64 x 64), B 64 elements x vocab_few_box(tokens) rows.

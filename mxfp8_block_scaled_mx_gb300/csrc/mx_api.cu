@@ -1145,7 +1145,18 @@ VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
   const int64_t tiles = few ? ceil_div(hidden, 128)
                             : ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
   const int64_t steps = ceil_div(v.cols, 64);
-  const int64_t splits = vocab_splits(tiles, steps, few ? mx::kVocabFewBlocks : 76);
+  int64_t splits = 1;
+  if (few) {
+    splits = vocab_splits(tiles, steps, mx::kVocabFewBlocks);
+  } else {
+    // dW's tiles share the launch and fill what dx leaves: a part of dx only has to
+    // be shorter than a pair of blocks' share of all steps
+    const int64_t dw_steps = ceil_div(v.cols, kVocabTile) * ceil_div(hidden, kVocabTile) *
+                             ceil_div(tokens, 64);
+    const int64_t share = (tiles * steps + dw_steps) / 76;
+    while (splits < 32 && (splits + 1) * 4 <= steps && ceil_div(steps, splits) * 4 > share * 3)
+      ++splits;
+  }
   v.steps = static_cast<int32_t>(ceil_div(steps, splits));
   v.splits = static_cast<int32_t>(ceil_div(steps, v.steps));
   v.direct = !few && v.splits == 1 && v.cols >= vocab;
@@ -1257,7 +1268,7 @@ mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
   p.n = static_cast<int32_t>(few ? tokens : vocab);
   const cudaError_t err =
       few ? mx::launch_vocab_few(mx::VocabProduct::kStats, p, tw, tx, stream)
-          : mx::launch_vocab_product(mx::VocabProduct::kStats, p, tx, tw, tx, st->num_sms, stream);
+          : mx::launch_vocab_logits(mx::VocabProduct::kStats, p, tx, tw, tx, st->num_sms, stream);
   if (err != cudaSuccess || mx::launch_vocab_finish(p, loss, lse, stream) != cudaSuccess)
     return MX_ERR_CUDA;
   return MX_OK;
@@ -1326,43 +1337,48 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
     if ((s = encode_output_map(&ty, dz, false, cols, tokens, v.cols, 1)) != MX_OK) return s;
     cudaError_t err =
         few ? mx::launch_vocab_few(mx::VocabProduct::kGrad, p, tb, ta, stream)
-            : mx::launch_vocab_product(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream);
+            : mx::launch_vocab_logits(mx::VocabProduct::kGrad, p, ta, tb, ty, st->num_sms, stream);
     if (err != cudaSuccess) return MX_ERR_CUDA;
     // dx of the piece: contiguous along the vocabulary times contiguous along hidden
+    mx::VocabParams px = p, pw = p;
+    CUtensorMap xa, xb, xy, wa, wb, wy;
     if (dx) {
-      p.m = static_cast<int32_t>(few ? hidden : tokens);
-      p.n = static_cast<int32_t>(few ? tokens : hidden);
-      p.k = static_cast<int32_t>(cols);
-      p.steps = v.steps;
-      p.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
-      p.y_fp32 = !v.direct;
-      p.add = col0 > 0;
-      p.out = parts;
-      p.ld_out = hidden;
-      if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
-      if ((s = encode_bf16_box(&tb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
-      if ((s = encode_output_map(&ty, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
+      px.m = static_cast<int32_t>(few ? hidden : tokens);
+      px.n = static_cast<int32_t>(few ? tokens : hidden);
+      px.k = static_cast<int32_t>(cols);
+      px.steps = v.steps;
+      px.splits = static_cast<int32_t>(ceil_div(ceil_div(cols, 64), v.steps));
+      px.y_fp32 = !v.direct;
+      px.add = col0 > 0;
+      px.out = parts;
+      px.ld_out = hidden;
+      if ((s = encode_bf16_box(&xa, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
+      if ((s = encode_bf16_box(&xb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
+      if ((s = encode_output_map(&xy, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
                                  v.splits)) != MX_OK)
         return s;
-      err = few ? mx::launch_vocab_few(mx::VocabProduct::kDx, p, tb, ta, stream)
-                : mx::launch_vocab_product(mx::VocabProduct::kDx, p, ta, tb, ty, st->num_sms, stream);
-      if (err != cudaSuccess) return MX_ERR_CUDA;
     }
     // dW of the piece: both operands contiguous along their rows
-    if (!dw) continue;
-    p.m = static_cast<int32_t>(cols);
-    p.n = static_cast<int32_t>(hidden);
-    p.k = static_cast<int32_t>(tokens);
-    p.steps = static_cast<int32_t>(ceil_div(tokens, 64));
-    p.splits = 1;
-    p.y_fp32 = dw_f32;
-    if ((s = encode_bf16_box(&ta, dz, cols, tokens, v.cols, 64)) != MX_OK) return s;
-    if ((s = encode_bf16_box(&tb, x, hidden, tokens, ldx, 64)) != MX_OK) return s;
-    if ((s = encode_output_map(&ty, static_cast<uint8_t*>(dw) + col0 * hidden * dw_elt, dw_f32,
-                               hidden, cols, hidden, 1)) != MX_OK)
-      return s;
-    if (mx::launch_vocab_product(mx::VocabProduct::kDw, p, ta, tb, ty, st->num_sms, stream) !=
-        cudaSuccess)
+    if (dw) {
+      pw.m = static_cast<int32_t>(cols);
+      pw.n = static_cast<int32_t>(hidden);
+      pw.k = static_cast<int32_t>(tokens);
+      pw.steps = static_cast<int32_t>(ceil_div(tokens, 64));
+      pw.splits = 1;
+      pw.y_fp32 = dw_f32;
+      if ((s = encode_bf16_box(&wa, dz, cols, tokens, v.cols, 64)) != MX_OK) return s;
+      if ((s = encode_bf16_box(&wb, x, hidden, tokens, ldx, 64)) != MX_OK) return s;
+      if ((s = encode_output_map(&wy, static_cast<uint8_t*>(dw) + col0 * hidden * dw_elt, dw_f32,
+                                 hidden, cols, hidden, 1)) != MX_OK)
+        return s;
+    }
+    if (dx && few) {
+      if (mx::launch_vocab_few(mx::VocabProduct::kDx, px, xb, xa, stream) != cudaSuccess)
+        return MX_ERR_CUDA;
+    }
+    const mx::VocabGradient gx = {&px, &xa, &xb, &xy}, gw = {&pw, &wa, &wb, &wy};
+    if (mx::launch_vocab_gradients(dx && !few ? &gx : nullptr, dw ? &gw : nullptr, st->num_sms,
+                                   stream) != cudaSuccess)
       return MX_ERR_CUDA;
   }
   if (dx && !v.direct && mx::launch_vocab_join(parts, v.splits, tokens * hidden, dx, st->num_sms,

@@ -10,8 +10,10 @@
 // runs beside the MMAs of the next.  The gradient goes through the vocabulary in
 // pieces: dz of a piece is computed again from x and W, rounded to bf16 (it is
 // an operand of bf16 MMAs; its 8 significant bits are those that x and W have)
-// and read by the two products.  Operands that are contiguous along M or N (dz
-// and x in dW, W in dx) are read as they lie: the tensor core transposes.
+// and read by the two products, which share a launch: where the tiles of one do not
+// fill the device's last round, those of the other do.  Operands that are
+// contiguous along M or N (dz and x in dW, W in dx) are read as they lie: the
+// tensor core transposes.
 //
 //   warp 0 (both blocks)  tensor copies of A and of this block's half of B
 //   warp 1                tensor memory; in block 0 the MMAs of the pair
@@ -56,8 +58,8 @@ struct Unit {
   int32_t m, n, step0, steps, part;
 };
 
-__device__ __forceinline__ Unit unit_of(const VocabParams& p, int32_t u, int32_t m_units,
-                                        int32_t n_tiles) {
+__device__ __forceinline__ Unit unit_of(const VocabParams& p, int32_t u) {
+  const int32_t m_units = (p.m + kTile - 1) / kTile, n_tiles = (p.n + kTile - 1) / kTile;
   Unit t;
   const int32_t tiles = m_units * n_tiles;
   t.part = u / tiles;
@@ -72,13 +74,32 @@ __device__ __forceinline__ Unit unit_of(const VocabParams& p, int32_t u, int32_t
   return t;
 }
 
+__host__ __device__ __forceinline__ int64_t units_of(const VocabParams& p) {
+  return static_cast<int64_t>((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile) * p.splits;
+}
+
+// A product and the maps of its operands and output.
+struct Product {
+  CUtensorMap a, b, y;
+  VocabParams p;
+};
+// What a kernel computes: the logits' product alone, or dx and dW, one after the other
+// (units of the second follow those of the first).
+template <bool GRADIENTS>
+struct Work {
+  Product first, second;
+};
+template <>
+struct Work<false> {
+  Product first;
+};
+
+// W: kStats, kGrad, or kDx for both gradients.
 template <VocabProduct W>
 __global__ void __launch_bounds__(kThreads, 1)
-    vocab_product_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                         const __grid_constant__ CUtensorMap tmap_b,
-                         const __grid_constant__ CUtensorMap tmap_y, const VocabParams p) {
-  constexpr bool kAMn = W == VocabProduct::kDw;
-  constexpr bool kBMn = W == VocabProduct::kDx || W == VocabProduct::kDw;
+    vocab_product_kernel(const __grid_constant__ Work<W == VocabProduct::kDx> work) {
+  constexpr bool kGradients = W == VocabProduct::kDx;
+  const VocabParams& p = work.first.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -111,9 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     *s_abort = 0u;
     fence_mbarrier_init();
-    tma_prefetch_desc(&tmap_a);
-    tma_prefetch_desc(&tmap_b);
-    if (W != VocabProduct::kStats) tma_prefetch_desc(&tmap_y);
+    tma_prefetch_desc(&work.first.a);
+    tma_prefetch_desc(&work.first.b);
   }
   if (warp == 1) {
     __syncwarp();
@@ -127,9 +147,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int32_t m_units = (p.m + kTile - 1) / kTile;
-  const int32_t n_tiles = (p.n + kTile - 1) / kTile;
-  const int32_t units = m_units * n_tiles * p.splits;
+  const int32_t units0 = static_cast<int32_t>(units_of(p));
+  int32_t units = units0;
+  if constexpr (kGradients) units += static_cast<int32_t>(units_of(work.second.p));
+  // the product that a unit belongs to
+  auto second = [&](int32_t u) { return kGradients && u >= units0; };
+  auto product = [&](int32_t u) -> const Product& {
+    if constexpr (kGradients) return u >= units0 ? work.second : work.first;
+    else return work.first;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -138,7 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t issued = 0;
     bool ok = true;
     for (int32_t u = cluster; u < units && ok; u += clusters) {
-      const Unit t = unit_of(p, u, m_units, n_tiles);
+      const Product& w = product(u);
+      const bool dw = second(u);
+      const Unit t = unit_of(w.p, dw ? u - units0 : u);
       const int32_t a0 = t.m * kTile + static_cast<int32_t>(rank) * kHalf;
       const int32_t b0 = t.n * kTile + static_cast<int32_t>(rank) * kHalf;
       for (int32_t i = 0; i < t.steps; ++i) {
@@ -152,17 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = full_leader0 + stage * 8u;
           uint8_t* a = sA + stage * kOperandBytes;
           uint8_t* b = sB + stage * kOperandBytes;
-          if constexpr (kAMn) {
-            tma_load_2d_pair(a, &tmap_a, bar, a0, k0);
-            tma_load_2d_pair(a + kOperandBytes / 2, &tmap_a, bar, a0 + 64, k0);
+          if (dw) {
+            tma_load_2d_pair(a, &w.a, bar, a0, k0);
+            tma_load_2d_pair(a + kOperandBytes / 2, &w.a, bar, a0 + 64, k0);
           } else {
-            tma_load_2d_pair(a, &tmap_a, bar, k0, a0);
+            tma_load_2d_pair(a, &w.a, bar, k0, a0);
           }
-          if constexpr (kBMn) {
-            tma_load_2d_pair(b, &tmap_b, bar, b0, k0);
-            tma_load_2d_pair(b + kOperandBytes / 2, &tmap_b, bar, b0 + 64, k0);
+          if constexpr (kGradients) {
+            tma_load_2d_pair(b, &w.b, bar, b0, k0);
+            tma_load_2d_pair(b + kOperandBytes / 2, &w.b, bar, b0 + 64, k0);
           } else {
-            tma_load_2d_pair(b, &tmap_b, bar, k0, b0);
+            tma_load_2d_pair(b, &w.b, bar, k0, b0);
           }
         }
         __syncwarp();
@@ -188,15 +216,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of 128 bytes, rows follow along K, the next 64 lie 8 KB on; 16 elements of K on
     // are 2 KB.
     constexpr uint32_t kHi = smem_desc_hi(1024, 2);
-    constexpr uint32_t kLboA = kAMn ? kOperandBytes / 2 : 16, kLboB = kBMn ? kOperandBytes / 2 : 16;
-    constexpr uint32_t kNextA = (kAMn ? 2048 : 32) >> 4, kNextB = (kBMn ? 2048 : 32) >> 4;
-    constexpr uint32_t kIdesc = bf16_idesc(kTile, kTile, kAMn, kBMn);
-    const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), kLboA);
-    const uint32_t b_lo0 = smem_desc_lo(smem_u32(sB), kLboB);
+    constexpr uint32_t kMnLbo = kOperandBytes / 2, kMnNext = 2048 >> 4, kKNext = 32 >> 4;
+    constexpr uint32_t kNextB = kGradients ? kMnNext : kKNext;
+    const uint32_t b_lo0 = smem_desc_lo(smem_u32(sB), kGradients ? kMnLbo : 16);
     uint32_t stage = 0, phase = 0, buf = 0, acc_phase = 0;
     bool ok = true;
     for (int32_t u = cluster; u < units && ok; u += clusters) {
-      const Unit t = unit_of(p, u, m_units, n_tiles);
+      const Product& w = product(u);
+      const bool dw = second(u);
+      const Unit t = unit_of(w.p, dw ? u - units0 : u);
+      const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), dw ? kMnLbo : 16);
+      const uint32_t next_a = dw ? kMnNext : kKNext;
+      const uint32_t idesc = bf16_idesc(kTile, kTile, dw, kGradients);
       const Runs runs(t.steps, W == VocabProduct::kStats);
       for (int32_t i0 = 0; i0 < t.steps && ok; i0 += runs.steps) {
         if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns)) {
@@ -217,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (uint32_t j = 0; j < kStep / 16; ++j)
-              tc_mma_pair_f16(acc, a_lo + j * kNextA, kHi, b_lo + j * kNextB, kHi, kIdesc,
+              tc_mma_pair_f16(acc, a_lo + j * next_a, kHi, b_lo + j * kNextB, kHi, idesc,
                               (i > i0 || j > 0) ? 1u : 0u);
             tc_commit_pair_multicast(&empty[stage], kBoth);
           }
@@ -247,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t empty_leader0 = cluster_map(&acc_empty[0], 0);
     uint32_t buf = 0, acc_phase = 0;
     for (int32_t u = cluster; u < units; u += clusters) {
-      const Unit t = unit_of(p, u, m_units, n_tiles);
+      const Product& w = product(u);
+      const bool dw = second(u);
+      const Unit t = unit_of(w.p, dw ? u - units0 : u);
       const int32_t row0 = t.m * kTile + static_cast<int32_t>(rank * kHalf + q * 32);
       const int32_t row = row0 + static_cast<int32_t>(lane);
       const int32_t col0 = t.n * kTile + static_cast<int32_t>(half) * kHalf;
@@ -341,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait()) break;
         tc_fence_after_sync();
         const uint32_t taddr = taddr0 + buf * kTile;
-        const bool f32 = W != VocabProduct::kGrad && p.y_fp32 != 0;
+        const bool f32 = W != VocabProduct::kGrad && w.p.y_fp32 != 0;
         const int32_t rounds = f32 ? 4 : 2;  // of 128 bytes a row
         for (int32_t c = 0; c < rounds; ++c) {
           const int32_t width = f32 ? 32 : 64;
@@ -377,11 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_shared();
           __syncwarp();
           const int32_t col = col0 + c * width;
-          if (lane == 0 && row0 < p.m && col < p.n) {
-            if (W == VocabProduct::kDx && p.add)
-              tma_add_3d(&tmap_y, store, col, row0, t.part);
+          if (lane == 0 && row0 < w.p.m && col < w.p.n) {
+            if (kGradients && w.p.add)
+              tma_add_3d(&w.y, store, col, row0, t.part);
             else
-              tma_store_3d(&tmap_y, store, col, row0, t.part);
+              tma_store_3d(&w.y, store, col, row0, t.part);
             bulk_commit();
           }
         }
@@ -403,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <VocabProduct W>
-cudaError_t launch(const VocabParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
-                   const CUtensorMap& ty, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const Work<W == VocabProduct::kDx>& work, int64_t units, int num_sms,
+                   cudaStream_t stream) {
   auto kern = vocab_product_kernel<W>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -439,11 +472,9 @@ cudaError_t launch(const VocabParams& p, const CUtensorMap& ta, const CUtensorMa
   });
   if (err != cudaSuccess) return err;
   const int max_clusters = clusters.load();
-  const int64_t units = static_cast<int64_t>((p.m + kTile - 1) / kTile) *
-                        ((p.n + kTile - 1) / kTile) * p.splits;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < max_clusters ? units : max_clusters)));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, p);
+  return cudaLaunchKernelEx(&cfg, kern, work);
 }
 
 // One warp per row joins the row's parts.
@@ -493,6 +524,7 @@ __global__ void vocab_join_kernel(const float* __restrict__ parts, int32_t split
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n / 8;
        i += step) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
     for (int32_t s = 0; s < splits; ++s) {
       const float4* src = reinterpret_cast<const float4*>(parts + s * n) + 2 * i;
       const float4 u = src[0], v = src[1];
@@ -506,19 +538,27 @@ __global__ void vocab_join_kernel(const float* __restrict__ parts, int32_t split
 
 }  // namespace
 
-cudaError_t launch_vocab_product(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
-                                 const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
-                                 cudaStream_t stream) {
-  switch (which) {
-    case VocabProduct::kStats:
-      return launch<VocabProduct::kStats>(p, tmap_a, tmap_b, tmap_y, num_sms, stream);
-    case VocabProduct::kGrad:
-      return launch<VocabProduct::kGrad>(p, tmap_a, tmap_b, tmap_y, num_sms, stream);
-    case VocabProduct::kDx:
-      return launch<VocabProduct::kDx>(p, tmap_a, tmap_b, tmap_y, num_sms, stream);
-    default:
-      return launch<VocabProduct::kDw>(p, tmap_a, tmap_b, tmap_y, num_sms, stream);
-  }
+cudaError_t launch_vocab_logits(VocabProduct which, const VocabParams& p, const CUtensorMap& tmap_a,
+                                const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
+                                cudaStream_t stream) {
+  const Work<false> work = {{tmap_a, tmap_b, tmap_y, p}};
+  return which == VocabProduct::kStats
+             ? launch<VocabProduct::kStats>(work, units_of(p), num_sms, stream)
+             : launch<VocabProduct::kGrad>(work, units_of(p), num_sms, stream);
+}
+
+cudaError_t launch_vocab_gradients(const VocabGradient* dx, const VocabGradient* dw, int num_sms,
+                                   cudaStream_t stream) {
+  if (!dx && !dw) return cudaSuccess;
+  Work<true> work;
+  const VocabGradient& any = dx ? *dx : *dw;
+  work.first = {*any.a, *any.b, *any.y, *any.p};
+  work.second = work.first;
+  if (!dx) work.first.p.m = 0;  // (no units)
+  if (!dw) work.second.p.m = 0;
+  if (dx && dw) work.second = {*dw->a, *dw->b, *dw->y, *dw->p};
+  return launch<VocabProduct::kDx>(work, units_of(work.first.p) + units_of(work.second.p), num_sms,
+                                   stream);
 }
 
 cudaError_t launch_vocab_finish(const VocabParams& p, float* loss, float* lse,

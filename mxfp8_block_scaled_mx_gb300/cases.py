@@ -123,6 +123,8 @@ def main(argv=None):
                     help="moe_few, block: format of the expert weights")
     ap.add_argument("--heads", type=int, default=40, help="rotate: a fifth of them keys")
     ap.add_argument("--dim", type=int, default=128, help="rotate: channels of a head")
+    ap.add_argument("--rotary", type=int, default=0, help="rotate: channels rotated (0: all)")
+    ap.add_argument("--interleaved", action="store_true", help="rotate: adjacent pairs")
     ap.add_argument("--vocab", type=int, default=131072)
     ap.add_argument("--gates", type=int, default=0, help="norm, norm_backward: rows of the gate")
     ap.add_argument("--out", default="bf16", choices=["bf16", "fp32"])
@@ -221,7 +223,7 @@ def main(argv=None):
                        for s, std in ((51, 1.5), (52, 1e-3)))
         w_q, w_k = (W.synth_matrix((a.dim,), 0.1, seed=s, device=dev) + 1 for s in (53, 54))
         args = (rows[:, keys:], rows[:, :keys], w_q, w_k, torch.arange(a.tokens, device=dev),
-                mx.rotary_frequencies(a.dim, device=dev))
+                mx.rotary_frequencies(a.rotary or a.dim, device=dev), a.interleaved)
         if a.case == "rotate":
             fn = lambda: mx.norm_rotate(*args)  # noqa: E731
         else:

@@ -1106,9 +1106,7 @@ mx_status vocab_check(int64_t tokens, int64_t hidden, int64_t vocab, int64_t ldx
   return MX_OK;
 }
 
-// How the gradient goes through the vocabulary: columns of a piece (whole
-// tiles), and the parts over which dx sums each piece.  Few tokens have kernels of
-// their own, with a tile's rows along hidden.
+// Few tokens have kernels of their own (vocab_few.cu).
 bool vocab_few(int64_t tokens) { return tokens <= mx::kVocabFewTokens; }
 
 // Parts of a contraction of `steps` steps, four at least a part, for `tiles` tiles on
@@ -1127,6 +1125,8 @@ int64_t vocab_splits(int64_t tiles, int64_t steps, int64_t places) {
   return best;
 }
 
+// How the gradient goes through the vocabulary: columns of a piece (whole
+// tiles), and the parts over which dx sums each piece.
 struct VocabPieces {
   int64_t cols;
   int32_t splits, steps;

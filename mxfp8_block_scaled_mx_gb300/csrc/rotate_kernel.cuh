@@ -1,8 +1,8 @@
 // rotate_kernel.cuh -- the norms of query and key heads with the rotation by
 // position, in one pass, and their gradient: kernels and their launches, which
 // rotate.cu, rotate_f32.cu, rotate_back.cu and rotate_back_f32.cu instantiate by type
-// and direction (four files, so that they compile side by side).  For every token t and head row x of D
-// channels:
+// and direction (four files, so that they compile side by side).  For every token t
+// and head row x of D channels:
 //
 //   n_c = x_c w_c / sqrt(mean(x^2) + eps)
 //   (y_a, y_b) = (n_a c - n_b s, n_a s + n_b c),  c, s = scale cos, sin(pos_t f_i)
@@ -13,12 +13,24 @@
 //
 // Bound by memory: a row is read once and written once.  A row belongs to a
 // group of lanes, each of which holds both channels of its pairs, so that the
-// only exchange is the sum (the gradient: two sums) over the row.  Angles are
-// shared by a token's heads: a block computes the cosines and sines of its tokens
-// once, in shared memory.  An angle is a product in turns: the frequency becomes
-// a 64-bit fraction of a turn per position, the product with the position keeps
-// its low 64 bits, which are the fraction of a turn -- exact to 2^-64 turns times
-// the position however far that is, in integers.
+// only exchange is the sum (the gradient: two sums) over the row.  Blocks stay on
+// the SMs and go from item to item (some tokens' heads); a row's registers take
+// the next item's row as soon as they are read, so that loads are always on their
+// way.  Arithmetic is FP32, two channels an instruction.  Angles are shared by a
+// token's heads: a block computes the cosines and sines of its next tokens in shared
+// memory beside the rows of these.
+// Measured on one GB300 (part of the measured copy bandwidth, 6.78 TB/s): 16384
+// tokens x 40 heads of 128, bf16: 53 us, 0.93; gradient 97 us, 0.77 (59 % of issue
+// slots busy at 16 warps an SM: the registers of five values a channel); one token
+// 2.7 us in a graph, 5.3 called.  Half of the channels rotated: 55 and 112 us; 40
+// heads of 80 (lanes without channels) 60 and 141; 52 of 128 channels rotated (not
+// a multiple of 8: single channels, twice the lanes and four times the accesses) 121
+// and 186.
+//
+// An angle is a product in turns: the frequency becomes a 64-bit fraction of a turn
+// per position, the product with the position keeps its low 64 bits, which are the
+// fraction of a turn -- exact to 2^-64 turns times the position however far that is,
+// in integers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -83,12 +95,14 @@ __device__ __forceinline__ float weight_of(const void* w, int32_t f32, int32_t i
 // A slot is two chunks of C channels, at a and b, whose values a lane holds as
 // pairs of floats: with C = 4 the first channels of four pairs, then their
 // second ones; with C = 1 a pair (b may be missing at the end of an odd row).
-// WHOLE: the row is 8 LPR S channels, all rotated, so every slot has its channels
-// and their distances are constants.
-template <int C_, int LPR_, int S_, bool INTER_, bool WHOLE_>
+// How much of it is known when compiled: in a full row (2 C LPR S channels) every slot
+// has its channels, in a whole one all of them are rotated too, so that their
+// distances are constants.
+enum Rows { kAny, kFull, kWhole };
+template <int C_, int LPR_, int S_, bool INTER_, Rows ROWS>
 struct Lane {
   static constexpr int C = C_, LPR = LPR_, S = S_;
-  static constexpr bool INTER = INTER_, WHOLE = WHOLE_;
+  static constexpr bool INTER = INTER_, WHOLE = ROWS == kWhole, FULL = ROWS != kAny;
   static constexpr int kHalves = C == 4 ? 4 : 1;  // float2 of a slot
   static constexpr int kHalf = C * LPR * S;       // pairs of a whole row
   int32_t first;         // WHOLE: first pair
@@ -107,8 +121,8 @@ struct Lane {
         } else {
           at_a[s] = p.rotary + 2 * C * (g - turned);
           at_b[s] = at_a[s] + C;
-          if (at_a[s] >= p.dim) at_a[s] = -1;
-          if (at_b[s] >= p.dim) at_b[s] = -1;
+          if (!FULL && at_a[s] >= p.dim) at_a[s] = -1;
+          if (!FULL && at_b[s] >= p.dim) at_b[s] = -1;
         }
       }
     }
@@ -122,8 +136,8 @@ struct Lane {
   __device__ __forceinline__ int32_t b(int s) const {
     return WHOLE ? (INTER ? 2 * pair(s) + C : pair(s) + kHalf) : at_b[s];
   }
-  __device__ __forceinline__ bool has_a(int s) const { return WHOLE || at_a[s] >= 0; }
-  __device__ __forceinline__ bool has_b(int s) const { return WHOLE || at_b[s] >= 0; }
+  __device__ __forceinline__ bool has_a(int s) const { return FULL || at_a[s] >= 0; }
+  __device__ __forceinline__ bool has_b(int s) const { return FULL || at_b[s] >= 0; }
   __device__ __forceinline__ bool turns(int s) const { return WHOLE || at_pair[s] >= 0; }
   // Channel of value e (0 .. 2 C - 1, in the order held) of slot s, or -1.
   __device__ __forceinline__ int32_t channel(int s, int e) const {
@@ -352,7 +366,7 @@ constexpr int rows_ahead() {
 // Blocks of an SM that the registers are shared out for.
 template <int C, int S, bool BACK>
 constexpr int resident() {
-  return BACK ? (C * S >= 8 || S >= 4 ? 1 : 2) : C == 1 && S >= 4 ? 2 : 3;
+  return BACK ? (C * S >= 8 || S >= 4 ? 1 : 2) : (C == 1 && S >= 4) || C * S > 8 ? 2 : 3;
 }
 
 // The rows of one kind of array: queries' heads and, behind them, keys', with
@@ -680,12 +694,16 @@ cudaError_t launch(RotateParams p, int num_sms, cudaStream_t stream) {
   }
 }
 
-// Rows of which every lane has whole slots are a form of their own.
+// Whole and full rows have forms of their own.
+template <typename T, int LPR, int S, bool INTER, bool BACK>
+cudaError_t full(const RotateParams& p, int num_sms, cudaStream_t stream) {
+  return p.rotary == p.dim ? launch<T, Lane<4, LPR, S, INTER, kWhole>, BACK>(p, num_sms, stream)
+                           : launch<T, Lane<4, LPR, S, INTER, kFull>, BACK>(p, num_sms, stream);
+}
 template <typename T, int LPR, int S, bool INTER, bool BACK>
 cudaError_t chunked(const RotateParams& p, int num_sms, cudaStream_t stream) {
-  if (p.dim == 8 * LPR * S && p.rotary == p.dim)
-    return launch<T, Lane<4, LPR, S, INTER, true>, BACK>(p, num_sms, stream);
-  return launch<T, Lane<4, LPR, S, INTER, false>, BACK>(p, num_sms, stream);
+  return p.dim == 8 * LPR * S ? full<T, LPR, S, INTER, BACK>(p, num_sms, stream)
+                              : launch<T, Lane<4, LPR, S, INTER, kAny>, BACK>(p, num_sms, stream);
 }
 
 // Chunks of four channels where every array allows them, else single ones.  A lane
@@ -698,14 +716,22 @@ cudaError_t by_shape(const RotateParams& p, int num_sms, cudaStream_t stream) {
   if (p.chunks) {
     if (n > 32) return chunked<T, 32, 2, INTER, BACK>(p, num_sms, stream);
     constexpr int S = BACK ? 1 : 2;
+    if constexpr (!BACK) {
+      // heads of 96 and 192 channels fill lanes of three slots (16384 tokens x 40 heads
+      // of 96: 61 -> 48 us)
+      if (n == 12) return full<T, 4, 3, INTER, BACK>(p, num_sms, stream);
+      if (n == 24) return full<T, 8, 3, INTER, BACK>(p, num_sms, stream);
+    }
     if (n > 16) return chunked<T, 32 / S, S, INTER, BACK>(p, num_sms, stream);
     if (n > 8) return chunked<T, 16 / S, S, INTER, BACK>(p, num_sms, stream);
     return chunked<T, 8 / S, S, INTER, BACK>(p, num_sms, stream);
   }
-  if (n <= 32) return launch<T, Lane<1, 32, 1, INTER, false>, BACK>(p, num_sms, stream);
-  if (n <= 64) return launch<T, Lane<1, 32, 2, INTER, false>, BACK>(p, num_sms, stream);
-  if (n <= 128) return launch<T, Lane<1, 32, 4, INTER, false>, BACK>(p, num_sms, stream);
-  return launch<T, Lane<1, 32, 8, INTER, false>, BACK>(p, num_sms, stream);
+  if (n <= 8) return launch<T, Lane<1, 8, 1, INTER, kAny>, BACK>(p, num_sms, stream);
+  if (n <= 16) return launch<T, Lane<1, 16, 1, INTER, kAny>, BACK>(p, num_sms, stream);
+  if (n <= 32) return launch<T, Lane<1, 32, 1, INTER, kAny>, BACK>(p, num_sms, stream);
+  if (n <= 64) return launch<T, Lane<1, 32, 2, INTER, kAny>, BACK>(p, num_sms, stream);
+  if (n <= 128) return launch<T, Lane<1, 32, 4, INTER, kAny>, BACK>(p, num_sms, stream);
+  return launch<T, Lane<1, 32, 8, INTER, kAny>, BACK>(p, num_sms, stream);
 }
 
 template <typename T, bool BACK>

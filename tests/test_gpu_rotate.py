@@ -81,7 +81,10 @@ def check_backward(mx, args, grads, interleaved=False, scale=1.0):
 SHAPES = [(1, 32, 8, 128, 128), (5, 3, 1, 64, 64), (7, 2, 2, 80, 32), (33, 1, 1, 128, 64),
           (9, 4, 2, 192, 192), (3, 5, 3, 256, 128), (6, 2, 1, 512, 256), (4, 2, 1, 50, 50),
           (11, 3, 2, 101, 100), (5, 1, 2, 200, 18), (2, 2, 2, 511, 510), (3, 1, 1, 2, 2),
-          (2, 40, 24, 7, 4), (700, 2, 1, 16, 8)]
+          (2, 40, 24, 7, 4), (700, 2, 1, 16, 8),
+          # full rows in part rotated, lanes of three slots, short single channels
+          (9, 3, 2, 128, 64), (6, 3, 2, 96, 96), (5, 2, 1, 96, 32), (4, 2, 1, 192, 64), (7, 2, 1, 14, 6),
+          (9, 3, 2, 30, 20)]
 
 
 @pytest.mark.parametrize("interleaved", [False, True])

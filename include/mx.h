@@ -65,7 +65,11 @@
  * tiles streamed by TMA); every GEMM runs in one block-pair kernel
  * (tcgen05 cta_group::2, 256x256 output tiles over two SMs).  A norm is one
  * kernel, its gradient two (rows, then the sums over rows); the expert layer
- * for few tokens two (logits, then everything else, one block per SM).  No
+ * for few tokens two (logits, then everything else, one block per SM).  The heads'
+ * norms with rotation are one kernel, their gradient two; routing is one for few
+ * tokens and two for more, its gradient one; the vocabulary loss two (the product
+ * with the softmax's parts, their join), its gradient two for each piece of the
+ * vocabulary (dz, then dx and dw; three for few tokens) and a join.  No
  * environment variable changes what the library does.
  */
 #ifndef MX_H_
@@ -521,7 +525,8 @@ size_t mx_norm_rotate_backward_workspace(int64_t tokens, int64_t dim);
  *    always written (zeros when tokens == 0).  Sums run in a fixed order for given
  *    sizes: the same inputs give the same bits.
  * workspace: device, at least mx_norm_rotate_backward_workspace(tokens, dim)
- *    bytes, 16-byte aligned; needs no set-up, undefined afterwards. */
+ *    bytes, 16-byte aligned; needs no set-up, undefined afterwards, and belongs to
+ *    one call at a time. */
 mx_status mx_norm_rotate_backward(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
                                   int64_t rotary,
                                   const void* d_q, int64_t dq_st, int64_t dq_sh,
@@ -565,7 +570,8 @@ size_t mx_route_workspace(int64_t tokens, int32_t experts);
  *    top_k <= min(experts, 32), tokens <= 4194303 (more is MX_ERR_UNSUPPORTED);
  *    tokens == 0 writes zeros to counts, offsets and balance.
  * workspace: device, at least mx_route_workspace(tokens, experts) bytes, 16-byte
- *    aligned; needs no set-up, undefined afterwards. */
+ *    aligned; needs no set-up, undefined afterwards, and belongs to one call at a
+ *    time. */
 mx_status mx_route(int64_t tokens, int32_t experts, int32_t top_k,
                    const void* logits, int64_t ld, mx_dtype dtype, const uint8_t* mask,
                    int32_t renormalize, int32_t* ids, float* weights, float* lse,
@@ -605,8 +611,9 @@ size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t
  * x, w and workspace on 16 bytes, ldx and ldw multiples of 8; hidden a multiple
  *    of 8; tokens and vocab below 2^24, hidden up to 2^20 (more is
  *    MX_ERR_UNSUPPORTED); tokens == 0 does nothing.
- * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes;
- *    needs no set-up, undefined afterwards. */
+ * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes (16 for
+ *    a token and 256 of the vocabulary); needs no set-up, undefined afterwards, and
+ *    belongs to one call at a time (the gradient's too). */
 mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
                                   const void* x, int64_t ldx, const void* w, int64_t ldw,
                                   const void* labels, int32_t label_bits, int64_t ignore_index,

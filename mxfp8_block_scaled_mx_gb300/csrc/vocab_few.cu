@@ -13,6 +13,11 @@
 // The softmax runs over rows here, so over lanes: a warp's share of z goes through
 // shared memory, token by token, and every lane keeps the running maximum and sum
 // of its tokens over all tiles of the block.  All waits are bounded.
+//
+// Bound by memory.  Measured on one GB300 over 131072 x 4096 weights (1.07 GB, 158 us
+// at the measured copy bandwidth): losses of 1 token 161 us, 0.98, of 64 tokens 160;
+// losses' gradients of 64 tokens 527 us (weights read twice, their gradient written:
+// 475).  The tiles of vocab_loss.cu take 291 us for one token, 175 for 65.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

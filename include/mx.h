@@ -621,7 +621,7 @@ mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Bytes of the workspace of mx_linear_cross_entropy_backward: dz of a piece of the
- * vocabulary (512 MB at most, or 256 columns) and, where dx is summed over
+ * vocabulary (512 MB at most, or 4096 columns) and, where dx is summed over
  * several pieces or parts, FP32 [parts, tokens, hidden].  0 for sizes that it
  * refuses. */
 size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden, int64_t vocab);

@@ -631,7 +631,8 @@ size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden
  *   dx = dz w,  dw = dz^T x
  * piece by piece of the vocabulary, z computed again.  d_loss counts as 0 for a
  * token whose label is ignore_index or outside the vocabulary.  dz is rounded to
- * bf16, as an operand of the two products, which accumulate in FP32.
+ * bf16 (for up to 64 tokens to two bf16 terms, 16 significant bits), as an operand
+ * of the two products, which accumulate in FP32.
  * d_loss, d_lse: device float [tokens], or NULL (zero).
  * lse: device float [tokens], of the forward pass.
  * dx: device bf16 [tokens, hidden] contiguous; dw: device [vocab, hidden]

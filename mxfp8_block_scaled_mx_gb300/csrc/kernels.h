@@ -274,7 +274,7 @@ cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_
 //   kStats   z = x W^T; per row and half tile of columns the running maximum
 //            and sum of the softmax, and the label's logit
 //   kGrad    dz = (d_loss + d_lse) exp(z - lse) - d_loss [label] of a piece of the
-//            vocabulary, bf16
+//            vocabulary, bf16 (few tokens: two terms)
 //   kDx      dx = dz W of the piece, over `splits` parts of its columns
 //   kDw      dW = dz^T x of the piece
 enum class VocabProduct { kStats, kGrad, kDx, kDw };
@@ -297,6 +297,8 @@ struct VocabParams {
   const float* d_lse;      // [tokens] or nullptr
   int32_t y_fp32;          // kDx, kDw: type of the output
   int32_t add;             // kDx: 1 adds to the output (FP32)
+  int32_t low_row;         // kDw of few tokens: first row of dz's low terms (else 0);
+                           // the contraction's second step is theirs, with x again
   void* out;               // few tokens, kGrad, kDx: the output, ld_out elements a row
   int64_t ld_out;
   uint32_t* status;
@@ -320,7 +322,8 @@ cudaError_t launch_vocab_gradients(const VocabGradient* dx, const VocabGradient*
 // kStats, kGrad and kDx for few tokens (vocab_few.cu), with rows of W (kDx: hidden
 // channels) as the m rows of the product and tokens as its columns.  Boxes: A 64
 // elements x 128 rows (kDx 64 x 64), B 64 elements x vocab_few_box(tokens) rows.
-// p.m = vocabulary, columns of the piece, or hidden; slots = 4 vocab_few_blocks.
+// p.m = vocabulary, columns of the piece, or hidden; slots = 4 vocab_few_blocks.  dz
+// has two bf16 terms: rows [0, tokens) the high ones, [tokens, 2 tokens) the low ones.
 constexpr int kVocabFewTokens = 64;
 constexpr int kVocabFewBlocks = 152;  // one an SM
 constexpr int vocab_few_box(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }

@@ -1138,13 +1138,14 @@ struct VocabPieces {
 
 VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
   VocabPieces v;
-  const int64_t most = kVocabPieceBytes / 2 / (tokens > 0 ? tokens : 1) / kVocabTile * kVocabTile;
+  const bool few = vocab_few(tokens);
+  const int64_t row = tokens * (few ? 4 : 2);  // bytes of dz a column (few tokens: two terms)
+  const int64_t most = kVocabPieceBytes / (row > 0 ? row : 1) / kVocabTile * kVocabTile;
   const int64_t all = ceil_div(vocab, kVocabTile) * kVocabTile;
   const int64_t cols = most < kVocabPieceCols ? kVocabPieceCols : most;
   v.cols = cols < all ? cols : all;
   // dx has few tiles where tokens and hidden are small: then parts of the
   // contraction side by side
-  const bool few = vocab_few(tokens);
   const int64_t tiles = few ? ceil_div(hidden, 128)
                             : ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
   const int64_t steps = ceil_div(v.cols, 64);
@@ -1163,7 +1164,7 @@ VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
   v.steps = static_cast<int32_t>(ceil_div(steps, splits));
   v.splits = static_cast<int32_t>(ceil_div(steps, v.steps));
   v.direct = !few && v.splits == 1 && v.cols >= vocab;
-  v.dz_bytes = static_cast<size_t>(tokens * v.cols * 2);
+  v.dz_bytes = static_cast<size_t>(row * v.cols);
   v.dx_bytes = v.direct ? 0 : static_cast<size_t>(tokens * hidden * 4 * v.splits);
   return v;
 }
@@ -1355,7 +1356,8 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
       px.add = col0 > 0;
       px.out = parts;
       px.ld_out = hidden;
-      if ((s = encode_bf16_box(&xa, dz, cols, tokens, v.cols, box)) != MX_OK) return s;
+      if ((s = encode_bf16_box(&xa, dz, cols, few ? 2 * tokens : tokens, v.cols, box)) != MX_OK)
+        return s;
       if ((s = encode_bf16_box(&xb, w_piece, hidden, cols, ldw, 64)) != MX_OK) return s;
       if ((s = encode_output_map(&xy, v.direct ? dx : parts, !v.direct, hidden, tokens, hidden,
                                  v.splits)) != MX_OK)
@@ -1367,9 +1369,15 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
       pw.n = static_cast<int32_t>(hidden);
       pw.k = static_cast<int32_t>(tokens);
       pw.steps = static_cast<int32_t>(ceil_div(tokens, 64));
+      if (few) {
+        pw.low_row = static_cast<int32_t>(tokens);
+        pw.k = 128;
+        pw.steps = 2;
+      }
       pw.splits = 1;
       pw.y_fp32 = dw_f32;
-      if ((s = encode_bf16_box(&wa, dz, cols, tokens, v.cols, 64)) != MX_OK) return s;
+      if ((s = encode_bf16_box(&wa, dz, cols, few ? 2 * tokens : tokens, v.cols, 64)) != MX_OK)
+        return s;
       if ((s = encode_bf16_box(&wb, x, hidden, tokens, ldx, 64)) != MX_OK) return s;
       if ((s = encode_output_map(&wy, static_cast<uint8_t*>(dw) + col0 * hidden * dw_elt, dw_f32,
                                  hidden, cols, hidden, 1)) != MX_OK)

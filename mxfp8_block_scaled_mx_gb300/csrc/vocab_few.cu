@@ -5,8 +5,13 @@
 //   dx^T = W^T dz^T  hidden channels are the rows; W is read as it lies (contiguous
 //                    along the rows of the tile), the tensor core transposes
 //
+// dz is held here as two bf16 terms, high and low (16 significant bits): one rounding
+// of a label's entry would be most of the gradient's error where few tokens share it,
+// and the second term costs MMAs that have nothing else to do.  dx takes both as
+// columns of one tile, dW (vocab_loss.cu) as two steps of its contraction.
+//
 // An MMA then does no work for tokens that are not there, and a stage of the ring
-// holds 16 KB of weights and only 2 to 8 KB of tokens, so that up to 208 KB of weights
+// holds 16 KB of weights and 2 to 16 KB of tokens, so that up to 208 KB of weights
 // are on their way to an SM.  One block per SM:
 //   warp 0       tensor copies          warp 1   tensor memory, MMAs
 //   warps 2..5   epilogue, 32 rows of the tile each
@@ -16,8 +21,8 @@
 //
 // Bound by memory.  Measured on one GB300 over 131072 x 4096 weights (1.07 GB, 158 us
 // at the measured copy bandwidth): losses of 1 token 161 us, 0.98, of 64 tokens 160;
-// losses' gradients of 64 tokens 527 us (weights read twice, their gradient written:
-// 475).  The tiles of vocab_loss.cu take 291 us for one token, 175 for 65.
+// losses' gradients of 64 tokens 517 us (weights read twice, their gradient written:
+// 475; with one term of dz 527).  The tiles of vocab_loss.cu take 291 us for one token, 175 for 65.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,16 +43,17 @@ constexpr int kABytes = kRows * kStep * 2;
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 
+// N columns of a tile: tokens, or (kDx) both terms of dz of half as many.
 template <int N>
 struct Few {
   static constexpr int kBBytes = N * kStep * 2;
-  static constexpr int kStages = N == 16 ? 12 : N == 32 ? 10 : 8;
+  static constexpr int kStages = N == 16 ? 12 : N == 32 ? 10 : N == 64 ? 8 : 6;
   static constexpr int kOffB = kStages * kABytes;
   static constexpr int kOffZ = kOffB + kStages * kBBytes;
   static constexpr int kShare = N < 32 ? N : 32;
   static constexpr int kZBytes = kShare * 33 * 4;  // 32 rows of z of a warp, up to 32 tokens
   static constexpr int kOffRow = kOffZ + kEpiWarps * kZBytes;
-  static constexpr int kOffBar = kOffRow + N * 16;
+  static constexpr int kOffBar = kOffRow + (N < 64 ? N : 64) * 16;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 1024;  // + alignment slack
   static constexpr uint32_t kTmemCols = 2 * N;  // two accumulators
@@ -149,7 +155,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d(a, &tmap_a, &full[stage], k0, row0);
           }
-          tma_load_2d(sB + stage * C::kBBytes, &tmap_b, &full[stage], k0, 0);
+          uint8_t* b = sB + stage * C::kBBytes;
+          tma_load_2d(b, &tmap_b, &full[stage], k0, 0);
+          // the low terms' rows follow the high ones' (what a box takes of them with the
+          // high ones lands in columns that nobody reads)
+          if constexpr (W == VocabProduct::kDx)
+            tma_load_2d(b + C::kBBytes / 2, &tmap_b, &full[stage], k0, p.tokens);
         }
         __syncwarp();
         ++issued;
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const uint32_t q = warp & 3u;  // lanes of tensor memory: rows 32 q .. 32 q + 31 of the tile
     float* z = reinterpret_cast<float*>(smem + C::kOffZ + (warp - 2) * C::kZBytes);
-    constexpr int kOwn = (N + 31) / 32;  // tokens of a lane (kStats)
+    constexpr int kOwn = (N + 31) / 32;  // tokens of a lane
     float top[kOwn], sum[kOwn];
     int64_t label[kOwn];
 #pragma unroll
@@ -257,18 +268,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t part = u / tiles;
       const int32_t row0 = (u - part * tiles) * kRows + static_cast<int32_t>(q * 32);
       const int32_t row = row0 + static_cast<int32_t>(lane);
+      auto wait = [&] {
+        const bool got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
+        return __all_sync(0xffffffffu, got);
+      };
+      auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      };
+      if constexpr (W == VocabProduct::kDx) {
+        // the high and the low terms' sums of 16 tokens at a time
+        if (!wait()) break;
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + buf * N;
+        float* y = static_cast<float*>(p.out) +
+                   (static_cast<int64_t>(part) * p.tokens) * p.ld_out + row;
+#pragma unroll
+        for (int c = 0; c < N / 2; c += 16) {
+          uint32_t high[16], low[16];
+          load_accumulator<16>(taddr + c, high);
+          load_accumulator<16>(taddr + N / 2 + c, low);
+          if (c + 16 == N / 2) release();
+          if (row < p.m) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (c + j >= p.tokens) break;
+              float* at = y + (c + j) * p.ld_out;
+              const float sum = __uint_as_float(high[j]) + __uint_as_float(low[j]);
+              *at = p.add ? *at + sum : sum;
+            }
+          }
+        }
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
+        continue;
+      }
       float v[N];
       const Runs runs(min(p.steps, all_steps - part * p.steps), W == VocabProduct::kStats);
       bool got = true;
       for (int32_t run = 0; run < runs.count; ++run) {
-        got = mbar_wait(&acc_full[buf], acc_phase, s_abort, p.status, p.wait_limit_ns);
-        if (!(got = __all_sync(0xffffffffu, got))) break;
+        if (!(got = wait())) break;
         tc_fence_after_sync();
         uint32_t w[N];
         load_accumulator<N>(tmem_base + ((q * 32u) << 16) + buf * N, w);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        release();
 #pragma unroll
         for (int j = 0; j < N; ++j)
           v[j] = run == 0 ? __uint_as_float(w[j]) : v[j] + __uint_as_float(w[j]);
@@ -302,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-      } else if constexpr (W == VocabProduct::kGrad) {
+      } else {
         __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(p.out) + row;
         if (row < p.m) {
 #pragma unroll
@@ -311,18 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 r = s_row[j];
             float d = r.y * exp2_fast(fmaf(v[j], kLog2e, -r.x));
             if (__float_as_int(r.w) == row) d -= r.z;
-            dz[j * p.ld_out] = __float2bfloat16_rn(d);
-          }
-        }
-      } else {
-        float* y = static_cast<float*>(p.out) +
-                   (static_cast<int64_t>(part) * p.tokens) * p.ld_out + row;
-        if (row < p.m) {
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            if (j >= p.tokens) break;
-            float* at = y + j * p.ld_out;
-            *at = p.add ? *at + v[j] : v[j];
+            const __nv_bfloat16 high = __float2bfloat16_rn(d);
+            dz[j * p.ld_out] = high;
+            dz[(p.tokens + j) * p.ld_out] = __float2bfloat16_rn(d - __bfloat162float(high));
           }
         }
       }
@@ -370,10 +405,11 @@ cudaError_t launch(const VocabParams& p, const CUtensorMap& ta, const CUtensorMa
 template <VocabProduct W>
 cudaError_t by_tokens(const VocabParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
                       int blocks, cudaStream_t stream) {
+  constexpr int kTerms = W == VocabProduct::kDx ? 2 : 1;
   switch (vocab_few_box(p.tokens)) {
-    case 16: return launch<W, 16>(p, ta, tb, blocks, stream);
-    case 32: return launch<W, 32>(p, ta, tb, blocks, stream);
-    default: return launch<W, 64>(p, ta, tb, blocks, stream);
+    case 16: return launch<W, 16 * kTerms>(p, ta, tb, blocks, stream);
+    case 32: return launch<W, 32 * kTerms>(p, ta, tb, blocks, stream);
+    default: return launch<W, 64 * kTerms>(p, ta, tb, blocks, stream);
   }
 }
 

@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const int32_t k0 = (t.step0 + i) * kStep;
+        int32_t k0 = (t.step0 + i) * kStep, kb = k0;
+        if (kGradients && w.p.low_row) k0 = i * w.p.low_row, kb = 0;
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[stage], 4u * kOperandBytes);
           const uint32_t bar = full_leader0 + stage * 8u;
@@ -196,10 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair(a, &w.a, bar, k0, a0);
           }
           if constexpr (kGradients) {
-            tma_load_2d_pair(b, &w.b, bar, b0, k0);
-            tma_load_2d_pair(b + kOperandBytes / 2, &w.b, bar, b0 + 64, k0);
+            tma_load_2d_pair(b, &w.b, bar, b0, kb);
+            tma_load_2d_pair(b + kOperandBytes / 2, &w.b, bar, b0 + 64, kb);
           } else {
-            tma_load_2d_pair(b, &w.b, bar, k0, b0);
+            tma_load_2d_pair(b, &w.b, bar, kb, b0);
           }
         }
         __syncwarp();

@@ -1148,7 +1148,8 @@ VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
   // contraction side by side
   const int64_t tiles = few ? ceil_div(hidden, 128)
                             : ceil_div(tokens, kVocabTile) * ceil_div(hidden, kVocabTile);
-  const int64_t steps = ceil_div(v.cols, 64);
+  // (steps of the first piece: each part has some, so the join reads what was written)
+  const int64_t steps = ceil_div(v.cols < vocab ? v.cols : vocab, 64);
   int64_t splits = 1;
   if (few) {
     splits = vocab_splits(tiles, steps, mx::kVocabFewBlocks);

@@ -220,6 +220,20 @@ def test_same_bits_again_and_a_workspace(mx):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+# vocabularies whose last 256 columns end before the last part of dx begins, with few
+# tokens and with many
+ENDS = [(16, 8, 2817), (5, 264, 1537), (64, 1000, 5377), (65, 1000, 5633), (300, 520, 3329), (777, 520, 1793)]
+
+
+@pytest.mark.parametrize("shape", SHAPES + ENDS, ids=str)
+def test_nothing_is_read_from_a_workspace_that_was_not_written(mx, shape):
+    """A workspace full of NaN."""
+    x, w, labels = inputs(*shape, seed=3)
+    dirty = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    check(mx, x, w, labels, workspace=dirty(mx.mx_linear_cross_entropy_workspace(*shape)))
+    check_backward(mx, x, w, labels, workspace=dirty(mx.mx_linear_cross_entropy_backward_workspace(*shape)))
+
+
 def test_refusals(mx):
     x, w, labels = inputs(20, 64, 100)
     lse = torch.zeros(20, device="cuda")

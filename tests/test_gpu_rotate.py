@@ -179,6 +179,16 @@ def test_without_tokens(mx):
     assert d.q.shape == (0, 2, 64) and (d.w_q == 0).all() and (d.w_k == 0).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 5, 153, 777, 5000])
+@pytest.mark.parametrize("dim,rotary", [(80, 32), (128, 128), (256, 64), (34, 34)])
+def test_nothing_is_read_from_a_workspace_that_was_not_written(mx, tokens, dim, rotary):
+    args, grads = inputs(tokens, 3, 1, dim, rotary, BF16, FP32)
+    need = mx.mx_norm_rotate_backward_workspace(tokens, dim)
+    a, b = (mx.norm_rotate_backward(*grads, *args, workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+            for fill in (0, 255))
+    assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
+
+
 def test_same_bits_again_and_a_workspace(mx):
     args, grads = inputs(3000, 4, 2, 128, 128, BF16, BF16)
     a = mx.norm_rotate_backward(*grads, *args)

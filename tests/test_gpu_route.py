@@ -161,6 +161,16 @@ def test_same_bits_again_and_a_workspace(mx):
             mx.route(z, 8, workspace=ws[:-1])
 
 
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 1, 1), (1, 128, 8), (33, 20, 3), (1025, 7, 7), (4097, 20, 3),
+                                                  (16384, 33, 4), (16385, 512, 8), (40001, 64, 8)])
+def test_nothing_is_read_from_a_workspace_that_was_not_written(mx, tokens, experts, top_k):
+    z = logits(tokens, experts, FP32)
+    need = mx.mx_route_workspace(tokens, experts)
+    a, b = (mx.route(z, top_k, workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+            for fill in (0, 255))
+    assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
+
+
 def test_refusals(mx):
     z = logits(10, 8, FP32)
     r = mx.route(z, 2)

@@ -252,6 +252,7 @@ struct RouteParams {
   float* balance;            // [1]
   int32_t* workspace;
   int32_t blocks, tokens_per_block, vec_ids;  // set by the launch
+  int32_t group;             // blocks whose pairs a block of the second kernel places
   // gradient
   const float* d_weights;    // [tokens, top_k] or nullptr
   const float* d_balance;    // [1] or nullptr

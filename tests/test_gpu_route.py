@@ -143,6 +143,11 @@ def test_strided_logits(mx):
                 check_backward(mx, z, 4)
 
 
+@pytest.mark.parametrize("tokens,experts,top_k", [(80000, 512, 2), (200000, 64, 8), (300000, 130, 1), (120000, 33, 32)])
+def test_more_tokens_of_a_block_than_it_places_at_a_time(mx, tokens, experts, top_k):
+    check(mx, logits(tokens, experts, FP32), top_k)
+
+
 def test_without_tokens(mx):
     z = torch.zeros(0, 8, device="cuda")
     r = mx.route(z, 2)

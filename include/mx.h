@@ -584,8 +584,8 @@ mx_status mx_route(int64_t tokens, int32_t experts, int32_t top_k,
  * d_weights: device float [tokens, top_k] or NULL (zero); d_balance: device float
  *    [1] or NULL; d_lse: device float [tokens] or NULL.
  * logits, mask, renormalize: those of the forward pass; ids, weights, lse,
- *    counts: what it wrote (an id outside [0, experts) is passed over).  d_logits: device [tokens, experts] contiguous, of
- *    dtype, rounded once. */
+ *    counts: what it wrote (an id outside [0, experts) is passed over).
+ * d_logits: device [tokens, experts] contiguous, of dtype, rounded once. */
 mx_status mx_route_backward(int64_t tokens, int32_t experts, int32_t top_k,
                             const float* d_weights, const float* d_balance, const float* d_lse,
                             const void* logits, int64_t ld, mx_dtype dtype, const uint8_t* mask,
@@ -632,7 +632,9 @@ size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden
  * piece by piece of the vocabulary, z computed again.  d_loss counts as 0 for a
  * token whose label is ignore_index or outside the vocabulary.  dz is rounded to
  * bf16 (for up to 64 tokens to two bf16 terms, 16 significant bits), as an operand
- * of the two products, which accumulate in FP32.
+ * of the two products, which accumulate in FP32.  Every row of x takes part in dw,
+ * with zeros of dz too: a NaN or an infinity in the row of a token that does not
+ * count reaches dw (rows of padding have to be finite).
  * d_loss, d_lse: device float [tokens], or NULL (zero).
  * lse: device float [tokens], of the forward pass.
  * dx: device bf16 [tokens, hidden] contiguous; dw: device [vocab, hidden]

@@ -21,10 +21,10 @@
 // does all of it in one launch.  The gradient is one kernel, with a group of lanes a token.
 //
 // 65536 tokens over 64 experts, top 8, FP32 (one GB300; 42 MB in all, 6.2 us of copy
-// bandwidth): 17.8 us forward, most of it the first kernel, whose loads come before its
+// bandwidth): 16.9 us forward, most of it the first kernel, whose loads come before its
 // instructions (14 warps an SM, one round; two lanes a token and 28 warps: 21.6 against
 // 20.8), then the second's chain of latencies (with lanes matched by expert and two
-// blocks an SM in both kernels 27); 10.6 us the gradient, bound by instructions (63 % of
+// blocks an SM in both kernels 27; 1048576 tokens 179); 10.6 us the gradient, bound by instructions (63 % of
 // issue slots busy).  One token: 4.4 us in a graph, 7 called.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,6 +33,7 @@
 
 #include "epilogue.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "softmax.cuh"
 
@@ -48,7 +49,9 @@ constexpr int kBackThreads = 256;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxBlocks = 304;
-constexpr int kTileBlocks = 152;  // of route_tile_kernel: one an SM
+// of route_tile_kernel: one an SM, less one for the second kernel's last block (68096
+// tokens, 152 blocks and one more: 22.1 us against 18.2)
+constexpr int kTileBlocks = 151;
 constexpr int kMasks = 4096;      // words of 32 tokens' choices
 constexpr int kOneBlock = 64;
 // Tokens from which on (also 128 an expert), and experts and winners up to which, a token
@@ -402,7 +405,7 @@ template <typename T, int EIGHTS>
 __global__ void __launch_bounds__(kTileWarps * 32) route_tile_kernel(const RouteParams r) {
   extern __shared__ float tiles[];
   __shared__ int32_t pairs[kTileExperts], counted[kTileExperts], tokens;
-  __shared__ float factor[kTileWarps][32];
+  __shared__ __align__(16) float factor[kTileWarps][32];
   const int32_t warp = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
   const int32_t row_size = (r.experts + 7) / 8 * 8 + 1;
   float* tile = tiles + warp * 32 * row_size;
@@ -496,14 +499,24 @@ __global__ void __launch_bounds__(kTileWarps * 32) route_tile_kernel(const Route
 #pragma unroll
       for (int j = 0; j < kTileTopK; ++j)
         if (j < r.top_k) mine[id[j]] = w[j];
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int32_t e = 0; e < r.experts; ++e) {
-        const float p = exp_below(mine[e] - top);
-        mine[e] = p;
-        s4[e & 3] += p;
+      // exponentials two at a time, as exp_below has them
+      float2 s2[2] = {both(0.f), both(0.f)};
+      const int32_t whole = r.experts & ~3;
+#pragma unroll 4
+      for (int32_t e = 0; e < whole; e += 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float2 p = make_float2(mine[e + 2 * i], mine[e + 2 * i + 1]);
+          p = mul2(add2(p, both(-top)), both(kLog2e));
+          p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
+          mine[e + 2 * i] = p.x;
+          mine[e + 2 * i + 1] = p.y;
+          s2[i] = add2(s2[i], p);
+        }
       }
-      const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]), inv = 1.f / sum;
+      float sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+      for (int32_t e = whole; e < r.experts; ++e) sum += mine[e] = exp_below(mine[e] - top);
+      const float inv = 1.f / sum;
       r.lse[t] = top + logf(sum);
       float picked = 0.f;
 #pragma unroll
@@ -537,13 +550,22 @@ __global__ void __launch_bounds__(kTileWarps * 32) route_tile_kernel(const Route
     const uint32_t count = __ballot_sync(0xffffffffu, valid);
     if (lane == 0) atomicAdd(&tokens, __popc(count));
     __syncwarp();
-    for (uint32_t left = count; left; left &= left - 1) {
-      const int32_t row = __ffs(left) - 1;
-      const float f = factor[warp][row];
+    auto add = [&](int32_t row, float f) {
 #pragma unroll
       for (int i = 0; i < EIGHTS / 4; ++i)
         if (i * 32 + lane < r.experts)
           acc[i] = fmaf(tile[row * row_size + i * 32 + lane], f, acc[i]);
+    };
+    if (count == 0xffffffffu) {  // (65536 tokens 17.8 -> 16.9 us, with the pairs above)
+      for (int32_t row = 0; row < 32; row += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&factor[warp][row]);
+        add(row, f.x), add(row + 1, f.y), add(row + 2, f.z), add(row + 3, f.w);
+      }
+    } else {
+      for (uint32_t left = count; left; left &= left - 1) {
+        const int32_t row = __ffs(left) - 1;
+        add(row, factor[warp][row]);
+      }
     }
     __syncwarp();
   }

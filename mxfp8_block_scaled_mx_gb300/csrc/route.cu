@@ -24,8 +24,8 @@
 // bandwidth): 16.9 us forward, most of it the first kernel, whose loads come before its
 // instructions (14 warps an SM, one round; two lanes a token and 28 warps: 21.6 against
 // 20.8), then the second's chain of latencies (with lanes matched by expert and two
-// blocks an SM in both kernels 27; 1048576 tokens 179); 10.6 us the gradient, bound by instructions (63 % of
-// issue slots busy).  One token: 4.4 us in a graph, 7 called.
+// blocks an SM in both kernels 27; 1048576 tokens 179); 10.4 us the gradient, bound by
+// instructions.  One token: 4.4 us in a graph, 6.6 called.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -852,22 +852,27 @@ cudaError_t forward(const RouteParams& r, cudaStream_t stream) {
 template <typename T, int L, int V>
 cudaError_t backward(const RouteParams& r, int num_sms, cudaStream_t stream) {
   constexpr int kTokens = kBackThreads / L;  // of a block at a time
+  // Blocks an SM: as many as run side by side where a row takes less than a warp (65536
+  // tokens over 64 experts 10.4 us, with 8 blocks 11.4; 262144 34.5 and 38), else more
+  // (256 experts 31 us with 8, 35 with 3).
+  constexpr int kBlocks = L == 32 ? 8 : V == 8 ? 3 : 6;
   const int64_t need = (static_cast<int64_t>(r.tokens) + kTokens - 1) / kTokens;
   return launch_pdl(route_backward_kernel<T, L, V>,
-                    static_cast<int>(need < 8 * num_sms ? need : 8 * num_sms), kBackThreads, r,
-                    stream);
+                    static_cast<int>(need < kBlocks * num_sms ? need : kBlocks * num_sms),
+                    kBackThreads, r, stream);
 }
 
-// Logits of a lane: a token has a warp forward, and in the gradient as many lanes
-// as give each four.
+// Logits of a lane: a token has a warp forward, and in the gradient as many lanes as
+// give each eight, or four for few experts, up to a warp (262144 tokens over 64 experts
+// with eight 37.8 us, with four 42.4; 65536 over 256 with sixteen 43, with eight 31).
 template <typename T>
 cudaError_t by_experts(const RouteParams& r, bool back, int num_sms, cudaStream_t stream) {
   if (r.experts <= 32)
     return back ? backward<T, 8, 4>(r, num_sms, stream) : forward<T, 1>(r, stream);
   if (r.experts <= 64)
-    return back ? backward<T, 16, 4>(r, num_sms, stream) : forward<T, 2>(r, stream);
+    return back ? backward<T, 8, 8>(r, num_sms, stream) : forward<T, 2>(r, stream);
   if (r.experts <= 128)
-    return back ? backward<T, 32, 4>(r, num_sms, stream) : forward<T, 4>(r, stream);
+    return back ? backward<T, 16, 8>(r, num_sms, stream) : forward<T, 4>(r, stream);
   if (r.experts <= 256)
     return back ? backward<T, 32, 8>(r, num_sms, stream) : forward<T, 8>(r, stream);
   return back ? backward<T, 32, 16>(r, num_sms, stream) : forward<T, 16>(r, stream);

@@ -920,9 +920,11 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     experts * sum_e (share of the pairs at e) * (mean probability of e).  mask:
     bool or uint8 [tokens]; a token that it leaves out is routed, but adds
     nothing to counts and balance.  Differentiable in weights, balance and lse:
-    where autograd records, the backward pass is route_backward.  workspace:
-    uint8, mx_route_workspace(tokens, experts) bytes, one call at a time;
-    allocated here when None."""
+    where autograd records, the backward pass is route_backward, which reads ids,
+    weights, counts and lse (change copies of these before it; offsets, order and
+    balance may be changed in place).  workspace: uint8,
+    mx_route_workspace(tokens, experts) bytes, one call at a time; allocated
+    here when None."""
     raw = None if stream is None else _stream(stream)
     r = _native().route(logits, top_k, renormalize, mask, workspace, raw)
     if r is None:
@@ -936,8 +938,9 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, renormalize, mask, workspace, stream):
         r = route(logits, top_k, renormalize, mask, workspace, stream)
-        ctx.save_for_backward(logits, mask, r.ids, r.weights, r.counts, r.offsets, r.order, r.balance,
-                              r.lse)
+        # (only what the gradient reads: the rest is the caller's to change, as by adding
+        # another layer's balance loss in place)
+        ctx.save_for_backward(logits, mask, r.ids, r.weights, r.counts, r.lse)
         ctx.mark_non_differentiable(r.ids, r.counts, r.offsets, r.order)
         ctx.set_materialize_grads(False)
         ctx.renormalize = renormalize
@@ -948,10 +951,11 @@ class _Route(torch.autograd.Function):
     def backward(ctx, _ids, d_weights, _counts, _offsets, _order, d_balance, d_lse):
         if d_weights is None and d_balance is None and d_lse is None:
             return (None,) * 6
-        logits, mask, *routing = ctx.saved_tensors
+        logits, mask, ids, weights, counts, lse = ctx.saved_tensors
         d_weights, d_balance, d_lse = (None if d is None else d.contiguous()
                                        for d in (d_weights, d_balance, d_lse))
-        return (route_backward(d_weights, d_balance, logits, Routing(*routing), ctx.renormalize, mask,
+        routing = Routing(ids, weights, counts, None, None, None, lse)
+        return (route_backward(d_weights, d_balance, logits, routing, ctx.renormalize, mask,
                                d_lse),) + (None,) * 5
 
 

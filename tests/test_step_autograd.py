@@ -1,0 +1,90 @@
+"""norm_rotate, route and linear_cross_entropy where autograd records: what they
+keep for the backward pass, and what a caller may do with their outputs before
+it.  The built module is replaced by the formulas in float64 on the CPU."""
+import pytest
+import torch
+
+import mxfp8_block_scaled_mx_gb300 as mx
+
+
+def routing(z, top_k, renormalize, mask):
+    """ids, weights, counts, offsets, order, balance, lse."""
+    experts = z.shape[1]
+    p = torch.softmax(z, 1)
+    ids = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top_k]
+    w = p.gather(1, ids)
+    if renormalize:
+        w = w / w.sum(1, keepdim=True)
+    valid = torch.ones(len(z), dtype=torch.bool) if mask is None else mask.bool()
+    n = int(valid.sum())
+    counts = torch.bincount(ids[valid].flatten(), minlength=experts)
+    load = torch.bincount(ids.flatten(), minlength=experts)
+    offsets = torch.cat([load.new_zeros(1), load.cumsum(0)])
+    order = torch.sort(ids.flatten(), stable=True).indices
+    balance = experts * (counts / (n * top_k) * p[valid].mean(0)).sum()
+    return (ids.int(), w, counts.int(), offsets.int(), order.int(), balance, torch.logsumexp(z, 1))
+
+
+class Module:
+    """What the built module does, None where a call is to be recorded among it."""
+
+    def route(self, z, top_k, renormalize, mask, *_):
+        if torch.is_grad_enabled() and z.requires_grad:
+            return None
+        return tuple(t.detach() for t in routing(z, top_k, renormalize, mask))
+
+    def route_backward(self, d_weights, d_balance, d_lse, z, ids, weights, counts, lse, renormalize, mask, _):
+        # what the gradient is computed from has the forward pass's values
+        assert all(torch.is_tensor(t) for t in (ids, weights, counts, lse))
+        with torch.enable_grad():
+            v = z.detach().clone().requires_grad_()
+            r = routing(v, ids.shape[1], renormalize, mask)
+            assert torch.equal(r[0], ids) and torch.equal(r[1], weights) and torch.equal(r[2], counts)
+            total = 0
+            for d, t in ((d_weights, r[1]), (d_balance, r[5]), (d_lse, r[6])):
+                total = total if d is None else total + (d * t).sum()
+            return torch.autograd.grad(total, v)[0]
+
+
+@pytest.fixture
+def module(monkeypatch):
+    m = Module()
+    monkeypatch.setattr(mx, "_native", lambda: m)
+    return m
+
+
+def logits(seed):
+    return torch.randn(7, 5, generator=torch.Generator().manual_seed(seed), dtype=torch.float64).requires_grad_()
+
+
+def test_balance_losses_added_in_place(module):
+    """The balance loss of several layers, summed into the first one's."""
+    layers = [logits(s) for s in range(3)]
+    total = None
+    for z in layers:
+        r = mx.route(z, 2)
+        if total is None:
+            total = r.balance
+        else:
+            total += r.balance
+    got = torch.autograd.grad(total, layers)
+    want = torch.autograd.grad(sum(routing(z, 2, True, None)[5] for z in layers), layers)
+    assert all(torch.allclose(a, b, rtol=1e-12, atol=0) for a, b in zip(got, want))
+
+
+def test_outputs_that_the_gradient_does_not_need_are_the_callers(module):
+    """Offsets and order may be overwritten before the backward pass; what it reads
+    (ids, weights, counts, lse) may not, and says so."""
+    z = logits(4)
+    r = mx.route(z, 2)
+    r.offsets.zero_()
+    r.order.zero_()
+    got, = torch.autograd.grad((r.weights ** 2).sum() + r.balance, z)
+    want, = torch.autograd.grad((routing(z, 2, True, None)[1] ** 2).sum() + routing(z, 2, True, None)[5], z)
+    assert torch.allclose(got, want, rtol=1e-12, atol=1e-15)
+    for name in ("ids", "weights", "counts", "lse"):
+        r = mx.route(z, 2)
+        with torch.no_grad():
+            getattr(r, name).zero_()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            torch.autograd.grad(r.balance, z)

@@ -83,6 +83,13 @@ struct Call {
       if (given(i) && THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
     return false;
   }
+  // Refuses tangents of forward-mode differentiation: a kernel does not carry them
+  // along, and an output without one would stand for a derivative of zero.
+  void refuse_tangents(Py_ssize_t n) const {
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i])._fw_grad(0).defined())
+        throw Refused{"forward-mode derivatives are not computed: no argument may be a dual tensor"};
+  }
   const at::Tensor& tensor(int i, const char* name) const {
     if (!THPVariable_Check(args[i])) throw Refused{std::string(name) + " must be a tensor"};
     return THPVariable_Unpack(args[i]);
@@ -758,7 +765,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
-    return F(Call{args});
+    const Call call{args};
+    call.refuse_tangents(n);
+    return F(call);
   } catch (const Refused& r) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, r.what.c_str());
   } catch (const c10::OutOfMemoryError& e) {

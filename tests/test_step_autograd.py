@@ -1,8 +1,12 @@
 """norm_rotate, route and linear_cross_entropy where autograd records: what they
 keep for the backward pass, and what a caller may do with their outputs before
-it.  The built module is replaced by the formulas in float64 on the CPU."""
+it.  The built module is replaced by the formulas in float64 on the CPU (and is
+itself asked what it refuses before it looks for a device)."""
 import pytest
 import torch
+from torch.autograd import forward_ad
+
+from mxcheck import ensure_built
 
 import mxfp8_block_scaled_mx_gb300 as mx
 
@@ -88,3 +92,41 @@ def test_outputs_that_the_gradient_does_not_need_are_the_callers(module):
             getattr(r, name).zero_()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             torch.autograd.grad(r.balance, z)
+
+
+def test_dual_tensors_are_refused():
+    """A tangent of forward-mode differentiation is not dropped silently, whether
+    backward-mode differentiation is on or off: by no operator of the module, for no argument."""
+    ensure_built()
+    x, w, z = torch.zeros(4, 2, 64), torch.ones(64), torch.zeros(4, 8)
+    pos, f = torch.arange(4), torch.ones(8, dtype=torch.float64)
+    h, v, lse = torch.zeros(4, 64), torch.zeros(9, 64), torch.zeros(4)
+    r = mx.Routing(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.zeros(8, dtype=torch.int32),
+                   None, None, None, lse)
+    e = mx.MxTensor(torch.zeros(9, 64, 64, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8), "e4m3")
+    calls = {
+        "norm_rotate": (mx.norm_rotate, dict(q=x, k=x, w_q=w, w_k=w, positions=pos, frequencies=f),
+                        ("q", "k", "w_q", "w_k", "frequencies")),
+        "norm_rotate_backward": (mx.norm_rotate_backward,
+                                 dict(d_q=x, d_k=x, q=x, k=x, w_q=w, w_k=w, positions=pos, frequencies=f),
+                                 ("d_q", "k")),
+        "route": (mx.route, dict(logits=z, top_k=2), ("logits",)),
+        "route_backward": (mx.route_backward, dict(d_weights=r.weights, d_balance=None, logits=z, routing=r),
+                           ("d_weights", "logits")),
+        "linear_cross_entropy": (mx.linear_cross_entropy, dict(x=h, weight=v, labels=pos), ("x", "weight")),
+        "linear_cross_entropy_backward": (mx.linear_cross_entropy_backward,
+                                          dict(d_loss=lse, d_lse=None, x=h, weight=v, labels=pos, lse=lse),
+                                          ("d_loss", "weight")),
+        "norm_residual": (mx.norm_residual, dict(block=h, residual=h, w_pre=w), ("block", "w_pre")),
+        "moe_few_tokens": (mx.moe_few_tokens, dict(x=h, router=v, gate=e, up=e, down=e, top_k=2), ("x", "router")),
+    }
+    for name, (call, args, duals) in calls.items():
+        for grad in (False, True):
+            for dual in duals:
+                with torch.set_grad_enabled(grad), forward_ad.dual_level():
+                    t = args[dual].detach().requires_grad_(grad)
+                    with pytest.raises(ValueError, match="forward-mode"):
+                        call(**{**args, dual: forward_ad.make_dual(t, torch.ones_like(t))})
+        with pytest.raises(ValueError) as plain:
+            call(**args)
+        assert "forward-mode" not in str(plain.value), name

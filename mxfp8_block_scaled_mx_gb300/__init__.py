@@ -831,9 +831,10 @@ def norm_rotate(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.
     or int64 [tokens]; frequencies: float64 [rotary / 2], radians per position
     (rotary_frequencies).  The first `rotary` channels are rotated, in pairs (i,
     i + rotary / 2), or (2 i, 2 i + 1) where interleaved, and scaled by `scale`.
-    out_q, out_k may be q and k themselves.  Differentiable in q, k, w_q and w_k:
-    where autograd records, the backward pass is norm_rotate_backward, on the
-    stream that autograd runs it on."""
+    out_q, out_k may be q and k themselves, but not where autograd records: the
+    backward pass needs q and k.  Differentiable in q, k, w_q and w_k (frequencies
+    that ask for a gradient are refused): where autograd records, the backward
+    pass is norm_rotate_backward, on the stream that autograd runs it on."""
     raw = None if stream is None else _stream(stream)
     r = _native().norm_rotate(q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, out_q,
                               out_k, raw)

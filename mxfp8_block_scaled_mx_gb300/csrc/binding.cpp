@@ -505,6 +505,7 @@ struct Heads {
 
 // q, k, w_q, w_k, positions, frequencies, interleaved, scale, eps, out_q, out_k, stream
 PyObject* norm_rotate(const Call& c) {
+  if (c.recorded({5})) throw Refused{"frequencies must not ask for a gradient: norm_rotate has none for them"};
   if (c.recorded({0, 1, 2, 3, 9, 10})) Py_RETURN_NONE;
   const Heads h(c, 0);
   int64_t oq_st = h.q_heads * h.dim, oq_sh = h.dim, ok_st = h.k_heads * h.dim, ok_sh = h.dim;

@@ -130,3 +130,17 @@ def test_dual_tensors_are_refused():
         with pytest.raises(ValueError) as plain:
             call(**args)
         assert "forward-mode" not in str(plain.value), name
+
+
+def test_frequencies_that_ask_for_a_gradient_are_refused():
+    """norm_rotate has none for them, and does not give them none silently; where
+    autograd is off they are numbers like any others."""
+    ensure_built()
+    x, w, pos = torch.zeros(4, 2, 64), torch.ones(64), torch.arange(4)
+    f = torch.ones(8, dtype=torch.float64, requires_grad=True)
+    for q in (x, x.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="frequencies"):
+            mx.norm_rotate(q, x, w, w, pos, f)
+    with torch.no_grad(), pytest.raises(ValueError) as plain:
+        mx.norm_rotate(x, x, w, w, pos, f)   # (host tensors)
+    assert "frequencies" not in str(plain.value)

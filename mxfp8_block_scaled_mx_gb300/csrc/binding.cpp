@@ -612,14 +612,21 @@ PyObject* route(const Call& c) {
   const size_t need = route_workspace_fn(l.tokens, static_cast<int32_t>(l.experts));
   const at::Tensor ws = need > 0 || c.given(4) ? memory.workspace(4, need) : at::Tensor();
   const int64_t pairs = l.tokens * l.top_k;
-  Together outputs(memory, 7, 4 * (3 * pairs + 2 * l.experts + 2 + l.tokens), l.z);
-  const at::Tensor ids = outputs.take({l.tokens, l.top_k}, at::kInt);
-  const at::Tensor weights = outputs.take({l.tokens, l.top_k}, at::kFloat);
-  const at::Tensor order = outputs.take({pairs}, at::kInt);
+  // (what is kept of many tokens' routing, a balance loss say, keeps the experts' sums alive
+  // but not the tokens' arrays)
+  const int64_t of_tokens = 4 * (3 * pairs + l.tokens), of_experts = 4 * (2 * l.experts + 2);
+  const bool small = of_tokens + of_experts <= kSmall;
+  Together outputs(memory, 7, of_experts + (small ? of_tokens : 0), l.z);
+  auto take = [&](at::IntArrayRef shape, at::ScalarType type) {
+    return small ? outputs.take(shape, type) : memory.output(shape, l.z.options().dtype(type));
+  };
+  const at::Tensor ids = take({l.tokens, l.top_k}, at::kInt);
+  const at::Tensor weights = take({l.tokens, l.top_k}, at::kFloat);
+  const at::Tensor order = take({pairs}, at::kInt);
+  const at::Tensor lse = take({l.tokens}, at::kFloat);
   const at::Tensor counts = outputs.take({l.experts}, at::kInt);
   const at::Tensor offsets = outputs.take({l.experts + 1}, at::kInt);
   const at::Tensor balance = outputs.take({}, at::kFloat);
-  const at::Tensor lse = outputs.take({l.tokens}, at::kFloat);
   // a tensor without tokens has no address; another one's stands in, unused
   void* none = counts.data_ptr();
   const bool empty = l.tokens == 0;
@@ -708,8 +715,15 @@ PyObject* linear_cross_entropy(const Call& c) {
   const Vocabulary v(c, 0);
   const int64_t ignore = c.integer(3);
   const Memory memory(c, 5);
-  Together outputs(memory, 2, 8 * v.tokens, v.x);
-  const at::Tensor loss = outputs.take({v.tokens}, at::kFloat), lse = outputs.take({v.tokens}, at::kFloat);
+  at::Tensor loss, lse;
+  if (8 * v.tokens <= kSmall) {
+    Together outputs(memory, 2, 8 * v.tokens, v.x);
+    loss = outputs.take({v.tokens}, at::kFloat);
+    lse = outputs.take({v.tokens}, at::kFloat);
+  } else {
+    loss = memory.output({v.tokens}, v.x.options().dtype(at::kFloat));
+    lse = memory.output({v.tokens}, v.x.options().dtype(at::kFloat));
+  }
   if (v.tokens > 0) {
     const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab));
     mx_status s;

@@ -13,9 +13,12 @@
 // loaded.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/StorageImpl.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -176,10 +179,15 @@ struct Call {
   }
 };
 
+// Whether torch's own operator has to make new tensors: a dispatch mode wants to see
+// them, or what they hold at first is to be filled in.
+bool through_torch() { return c10::impl::dispatch_mode_enabled() || at::globalContext().deterministicAlgorithms(); }
+
 // A contiguous tensor in new memory of the current device, for the current stream,
 // straight from the caching allocator: through torch's own operator it takes about a
 // microsecond longer, as long as a kernel of a single token.
 at::Tensor fresh(at::IntArrayRef shape, c10::ScalarType type) {
+  if (through_torch()) return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA));
   int64_t bytes = static_cast<int64_t>(c10::elementSize(type));
   for (int64_t n : shape) bytes *= n;
   c10::Allocator* allocator = c10::cuda::CUDACachingAllocator::get();
@@ -205,8 +213,8 @@ class Memory {
                                 : c10::cuda::getDefaultCUDAStream(c.device));
   }
   cudaStream_t stream() const { return stream_; }
-  at::Tensor output(at::IntArrayRef shape, const at::TensorOptions& options) const {
-    const at::Tensor t = fresh(shape, c10::typeMetaToScalarType(options.dtype()));
+  at::Tensor output(at::IntArrayRef shape, at::ScalarType type) const {
+    const at::Tensor t = fresh(shape, type);
     if (stream_ != caller_.stream()) t.record_stream(caller_);
     return t;
   }
@@ -235,9 +243,11 @@ class Memory {
 constexpr int64_t kSmall = 1 << 20;
 class Together {
  public:
-  Together(const Memory& memory, int64_t tensors, int64_t bytes, const at::Tensor& like)
-      : block_(memory.output({bytes + 16 * tensors}, like.options().dtype(at::kByte))) {}
+  Together(const Memory& memory, int64_t tensors, int64_t bytes) : memory_(memory) {
+    if (!through_torch()) block_ = memory.output({bytes + 16 * tensors}, at::kByte);
+  }
   at::Tensor take(at::IntArrayRef shape, at::ScalarType type) {
+    if (!block_.defined()) return memory_.output(shape, type);
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
         c10::Storage(block_.storage()), block_.key_set(), c10::scalarTypeToTypeMeta(type));
     const int64_t size = static_cast<int64_t>(c10::elementSize(type));
@@ -248,6 +258,7 @@ class Together {
   }
 
  private:
+  const Memory& memory_;
   at::Tensor block_;
   int64_t at_ = 0;
 };
@@ -304,9 +315,9 @@ PyObject* norm_residual(const Call& c) {
   const Memory memory(c, 9);
   const at::Tensor res_out =
       c.given(7) ? c.rows_of(7, "out_residual", rows, cols, residual.scalar_type(), &ldo)
-                 : memory.output({rows, cols}, residual.options());
+                 : memory.output({rows, cols}, residual.scalar_type());
   const at::Tensor y = c.given(8) ? c.rows_of(8, "out", rows, cols, block.scalar_type(), &ldy)
-                                  : memory.output({rows, cols}, block.options());
+                                  : memory.output({rows, cols}, block.scalar_type());
   if (rows > 0) {
     mx_status s;
     Py_BEGIN_ALLOW_THREADS
@@ -353,9 +364,9 @@ PyObject* norm_residual_backward(const Call& c) {
   const Memory memory(c, 10);
   const size_t need = norm_workspace_fn(rows, cols, w.gates);
   const at::Tensor ws = memory.workspace(9, need);
-  const at::TensorOptions f32 = block.options().dtype(at::kFloat);
-  const at::Tensor d_block = memory.output({rows, cols}, block.options());
-  const at::Tensor d_residual = memory.output({rows, cols}, residual.options());
+  constexpr at::ScalarType f32 = at::kFloat;
+  const at::Tensor d_block = memory.output({rows, cols}, block.scalar_type());
+  const at::Tensor d_residual = memory.output({rows, cols}, residual.scalar_type());
   const at::Tensor d_pre = memory.output({cols}, f32);
   at::Tensor d_post, d_gate;
   if (w.post) d_post = memory.output({cols}, f32);
@@ -416,9 +427,9 @@ PyObject* moe_few_tokens(const Call& c) {
     throw Refused{"top_k must be 1 to " + std::to_string(experts) + ", got " + std::to_string(top_k)};
   const Memory memory(c, 16);
   const at::Tensor y = c.given(14) ? c.rows_of(14, "out", tokens, hidden, at::kBFloat16, &ldy)
-                                   : memory.output({tokens, hidden}, x.options());
-  const at::Tensor ids = memory.output({tokens, top_k}, x.options().dtype(at::kInt));
-  const at::Tensor weights = memory.output({tokens, top_k}, x.options().dtype(at::kFloat));
+                                   : memory.output({tokens, hidden}, x.scalar_type());
+  const at::Tensor ids = memory.output({tokens, top_k}, at::kInt);
+  const at::Tensor weights = memory.output({tokens, top_k}, at::kFloat);
   if (tokens > 0) {
     const bool fits = tokens <= INT32_MAX && experts <= INT32_MAX;
     const size_t need =
@@ -516,12 +527,12 @@ PyObject* norm_rotate(const Call& c) {
   if (c.given(10))
     out_k = c.heads_of(10, "out_k", h.tokens, h.k_heads, h.dim, h.q.scalar_type(), &ok_st, &ok_sh);
   if (!c.given(9) && !c.given(10) && h.bytes() <= kSmall) {
-    Together outputs(memory, 2, h.bytes(), h.q);
+    Together outputs(memory, 2, h.bytes());
     out_q = outputs.take({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
     out_k = outputs.take({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
   } else {
-    if (!c.given(9)) out_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
-    if (!c.given(10)) out_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.options());
+    if (!c.given(9)) out_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
+    if (!c.given(10)) out_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
   }
   if (h.tokens > 0) {
     mx_status s;
@@ -557,15 +568,15 @@ PyObject* norm_rotate_backward(const Call& c) {
   const Memory memory(c, 12);
   const at::Tensor ws = memory.workspace(11, rotate_workspace_fn(h.tokens, h.dim));
   const bool small = h.bytes() <= kSmall;
-  Together outputs(memory, 4, (small ? h.bytes() : 0) + 8 * h.dim, h.q);
+  Together outputs(memory, 4, (small ? h.bytes() : 0) + 8 * h.dim);
   const at::Tensor dw_q = outputs.take({h.dim}, at::kFloat), dw_k = outputs.take({h.dim}, at::kFloat);
   at::Tensor dx_q, dx_k;
   if (small) {
     dx_q = outputs.take({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
     dx_k = outputs.take({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
   } else {
-    dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.options());
-    dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.options());
+    dx_q = memory.output({h.tokens, h.q_heads, h.dim}, h.q.scalar_type());
+    dx_k = memory.output({h.tokens, h.k_heads, h.dim}, h.q.scalar_type());
   }
   // a tensor without tokens has no address; the workspace's stands in, unused
   void* none = ws.data_ptr();
@@ -616,9 +627,9 @@ PyObject* route(const Call& c) {
   // but not the tokens' arrays)
   const int64_t of_tokens = 4 * (3 * pairs + l.tokens), of_experts = 4 * (2 * l.experts + 2);
   const bool small = of_tokens + of_experts <= kSmall;
-  Together outputs(memory, 7, of_experts + (small ? of_tokens : 0), l.z);
+  Together outputs(memory, 7, of_experts + (small ? of_tokens : 0));
   auto take = [&](at::IntArrayRef shape, at::ScalarType type) {
-    return small ? outputs.take(shape, type) : memory.output(shape, l.z.options().dtype(type));
+    return small ? outputs.take(shape, type) : memory.output(shape, type);
   };
   const at::Tensor ids = take({l.tokens, l.top_k}, at::kInt);
   const at::Tensor weights = take({l.tokens, l.top_k}, at::kFloat);
@@ -674,7 +685,7 @@ PyObject* route_backward(const Call& c) {
   const uint8_t* mask = c.mask_of(9, tokens);
   const int32_t renormalize = static_cast<int32_t>(c.integer(8));
   const Memory memory(c, 10);
-  const at::Tensor d = memory.output({tokens, experts}, z.options());
+  const at::Tensor d = memory.output({tokens, experts}, z.scalar_type());
   if (tokens > 0) {
     mx_status s;
     Py_BEGIN_ALLOW_THREADS
@@ -717,12 +728,12 @@ PyObject* linear_cross_entropy(const Call& c) {
   const Memory memory(c, 5);
   at::Tensor loss, lse;
   if (8 * v.tokens <= kSmall) {
-    Together outputs(memory, 2, 8 * v.tokens, v.x);
+    Together outputs(memory, 2, 8 * v.tokens);
     loss = outputs.take({v.tokens}, at::kFloat);
     lse = outputs.take({v.tokens}, at::kFloat);
   } else {
-    loss = memory.output({v.tokens}, v.x.options().dtype(at::kFloat));
-    lse = memory.output({v.tokens}, v.x.options().dtype(at::kFloat));
+    loss = memory.output({v.tokens}, at::kFloat);
+    lse = memory.output({v.tokens}, at::kFloat);
   }
   if (v.tokens > 0) {
     const at::Tensor ws = memory.workspace(4, loss_workspace_fn(v.tokens, v.hidden, v.vocab));
@@ -751,8 +762,8 @@ PyObject* linear_cross_entropy_backward(const Call& c) {
   const Memory memory(c, 11);
   const at::Tensor ws = memory.workspace(10, loss_backward_workspace_fn(v.tokens, v.hidden, v.vocab));
   at::Tensor dx, dw;
-  if (need_x) dx = memory.output({v.tokens, v.hidden}, v.x.options());
-  if (need_w) dw = memory.output({v.vocab, v.hidden}, v.x.options().dtype(f32 ? at::kFloat : at::kBFloat16));
+  if (need_x) dx = memory.output({v.tokens, v.hidden}, v.x.scalar_type());
+  if (need_w) dw = memory.output({v.vocab, v.hidden}, f32 ? at::kFloat : at::kBFloat16);
   void* none = ws.data_ptr();
   const bool empty = v.tokens == 0;
   mx_status s;

@@ -1,7 +1,8 @@
 """What a program does around the training step's operators: sums of balance losses in
-place, outputs of which it keeps some."""
+place, outputs of which it keeps some, modes of torch's that watch or fill new tensors."""
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from mxcheck import ensure_built
 
@@ -53,3 +54,58 @@ def test_a_kept_output_keeps_no_large_one(mx):
     # the winners are those of a call whose outputs share one
     z = randn(20000, 32, seed=3)
     assert torch.equal(mx.route(z, 4).ids[:2000], mx.route(z[:2000], 4).ids) and mx.device_status() == 0
+
+
+class Seen(TorchDispatchMode):
+    """The sizes and types that are asked of torch's allocating operator."""
+
+    def __init__(self):
+        super().__init__()
+        self.made = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if func is torch.ops.aten.empty.memory_format:
+            self.made.append((tuple(out.shape), out.dtype))
+        return out
+
+
+def calls_of_every_kind(mx):
+    heads, w = randn(30, 6, 64, seed=1, dtype=BF16), randn(64, seed=2, dtype=BF16)
+    args = (heads[:, :4], heads[:, 4:], w, w, torch.arange(30, device="cuda"), mx.rotary_frequencies(64))
+    z = {n: randn(n, 16, seed=3) for n in (20, 20000)}
+    r = mx.route(z[20], 2)
+    x, v, labels = randn(30, 64, seed=4, dtype=BF16), randn(100, 64, seed=5, dtype=BF16), torch.arange(30, device="cuda")
+    lse = mx.linear_cross_entropy(x, v, labels)[1]
+    return [lambda: mx.norm_rotate(*args), lambda: vars(mx.norm_rotate_backward(*args[:2], *args)).values(),
+            lambda: vars(mx.route(z[20], 2)).values(), lambda: vars(mx.route(z[20000], 2)).values(),
+            lambda: [mx.route_backward(r.weights, None, z[20], r)], lambda: mx.linear_cross_entropy(x, v, labels),
+            lambda: mx.linear_cross_entropy_backward(lse, None, x, v, labels, lse),
+            lambda: mx.norm_residual(x, x, x[0].contiguous()),
+            lambda: [t for t in vars(mx.norm_residual_backward(x, x, x, x, x[0].contiguous())).values() if t is not None]]
+
+
+def test_new_tensors_are_seen_by_dispatch_modes(mx):
+    for call in calls_of_every_kind(mx):
+        want = list(call())
+        with Seen() as seen:
+            got = list(call())
+        for a, b in zip(want, got):
+            assert torch.equal(a, b) and (tuple(b.shape), b.dtype) in seen.made
+
+
+def test_new_tensors_are_filled_where_algorithms_are_deterministic(mx):
+    calls = calls_of_every_kind(mx)
+    want = [list(c()) for c in calls]
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        for call, ref in zip(calls, want):
+            with torch.autograd.profiler.profile() as p:
+                got = list(call())
+            assert all(torch.equal(a, b) for a, b in zip(ref, got))
+            names = [e.name for e in p.function_events]
+            assert names.count("aten::fill_") >= len(got), names
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert mx.device_status() == 0

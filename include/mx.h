@@ -540,7 +540,8 @@ mx_status mx_norm_rotate_backward(int64_t tokens, int64_t q_heads, int64_t k_hea
                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Bytes of the workspace of mx_route; 0 where it needs none (few tokens) and for
- * sizes that it refuses. */
+ * sizes that it refuses.  Does not fall as tokens grow: one for the most tokens of
+ * several calls suffices for each. */
 size_t mx_route_workspace(int64_t tokens, int32_t experts);
 
 /* The experts of every token from the router's logits z, what the grouped
@@ -593,8 +594,10 @@ mx_status mx_route_backward(int64_t tokens, int32_t experts, int32_t top_k,
                             const float* lse, const int32_t* counts, void* d_logits,
                             cudaStream_t stream);
 
-/* Bytes of the workspace of mx_linear_cross_entropy; 0 for sizes that it
- * refuses. */
+/* Bytes of the workspace of mx_linear_cross_entropy: 4 a token and, up to 64
+ * tokens, 32 a token for each 128 of the vocabulary (for 152 times that at most),
+ * above 16 for each 256; 0 for sizes that it refuses.  Does not fall as tokens grow:
+ * one for the most tokens of several calls suffices for each. */
 size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t vocab);
 
 /* Softmax cross entropy over a vocabulary with the product that gives its
@@ -611,9 +614,9 @@ size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t
  * x, w and workspace on 16 bytes, ldx and ldw multiples of 8; hidden a multiple
  *    of 8; tokens and vocab below 2^24, hidden up to 2^20 (more is
  *    MX_ERR_UNSUPPORTED); tokens == 0 does nothing.
- * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes (16 for
- *    a token and 256 of the vocabulary); needs no set-up, undefined afterwards, and
- *    belongs to one call at a time (the gradient's too). */
+ * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes; needs no
+ *    set-up, undefined afterwards, and belongs to one call at a time (the gradient's
+ *    too). */
 mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
                                   const void* x, int64_t ldx, const void* w, int64_t ldw,
                                   const void* labels, int32_t label_bits, int64_t ignore_index,
@@ -621,9 +624,10 @@ mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Bytes of the workspace of mx_linear_cross_entropy_backward: dz of a piece of the
- * vocabulary (512 MB at most, or 4096 columns) and, where dx is summed over
+ * vocabulary (512 MB at most, or 4096 columns) and, for a dx that is summed over
  * several pieces or parts, FP32 [parts, tokens, hidden].  0 for sizes that it
- * refuses. */
+ * refuses.  Does not fall as tokens grow: one for the most tokens of several calls
+ * suffices for each. */
 size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden, int64_t vocab);
 
 /* Gradients of mx_linear_cross_entropy:

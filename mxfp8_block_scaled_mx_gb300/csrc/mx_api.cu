@@ -1095,6 +1095,10 @@ constexpr int64_t kVocabTile = 256;
 // 66.9 ms with the 2048 columns of 512 MB, 65.0 with 4096).
 constexpr int64_t kVocabPieceBytes = int64_t{1} << 29;
 constexpr int64_t kVocabPieceCols = 4096;
+// Bytes of the parts over which dx of more than 64 tokens is summed side by side, at
+// most.  (What the device's places ask for stays below 26 MB at any sizes: it limits
+// none of them, but bounds the workspace.)
+constexpr int64_t kVocabPartBytes = int64_t{32} << 20;
 
 mx_status vocab_check(int64_t tokens, int64_t hidden, int64_t vocab, int64_t ldx, int64_t ldw,
                       int32_t label_bits) {
@@ -1159,7 +1163,8 @@ VocabPieces vocab_pieces(int64_t tokens, int64_t hidden, int64_t vocab) {
     const int64_t dw_steps = ceil_div(v.cols, kVocabTile) * ceil_div(hidden, kVocabTile) *
                              ceil_div(tokens, 64);
     const int64_t share = (tiles * steps + dw_steps) / 76;
-    while (splits < 32 && (splits + 1) * 4 <= steps && ceil_div(steps, splits) * 4 > share * 3)
+    while (splits < 32 && (splits + 1) * 4 <= steps && ceil_div(steps, splits) * 4 > share * 3 &&
+           (splits + 1) * tokens * hidden * 4 <= kVocabPartBytes)
       ++splits;
   }
   v.steps = static_cast<int32_t>(ceil_div(steps, splits));
@@ -1176,9 +1181,30 @@ int64_t vocab_slots(int64_t tokens, int64_t vocab) {
   return vocab_few(tokens) ? 4 * mx::vocab_few_blocks(vocab, 1) : 2 * ceil_div(vocab, kVocabTile);
 }
 
+// Workspaces do not shrink as tokens grow, so that one for the most tokens of a
+// program's calls suffices for all of them, although few tokens take more bytes each.
 size_t vocab_forward_bytes(int64_t tokens, int64_t vocab) {
   // the label's logits (rounded up to 16 bytes), then the parts
-  return static_cast<size_t>(ceil_div(tokens, 4) * 16 + tokens * vocab_slots(tokens, vocab) * 8);
+  auto need = [&](int64_t t) { return ceil_div(t, 4) * 16 + t * vocab_slots(t, vocab) * 8; };
+  const int64_t few = need(mx::kVocabFewTokens), all = need(tokens);
+  return static_cast<size_t>(vocab_few(tokens) || all > few ? all : few);
+}
+
+// No less than dz_bytes + dx_bytes of VocabPieces: dz of the most columns that a piece
+// of `tokens` or fewer has, and dx over the most parts.
+size_t vocab_backward_bytes(int64_t tokens, int64_t hidden, int64_t vocab) {
+  auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
+  auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  auto dz_of = [&](int64_t t) {
+    const int64_t row = t * (vocab_few(t) ? 4 : 2);
+    return least(row * ceil_div(vocab, kVocabTile) * kVocabTile,
+                 most(row * kVocabPieceCols, kVocabPieceBytes));
+  };
+  const int64_t dz = vocab_few(tokens) ? dz_of(tokens) : most(dz_of(tokens), dz_of(mx::kVocabFewTokens));
+  // 32 parts at most, of few tokens any, of more up to kVocabPartBytes; one part as it is
+  const int64_t one = tokens * hidden * 4;
+  const int64_t parts = most(kVocabPartBytes, 32 * mx::kVocabFewTokens * hidden * 4);
+  return static_cast<size_t>(dz + most(one, least(32 * one, parts)));
 }
 
 // 2-D bf16 tensor map, box 64 columns x box_rows, 128-byte swizzle, zero fill.
@@ -1281,8 +1307,7 @@ mx_status mx_linear_cross_entropy(int64_t tokens, int64_t hidden, int64_t vocab,
 
 size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden, int64_t vocab) {
   if (vocab_check(tokens, hidden, vocab, hidden, hidden, 64) != MX_OK) return 0;
-  const VocabPieces v = vocab_pieces(tokens, hidden, vocab);
-  return v.dz_bytes + v.dx_bytes;
+  return vocab_backward_bytes(tokens, hidden, vocab);
 }
 
 mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64_t vocab,
@@ -1297,7 +1322,7 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
   mx_status s = vocab_check(tokens, hidden, vocab, ldx, ldw, label_bits);
   if (s != MX_OK) return s;
   const VocabPieces v = vocab_pieces(tokens, hidden, vocab);
-  const size_t need = v.dz_bytes + v.dx_bytes;
+  const size_t need = vocab_backward_bytes(tokens, hidden, vocab);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MX_ERR_INVALID_ARG;
   const bool dw_f32 = dw_dtype == MX_FP32;
   if (!aligned16(x) || !aligned16(w) || ldx % 8 != 0 || ldw % 8 != 0 || !aligned16(dx) ||

@@ -894,11 +894,13 @@ void split(int64_t tokens, int32_t most, int32_t* blocks, int32_t* per) {
 
 }  // namespace
 
+// For the most blocks that `tokens` or fewer have, in either first kernel (their number
+// itself falls where a block's tokens step up: 304 blocks for 9728, 153 for 9729).
 size_t route_workspace(int64_t tokens, int32_t experts) {
-  int32_t blocks, per;
-  split(tokens, kMaxBlocks, &blocks, &per);
+  if (tokens <= kOneBlock) return 0;
+  const int64_t most = (tokens + 31) / 32, blocks = most < kMaxBlocks ? most : kMaxBlocks;
   const size_t row = (experts + 3) / 4 * 4;
-  return blocks == 1 ? 0 : sizeof(int32_t) * (blocks * row * 3 + blocks);
+  return sizeof(int32_t) * (blocks * row * 3 + blocks);
 }
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {

@@ -158,3 +158,22 @@ def test_frequencies(mx):
                 dict(rotary=8, fast=1.0, slow=1.0)):
         with pytest.raises(ValueError):
             mx.rotary_frequencies(device="cpu", **bad)
+
+
+def test_a_workspace_for_more_tokens_suffices_for_fewer(mx):
+    """Sizes do not fall as tokens grow: around every count where a kernel, its blocks or
+    its pieces change, and over counts of all magnitudes."""
+    counts = sorted({t for b in (1, 16, 32, 64, 128, 256, 1024, 2048, 4096, 4864, 8192, 9728, 16384, 19456, 65536,
+                                 131072, 262144, 1 << 20, (1 << 22) - 64) for t in range(b, b + 34)}
+                    | {int(1.07 ** i) for i in range(1, 220)})
+    for experts in (1, 5, 64, 65, 128, 129, 512):
+        sizes = [mx.mx_route_workspace(t, experts) for t in counts]
+        assert sizes == sorted(sizes) and sizes[-1] > 0, experts
+    for hidden, vocab in ((8, 1), (64, 300), (1000, 1000), (1000, 18433), (2048, 32768), (4096, 131072),
+                          (7168, 131072), (128, 1 << 22), (32768, 5000)):
+        for size in (mx.mx_linear_cross_entropy_workspace, mx.mx_linear_cross_entropy_backward_workspace):
+            sizes = [size(t, hidden, vocab) for t in counts]
+            assert sizes == sorted(sizes) and sizes[0] > 0, (hidden, vocab)
+    # and stay in proportion: dz of one piece and a few MB beside it
+    assert mx.mx_linear_cross_entropy_backward_workspace(2048, 2048, 32768) <= 2 * 2048 * 32768 + (32 << 20)
+    assert mx.mx_linear_cross_entropy_backward_workspace(1, 4096, 131072) <= 2 << 20

@@ -1,5 +1,6 @@
 """What a program does around the training step's operators: sums of balance losses in
-place, outputs of which it keeps some, modes of torch's that watch or fill new tensors."""
+place, outputs of which it keeps some, modes of torch's that watch or fill new tensors, one
+workspace for batches of any size."""
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
@@ -108,4 +109,24 @@ def test_new_tensors_are_filled_where_algorithms_are_deterministic(mx):
             assert names.count("aten::fill_") >= len(got), names
     finally:
         torch.use_deterministic_algorithms(before)
+    assert mx.device_status() == 0
+
+
+def test_one_workspace_for_batches_of_any_size(mx):
+    """A workspace for the largest, full of NaN, gives what a call's own gives."""
+    dirty = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    z = randn(10000, 64, seed=1)
+    ws = dirty(mx.mx_route_workspace(10000, 64))
+    for tokens in (10000, 9729, 9728, 8192, 8191, 300, 64):
+        a, b = mx.route(z[:tokens], 8), mx.route(z[:tokens], 8, workspace=ws)
+        assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values())), tokens
+    x, w, labels = randn(400, 72, seed=2, dtype=BF16), randn(1000, 72, seed=3, dtype=BF16), torch.arange(400, device="cuda")
+    ws = dirty(mx.mx_linear_cross_entropy_workspace(400, 72, 1000))
+    back = dirty(mx.mx_linear_cross_entropy_backward_workspace(400, 72, 1000))
+    for tokens in (400, 65, 64, 33, 1):
+        xs, ls, d = x[:tokens], labels[:tokens], torch.ones(tokens, device="cuda")
+        a, b = mx.linear_cross_entropy(xs, w, ls), mx.linear_cross_entropy(xs, w, ls, workspace=ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), tokens
+        a, b = (mx.linear_cross_entropy_backward(d, None, xs, w, ls, b[1], workspace=s) for s in (None, back))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), tokens
     assert mx.device_status() == 0

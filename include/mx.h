@@ -494,14 +494,14 @@ mx_status mx_moe_few_tokens(int32_t tokens, int64_t hidden, int64_t inter, int32
  * positions: device int32 or int64 [tokens] (position_bits 32 or 64), of any sign.
  * frequencies: device double [rotary / 2], finite, radians per position.  An
  *    angle is taken modulo a turn in 64-bit integers, so that far positions lose
- *    nothing: it is off by at most 2^-64 turns times the position, then rounded to
- *    FP32.
+ *    nothing: it is off by at most 2^-64 turns + 2^-69 of the frequency in turns,
+ *    times the position, then rounded to FP32.
  * Pointers and strides need the alignment of one element only (chunks of four
  *    channels -- dim and rotary multiples of 8, rows on four elements -- are the
  *    fast case);
- * 2 <= rotary <= dim <= 512, rotary even, strides below 2^29, fewer than 2^31
- *    heads in all (more is MX_ERR_UNSUPPORTED), eps >= 0; tokens == 0 does
- *    nothing. */
+ * 2 <= rotary <= dim <= 512, rotary even, strides below 2^29, up to 65536 heads of
+ *    either kind, 2^30 tokens and 2^31 - 1 heads of all tokens (more is
+ *    MX_ERR_UNSUPPORTED), eps >= 0; tokens == 0 does nothing. */
 mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim,
                          int64_t rotary,
                          const void* q, int64_t q_st, int64_t q_sh,
@@ -612,8 +612,9 @@ size_t mx_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64_t
  *    loss NaN and is reported through mx_device_status (MX_ERR_DEVICE_ARG).
  * loss, lse: device float [tokens].
  * x, w and workspace on 16 bytes, ldx and ldw multiples of 8; hidden a multiple
- *    of 8; tokens and vocab below 2^24, hidden up to 2^20 (more is
- *    MX_ERR_UNSUPPORTED); tokens == 0 does nothing.
+ *    of 8; tokens and vocab up to 2^24, hidden up to 2^20, fewer than 2^31 tiles of
+ *    256 tokens x 256 of the vocabulary (more is MX_ERR_UNSUPPORTED); tokens == 0
+ *    does nothing.
  * workspace: device, at least mx_linear_cross_entropy_workspace(...) bytes; needs no
  *    set-up, undefined afterwards, and belongs to one call at a time (the gradient's
  *    too). */

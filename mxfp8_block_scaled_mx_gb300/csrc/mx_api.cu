@@ -855,12 +855,12 @@ mx_status mx_norm_rotate(int64_t tokens, int64_t q_heads, int64_t k_heads, int64
   mx_status s = rotate_check(tokens, q_heads, k_heads, dim, rotary, x_dtype, w_dtype,
                              position_bits, eps);
   if (s != MX_OK) return s;
-  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 ||
-      !rows_apart(tokens, q_heads, dim, oq_st, oq_sh) ||
-      !rows_apart(tokens, k_heads, dim, ok_st, ok_sh))
-    return MX_ERR_INVALID_ARG;
+  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0) return MX_ERR_INVALID_ARG;
   if (!strides_fit({q_st, q_sh, k_st, k_sh, oq_st, oq_sh, ok_st, ok_sh}))
     return MX_ERR_UNSUPPORTED;
+  if (!rows_apart(tokens, q_heads, dim, oq_st, oq_sh) ||
+      !rows_apart(tokens, k_heads, dim, ok_st, ok_sh))
+    return MX_ERR_INVALID_ARG;
   if (!aligned_elt(q, x_dtype) || !aligned_elt(k, x_dtype) || !aligned_elt(w_q, w_dtype) ||
       !aligned_elt(w_k, w_dtype) || !aligned_elt(out_q, x_dtype) || !aligned_elt(out_k, x_dtype) ||
       (reinterpret_cast<uintptr_t>(frequencies) & 7u) != 0 ||

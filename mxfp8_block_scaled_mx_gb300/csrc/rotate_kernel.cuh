@@ -29,8 +29,9 @@
 //
 // An angle is a product in turns: the frequency becomes a 64-bit fraction of a turn
 // per position, the product with the position keeps its low 64 bits, which are the
-// fraction of a turn -- exact to 2^-64 turns times the position however far that is,
-// in integers.
+// fraction of a turn -- in integers, exact to the position times 2^-64 turns (the
+// fraction is cut off) and 2^-69 of the frequency in turns (2^66 / (2 pi) is rounded),
+// however far that is.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -177,3 +177,23 @@ def test_a_workspace_for_more_tokens_suffices_for_fewer(mx):
     # and stay in proportion: dz of one piece and a few MB beside it
     assert mx.mx_linear_cross_entropy_backward_workspace(2048, 2048, 32768) <= 2 * 2048 * 32768 + (32 << 20)
     assert mx.mx_linear_cross_entropy_backward_workspace(1, 4096, 131072) <= 2 << 20
+
+
+def test_limits_of_sizes(mx):
+    """What the header states, each just above."""
+    rotate = lambda **kw: mx.mx_norm_rotate(*{**ROTATE, **kw}.values())  # noqa: E731
+    back = lambda **kw: mx.mx_norm_rotate_backward(*{**ROTATE_BACK, **kw}.values())  # noqa: E731
+    for call in (rotate, back):
+        assert call(q_heads=65537) == 3 and call(k_heads=65537) == 3 and call(tokens=(1 << 30) + 1) == 3
+        assert call(tokens=1 << 29, q_heads=2, k_heads=2) == 3
+        for huge in (1 << 29, 1 << 61, (1 << 63) - 1):
+            assert call(q_st=huge) == 3 and call(k_sh=huge) == 3
+    for name in ("oq_st", "oq_sh", "ok_st", "ok_sh"):
+        for huge in (1 << 29, 1 << 61, (1 << 63) - 1):
+            assert rotate(**{name: huge}) == 3, name
+    for size in (mx.mx_linear_cross_entropy_workspace, mx.mx_linear_cross_entropy_backward_workspace):
+        assert size(1 << 24, 8, 256) > 0 and size((1 << 24) + 1, 8, 256) == 0
+        assert size(1, 8, 1 << 24) > 0 and size(1, 8, (1 << 24) + 1) == 0
+        assert size(1, 1 << 20, 8) > 0 and size(1, (1 << 20) + 8, 8) == 0
+        assert size(1 << 24, 8, 1 << 23) == 0 and size(1 << 24, 8, (1 << 23) - 256) > 0
+    assert mx.mx_route_workspace(4194303, 512) > 0 and mx.mx_route_workspace(4194304, 512) == 0

@@ -1,0 +1,126 @@
+"""Sizes at which the training step's operators take a path of their own, against the
+oracle: contractions of several runs in the vocabulary loss, routing of many tokens
+over 65 to 128 experts and around the rules that choose a kernel, more heads than a
+block takes at a time.
+
+Tolerances are those of the operators' own tests (their checks are used here); the
+sums over tokens of the routing below run in chains of at most 96 rows a lane, 27 warps,
+5 blocks a thread and 32 threads, which is less than the 400 half steps allowed."""
+import pytest
+import torch
+
+import test_gpu_rotate as rotate
+import test_gpu_route as routing
+import test_gpu_vocab_loss as loss
+from mxcheck import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def mx():
+    ensure_built()
+    import mxfp8_block_scaled_mx_gb300 as mx
+    return mx
+
+
+# ------------------------------------------------------------------ vocabulary loss
+
+# (runs of at most 16 steps of 64: two, three and four of them, the last short or as
+# long as the others; more tiles than pairs of blocks, or than blocks where tokens are
+# few, in boxes of 16, 32 and 64)
+RUNS = [(130, 1032, 20000), (300, 2056, 10300), (257, 4096, 700), (66, 1088, 40), (70, 2048, 513),
+        (1, 4096, 20001), (20, 1032, 20001), (32, 2056, 300), (40, 1088, 20001), (64, 4096, 2000)]
+
+
+@pytest.mark.parametrize("shape", RUNS, ids=str)
+def test_loss_of_several_runs(mx, shape):
+    x, w, labels = loss.inputs(*shape, seed=sum(shape))
+    loss.check(mx, x, w, labels)
+    loss.check_backward(mx, x, w, labels)
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 17, 64, 130, 300])
+def test_runs_keep_what_one_accumulator_would_cut_off(mx, tokens):
+    """The first 1024 terms of a logit make 2^20, the other 3072 are 2^-8 each, 12
+    together (or nothing, in every other column).  In a single FP32 accumulator, whose
+    step at 2^20 is 2^-3, sixteen of them at a time are lost; in runs of 1024 all sums
+    are exact, the last ones in FP32 too.
+
+    lse is 2^20 + 12 + log(columns) of a logit of such size: its product with log2 e is
+    rounded by 2^-4 and by the constant's 2^-25, that with ln 2 by as much and its sum by
+    2^-4: together less than 1/4."""
+    hidden, vocab = 4096, 520
+    x = torch.ones(tokens, hidden, dtype=BF16, device="cuda")
+    w = torch.zeros(vocab, hidden, dtype=BF16, device="cuda")
+    w[:, :1024] = 2.0 ** 10
+    w[::2, 1024:] = 2.0 ** -8
+    labels = torch.arange(tokens, device="cuda")
+    value, lse = mx.linear_cross_entropy(x, w, labels)
+    want = 2.0 ** 20 + 12 + torch.tensor(260 + 260 * 2.718281828459045 ** -12, dtype=torch.float64).log()
+    z = 2.0 ** 20 + 12 * (labels % 2 == 0).double()
+    assert ((lse.double() - want.item()).abs() < 0.25).all()
+    assert ((value.double() - (want.item() - z)).abs() < 0.25).all()
+    assert mx.device_status() == 0
+
+
+# ------------------------------------------------------------------ routing
+
+# (a lane a token from 8192 tokens and 128 an expert on, up to 128 experts and 8
+# winners: the form of 65 to 128 experts, in one round of warps and in several; each rule
+# from both sides)
+WIDE = [(16389, 128, 8), (8321, 65, 8), (14001, 100, 3), (100003, 128, 8), (50001, 97, 1),
+        (16383, 128, 8), (16384, 128, 8), (8319, 65, 8), (8320, 65, 8), (8191, 64, 8), (8192, 64, 8),
+        (20000, 128, 9), (20000, 129, 8)]
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", WIDE, ids=str)
+def test_routing_of_many_tokens(mx, shape, dtype, masked):
+    tokens, experts, k = shape
+    z = routing.logits(tokens, experts, dtype, seed=experts)
+    mask = torch.arange(tokens, device="cuda") % 5 != 2 if masked else None
+    routing.check_backward(mx, z, k, not masked, mask)
+
+
+@pytest.mark.parametrize("experts", [65, 72, 100, 128])
+def test_special_logits_of_many_tokens(mx, experts):
+    routing.test_special_logits(mx, 16500, experts)
+
+
+@pytest.mark.parametrize("experts", [70, 96, 128])
+def test_ties_of_many_tokens(mx, experts):
+    """16389 tokens, equal logits (among them +0 and -0): the lowest index first."""
+    routing.test_ties(mx, experts)
+
+
+def test_strided_logits_of_many_tokens(mx):
+    for dtype in (BF16, FP32):
+        wide = routing.logits(33000, 140, dtype)
+        for z in (wide[:, :128], wide[:, 1:101], wide[::2, 4:104]):
+            routing.check_backward(mx, z, 6)
+
+
+# ------------------------------------------------------------------ heads' norms
+
+# (more heads than the places of an item's rows, and tokens for every block: a block
+# goes from part to part of a token's heads, queries and keys in one part, the last short)
+MANY_HEADS = [(400, 64, 17, 256, 128, BF16), (500, 9, 4, 512, 512, FP32), (400, 70, 9, 101, 100, BF16),
+              (333, 60, 60, 64, 64, FP32), (200, 300, 5, 96, 96, BF16)]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", MANY_HEADS, ids=str)
+def test_many_heads_of_many_tokens(mx, shape, interleaved):
+    *sizes, x = shape
+    args, grads = rotate.inputs(*sizes, x, FP32, seed=1)
+    want = rotate.check_forward(mx, args, interleaved)
+    rotate.check_backward(mx, args, grads, interleaved)
+    q, k = (t.clone(memory_format=torch.contiguous_format) for t in args[:2])
+    got = mx.norm_rotate(q, k, *args[2:], interleaved=interleaved, eps=rotate.EPS, out_q=q, out_k=k)
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert mx.device_status() == 0

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int32_t u = block; u < units && ok; u += blocks) {
       const int32_t step0 = u / tiles * p.steps, steps = min(p.steps, all_steps - step0);
-      const Runs runs(steps, W == VocabProduct::kStats);
+      const Runs runs(steps, W != VocabProduct::kDx);
       for (int32_t i0 = 0; i0 < steps && ok; i0 += runs.steps) {
         if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns)) {
           ok = false;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       float v[N];
-      const Runs runs(min(p.steps, all_steps - part * p.steps), W == VocabProduct::kStats);
+      const Runs runs(min(p.steps, all_steps - part * p.steps), true);
       bool got = true;
       for (int32_t run = 0; run < runs.count; ++run) {
         if (!(got = wait())) break;

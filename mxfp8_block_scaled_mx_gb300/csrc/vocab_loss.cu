@@ -29,6 +29,7 @@
 // Six stages: with five and a second staging buffer in the gradients' epilogue 12.97
 // -> 13.07 ms at the largest, 64.3 -> 62.8 us at the smallest of these.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -103,8 +104,9 @@ struct Work<false> {
   Product first;
 };
 
-// W: kStats, kGrad, or kDx for both gradients.
-template <VocabProduct W>
+// W: kStats, kGrad, or kDx for both gradients.  RUNS: the contraction is taken in runs
+// (kStats: one or more; kGrad: more than one).
+template <VocabProduct W, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ Work<W == VocabProduct::kDx> work) {
   constexpr bool kGradients = W == VocabProduct::kDx;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t a_lo0 = smem_desc_lo(smem_u32(sA), dw ? kMnLbo : 16);
       const uint32_t next_a = dw ? kMnNext : kKNext;
       const uint32_t idesc = bf16_idesc(kTile, kTile, dw, kGradients);
-      const Runs runs(t.steps, W == VocabProduct::kStats);
+      const Runs runs(t.steps, RUNS);
       for (int32_t i0 = 0; i0 < t.steps && ok; i0 += runs.steps) {
         if (!mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, s_abort, p.status, p.wait_limit_ns)) {
           ok = false;
@@ -322,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, got);
       };
       const uint32_t taddr0 = tmem_base + ((q * 32u) << 16) + half * kHalf;
-      if constexpr (W == VocabProduct::kStats) {
-        // the runs' sums, each accumulator released as soon as it is read
-        float z[kHalf];
+      // the runs' sums, each accumulator released as soon as it is read
+      float z[RUNS ? kHalf : 1];
+      if constexpr (RUNS) {
         const Runs runs(t.steps, true);
         bool got = true;
         for (int32_t run = 0; run < runs.count; ++run) {
@@ -347,6 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (buf == 0) acc_phase ^= 1u;
         }
         if (!got) break;
+      }
+      if constexpr (W == VocabProduct::kStats) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -380,6 +384,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row < p.m)
           p.partial[static_cast<int64_t>(row) * p.slots + t.n * 2 + half] = make_float2(top, sum);
+      } else if constexpr (RUNS) {
+        // dz, rounded to bf16, straight from the logits' registers to the staging rows
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // 128 bytes a row
+          const int32_t at = label - c * 64;
+          const bool mine = label >= 0 && at >= 0 && at < 64;
+          float chosen = 0.f;
+          const bool any = __any_sync(0xffffffffu, mine);
+          if (any) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (j == at) chosen = z[c * 64 + j];
+          }
+          auto softmax = [&](float v) { return both * exp2_fast(fmaf(v, kLog2e, -lse2)); };
+          if (lane == 0) bulk_wait_read<0>();  // the copy before has left the staging rows
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = pack_bf16x2(softmax(z[c * 64 + j * 8 + 2 * i]),
+                                 softmax(z[c * 64 + j * 8 + 2 * i + 1]));
+            *reinterpret_cast<uint4*>(store + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          if (any && mine)
+            *reinterpret_cast<__nv_bfloat16*>(store + lane * 128 + (((at >> 3) ^ (lane & 7)) * 16) +
+                                              (at & 7) * 2) =
+                __float2bfloat16_rn(softmax(chosen) - once);
+          fence_proxy_async_shared();
+          __syncwarp();
+          const int32_t col = col0 + c * 64;
+          if (lane == 0 && row0 < p.m && col < p.n) {
+            tma_store_3d(&work.first.y, store, col, row0, 0);
+            bulk_commit();
+          }
+        }
       } else {
         if (!wait()) break;
         tc_fence_after_sync();
@@ -445,10 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <VocabProduct W>
+template <VocabProduct W, bool RUNS>
 cudaError_t launch(const Work<W == VocabProduct::kDx>& work, int64_t units, int num_sms,
                    cudaStream_t stream) {
-  auto kern = vocab_product_kernel<W>;
+  auto kern = vocab_product_kernel<W, RUNS>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -552,9 +594,13 @@ cudaError_t launch_vocab_logits(VocabProduct which, const VocabParams& p, const 
                                 const CUtensorMap& tmap_b, const CUtensorMap& tmap_y, int num_sms,
                                 cudaStream_t stream) {
   const Work<false> work = {{tmap_a, tmap_b, tmap_y, p}};
-  return which == VocabProduct::kStats
-             ? launch<VocabProduct::kStats>(work, units_of(p), num_sms, stream)
-             : launch<VocabProduct::kGrad>(work, units_of(p), num_sms, stream);
+  if (which == VocabProduct::kStats)
+    return launch<VocabProduct::kStats, true>(work, units_of(p), num_sms, stream);
+  // (a single run's logits go to dz from the accumulator, by halves: 4096 tokens x 512 over
+  // 65536 columns 586 us, through the registers that several runs take 650; 2048 x 2048
+  // over 32768, two runs, 437 us either way)
+  return p.steps > kRunSteps ? launch<VocabProduct::kGrad, true>(work, units_of(p), num_sms, stream)
+                             : launch<VocabProduct::kGrad, false>(work, units_of(p), num_sms, stream);
 }
 
 cudaError_t launch_vocab_gradients(const VocabGradient* dx, const VocabGradient* dw, int num_sms,
@@ -567,7 +613,7 @@ cudaError_t launch_vocab_gradients(const VocabGradient* dx, const VocabGradient*
   if (!dx) work.first.p.m = 0;  // (no units)
   if (!dw) work.second.p.m = 0;
   if (dx && dw) work.second = {*dw->a, *dw->b, *dw->y, *dw->p};
-  return launch<VocabProduct::kDx>(work, units_of(work.first.p) + units_of(work.second.p), num_sms,
+  return launch<VocabProduct::kDx, false>(work, units_of(work.first.p) + units_of(work.second.p), num_sms,
                                    stream);
 }
 

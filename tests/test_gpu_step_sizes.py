@@ -67,6 +67,32 @@ def test_runs_keep_what_one_accumulator_would_cut_off(mx, tokens):
     assert mx.device_status() == 0
 
 
+@pytest.mark.parametrize("tokens", [1, 17, 64, 130, 300])
+def test_the_gradient_exponentiates_the_logits_of_the_losses(mx, tokens):
+    """Logits of 2^15, every other one with 3072 terms of 2^-13 more, 3/8 together, of
+    which a single accumulator (step 2^-8) would lose all: a gradient whose logits were
+    summed in another way than those of lse would give these columns two thirds of
+    their probability.
+
+    Exponents are off by 2^-9 each of lse's last rounding and of log2 e and ln 2 and, in the
+    gradient, of lse's product with log2 e and the logit's: less than 2^-7; dz is rounded
+    by 2^-8 at most, sums of 300 equal terms by less than 2^-16."""
+    hidden, vocab = 4096, 520
+    x = torch.ones(tokens, hidden, dtype=BF16, device="cuda")
+    w = torch.zeros(vocab, hidden, dtype=BF16, device="cuda")
+    w[:, :1024] = 2.0 ** 5
+    w[::2, 1024:] = 2.0 ** -13
+    labels = torch.full((tokens,), -100, device="cuda")
+    _, lse = mx.linear_cross_entropy(x, w, labels)
+    ones = torch.ones(tokens, device="cuda")
+    _, dw = mx.linear_cross_entropy_backward(None, ones, x, w, labels, lse, weight_dtype="fp32")
+    z = torch.zeros(vocab, dtype=torch.float64)
+    z[::2] = 0.375
+    want = tokens * torch.softmax(z, 0)[:, None].cuda()
+    assert ((dw.double() - want).abs() <= (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -16) * 1.01 * want).all()
+    assert mx.device_status() == 0
+
+
 # ------------------------------------------------------------------ routing
 
 # (a lane a token from 8192 tokens and 128 an expert on, up to 128 experts and 8

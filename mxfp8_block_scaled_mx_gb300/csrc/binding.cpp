@@ -89,9 +89,12 @@ struct Call {
   // Refuses tangents of forward-mode differentiation: a kernel does not carry them
   // along, and an output without one would stand for a derivative of zero.
   void refuse_tangents(Py_ssize_t n) const {
-    for (Py_ssize_t i = 0; i < n; ++i)
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      // (asking a number or None whether it is a tensor takes as long as the rest of it)
+      if (args[i] == Py_None || PyLong_Check(args[i]) || PyFloat_Check(args[i])) continue;
       if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i])._fw_grad(0).defined())
         throw Refused{"forward-mode derivatives are not computed: no argument may be a dual tensor"};
+    }
   }
   const at::Tensor& tensor(int i, const char* name) const {
     if (!THPVariable_Check(args[i])) throw Refused{std::string(name) + " must be a tensor"};

@@ -826,11 +826,12 @@ def norm_rotate(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.
                 out_k: torch.Tensor | None = None, stream=None):
     """The norms of query and key heads and their rotation by position in one
     pass: returns (q', k').  q [tokens, q_heads, dim], k [tokens, k_heads,
-    dim]: bf16 or fp32, channels contiguous, any strides of tokens and heads
-    (parts of a product's rows); w_q, w_k: [dim], bf16 or fp32; positions: int32
-    or int64 [tokens]; frequencies: float64 [rotary / 2], radians per position
-    (rotary_frequencies).  The first `rotary` channels are rotated, in pairs (i,
-    i + rotary / 2), or (2 i, 2 i + 1) where interleaved, and scaled by `scale`.
+    dim]: bf16 or fp32, up to 512 channels, contiguous, any strides of tokens and
+    heads (parts of a product's rows); w_q, w_k: [dim], bf16 or fp32; positions:
+    int32 or int64 [tokens]; frequencies: float64 [rotary / 2], radians per
+    position (rotary_frequencies).  The first `rotary` channels are rotated, in
+    pairs (i, i + rotary / 2), or (2 i, 2 i + 1) where interleaved, and scaled by
+    `scale`.
     out_q, out_k may be q and k themselves, but not where autograd records: the
     backward pass needs q and k.  Differentiable in q, k, w_q and w_k (frequencies
     that ask for a gradient are refused): where autograd records, the backward
@@ -915,8 +916,9 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
           mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
           stream=None) -> Routing:
     """The experts of every token from the router's logits (bf16 or fp32
-    [tokens, experts]): the top_k largest (equal ones: the lowest index first)
-    with their softmax weights, divided by their sum where renormalize, the
+    [tokens, experts], up to 512 experts): the top_k largest, up to 32 (equal ones:
+    the lowest index first), with their softmax weights, divided by their sum
+    where renormalize, the
     counts, offsets and order of the pairs by expert, and the balance loss,
     experts * sum_e (share of the pairs at e) * (mean probability of e).  mask:
     bool or uint8 [tokens]; a token that it leaves out is routed, but adds
@@ -981,8 +983,8 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, labels: torch.Te
                          stream=None):
     """Softmax cross entropy of the logits x weight^T, which are never stored:
     returns (loss, lse), fp32 [tokens], lse the logarithm of each token's sum
-    of exponentials.  x: bf16 [tokens, hidden]; weight: bf16 [vocab, hidden];
-    labels: int32 or int64 [tokens].  A token whose label is ignore_index has
+    of exponentials.  x: bf16 [tokens, hidden]; weight: bf16 [vocab, hidden]
+    (hidden a multiple of 8, rows on 16 bytes); labels: int32 or int64 [tokens].  A token whose label is ignore_index has
     loss 0; any other label outside the vocabulary gives NaN and is reported by
     device_status.  Differentiable in both outputs: where autograd records, the
     backward pass is linear_cross_entropy_backward.  workspace: uint8,
@@ -1027,7 +1029,9 @@ def linear_cross_entropy_backward(d_loss: torch.Tensor | None, d_lse: torch.Tens
     """Gradients (of x: bf16, of weight: bf16 or, with weight_dtype "fp32",
     fp32) of linear_cross_entropy from those of its outputs (fp32 [tokens];
     None: zero).  lse: what the forward pass returned.  Goes through the
-    vocabulary in pieces, whose logits are computed again.  need_x, need_weight:
+    vocabulary in pieces, whose logits are computed again; their gradient is
+    rounded to bf16 as an operand of both products, whatever weight_dtype is (for up
+    to 64 tokens to two bf16 terms).  need_x, need_weight:
     a gradient that is not needed is None, and its product left out.  The same
     inputs give the same bits.  workspace: uint8,
     mx_linear_cross_entropy_backward_workspace(tokens, hidden, vocab) bytes, one

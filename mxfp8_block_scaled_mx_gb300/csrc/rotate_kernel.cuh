@@ -22,10 +22,10 @@
 // Measured on one GB300 (part of the measured copy bandwidth, 6.78 TB/s): 16384
 // tokens x 40 heads of 128, bf16: 53 us, 0.93; gradient 97 us, 0.77 (59 % of issue
 // slots busy at 16 warps an SM: the registers of five values a channel); one token
-// 2.7 us in a graph, 5.3 called.  Half of the channels rotated: 55 and 112 us; 40
-// heads of 80 (lanes without channels) 60 and 141; 52 of 128 channels rotated (not
-// a multiple of 8: single channels, twice the lanes and four times the accesses) 121
-// and 186.
+// 2.7 us in a graph, 5.3 called.  Half of the channels rotated: 54 and 107 us; 40
+// heads of 80 (lanes without channels) 59 and 137; 52 of 128 channels rotated (not
+// a multiple of 8: single channels, twice the lanes and four times the accesses) 119
+// and 180.
 //
 // An angle is a product in turns: the frequency becomes a 64-bit fraction of a turn
 // per position, the product with the position keeps its low 64 bits, which are the

@@ -20,9 +20,9 @@
 // of its tokens over all tiles of the block.  All waits are bounded.
 //
 // Bound by memory.  Measured on one GB300 over 131072 x 4096 weights (1.07 GB, 158 us
-// at the measured copy bandwidth): losses of 1 token 161 us, 0.98, of 64 tokens 160;
-// losses' gradients of 64 tokens 517 us (weights read twice, their gradient written:
-// 475; with one term of dz 527).  The tiles of vocab_loss.cu take 291 us for one token, 175 for 65.
+// at the measured copy bandwidth): losses of 1 token 168 us, 0.94, of 64 tokens 159;
+// losses' gradients of 64 tokens 519 us (weights read twice, their gradient written:
+// 475; with one term of dz 527).  The tiles of vocab_loss.cu take 291 us for one token, 181 for 65.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

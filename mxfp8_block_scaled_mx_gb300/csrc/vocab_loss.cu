@@ -20,12 +20,13 @@
 //   warps 2..9 (both)     epilogue, 32 rows x 128 columns of the tile each
 // All waits are bounded.
 //
-// Bound by the tensor cores.  Measured on one GB300 (cuBLAS bf16: 1884 TFLOP/s in a
-// burst, 1692 under the power cap): losses of 4096 tokens over 131072 x 7168 3.83 ms,
-// 2010 TFLOP/s; losses and gradients (four products, one of them z again) 17.4-18.4
-// ms, 1680-1770 TFLOP/s at the power cap; 2048 tokens over 32768 x 2048 666 us; 777
-// over 50257 x 2048 110 us for losses (1434; its 1024 rows of tiles run at 1890); 333
-// over 18433 x 1000 77 us, latencies of six launches and two rounds of tiles.
+// Bound by the tensor cores.  Measured on one GB300 in a burst and, behind the slash,
+// after seconds of such work, at the power cap (1560 to 1680 MHz; cuBLAS bf16 1884 /
+// 1692 TFLOP/s): losses of 4096 tokens over 131072 x 7168 3.9 / 4.3 ms, 1950 / 1780
+// TFLOP/s; losses and gradients (four products, one of them z again) 17.1 / 18.5 ms, 1800
+// / 1670 TFLOP/s; 2048 tokens over 32768 x 2048 575 / 670 us; 777 over 50257 x 2048 112 /
+// 128 us for losses (1430 / 1250; 1880 / 1650 on its 1024 rows of tiles); 333 over
+// 18433 x 1000 78 us, latencies of six launches and two rounds of tiles.
 // Six stages: with five and a second staging buffer in the gradients' epilogue 12.97
 // -> 13.07 ms at the largest, 64.3 -> 62.8 us at the smallest of these.
 #include <cuda.h>

@@ -130,3 +130,16 @@ def test_one_workspace_for_batches_of_any_size(mx):
         a, b = (mx.linear_cross_entropy_backward(d, None, xs, w, ls, b[1], workspace=s) for s in (None, back))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), tokens
     assert mx.device_status() == 0
+
+
+def test_heads_in_place_where_autograd_records(mx):
+    """The backward pass needs q and k: it says that they were overwritten."""
+    heads = randn(20, 4, 32, seed=1, dtype=BF16)
+    w = torch.ones(32, device="cuda").requires_grad_()
+    q, k = heads[:, :3].clone(), heads[:, 3:].clone()
+    args = (w, w, torch.arange(20, device="cuda"), mx.rotary_frequencies(32))
+    want = mx.norm_rotate(q, k, *args)
+    a, _ = mx.norm_rotate(q, k, *args, out_q=q)
+    assert a is q and torch.equal(q, want[0])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        a.float().sum().backward()

@@ -1,7 +1,7 @@
 """Sizes at which the training step's operators take a path of their own, against the
 oracle: contractions of several runs in the vocabulary loss, routing of many tokens
 over 65 to 128 experts and around the rules that choose a kernel, more heads than a
-block takes at a time.
+block takes at a time, elements further apart than 32 bits count.
 
 Tolerances are those of the operators' own tests (their checks are used here); the
 sums over tokens of the routing below run in chains of at most 96 rows a lane, 27 warps,
@@ -149,4 +149,110 @@ def test_many_heads_of_many_tokens(mx, shape, interleaved):
     q, k = (t.clone(memory_format=torch.contiguous_format) for t in args[:2])
     got = mx.norm_rotate(q, k, *args[2:], interleaved=interleaved, eps=rotate.EPS, out_q=q, out_k=k)
     assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert mx.device_status() == 0
+
+
+# ------------------------------------------------------------------ beyond 32 bits
+
+def apart(t, stride, offset=0):
+    """A copy of t whose rows lie `stride` elements apart, `offset` into a buffer."""
+    rows = t.reshape(len(t), -1)
+    buf = torch.empty(offset + (len(t) - 1) * stride + rows.shape[1], dtype=t.dtype, device="cuda")
+    far = buf[offset:].as_strided(rows.shape, (stride, 1))
+    far.copy_(rows)
+    return buf[offset:].as_strided(t.shape, (stride, *t.stride()[1:]))
+
+
+def test_heads_far_apart(mx):
+    args, grads = rotate.inputs(17, 3, 1, 64, 32, BF16, BF16)
+    near = [t.contiguous() for t in (*args[:2], *grads)]
+    q, k, dq, dk = (apart(t, 2 ** 28 - 64, 8) for t in near)
+    a = mx.norm_rotate(*near[:2], *args[2:])
+    b = mx.norm_rotate(q, k, *args[2:])
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    a = mx.norm_rotate_backward(*near[2:], *near[:2], *args[2:])
+    b = mx.norm_rotate_backward(dq, dk, q, k, *args[2:])
+    assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
+    got = mx.norm_rotate(q, k, *args[2:], out_q=q, out_k=k)
+    want = mx.norm_rotate(*near[:2], *args[2:])
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+@pytest.mark.parametrize("tokens,experts,stride", [(40, 64, 2 ** 27), (3000, 200, 2 ** 21), (9000, 64, 2 ** 19)])
+def test_logits_far_apart(mx, tokens, experts, stride):
+    z = routing.logits(tokens, experts, BF16)
+    far = apart(z, stride)
+    a, b = mx.route(z, 4), mx.route(far, 4)
+    assert all(torch.equal(u, v) for u, v in zip(vars(a).values(), vars(b).values()))
+    one = torch.ones((), device="cuda")
+    assert torch.equal(mx.route_backward(a.weights, one, z, a), mx.route_backward(a.weights, one, far, a))
+
+
+def test_as_many_tokens_and_experts_as_routing_takes(mx):
+    """2^31 logits less a few: every token's own outputs are those of a smaller call;
+    offsets, order and counts belong together."""
+    tokens, experts, k = 4194303, 512, 2
+    z = torch.randn(1 << 16, experts, device="cuda").bfloat16().repeat(64, 1)[:tokens]
+    r, few = mx.route(z, k), mx.route(z[:1 << 16], k)
+    for name in ("ids", "weights", "lse"):
+        got, want = getattr(r, name), getattr(few, name)
+        for at in range(0, tokens, 1 << 16):
+            part = got[at:at + (1 << 16)]
+            assert torch.equal(part, want[:len(part)]), (name, at)
+    flat = r.ids.flatten()
+    counts = torch.bincount(flat, minlength=experts)
+    assert torch.equal(r.counts.long(), counts)
+    assert torch.equal(r.offsets[1:].long(), counts.cumsum(0)) and r.offsets[0].item() == 0
+    assert torch.equal(r.order.long(), torch.sort(flat, stable=True).indices)
+    d = torch.randn(1 << 16, k, device="cuda").repeat(64, 1)[:tokens].contiguous()
+    got, want = mx.route_backward(d, None, z, r), mx.route_backward(d[:1 << 16], None, z[:1 << 16], few)
+    for at in range(0, tokens, 1 << 16):
+        part = got[at:at + (1 << 16)]
+        assert torch.equal(part, want[:len(part)]), at
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [5, 130])
+def test_rows_of_the_loss_far_apart(mx, tokens):
+    x, w, labels = loss.inputs(tokens, 72, 130)
+    far_x, far_w = apart(x, 2 ** 32 // (tokens - 1) // 8 * 8 + 8), apart(w, 2 ** 25 + 8)
+    a, b = mx.linear_cross_entropy(x, w, labels), mx.linear_cross_entropy(far_x, far_w, labels)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ones = torch.ones(tokens, device="cuda")
+    a = mx.linear_cross_entropy_backward(ones, None, x, w, labels, a[1])
+    b = mx.linear_cross_entropy_backward(ones, None, far_x, far_w, labels, b[1])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("tokens", [3, 70])
+def test_weights_of_more_than_two_to_the_31_elements(mx, tokens):
+    """Losses against a softmax in 64 bits, a piece of the vocabulary at a time; rows of
+    the weights' gradient from its start, its middle and its end."""
+    hidden, vocab = 2056, (1 << 20) + 5
+    g = torch.Generator("cuda").manual_seed(tokens)
+    w = torch.empty(vocab, hidden, dtype=BF16, device="cuda")
+    for v in range(0, vocab, 1 << 17):
+        part = w[v:v + (1 << 17)]
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * 2 / hidden ** 0.5)
+    x = torch.randn(tokens, hidden, generator=g, device="cuda").to(BF16)
+    labels = vocab - 1 - 7 * torch.arange(tokens, device="cuda")
+    z = torch.cat([x.double() @ w[v:v + (1 << 17)].double().T for v in range(0, vocab, 1 << 17)], 1)
+    want = torch.logsumexp(z, 1)
+    value, lse = mx.linear_cross_entropy(x, w, labels)
+    mag = max((x.double().abs() @ w[v:v + (1 << 17)].double().abs().T).max().item() for v in range(0, vocab, 1 << 17))
+    tol = loss.z_error(hidden, mag) + 2.0 ** -20 + 2.0 ** -22 * want.abs().max().item()
+    assert ((lse.double() - want).abs() <= tol).all()
+    assert ((value.double() - (want - z.gather(1, labels[:, None])[:, 0])).abs() <= 2 * tol).all()
+    d = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    _, dw = mx.linear_cross_entropy_backward(d, None, x, w, labels, lse, need_x=False)
+    for lo in (0, vocab // 2, vocab - 600):
+        p = torch.exp(z[:, lo:lo + 600] - want[:, None]) / tokens
+        for t in range(tokens):
+            at = int(labels[t]) - lo
+            if 0 <= at < 600:
+                p[t, at] -= 1.0 / tokens
+        ref, m = p.T @ x.double(), p.abs().T @ x.double().abs()
+        # dz: half a step of bf16 and the softmax's relative error; sums; the output's half step
+        bound = (2.0 ** -8 + 2 * tol + 2.0 ** -18) * 1.01 * m
+        assert ((dw[lo:lo + 600].double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound) + 1e-37).all(), lo
     assert mx.device_status() == 0

@@ -636,8 +636,10 @@ size_t mx_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t hidden
  *   dx = dz w,  dw = dz^T x
  * piece by piece of the vocabulary, z computed again.  d_loss counts as 0 for a
  * token whose label is ignore_index or outside the vocabulary.  dz is rounded to
- * bf16 (for up to 64 tokens to two bf16 terms, 16 significant bits), as an operand
- * of the two products, which accumulate in FP32.  Every row of x takes part in dw,
+ * bf16, in units of the largest |d_loss| of the tokens that count (so that a label's
+ * entry of a mean is exact but for its probability), or for up to 64 tokens to two
+ * bf16 terms, 16 significant bits, as an operand of the two products, which
+ * accumulate in FP32.  Every row of x takes part in dw,
  * with zeros of dz too: a NaN or an infinity in the row of a token that does not
  * count reaches dw (rows of padding have to be finite).
  * d_loss, d_lse: device float [tokens], or NULL (zero).

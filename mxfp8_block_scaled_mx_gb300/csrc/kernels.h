@@ -275,7 +275,7 @@ cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_
 //   kStats   z = x W^T; per row and half tile of columns the running maximum
 //            and sum of the softmax, and the label's logit
 //   kGrad    dz = (d_loss + d_lse) exp(z - lse) - d_loss [label] of a piece of the
-//            vocabulary, bf16 (few tokens: two terms)
+//            vocabulary, bf16 in units of the largest d_loss (few tokens: two terms)
 //   kDx      dx = dz W of the piece, over `splits` parts of its columns
 //   kDw      dW = dz^T x of the piece
 enum class VocabProduct { kStats, kGrad, kDx, kDw };
@@ -296,6 +296,8 @@ struct VocabParams {
   const float* lse;        // kGrad: [tokens]
   const float* d_loss;     // [tokens] or nullptr (zero)
   const float* d_lse;      // [tokens] or nullptr
+  float* scale;            // what dz is held in units of, written by kGrad, read by kDx and
+                           // kDw; nullptr (few tokens): 1
   int32_t y_fp32;          // kDx, kDw: type of the output
   int32_t add;             // kDx: 1 adds to the output (FP32)
   int32_t low_row;         // kDw of few tokens: first row of dz's low terms (else 0);

@@ -1098,7 +1098,8 @@ constexpr int64_t kVocabPieceCols = 4096;
 // Bytes of the parts over which dx of more than 64 tokens is summed side by side, at
 // most.  (What the device's places ask for stays below 26 MB at any sizes: it limits
 // none of them, but bounds the workspace.)
-constexpr int64_t kVocabPartBytes = int64_t{32} << 20;
+constexpr int64_t kVocabPartBytes = (int64_t{32} << 20) - 16;
+constexpr int64_t kVocabUnitBytes = 16;  // what dz is held in units of, behind the parts
 
 mx_status vocab_check(int64_t tokens, int64_t hidden, int64_t vocab, int64_t ldx, int64_t ldw,
                       int32_t label_bits) {
@@ -1204,7 +1205,8 @@ size_t vocab_backward_bytes(int64_t tokens, int64_t hidden, int64_t vocab) {
   // 32 parts at most, of few tokens any, of more up to kVocabPartBytes; one part as it is
   const int64_t one = tokens * hidden * 4;
   const int64_t parts = most(kVocabPartBytes, 32 * mx::kVocabFewTokens * hidden * 4);
-  return static_cast<size_t>(dz + most(one, least(32 * one, parts)));
+  return static_cast<size_t>(dz + most(one, least(32 * one, parts)) +
+                             (tokens > 0 ? kVocabUnitBytes : 0));
 }
 
 // 2-D bf16 tensor map, box 64 columns x box_rows, 128-byte swizzle, zero fill.
@@ -1360,6 +1362,7 @@ mx_status mx_linear_cross_entropy_backward(int64_t tokens, int64_t hidden, int64
     p.lse = lse;
     p.d_loss = d_loss;
     p.d_lse = d_lse;
+    p.scale = few ? nullptr : reinterpret_cast<float*>(dz + v.dz_bytes + v.dx_bytes);
     p.out = dz;
     p.ld_out = v.cols;
     if ((s = encode_bf16_box(&ta, x, hidden, tokens, ldx, box)) != MX_OK) return s;

@@ -9,8 +9,8 @@
 // six stages, two accumulators in tensor memory so that the epilogue of a tile
 // runs beside the MMAs of the next.  The gradient goes through the vocabulary in
 // pieces: dz of a piece is computed again from x and W, rounded to bf16 (it is
-// an operand of bf16 MMAs; its 8 significant bits are those that x and W have)
-// and read by the two products, which share a launch: where the tiles of one do not
+// an operand of bf16 MMAs; its 8 significant bits are those that x and W have), in
+// units of the largest |d_loss|, and read by the two products, which share a launch: where the tiles of one do not
 // fill the device's last round, those of the other do.  Operands that are
 // contiguous along M or N (dz and x in dW, W in dx) are read as they lie: the
 // tensor core transposes.
@@ -57,7 +57,8 @@ constexpr int kOffB = kStages * kOperandBytes;
 constexpr int kOffStore = 2 * kOffB;
 constexpr int kOffBar = kOffStore + kEpiWarps * kStoreBytes;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 1024;  // + alignment slack
+constexpr int kOffMost = kOffBar + kNumBars * 8 + 16;  // a float a warp of the epilogue
+constexpr int kSmemBytes = kOffMost + kEpiWarps * 4 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 0x3;
@@ -87,6 +88,28 @@ __device__ __forceinline__ Unit unit_of(const VocabParams& p, int32_t u) {
 
 __host__ __device__ __forceinline__ int64_t units_of(const VocabParams& p) {
   return static_cast<int64_t>((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile) * p.splits;
+}
+
+// What dz is held in units of: the largest |d_loss| of the tokens that count.  A mean's
+// d_loss is the same for all of them, and so would be its rounding in every label's entry:
+// the gradient would be off by up to 2^-8 in one direction (255 tokens).  In these units the
+// entry is -1 and the label's probability.  (1 where that is nothing, not finite, or so far
+// from 1 that dz could leave the type's range.)  Of all epilogue threads of a block.
+__device__ __forceinline__ float dz_unit(const VocabParams& p, float* most_of_warp) {
+  const int32_t first = static_cast<int32_t>(threadIdx.x) - 64;
+  float most = 0.f;
+  if (p.d_loss) {
+#pragma unroll 4
+    for (int32_t t = first; t < p.tokens; t += kEpiWarps * 32)
+      if (counts(p, label_of(p, t))) most = fmaxf(most, fabsf(p.d_loss[t]));
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+  if (lane_id() == 0) most_of_warp[first / 32] = most;
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+#pragma unroll
+  for (int i = 0; i < kEpiWarps; ++i) most = fmaxf(most, most_of_warp[i]);
+  return most >= 0x1p-100f && most <= 0x1p100f ? most : 1.f;
 }
 
 // A product and the maps of its operands and output.
@@ -289,6 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t half = (warp - 2) >> 2;   // columns 128 half .. + 127
     uint8_t* store = smem + kOffStore + (warp - 2) * kStoreBytes;
     const uint32_t empty_leader0 = cluster_map(&acc_empty[0], 0);
+    float unit = 1.f;  // of dz
+    if constexpr (W == VocabProduct::kGrad) {
+      unit = dz_unit(p, reinterpret_cast<float*>(smem + kOffMost));
+      if (blockIdx.x == 0 && threadIdx.x == 64) *p.scale = unit;
+    } else if constexpr (kGradients) {
+      if (p.scale) unit = *p.scale;
+    }
     uint32_t buf = 0, acc_phase = 0;
     for (int32_t u = cluster; u < units; u += clusters) {
       const Product& w = product(u);
@@ -311,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (W == VocabProduct::kGrad) {
             lse2 = p.lse[row] * kLog2e;
             once = valid && p.d_loss ? p.d_loss[row] : 0.f;
-            both = once + (p.d_lse ? p.d_lse[row] : 0.f);
+            both = (once + (p.d_lse ? p.d_lse[row] : 0.f)) / unit;
+            once /= unit;
           }
         }
       }
@@ -447,6 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 64; ++j)
                 if (label >= 0 && j == at) v[j] = __float_as_uint(__uint_as_float(v[j]) - once);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * unit);
+            if (!f32) {
+#pragma unroll
+              for (int j = 32; j < 64; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * unit);
             }
           }
           if (!f32) {

@@ -1030,8 +1030,8 @@ def linear_cross_entropy_backward(d_loss: torch.Tensor | None, d_lse: torch.Tens
     fp32) of linear_cross_entropy from those of its outputs (fp32 [tokens];
     None: zero).  lse: what the forward pass returned.  Goes through the
     vocabulary in pieces, whose logits are computed again; their gradient is
-    rounded to bf16 as an operand of both products, whatever weight_dtype is (for up
-    to 64 tokens to two bf16 terms).  need_x, need_weight:
+    rounded to bf16 as an operand of both products, whatever weight_dtype is, in
+    units of the largest |d_loss| (for up to 64 tokens to two bf16 terms).  need_x, need_weight:
     a gradient that is not needed is None, and its product left out.  The same
     inputs give the same bits.  workspace: uint8,
     mx_linear_cross_entropy_backward_workspace(tokens, hidden, vocab) bytes, one
